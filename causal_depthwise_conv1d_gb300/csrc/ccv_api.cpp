@@ -83,6 +83,32 @@ bool unique_writes(const int64_t* shape, const int64_t* strides, int nd) {
 
 }  // namespace
 
+namespace ccv {
+
+int api_fail(int status, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  g_last_error = buf;
+  return status;
+}
+
+void api_begin() { g_last_error.clear(); }
+
+void api_kernel(const char* name) { g_last_kernel = name; }
+
+int api_device(Device* out) {
+  int dev = 0;
+  const cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return fail(CCV_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(err));
+  if (!device_info(dev, out)) return fail(CCV_ERR_CUDA, "cannot query device %d", dev);
+  return CCV_OK;
+}
+
+}  // namespace ccv
+
 extern "C" {
 
 const char* ccv_last_error(void) { return g_last_error.c_str(); }

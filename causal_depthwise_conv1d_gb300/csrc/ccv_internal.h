@@ -145,4 +145,12 @@ void set_chlast_wait_test(long long budget_cycles, long long skip_stage);
 // synchronous).  Non-zero means a wait ran out of budget.
 unsigned read_and_clear_fault_chlast_tma();
 
+// Shared by the ABI front ends (ccv_api.cpp, mix_api.cpp): the thread's error
+// message and kernel name, and the current device's properties (a non-OK
+// status, already recorded, when they cannot be read).
+int api_fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+void api_begin();
+void api_kernel(const char* name);
+int api_device(Device* out);
+
 }  // namespace ccv

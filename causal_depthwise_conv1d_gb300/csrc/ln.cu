@@ -1,0 +1,410 @@
+// Layer normalisation over the last dimension, forward and backward.
+//
+//   xh = (x - m) r,  m = mean(x),  r = 1 / sqrt(mean((x - m)^2) + eps);   y = xh w + b
+//   d = dy w;   dx = r (d - mean(d) - xh mean(d xh));   dw = sum_rows dy xh;   db = sum_rows dy
+//
+// Mean and variance are two reductions over the row held in registers (the
+// variance of x - m, so a large mean costs no precision), all sums in FP32.
+// The backward pass needs nothing saved by the forward: it reads x and dy
+// once, takes the row's statistics again, and keeps each column's dw and db
+// in registers over all rows of a block; a block writes one partial sum per
+// column, and a second kernel adds the partials in a fixed order (bitwise
+// reproducible, no atomics).
+//
+// What bounds it: HBM (2 N D elements forward, 3 N D backward).
+#include "ccv_common.cuh"
+#include "mix_internal.h"
+
+namespace ccv {
+namespace {
+
+// Sum of NS values over the threads that share a row: one warp, or the block.
+template <bool WARP, int NS>
+__device__ __forceinline__ void row_sum(float (&v)[NS], float* red, int nwarps) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1)
+#pragma unroll
+    for (int i = 0; i < NS; ++i) v[i] += __shfl_xor_sync(kFullMask, v[i], m);
+  if constexpr (!WARP) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0)
+#pragma unroll
+      for (int i = 0; i < NS; ++i) red[warp * NS + i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      float x = lane < nwarps ? red[lane * NS + i] : 0.f;
+#pragma unroll
+      for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(kFullMask, x, m);
+      v[i] = x;
+    }
+    __syncthreads();
+  }
+}
+
+// Elements of one vector access: 16 bytes, or one element where the row is
+// not aligned (V = 1).
+template <int DT, int V>
+__device__ __forceinline__ void load_v(const void* base, int64_t off, int64_t stride, float* f) {
+  using E = typename Fmt<DT>::E;
+  const E* p = static_cast<const E*>(base);
+  if constexpr (V == 1) {
+    f[0] = Fmt<DT>::to_f(p[off * stride]);
+  } else {
+    unpack16<DT>(*reinterpret_cast<const uint4*>(p + off), f);
+  }
+}
+
+template <int DT, int V>
+__device__ __forceinline__ void store_v(void* base, int64_t off, int64_t stride, const float* f) {
+  using E = typename Fmt<DT>::E;
+  E* p = static_cast<E*>(base);
+  if constexpr (V == 1) {
+    p[off * stride] = Fmt<DT>::from_f(f[0]);
+  } else {
+    *reinterpret_cast<uint4*>(p + off) = pack16<DT>(f);
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void load_par(const void* w, int64_t col, int64_t ws, int wdt, float fill, float* f) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) f[j] = w != nullptr ? ld_param(w, (col + j) * ws, wdt) : fill;
+}
+
+// NV vectors of V elements a thread; WARP: a warp owns a row, else the block.
+template <int DT, int V, int NV, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : 1024) ln_fwd_kernel(const LnArgs a) {
+  pdl_enter();
+  __shared__ float red[32];
+  const int G = WARP ? 32 : blockDim.x;  // threads of one row
+  const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int nwarps = blockDim.x >> 5;
+  const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * nwarps + (threadIdx.x >> 5) : blockIdx.x;
+  if (row >= a.N) return;
+  using E = typename Fmt<DT>::E;
+  const E* x = static_cast<const E*>(a.x) + row * a.xs0;
+  E* y = static_cast<E*>(a.out) + row * a.os0;
+  float f[NV][V];
+  float s[1] = {0.f};
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t col = (static_cast<int64_t>(i) * G + t) * V;
+    if (col < a.D) {
+      load_v<DT, V>(x, col, a.xs1, f[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[i][j] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[0] += f[i][j];
+  }
+  row_sum<WARP>(s, red, nwarps);
+  const float inv_d = 1.f / static_cast<float>(a.D);
+  const float mean = s[0] * inv_d;
+  float q[1] = {0.f};
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t col = (static_cast<int64_t>(i) * G + t) * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      f[i][j] -= mean;
+      if (col < a.D) q[0] = fmaf(f[i][j], f[i][j], q[0]);
+    }
+  }
+  row_sum<WARP>(q, red, nwarps);
+  const float r = rsqrtf(q[0] * inv_d + a.eps);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t col = (static_cast<int64_t>(i) * G + t) * V;
+    if (col < a.D) {
+      float w[V], b[V];
+      load_par<V>(a.w, col, a.ws, a.wdt, 1.f, w);
+      load_par<V>(a.b, col, a.bs, a.wdt, 0.f, b);
+#pragma unroll
+      for (int j = 0; j < V; ++j) w[j] = fmaf(f[i][j] * r, w[j], b[j]);
+      store_v<DT, V>(y, col, a.os1, w);
+    }
+  }
+}
+
+// Rows of any size and strides: three sweeps over the row by one block.
+template <int DT>
+__global__ void ln_fwd_any(const LnArgs a) {
+  pdl_enter();
+  __shared__ float red[32];
+  using F = Fmt<DT>;
+  using E = typename F::E;
+  const int nwarps = blockDim.x >> 5;
+  const E* x = static_cast<const E*>(a.x) + blockIdx.x * a.xs0;
+  E* y = static_cast<E*>(a.out) + blockIdx.x * a.os0;
+  float s[1] = {0.f};
+  for (int64_t c = threadIdx.x; c < a.D; c += blockDim.x) s[0] += F::to_f(x[c * a.xs1]);
+  row_sum<false>(s, red, nwarps);
+  const float inv_d = 1.f / static_cast<float>(a.D), mean = s[0] * inv_d;
+  float q[1] = {0.f};
+  for (int64_t c = threadIdx.x; c < a.D; c += blockDim.x) {
+    const float d = F::to_f(x[c * a.xs1]) - mean;
+    q[0] = fmaf(d, d, q[0]);
+  }
+  row_sum<false>(q, red, nwarps);
+  const float r = rsqrtf(q[0] * inv_d + a.eps);
+  for (int64_t c = threadIdx.x; c < a.D; c += blockDim.x) {
+    const float w = a.w != nullptr ? ld_param(a.w, c * a.ws, a.wdt) : 1.f;
+    const float b = a.b != nullptr ? ld_param(a.b, c * a.bs, a.wdt) : 0.f;
+    y[c * a.os1] = F::from_f(fmaf((F::to_f(x[c * a.xs1]) - mean) * r, w, b));
+  }
+}
+
+// Backward: block (or warp) rows blockIdx, blockIdx + grid, ...; partial sums
+// of dw and db in registers.
+template <int DT, int V, int NV, bool WARP, int MAXT>
+__global__ void __launch_bounds__(MAXT) ln_bwd_kernel(const LnBwdArgs a) {
+  pdl_enter();
+  extern __shared__ float sh[];  // WARP: [warps][2][D]; else the row sums
+  const int G = WARP ? 32 : blockDim.x;
+  const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int nwarps = blockDim.x >> 5, warp = threadIdx.x >> 5;
+  using E = typename Fmt<DT>::E;
+  float dw[NV][V], db[NV][V], w[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t col = (static_cast<int64_t>(i) * G + t) * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) dw[i][j] = db[i][j] = w[i][j] = 0.f;
+    if (col < a.D) load_par<V>(a.w, col, a.ws, a.wdt, 1.f, w[i]);
+  }
+  const float inv_d = 1.f / static_cast<float>(a.D);
+  const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * nwarps : gridDim.x;
+  for (int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * nwarps + warp : blockIdx.x; row < a.N; row += step) {
+    const E* x = static_cast<const E*>(a.x) + row * a.xs0;
+    const E* gr = static_cast<const E*>(a.dout) + row * a.gs0;
+    E* dx = static_cast<E*>(a.dx) + row * a.dxs0;
+    float f[NV][V], d[NV][V];
+    float s[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t col = (static_cast<int64_t>(i) * G + t) * V;
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[i][j] = d[i][j] = 0.f;
+      if (col < a.D) {
+        load_v<DT, V>(x, col, a.xs1, f[i]);
+        load_v<DT, V>(gr, col, a.gs1, d[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[0] += f[i][j];
+    }
+    row_sum<WARP>(s, sh, nwarps);
+    const float mean = s[0] * inv_d;
+    float q[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t col = (static_cast<int64_t>(i) * G + t) * V;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        f[i][j] -= mean;
+        if (col >= a.D) f[i][j] = 0.f;
+        q[0] = fmaf(f[i][j], f[i][j], q[0]);
+        const float dd = d[i][j] * w[i][j];
+        q[1] += dd;
+        q[2] = fmaf(dd, f[i][j], q[2]);
+      }
+    }
+    row_sum<WARP>(q, sh, nwarps);
+    const float r = rsqrtf(q[0] * inv_d + a.eps);
+    const float c1 = q[1] * inv_d, c2 = q[2] * inv_d * r;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t col = (static_cast<int64_t>(i) * G + t) * V;
+      float o[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float xh = f[i][j] * r;
+        dw[i][j] = fmaf(d[i][j], xh, dw[i][j]);
+        db[i][j] += d[i][j];
+        o[j] = r * (d[i][j] * w[i][j] - c1 - xh * c2);
+      }
+      if (col < a.D) store_v<DT, V>(dx, col, a.dxs1, o);
+    }
+  }
+  if (a.part == nullptr) return;
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.D;
+  if constexpr (WARP) {
+    // the block's warps in order
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t col = (static_cast<int64_t>(i) * 32 + t) * V;
+      if (col < a.D)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          sh[(warp * 2 + 0) * a.D + col + j] = dw[i][j];
+          sh[(warp * 2 + 1) * a.D + col + j] = db[i][j];
+        }
+    }
+    __syncthreads();
+    for (int64_t c = threadIdx.x; c < 2 * a.D; c += blockDim.x) {
+      float x = 0.f;
+      for (int k = 0; k < nwarps; ++k) x += sh[k * 2 * a.D + c];
+      part[c] = x;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t col = (static_cast<int64_t>(i) * G + t) * V;
+      if (col < a.D)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          part[col + j] = dw[i][j];
+          part[a.D + col + j] = db[i][j];
+        }
+    }
+  }
+}
+
+// Rows too long for registers: sweeps over the row, the partial sums of dw
+// and db in the block's own slice of the workspace.
+template <int DT>
+__global__ void ln_bwd_any(const LnBwdArgs a) {
+  pdl_enter();
+  __shared__ float red[96];
+  using F = Fmt<DT>;
+  using E = typename F::E;
+  const int nwarps = blockDim.x >> 5;
+  float* part = a.part != nullptr ? a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.D : nullptr;
+  const float inv_d = 1.f / static_cast<float>(a.D);
+  for (int64_t row = blockIdx.x; row < a.N; row += gridDim.x) {
+    const E* x = static_cast<const E*>(a.x) + row * a.xs0;
+    const E* gr = static_cast<const E*>(a.dout) + row * a.gs0;
+    E* dx = static_cast<E*>(a.dx) + row * a.dxs0;
+    float s[1] = {0.f};
+    for (int64_t c = threadIdx.x; c < a.D; c += blockDim.x) s[0] += F::to_f(x[c * a.xs1]);
+    row_sum<false>(s, red, nwarps);
+    const float mean = s[0] * inv_d;
+    float q[3] = {0.f, 0.f, 0.f};
+    for (int64_t c = threadIdx.x; c < a.D; c += blockDim.x) {
+      const float f = F::to_f(x[c * a.xs1]) - mean;
+      const float d = F::to_f(gr[c * a.gs1]) * (a.w != nullptr ? ld_param(a.w, c * a.ws, a.wdt) : 1.f);
+      q[0] = fmaf(f, f, q[0]);
+      q[1] += d;
+      q[2] = fmaf(d, f, q[2]);
+    }
+    row_sum<false>(q, red, nwarps);
+    const float r = rsqrtf(q[0] * inv_d + a.eps);
+    const float c1 = q[1] * inv_d, c2 = q[2] * inv_d * r;
+    for (int64_t c = threadIdx.x; c < a.D; c += blockDim.x) {
+      const float g = F::to_f(gr[c * a.gs1]);
+      const float w = a.w != nullptr ? ld_param(a.w, c * a.ws, a.wdt) : 1.f;
+      const float xh = (F::to_f(x[c * a.xs1]) - mean) * r;
+      dx[c * a.dxs1] = F::from_f(r * (g * w - c1 - xh * c2));
+      if (part != nullptr) {
+        const bool first = row == blockIdx.x;
+        part[c] = fmaf(g, xh, first ? 0.f : part[c]);
+        part[a.D + c] = g + (first ? 0.f : part[a.D + c]);
+      }
+    }
+  }
+}
+
+// dw and db: partials added in order, 8 strided subsequences and then these.
+__global__ void ln_bwd_reduce(const LnBwdArgs a, int P) {
+  pdl_enter();
+  __shared__ float sh[8][33];
+  const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + c;
+  float x = 0.f;
+  if (col < 2 * a.D)
+    for (int p = r; p < P; p += 8) x += a.part[static_cast<int64_t>(p) * 2 * a.D + col];
+  sh[r][c] = x;
+  __syncthreads();
+  if (r == 0 && col < 2 * a.D) {
+    x = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x += sh[i][c];
+    if (col < a.D) {
+      if (a.dw != nullptr) st_param(a.dw, col * a.dws, a.wdt, x);
+    } else if (a.db != nullptr) {
+      st_param(a.db, (col - a.D) * a.dbs, a.wdt, x);
+    }
+  }
+}
+
+bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+template <int DT>
+cudaError_t fwd_dt(const LnArgs& a, cudaStream_t s) {
+  constexpr int V = Fmt<DT>::VEC;
+  const bool vec = a.xs1 == 1 && a.os1 == 1 && a.D % V == 0 && al16(a.x) && al16(a.out) &&
+                   (a.N == 1 || (a.xs0 % V == 0 && a.os0 % V == 0));
+  const unsigned warps_grid = static_cast<unsigned>((a.N + 7) / 8);
+  const unsigned rows = static_cast<unsigned>(a.N);
+  auto threads = [](int64_t n, int nv) { return static_cast<unsigned>(((n + nv - 1) / nv + 31) / 32 * 32); };
+  if (vec) {
+    const int64_t n = a.D / V;
+    if (n <= 32) return launch_pdl(ln_fwd_kernel<DT, V, 1, true>, warps_grid, 256, 0, s, a);
+    if (n <= 128) return launch_pdl(ln_fwd_kernel<DT, V, 4, true>, warps_grid, 256, 0, s, a);
+    if (n <= 4096) return launch_pdl(ln_fwd_kernel<DT, V, 4, false>, rows, threads(n, 4), 0, s, a);
+  } else {
+    if (a.D <= 256) return launch_pdl(ln_fwd_kernel<DT, 1, 8, true>, warps_grid, 256, 0, s, a);
+    if (a.D <= 8192) return launch_pdl(ln_fwd_kernel<DT, 1, 8, false>, rows, threads(a.D, 8), 0, s, a);
+  }
+  return launch_pdl(ln_fwd_any<DT>, rows, 512, 0, s, a);
+}
+
+template <int DT>
+cudaError_t bwd_dt(const LnBwdArgs& a, cudaStream_t s) {
+  if (a.N == 0) {  // no rows: the parameters' gradients are zero
+    if (a.dw == nullptr && a.db == nullptr) return cudaSuccess;
+    return launch_pdl(ln_bwd_reduce, static_cast<unsigned>((2 * a.D + 31) / 32), 256, 0, s, a, 0);
+  }
+  constexpr int V = Fmt<DT>::VEC;
+  const bool vec = a.xs1 == 1 && a.gs1 == 1 && a.dxs1 == 1 && a.D % V == 0 && al16(a.x) && al16(a.dout) &&
+                   al16(a.dx) && (a.N == 1 || (a.xs0 % V == 0 && a.gs0 % V == 0 && a.dxs0 % V == 0));
+  const unsigned grid = static_cast<unsigned>(ln_bwd_blocks(a.N, a.D));
+  auto threads = [](int64_t n, int nv) { return static_cast<unsigned>(((n + nv - 1) / nv + 31) / 32 * 32); };
+  const size_t warp_sh = static_cast<size_t>(a.D) * 2 * 8 * sizeof(float);
+  const size_t row_sh = 96 * sizeof(float);
+  cudaError_t e;
+  if (vec && a.D <= 32 * V)
+    e = launch_pdl(ln_bwd_kernel<DT, V, 1, true, 256>, grid, 256, warp_sh, s, a);
+  else if (!vec && a.D <= 128)
+    e = launch_pdl(ln_bwd_kernel<DT, 1, 4, true, 256>, grid, 256, warp_sh, s, a);
+  else if (vec && a.D <= 1024 * V)
+    e = launch_pdl(ln_bwd_kernel<DT, V, 2, false, 512>, grid, threads(a.D / V, 2), row_sh, s, a);
+  else if (vec && a.D <= 2048 * V)
+    e = launch_pdl(ln_bwd_kernel<DT, V, 2, false, 1024>, grid, threads(a.D / V, 2), row_sh, s, a);
+  else if (!vec && a.D <= 4096)
+    e = launch_pdl(ln_bwd_kernel<DT, 1, 4, false, 1024>, grid, threads(a.D, 4), row_sh, s, a);
+  else
+    e = launch_pdl(ln_bwd_any<DT>, grid, 512, 0, s, a);
+  if (e != cudaSuccess || a.part == nullptr) return e;
+  return launch_pdl(ln_bwd_reduce, static_cast<unsigned>((2 * a.D + 31) / 32), 256, 0, s, a, static_cast<int>(grid));
+}
+
+}  // namespace
+
+cudaError_t launch_ln_fwd(const LnArgs& a, Dtype dt, cudaStream_t stream) {
+  switch (dt) {
+    case kF32: return fwd_dt<kF32>(a, stream);
+    case kF16: return fwd_dt<kF16>(a, stream);
+    case kBF16: return fwd_dt<kBF16>(a, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+// Two blocks for each of 304 (two per SM of a 152-SM device); a block of the
+// warp-per-row kernels takes at least eight rows.
+int64_t ln_bwd_blocks(int64_t N, int64_t D) {
+  const int64_t rows = D <= 256 ? (N + 7) / 8 : N;
+  return rows < 608 ? rows : 608;
+}
+
+cudaError_t launch_ln_bwd(const LnBwdArgs& a, Dtype dt, cudaStream_t stream) {
+  switch (dt) {
+    case kF32: return bwd_dt<kF32>(a, stream);
+    case kF16: return bwd_dt<kF16>(a, stream);
+    case kBF16: return bwd_dt<kBF16>(a, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace ccv

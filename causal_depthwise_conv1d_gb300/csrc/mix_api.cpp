@@ -1,0 +1,355 @@
+// C-ABI front end of the gated delta rule (ccv_gdr_*) and of layer
+// normalisation (ccv_ln_*): argument validation, kernel selection and launch
+// on the caller's stream.  See include/ccv.h for the contract.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ccv.h"
+#include "mix_internal.h"
+
+namespace {
+
+using ccv::api_fail;
+
+ccv_status fail_invalid(const char* name, const char* what) {
+  return static_cast<ccv_status>(api_fail(CCV_ERR_INVALID_ARG, "%s %s", name, what));
+}
+
+#define CCV_FAIL(st, ...) return static_cast<ccv_status>(api_fail(st, __VA_ARGS__))
+#define CCV_TRY(expr)                  \
+  do {                                 \
+    const ccv_status st_ = (expr);     \
+    if (st_ != CCV_OK) return st_;     \
+  } while (0)
+
+bool valid_dtype(ccv_dtype d) { return d == CCV_F32 || d == CCV_F16 || d == CCV_BF16; }
+int64_t dtype_size(ccv_dtype d) { return d == CCV_F32 ? 4 : 2; }
+
+// The tensors of one call: each is checked when it is added (strides given,
+// alignment, extent, an output's elements distinct), and then the outputs are
+// checked against all others.
+class Tensors {
+ public:
+  ccv_status add(const char* name, const void* p, const int64_t* strides, int nd, const int64_t* shape, int64_t esz,
+                 bool out, bool required) {
+    bool empty = false;
+    for (int d = 0; d < nd; ++d) empty |= shape[d] == 0;
+    if (empty) return CCV_OK;
+    if (p == nullptr) {
+      if (required) return fail_invalid(name, "is required");
+      return CCV_OK;
+    }
+    if (strides == nullptr) return fail_invalid(name, "needs its strides");
+    if (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(esz) != 0)
+      return fail_invalid(name, "must be aligned to its element size");
+    __int128 lo = 0, hi = 0;
+    for (int d = 0; d < nd; ++d) {
+      const __int128 span = static_cast<__int128>(strides[d]) * (shape[d] - 1);
+      if (span < 0) lo += span; else hi += span;
+      if (out && shape[d] > 1 && strides[d] == 0) return fail_invalid(name, "has a zero stride on a dimension of size > 1");
+    }
+    const __int128 lim = static_cast<__int128>(INT64_MAX) / 16;
+    if (lo < -lim || hi > lim) return fail_invalid(name, "extent overflows int64");
+    T& t = t_[n_++];
+    t.name = name;
+    t.base = static_cast<const char*>(p);
+    t.lo = t.base + static_cast<int64_t>(lo) * esz;
+    t.hi = t.base + static_cast<int64_t>(hi) * esz + (esz - 1);
+    t.esz = esz;
+    t.out = out;
+    t.nd = nd;
+    for (int d = 0; d < nd; ++d) {
+      t.strides[d] = strides[d];
+      t.shape[d] = shape[d];
+    }
+    return CCV_OK;
+  }
+
+  // No output shares an element with another tensor.  Views that interleave
+  // token by token (channel slices of one buffer) are told apart; other
+  // interleaved views of different strides are the caller's responsibility.
+  ccv_status disjoint() const {
+    for (int i = 0; i < n_; ++i) {
+      if (!t_[i].out) continue;
+      for (int j = 0; j < n_; ++j) {
+        if (j == i) continue;
+        const T &a = t_[i], &b = t_[j];
+        if (a.lo > b.hi || b.lo > a.hi) continue;
+        if (a.base == b.base || overlaps(a, b))
+          return static_cast<ccv_status>(
+              api_fail(CCV_ERR_INVALID_ARG, "%s must not alias or overlap %s", a.name, b.name));
+      }
+    }
+    return CCV_OK;
+  }
+
+ private:
+  struct T {
+    const char* name;
+    const char *base, *lo, *hi;
+    int64_t esz;
+    int nd;
+    bool out;
+    int64_t strides[4], shape[4];
+  };
+
+  static bool dense(const T& t) {  // every element between lo and hi belongs to it
+    __int128 n = t.esz;
+    for (int d = 0; d < t.nd; ++d) n *= t.shape[d];
+    return n == static_cast<__int128>(t.hi - t.lo) + 1;
+  }
+
+  static bool overlaps(const T& a, const T& b) {
+    if (dense(a) || dense(b)) return true;
+    if (a.nd < 2 || b.nd < 2 || a.esz != b.esz) return false;
+    // channel slices: the same token stride, and the channels of one token
+    // inside one stride, apart from each other
+    const int64_t sa = a.strides[1] * a.esz, sb = b.strides[1] * b.esz;
+    if (a.nd != 4 || b.nd != 4 || sa != sb || sa <= 0) return false;
+    int64_t w[2];
+    const T* t[2] = {&a, &b};
+    for (int k = 0; k < 2; ++k) {
+      w[k] = t[k]->esz;
+      for (int d = 2; d < 4; ++d) {
+        if (t[k]->strides[d] < 0) return false;
+        w[k] += t[k]->strides[d] * (t[k]->shape[d] - 1) * t[k]->esz;
+      }
+    }
+    if (w[0] > sa || w[1] > sa) return false;
+    int64_t m = (b.base - a.base) % sa;
+    if (m < 0) m += sa;
+    return !(m >= w[0] && m + w[1] <= sa);
+  }
+
+  T t_[20];
+  int n_ = 0;
+};
+
+ccv_status check_gdr_sizes(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int64_t max_dk,
+                           ccv_dtype dtype) {
+  if (B < 0 || L < 0 || Hk < 0 || Hv < 0 || Dk < 0 || Dv < 0)
+    CCV_FAIL(CCV_ERR_INVALID_ARG, "B, L, Hk, Hv, Dk and Dv must be >= 0");
+  if (!valid_dtype(dtype)) CCV_FAIL(CCV_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dtype));
+  if (Hv > 0 && (Hk == 0 || Hv % Hk != 0))
+    CCV_FAIL(CCV_ERR_INVALID_ARG, "Hv must be a multiple of Hk (got %lld, %lld)", (long long)Hv, (long long)Hk);
+  if (Dk > max_dk)
+    CCV_FAIL(CCV_ERR_UNSUPPORTED, "Dk must be at most %lld (got %lld)", (long long)max_dk, (long long)Dk);
+  if (Dk == 0 && Hv > 0 && Dv > 0) CCV_FAIL(CCV_ERR_INVALID_ARG, "Dk must be >= 1");
+  // counts and the index arithmetic on them stay within int64, grids within int32
+  const __int128 lim = static_cast<__int128>(INT64_MAX) >> 8;
+  const __int128 n = static_cast<__int128>(B) * (L > 0 ? L : 1) * (Hv > 0 ? Hv : 1);
+  if (n > lim || n * (Dv > 0 ? Dv : 1) > lim || n * (Dk > 0 ? Dk : 1) > lim || L > 0x7fffffc0)
+    CCV_FAIL(CCV_ERR_INVALID_ARG, "B*L*Hv*Dv is too large");
+  if (static_cast<__int128>(B) * Hv * ((Dv + 15) / 16) > 0x7fffffff ||
+      static_cast<__int128>(B) * Hk * ((L + ccv::kGdrChunk - 1) / ccv::kGdrChunk) > 0x7fffffff)
+    CCV_FAIL(CCV_ERR_INVALID_ARG, "B*Hv*Dv is too large");
+  return CCV_OK;
+}
+
+void copy(int64_t* dst, const int64_t* src, int n) {
+  for (int i = 0; i < n; ++i) dst[i] = src != nullptr ? src[i] : 0;
+}
+
+ccv_status launched(cudaError_t err, const char* kernel) {
+  if (err != cudaSuccess) {
+    ccv::api_kernel("none");
+    CCV_FAIL(CCV_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(err));
+  }
+  ccv::api_kernel(kernel);
+  return CCV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ccv_status ccv_gdr_fwd(const void* q, const int64_t q_strides[4], const void* k, const int64_t k_strides[4],
+                       const void* v, const int64_t v_strides[4], const float* g, const int64_t g_strides[3],
+                       const void* beta, const int64_t beta_strides[3], const int32_t* seq_idx,
+                       const int64_t seq_idx_strides[2], const float* initial_state,
+                       const int64_t initial_state_strides[4], void* out, const int64_t out_strides[4],
+                       float* final_state_out, const int64_t final_state_strides[4], void* workspace,
+                       uint64_t workspace_bytes, int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
+                       float scale, ccv_dtype dtype, void* stream) {
+  ccv::api_begin();
+  CCV_TRY(check_gdr_sizes(B, L, Hk, Hv, Dk, Dv, ccv::kGdrMaxDk, dtype));
+  if (B == 0 || Hv == 0 || Dv == 0) {
+    ccv::api_kernel("none");
+    return CCV_OK;
+  }
+  const int64_t e = dtype_size(dtype);
+  const int64_t qk[4] = {B, L, Hk, Dk}, vo[4] = {B, L, Hv, Dv}, gate[3] = {B, L, Hv}, st[4] = {B, Hv, Dk, Dv},
+                ids[2] = {B, L};
+  Tensors t;
+  CCV_TRY(t.add("q", q, q_strides, 4, qk, e, false, true));
+  CCV_TRY(t.add("k", k, k_strides, 4, qk, e, false, true));
+  CCV_TRY(t.add("v", v, v_strides, 4, vo, e, false, true));
+  CCV_TRY(t.add("g", g, g_strides, 3, gate, 4, false, true));
+  CCV_TRY(t.add("beta", beta, beta_strides, 3, gate, e, false, true));
+  CCV_TRY(t.add("seq_idx", seq_idx, seq_idx_strides, 2, ids, 4, false, false));
+  CCV_TRY(t.add("initial_state", initial_state, initial_state_strides, 4, st, 4, false, false));
+  CCV_TRY(t.add("out", out, out_strides, 4, vo, e, true, true));
+  CCV_TRY(t.add("final_state_out", final_state_out, final_state_strides, 4, st, 4, true, false));
+  CCV_TRY(t.disjoint());
+  if (L == 0 && final_state_out == nullptr) {
+    ccv::api_kernel("none");
+    return CCV_OK;
+  }
+  (void)workspace;
+  (void)workspace_bytes;
+  ccv::Device dev;
+  CCV_TRY(static_cast<ccv_status>(ccv::api_device(&dev)));
+  ccv::GdrArgs a = {};
+  a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.seq = seq_idx, a.s0 = initial_state, a.s1 = final_state_out;
+  a.out = out;
+  copy(a.qs, q_strides, 4), copy(a.ks, k_strides, 4), copy(a.vs, v_strides, 4), copy(a.gs, g_strides, 3);
+  copy(a.bs, beta_strides, 3), copy(a.ss, seq_idx_strides, 2), copy(a.s0s, initial_state_strides, 4);
+  copy(a.s1s, final_state_strides, 4), copy(a.os, out_strides, 4);
+  a.B = B, a.L = L, a.Hk = Hk, a.Hv = Hv, a.Dk = Dk, a.Dv = Dv, a.scale = scale;
+  return launched(ccv::launch_gdr_step(a, static_cast<ccv::Dtype>(dtype), dev, static_cast<cudaStream_t>(stream)),
+                  "gdr_step");
+}
+
+ccv_status ccv_gdr_fwd_workspace_size(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
+                                      ccv_dtype dtype, uint64_t* bytes) {
+  ccv::api_begin();
+  if (bytes == nullptr) CCV_FAIL(CCV_ERR_INVALID_ARG, "bytes is required");
+  CCV_TRY(check_gdr_sizes(B, L, Hk, Hv, Dk, Dv, ccv::kGdrMaxDk, dtype));
+  *bytes = 0;
+  return CCV_OK;
+}
+
+ccv_status ccv_gdr_step(const void* q, const int64_t q_strides[4], const void* k, const int64_t k_strides[4],
+                        const void* v, const int64_t v_strides[4], const float* g, const int64_t g_strides[3],
+                        const void* beta, const int64_t beta_strides[3], float* state, const int64_t state_strides[4],
+                        int64_t n_slots, const int32_t* state_indices, int64_t state_indices_stride, void* out,
+                        const int64_t out_strides[4], int64_t B, int64_t S, int64_t Hk, int64_t Hv, int64_t Dk,
+                        int64_t Dv, float scale, ccv_dtype dtype, void* stream) {
+  ccv::api_begin();
+  CCV_TRY(check_gdr_sizes(B, S, Hk, Hv, Dk, Dv, ccv::kGdrMaxDk, dtype));
+  if (n_slots < 0) CCV_FAIL(CCV_ERR_INVALID_ARG, "n_slots must be >= 0");
+  if (state_indices == nullptr && n_slots < B)
+    CCV_FAIL(CCV_ERR_INVALID_ARG, "n_slots must be at least B without state_indices");
+  if (B == 0 || Hv == 0 || Dv == 0 || S == 0) {
+    ccv::api_kernel("none");
+    return CCV_OK;
+  }
+  const int64_t e = dtype_size(dtype);
+  const int64_t qk[4] = {B, S, Hk, Dk}, vo[4] = {B, S, Hv, Dv}, gate[3] = {B, S, Hv},
+                st[4] = {n_slots, Hv, Dk, Dv}, idx[1] = {B};
+  Tensors t;
+  CCV_TRY(t.add("q", q, q_strides, 4, qk, e, false, true));
+  CCV_TRY(t.add("k", k, k_strides, 4, qk, e, false, true));
+  CCV_TRY(t.add("v", v, v_strides, 4, vo, e, false, true));
+  CCV_TRY(t.add("g", g, g_strides, 3, gate, 4, false, true));
+  CCV_TRY(t.add("beta", beta, beta_strides, 3, gate, e, false, true));
+  CCV_TRY(t.add("state_indices", state_indices, &state_indices_stride, 1, idx, 4, false, false));
+  CCV_TRY(t.add("state", state, state_strides, 4, st, 4, true, true));
+  CCV_TRY(t.add("out", out, out_strides, 4, vo, e, true, true));
+  CCV_TRY(t.disjoint());
+  ccv::Device dev;
+  CCV_TRY(static_cast<ccv_status>(ccv::api_device(&dev)));
+  ccv::GdrArgs a = {};
+  a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.s0 = state, a.s1 = state, a.out = out;
+  a.slots = state_indices, a.slot_stride = state_indices_stride, a.n_slots = n_slots;
+  copy(a.qs, q_strides, 4), copy(a.ks, k_strides, 4), copy(a.vs, v_strides, 4), copy(a.gs, g_strides, 3);
+  copy(a.bs, beta_strides, 3), copy(a.s0s, state_strides, 4), copy(a.s1s, state_strides, 4);
+  copy(a.os, out_strides, 4);
+  a.B = B, a.L = S, a.Hk = Hk, a.Hv = Hv, a.Dk = Dk, a.Dv = Dv, a.scale = scale;
+  return launched(ccv::launch_gdr_step(a, static_cast<ccv::Dtype>(dtype), dev, static_cast<cudaStream_t>(stream)),
+                  "gdr_step");
+}
+
+}  // extern "C"
+
+namespace {
+
+ccv_status check_ln(int64_t N, int64_t D, float eps, ccv_dtype dtype, ccv_dtype wdtype) {
+  if (N < 0 || D < 0) CCV_FAIL(CCV_ERR_INVALID_ARG, "N and D must be >= 0");
+  if (!valid_dtype(dtype)) CCV_FAIL(CCV_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dtype));
+  if (!valid_dtype(wdtype)) CCV_FAIL(CCV_ERR_INVALID_ARG, "unknown weight dtype %d", static_cast<int>(wdtype));
+  if (!(eps >= 0.f)) CCV_FAIL(CCV_ERR_INVALID_ARG, "eps must be >= 0");
+  if (N > 0x7fffffff || D > 0x7fffffff / 2 || static_cast<__int128>(N) * D > (INT64_MAX >> 4))
+    CCV_FAIL(CCV_ERR_INVALID_ARG, "N*D is too large");
+  return CCV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ccv_status ccv_ln_fwd(const void* x, const int64_t x_strides[2], const void* weight, int64_t weight_stride,
+                      const void* bias, int64_t bias_stride, void* out, const int64_t out_strides[2], int64_t N,
+                      int64_t D, float eps, ccv_dtype dtype, ccv_dtype weight_dtype, void* stream) {
+  ccv::api_begin();
+  CCV_TRY(check_ln(N, D, eps, dtype, weight_dtype));
+  if (N == 0 || D == 0) {
+    ccv::api_kernel("none");
+    return CCV_OK;
+  }
+  const int64_t nd[2] = {N, D}, d[1] = {D};
+  const int64_t e = dtype_size(dtype), we = dtype_size(weight_dtype);
+  Tensors t;
+  CCV_TRY(t.add("x", x, x_strides, 2, nd, e, false, true));
+  CCV_TRY(t.add("weight", weight, &weight_stride, 1, d, we, false, false));
+  CCV_TRY(t.add("bias", bias, &bias_stride, 1, d, we, false, false));
+  CCV_TRY(t.add("out", out, out_strides, 2, nd, e, true, true));
+  CCV_TRY(t.disjoint());
+  ccv::LnArgs a = {x, x_strides[0], x_strides[1], weight, weight_stride, bias, bias_stride,
+                   out, out_strides[0], out_strides[1], N, D, eps, static_cast<int>(weight_dtype)};
+  return launched(ccv::launch_ln_fwd(a, static_cast<ccv::Dtype>(dtype), static_cast<cudaStream_t>(stream)), "ln_fwd");
+}
+
+ccv_status ccv_ln_bwd_workspace_size(int64_t N, int64_t D, uint64_t* bytes) {
+  ccv::api_begin();
+  if (bytes == nullptr) CCV_FAIL(CCV_ERR_INVALID_ARG, "bytes is required");
+  CCV_TRY(check_ln(N, D, 0.f, CCV_F32, CCV_F32));
+  *bytes = static_cast<uint64_t>(ccv::ln_bwd_blocks(N, D)) * 2u * static_cast<uint64_t>(D) * sizeof(float);
+  return CCV_OK;
+}
+
+ccv_status ccv_ln_bwd(const void* x, const int64_t x_strides[2], const void* weight, int64_t weight_stride,
+                      const void* dout, const int64_t dout_strides[2], void* dx, const int64_t dx_strides[2],
+                      void* dweight, int64_t dweight_stride, void* dbias, int64_t dbias_stride, void* workspace,
+                      uint64_t workspace_bytes, int64_t N, int64_t D, float eps, ccv_dtype dtype,
+                      ccv_dtype weight_dtype, void* stream) {
+  ccv::api_begin();
+  CCV_TRY(check_ln(N, D, eps, dtype, weight_dtype));
+  if (D == 0) {
+    ccv::api_kernel("none");
+    return CCV_OK;
+  }
+  const int64_t nd[2] = {N, D}, d[1] = {D};
+  const int64_t e = dtype_size(dtype), we = dtype_size(weight_dtype);
+  const bool params = dweight != nullptr || dbias != nullptr;
+  const uint64_t need =
+      params ? static_cast<uint64_t>(ccv::ln_bwd_blocks(N, D)) * 2u * static_cast<uint64_t>(D) * sizeof(float) : 0;
+  Tensors t;
+  CCV_TRY(t.add("x", x, x_strides, 2, nd, e, false, true));
+  CCV_TRY(t.add("weight", weight, &weight_stride, 1, d, we, false, false));
+  CCV_TRY(t.add("dout", dout, dout_strides, 2, nd, e, false, true));
+  CCV_TRY(t.add("dx", dx, dx_strides, 2, nd, e, true, true));
+  CCV_TRY(t.add("dweight", dweight, &dweight_stride, 1, d, we, true, false));
+  CCV_TRY(t.add("dbias", dbias, &dbias_stride, 1, d, we, true, false));
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need)
+      CCV_FAIL(CCV_ERR_INVALID_ARG, "workspace too small: need %llu bytes (got %llu)", (unsigned long long)need,
+               (unsigned long long)(workspace ? workspace_bytes : 0));
+    const int64_t wsh[1] = {static_cast<int64_t>((need + 15) / 16)}, one = 1;
+    CCV_TRY(t.add("workspace", workspace, &one, 1, wsh, 16, true, true));
+  }
+  CCV_TRY(t.disjoint());
+  ccv::LnBwdArgs a = {};
+  a.x = x, a.w = weight, a.ws = weight_stride, a.dout = dout, a.dx = dx;
+  a.dw = dweight, a.dws = dweight_stride, a.db = dbias, a.dbs = dbias_stride;
+  a.part = need > 0 ? static_cast<float*>(workspace) : nullptr;
+  if (N > 0) {
+    a.xs0 = x_strides[0], a.xs1 = x_strides[1], a.gs0 = dout_strides[0], a.gs1 = dout_strides[1];
+    a.dxs0 = dx_strides[0], a.dxs1 = dx_strides[1];
+  }
+  a.N = N, a.D = D, a.eps = eps, a.wdt = static_cast<int>(weight_dtype);
+  return launched(ccv::launch_ln_bwd(a, static_cast<ccv::Dtype>(dtype), static_cast<cudaStream_t>(stream)), "ln_bwd");
+}
+
+}  // extern "C"

@@ -317,6 +317,118 @@ ccv_status ccv_bwd_mixed(const void* x, const int64_t x_strides[3],
                          int64_t B, int64_t C, int64_t L, int K,
                          ccv_dtype dtype, ccv_dtype weight_dtype, ccv_activation activation, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Sequence mixing behind the convolution, and the block's normalisation.
+ * Execution, memory model, errors and thread safety as stated above: device
+ * pointers with signed element strides, validation on the host, kernels
+ * enqueued on `stream`, nothing allocated.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * ccv_gdr_fwd -- gated delta rule over whole sequences.
+ *
+ * For every batch row b and value head h, with a state S [Dk,Dv] that starts
+ * as initial_state (or zero), token by token:
+ *     S <- exp(g[b,t,h]) S
+ *     u  = beta[b,t,h] (v[b,t,h,:] - k[b,t,h',:]^T S)
+ *     S <- S + k[b,t,h',:] u^T
+ *     out[b,t,h,:] = scale q[b,t,h',:]^T S
+ * where h' = h / (Hv/Hk): each key head serves Hv/Hk adjacent value heads.
+ *
+ *   q, k              [B,L,Hk,Dk], strides q_strides, k_strides.
+ *   v, out            [B,L,Hv,Dv].
+ *   g                 FP32 [B,L,Hv], the logarithm of the decay (usually <= 0).
+ *   beta              [B,L,Hv] in dtype.
+ *   seq_idx           int32 [B,L] or NULL.  Where seq_idx[b,t] differs from
+ *                     seq_idx[b,t-1] a new sequence begins: token t sees the
+ *                     zero state.  initial_state belongs to the sequence of
+ *                     token 0.
+ *   initial_state     FP32 [B,Hv,Dk,Dv] or NULL (zero).
+ *   final_state_out   FP32 [B,Hv,Dk,Dv] or NULL; the state after token L-1.
+ *   workspace         device buffer of ccv_gdr_fwd_workspace_size() bytes,
+ *                     128-byte aligned (may be NULL where that is 0).  Contents
+ *                     undefined before and after; calls in flight at the same
+ *                     time must not share it.
+ *   Dk                1..256.  Dv >= 1.  Any strides; rows of 16-byte aligned
+ *                     vectors with unit stride in the last dimension are the
+ *                     fast ones.
+ *   dtype             of q, k, v, beta and out.  All arithmetic keeps at least
+ *                     FP32 precision; out is rounded once (nearest even).
+ *
+ * out and final_state_out must not share memory with an input or each other.
+ * Non-finite values affect what the token-by-token definition says, and
+ * nothing before their own token or across a change of seq_idx.
+ * B, Hv or Dv == 0 is a no-op; L == 0 copies the initial state.
+ */
+ccv_status ccv_gdr_fwd(const void* q, const int64_t q_strides[4], const void* k, const int64_t k_strides[4],
+                       const void* v, const int64_t v_strides[4], const float* g, const int64_t g_strides[3],
+                       const void* beta, const int64_t beta_strides[3], const int32_t* seq_idx,
+                       const int64_t seq_idx_strides[2], const float* initial_state,
+                       const int64_t initial_state_strides[4], void* out, const int64_t out_strides[4],
+                       float* final_state_out, const int64_t final_state_strides[4], void* workspace,
+                       uint64_t workspace_bytes, int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
+                       float scale, ccv_dtype dtype, void* stream);
+
+/* Bytes of workspace ccv_gdr_fwd needs for these sizes (0: none).  Host only. */
+ccv_status ccv_gdr_fwd_workspace_size(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
+                                      ccv_dtype dtype, uint64_t* bytes);
+
+/*
+ * ccv_gdr_step -- gated delta rule, decode step: S new tokens per request
+ * (S is usually 1) against a cache of states, advanced in place.
+ *
+ * The operation is ccv_gdr_fwd without seq_idx whose initial state is the
+ * request's slot of the cache and whose final state overwrites it.
+ *
+ *   state             FP32 [n_slots,Hv,Dk,Dv], read and overwritten.
+ *   state_indices     int32 [B] or NULL (request b uses slot b).  A negative
+ *                     index, or one >= n_slots, marks a padding row: no state
+ *                     is touched and its outputs are zero.  Two requests of
+ *                     one call must not name the same slot.
+ *   q, k, v, g, beta, out as for ccv_gdr_fwd with L = S.
+ */
+ccv_status ccv_gdr_step(const void* q, const int64_t q_strides[4], const void* k, const int64_t k_strides[4],
+                        const void* v, const int64_t v_strides[4], const float* g, const int64_t g_strides[3],
+                        const void* beta, const int64_t beta_strides[3], float* state, const int64_t state_strides[4],
+                        int64_t n_slots, const int32_t* state_indices, int64_t state_indices_stride, void* out,
+                        const int64_t out_strides[4], int64_t B, int64_t S, int64_t Hk, int64_t Hv, int64_t Dk,
+                        int64_t Dv, float scale, ccv_dtype dtype, void* stream);
+
+/*
+ * ccv_ln_fwd -- layer normalisation of the rows of x [N,D]:
+ *     out = (x - mean) / sqrt(var + eps) * weight + bias,
+ * mean and (biased) variance over the row in FP32, out rounded once to dtype.
+ *
+ *   weight, bias      [D] in weight_dtype, or NULL (one, zero); any of the
+ *                     nine pairs of dtype and weight_dtype.
+ *   eps               >= 0.
+ * out must not share memory with an input.  N or D == 0 is a no-op.
+ */
+ccv_status ccv_ln_fwd(const void* x, const int64_t x_strides[2], const void* weight, int64_t weight_stride,
+                      const void* bias, int64_t bias_stride, void* out, const int64_t out_strides[2], int64_t N,
+                      int64_t D, float eps, ccv_dtype dtype, ccv_dtype weight_dtype, void* stream);
+
+/*
+ * ccv_ln_bwd -- its backward pass.  The row statistics are taken again from x:
+ * nothing has to be kept from the forward pass.  With xh the normalised row
+ * and d = dout * weight:
+ *     dx      = (d - mean(d) - xh mean(d xh)) / sqrt(var + eps)
+ *     dweight = sum over rows of dout * xh,   dbias = sum over rows of dout
+ *   dx                [N,D] in dtype, required.
+ *   dweight, dbias    [D] in weight_dtype, or NULL.  Summed in FP32 in a fixed
+ *                     order (bitwise reproducible); zero where N == 0.
+ *   workspace         ccv_ln_bwd_workspace_size() bytes, 16-byte aligned;
+ *                     needed when dweight or dbias is requested.
+ */
+ccv_status ccv_ln_bwd(const void* x, const int64_t x_strides[2], const void* weight, int64_t weight_stride,
+                      const void* dout, const int64_t dout_strides[2], void* dx, const int64_t dx_strides[2],
+                      void* dweight, int64_t dweight_stride, void* dbias, int64_t dbias_stride, void* workspace,
+                      uint64_t workspace_bytes, int64_t N, int64_t D, float eps, ccv_dtype dtype,
+                      ccv_dtype weight_dtype, void* stream);
+
+/* Bytes of workspace ccv_ln_bwd needs (0 where N or D is 0).  Host only. */
+ccv_status ccv_ln_bwd_workspace_size(int64_t N, int64_t D, uint64_t* bytes);
+
 /* Message for the last non-OK status returned on the calling thread ("" if
  * none).  The pointer stays valid until the next ccv_* call on that thread. */
 const char* ccv_last_error(void);
@@ -324,7 +436,7 @@ const char* ccv_last_error(void);
 /* Name of the kernel variant the last successful ccv_fwd, ccv_update or
  * ccv_bwd on this thread enqueued (e.g. "time_vec", "chlast_tma",
  * "chlast_vec", "generic", "update", "bwd_time", "bwd_chlast",
- * "bwd_generic", "none"). */
+ * "bwd_generic", "gdr_step", "ln_fwd", "ln_bwd", "none"). */
 const char* ccv_last_kernel(void);
 
 /* Library ABI version: (major << 16) | minor. */
