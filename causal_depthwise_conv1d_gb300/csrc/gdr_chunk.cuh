@@ -1,0 +1,206 @@
+// Shared by the chunked kernels of the gated delta rule.
+//
+// A sequence is cut into chunks of C = 64 tokens.  With G_i the cumulative
+// log decay inside the chunk, Gam_ij = exp(G_i - G_j) for j <= i (0 where a
+// new sequence begins between them), S0 the state before the chunk:
+//
+//   L_ij = beta_i Gam_ij k_i.k_j (j < i),   T = (I + L)^-1,   P_ij = Gam_ij q_i.k_j (j <= i)
+//   E = V - gi (K S0),   U = T (beta E),   O = scale (gi (Q S0) + P U),   S1 = ga S0 + K^T (gc U)
+//
+// with gi_i = exp(G_i), gc_i = exp(G_last - G_i), ga = exp(G_last) (0 across a
+// new sequence).  One kernel (gdr_prep.cu) makes what does not depend on the
+// state, for all chunks at once; another (gdr_scan.cu) carries the state.
+//
+// Precision.  The state and all sums are FP32.  The products run on FP16
+// tensor instructions with FP32 accumulation; an FP32 operand x enters as two
+// FP16 numbers, hi = fp16(s x) and lo = fp16(s x - hi), where s is the power
+// of two that brings the largest magnitude of x's row (the index that is not
+// summed over) to [2^14, 2^15).  hi + lo holds 22 bits of the row's largest
+// element, and 2^28 below it still 11 bits.  16-bit inputs are exact in hi,
+// so a product with q or k takes two instructions (hi and lo of the other
+// factor), a product of two FP32 operands three (lo lo is below 2^-22).  The
+// row factors are powers of two and are taken out exactly in FP32.
+#pragma once
+
+#include "ccv_common.cuh"
+#include "ccv_tma.cuh"
+#include "mix_internal.h"
+
+namespace ccv {
+
+constexpr int kC = kGdrChunk;
+
+// Per-chunk factors in FP32: a head of kVecHead floats, then arrays of 64.
+constexpr int kVecHead = 16;
+enum VecHead { kHdGa = 0, kHdBad = 1 };
+enum VecSlot {
+  kVKS = 0,     // gi / k's factor: true gi (K S0) from the scaled product
+  kVQS = 1,     // scale gi / q's factor
+  kVP = 2,      // scale / P's row factor
+  kVBeta = 3,
+  kVTInv = 4,   // 1 / T's row factor
+  kVU = 5,      // gc / k's factor
+  kVGi = 6,     // the remaining slots serve the backward pass
+  kVGc = 7,
+  kVKInv = 8,   // 1 / k's row factor
+  kVQInv = 9,
+  kVPInv = 10,
+  kVGHi = 11,   // G as a sum of two floats
+  kVGLo = 12,
+  kVSeg = 13,   // number of sequence starts in the chunk up to the token (as an integer)
+  kVSlots = 14
+};
+constexpr int kVecBytes = 4096;
+constexpr int kVecFwdBytes = (kVecHead + 6 * kC) * 4;  // what the forward scan reads
+static_assert((kVecHead + kVSlots * kC) * 4 <= kVecBytes, "vector part");
+constexpr int kMatBytes = kC * kC * 2;                     // one FP16 64 x 64 matrix
+constexpr int kPackBytes = kVecBytes + 4 * kMatBytes;      // factors, T hi, T lo, P hi, P lo
+
+// Bytes of the [64, DK] FP16 tiles of k and q of one chunk and key head
+// (hi, and lo for FP32 inputs): k hi, (k lo,) q hi, (q lo).
+__host__ __device__ constexpr int qk_tile_bytes(int DK) { return kC * DK * 2; }
+__host__ __device__ constexpr int qk_pack_bytes(int DK, int terms) { return 2 * terms * qk_tile_bytes(DK); }
+
+// Tiles are rows of RB bytes in 16-byte pieces; piece p of row r lies at
+// p ^ (r & 7), so the eight rows of a matrix load touch all banks.
+template <int RB>
+__device__ __forceinline__ uint32_t tile_off(int row, int piece) {
+  return static_cast<uint32_t>(row * RB + ((piece ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void stsm4t(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+// B operand of two column tiles (n0, n0 + 8) and 16 summed indices: rows of
+// the tile are columns of B (summed index along the row).
+template <int RB>
+__device__ __forceinline__ uint32_t addr_b(uint32_t tile, int n0, int piece, int lane) {
+  return tile + tile_off<RB>(n0 + (lane & 7) + ((lane >> 4) & 1) * 8, piece + ((lane >> 3) & 1));
+}
+
+// The same where rows of the tile are the summed index (transposed load).
+template <int RB>
+__device__ __forceinline__ uint32_t addr_bt(uint32_t tile, int k0, int piece, int lane) {
+  return tile + tile_off<RB>(k0 + (lane & 7) + ((lane >> 3) & 1) * 8, piece + (lane >> 4));
+}
+
+// A operand: 16 rows of the tile from r0, 16 summed indices along the row.
+template <int RB>
+__device__ __forceinline__ uint32_t addr_a(uint32_t tile, int r0, int piece, int lane) {
+  return tile + tile_off<RB>(r0 + (lane & 7) + ((lane >> 3) & 1) * 8, piece + (lane >> 4));
+}
+
+// A operand where rows of the tile are the summed index (transposed load):
+// 16 columns from piece's first, 16 rows from k0.
+template <int RB>
+__device__ __forceinline__ uint32_t addr_at(uint32_t tile, int k0, int piece, int lane) {
+  return tile + tile_off<RB>(k0 + (lane & 7) + ((lane >> 4) & 1) * 8, piece + ((lane >> 3) & 1));
+}
+
+// d += a b for 16 x 8 x 16, FP16 operands, FP32 sums.
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// hi = fp16(x, y), lo = fp16(x - hi, y - hi).
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = h2(x - f.x, y - f.y);
+}
+
+__device__ __forceinline__ unsigned mag(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+constexpr unsigned kInfBits = 0x7f800000u;  // magnitudes from here on are not finite
+
+// Power of two that brings a finite magnitude to [2^14, 2^15), and its inverse.
+__device__ __forceinline__ void row_factor(unsigned m, float& f, float& inv) {
+  const unsigned e = max(15u, min(254u, m >> 23));
+  f = __uint_as_float((268u - e) << 23);
+  inv = __uint_as_float((e - 14u) << 23);
+}
+
+__device__ __forceinline__ unsigned quad_max(unsigned m) {
+  m = max(m, __shfl_xor_sync(kFullMask, m, 1));
+  return max(m, __shfl_xor_sync(kFullMask, m, 2));
+}
+
+__device__ __forceinline__ unsigned warp_max(unsigned m) {
+  return __reduce_max_sync(kFullMask, m);
+}
+
+// 16 x 64 accumulator fragments (8 column tiles) as A operands of the next
+// product: each row scaled by its factor and split.  Returns the inverse
+// factors of rows g and g + 8; `bad` is set where a value is not finite.
+template <int NT, bool LO>
+__device__ __forceinline__ void split_rows(const float (&x)[NT][4], uint32_t (&hi)[NT / 2][4],
+                                           uint32_t (&lo)[NT / 2][4], float& inv0, float& inv1, bool& bad) {
+  unsigned m0 = 0, m1 = 0;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    m0 = max(m0, max(mag(x[i][0]), mag(x[i][1])));
+    m1 = max(m1, max(mag(x[i][2]), mag(x[i][3])));
+  }
+  m0 = quad_max(m0);
+  m1 = quad_max(m1);
+  bad = bad || m0 >= kInfBits || m1 >= kInfBits;
+  float f0, f1;
+  row_factor(m0, f0, inv0);
+  row_factor(m1, f1, inv1);
+#pragma unroll
+  for (int i = 0; i < NT / 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (LO) {
+        split2(x[2 * i + j][0] * f0, x[2 * i + j][1] * f0, hi[i][2 * j], lo[i][2 * j]);
+        split2(x[2 * i + j][2] * f1, x[2 * i + j][3] * f1, hi[i][2 * j + 1], lo[i][2 * j + 1]);
+      } else {
+        hi[i][2 * j] = h2(x[2 * i + j][0] * f0, x[2 * i + j][1] * f0);
+        hi[i][2 * j + 1] = h2(x[2 * i + j][2] * f1, x[2 * i + j][3] * f1);
+      }
+    }
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool in) {
+  // a false predicate copies nothing and fills the piece with zeros
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+}  // namespace ccv

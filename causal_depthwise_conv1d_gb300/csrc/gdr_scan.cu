@@ -1,0 +1,588 @@
+// Gated delta rule, chunked: the scan that carries the state over the chunks
+// (formulas and precision in gdr_chunk.cuh).
+//
+// Everything is kept transposed: a warp owns 16 columns of the state (value
+// channels) as S^T, 16 rows of accumulator fragments over all Dk key
+// channels.  Then every product of a chunk has the warp's own fragments as
+// its A operand and a tile that all warps share as its B operand,
+//
+//   (K S)^T = S^T K^T,   U^T = R^T T^T,   O^T = .. + U^T P^T,   S^T += U'^T K,
+//
+// an accumulator fragment is an A fragment of the next product, and no warp
+// waits for another: the state never leaves registers.  The shared tiles (k,
+// q, T, P and the factors of one chunk) come by bulk copies two chunks deep;
+// the warp that is the last to leave a stage refills it, so no warp waits for
+// another and none is set aside for the copies.  v is fetched by each warp for
+// itself.
+//
+// What bounds it: the tensor instructions of 16-bit mma.sync (8 cycles each a
+// quarter SM) in the chain of one chunk after the other; a head's columns are
+// spread over as many blocks as it takes to fill the SMs.
+//
+// A chunk with a value that is not finite (in its inputs or in the state) is
+// taken token by token from the original inputs instead, so that nothing
+// reaches tokens before it, or past a new sequence, through a product with 0.
+#include "gdr_chunk.cuh"
+
+namespace ccv {
+namespace {
+
+__device__ unsigned g_fault;
+
+template <int DT, int DK, int NW, bool SAVE>
+struct ScanCfg {
+  static constexpr int TERMS = DT == kF32 ? 2 : 1;             // of k and q
+  // Terms of S, U and P in the output: bf16 outputs (8 bits) take 11 bits of
+  // each operand, the others 22.
+  static constexpr bool OLO = DT != kBF16;
+  static constexpr int TILE = qk_tile_bytes(DK);
+  static constexpr int QKB = SAVE ? TERMS * TILE : 2 * TERMS * TILE;  // k alone, or k and q
+  static constexpr int MATS = SAVE ? 2 : (OLO ? 4 : 3);        // T hi, T lo, P hi, P lo
+  static constexpr int STAGE = QKB + kVecBytes + MATS * kMatBytes;
+  static constexpr int VROW = DT == kF32 ? 64 : 32;            // bytes of a warp's 16 channels of one token
+  static constexpr int VBYTES = kC * VROW;
+  static constexpr int OBYTES = (DT == kF32 || SAVE) ? 0 : kC * 32;
+  static constexpr int BYTES = 2 * STAGE + NW * (VBYTES + OBYTES) + 64;
+  static constexpr int THREADS = 32 * NW;
+};
+
+// This warp's v of one chunk into its buffer; rows past the sequence and
+// channels past Dv are zero.
+template <int DT>
+__device__ __forceinline__ void fetch_v(const GdrArgs& a, int64_t b, int64_t h, int64_t t0, int64_t v0, bool vec,
+                                        uint8_t* buf, int lane) {
+  using F = Fmt<DT>;
+  using E = typename F::E;
+  constexpr int VROW = DT == kF32 ? 64 : 32;
+  constexpr int PIECES = VROW / 16;
+  const E* p = static_cast<const E*>(a.v) + b * a.vs[0] + h * a.vs[2] + v0 * a.vs[3];
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < kC * PIECES / 32; ++i) {
+      const int x = i * 32 + lane, r = x / PIECES, pc = x % PIECES;
+      const bool in = t0 + r < a.L;
+      const E* src = p + (in ? (t0 + r) * a.vs[1] : 0) + pc * (16 / static_cast<int>(sizeof(E)));
+      cp_async16(buf + r * VROW + pc * 16, src, in);
+    }
+  } else {
+    for (int x = lane; x < kC * 16; x += 32) {
+      const int r = x >> 4, c = x & 15;
+      E e = F::from_f(0.f);
+      if (t0 + r < a.L && v0 + c < a.Dv) e = p[(t0 + r) * a.vs[1] + c * a.vs[3]];
+      *reinterpret_cast<E*>(buf + r * VROW + c * sizeof(E)) = e;
+    }
+  }
+  cp_async_commit();
+}
+
+// One chunk token by token, from the original inputs, on the warp's 16 rows
+// of S^T (rows g and g + 8 of this thread, key channels 8 i + 2 qd + {0, 1}).
+template <int DT, int DK, bool SAVE>
+__device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[DK / 8][4], int64_t b, int64_t h,
+                                            int64_t t0, int64_t v0, float* u_out, int64_t dvp, int lane) {
+  using F = Fmt<DT>;
+  using E = typename F::E;
+  const int g = lane >> 2, qd = lane & 3;
+  const int64_t hk = h / (a.Hv / a.Hk);
+  const E* kp = static_cast<const E*>(a.k) + b * a.ks[0] + hk * a.ks[2];
+  const E* qp = static_cast<const E*>(a.q) + b * a.qs[0] + hk * a.qs[2];
+  const int64_t r0 = v0 + g, r1 = v0 + g + 8;
+  for (int i = 0; i < kC && t0 + i < a.L; ++i) {
+    const int64_t t = t0 + i;
+    float dec = expf(a.g[b * a.gs[0] + t * a.gs[1] + h * a.gs[2]]);
+    const float be = F::to_f(static_cast<const E*>(a.beta)[b * a.bs[0] + t * a.bs[1] + h * a.bs[2]]);
+    if (a.seq != nullptr && t > 0 && a.seq[b * a.ss[0] + t * a.ss[1]] != a.seq[b * a.ss[0] + (t - 1) * a.ss[1]]) {
+      dec = 0.f;
+#pragma unroll
+      for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st[n][j] = 0.f;
+    }
+    float p0 = 0.f, p1 = 0.f, o0 = 0.f, o1 = 0.f, qk = 0.f;
+#pragma unroll
+    for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int64_t kd = 8 * n + 2 * qd + e;
+        const float kv = kd < a.Dk ? F::to_f(kp[t * a.ks[1] + kd * a.ks[3]]) : 0.f;
+        const float qv = kd < a.Dk ? F::to_f(qp[t * a.qs[1] + kd * a.qs[3]]) : 0.f;
+        if (kd < a.Dk) {
+          p0 = fmaf(kv, st[n][e], p0);
+          p1 = fmaf(kv, st[n][2 + e], p1);
+          o0 = fmaf(qv, st[n][e], o0);
+          o1 = fmaf(qv, st[n][2 + e], o1);
+        }
+        qk = fmaf(kv, qv, qk);
+      }
+#pragma unroll
+    for (int m = 1; m < 4; m <<= 1) {
+      p0 += __shfl_xor_sync(kFullMask, p0, m);
+      p1 += __shfl_xor_sync(kFullMask, p1, m);
+      o0 += __shfl_xor_sync(kFullMask, o0, m);
+      o1 += __shfl_xor_sync(kFullMask, o1, m);
+      qk += __shfl_xor_sync(kFullMask, qk, m);
+    }
+    const E* vp = static_cast<const E*>(a.v) + b * a.vs[0] + t * a.vs[1] + h * a.vs[2];
+    const float x0 = r0 < a.Dv ? F::to_f(vp[r0 * a.vs[3]]) : 0.f, x1 = r1 < a.Dv ? F::to_f(vp[r1 * a.vs[3]]) : 0.f;
+    const float u0 = be * (x0 - dec * p0), u1 = be * (x1 - dec * p1);
+    if (qd == 0) {
+      if constexpr (SAVE) {
+        u_out[i * dvp + r0] = u0;
+        u_out[i * dvp + r1] = u1;
+      } else {
+        E* op = static_cast<E*>(a.out) + b * a.os[0] + t * a.os[1] + h * a.os[2];
+        if (r0 < a.Dv) op[r0 * a.os[3]] = F::from_f(a.scale * fmaf(qk, u0, dec * o0));
+        if (r1 < a.Dv) op[r1 * a.os[3]] = F::from_f(a.scale * fmaf(qk, u1, dec * o1));
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int64_t kd = 8 * n + 2 * qd + e;
+        const float kv = kd < a.Dk ? F::to_f(kp[t * a.ks[1] + kd * a.ks[3]]) : 0.f;
+        if (kd < a.Dk) {
+          st[n][e] = fmaf(kv, u0, dec * st[n][e]);
+          st[n][2 + e] = fmaf(kv, u1, dec * st[n][2 + e]);
+        }
+      }
+  }
+}
+
+template <int DT, int DK, int NW, bool SAVE>
+__global__ void __launch_bounds__(32 * NW, 1)
+    gdr_scan_kernel(const GdrArgs a, const uint8_t* qk_ws, const uint8_t* pack_ws, float* s_ws, float* u_ws, int nc,
+                    int vtiles, bool vvec, bool ovec) {
+  pdl_enter();
+  using C = ScanCfg<DT, DK, NW, SAVE>;
+  using F = Fmt<DT>;
+  using E = typename F::E;
+  constexpr int RB = DK * 2;
+  constexpr int NK = DK / 8;
+  extern __shared__ __align__(128) uint8_t sm[];
+  uint8_t* vbuf0 = sm + 2 * C::STAGE;
+  uint8_t* obuf0 = vbuf0 + NW * C::VBYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(obuf0 + NW * C::OBYTES);
+  unsigned* left = reinterpret_cast<unsigned*>(full + 2);  // warps that have left a stage
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, qd = lane & 3;
+  const int64_t bh = blockIdx.x / vtiles;
+  const int64_t b = bh / a.Hv, h = bh - b * a.Hv;
+  const int64_t hk = h / (a.Hv / a.Hk);
+  const int64_t v0 = (static_cast<int64_t>(blockIdx.x % vtiles) * NW + warp) * 16;
+
+  const uint8_t* qk = qk_ws + (b * a.Hk + hk) * nc * qk_pack_bytes(DK, C::TERMS);
+  const uint8_t* pk = pack_ws + bh * nc * kPackBytes;
+  auto fill = [&](int c) {
+    uint8_t* dst = sm + (c & 1) * C::STAGE;
+    uint64_t* bar = &full[c & 1];
+    constexpr uint32_t kVec = SAVE ? kVecBytes : kVecFwdBytes;
+    const uint8_t* pc = pk + static_cast<int64_t>(c) * kPackBytes;
+    mbar_arrive_expect_tx(bar, C::QKB + kVec + C::MATS * kMatBytes);
+    bulk_load(dst, qk + static_cast<int64_t>(c) * qk_pack_bytes(DK, C::TERMS), C::QKB, bar);
+    bulk_load(dst + C::QKB, pc, kVec, bar);
+    bulk_load(dst + C::QKB + kVecBytes, pc + kVecBytes, C::MATS * kMatBytes, bar);
+  };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&full[s], 1);
+      left[s] = 0;
+    }
+    fence_barrier_init();
+    for (int c = 0; c < 2 && c < nc; ++c) fill(c);
+  }
+  __syncthreads();
+
+  const bool active = v0 < a.Dv;
+  uint8_t* vb = vbuf0 + warp * C::VBYTES;
+  uint8_t* ob = obuf0 + warp * C::OBYTES;
+  const bool wvec = vvec && v0 + 16 <= a.Dv, wovec = ovec && v0 + 16 <= a.Dv;
+  const int64_t dvp = (a.Dv + 15) / 16 * 16;
+
+  float st[NK][4];
+#pragma unroll
+  for (int n = 0; n < NK; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t kd = 8 * n + 2 * qd + (j & 1), vc = v0 + g + (j >> 1) * 8;
+      st[n][j] = (a.s0 != nullptr && kd < a.Dk && vc < a.Dv)
+                     ? a.s0[b * a.s0s[0] + h * a.s0s[1] + kd * a.s0s[2] + vc * a.s0s[3]]
+                     : 0.f;
+    }
+  if (active && nc > 0) fetch_v<DT>(a, b, h, 0, v0, wvec, vb, lane);
+
+  for (int c = 0; c < nc; ++c) {
+    const int s = c & 1;
+    const int64_t t0 = static_cast<int64_t>(c) * kC;
+    if (!mbar_wait(&full[s], (c >> 1) & 1)) {
+      // give up: the other stage's copy must not outlive the block either
+      if (lane == 0) {
+        atomicOr(&g_fault, kFaultConsumerWait);
+        if (c + 1 < nc && !mbar_wait(&full[s ^ 1], ((c + 1) >> 1) & 1)) atomicOr(&g_fault, kFaultDrainWait);
+      }
+      return;
+    }
+    if (active) {
+      const uint32_t kt_hi = smem_u32(sm + s * C::STAGE);
+      const uint32_t kt_lo = kt_hi + C::TILE;
+      const uint32_t qt_hi = kt_hi + C::TERMS * C::TILE;
+      const uint32_t qt_lo = qt_hi + C::TILE;
+      const float* vecs = reinterpret_cast<const float*>(sm + s * C::STAGE + C::QKB);
+      const float* slot = vecs + kVecHead;
+      const uint32_t th = kt_hi + C::QKB + kVecBytes, tl = th + kMatBytes, ph = tl + kMatBytes, pl = ph + kMatBytes;
+      const float ga = vecs[kHdGa];
+      float* u_out = SAVE ? u_ws + (bh * nc + c) * kC * dvp : nullptr;
+      if constexpr (SAVE) {
+        float* so = s_ws + (bh * nc + c) * DK * dvp;
+#pragma unroll
+        for (int n = 0; n < NK; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) so[(8 * n + 2 * qd + (j & 1)) * dvp + v0 + g + (j >> 1) * 8] = st[n][j];
+      }
+      bool bad = vecs[kHdBad] != 0.f;
+
+      // the state's row factors
+      unsigned m0 = 0, m1 = 0;
+#pragma unroll
+      for (int n = 0; n < NK; ++n) {
+        m0 = max(m0, max(mag(st[n][0]), mag(st[n][1])));
+        m1 = max(m1, max(mag(st[n][2]), mag(st[n][3])));
+      }
+      m0 = quad_max(m0);
+      m1 = quad_max(m1);
+      bad = bad || m0 >= kInfBits || m1 >= kInfBits;
+      float f0, f1, si0, si1;
+      row_factor(m0, f0, si0);
+      row_factor(m1, f1, si1);
+
+      // (K S)^T and (Q S)^T
+      float ks[8][4], qs[8][4];
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ks[n][j] = qs[n][j] = 0.f;
+#pragma unroll
+      for (int kt = 0; kt < DK / 16; ++kt) {
+        uint32_t hi[4], lo[4];
+        split2(st[2 * kt][0] * f0, st[2 * kt][1] * f0, hi[0], lo[0]);
+        split2(st[2 * kt][2] * f1, st[2 * kt][3] * f1, hi[1], lo[1]);
+        split2(st[2 * kt + 1][0] * f0, st[2 * kt + 1][1] * f0, hi[2], lo[2]);
+        split2(st[2 * kt + 1][2] * f1, st[2 * kt + 1][3] * f1, hi[3], lo[3]);
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+          uint32_t bk[4];
+          ldsm4(bk, addr_b<RB>(kt_hi, np * 16, 2 * kt, lane));
+          mma(ks[2 * np], hi, bk[0], bk[1]);
+          mma(ks[2 * np + 1], hi, bk[2], bk[3]);
+          mma(ks[2 * np], lo, bk[0], bk[1]);
+          mma(ks[2 * np + 1], lo, bk[2], bk[3]);
+          if constexpr (DT == kF32) {
+            ldsm4(bk, addr_b<RB>(kt_lo, np * 16, 2 * kt, lane));
+            mma(ks[2 * np], hi, bk[0], bk[1]);
+            mma(ks[2 * np + 1], hi, bk[2], bk[3]);
+          }
+          if constexpr (!SAVE) {
+            ldsm4(bk, addr_b<RB>(qt_hi, np * 16, 2 * kt, lane));
+            mma(qs[2 * np], hi, bk[0], bk[1]);
+            mma(qs[2 * np + 1], hi, bk[2], bk[3]);
+            if constexpr (C::OLO) {
+              mma(qs[2 * np], lo, bk[0], bk[1]);
+              mma(qs[2 * np + 1], lo, bk[2], bk[3]);
+            }
+            if constexpr (DT == kF32) {
+              ldsm4(bk, addr_b<RB>(qt_lo, np * 16, 2 * kt, lane));
+              mma(qs[2 * np], hi, bk[0], bk[1]);
+              mma(qs[2 * np + 1], hi, bk[2], bk[3]);
+            }
+          }
+        }
+      }
+
+      // R = beta (V - gi K S)
+      cp_async_wait_all();
+      __syncwarp();
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        float x[2][4];
+        if constexpr (DT == kF32) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              x[t][j] = *reinterpret_cast<const float*>(vb + (np * 16 + t * 8 + qd * 2 + (j & 1)) * C::VROW +
+                                                        (g + (j >> 1) * 8) * 4);
+        } else {
+          uint32_t r[4];
+          ldsm4t(r, smem_u32(vb) + (np * 16 + (lane & 7) + ((lane >> 4) & 1) * 8) * C::VROW + ((lane >> 3) & 1) * 16);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[t][j] = F::word_elem(r[2 * t + (j >> 1)], j & 1);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int n = 2 * np + t;
+          const float2 cf = *reinterpret_cast<const float2*>(slot + kVKS * kC + n * 8 + qd * 2);
+          const float2 be = *reinterpret_cast<const float2*>(slot + kVBeta * kC + n * 8 + qd * 2);
+          ks[n][0] = be.x * (x[t][0] - cf.x * (ks[n][0] * si0));
+          ks[n][1] = be.y * (x[t][1] - cf.y * (ks[n][1] * si0));
+          ks[n][2] = be.x * (x[t][2] - cf.x * (ks[n][2] * si1));
+          ks[n][3] = be.y * (x[t][3] - cf.y * (ks[n][3] * si1));
+        }
+      }
+      uint32_t hi[4][4], lo[4][4];
+      float ri0, ri1;
+      split_rows<8, true>(ks, hi, lo, ri0, ri1, bad);
+      bad = __any_sync(kFullMask, bad);
+
+      if (bad) {
+        float tmp[NK][4];  // a copy: the state itself has to stay in registers
+#pragma unroll
+        for (int n = 0; n < NK; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tmp[n][j] = st[n][j];
+        token_by_token<DT, DK, SAVE>(a, tmp, b, h, t0, v0, u_out, dvp, lane);
+#pragma unroll
+        for (int n = 0; n < NK; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) st[n][j] = tmp[n][j];
+        __syncwarp();
+        if (c + 1 < nc) fetch_v<DT>(a, b, h, t0 + kC, v0, wvec, vb, lane);
+      } else {
+        __syncwarp();
+        if (c + 1 < nc) fetch_v<DT>(a, b, h, t0 + kC, v0, wvec, vb, lane);
+        // U^T = R^T T^T, T lower triangular
+        float u[8][4];
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+          float x[2][2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[0][i][j] = x[1][i][j] = 0.f;
+#pragma unroll
+          for (int kt = 0; kt <= np; ++kt) {
+            uint32_t bt[4];
+            ldsm4(bt, addr_b<128>(th, np * 16, 2 * kt, lane));
+            mma(x[0][0], hi[kt], bt[0], bt[1]);
+            mma(x[0][1], hi[kt], bt[2], bt[3]);
+            mma(x[1][0], lo[kt], bt[0], bt[1]);
+            mma(x[1][1], lo[kt], bt[2], bt[3]);
+            ldsm4(bt, addr_b<128>(tl, np * 16, 2 * kt, lane));
+            mma(x[1][0], hi[kt], bt[0], bt[1]);
+            mma(x[1][1], hi[kt], bt[2], bt[3]);
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const float2 ti = *reinterpret_cast<const float2*>(slot + kVTInv * kC + (2 * np + t) * 8 + qd * 2);
+            u[2 * np + t][0] = (x[0][t][0] + x[1][t][0]) * (ti.x * ri0);
+            u[2 * np + t][1] = (x[0][t][1] + x[1][t][1]) * (ti.y * ri0);
+            u[2 * np + t][2] = (x[0][t][2] + x[1][t][2]) * (ti.x * ri1);
+            u[2 * np + t][3] = (x[0][t][3] + x[1][t][3]) * (ti.y * ri1);
+          }
+        }
+        if constexpr (SAVE) {
+#pragma unroll
+          for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u_out[(n * 8 + qd * 2 + (j & 1)) * dvp + v0 + g + (j >> 1) * 8] = u[n][j];
+        } else {
+          // O^T = scale (gi (Q S)^T + U^T P^T)
+          float ui0, ui1;
+          bool ignore = false;
+          split_rows<8, C::OLO>(u, hi, lo, ui0, ui1, ignore);
+#pragma unroll
+          for (int np = 0; np < 4; ++np) {
+            float x[2][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[0][j] = x[1][j] = 0.f;
+#pragma unroll
+            for (int kt = 0; kt <= np; ++kt) {
+              uint32_t bp[4];
+              ldsm4(bp, addr_b<128>(ph, np * 16, 2 * kt, lane));
+              mma(x[0], hi[kt], bp[0], bp[1]);
+              mma(x[1], hi[kt], bp[2], bp[3]);
+              if constexpr (C::OLO) {
+                mma(x[0], lo[kt], bp[0], bp[1]);
+                mma(x[1], lo[kt], bp[2], bp[3]);
+                ldsm4(bp, addr_b<128>(pl, np * 16, 2 * kt, lane));
+                mma(x[0], hi[kt], bp[0], bp[1]);
+                mma(x[1], hi[kt], bp[2], bp[3]);
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int n = 2 * np + t;
+              const float2 cq = *reinterpret_cast<const float2*>(slot + kVQS * kC + n * 8 + qd * 2);
+              const float2 cp = *reinterpret_cast<const float2*>(slot + kVP * kC + n * 8 + qd * 2);
+              x[t][0] = fmaf(cp.x * ui0, x[t][0], cq.x * (qs[n][0] * si0));
+              x[t][1] = fmaf(cp.y * ui0, x[t][1], cq.y * (qs[n][1] * si0));
+              x[t][2] = fmaf(cp.x * ui1, x[t][2], cq.x * (qs[n][2] * si1));
+              x[t][3] = fmaf(cp.y * ui1, x[t][3], cq.y * (qs[n][3] * si1));
+            }
+            if (DT != kF32 && wovec) {
+              if constexpr (DT != kF32) {
+                const uint32_t r[4] = {F::pack2(x[0][0], x[0][1]), F::pack2(x[0][2], x[0][3]),
+                                       F::pack2(x[1][0], x[1][1]), F::pack2(x[1][2], x[1][3])};
+                stsm4t(smem_u32(ob) + (np * 16 + (lane & 7) + ((lane >> 4) & 1) * 8) * 32 + ((lane >> 3) & 1) * 16, r);
+              }
+            } else {
+              E* op = static_cast<E*>(a.out) + b * a.os[0] + h * a.os[2];
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int64_t tok = t0 + np * 16 + t * 8 + qd * 2 + (j & 1), vc = v0 + g + (j >> 1) * 8;
+                  if (tok < a.L && vc < a.Dv) op[tok * a.os[1] + vc * a.os[3]] = F::from_f(x[t][j]);
+                }
+            }
+          }
+          if (DT != kF32 && wovec) {
+            __syncwarp();
+            E* op = static_cast<E*>(a.out) + b * a.os[0] + h * a.os[2] + v0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int x = i * 32 + lane, r = x >> 1, pc = x & 1;
+              const uint4 w = lds128(ob + r * 32 + pc * 16);
+              if (t0 + r < a.L) *reinterpret_cast<uint4*>(op + (t0 + r) * a.os[1] + pc * 8) = w;
+            }
+          }
+        }
+        // S^T <- ga S^T + (gc U)^T K
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const float2 cu = *reinterpret_cast<const float2*>(slot + kVU * kC + n * 8 + qd * 2);
+          u[n][0] *= cu.x, u[n][1] *= cu.y, u[n][2] *= cu.x, u[n][3] *= cu.y;
+        }
+        float ui0, ui1;
+        bool ignore = false;
+        split_rows<8, true>(u, hi, lo, ui0, ui1, ignore);
+#pragma unroll
+        for (int n4 = 0; n4 < NK / 4; ++n4) {
+          float x[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+#pragma unroll
+          for (int kt = 0; kt < 4; ++kt) {
+            uint32_t bk[2][4];
+            ldsm4t(bk[0], addr_bt<RB>(kt_hi, kt * 16, n4 * 4, lane));
+            ldsm4t(bk[1], addr_bt<RB>(kt_hi, kt * 16, n4 * 4 + 2, lane));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma(x[i], hi[kt], bk[i >> 1][(i & 1) * 2], bk[i >> 1][(i & 1) * 2 + 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma(x[i], lo[kt], bk[i >> 1][(i & 1) * 2], bk[i >> 1][(i & 1) * 2 + 1]);
+            if constexpr (DT == kF32) {
+              ldsm4t(bk[0], addr_bt<RB>(kt_lo, kt * 16, n4 * 4, lane));
+              ldsm4t(bk[1], addr_bt<RB>(kt_lo, kt * 16, n4 * 4 + 2, lane));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mma(x[i], hi[kt], bk[i >> 1][(i & 1) * 2], bk[i >> 1][(i & 1) * 2 + 1]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int n = n4 * 4 + i;
+            st[n][0] = fmaf(ga, st[n][0], ui0 * x[i][0]);
+            st[n][1] = fmaf(ga, st[n][1], ui0 * x[i][1]);
+            st[n][2] = fmaf(ga, st[n][2], ui1 * x[i][2]);
+            st[n][3] = fmaf(ga, st[n][3], ui1 * x[i][3]);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) {
+      unsigned n;
+      asm volatile("atom.acq_rel.cta.shared.add.u32 %0, [%1], 1;" : "=r"(n) : "r"(smem_u32(&left[s])) : "memory");
+      if (n == NW - 1) {  // every warp has left the stage
+        left[s] = 0;
+        if (c + 2 < nc) fill(c + 2);
+      }
+    }
+  }
+  if (a.s1 != nullptr) {
+#pragma unroll
+    for (int n = 0; n < NK; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t kd = 8 * n + 2 * qd + (j & 1), vc = v0 + g + (j >> 1) * 8;
+        if (kd < a.Dk && vc < a.Dv)
+          a.s1[b * a.s1s[0] + h * a.s1s[1] + kd * a.s1s[2] + vc * a.s1s[3]] = st[n][j];
+      }
+  }
+}
+
+template <int DT, int DK, int NW, bool SAVE>
+cudaError_t launch(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, int nc,
+                   cudaStream_t s) {
+  using C = ScanCfg<DT, DK, NW, SAVE>;
+  static_assert(C::BYTES <= 232448, "shared memory of one block");
+  using E = typename Fmt<DT>::E;
+  constexpr int64_t V = 16 / sizeof(E);
+  auto al = [&](const void* p, const int64_t* st) {
+    return st[3] == 1 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && st[0] % V == 0 && st[1] % V == 0 && st[2] % V == 0;
+  };
+  const int vtiles = static_cast<int>((a.Dv + 16 * NW - 1) / (16 * NW));
+  const cudaError_t e = cudaFuncSetAttribute(gdr_scan_kernel<DT, DK, NW, SAVE>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(gdr_scan_kernel<DT, DK, NW, SAVE>, static_cast<unsigned>(a.B * a.Hv * vtiles), C::THREADS,
+                    C::BYTES, s, a, qk, pk, sw, uw, nc, vtiles, al(a.v, a.vs), !SAVE && al(a.out, a.os));
+}
+
+template <int DT, int DK, bool SAVE>
+cudaError_t launch_nw(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, int nc,
+                      const Device& dev, cudaStream_t s) {
+  // Blocks of few warps while that still puts no more than one on an SM: a
+  // warp alone on its quarter of an SM runs its chain at full rate.
+  const int64_t heads = a.B * a.Hv, groups = (a.Dv + 15) / 16;
+  if (heads * ((groups + 1) / 2) <= dev.sm_count) return launch<DT, DK, 2, SAVE>(a, qk, pk, sw, uw, nc, s);
+  if (DT == kF32 || heads * ((groups + 3) / 4) <= dev.sm_count)
+    return launch<DT, DK, 4, SAVE>(a, qk, pk, sw, uw, nc, s);
+  if constexpr (DT != kF32) return launch<DT, DK, 8, SAVE>(a, qk, pk, sw, uw, nc, s);
+  return cudaErrorInvalidValue;
+}
+
+template <int DT, int DK>
+cudaError_t launch_k(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, int nc,
+                     const Device& dev, cudaStream_t s) {
+  return sw != nullptr ? launch_nw<DT, DK, true>(a, qk, pk, sw, uw, nc, dev, s)
+                       : launch_nw<DT, DK, false>(a, qk, pk, sw, uw, nc, dev, s);
+}
+
+template <int DT>
+cudaError_t launch_dt(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, int nc,
+                      const Device& dev, cudaStream_t s) {
+  return a.Dk <= 64 ? launch_k<DT, 64>(a, qk, pk, sw, uw, nc, dev, s)
+                    : launch_k<DT, 128>(a, qk, pk, sw, uw, nc, dev, s);
+}
+
+}  // namespace
+
+cudaError_t launch_gdr_scan(const GdrArgs& a, Dtype dt, const uint8_t* qk_ws, const uint8_t* pack_ws, float* s_ws,
+                            float* u_ws, int nc, const Device& dev, cudaStream_t stream) {
+  switch (dt) {
+    case kF32: return launch_dt<kF32>(a, qk_ws, pack_ws, s_ws, u_ws, nc, dev, stream);
+    case kF16: return launch_dt<kF16>(a, qk_ws, pack_ws, s_ws, u_ws, nc, dev, stream);
+    case kBF16: return launch_dt<kBF16>(a, qk_ws, pack_ws, s_ws, u_ws, nc, dev, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+uint64_t gdr_qk_bytes(const GdrArgs& a, Dtype dt, int nc) {
+  return static_cast<uint64_t>(a.B * a.Hk) * nc * qk_pack_bytes(a.Dk <= 64 ? 64 : 128, dt == kF32 ? 2 : 1);
+}
+
+uint64_t gdr_pack_bytes(const GdrArgs& a, int nc) { return static_cast<uint64_t>(a.B * a.Hv) * nc * kPackBytes; }
+
+unsigned read_and_clear_fault_gdr() {
+  unsigned v = 0;
+  const unsigned zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_fault, sizeof(v)) != cudaSuccess) return ~0u;
+  if (v != 0 && cudaMemcpyToSymbol(g_fault, &zero, sizeof(zero)) != cudaSuccess) return ~0u;
+  return v;
+}
+
+}  // namespace ccv

@@ -26,6 +26,27 @@ ccv_status fail_invalid(const char* name, const char* what) {
 bool valid_dtype(ccv_dtype d) { return d == CCV_F32 || d == CCV_F16 || d == CCV_BF16; }
 int64_t dtype_size(ccv_dtype d) { return d == CCV_F32 ? 4 : 2; }
 
+// The chunked kernels take Dk up to kGdrChunkDk.  Below kGdrChunkMin tokens the
+// token-by-token kernel is as fast and needs no workspace.
+constexpr int64_t kGdrChunkMin = 48;
+bool gdr_chunked(int64_t L, int64_t Dk) { return L >= kGdrChunkMin && Dk <= ccv::kGdrChunkDk; }
+int gdr_chunks(int64_t L) { return static_cast<int>((L + ccv::kGdrChunk - 1) / ccv::kGdrChunk); }
+
+struct GdrWorkspace {
+  uint64_t qk, pack, total;
+};
+
+GdrWorkspace gdr_workspace(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, ccv_dtype dtype) {
+  GdrWorkspace w = {0, 0, 0};
+  if (B == 0 || Hv == 0 || Dv == 0 || !gdr_chunked(L, Dk)) return w;
+  ccv::GdrArgs a = {};
+  a.B = B, a.L = L, a.Hk = Hk, a.Hv = Hv, a.Dk = Dk, a.Dv = Dv;
+  w.qk = ccv::gdr_qk_bytes(a, static_cast<ccv::Dtype>(dtype), gdr_chunks(L));
+  w.pack = ccv::gdr_pack_bytes(a, gdr_chunks(L));
+  w.total = w.qk + w.pack;
+  return w;
+}
+
 // The tensors of one call: each is checked when it is added (strides given,
 // alignment, extent, an output's elements distinct), and then the outputs are
 // checked against all others.
@@ -126,6 +147,16 @@ class Tensors {
   int n_ = 0;
 };
 
+// A workspace of at least `need` bytes (none needed: whatever is given is left alone).
+ccv_status add_workspace(Tensors& t, const void* workspace, uint64_t bytes, uint64_t need, int64_t align) {
+  if (need == 0) return CCV_OK;
+  if (workspace == nullptr || bytes < need)
+    CCV_FAIL(CCV_ERR_INVALID_ARG, "workspace too small: need %llu bytes (got %llu)", (unsigned long long)need,
+             (unsigned long long)(workspace ? bytes : 0));
+  const int64_t shape[1] = {static_cast<int64_t>((need + align - 1) / align)}, one = 1;
+  return t.add("workspace", workspace, &one, 1, shape, align, true, true);
+}
+
 ccv_status check_gdr_sizes(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int64_t max_dk,
                            ccv_dtype dtype) {
   if (B < 0 || L < 0 || Hk < 0 || Hv < 0 || Dk < 0 || Dv < 0)
@@ -191,13 +222,13 @@ ccv_status ccv_gdr_fwd(const void* q, const int64_t q_strides[4], const void* k,
   CCV_TRY(t.add("initial_state", initial_state, initial_state_strides, 4, st, 4, false, false));
   CCV_TRY(t.add("out", out, out_strides, 4, vo, e, true, true));
   CCV_TRY(t.add("final_state_out", final_state_out, final_state_strides, 4, st, 4, true, false));
+  const GdrWorkspace w = gdr_workspace(B, L, Hk, Hv, Dk, Dv, dtype);
+  CCV_TRY(add_workspace(t, workspace, workspace_bytes, w.total, 128));
   CCV_TRY(t.disjoint());
   if (L == 0 && final_state_out == nullptr) {
     ccv::api_kernel("none");
     return CCV_OK;
   }
-  (void)workspace;
-  (void)workspace_bytes;
   ccv::Device dev;
   CCV_TRY(static_cast<ccv_status>(ccv::api_device(&dev)));
   ccv::GdrArgs a = {};
@@ -207,8 +238,14 @@ ccv_status ccv_gdr_fwd(const void* q, const int64_t q_strides[4], const void* k,
   copy(a.bs, beta_strides, 3), copy(a.ss, seq_idx_strides, 2), copy(a.s0s, initial_state_strides, 4);
   copy(a.s1s, final_state_strides, 4), copy(a.os, out_strides, 4);
   a.B = B, a.L = L, a.Hk = Hk, a.Hv = Hv, a.Dk = Dk, a.Dv = Dv, a.scale = scale;
-  return launched(ccv::launch_gdr_step(a, static_cast<ccv::Dtype>(dtype), dev, static_cast<cudaStream_t>(stream)),
-                  "gdr_step");
+  const ccv::Dtype dt = static_cast<ccv::Dtype>(dtype);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (w.total == 0) return launched(ccv::launch_gdr_step(a, dt, dev, s), "gdr_step");
+  uint8_t* qk_ws = static_cast<uint8_t*>(workspace);
+  uint8_t* pack_ws = qk_ws + w.qk;
+  cudaError_t err = ccv::launch_gdr_prep(a, dt, qk_ws, pack_ws, gdr_chunks(L), s);
+  if (err == cudaSuccess) err = ccv::launch_gdr_scan(a, dt, qk_ws, pack_ws, nullptr, nullptr, gdr_chunks(L), dev, s);
+  return launched(err, "gdr_chunk");
 }
 
 ccv_status ccv_gdr_fwd_workspace_size(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
@@ -216,7 +253,7 @@ ccv_status ccv_gdr_fwd_workspace_size(int64_t B, int64_t L, int64_t Hk, int64_t 
   ccv::api_begin();
   if (bytes == nullptr) CCV_FAIL(CCV_ERR_INVALID_ARG, "bytes is required");
   CCV_TRY(check_gdr_sizes(B, L, Hk, Hv, Dk, Dv, ccv::kGdrMaxDk, dtype));
-  *bytes = 0;
+  *bytes = gdr_workspace(B, L, Hk, Hv, Dk, Dv, dtype).total;
   return CCV_OK;
 }
 
@@ -332,13 +369,7 @@ ccv_status ccv_ln_bwd(const void* x, const int64_t x_strides[2], const void* wei
   CCV_TRY(t.add("dx", dx, dx_strides, 2, nd, e, true, true));
   CCV_TRY(t.add("dweight", dweight, &dweight_stride, 1, d, we, true, false));
   CCV_TRY(t.add("dbias", dbias, &dbias_stride, 1, d, we, true, false));
-  if (need > 0) {
-    if (workspace == nullptr || workspace_bytes < need)
-      CCV_FAIL(CCV_ERR_INVALID_ARG, "workspace too small: need %llu bytes (got %llu)", (unsigned long long)need,
-               (unsigned long long)(workspace ? workspace_bytes : 0));
-    const int64_t wsh[1] = {static_cast<int64_t>((need + 15) / 16)}, one = 1;
-    CCV_TRY(t.add("workspace", workspace, &one, 1, wsh, 16, true, true));
-  }
+  CCV_TRY(add_workspace(t, workspace, workspace_bytes, need, 16));
   CCV_TRY(t.disjoint());
   ccv::LnBwdArgs a = {};
   a.x = x, a.w = weight, a.ws = weight_stride, a.dout = dout, a.dx = dx;

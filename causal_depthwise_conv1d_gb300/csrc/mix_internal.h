@@ -62,6 +62,18 @@ struct GdrGrads {
 // (slots/n_slots) and short or unusual whole sequences.
 cudaError_t launch_gdr_step(const GdrArgs& a, Dtype dt, const Device& dev, cudaStream_t stream);
 
+// Chunked forward pass: the parts that do not depend on the state (qk_ws,
+// pack_ws: see gdr_chunk.cuh), then the scan that carries it.  nc = chunks.
+cudaError_t launch_gdr_prep(const GdrArgs& a, Dtype dt, uint8_t* qk_ws, uint8_t* pack_ws, int nc, cudaStream_t stream);
+// For the backward pass the scan makes no output but keeps each chunk's first
+// state and its U (FP32, [b][h][chunk][Dk or 64][dvp]) in s_ws and u_ws.
+cudaError_t launch_gdr_scan(const GdrArgs& a, Dtype dt, const uint8_t* qk_ws, const uint8_t* pack_ws, float* s_ws,
+                            float* u_ws, int nc, const Device& dev, cudaStream_t stream);
+// Bytes of qk_ws and pack_ws.
+uint64_t gdr_qk_bytes(const GdrArgs& a, Dtype dt, int nc);
+uint64_t gdr_pack_bytes(const GdrArgs& a, int nc);
+unsigned read_and_clear_fault_gdr();
+
 struct LnArgs {
   const void* x;
   int64_t xs0, xs1;
