@@ -12,8 +12,9 @@ _BINDING_NAMES = ("ccv_fwd", "ccv_fwd_ptr", "ccv_update", "ccv_bwd", "ccv_bwd_pt
                   "ccv_last_error", "ccv_last_kernel", "ccv_version", "ccv_device_fault", "ccv_test_bounded_wait",
                   "load_library",
                   "CcvError", "causal_conv1d_fwd", "causal_conv1d_update", "causal_conv1d_bwd")
-_MIXER_NAMES = ("ccv_gdr_fwd", "ccv_gdr_fwd_workspace_size", "ccv_gdr_step", "ccv_ln_fwd", "ccv_ln_bwd",
-                "ccv_ln_bwd_workspace_size", "gated_delta_rule_fwd", "gated_delta_rule_step", "layer_norm_fwd",
+_MIXER_NAMES = ("ccv_gdr_fwd", "ccv_gdr_fwd_workspace_size", "ccv_gdr_step", "ccv_gdr_bwd",
+                "ccv_gdr_bwd_workspace_size", "ccv_ln_fwd", "ccv_ln_bwd", "ccv_ln_bwd_workspace_size",
+                "gated_delta_rule_fwd", "gated_delta_rule_bwd", "gated_delta_rule_step", "layer_norm_fwd",
                 "layer_norm_bwd")
 
 

@@ -139,7 +139,8 @@ __device__ __forceinline__ unsigned mag(float x) { return __float_as_uint(x) & 0
 
 constexpr unsigned kInfBits = 0x7f800000u;  // magnitudes from here on are not finite
 
-// Power of two that brings a finite magnitude to [2^14, 2^15), and its inverse.
+// Power of two that brings a finite magnitude to [2^14, 2^15), and its inverse
+// (2^126 and 2^-126 where the magnitude is zero or smaller than any product needs).
 __device__ __forceinline__ void row_factor(unsigned m, float& f, float& inv) {
   const unsigned e = max(15u, min(254u, m >> 23));
   f = __uint_as_float((268u - e) << 23);

@@ -87,6 +87,9 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[DK / 8
   const E* kp = static_cast<const E*>(a.k) + b * a.ks[0] + hk * a.ks[2];
   const E* qp = static_cast<const E*>(a.q) + b * a.qs[0] + hk * a.qs[2];
   const int64_t r0 = v0 + g, r1 = v0 + g + 8;
+  if (SAVE && qd == 0) {  // rows past the sequence
+    for (int64_t i = a.L - t0; i < kC; ++i) u_out[i * dvp + r0] = u_out[i * dvp + r1] = 0.f;
+  }
   for (int i = 0; i < kC && t0 + i < a.L; ++i) {
     const int64_t t = t0 + i;
     float dec = expf(a.g[b * a.gs[0] + t * a.gs[1] + h * a.gs[2]]);
@@ -151,8 +154,8 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[DK / 8
 
 template <int DT, int DK, int NW, bool SAVE>
 __global__ void __launch_bounds__(32 * NW, 1)
-    gdr_scan_kernel(const GdrArgs a, const uint8_t* qk_ws, const uint8_t* pack_ws, float* s_ws, float* u_ws, int nc,
-                    int vtiles, bool vvec, bool ovec) {
+    gdr_scan_kernel(const GdrArgs a, const uint8_t* qk_ws, const uint8_t* pack_ws, float* s_ws, float* u_ws,
+                    unsigned* s_max, int nc, int vtiles, bool vvec, bool ovec) {
   pdl_enter();
   using C = ScanCfg<DT, DK, NW, SAVE>;
   using F = Fmt<DT>;
@@ -255,6 +258,10 @@ __global__ void __launch_bounds__(32 * NW, 1)
       float f0, f1, si0, si1;
       row_factor(m0, f0, si0);
       row_factor(m1, f1, si1);
+      if constexpr (SAVE) {  // the chunk's largest state element: one factor for the whole matrix later
+        const unsigned mx = warp_max(max(m0, m1));
+        if (lane == 0) atomicMax(s_max + bh * nc + c, mx);
+      }
 
       // (K S)^T and (Q S)^T
       float ks[8][4], qs[8][4];
@@ -515,7 +522,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
 }
 
 template <int DT, int DK, int NW, bool SAVE>
-cudaError_t launch(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, int nc,
+cudaError_t launch(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, unsigned* sm, int nc,
                    cudaStream_t s) {
   using C = ScanCfg<DT, DK, NW, SAVE>;
   static_assert(C::BYTES <= 232448, "shared memory of one block");
@@ -529,44 +536,44 @@ cudaError_t launch(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e != cudaSuccess) return e;
   return launch_pdl(gdr_scan_kernel<DT, DK, NW, SAVE>, static_cast<unsigned>(a.B * a.Hv * vtiles), C::THREADS,
-                    C::BYTES, s, a, qk, pk, sw, uw, nc, vtiles, al(a.v, a.vs), !SAVE && al(a.out, a.os));
+                    C::BYTES, s, a, qk, pk, sw, uw, sm, nc, vtiles, al(a.v, a.vs), !SAVE && al(a.out, a.os));
 }
 
 template <int DT, int DK, bool SAVE>
-cudaError_t launch_nw(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, int nc,
+cudaError_t launch_nw(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, unsigned* sm, int nc,
                       const Device& dev, cudaStream_t s) {
   // Blocks of few warps while that still puts no more than one on an SM: a
   // warp alone on its quarter of an SM runs its chain at full rate.
   const int64_t heads = a.B * a.Hv, groups = (a.Dv + 15) / 16;
-  if (heads * ((groups + 1) / 2) <= dev.sm_count) return launch<DT, DK, 2, SAVE>(a, qk, pk, sw, uw, nc, s);
+  if (heads * ((groups + 1) / 2) <= dev.sm_count) return launch<DT, DK, 2, SAVE>(a, qk, pk, sw, uw, sm, nc, s);
   if (DT == kF32 || heads * ((groups + 3) / 4) <= dev.sm_count)
-    return launch<DT, DK, 4, SAVE>(a, qk, pk, sw, uw, nc, s);
-  if constexpr (DT != kF32) return launch<DT, DK, 8, SAVE>(a, qk, pk, sw, uw, nc, s);
+    return launch<DT, DK, 4, SAVE>(a, qk, pk, sw, uw, sm, nc, s);
+  if constexpr (DT != kF32) return launch<DT, DK, 8, SAVE>(a, qk, pk, sw, uw, sm, nc, s);
   return cudaErrorInvalidValue;
 }
 
 template <int DT, int DK>
-cudaError_t launch_k(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, int nc,
+cudaError_t launch_k(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, unsigned* sm, int nc,
                      const Device& dev, cudaStream_t s) {
-  return sw != nullptr ? launch_nw<DT, DK, true>(a, qk, pk, sw, uw, nc, dev, s)
-                       : launch_nw<DT, DK, false>(a, qk, pk, sw, uw, nc, dev, s);
+  return sw != nullptr ? launch_nw<DT, DK, true>(a, qk, pk, sw, uw, sm, nc, dev, s)
+                       : launch_nw<DT, DK, false>(a, qk, pk, sw, uw, sm, nc, dev, s);
 }
 
 template <int DT>
-cudaError_t launch_dt(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, int nc,
+cudaError_t launch_dt(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, unsigned* sm, int nc,
                       const Device& dev, cudaStream_t s) {
-  return a.Dk <= 64 ? launch_k<DT, 64>(a, qk, pk, sw, uw, nc, dev, s)
-                    : launch_k<DT, 128>(a, qk, pk, sw, uw, nc, dev, s);
+  return a.Dk <= 64 ? launch_k<DT, 64>(a, qk, pk, sw, uw, sm, nc, dev, s)
+                    : launch_k<DT, 128>(a, qk, pk, sw, uw, sm, nc, dev, s);
 }
 
 }  // namespace
 
 cudaError_t launch_gdr_scan(const GdrArgs& a, Dtype dt, const uint8_t* qk_ws, const uint8_t* pack_ws, float* s_ws,
-                            float* u_ws, int nc, const Device& dev, cudaStream_t stream) {
+                            float* u_ws, unsigned* s_max, int nc, const Device& dev, cudaStream_t stream) {
   switch (dt) {
-    case kF32: return launch_dt<kF32>(a, qk_ws, pack_ws, s_ws, u_ws, nc, dev, stream);
-    case kF16: return launch_dt<kF16>(a, qk_ws, pack_ws, s_ws, u_ws, nc, dev, stream);
-    case kBF16: return launch_dt<kBF16>(a, qk_ws, pack_ws, s_ws, u_ws, nc, dev, stream);
+    case kF32: return launch_dt<kF32>(a, qk_ws, pack_ws, s_ws, u_ws, s_max, nc, dev, stream);
+    case kF16: return launch_dt<kF16>(a, qk_ws, pack_ws, s_ws, u_ws, s_max, nc, dev, stream);
+    case kBF16: return launch_dt<kBF16>(a, qk_ws, pack_ws, s_ws, u_ws, s_max, nc, dev, stream);
   }
   return cudaErrorInvalidValue;
 }

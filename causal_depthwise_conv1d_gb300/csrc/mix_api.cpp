@@ -47,6 +47,29 @@ GdrWorkspace gdr_workspace(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t
   return w;
 }
 
+// The backward pass: every part on a 256-byte boundary.
+struct GdrBwdWorkspace {
+  uint64_t qk, pack, state, tok, max, total;
+};
+
+GdrBwdWorkspace gdr_bwd_workspace(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
+                                  ccv_dtype dtype) {
+  GdrBwdWorkspace w = {0, 0, 0, 0, 0, 0};
+  if (B == 0 || Hv == 0 || Dv == 0 || L == 0) return w;
+  ccv::GdrArgs a = {};
+  a.B = B, a.L = L, a.Hk = Hk, a.Hv = Hv, a.Dk = Dk, a.Dv = Dv;
+  const int nc = gdr_chunks(L);
+  const uint64_t chunks = static_cast<uint64_t>(B * Hv) * nc, dvp = static_cast<uint64_t>((Dv + 15) / 16 * 16);
+  auto up = [](uint64_t x) { return (x + 255) / 256 * 256; };
+  w.qk = up(ccv::gdr_qk_bytes(a, static_cast<ccv::Dtype>(dtype), nc));
+  w.pack = up(ccv::gdr_pack_bytes(a, nc));
+  w.state = up(chunks * (Dk <= 64 ? 64 : 128) * dvp * 4);
+  w.tok = up(chunks * ccv::kGdrChunk * dvp * 4);
+  w.max = up(chunks * 4);
+  w.total = w.qk + w.pack + 2 * (w.state + w.tok + w.max);
+  return w;
+}
+
 // The tensors of one call: each is checked when it is added (strides given,
 // alignment, extent, an output's elements distinct), and then the outputs are
 // checked against all others.
@@ -244,7 +267,7 @@ ccv_status ccv_gdr_fwd(const void* q, const int64_t q_strides[4], const void* k,
   uint8_t* qk_ws = static_cast<uint8_t*>(workspace);
   uint8_t* pack_ws = qk_ws + w.qk;
   cudaError_t err = ccv::launch_gdr_prep(a, dt, qk_ws, pack_ws, gdr_chunks(L), s);
-  if (err == cudaSuccess) err = ccv::launch_gdr_scan(a, dt, qk_ws, pack_ws, nullptr, nullptr, gdr_chunks(L), dev, s);
+  if (err == cudaSuccess) err = ccv::launch_gdr_scan(a, dt, qk_ws, pack_ws, nullptr, nullptr, nullptr, gdr_chunks(L), dev, s);
   return launched(err, "gdr_chunk");
 }
 
@@ -296,6 +319,97 @@ ccv_status ccv_gdr_step(const void* q, const int64_t q_strides[4], const void* k
   a.B = B, a.L = S, a.Hk = Hk, a.Hv = Hv, a.Dk = Dk, a.Dv = Dv, a.scale = scale;
   return launched(ccv::launch_gdr_step(a, static_cast<ccv::Dtype>(dtype), dev, static_cast<cudaStream_t>(stream)),
                   "gdr_step");
+}
+
+ccv_status ccv_gdr_bwd_workspace_size(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
+                                      ccv_dtype dtype, uint64_t* bytes) {
+  ccv::api_begin();
+  if (bytes == nullptr) CCV_FAIL(CCV_ERR_INVALID_ARG, "bytes is required");
+  CCV_TRY(check_gdr_sizes(B, L, Hk, Hv, Dk, Dv, ccv::kGdrChunkDk, dtype));
+  *bytes = gdr_bwd_workspace(B, L, Hk, Hv, Dk, Dv, dtype).total;
+  return CCV_OK;
+}
+
+ccv_status ccv_gdr_bwd(const void* q, const int64_t q_strides[4], const void* k, const int64_t k_strides[4],
+                       const void* v, const int64_t v_strides[4], const float* g, const int64_t g_strides[3],
+                       const void* beta, const int64_t beta_strides[3], const int32_t* seq_idx,
+                       const int64_t seq_idx_strides[2], const float* initial_state,
+                       const int64_t initial_state_strides[4], const void* dout, const int64_t dout_strides[4],
+                       const float* dfinal_state, const int64_t dfinal_state_strides[4], void* dq,
+                       const int64_t dq_strides[4], void* dk, const int64_t dk_strides[4], void* dv,
+                       const int64_t dv_strides[4], float* dg, const int64_t dg_strides[3], void* dbeta,
+                       const int64_t dbeta_strides[3], float* dinitial_state, const int64_t dinitial_state_strides[4],
+                       void* workspace, uint64_t workspace_bytes, int64_t B, int64_t L, int64_t Hk, int64_t Hv,
+                       int64_t Dk, int64_t Dv, float scale, ccv_dtype dtype, void* stream) {
+  ccv::api_begin();
+  CCV_TRY(check_gdr_sizes(B, L, Hk, Hv, Dk, Dv, ccv::kGdrChunkDk, dtype));
+  if (dinitial_state != nullptr && initial_state == nullptr)
+    CCV_FAIL(CCV_ERR_INVALID_ARG, "dinitial_state requires initial_state");
+  if (B == 0 || Hv == 0) {
+    ccv::api_kernel("none");
+    return CCV_OK;
+  }
+  if (Dv == 0) CCV_FAIL(CCV_ERR_INVALID_ARG, "Dv must be >= 1");
+  const int64_t e = dtype_size(dtype);
+  const int64_t qk[4] = {B, L, Hk, Dk}, vo[4] = {B, L, Hv, Dv}, gate[3] = {B, L, Hv}, st[4] = {B, Hv, Dk, Dv},
+                ids[2] = {B, L};
+  Tensors t;
+  CCV_TRY(t.add("q", q, q_strides, 4, qk, e, false, true));
+  CCV_TRY(t.add("k", k, k_strides, 4, qk, e, false, true));
+  CCV_TRY(t.add("v", v, v_strides, 4, vo, e, false, true));
+  CCV_TRY(t.add("g", g, g_strides, 3, gate, 4, false, true));
+  CCV_TRY(t.add("beta", beta, beta_strides, 3, gate, e, false, true));
+  CCV_TRY(t.add("seq_idx", seq_idx, seq_idx_strides, 2, ids, 4, false, false));
+  CCV_TRY(t.add("initial_state", initial_state, initial_state_strides, 4, st, 4, false, false));
+  CCV_TRY(t.add("dout", dout, dout_strides, 4, vo, e, false, true));
+  CCV_TRY(t.add("dfinal_state", dfinal_state, dfinal_state_strides, 4, st, 4, false, false));
+  CCV_TRY(t.add("dq", dq, dq_strides, 4, qk, e, true, true));
+  CCV_TRY(t.add("dk", dk, dk_strides, 4, qk, e, true, true));
+  CCV_TRY(t.add("dv", dv, dv_strides, 4, vo, e, true, true));
+  CCV_TRY(t.add("dg", dg, dg_strides, 3, gate, 4, true, true));
+  CCV_TRY(t.add("dbeta", dbeta, dbeta_strides, 3, gate, e, true, true));
+  CCV_TRY(t.add("dinitial_state", dinitial_state, dinitial_state_strides, 4, st, 4, true, false));
+  const GdrBwdWorkspace ws = gdr_bwd_workspace(B, L, Hk, Hv, Dk, Dv, dtype);
+  CCV_TRY(add_workspace(t, workspace, workspace_bytes, ws.total, 128));
+  CCV_TRY(t.disjoint());
+  if (L == 0 && dinitial_state == nullptr) {
+    ccv::api_kernel("none");
+    return CCV_OK;
+  }
+  ccv::Device dev;
+  CCV_TRY(static_cast<ccv_status>(ccv::api_device(&dev)));
+  ccv::GdrArgs a = {};
+  a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.seq = seq_idx, a.s0 = initial_state;
+  copy(a.qs, q_strides, 4), copy(a.ks, k_strides, 4), copy(a.vs, v_strides, 4), copy(a.gs, g_strides, 3);
+  copy(a.bs, beta_strides, 3), copy(a.ss, seq_idx_strides, 2), copy(a.s0s, initial_state_strides, 4);
+  a.B = B, a.L = L, a.Hk = Hk, a.Hv = Hv, a.Dk = Dk, a.Dv = Dv, a.scale = scale;
+  ccv::GdrGrads gr = {};
+  gr.dout = dout, gr.ds1 = dfinal_state, gr.dq = dq, gr.dk = dk, gr.dv = dv, gr.dg = dg, gr.dbeta = dbeta;
+  gr.ds0 = dinitial_state;
+  copy(gr.dos, dout_strides, 4), copy(gr.ds1s, dfinal_state_strides, 4), copy(gr.dqs, dq_strides, 4);
+  copy(gr.dks, dk_strides, 4), copy(gr.dvs, dv_strides, 4), copy(gr.dgs, dg_strides, 3);
+  copy(gr.dbs, dbeta_strides, 3), copy(gr.ds0s, dinitial_state_strides, 4);
+  const ccv::Dtype dt = static_cast<ccv::Dtype>(dtype);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int nc = gdr_chunks(L);
+  uint8_t* p = static_cast<uint8_t*>(workspace);
+  uint8_t *qk_ws = p, *pack_ws = qk_ws + ws.qk;
+  float* s_ws = reinterpret_cast<float*>(pack_ws + ws.pack);
+  float* u_ws = s_ws + ws.state / 4;
+  float* d_ws = u_ws + ws.tok / 4;
+  float* r_ws = d_ws + ws.state / 4;
+  unsigned* s_max = reinterpret_cast<unsigned*>(r_ws + ws.tok / 4);
+  unsigned* d_max = s_max + ws.max / 4;
+  const ccv::GdrBwdWs w = {qk_ws, pack_ws, s_ws, u_ws, s_max, d_ws, r_ws, d_max};
+  cudaError_t err = cudaSuccess;
+  if (L > 0) {
+    err = cudaMemsetAsync(s_max, 0, 2 * ws.max, s);
+    if (err == cudaSuccess) err = ccv::launch_gdr_prep(a, dt, qk_ws, pack_ws, nc, s);
+    if (err == cudaSuccess) err = ccv::launch_gdr_scan(a, dt, qk_ws, pack_ws, s_ws, u_ws, s_max, nc, dev, s);
+  }
+  if (err == cudaSuccess) err = ccv::launch_gdr_bwd_scan(a, gr, dt, w, nc, dev, s);
+  if (err == cudaSuccess && L > 0) err = ccv::launch_gdr_bwd_grad(a, gr, dt, w, nc, s);
+  return launched(err, "gdr_bwd");
 }
 
 }  // extern "C"

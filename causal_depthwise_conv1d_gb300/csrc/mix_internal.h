@@ -66,13 +66,31 @@ cudaError_t launch_gdr_step(const GdrArgs& a, Dtype dt, const Device& dev, cudaS
 // pack_ws: see gdr_chunk.cuh), then the scan that carries it.  nc = chunks.
 cudaError_t launch_gdr_prep(const GdrArgs& a, Dtype dt, uint8_t* qk_ws, uint8_t* pack_ws, int nc, cudaStream_t stream);
 // For the backward pass the scan makes no output but keeps each chunk's first
-// state and its U (FP32, [b][h][chunk][Dk or 64][dvp]) in s_ws and u_ws.
+// state and its U (FP32, [b][h][chunk][DK or 64][dvp], DK = 64 or 128 and dvp
+// = Dv rounded up to 16) in s_ws and u_ws, and raises s_max[b][h][chunk] to the
+// magnitude (as bits) of the state's largest element.
 cudaError_t launch_gdr_scan(const GdrArgs& a, Dtype dt, const uint8_t* qk_ws, const uint8_t* pack_ws, float* s_ws,
-                            float* u_ws, int nc, const Device& dev, cudaStream_t stream);
+                            float* u_ws, unsigned* s_max, int nc, const Device& dev, cudaStream_t stream);
+
+// Backward pass after these two: the reverse scan (dv, the state's gradient
+// after each chunk in d_ws, the gradient of U in r_ws) and the gradients of
+// one chunk each.
+struct GdrBwdWs {
+  const uint8_t *qk, *pack;
+  const float *s, *u;
+  const unsigned* s_max;
+  float *d, *r;
+  unsigned* d_max;
+};
+cudaError_t launch_gdr_bwd_scan(const GdrArgs& a, const GdrGrads& g, Dtype dt, const GdrBwdWs& w, int nc,
+                                const Device& dev, cudaStream_t stream);
+cudaError_t launch_gdr_bwd_grad(const GdrArgs& a, const GdrGrads& g, Dtype dt, const GdrBwdWs& w, int nc,
+                                cudaStream_t stream);
 // Bytes of qk_ws and pack_ws.
 uint64_t gdr_qk_bytes(const GdrArgs& a, Dtype dt, int nc);
 uint64_t gdr_pack_bytes(const GdrArgs& a, int nc);
 unsigned read_and_clear_fault_gdr();
+unsigned read_and_clear_fault_gdr_bwd();
 
 struct LnArgs {
   const void* x;

@@ -5,6 +5,7 @@ outputs and of the workspace, and the C call on the tensor's current stream.
 The compute is in the library's kernels alone.
 
     gated_delta_rule_fwd    whole sequences         (ccv_gdr_fwd)
+    gated_delta_rule_bwd    its backward pass       (ccv_gdr_bwd)
     gated_delta_rule_step   decode step             (ccv_gdr_step)
     layer_norm_fwd          layer normalisation     (ccv_ln_fwd)
     layer_norm_bwd          its backward pass       (ccv_ln_bwd)
@@ -25,6 +26,8 @@ _SIGNATURES = {
     "ccv_gdr_fwd": _T * 9 + [_vp, _u64] + [_i64] * 6 + [_f32, _int, _vp],
     "ccv_gdr_fwd_workspace_size": [_i64] * 6 + [_int, ctypes.POINTER(_u64)],
     "ccv_gdr_step": _T * 6 + [_i64, _vp, _i64] + _T + [_i64] * 6 + [_f32, _int, _vp],
+    "ccv_gdr_bwd": _T * 15 + [_vp, _u64] + [_i64] * 6 + [_f32, _int, _vp],
+    "ccv_gdr_bwd_workspace_size": [_i64] * 6 + [_int, ctypes.POINTER(_u64)],
     "ccv_ln_fwd": _T + [_vp, _i64] * 2 + _T + [_i64, _i64, _f32, _int, _int, _vp],
     "ccv_ln_bwd": _T + [_vp, _i64] + _T * 2 + [_vp, _i64] * 2 + [_vp, _u64, _i64, _i64, _f32, _int, _int, _vp],
     "ccv_ln_bwd_workspace_size": [_i64, _i64, ctypes.POINTER(_u64)],
@@ -167,6 +170,56 @@ def ccv_gdr_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Ten
     return res
 
 
+def ccv_gdr_bwd_workspace_size(B: int, L: int, Hk: int, Hv: int, Dk: int, Dv: int, dtype: int) -> int:
+    """Bytes of workspace ``ccv_gdr_bwd`` needs for these sizes."""
+    n = _u64(0)
+    _call("ccv_gdr_bwd_workspace_size", int(B), int(L), int(Hk), int(Hv), int(Dk), int(Dv), int(dtype),
+          ctypes.byref(n))
+    return int(n.value)
+
+
+def ccv_gdr_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                dout: torch.Tensor, scale: Optional[float] = None, seq_idx: Optional[torch.Tensor] = None,
+                initial_state: Optional[torch.Tensor] = None, dfinal_state: Optional[torch.Tensor] = None,
+                dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                dv: Optional[torch.Tensor] = None, dg: Optional[torch.Tensor] = None,
+                dbeta: Optional[torch.Tensor] = None, dinitial_state: Optional[torch.Tensor] = None,
+                return_dinitial_state: bool = False, workspace: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None):
+    """Backward pass of ``ccv_gdr_fwd``: returns (dq, dk, dv, dg, dbeta, dinitial_state).
+
+    The forward's inputs plus dout [B,L,Hv,Dv] and dfinal_state FP32
+    [B,Hv,Dk,Dv] (or None).  Gradients have their inputs' shapes and dtypes;
+    dinitial_state is made when initial_state is given and
+    ``return_dinitial_state`` is set (or the tensor is passed in).
+    """
+    B, L, Hk, Hv, Dk, Dv = _gdr_sizes(q, k, v)
+    dt, st, dev = v.dtype, (B, Hv, Dk, Dv), v.device
+    qk, vo, gate = (B, L, Hk, Dk), (B, L, Hv, Dv), (B, L, Hv)
+    dq = torch.empty(qk, dtype=dt, device=dev) if dq is None else dq
+    dk = torch.empty(qk, dtype=dt, device=dev) if dk is None else dk
+    dv = torch.empty(vo, dtype=dt, device=dev) if dv is None else dv
+    dg = torch.empty(gate, dtype=torch.float32, device=dev) if dg is None else dg
+    dbeta = torch.empty(gate, dtype=dt, device=dev) if dbeta is None else dbeta
+    if dinitial_state is None and return_dinitial_state and initial_state is not None:
+        dinitial_state = torch.empty(st, dtype=torch.float32, device=dev)
+    f32 = torch.float32
+    _check(v, q=(q, qk, dt), k=(k, qk, dt), v=(v, vo, dt), g=(g, gate, f32), beta=(beta, gate, dt),
+           seq_idx=(seq_idx, (B, L), torch.int32), initial_state=(initial_state, st, f32), dout=(dout, vo, dt),
+           dfinal_state=(dfinal_state, st, f32), dq=(dq, qk, dt), dk=(dk, qk, dt), dv=(dv, vo, dt),
+           dg=(dg, gate, f32), dbeta=(dbeta, gate, dt), dinitial_state=(dinitial_state, st, f32))
+    need = ccv_gdr_bwd_workspace_size(B, L, Hk, Hv, Dk, Dv, TORCH_DTYPE[dt])
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    with torch.cuda.device(dev):
+        ws = _workspace("workspace", need, workspace, dev)
+        _call("ccv_gdr_bwd", *_t(q), *_t(k), *_t(v), *_t(g), *_t(beta), *_t(seq_idx), *_t(initial_state), *_t(dout),
+              *_t(dfinal_state), *_t(dq), *_t(dk), *_t(dv), *_t(dg), *_t(dbeta), *_t(dinitial_state),
+              None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(), B, L, Hk,
+              Hv, Dk, Dv, float(Dk ** -0.5 if scale is None else scale), TORCH_DTYPE[dt], stream.cuda_stream)
+    return dq, dk, dv, dg, dbeta, dinitial_state
+
+
 def _rows(x: torch.Tensor) -> torch.Tensor:
     """[..., D] as [N, D] without a copy."""
     if x.dim() == 2:
@@ -253,6 +306,7 @@ def ccv_ln_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], dout: torch.Tens
 
 
 gated_delta_rule_fwd = ccv_gdr_fwd
+gated_delta_rule_bwd = ccv_gdr_bwd
 gated_delta_rule_step = ccv_gdr_step
 layer_norm_fwd = ccv_ln_fwd
 layer_norm_bwd = ccv_ln_bwd

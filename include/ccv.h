@@ -395,6 +395,45 @@ ccv_status ccv_gdr_step(const void* q, const int64_t q_strides[4], const void* k
                         int64_t Dv, float scale, ccv_dtype dtype, void* stream);
 
 /*
+ * ccv_gdr_bwd -- gated delta rule, backward pass: the gradients of
+ * sum(out dout) + sum(final_state dfinal_state), everything recomputed from
+ * the forward's inputs.
+ *
+ *   q .. initial_state  the forward pass's arguments.
+ *   dout              [B,L,Hv,Dv] in dtype.
+ *   dfinal_state      FP32 [B,Hv,Dk,Dv] or NULL (zero).
+ *   dq, dk            [B,L,Hk,Dk] in dtype, summed over the value heads that
+ *                     share a key head.
+ *   dv                [B,L,Hv,Dv] in dtype;  dg FP32 [B,L,Hv];  dbeta
+ *                     [B,L,Hv] in dtype.  All five are required.
+ *   dinitial_state    FP32 [B,Hv,Dk,Dv] or NULL; needs initial_state.
+ *   workspace         ccv_gdr_bwd_workspace_size() bytes, 128-byte aligned.
+ *   Dk                1..128.
+ *
+ * All sums are FP32 or better, in a fixed order (bitwise reproducible), with
+ * one rounding to the output's type.  dg is zero at a sequence's first token
+ * that has no state before it.  A non-finite value may reach the gradients of
+ * every token of its aligned chunk of 64 besides those that the definition
+ * gives, but no other chunk of another sequence.  Outputs must not share
+ * memory with an input or each other.
+ */
+ccv_status ccv_gdr_bwd(const void* q, const int64_t q_strides[4], const void* k, const int64_t k_strides[4],
+                       const void* v, const int64_t v_strides[4], const float* g, const int64_t g_strides[3],
+                       const void* beta, const int64_t beta_strides[3], const int32_t* seq_idx,
+                       const int64_t seq_idx_strides[2], const float* initial_state,
+                       const int64_t initial_state_strides[4], const void* dout, const int64_t dout_strides[4],
+                       const float* dfinal_state, const int64_t dfinal_state_strides[4], void* dq,
+                       const int64_t dq_strides[4], void* dk, const int64_t dk_strides[4], void* dv,
+                       const int64_t dv_strides[4], float* dg, const int64_t dg_strides[3], void* dbeta,
+                       const int64_t dbeta_strides[3], float* dinitial_state, const int64_t dinitial_state_strides[4],
+                       void* workspace, uint64_t workspace_bytes, int64_t B, int64_t L, int64_t Hk, int64_t Hv,
+                       int64_t Dk, int64_t Dv, float scale, ccv_dtype dtype, void* stream);
+
+/* Bytes of workspace ccv_gdr_bwd needs for these sizes.  Host only. */
+ccv_status ccv_gdr_bwd_workspace_size(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
+                                      ccv_dtype dtype, uint64_t* bytes);
+
+/*
  * ccv_ln_fwd -- layer normalisation of the rows of x [N,D]:
  *     out = (x - mean) / sqrt(var + eps) * weight + bias,
  * mean and (biased) variance over the row in FP32, out rounded once to dtype.
@@ -436,7 +475,7 @@ const char* ccv_last_error(void);
 /* Name of the kernel variant the last successful ccv_fwd, ccv_update or
  * ccv_bwd on this thread enqueued (e.g. "time_vec", "chlast_tma",
  * "chlast_vec", "generic", "update", "bwd_time", "bwd_chlast",
- * "bwd_generic", "gdr_step", "gdr_chunk", "ln_fwd", "ln_bwd", "none"). */
+ * "bwd_generic", "gdr_step", "gdr_chunk", "gdr_bwd", "ln_fwd", "ln_bwd", "none"). */
 const char* ccv_last_kernel(void);
 
 /* Library ABI version: (major << 16) | minor. */

@@ -118,3 +118,83 @@ def ln_bwd(x, w, dy, eps=1e-5):
 
 def np_rng(seed):
     return np.random.default_rng(seed)
+
+
+def gdr_bwd(c, scale=None, chunk=64):
+    """{name: (gradient, error bound)} from the token-by-token definition in FP64.
+
+    The bounds follow the same argument as ``gdr``'s: for |k| <= 1,
+    0 <= beta <= 1 and decays <= 1 both the state and, backwards, its gradient
+    are mapped by contractions, so the errors of the tokens add up, decayed.  A
+    token's own error is gamma times the norms that enter it, gamma =
+    4 (D + 64) 2^-24 for the up to four sums of D products between its inputs
+    and a result.  e* below are errors of norms: eS of the state, eD of its
+    gradient.  dg is summed from terms of the tokens up to the end of its chunk,
+    so the errors of those add to its own."""
+    q, k, v, g, beta = (c[n] for n in ("q", "k", "v", "g", "beta"))
+    B, L, Hk, Dk = q.shape
+    Hv, Dv = v.shape[2:]
+    rep = Hv // Hk
+    q, k = (x.double().repeat_interleave(rep, 2) for x in (q, k))
+    v, beta, a, do = v.double(), beta.double(), torch.exp(g.double()), c["dout"].double()
+    scale = Dk ** -0.5 if scale is None else scale
+    keep = _keep(c["seq_idx"], B, L)
+    zero = torch.zeros(()).double()
+    gam = 4 * (max(Dk, Dv) + 64) * 2.0 ** -24
+    fro = lambda x: x.flatten(2).norm(dim=2)  # noqa: E731
+    nrm = lambda x: x.norm(dim=-1)  # noqa: E731
+    S = torch.zeros((B, Hv, Dk, Dv), dtype=torch.float64) if c["initial_state"] is None \
+        else c["initial_state"].double()
+    eS = torch.zeros((B, Hv), dtype=torch.float64)
+    hist = []
+    for t in range(L):
+        on = keep[:, t, None]
+        A = torch.where(on[..., None, None] > 0, S * a[:, t, :, None, None], zero)
+        eA = torch.where(on > 0, eS * a[:, t], zero)
+        w = v[:, t] - torch.einsum("bhk,bhkv->bhv", k[:, t], A)
+        u = beta[:, t, :, None] * w
+        ew = eA + gam * (fro(A) + nrm(v[:, t]))
+        S = A + k[:, t, :, :, None] * u[:, :, None, :]
+        eS = eA + gam * (fro(A) + nrm(v[:, t]) + nrm(u))
+        hist.append((A, eA, w, ew, u, S, eS))
+    D = torch.zeros_like(S) if c["dfinal_state"] is None else c["dfinal_state"].double()
+    eD = torch.zeros((B, Hv), dtype=torch.float64)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    eq, ek, ev, eb, own = (torch.empty((B, L, Hv), dtype=torch.float64) for _ in range(5))
+    dg, db = torch.empty_like(a), torch.empty_like(a)
+    for t in reversed(range(L)):
+        A, eA, w, ew, u, S1, eS1 = hist[t]
+        d = scale * do[:, t]
+        eD = eD + gam * nrm(q[:, t]) * nrm(d)
+        D = D + q[:, t, :, :, None] * d[:, :, None, :]
+        du = torch.einsum("bhk,bhkv->bhv", k[:, t], D)
+        edu = eD + gam * fro(D)
+        be = beta[:, t]
+        dq[:, t] = torch.einsum("bhkv,bhv->bhk", S1, d)
+        eq[:, t] = (eS1 + gam * fro(S1)) * nrm(d)
+        db[:, t] = (du * w).sum(-1)
+        eb[:, t] = edu * nrm(w) + nrm(du) * ew + gam * nrm(du) * (nrm(w) + nrm(v[:, t]))
+        dv[:, t] = be[..., None] * du
+        ev[:, t] = be * edu
+        dk[:, t] = torch.einsum("bhkv,bhv->bhk", D, u) - torch.einsum("bhkv,bhv->bhk", A, dv[:, t])
+        ek[:, t] = eD * nrm(u) + fro(D) * be * ew + eA * nrm(dv[:, t]) + fro(A) * ev[:, t] + \
+            gam * (fro(D) * nrm(u) + fro(A) * nrm(dv[:, t]))
+        dA = D - k[:, t, :, :, None] * dv[:, t, :, None, :]
+        edA = eD + ev[:, t] + gam * fro(D)
+        dg[:, t] = (dA * A).sum((2, 3))
+        own[:, t] = edA * fro(A) + fro(dA) * eA + gam * fro(dA) * fro(A)
+        on = keep[:, t, None]
+        D = torch.where(on[..., None, None] > 0, dA * a[:, t, :, None, None], zero)
+        eD = torch.where(on > 0, edA * a[:, t], zero)
+    term = eq + 3 * ek + 2 * eb  # of one token's share of dg (|q|, |k|, beta <= 1)
+    tail = torch.empty_like(term)
+    for t in range(L):
+        tail[:, t] = term[:, t:(t // chunk + 1) * chunk].sum(1)
+        last = min(L, (t // chunk + 1) * chunk) - 1
+        tail[:, t] += own[:, last] + own[:, t]
+    share = lambda x: x.unflatten(2, (Hk, rep)).sum(3)  # noqa: E731
+    res = {"dq": (share(dq), share(eq)[..., None]), "dk": (share(dk), share(ek)[..., None]),
+           "dv": (dv, ev[..., None]), "dg": (dg, tail), "dbeta": (db, eb)}
+    if c["initial_state"] is not None:
+        res["dinitial_state"] = (D, eD[..., None, None] + gam * fro(D)[..., None, None])
+    return res

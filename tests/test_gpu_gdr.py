@@ -242,3 +242,138 @@ def test_back_to_back_calls_keep_stream_order():
 
     (a, sa), (b, sb) = chain(False), chain(True)
     assert torch.equal(a, b) and torch.equal(sa, sb)
+
+
+NAMES = ("dq", "dk", "dv", "dg", "dbeta", "dinitial_state")
+
+
+def run_bwd(d, **kw):
+    return dict(zip(NAMES, ccv.gated_delta_rule_bwd(
+        d["q"], d["k"], d["v"], d["g"], d["beta"], d["dout"], seq_idx=d["seq_idx"], initial_state=d["initial_state"],
+        dfinal_state=d["dfinal_state"], return_dinitial_state=True, **kw)))
+
+
+def check_bwd(c, dtype, d=None, **kw):
+    got = run_bwd(dev(c) if d is None else d, **kw)
+    assert ccv.ccv_last_kernel() == "gdr_bwd"
+    want = ref.gdr_bwd(c)
+    assert (got["dinitial_state"] is None) == (c["initial_state"] is None)
+    for n, (e, bound) in want.items():
+        if n not in ("dg", "dinitial_state"):
+            bound = bound + ref.rounding(e, dtype)
+        assert ref.worst(got[n], e, bound) <= 1, n
+    return got
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("size", [s for s in SIZES if s[4] <= 128], ids=str)
+def test_backward(size, dtype):
+    check_bwd(ref.gdr_inputs(21, *size, dtype, grads=True), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("size,seqs", [((2, 150, 1, 2, 128, 64), 4), ((1, 64, 1, 1, 64, 64), 64),
+                                       ((1, 200, 2, 6, 64, 160), 3), ((3, 40, 1, 1, 64, 32), 2)], ids=str)
+def test_backward_of_packed_sequences_and_states(size, seqs, dtype):
+    c = ref.gdr_inputs(22, *size, dtype, seqs=seqs, state=True, grads=True)
+    got = check_bwd(c, dtype)
+    again = run_bwd(dev(c))
+    assert all(torch.equal(got[n], again[n]) for n in NAMES)  # fixed order
+    first = torch.zeros_like(c["seq_idx"], dtype=torch.bool)
+    first[:, 1:] = c["seq_idx"][:, 1:] != c["seq_idx"][:, :-1]
+    assert not got["dg"].cpu()[first].any()  # nothing decays into a new sequence
+
+
+def test_backward_against_differences_of_the_forward():
+    """f32: directional derivatives of the forward kernel itself."""
+    c = ref.gdr_inputs(23, 1, 130, 1, 2, 64, 64, "f32", seqs=2, state=True, grads=True)
+    d = dev(c)
+    got = run_bwd(d)
+
+    def loss(n, delta):
+        x = dict(d)
+        x[n] = d[n] + delta
+        o, s = ccv.gated_delta_rule_fwd(x["q"], x["k"], x["v"], x["g"], x["beta"], seq_idx=x["seq_idx"],
+                                        initial_state=x["initial_state"], return_final_state=True)
+        return float((o.double() * d["dout"].double()).sum() + (s.double() * d["dfinal_state"].double()).sum())
+
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    for n in ("q", "k", "v", "g", "beta", "initial_state"):
+        way = torch.randn(d[n].shape, generator=gen, device="cuda") * d[n].abs().mean()
+        want = float((way.double() * got["d" + n].double()).sum())
+        size = float((way.double() * got["d" + n].double()).abs().sum())
+        h = 2.0 ** -8
+        # the third derivative's share is of order h^2, the outputs' roundings of order 2^-22 / h
+        assert abs((loss(n, h * way) - loss(n, -h * way)) / (2 * h) - want) < 2e-3 * size, n
+
+
+def test_backward_views_and_outputs():
+    """Gradients written into channel slices of one buffer; strided inputs."""
+    B, L, Hk, Hv, Dk, Dv = 2, 100, 2, 2, 64, 64
+    c = ref.gdr_inputs(24, B, L, Hk, Hv, Dk, Dv, "bf16", grads=True)
+    d = dev(c)
+    plain = check_bwd(c, "bf16", d)
+    n = Hk * Dk
+    for off in (0, 1):  # aligned slices, and slices off by one element
+        buf = torch.zeros(B * L * 3 * n + off, dtype=torch.bfloat16, device="cuda")[off:].view(B, L, 3 * n)
+        x = torch.cat([d[m].flatten(2) for m in ("q", "k", "v")], 2)
+        src = torch.empty(x.numel() + off, dtype=x.dtype, device="cuda")[off:].view(x.shape)
+        src.copy_(x)
+        e = dict(d)
+        e["q"], e["k"], e["v"] = (src[..., i * n:(i + 1) * n].unflatten(-1, (Hk, Dk)) for i in range(3))
+        e["dout"] = d["dout"].transpose(1, 2).contiguous().transpose(1, 2)
+        dq, dk, dv = (buf[..., i * n:(i + 1) * n].unflatten(-1, (Hk, Dk)) for i in range(3))
+        got = run_bwd(e, dq=dq, dk=dk, dv=dv)
+        assert all(torch.equal(got[m], plain[m]) for m in ("dq", "dk", "dv", "dg", "dbeta"))
+
+
+def test_backward_empty():
+    d = dev(ref.gdr_inputs(25, 2, 0, 1, 2, 64, 32, "bf16", state=True, grads=True))
+    got = run_bwd(d)
+    assert got["dq"].shape == (2, 0, 1, 64) and torch.equal(got["dinitial_state"], d["dfinal_state"])
+    e = dev(ref.gdr_inputs(25, 0, 5, 1, 2, 64, 32, "bf16", grads=True))
+    assert run_bwd(e)["dv"].shape == (0, 5, 2, 32)
+
+
+def test_backward_magnitudes():
+    """Rows of q and k of very different length keep gradients of full precision; zero rows too."""
+    c = ref.gdr_inputs(26, 1, 100, 1, 2, 64, 64, "bf16", grads=True)
+    c["k"][:, 5:9] = (c["k"][:, 5:9].float() * 1e-12).to(torch.bfloat16)
+    c["q"][:, 20:30] = (c["q"][:, 20:30].float() * 1e-12).to(torch.bfloat16)
+    c["k"][:, 40] = 0
+    c["q"][:, 41] = 0
+    c["beta"][:, 50:60] = 0
+    c["g"][:, 70] = -300.0
+    check_bwd(c, "bf16")
+
+
+def test_backward_non_finite_sequences_leave_others_alone():
+    c = ref.gdr_inputs(27, 1, 256, 1, 2, 64, 32, "bf16", state=True, grads=True)
+    ids = torch.zeros(1, 256, dtype=torch.int32)
+    ids[:, 64:] = 1
+    ids[:, 192:] = 2
+    c["seq_idx"] = ids
+    clean = ref.gdr_bwd(c)
+    for n in ("q", "k", "v", "g", "beta", "dout"):
+        d = dev(c)
+        d[n][0, 100, 0] = float("nan")  # in the second sequence, chunks 1 and 2
+        got = run_bwd(d)
+        for m in ("dq", "dk", "dv", "dg", "dbeta"):
+            e, bound = clean[m]
+            if m != "dg":
+                bound = bound + ref.rounding(e, "bf16")
+            for part in (slice(0, 64), slice(192, 256)):
+                assert ref.worst(got[m][:, part], e[:, part], bound[:, part]) <= 1, (n, m)
+
+
+def test_backward_other_stream_and_workspace():
+    d = dev(ref.gdr_inputs(28, 1, 150, 1, 2, 64, 64, "f16", state=True, grads=True))
+    want = run_bwd(d)
+    ws = torch.full((ccv.ccv_gdr_bwd_workspace_size(1, 150, 1, 2, 64, 64, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = run_bwd(d, workspace=ws, stream=side)
+    side.synchronize()
+    assert all(torch.equal(got[n], want[n]) for n in NAMES)
+    with pytest.raises(ccv.CcvError, match="workspace too small"):
+        run_bwd(d, workspace=ws[:-256])

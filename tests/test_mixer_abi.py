@@ -83,6 +83,61 @@ def test_empty_problems_are_no_ops(mx, kw):
     assert status(mx, "ccv_gdr_fwd", gdr_args(mx, L=0))[0] == 0
 
 
+def bwd_args(mx, **kw):
+    L, Hk, Hv, Dk, Dv = 8, 2, 4, 16, 32
+    qs, vs, gs, ss = (L * Hk * Dk, Hk * Dk, Dk, 1), (L * Hv * Dv, Hv * Dv, Dv, 1), (L * Hv, Hv, 1), \
+        (Hv * Dk * Dv, Dk * Dv, Dv, 1)
+    a = dict(q=F, k=2 * F, v=3 * F, g=4 * F, beta=5 * F, seq=None, s0=None, dout=6 * F, ds1=None, dq=7 * F, dk=8 * F,
+             dv=9 * F, dg=10 * F, dbeta=11 * F, ds0=None, ws=12 * F, wsb=1 << 24, B=2, L=L, Hk=Hk, Hv=Hv, Dk=Dk, Dv=Dv,
+             scale=1.0, dtype=2)
+    st = dict(q=qs, k=qs, v=vs, g=gs, beta=gs, seq=(L, 1), s0=ss, dout=vs, ds1=ss, dq=qs, dk=qs, dv=vs, dg=gs,
+              dbeta=gs, ds0=ss)
+    st.update({n[2:]: x for n, x in kw.items() if n.startswith("s_")})
+    a.update({n: x for n, x in kw.items() if not n.startswith("s_")})
+    arr = mx._arr
+    out = []
+    for n in ("q", "k", "v", "g", "beta", "seq", "s0", "dout", "ds1", "dq", "dk", "dv", "dg", "dbeta", "ds0"):
+        out += [a[n], arr(st[n])]
+    return out + [a["ws"], a["wsb"]] + [a[n] for n in ("B", "L", "Hk", "Hv", "Dk", "Dv", "scale", "dtype")] + [None]
+
+
+@pytest.mark.parametrize("kw,st,needle", [
+    (dict(dtype=4), 1, "unknown dtype"), (dict(Dk=129), 2, "at most 128"), (dict(dout=None), 1, "dout is required"),
+    (dict(dq=None), 1, "dq is required"), (dict(dg=None), 1, "dg is required"), (dict(dbeta=None), 1, "dbeta is req"),
+    (dict(ds0=13 * F), 1, "requires initial_state"), (dict(ws=None), 1, "workspace too small"),
+    (dict(wsb=4096), 1, "workspace too small"), (dict(ws=12 * F + 16), 1, "workspace must be aligned"),
+    (dict(dq=8 * F), 1, "must not alias"), (dict(dv=6 * F), 1, "must not alias"), (dict(dv=9 * F + 1), 1, "aligned"),
+    (dict(s_dk=(0, 32, 16, 1)), 1, "zero stride"), (dict(ws=7 * F), 1, "must not alias"), (dict(Dv=0), 1, "Dv"),
+    (dict(s_dout=None), 1, "dout needs its strides"), (dict(B=1 << 45), 1, "too large")])
+def test_backward_refusals(mx, kw, st, needle):
+    rc, msg = status(mx, "ccv_gdr_bwd", bwd_args(mx, **kw))
+    assert rc == st and needle in msg, msg
+
+
+def test_channel_slices_of_one_buffer_are_told_apart(mx):
+    """dq, dk, dv as slices of one [B, L, 2 Hk Dk + Hv Dv] buffer pass; slices that share channels do not."""
+    n = 2 * 2 * 16 + 4 * 32
+    st = (8 * n, n, 16, 1)
+    ok = dict(dq=7 * F, dk=7 * F + 2 * 32, dv=7 * F + 2 * 64, s_dq=st, s_dk=st, s_dv=(8 * n, n, 32, 1))
+    # (the aliasing check comes last: an output that repeats the workspace's address shows that it got that far)
+    rc, msg = status(mx, "ccv_gdr_bwd", bwd_args(mx, dg=12 * F, **ok))
+    assert rc == 1 and "dg" in msg and "workspace" in msg
+    rc, msg = status(mx, "ccv_gdr_bwd", bwd_args(mx, **dict(ok, dk=7 * F + 2 * 31, wsb=1 << 24)))
+    assert rc == 1 and "must not alias" in msg
+    rc, msg = status(mx, "ccv_gdr_bwd", bwd_args(mx, **dict(ok, dv=7 * F + 2 * 63)))
+    assert rc == 1 and "must not alias" in msg
+
+
+def test_workspace_sizes(mx):
+    assert mx.ccv_gdr_fwd_workspace_size(1, 16, 1, 1, 128, 128, 2) == 0
+    assert mx.ccv_gdr_fwd_workspace_size(1, 4096, 1, 1, 256, 128, 2) == 0  # token by token
+    a = mx.ccv_gdr_fwd_workspace_size(1, 4096, 2, 4, 128, 128, 2)
+    assert a > 0 and mx.ccv_gdr_fwd_workspace_size(2, 4096, 2, 4, 128, 128, 2) == 2 * a
+    assert mx.ccv_gdr_bwd_workspace_size(0, 16, 1, 1, 128, 128, 2) == 0
+    assert mx.ccv_gdr_bwd_workspace_size(1, 65, 1, 1, 128, 128, 2) == \
+        mx.ccv_gdr_bwd_workspace_size(1, 128, 1, 1, 128, 128, 2)
+
+
 def ln_args(mx, bwd=False, **kw):
     a = dict(x=F, xs=(64, 1), w=2 * F, ws=1, b=3 * F, bs=1, out=4 * F, os=(64, 1), dout=5 * F, gs=(64, 1), dw=6 * F,
              dws=1, db=7 * F, dbs=1, ws_p=8 * F, ws_n=1 << 20, N=4, D=64, eps=1e-5, dtype=2, wdtype=0)
