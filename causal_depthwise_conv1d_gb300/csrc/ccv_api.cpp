@@ -239,9 +239,10 @@ ccv_status ccv_test_bounded_wait(int64_t wait_budget_cycles, int64_t skip_stage)
 ccv_status ccv_device_fault(unsigned* fault_bits) {
   g_last_error.clear();
   if (fault_bits == nullptr) return fail(CCV_ERR_INVALID_ARG, "fault_bits is required");
-  const unsigned conv = ccv::read_and_clear_fault_chlast_tma();
-  const unsigned gdr = ccv::read_and_clear_fault_gdr(), gdr_bwd = ccv::read_and_clear_fault_gdr_bwd();
-  const unsigned v = conv == ~0u || gdr == ~0u || gdr_bwd == ~0u ? ~0u : conv | gdr | gdr_bwd;
+  const unsigned words[] = {ccv::read_and_clear_fault_chlast_tma(), ccv::read_and_clear_fault_gdr(),
+                            ccv::read_and_clear_fault_gdr_bwd(), ccv::read_and_clear_fault_ln()};
+  unsigned v = 0;
+  for (const unsigned w : words) v |= w;
   if (v == ~0u) return fail(CCV_ERR_CUDA, "cannot read the fault word");
   *fault_bits = v;
   return CCV_OK;

@@ -11,12 +11,24 @@
 // column, and a second kernel adds the partials in a fixed order (bitwise
 // reproducible, no atomics).
 //
-// What bounds it: HBM (2 N D elements forward, 3 N D backward).
+// What bounds it: HBM (2 N D elements forward, 3 N D backward).  Rows of more
+// than 32 vectors come through a ring of row-sized stages in shared memory,
+// filled by bulk copies: the bytes in flight do not depend on how many
+// registers the arithmetic takes, blocks are persistent (weights stay in
+// registers), and a stage is refilled right after the row's first reduction,
+// whose barrier is also the proof that every thread has read it.  Shorter
+// rows take a warp each.
 #include "ccv_common.cuh"
+#include "ccv_tma.cuh"
 #include "mix_internal.h"
 
 namespace ccv {
 namespace {
+
+__device__ unsigned g_fault;
+
+constexpr int kRingBytes = 200 * 1024;  // stages of all blocks of an SM
+constexpr int kMaxStages = 8;
 
 // Sum of NS values over the threads that share a row: one warp, or the block.
 template <bool WARP, int NS>
@@ -66,10 +78,57 @@ __device__ __forceinline__ void store_v(void* base, int64_t off, int64_t stride,
   }
 }
 
-template <int V>
-__device__ __forceinline__ void load_par(const void* w, int64_t col, int64_t ws, int wdt, float fill, float* f) {
+// Sum over the block with one barrier: `red` (32 NS floats) is not written
+// again before another barrier has passed.
+template <int NS>
+__device__ __forceinline__ void block_sum(float (&v)[NS], float* red, int nwarps) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) f[j] = w != nullptr ? ld_param(w, (col + j) * ws, wdt) : fill;
+  for (int m = 16; m > 0; m >>= 1)
+#pragma unroll
+    for (int i = 0; i < NS; ++i) v[i] += __shfl_xor_sync(kFullMask, v[i], m);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0)
+#pragma unroll
+    for (int i = 0; i < NS; ++i) red[i * 32 + warp] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    float x = lane < nwarps ? red[i * 32 + lane] : 0.f;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(kFullMask, x, m);
+    v[i] = x;
+  }
+}
+
+// V parameters from column col: one or two vector loads where the vector is
+// dense and aligned (`vec`).
+template <int V>
+__device__ __forceinline__ void load_par_vec(const void* w, int64_t col, int64_t ws, int wdt, bool vec, float fill,
+                                             float* f) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = fill;
+  } else if (vec && V >= 4) {
+    if (wdt == kF32) {
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + col + j));
+        f[j] = x.x, f[j + 1] = x.y, f[j + 2] = x.z, f[j + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + col + j));
+        const uint32_t y[2] = {x.x, x.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          f[j + i] = wdt == kF16 ? Fmt<kF16>::word_elem(y[i >> 1], i & 1) : Fmt<kBF16>::word_elem(y[i >> 1], i & 1);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = ld_param(w, (col + j) * ws, wdt);
+  }
 }
 
 // NV vectors of V elements a thread; WARP: a warp owns a row, else the block.
@@ -119,11 +178,98 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) ln_fwd_kernel(const LnArgs 
     const int64_t col = (static_cast<int64_t>(i) * G + t) * V;
     if (col < a.D) {
       float w[V], b[V];
-      load_par<V>(a.w, col, a.ws, a.wdt, 1.f, w);
-      load_par<V>(a.b, col, a.bs, a.wdt, 0.f, b);
+      load_par_vec<V>(a.w, col, a.ws, a.wdt, a.wvec, 1.f, w);
+      load_par_vec<V>(a.b, col, a.bs, a.wdt, a.wvec, 0.f, b);
 #pragma unroll
       for (int j = 0; j < V; ++j) w[j] = fmaf(f[i][j] * r, w[j], b[j]);
       store_v<DT, V>(y, col, a.os1, w);
+    }
+  }
+}
+
+// Persistent block, rows blockIdx, blockIdx + grid, ... through the ring.
+template <int DT, int NV>
+__global__ void __launch_bounds__(512) ln_fwd_ring(const LnArgs a, int stages) {
+  constexpr int V = Fmt<DT>::VEC;
+  using E = typename Fmt<DT>::E;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ float red[2][32];
+  const uint32_t row_bytes = static_cast<uint32_t>(a.D) * sizeof(E);
+  const int t = threadIdx.x, T = blockDim.x, nwarps = T >> 5;
+  const int64_t step = gridDim.x;
+  auto fill = [&](int64_t row, int s) {
+    mbar_arrive_expect_tx(&full[s], row_bytes);
+    bulk_load(ring + s * row_bytes, static_cast<const E*>(a.x) + row * a.xs0, row_bytes, &full[s]);
+  };
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+  }
+  pdl_enter();
+  if (t == 0)
+    for (int s = 0; s < stages && blockIdx.x + s * step < a.N; ++s) fill(blockIdx.x + s * step, s);
+  float w[NV][V], b[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t col = (static_cast<int64_t>(i) * T + t) * V;
+    if (col < a.D) {
+      load_par_vec<V>(a.w, col, a.ws, a.wdt, a.wvec, 1.f, w[i]);
+      load_par_vec<V>(a.b, col, a.bs, a.wdt, a.wvec, 0.f, b[i]);
+    }
+  }
+  __syncthreads();
+  const float inv_d = 1.f / static_cast<float>(a.D);
+  int s = 0;
+  uint32_t parity = 0;
+  for (int64_t row = blockIdx.x; row < a.N; row += step) {
+    if (!mbar_wait(&full[s], parity)) {
+      if (t == 0) {
+        atomicOr(&g_fault, kFaultConsumerWait);
+        for (int k = 1; k < stages && row + k * step < a.N; ++k)  // the copies still in flight
+          mbar_wait(&full[(s + k) % stages], (s + k >= stages) ? parity ^ 1 : parity);
+      }
+      return;
+    }
+    float f[NV][V];
+    float sum[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (i * T + t) * V;
+      if (col < a.D) {
+        unpack16<DT>(lds128(ring + s * row_bytes + col * sizeof(E)), f[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[i][j] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum[0] += f[i][j];
+    }
+    block_sum(sum, red[0], nwarps);
+    if (t == 0 && row + stages * step < a.N) fill(row + stages * step, s);
+    if (++s == stages) s = 0, parity ^= 1;
+    const float mean = sum[0] * inv_d;
+    float q[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool in = (i * T + t) * V < a.D;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        f[i][j] -= mean;
+        if (in) q[0] = fmaf(f[i][j], f[i][j], q[0]);
+      }
+    }
+    block_sum(q, red[1], nwarps);
+    const float r = rsqrtf(q[0] * inv_d + a.eps);
+    E* y = static_cast<E*>(a.out) + row * a.os0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (i * T + t) * V;
+      if (col < a.D) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[i][j] = fmaf(f[i][j] * r, w[i][j], b[i][j]);
+        *reinterpret_cast<uint4*>(y + col) = pack16<DT>(f[i]);
+      }
     }
   }
 }
@@ -172,7 +318,7 @@ __global__ void __launch_bounds__(MAXT) ln_bwd_kernel(const LnBwdArgs a) {
     const int64_t col = (static_cast<int64_t>(i) * G + t) * V;
 #pragma unroll
     for (int j = 0; j < V; ++j) dw[i][j] = db[i][j] = w[i][j] = 0.f;
-    if (col < a.D) load_par<V>(a.w, col, a.ws, a.wdt, 1.f, w[i]);
+    if (col < a.D) load_par_vec<V>(a.w, col, a.ws, a.wdt, a.wvec, 1.f, w[i]);
   }
   const float inv_d = 1.f / static_cast<float>(a.D);
   const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * nwarps : gridDim.x;
@@ -261,6 +407,114 @@ __global__ void __launch_bounds__(MAXT) ln_bwd_kernel(const LnBwdArgs a) {
   }
 }
 
+// The same through the ring: a stage holds a row of x and of dout.
+template <int DT, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT) ln_bwd_ring(const LnBwdArgs a, int stages) {
+  constexpr int V = Fmt<DT>::VEC;
+  using E = typename Fmt<DT>::E;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ float red0[32], red1[96];
+  const uint32_t row_bytes = static_cast<uint32_t>(a.D) * sizeof(E);
+  const int t = threadIdx.x, T = blockDim.x, nwarps = T >> 5;
+  const int64_t step = gridDim.x;
+  auto fill = [&](int64_t row, int s) {
+    mbar_arrive_expect_tx(&full[s], 2 * row_bytes);
+    bulk_load(ring + 2 * s * row_bytes, static_cast<const E*>(a.x) + row * a.xs0, row_bytes, &full[s]);
+    bulk_load(ring + (2 * s + 1) * row_bytes, static_cast<const E*>(a.dout) + row * a.gs0, row_bytes, &full[s]);
+  };
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+  }
+  pdl_enter();
+  if (t == 0)
+    for (int s = 0; s < stages && blockIdx.x + s * step < a.N; ++s) fill(blockIdx.x + s * step, s);
+  float w[NV][V], dw[NV][V], db[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t col = (static_cast<int64_t>(i) * T + t) * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) dw[i][j] = db[i][j] = w[i][j] = 0.f;
+    if (col < a.D) load_par_vec<V>(a.w, col, a.ws, a.wdt, a.wvec, 1.f, w[i]);
+  }
+  __syncthreads();
+  const float inv_d = 1.f / static_cast<float>(a.D);
+  int s = 0;
+  uint32_t parity = 0;
+  for (int64_t row = blockIdx.x; row < a.N; row += step) {
+    if (!mbar_wait(&full[s], parity)) {
+      if (t == 0) {
+        atomicOr(&g_fault, kFaultConsumerWait);
+        for (int k = 1; k < stages && row + k * step < a.N; ++k)  // the copies still in flight
+          mbar_wait(&full[(s + k) % stages], (s + k >= stages) ? parity ^ 1 : parity);
+      }
+      return;
+    }
+    float f[NV][V], d[NV][V];
+    float sum[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (i * T + t) * V;
+      if (col < a.D) {
+        unpack16<DT>(lds128(ring + 2 * s * row_bytes + col * sizeof(E)), f[i]);
+        unpack16<DT>(lds128(ring + (2 * s + 1) * row_bytes + col * sizeof(E)), d[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[i][j] = d[i][j] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum[0] += f[i][j];
+    }
+    block_sum(sum, red0, nwarps);
+    if (t == 0 && row + stages * step < a.N) fill(row + stages * step, s);
+    if (++s == stages) s = 0, parity ^= 1;
+    const float mean = sum[0] * inv_d;
+    float q[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool in = (i * T + t) * V < a.D;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        f[i][j] = in ? f[i][j] - mean : 0.f;
+        q[0] = fmaf(f[i][j], f[i][j], q[0]);
+        const float dd = d[i][j] * w[i][j];
+        q[1] += dd;
+        q[2] = fmaf(dd, f[i][j], q[2]);
+      }
+    }
+    block_sum(q, red1, nwarps);
+    const float r = rsqrtf(q[0] * inv_d + a.eps);
+    const float c1 = q[1] * inv_d, c2 = q[2] * inv_d * r;
+    E* dx = static_cast<E*>(a.dx) + row * a.dxs0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (i * T + t) * V;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float xh = f[i][j] * r;
+        dw[i][j] = fmaf(d[i][j], xh, dw[i][j]);
+        db[i][j] += d[i][j];
+        f[i][j] = r * (d[i][j] * w[i][j] - c1 - xh * c2);
+      }
+      if (col < a.D) *reinterpret_cast<uint4*>(dx + col) = pack16<DT>(f[i]);
+    }
+  }
+  if (a.part == nullptr) return;
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.D;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t col = (static_cast<int64_t>(i) * T + t) * V;
+    if (col < a.D)
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        *reinterpret_cast<float4*>(part + col + j) = make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
+        *reinterpret_cast<float4*>(part + a.D + col + j) =
+            make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]);
+      }
+  }
+}
+
 // Rows too long for registers: sweeps over the row, the partial sums of dw
 // and db in the block's own slice of the workspace.
 template <int DT>
@@ -330,24 +584,59 @@ __global__ void ln_bwd_reduce(const LnBwdArgs a, int P) {
 
 bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+unsigned threads(int64_t n, int nv) { return static_cast<unsigned>(((n + nv - 1) / nv + 31) / 32 * 32); }
+
+// Blocks of an SM and stages of a block for rows of `bytes` a stage.
+int ring_blocks(unsigned T) { return T >= 512 ? 2 : static_cast<int>(1024 / T < 8 ? 1024 / T : 8); }
+int ring_stages(int blocks, int64_t bytes) {
+  const int64_t n = kRingBytes / (blocks * bytes);
+  return static_cast<int>(n < kMaxStages ? n : kMaxStages);
+}
+
+template <int DT, int NV>
+cudaError_t fwd_ring(const LnArgs& a, const Device& dev, cudaStream_t s) {
+  const unsigned T = threads(a.D / Fmt<DT>::VEC, NV);
+  const int64_t bytes = a.D * static_cast<int64_t>(sizeof(typename Fmt<DT>::E));
+  const int blocks = ring_blocks(T), stages = ring_stages(blocks, bytes);
+  const int64_t grid = static_cast<int64_t>(dev.sm_count) * blocks;
+  const cudaError_t e =
+      cudaFuncSetAttribute(ln_fwd_ring<DT, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(ln_fwd_ring<DT, NV>, static_cast<unsigned>(a.N < grid ? a.N : grid), T, stages * bytes, s, a,
+                    stages);
+}
+
 template <int DT>
-cudaError_t fwd_dt(const LnArgs& a, cudaStream_t s) {
+cudaError_t fwd_dt(const LnArgs& a, const Device& dev, cudaStream_t s) {
   constexpr int V = Fmt<DT>::VEC;
   const bool vec = a.xs1 == 1 && a.os1 == 1 && a.D % V == 0 && al16(a.x) && al16(a.out) &&
                    (a.N == 1 || (a.xs0 % V == 0 && a.os0 % V == 0));
   const unsigned warps_grid = static_cast<unsigned>((a.N + 7) / 8);
   const unsigned rows = static_cast<unsigned>(a.N);
-  auto threads = [](int64_t n, int nv) { return static_cast<unsigned>(((n + nv - 1) / nv + 31) / 32 * 32); };
   if (vec) {
     const int64_t n = a.D / V;
     if (n <= 32) return launch_pdl(ln_fwd_kernel<DT, V, 1, true>, warps_grid, 256, 0, s, a);
-    if (n <= 128) return launch_pdl(ln_fwd_kernel<DT, V, 4, true>, warps_grid, 256, 0, s, a);
-    if (n <= 4096) return launch_pdl(ln_fwd_kernel<DT, V, 4, false>, rows, threads(n, 4), 0, s, a);
+    if (n <= 64) return launch_pdl(ln_fwd_kernel<DT, V, 2, true>, warps_grid, 256, 0, s, a);
+    if (n <= 256) return fwd_ring<DT, 1>(a, dev, s);
+    if (n <= 1024) return fwd_ring<DT, 2>(a, dev, s);
+    if (n <= 2048) return fwd_ring<DT, 4>(a, dev, s);
   } else {
     if (a.D <= 256) return launch_pdl(ln_fwd_kernel<DT, 1, 8, true>, warps_grid, 256, 0, s, a);
     if (a.D <= 8192) return launch_pdl(ln_fwd_kernel<DT, 1, 8, false>, rows, threads(a.D, 8), 0, s, a);
   }
   return launch_pdl(ln_fwd_any<DT>, rows, 512, 0, s, a);
+}
+
+template <int DT, int NV, int MAXT>
+cudaError_t bwd_ring(const LnBwdArgs& a, unsigned grid, cudaStream_t s) {
+  const unsigned T = threads(a.D / Fmt<DT>::VEC, NV);
+  const int64_t bytes = 2 * a.D * static_cast<int64_t>(sizeof(typename Fmt<DT>::E));
+  // as many blocks as the grid puts on an SM of 152
+  const int blocks = static_cast<int>((grid + 151) / 152), stages = ring_stages(blocks, bytes);
+  const cudaError_t e =
+      cudaFuncSetAttribute(ln_bwd_ring<DT, NV, MAXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(ln_bwd_ring<DT, NV, MAXT>, grid, T, stages * bytes, s, a, stages);
 }
 
 template <int DT>
@@ -360,18 +649,20 @@ cudaError_t bwd_dt(const LnBwdArgs& a, cudaStream_t s) {
   const bool vec = a.xs1 == 1 && a.gs1 == 1 && a.dxs1 == 1 && a.D % V == 0 && al16(a.x) && al16(a.dout) &&
                    al16(a.dx) && (a.N == 1 || (a.xs0 % V == 0 && a.gs0 % V == 0 && a.dxs0 % V == 0));
   const unsigned grid = static_cast<unsigned>(ln_bwd_blocks(a.N, a.D));
-  auto threads = [](int64_t n, int nv) { return static_cast<unsigned>(((n + nv - 1) / nv + 31) / 32 * 32); };
   const size_t warp_sh = static_cast<size_t>(a.D) * 2 * 8 * sizeof(float);
   const size_t row_sh = 96 * sizeof(float);
+  const int64_t n = a.D / V;
   cudaError_t e;
-  if (vec && a.D <= 32 * V)
+  if (vec && n <= 32)
     e = launch_pdl(ln_bwd_kernel<DT, V, 1, true, 256>, grid, 256, warp_sh, s, a);
   else if (!vec && a.D <= 128)
     e = launch_pdl(ln_bwd_kernel<DT, 1, 4, true, 256>, grid, 256, warp_sh, s, a);
-  else if (vec && a.D <= 1024 * V)
-    e = launch_pdl(ln_bwd_kernel<DT, V, 2, false, 512>, grid, threads(a.D / V, 2), row_sh, s, a);
-  else if (vec && a.D <= 2048 * V)
-    e = launch_pdl(ln_bwd_kernel<DT, V, 2, false, 1024>, grid, threads(a.D / V, 2), row_sh, s, a);
+  else if (vec && n <= 512)
+    e = bwd_ring<DT, 1, 512>(a, grid, s);
+  else if (vec && n <= 1024)
+    e = bwd_ring<DT, 2, 512>(a, grid, s);
+  else if (vec && n <= 2048)
+    e = bwd_ring<DT, 4, 512>(a, grid, s);
   else if (!vec && a.D <= 4096)
     e = launch_pdl(ln_bwd_kernel<DT, 1, 4, false, 1024>, grid, threads(a.D, 4), row_sh, s, a);
   else
@@ -382,20 +673,30 @@ cudaError_t bwd_dt(const LnBwdArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_ln_fwd(const LnArgs& a, Dtype dt, cudaStream_t stream) {
+cudaError_t launch_ln_fwd(const LnArgs& a, Dtype dt, const Device& dev, cudaStream_t stream) {
   switch (dt) {
-    case kF32: return fwd_dt<kF32>(a, stream);
-    case kF16: return fwd_dt<kF16>(a, stream);
-    case kBF16: return fwd_dt<kBF16>(a, stream);
+    case kF32: return fwd_dt<kF32>(a, dev, stream);
+    case kF16: return fwd_dt<kF16>(a, dev, stream);
+    case kBF16: return fwd_dt<kBF16>(a, dev, stream);
   }
   return cudaErrorInvalidValue;
 }
 
-// Two blocks for each of 304 (two per SM of a 152-SM device); a block of the
-// warp-per-row kernels takes at least eight rows.
+// Multiples of 152 (the SMs of the device this is written for), so that the
+// workspace's size depends on nothing but N and D: one wave of the ring
+// kernels, whose blocks have a thread for every vector.
 int64_t ln_bwd_blocks(int64_t N, int64_t D) {
   const int64_t rows = D <= 256 ? (N + 7) / 8 : N;
-  return rows < 608 ? rows : 608;
+  const int64_t most = 152 * (D <= 1024 ? 6 : D <= 2048 ? 4 : D <= 4096 ? 2 : 1);
+  return rows < most ? rows : most;
+}
+
+unsigned read_and_clear_fault_ln() {
+  unsigned v = 0;
+  const unsigned zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_fault, sizeof(v)) != cudaSuccess) return ~0u;
+  if (v != 0 && cudaMemcpyToSymbol(g_fault, &zero, sizeof(zero)) != cudaSuccess) return ~0u;
+  return v;
 }
 
 cudaError_t launch_ln_bwd(const LnBwdArgs& a, Dtype dt, cudaStream_t stream) {

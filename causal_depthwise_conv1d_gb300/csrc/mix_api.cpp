@@ -416,6 +416,11 @@ ccv_status ccv_gdr_bwd(const void* q, const int64_t q_strides[4], const void* k,
 
 namespace {
 
+// Parameters that vector loads of four elements may read (or none).
+bool dense_par(const void* p, int64_t stride, int64_t esz) {
+  return p == nullptr || (stride == 1 && reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(4 * esz) == 0);
+}
+
 ccv_status check_ln(int64_t N, int64_t D, float eps, ccv_dtype dtype, ccv_dtype wdtype) {
   if (N < 0 || D < 0) CCV_FAIL(CCV_ERR_INVALID_ARG, "N and D must be >= 0");
   if (!valid_dtype(dtype)) CCV_FAIL(CCV_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dtype));
@@ -448,8 +453,12 @@ ccv_status ccv_ln_fwd(const void* x, const int64_t x_strides[2], const void* wei
   CCV_TRY(t.add("out", out, out_strides, 2, nd, e, true, true));
   CCV_TRY(t.disjoint());
   ccv::LnArgs a = {x, x_strides[0], x_strides[1], weight, weight_stride, bias, bias_stride,
-                   out, out_strides[0], out_strides[1], N, D, eps, static_cast<int>(weight_dtype)};
-  return launched(ccv::launch_ln_fwd(a, static_cast<ccv::Dtype>(dtype), static_cast<cudaStream_t>(stream)), "ln_fwd");
+                   out, out_strides[0], out_strides[1], N, D, eps, static_cast<int>(weight_dtype),
+                   dense_par(weight, weight_stride, we) && dense_par(bias, bias_stride, we)};
+  ccv::Device dev;
+  CCV_TRY(static_cast<ccv_status>(ccv::api_device(&dev)));
+  return launched(ccv::launch_ln_fwd(a, static_cast<ccv::Dtype>(dtype), dev, static_cast<cudaStream_t>(stream)),
+                  "ln_fwd");
 }
 
 ccv_status ccv_ln_bwd_workspace_size(int64_t N, int64_t D, uint64_t* bytes) {
@@ -494,6 +503,7 @@ ccv_status ccv_ln_bwd(const void* x, const int64_t x_strides[2], const void* wei
     a.dxs0 = dx_strides[0], a.dxs1 = dx_strides[1];
   }
   a.N = N, a.D = D, a.eps = eps, a.wdt = static_cast<int>(weight_dtype);
+  a.wvec = dense_par(weight, weight_stride, we);
   return launched(ccv::launch_ln_bwd(a, static_cast<ccv::Dtype>(dtype), static_cast<cudaStream_t>(stream)), "ln_bwd");
 }
 

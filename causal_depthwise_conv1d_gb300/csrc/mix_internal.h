@@ -104,6 +104,7 @@ struct LnArgs {
   int64_t N, D;
   float eps;
   int wdt;
+  bool wvec;  // weight and bias are dense and aligned to four elements
 };
 
 struct LnBwdArgs {
@@ -123,9 +124,11 @@ struct LnBwdArgs {
   int64_t N, D;
   float eps;
   int wdt;
+  bool wvec;  // weight and bias are dense and aligned to four elements
 };
 
-cudaError_t launch_ln_fwd(const LnArgs& a, Dtype dt, cudaStream_t stream);
+cudaError_t launch_ln_fwd(const LnArgs& a, Dtype dt, const Device& dev, cudaStream_t stream);
+unsigned read_and_clear_fault_ln();
 // Blocks (= partial sums) of the backward pass: a function of N and D alone.
 int64_t ln_bwd_blocks(int64_t N, int64_t D);
 cudaError_t launch_ln_bwd(const LnBwdArgs& a, Dtype dt, cudaStream_t stream);

@@ -51,27 +51,54 @@ def _call(name: str, *args) -> None:
         raise CcvError(rc, load_library().ccv_last_error().decode())
 
 
+_strides = {}  # the C arrays of stride tuples seen: a decode step's are the same every time
+
+
+def _st(strides):
+    a = _strides.get(strides)
+    if a is None:
+        if len(_strides) > 4096:
+            _strides.clear()
+        a = _strides[strides] = _arr(strides)
+    return a
+
+
 def _t(x: Optional[torch.Tensor]):
     """(pointer, strides) of a tensor or of a missing one."""
-    return (None, None) if x is None else (x.data_ptr() or None, _arr(x.stride()))
+    return (None, None) if x is None else (x.data_ptr() or None, _st(x.stride()))
 
 
 def _v(x: Optional[torch.Tensor]):
     """(pointer, stride) of a vector."""
-    return (None, 0) if x is None else (x.data_ptr() or None, int(x.stride(0)))
+    return (None, 0) if x is None else (x.data_ptr() or None, x.stride(0))
 
 
-def _check(ref: torch.Tensor, **tensors) -> None:
-    """name=(tensor, shape, dtype): None, or that shape and dtype on ref's device."""
-    for name, (t, shape, dtype) in tensors.items():
+def _ws(x: Optional[torch.Tensor]):
+    """(pointer, bytes) of a workspace."""
+    return (None, 0) if x is None else (x.data_ptr(), x.numel() * x.element_size())
+
+
+def _check(dev: int, tensors) -> None:
+    """(name, tensor, shape, dtype) each: None, or that shape and dtype on the device."""
+    for name, t, shape, dtype in tensors:
         if t is None:
             continue
-        if not t.is_cuda or t.device != ref.device:
+        if t.get_device() != dev or dev < 0:
             raise ValueError("all tensors must live on one CUDA device")
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         if t.dtype != dtype:
             raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+
+
+def _launch(dev: int, stream: Optional[torch.cuda.Stream], name: str, *args) -> None:
+    """The call on `stream` (default: the device's current one), with the device current."""
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        _call(name, *args, raw)
+    else:
+        with torch.cuda.device(dev):
+            _call(name, *args, raw)
 
 
 def _gdr_sizes(q, k, v):
@@ -83,7 +110,7 @@ def _gdr_sizes(q, k, v):
     return B, L, Hk, v.shape[2], Dk, v.shape[3]
 
 
-def _workspace(name: str, need: int, workspace: Optional[torch.Tensor], device) -> Optional[torch.Tensor]:
+def _workspace(need: int, workspace: Optional[torch.Tensor], device) -> Optional[torch.Tensor]:
     if workspace is None:
         return torch.empty((need,), dtype=torch.uint8, device=device) if need > 0 else None
     if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
@@ -118,19 +145,15 @@ def ccv_gdr_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
         out = torch.empty((B, L, Hv, Dv), dtype=dt, device=v.device)
     if return_final_state and final_state_out is None:
         final_state_out = torch.empty(st, dtype=torch.float32, device=v.device)
-    _check(v, q=(q, (B, L, Hk, Dk), dt), k=(k, (B, L, Hk, Dk), dt), v=(v, (B, L, Hv, Dv), dt),
-           g=(g, (B, L, Hv), torch.float32), beta=(beta, (B, L, Hv), dt), seq_idx=(seq_idx, (B, L), torch.int32),
-           initial_state=(initial_state, st, torch.float32), out=(out, (B, L, Hv, Dv), dt),
-           final_state_out=(final_state_out, st, torch.float32))
+    dev, qk, vo, gate, f32 = v.get_device(), (B, L, Hk, Dk), (B, L, Hv, Dv), (B, L, Hv), torch.float32
+    _check(dev, (("q", q, qk, dt), ("k", k, qk, dt), ("v", v, vo, dt), ("g", g, gate, f32), ("beta", beta, gate, dt),
+                 ("seq_idx", seq_idx, (B, L), torch.int32), ("initial_state", initial_state, st, f32),
+                 ("out", out, vo, dt), ("final_state_out", final_state_out, st, f32)))
     need = ccv_gdr_fwd_workspace_size(B, L, Hk, Hv, Dk, Dv, TORCH_DTYPE[dt])
-    if stream is None:
-        stream = torch.cuda.current_stream(v.device)
-    with torch.cuda.device(v.device):
-        ws = _workspace("workspace", need, workspace, v.device)
-        _call("ccv_gdr_fwd", *_t(q), *_t(k), *_t(v), *_t(g), *_t(beta), *_t(seq_idx), *_t(initial_state), *_t(out),
-              *_t(final_state_out), None if ws is None else ws.data_ptr(),
-              0 if ws is None else ws.numel() * ws.element_size(), B, L, Hk, Hv, Dk, Dv,
-              float(Dk ** -0.5 if scale is None else scale), TORCH_DTYPE[dt], stream.cuda_stream)
+    ws = _workspace(need, workspace, v.device)
+    _launch(dev, stream, "ccv_gdr_fwd", *_t(q), *_t(k), *_t(v), *_t(g), *_t(beta), *_t(seq_idx), *_t(initial_state),
+            *_t(out), *_t(final_state_out), *_ws(ws), B, L, Hk, Hv, Dk, Dv, max(Dk, 1) ** -0.5 if scale is None else scale,
+            TORCH_DTYPE[dt])
     return (out, final_state_out) if final_state_out is not None else out
 
 
@@ -157,16 +180,14 @@ def ccv_gdr_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Ten
         res = out.squeeze(1) if one else out
     else:
         res, out = out, (out.unsqueeze(1) if one else out)
-    _check(v, q=(q, (B, S, Hk, Dk), dt), k=(k, (B, S, Hk, Dk), dt), v=(v, (B, S, Hv, Dv), dt),
-           g=(g, (B, S, Hv), torch.float32), beta=(beta, (B, S, Hv), dt),
-           state=(state, (state.shape[0], Hv, Dk, Dv), torch.float32),
-           state_indices=(state_indices, (B,), torch.int32), out=(out, (B, S, Hv, Dv), dt))
-    if stream is None:
-        stream = torch.cuda.current_stream(v.device)
-    with torch.cuda.device(v.device):
-        _call("ccv_gdr_step", *_t(q), *_t(k), *_t(v), *_t(g), *_t(beta), *_t(state), int(state.shape[0]),
-              *_v(state_indices), *_t(out), B, S, Hk, Hv, Dk, Dv, float(Dk ** -0.5 if scale is None else scale),
-              TORCH_DTYPE[dt], stream.cuda_stream)
+    dev, qk, vo, gate, f32 = v.get_device(), (B, S, Hk, Dk), (B, S, Hv, Dv), (B, S, Hv), torch.float32
+    slots = state.shape[0]
+    _check(dev, (("q", q, qk, dt), ("k", k, qk, dt), ("v", v, vo, dt), ("g", g, gate, f32), ("beta", beta, gate, dt),
+                 ("state", state, (slots, Hv, Dk, Dv), f32), ("state_indices", state_indices, (B,), torch.int32),
+                 ("out", out, vo, dt)))
+    _launch(dev, stream, "ccv_gdr_step", *_t(q), *_t(k), *_t(v), *_t(g), *_t(beta), *_t(state), slots,
+            *_v(state_indices), *_t(out), B, S, Hk, Hv, Dk, Dv, max(Dk, 1) ** -0.5 if scale is None else scale,
+            TORCH_DTYPE[dt])
     return res
 
 
@@ -204,19 +225,17 @@ def ccv_gdr_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
     if dinitial_state is None and return_dinitial_state and initial_state is not None:
         dinitial_state = torch.empty(st, dtype=torch.float32, device=dev)
     f32 = torch.float32
-    _check(v, q=(q, qk, dt), k=(k, qk, dt), v=(v, vo, dt), g=(g, gate, f32), beta=(beta, gate, dt),
-           seq_idx=(seq_idx, (B, L), torch.int32), initial_state=(initial_state, st, f32), dout=(dout, vo, dt),
-           dfinal_state=(dfinal_state, st, f32), dq=(dq, qk, dt), dk=(dk, qk, dt), dv=(dv, vo, dt),
-           dg=(dg, gate, f32), dbeta=(dbeta, gate, dt), dinitial_state=(dinitial_state, st, f32))
+    _check(v.get_device(), (
+        ("q", q, qk, dt), ("k", k, qk, dt), ("v", v, vo, dt), ("g", g, gate, f32), ("beta", beta, gate, dt),
+        ("seq_idx", seq_idx, (B, L), torch.int32), ("initial_state", initial_state, st, f32), ("dout", dout, vo, dt),
+        ("dfinal_state", dfinal_state, st, f32), ("dq", dq, qk, dt), ("dk", dk, qk, dt), ("dv", dv, vo, dt),
+        ("dg", dg, gate, f32), ("dbeta", dbeta, gate, dt), ("dinitial_state", dinitial_state, st, f32)))
     need = ccv_gdr_bwd_workspace_size(B, L, Hk, Hv, Dk, Dv, TORCH_DTYPE[dt])
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    with torch.cuda.device(dev):
-        ws = _workspace("workspace", need, workspace, dev)
-        _call("ccv_gdr_bwd", *_t(q), *_t(k), *_t(v), *_t(g), *_t(beta), *_t(seq_idx), *_t(initial_state), *_t(dout),
-              *_t(dfinal_state), *_t(dq), *_t(dk), *_t(dv), *_t(dg), *_t(dbeta), *_t(dinitial_state),
-              None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(), B, L, Hk,
-              Hv, Dk, Dv, float(Dk ** -0.5 if scale is None else scale), TORCH_DTYPE[dt], stream.cuda_stream)
+    ws = _workspace(need, workspace, dev)
+    _launch(v.get_device(), stream, "ccv_gdr_bwd", *_t(q), *_t(k), *_t(v), *_t(g), *_t(beta), *_t(seq_idx),
+            *_t(initial_state), *_t(dout), *_t(dfinal_state), *_t(dq), *_t(dk), *_t(dv), *_t(dg), *_t(dbeta),
+            *_t(dinitial_state), *_ws(ws), B, L, Hk, Hv, Dk, Dv, max(Dk, 1) ** -0.5 if scale is None else scale,
+            TORCH_DTYPE[dt])
     return dq, dk, dv, dg, dbeta, dinitial_state
 
 
@@ -241,7 +260,7 @@ def _ln_check(x, weight, bias):
     wdt = par.dtype if par is not None else x.dtype
     if wdt not in TORCH_DTYPE:
         raise ValueError(f"unsupported weight dtype {wdt}")
-    _check(x, x=(x, x.shape, x.dtype), weight=(weight, (D,), wdt), bias=(bias, (D,), wdt))
+    _check(x.get_device(), (("x", x, x.shape, x.dtype), ("weight", weight, (D,), wdt), ("bias", bias, (D,), wdt)))
     return D, wdt
 
 
@@ -253,16 +272,14 @@ def ccv_ln_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     D, wdt = _ln_check(x, weight, bias)
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _check(x, out=(out, x.shape, x.dtype))
+    else:
+        _check(x.get_device(), (("out", out, x.shape, x.dtype),))
     x2, o2 = (x, out) if x.numel() == 0 else (_rows(x), _rows(out))
     N = x.numel() // D if D else 0
     if N == 0:
         return out
-    if stream is None:
-        stream = torch.cuda.current_stream(x.device)
-    with torch.cuda.device(x.device):
-        _call("ccv_ln_fwd", *_t(x2), *_v(weight), *_v(bias), *_t(o2), N, D, float(eps), TORCH_DTYPE[x.dtype],
-              TORCH_DTYPE[wdt], stream.cuda_stream)
+    _launch(x.get_device(), stream, "ccv_ln_fwd", *_t(x2), *_v(weight), *_v(bias), *_t(o2), N, D, eps,
+            TORCH_DTYPE[x.dtype], TORCH_DTYPE[wdt])
     return out
 
 
@@ -290,18 +307,15 @@ def ccv_ln_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], dout: torch.Tens
         dweight = torch.empty((D,), dtype=wdt, device=x.device)
     if dbias is None and bias is not None:
         dbias = torch.empty((D,), dtype=wdt, device=x.device)
-    _check(x, dout=(dout, x.shape, x.dtype), dx=(dx, x.shape, x.dtype), dweight=(dweight, (D,), wdt),
-           dbias=(dbias, (D,), wdt))
+    dev = x.get_device()
+    _check(dev, (("dout", dout, x.shape, x.dtype), ("dx", dx, x.shape, x.dtype), ("dweight", dweight, (D,), wdt),
+                 ("dbias", dbias, (D,), wdt)))
     N = x.numel() // D if D else 0
     x2, g2, d2 = (_rows(x), _rows(dout), _rows(dx)) if N else (x.new_empty((0, D)),) * 3
-    if stream is None:
-        stream = torch.cuda.current_stream(x.device)
-    with torch.cuda.device(x.device):
-        need = ccv_ln_bwd_workspace_size(N, D) if dweight is not None or dbias is not None else 0
-        ws = _workspace("workspace", need, workspace, x.device)
-        _call("ccv_ln_bwd", *_t(x2), *_v(weight), *_t(g2), *_t(d2), *_v(dweight), *_v(dbias),
-              None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(), N, D,
-              float(eps), TORCH_DTYPE[x.dtype], TORCH_DTYPE[wdt], stream.cuda_stream)
+    need = ccv_ln_bwd_workspace_size(N, D) if dweight is not None or dbias is not None else 0
+    ws = _workspace(need, workspace, x.device)
+    _launch(dev, stream, "ccv_ln_bwd", *_t(x2), *_v(weight), *_t(g2), *_t(d2), *_v(dweight), *_v(dbias), *_ws(ws), N,
+            D, eps, TORCH_DTYPE[x.dtype], TORCH_DTYPE[wdt])
     return dx, dweight, dbias
 
 

@@ -175,7 +175,8 @@ def test_ln_backward_refusals(mx, kw, st, needle):
 def test_ln_workspace(mx):
     assert mx.ccv_ln_bwd_workspace_size(0, 64) == 0
     assert mx.ccv_ln_bwd_workspace_size(1, 4096) == 2 * 4096 * 4
-    assert mx.ccv_ln_bwd_workspace_size(10 ** 6, 4096) == 608 * 2 * 4096 * 4
+    # one partial sum per block, and no more blocks than rows or than fill the device
+    assert 0 < mx.ccv_ln_bwd_workspace_size(10 ** 6, 4096) <= 1024 * 2 * 4096 * 4
     with pytest.raises(Exception, match="bytes is required"):
         rc = mx._fn("ccv_ln_bwd_workspace_size")(4, 4, ctypes.POINTER(ctypes.c_uint64)())
         assert rc == 1
