@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int i = e < 2 ? i0 : i1;
           const bool in = j <= i && seg[j] == (e < 2 ? s0 : s1);
           const float ju = fs[kFU + j];
-          const float gam = in ? expf(((e < 2 ? gh0 : gh1) - slot[kVGHi * kC + j]) +
+          const float gam = in ? ex2_approx(((e < 2 ? gh0 : gh1) - slot[kVGHi * kC + j]) +
                                       ((e < 2 ? gl0 : gl1) - slot[kVGLo * kC + j]))
                                : 0.f;
           dp[n][e] = in ? dp[n][e] * ((e < 2 ? po0 : po1) * ju) * gam : 0.f;

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
   const int64_t hk = h / (a.Hv / a.Hk);
   const int64_t v0 = (static_cast<int64_t>(blockIdx.x % vtiles) * NW + warp) * 16;
   const uint8_t* qk = w.qk + (b * a.Hk + hk) * nc * qk_pack_bytes(DK, C::TERMS);
-  const uint8_t* pk = w.pack + bh * nc * kPackBytes;
+  const uint8_t* pkg = w.pack + bh * nc * kPackBytes;
   // step n takes chunk nc - 1 - n
   auto fill = [&](int n) {
     const int c = nc - 1 - n;
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
     uint64_t* bar = &full[n % NS];
     mbar_arrive_expect_tx(bar, C::STAGE);
     bulk_load(dst, qk + static_cast<int64_t>(c) * C::QKB, C::QKB, bar);
-    bulk_load(dst + C::QKB, pk + static_cast<int64_t>(c) * kPackBytes, kPackBytes, bar);
+    bulk_load(dst + C::QKB, pkg + static_cast<int64_t>(c) * kPackBytes, kPackBytes, bar);
   };
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -215,23 +215,23 @@ __global__ void __launch_bounds__(32 * NW, 1)
       const uint32_t th = kt_hi + C::QKB + kVecBytes, tl = th + kMatBytes, ph = tl + kMatBytes, pl = ph + kMatBytes;
       const float ga = vecs[kHdGa];
 
-      unsigned m0 = 0, m1 = 0;
+      float a0 = 0.f, a1 = 0.f;
       float* dst = w.d + (bh * nc + c) * DK * dvp;
 #pragma unroll
       for (int n = 0; n < NK; ++n) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) dst[(8 * n + 2 * qd + (j & 1)) * dvp + v0 + g + (j >> 1) * 8] = d[n][j];
-        m0 = max(m0, max(mag(d[n][0]), mag(d[n][1])));
-        m1 = max(m1, max(mag(d[n][2]), mag(d[n][3])));
+        a0 = amax3(a0, d[n][0], d[n][1]);
+        a1 = amax3(a1, d[n][2], d[n][3]);
       }
-      m0 = quad_max(m0);
-      m1 = quad_max(m1);
+      const unsigned m0 = quad_max(__float_as_uint(a0)), m1 = quad_max(__float_as_uint(a1));
       bool bad = vecs[kHdBad] != 0.f || m0 >= kInfBits || m1 >= kInfBits;
       const unsigned mx = warp_max(max(m0, m1));
       if (lane == 0) atomicMax(w.d_max + bh * nc + c, mx);
       float f0, f1, di0, di1;
       row_factor(m0, f0, di0);
       row_factor(m1, f1, di1);
+      const uint64_t p0 = pk(f0, f0), p1 = pk(f1, f1);
 
       // (K D)^T
       float u[8][4];
@@ -242,10 +242,10 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
       for (int kt = 0; kt < DK / 16; ++kt) {
         uint32_t hi[4], lo[4];
-        split2(d[2 * kt][0] * f0, d[2 * kt][1] * f0, hi[0], lo[0]);
-        split2(d[2 * kt][2] * f1, d[2 * kt][3] * f1, hi[1], lo[1]);
-        split2(d[2 * kt + 1][0] * f0, d[2 * kt + 1][1] * f0, hi[2], lo[2]);
-        split2(d[2 * kt + 1][2] * f1, d[2 * kt + 1][3] * f1, hi[3], lo[3]);
+        split2f(d[2 * kt][0], d[2 * kt][1], p0, hi[0], lo[0]);
+        split2f(d[2 * kt][2], d[2 * kt][3], p1, hi[1], lo[1]);
+        split2f(d[2 * kt + 1][0], d[2 * kt + 1][1], p0, hi[2], lo[2]);
+        split2f(d[2 * kt + 1][2], d[2 * kt + 1][3], p1, hi[3], lo[3]);
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
           uint32_t bk[4];

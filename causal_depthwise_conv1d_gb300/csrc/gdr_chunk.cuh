@@ -45,7 +45,7 @@ enum VecSlot {
   kVKInv = 8,   // 1 / k's row factor
   kVQInv = 9,
   kVPInv = 10,
-  kVGHi = 11,   // G as a sum of two floats
+  kVGHi = 11,   // G in units of log 2, as a sum of two floats
   kVGLo = 12,
   kVSeg = 13,   // number of sequence starts in the chunk up to the token (as an integer)
   kVSlots = 14
@@ -135,6 +135,25 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   lo = h2(x - f.x, y - f.y);
 }
 
+// The same of (x, y) times f, packed arithmetic.
+__device__ __forceinline__ void split2f(float x, float y, uint64_t f, uint32_t& hi, uint32_t& lo) {
+  const uint64_t v = fmul2(pk(x, y), f);
+  float a, b;
+  upk(v, a, b);
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 e = __half22float2(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  upk(ffma2(pk(e.x, e.y), pk(-1.f, -1.f), v), a, b);
+  lo = h2(a, b);
+}
+
+// max(m, |x|, |y|), NaN where one of them is.
+__device__ __forceinline__ float amax3(float m, float x, float y) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(x), "f"(y));
+  return d;
+}
+
 __device__ __forceinline__ unsigned mag(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 constexpr unsigned kInfBits = 0x7f800000u;  // magnitudes from here on are not finite
@@ -162,25 +181,25 @@ __device__ __forceinline__ unsigned warp_max(unsigned m) {
 template <int NT, bool LO>
 __device__ __forceinline__ void split_rows(const float (&x)[NT][4], uint32_t (&hi)[NT / 2][4],
                                            uint32_t (&lo)[NT / 2][4], float& inv0, float& inv1, bool& bad) {
-  unsigned m0 = 0, m1 = 0;
+  float a0 = 0.f, a1 = 0.f;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    m0 = max(m0, max(mag(x[i][0]), mag(x[i][1])));
-    m1 = max(m1, max(mag(x[i][2]), mag(x[i][3])));
+    a0 = amax3(a0, x[i][0], x[i][1]);
+    a1 = amax3(a1, x[i][2], x[i][3]);
   }
-  m0 = quad_max(m0);
-  m1 = quad_max(m1);
+  const unsigned m0 = quad_max(__float_as_uint(a0)), m1 = quad_max(__float_as_uint(a1));
   bad = bad || m0 >= kInfBits || m1 >= kInfBits;
   float f0, f1;
   row_factor(m0, f0, inv0);
   row_factor(m1, f1, inv1);
+  const uint64_t p0 = pk(f0, f0), p1 = pk(f1, f1);
 #pragma unroll
   for (int i = 0; i < NT / 2; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if constexpr (LO) {
-        split2(x[2 * i + j][0] * f0, x[2 * i + j][1] * f0, hi[i][2 * j], lo[i][2 * j]);
-        split2(x[2 * i + j][2] * f1, x[2 * i + j][3] * f1, hi[i][2 * j + 1], lo[i][2 * j + 1]);
+        split2f(x[2 * i + j][0], x[2 * i + j][1], p0, hi[i][2 * j], lo[i][2 * j]);
+        split2f(x[2 * i + j][2], x[2 * i + j][3], p1, hi[i][2 * j + 1], lo[i][2 * j + 1]);
       } else {
         hi[i][2 * j] = h2(x[2 * i + j][0] * f0, x[2 * i + j][1] * f0);
         hi[i][2 * j + 1] = h2(x[2 * i + j][2] * f1, x[2 * i + j][3] * f1);

@@ -176,12 +176,12 @@ __global__ void __launch_bounds__(32 * NW, 1)
   const int64_t v0 = (static_cast<int64_t>(blockIdx.x % vtiles) * NW + warp) * 16;
 
   const uint8_t* qk = qk_ws + (b * a.Hk + hk) * nc * qk_pack_bytes(DK, C::TERMS);
-  const uint8_t* pk = pack_ws + bh * nc * kPackBytes;
+  const uint8_t* pkg = pack_ws + bh * nc * kPackBytes;
   auto fill = [&](int c) {
     uint8_t* dst = sm + (c & 1) * C::STAGE;
     uint64_t* bar = &full[c & 1];
     constexpr uint32_t kVec = SAVE ? kVecBytes : kVecFwdBytes;
-    const uint8_t* pc = pk + static_cast<int64_t>(c) * kPackBytes;
+    const uint8_t* pc = pkg + static_cast<int64_t>(c) * kPackBytes;
     mbar_arrive_expect_tx(bar, C::QKB + kVec + C::MATS * kMatBytes);
     bulk_load(dst, qk + static_cast<int64_t>(c) * qk_pack_bytes(DK, C::TERMS), C::QKB, bar);
     bulk_load(dst + C::QKB, pc, kVec, bar);
@@ -246,18 +246,18 @@ __global__ void __launch_bounds__(32 * NW, 1)
       bool bad = vecs[kHdBad] != 0.f;
 
       // the state's row factors
-      unsigned m0 = 0, m1 = 0;
+      float a0 = 0.f, a1 = 0.f;
 #pragma unroll
       for (int n = 0; n < NK; ++n) {
-        m0 = max(m0, max(mag(st[n][0]), mag(st[n][1])));
-        m1 = max(m1, max(mag(st[n][2]), mag(st[n][3])));
+        a0 = amax3(a0, st[n][0], st[n][1]);
+        a1 = amax3(a1, st[n][2], st[n][3]);
       }
-      m0 = quad_max(m0);
-      m1 = quad_max(m1);
+      const unsigned m0 = quad_max(__float_as_uint(a0)), m1 = quad_max(__float_as_uint(a1));
       bad = bad || m0 >= kInfBits || m1 >= kInfBits;
       float f0, f1, si0, si1;
       row_factor(m0, f0, si0);
       row_factor(m1, f1, si1);
+      const uint64_t p0 = pk(f0, f0), p1 = pk(f1, f1);
       if constexpr (SAVE) {  // the chunk's largest state element: one factor for the whole matrix later
         const unsigned mx = warp_max(max(m0, m1));
         if (lane == 0) atomicMax(s_max + bh * nc + c, mx);
@@ -272,10 +272,10 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
       for (int kt = 0; kt < DK / 16; ++kt) {
         uint32_t hi[4], lo[4];
-        split2(st[2 * kt][0] * f0, st[2 * kt][1] * f0, hi[0], lo[0]);
-        split2(st[2 * kt][2] * f1, st[2 * kt][3] * f1, hi[1], lo[1]);
-        split2(st[2 * kt + 1][0] * f0, st[2 * kt + 1][1] * f0, hi[2], lo[2]);
-        split2(st[2 * kt + 1][2] * f1, st[2 * kt + 1][3] * f1, hi[3], lo[3]);
+        split2f(st[2 * kt][0], st[2 * kt][1], p0, hi[0], lo[0]);
+        split2f(st[2 * kt][2], st[2 * kt][3], p1, hi[1], lo[1]);
+        split2f(st[2 * kt + 1][0], st[2 * kt + 1][1], p0, hi[2], lo[2]);
+        split2f(st[2 * kt + 1][2], st[2 * kt + 1][3], p1, hi[3], lo[3]);
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
           uint32_t bk[4];

@@ -46,7 +46,7 @@ def _fn(name: str):
 
 
 def _call(name: str, *args) -> None:
-    rc = _fn(name)(*args)
+    rc = (_bound.get(name) or _fn(name))(*args)
     if rc != 0:
         raise CcvError(rc, load_library().ccv_last_error().decode())
 
@@ -81,7 +81,7 @@ def _ws(x: Optional[torch.Tensor]):
 def _check(dev: int, tensors) -> None:
     """(name, tensor, shape, dtype) each: None, or that shape and dtype on the device."""
     for name, t, shape, dtype in tensors:
-        if t is None:
+        if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0):
             continue
         if t.get_device() != dev or dev < 0:
             raise ValueError("all tensors must live on one CUDA device")
@@ -94,7 +94,7 @@ def _check(dev: int, tensors) -> None:
 def _launch(dev: int, stream: Optional[torch.cuda.Stream], name: str, *args) -> None:
     """The call on `stream` (default: the device's current one), with the device current."""
     raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         _call(name, *args, raw)
     else:
         with torch.cuda.device(dev):
@@ -107,7 +107,22 @@ def _gdr_sizes(q, k, v):
     if v.dtype not in TORCH_DTYPE:
         raise ValueError(f"unsupported dtype {v.dtype}")
     B, L, Hk, Dk = q.shape
-    return B, L, Hk, v.shape[2], Dk, v.shape[3]
+    _, _, Hv, Dv = v.shape
+    return B, L, Hk, Hv, Dk, Dv
+
+
+_sizes = {}  # workspace sizes by the sizes they follow from
+
+
+def _need(name: str, *key: int) -> int:
+    n = _sizes.get((name, key))
+    if n is None:
+        c = _u64(0)
+        _call(name, *key, ctypes.byref(c))
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        n = _sizes[name, key] = int(c.value)
+    return n
 
 
 def _workspace(need: int, workspace: Optional[torch.Tensor], device) -> Optional[torch.Tensor]:
@@ -120,10 +135,7 @@ def _workspace(need: int, workspace: Optional[torch.Tensor], device) -> Optional
 
 def ccv_gdr_fwd_workspace_size(B: int, L: int, Hk: int, Hv: int, Dk: int, Dv: int, dtype: int) -> int:
     """Bytes of workspace ``ccv_gdr_fwd`` needs for these sizes."""
-    n = _u64(0)
-    _call("ccv_gdr_fwd_workspace_size", int(B), int(L), int(Hk), int(Hv), int(Dk), int(Dv), int(dtype),
-          ctypes.byref(n))
-    return int(n.value)
+    return _need("ccv_gdr_fwd_workspace_size", B, L, Hk, Hv, Dk, Dv, dtype)
 
 
 def ccv_gdr_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
@@ -170,7 +182,7 @@ def ccv_gdr_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Ten
     """
     one = v.dim() == 3
     if one:
-        q, k, v, g, beta = (x.unsqueeze(1) for x in (q, k, v, g, beta))
+        q, k, v, g, beta = q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), g.unsqueeze(1), beta.unsqueeze(1)
     B, S, Hk, Hv, Dk, Dv = _gdr_sizes(q, k, v)
     dt = v.dtype
     if state.dim() != 4:
@@ -193,10 +205,7 @@ def ccv_gdr_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Ten
 
 def ccv_gdr_bwd_workspace_size(B: int, L: int, Hk: int, Hv: int, Dk: int, Dv: int, dtype: int) -> int:
     """Bytes of workspace ``ccv_gdr_bwd`` needs for these sizes."""
-    n = _u64(0)
-    _call("ccv_gdr_bwd_workspace_size", int(B), int(L), int(Hk), int(Hv), int(Dk), int(Dv), int(dtype),
-          ctypes.byref(n))
-    return int(n.value)
+    return _need("ccv_gdr_bwd_workspace_size", B, L, Hk, Hv, Dk, Dv, dtype)
 
 
 def ccv_gdr_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
@@ -285,9 +294,7 @@ def ccv_ln_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
 
 def ccv_ln_bwd_workspace_size(N: int, D: int) -> int:
     """Bytes of workspace ``ccv_ln_bwd`` needs."""
-    n = _u64(0)
-    _call("ccv_ln_bwd_workspace_size", int(N), int(D), ctypes.byref(n))
-    return int(n.value)
+    return _need("ccv_ln_bwd_workspace_size", N, D)
 
 
 def ccv_ln_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], dout: torch.Tensor,
