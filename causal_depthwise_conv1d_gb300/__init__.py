@@ -21,7 +21,8 @@ _MIXER_NAMES = ("ccv_gdr_fwd", "ccv_gdr_fwd_workspace_size", "ccv_gdr_step", "cc
 def __getattr__(name):
     if name in _MIXER_NAMES:
         from . import mixer
-        return getattr(mixer, name)
+        globals()[name] = getattr(mixer, name)  # found at once from now on
+        return globals()[name]
     if name in _BINDING_NAMES:
         from . import binding
         return getattr(binding, name)

@@ -19,6 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libccv.so")
+EXT_SRC = os.path.join(HERE, "ext", "mixer_ext.cpp")
+EXT = os.path.join(HERE, "_mixer_ext.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -42,11 +44,28 @@ def _deps():
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
+def _ext_command(out: str):
+    """g++ command of the tensor front end (mixer.py), which takes the C ABI from the loaded libccv.so."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    inc = cpp_extension.include_paths() + [INCLUDE, sysconfig.get_paths()["include"],
+                                           os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    lib = cpp_extension.library_paths()
+    return (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+            + [f"-isystem{p}" for p in inc] + [EXT_SRC, "-o", out] + [f"-L{p}" for p in lib] +
+            [f"-Wl,-rpath,{p}" for p in lib] + ["-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda",
+                                                "-Wl,-rpath,$ORIGIN"])
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
+    return all(os.path.getmtime(p) <= t for p in _deps() + [EXT_SRC])
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -70,6 +89,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    ext_tmp = EXT + f".tmp{os.getpid()}"
+    procs.append((EXT_SRC, subprocess.Popen(_ext_command(ext_tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     logs = []
     for src, p in procs:
@@ -80,13 +101,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if p.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError("nvcc failed for " + ", ".join(failed) + "\n" + "\n".join(logs))
+        raise RuntimeError("compilation failed for " + ", ".join(failed) + "\n" + "\n".join(logs))
     if verbose or ptxas_info:
         print("\n".join(logs), file=sys.stderr)
     tmp = LIB + f".tmp{os.getpid()}"
     link = [nvcc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs
     subprocess.run(link, check=True)
     os.replace(tmp, LIB)
+    os.replace(ext_tmp, EXT)
     return LIB
 
 

@@ -13,7 +13,7 @@
 // What bounds it: HBM (8 bytes a state element) for serving batches, latency
 // for a single request.  A block owns one head and a tile of columns; a thread
 // holds VEC adjacent columns of every RG-th row, so a warp's loads are whole
-// 128- or 512-byte row pieces, all in flight at once.
+// 128- or 256-byte row pieces, all in flight at once.
 #include "ccv_common.cuh"
 #include "mix_internal.h"
 
@@ -25,7 +25,7 @@ constexpr int kTok = 8;  // tokens staged at a time
 
 // MAXK: rows of the register tile (Dk <= MAXK); CL lanes of VEC columns.
 template <int DT, int MAXK, int CL, int VEC>
-__global__ void __launch_bounds__(kThreads, 2) gdr_step_kernel(const GdrArgs a, int tiles) {
+__global__ void __launch_bounds__(kThreads, MAXK * CL * VEC > 8192 ? 2 : 4) gdr_step_kernel(const GdrArgs a, int tiles) {
   using F = Fmt<DT>;
   using E = typename F::E;
   constexpr int RG = kThreads / CL;   // row groups
@@ -35,8 +35,8 @@ __global__ void __launch_bounds__(kThreads, 2) gdr_step_kernel(const GdrArgs a, 
   __shared__ float sk[kTok][MAXK], sq[kTok][MAXK];
   __shared__ float sv[kTok][COLS];
   __shared__ float sa[kTok], sb[kTok];
-  __shared__ __align__(16) float red[2][NW][COLS];
-  __shared__ float redqk[NW];
+  __shared__ __align__(16) float red[2][2][NW][COLS];  // of even and odd tokens: one barrier a token
+  __shared__ float redqk[2][NW];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cl = tid % CL, rg = tid / CL;
@@ -140,10 +140,10 @@ __global__ void __launch_bounds__(kThreads, 2) gdr_step_kernel(const GdrArgs a, 
       if (lane < CL) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          red[0][warp][cl * VEC + j] = p[j];
-          red[1][warp][cl * VEC + j] = r[j];
+          red[t & 1][0][warp][cl * VEC + j] = p[j];
+          red[t & 1][1][warp][cl * VEC + j] = r[j];
         }
-        if (lane == 0) redqk[warp] = qk;
+        if (lane == 0) redqk[t & 1][warp] = qk;
       }
       __syncthreads();
       qk = 0.f;
@@ -151,11 +151,11 @@ __global__ void __launch_bounds__(kThreads, 2) gdr_step_kernel(const GdrArgs a, 
       for (int j = 0; j < VEC; ++j) p[j] = r[j] = 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        qk += redqk[w];
+        qk += redqk[t & 1][w];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          p[j] += red[0][w][cl * VEC + j];
-          r[j] += red[1][w][cl * VEC + j];
+          p[j] += red[t & 1][0][w][cl * VEC + j];
+          r[j] += red[t & 1][1][w][cl * VEC + j];
         }
       }
       float u[VEC];
@@ -173,7 +173,6 @@ __global__ void __launch_bounds__(kThreads, 2) gdr_step_kernel(const GdrArgs a, 
 #pragma unroll
         for (int j = 0; j < VEC; ++j) s[i][j] = fmaf(kv, u[j], dec * s[i][j]);
       }
-      __syncthreads();
     }
   }
 
@@ -210,10 +209,10 @@ template <int DT, int MAXK>
 cudaError_t launch_k(const GdrArgs& a, const Device& dev, cudaStream_t s) {
   const bool vec = a.Dv % 4 == 0 && vec4_state(a.s0, a.s0s) && vec4_state(a.s1, a.s1s);
   if (!vec) return launch_tile<DT, MAXK, 32, 1>(a, s);
-  // Narrow tiles while whole rows would not give every SM two blocks: more
-  // blocks share one head's latency.  Whole 128-column rows once they do.
-  if (a.B * a.Hv * ((a.Dv + 127) / 128) < 2 * dev.sm_count) return launch_tile<DT, MAXK, 8, 4>(a, s);
-  return launch_tile<DT, MAXK, 32, 4>(a, s);
+  // Narrow tiles while half rows would not give every SM four blocks: more
+  // blocks share one head's latency.  Half rows of 64 columns once they do.
+  if (a.B * a.Hv * ((a.Dv + 63) / 64) < 4 * dev.sm_count) return launch_tile<DT, MAXK, 8, 4>(a, s);
+  return launch_tile<DT, MAXK, 16, 4>(a, s);
 }
 
 template <int DT>

@@ -2,7 +2,9 @@
 
 As in ``binding.py``: argument checks that need tensors, allocation of missing
 outputs and of the workspace, and the C call on the tensor's current stream.
-The compute is in the library's kernels alone.
+These are made by a small C++ extension (``ext/mixer_ext.cpp``): in Python they
+took 15-20 us a call, several times a decode step's kernel.  The compute is in
+the library's kernels alone.
 
     gated_delta_rule_fwd    whole sequences         (ccv_gdr_fwd)
     gated_delta_rule_bwd    its backward pass       (ccv_gdr_bwd)
@@ -13,11 +15,15 @@ The compute is in the library's kernels alone.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 from typing import Optional, Tuple, Union
 
 import torch
 
-from .binding import TORCH_DTYPE, CcvError, _arr, _i64p, load_library
+from .binding import CcvError, _arr, _i64p, load_library  # noqa: F401
+
+EXT_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_mixer_ext.so")
 
 _vp, _i64, _f32, _int, _u64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int, ctypes.c_uint64
 _T = [_vp, _i64p]  # a tensor: pointer, strides
@@ -51,86 +57,34 @@ def _call(name: str, *args) -> None:
         raise CcvError(rc, load_library().ccv_last_error().decode())
 
 
-_strides = {}  # the C arrays of stride tuples seen: a decode step's are the same every time
+_ext_module = None
 
 
-def _st(strides):
-    a = _strides.get(strides)
-    if a is None:
-        if len(_strides) > 4096:
-            _strides.clear()
-        a = _strides[strides] = _arr(strides)
-    return a
+def _ext():
+    """The tensor front end (ext/mixer_ext.cpp), loaded with the library it calls."""
+    global _ext_module
+    if _ext_module is None:
+        lib = load_library()
+        if not os.path.exists(EXT_PATH):
+            raise CcvError(-1, f"{EXT_PATH} is missing: build it with __graft_entry__.build() "
+                               "or python causal_depthwise_conv1d_gb300/build.py")
+        # the extension resolves the C ABI from the library that is already loaded
+        ctypes.CDLL(lib._name, mode=ctypes.RTLD_GLOBAL)
+        spec = importlib.util.spec_from_file_location("_mixer_ext", EXT_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _ext_module = module
+    return _ext_module
 
 
-def _t(x: Optional[torch.Tensor]):
-    """(pointer, strides) of a tensor or of a missing one."""
-    return (None, None) if x is None else (x.data_ptr() or None, _st(x.stride()))
-
-
-def _v(x: Optional[torch.Tensor]):
-    """(pointer, stride) of a vector."""
-    return (None, 0) if x is None else (x.data_ptr() or None, x.stride(0))
-
-
-def _ws(x: Optional[torch.Tensor]):
-    """(pointer, bytes) of a workspace."""
-    return (None, 0) if x is None else (x.data_ptr(), x.numel() * x.element_size())
-
-
-def _check(dev: int, tensors) -> None:
-    """(name, tensor, shape, dtype) each: None, or that shape and dtype on the device."""
-    for name, t, shape, dtype in tensors:
-        if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0):
-            continue
-        if t.get_device() != dev or dev < 0:
-            raise ValueError("all tensors must live on one CUDA device")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-
-
-def _launch(dev: int, stream: Optional[torch.cuda.Stream], name: str, *args) -> None:
-    """The call on `stream` (default: the device's current one), with the device current."""
-    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        _call(name, *args, raw)
-    else:
-        with torch.cuda.device(dev):
-            _call(name, *args, raw)
-
-
-def _gdr_sizes(q, k, v):
-    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
-        raise ValueError("q and k must be [B, L, Hk, Dk] and v [B, L, Hv, Dv]")
-    if v.dtype not in TORCH_DTYPE:
-        raise ValueError(f"unsupported dtype {v.dtype}")
-    B, L, Hk, Dk = q.shape
-    _, _, Hv, Dv = v.shape
-    return B, L, Hk, Hv, Dk, Dv
-
-
-_sizes = {}  # workspace sizes by the sizes they follow from
+def _raise(rc: int):
+    raise CcvError(rc, load_library().ccv_last_error().decode())
 
 
 def _need(name: str, *key: int) -> int:
-    n = _sizes.get((name, key))
-    if n is None:
-        c = _u64(0)
-        _call(name, *key, ctypes.byref(c))
-        if len(_sizes) > 4096:
-            _sizes.clear()
-        n = _sizes[name, key] = int(c.value)
-    return n
-
-
-def _workspace(need: int, workspace: Optional[torch.Tensor], device) -> Optional[torch.Tensor]:
-    if workspace is None:
-        return torch.empty((need,), dtype=torch.uint8, device=device) if need > 0 else None
-    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' CUDA device")
-    return workspace
+    n = _u64(0)
+    _call(name, *key, ctypes.byref(n))
+    return int(n.value)
 
 
 def ccv_gdr_fwd_workspace_size(B: int, L: int, Hk: int, Hv: int, Dk: int, Dv: int, dtype: int) -> int:
@@ -151,22 +105,12 @@ def ccv_gdr_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
     initial_state FP32 [B,Hv,Dk,Dv]; scale defaults to Dk ** -0.5.  Returns
     ``out`` [B,L,Hv,Dv] or ``(out, final_state)`` when it is requested.
     """
-    B, L, Hk, Hv, Dk, Dv = _gdr_sizes(q, k, v)
-    dt, st = v.dtype, (B, Hv, Dk, Dv)
-    if out is None:
-        out = torch.empty((B, L, Hv, Dv), dtype=dt, device=v.device)
-    if return_final_state and final_state_out is None:
-        final_state_out = torch.empty(st, dtype=torch.float32, device=v.device)
-    dev, qk, vo, gate, f32 = v.get_device(), (B, L, Hk, Dk), (B, L, Hv, Dv), (B, L, Hv), torch.float32
-    _check(dev, (("q", q, qk, dt), ("k", k, qk, dt), ("v", v, vo, dt), ("g", g, gate, f32), ("beta", beta, gate, dt),
-                 ("seq_idx", seq_idx, (B, L), torch.int32), ("initial_state", initial_state, st, f32),
-                 ("out", out, vo, dt), ("final_state_out", final_state_out, st, f32)))
-    need = ccv_gdr_fwd_workspace_size(B, L, Hk, Hv, Dk, Dv, TORCH_DTYPE[dt])
-    ws = _workspace(need, workspace, v.device)
-    _launch(dev, stream, "ccv_gdr_fwd", *_t(q), *_t(k), *_t(v), *_t(g), *_t(beta), *_t(seq_idx), *_t(initial_state),
-            *_t(out), *_t(final_state_out), *_ws(ws), B, L, Hk, Hv, Dk, Dv, max(Dk, 1) ** -0.5 if scale is None else scale,
-            TORCH_DTYPE[dt])
-    return (out, final_state_out) if final_state_out is not None else out
+    rc, out, final = (_ext_module or _ext()).gdr_fwd(q, k, v, g, beta, scale, seq_idx, initial_state,
+                                                     return_final_state, final_state_out, out, workspace,
+                                                     None if stream is None else stream.cuda_stream)
+    if rc:
+        _raise(rc)
+    return out if final is None else (out, final)
 
 
 def ccv_gdr_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
@@ -180,27 +124,11 @@ def ccv_gdr_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Ten
     request b uses slot b); negative or too large: a padding row, whose outputs
     are zero.  Returns out in v's shape.
     """
-    one = v.dim() == 3
-    if one:
-        q, k, v, g, beta = q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), g.unsqueeze(1), beta.unsqueeze(1)
-    B, S, Hk, Hv, Dk, Dv = _gdr_sizes(q, k, v)
-    dt = v.dtype
-    if state.dim() != 4:
-        raise ValueError("state must be [n_slots, Hv, Dk, Dv]")
-    if out is None:
-        out = torch.empty((B, S, Hv, Dv), dtype=dt, device=v.device)
-        res = out.squeeze(1) if one else out
-    else:
-        res, out = out, (out.unsqueeze(1) if one else out)
-    dev, qk, vo, gate, f32 = v.get_device(), (B, S, Hk, Dk), (B, S, Hv, Dv), (B, S, Hv), torch.float32
-    slots = state.shape[0]
-    _check(dev, (("q", q, qk, dt), ("k", k, qk, dt), ("v", v, vo, dt), ("g", g, gate, f32), ("beta", beta, gate, dt),
-                 ("state", state, (slots, Hv, Dk, Dv), f32), ("state_indices", state_indices, (B,), torch.int32),
-                 ("out", out, vo, dt)))
-    _launch(dev, stream, "ccv_gdr_step", *_t(q), *_t(k), *_t(v), *_t(g), *_t(beta), *_t(state), slots,
-            *_v(state_indices), *_t(out), B, S, Hk, Hv, Dk, Dv, max(Dk, 1) ** -0.5 if scale is None else scale,
-            TORCH_DTYPE[dt])
-    return res
+    rc, out = (_ext_module or _ext()).gdr_step(q, k, v, g, beta, state, scale, state_indices, out,
+                                               None if stream is None else stream.cuda_stream)
+    if rc:
+        _raise(rc)
+    return out
 
 
 def ccv_gdr_bwd_workspace_size(B: int, L: int, Hk: int, Hv: int, Dk: int, Dv: int, dtype: int) -> int:
@@ -223,54 +151,12 @@ def ccv_gdr_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
     dinitial_state is made when initial_state is given and
     ``return_dinitial_state`` is set (or the tensor is passed in).
     """
-    B, L, Hk, Hv, Dk, Dv = _gdr_sizes(q, k, v)
-    dt, st, dev = v.dtype, (B, Hv, Dk, Dv), v.device
-    qk, vo, gate = (B, L, Hk, Dk), (B, L, Hv, Dv), (B, L, Hv)
-    dq = torch.empty(qk, dtype=dt, device=dev) if dq is None else dq
-    dk = torch.empty(qk, dtype=dt, device=dev) if dk is None else dk
-    dv = torch.empty(vo, dtype=dt, device=dev) if dv is None else dv
-    dg = torch.empty(gate, dtype=torch.float32, device=dev) if dg is None else dg
-    dbeta = torch.empty(gate, dtype=dt, device=dev) if dbeta is None else dbeta
-    if dinitial_state is None and return_dinitial_state and initial_state is not None:
-        dinitial_state = torch.empty(st, dtype=torch.float32, device=dev)
-    f32 = torch.float32
-    _check(v.get_device(), (
-        ("q", q, qk, dt), ("k", k, qk, dt), ("v", v, vo, dt), ("g", g, gate, f32), ("beta", beta, gate, dt),
-        ("seq_idx", seq_idx, (B, L), torch.int32), ("initial_state", initial_state, st, f32), ("dout", dout, vo, dt),
-        ("dfinal_state", dfinal_state, st, f32), ("dq", dq, qk, dt), ("dk", dk, qk, dt), ("dv", dv, vo, dt),
-        ("dg", dg, gate, f32), ("dbeta", dbeta, gate, dt), ("dinitial_state", dinitial_state, st, f32)))
-    need = ccv_gdr_bwd_workspace_size(B, L, Hk, Hv, Dk, Dv, TORCH_DTYPE[dt])
-    ws = _workspace(need, workspace, dev)
-    _launch(v.get_device(), stream, "ccv_gdr_bwd", *_t(q), *_t(k), *_t(v), *_t(g), *_t(beta), *_t(seq_idx),
-            *_t(initial_state), *_t(dout), *_t(dfinal_state), *_t(dq), *_t(dk), *_t(dv), *_t(dg), *_t(dbeta),
-            *_t(dinitial_state), *_ws(ws), B, L, Hk, Hv, Dk, Dv, max(Dk, 1) ** -0.5 if scale is None else scale,
-            TORCH_DTYPE[dt])
-    return dq, dk, dv, dg, dbeta, dinitial_state
-
-
-def _rows(x: torch.Tensor) -> torch.Tensor:
-    """[..., D] as [N, D] without a copy."""
-    if x.dim() == 2:
-        return x
-    if x.dim() == 1:
-        return x.unsqueeze(0)
-    try:
-        return x.view(-1, x.shape[-1])
-    except RuntimeError as e:
-        raise ValueError("the leading dimensions of a layer norm's tensor must collapse into one stride "
-                         "(pass a 2-D view)") from e
-
-
-def _ln_check(x, weight, bias):
-    if x.dim() < 1 or x.dtype not in TORCH_DTYPE:
-        raise ValueError(f"x must be [..., D] of a supported dtype, got {x.dtype}")
-    D = x.shape[-1]
-    par = weight if weight is not None else bias
-    wdt = par.dtype if par is not None else x.dtype
-    if wdt not in TORCH_DTYPE:
-        raise ValueError(f"unsupported weight dtype {wdt}")
-    _check(x.get_device(), (("x", x, x.shape, x.dtype), ("weight", weight, (D,), wdt), ("bias", bias, (D,), wdt)))
-    return D, wdt
+    rc, *grads = (_ext_module or _ext()).gdr_bwd(q, k, v, g, beta, dout, scale, seq_idx, initial_state, dfinal_state,
+                                                 dq, dk, dv, dg, dbeta, dinitial_state, return_dinitial_state,
+                                                 workspace, None if stream is None else stream.cuda_stream)
+    if rc:
+        _raise(rc)
+    return tuple(grads)
 
 
 def ccv_ln_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -278,17 +164,9 @@ def ccv_ln_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Layer normalisation of x [..., D] over its last dimension; weight and
     bias [D] in a dtype of their own, or None."""
-    D, wdt = _ln_check(x, weight, bias)
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    else:
-        _check(x.get_device(), (("out", out, x.shape, x.dtype),))
-    x2, o2 = (x, out) if x.numel() == 0 else (_rows(x), _rows(out))
-    N = x.numel() // D if D else 0
-    if N == 0:
-        return out
-    _launch(x.get_device(), stream, "ccv_ln_fwd", *_t(x2), *_v(weight), *_v(bias), *_t(o2), N, D, eps,
-            TORCH_DTYPE[x.dtype], TORCH_DTYPE[wdt])
+    rc, out = (_ext_module or _ext()).ln_fwd(x, weight, bias, eps, out, None if stream is None else stream.cuda_stream)
+    if rc:
+        _raise(rc)
     return out
 
 
@@ -307,23 +185,11 @@ def ccv_ln_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], dout: torch.Tens
     wanted); dout [..., D].  dweight (dbias) is made when weight (bias) is
     given, in its dtype.
     """
-    D, wdt = _ln_check(x, weight, bias)
-    if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if dweight is None and weight is not None:
-        dweight = torch.empty((D,), dtype=wdt, device=x.device)
-    if dbias is None and bias is not None:
-        dbias = torch.empty((D,), dtype=wdt, device=x.device)
-    dev = x.get_device()
-    _check(dev, (("dout", dout, x.shape, x.dtype), ("dx", dx, x.shape, x.dtype), ("dweight", dweight, (D,), wdt),
-                 ("dbias", dbias, (D,), wdt)))
-    N = x.numel() // D if D else 0
-    x2, g2, d2 = (_rows(x), _rows(dout), _rows(dx)) if N else (x.new_empty((0, D)),) * 3
-    need = ccv_ln_bwd_workspace_size(N, D) if dweight is not None or dbias is not None else 0
-    ws = _workspace(need, workspace, x.device)
-    _launch(dev, stream, "ccv_ln_bwd", *_t(x2), *_v(weight), *_t(g2), *_t(d2), *_v(dweight), *_v(dbias), *_ws(ws), N,
-            D, eps, TORCH_DTYPE[x.dtype], TORCH_DTYPE[wdt])
-    return dx, dweight, dbias
+    rc, *grads = (_ext_module or _ext()).ln_bwd(x, weight, dout, bias, eps, dx, dweight, dbias, workspace,
+                                                None if stream is None else stream.cuda_stream)
+    if rc:
+        _raise(rc)
+    return tuple(grads)
 
 
 gated_delta_rule_fwd = ccv_gdr_fwd
