@@ -78,8 +78,8 @@ __device__ __forceinline__ void store_v(void* base, int64_t off, int64_t stride,
   }
 }
 
-// Sum over the block with one barrier: `red` (32 NS floats) is not written
-// again before another barrier has passed.
+// Sum over the block with one barrier: `red` (NS x 32 floats, zero beyond the
+// block's warps) is not written again before another barrier has passed.
 template <int NS>
 __device__ __forceinline__ void block_sum(float (&v)[NS], float* red, int nwarps) {
 #pragma unroll
@@ -93,11 +93,15 @@ __device__ __forceinline__ void block_sum(float (&v)[NS], float* red, int nwarps
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    float x = lane < nwarps ? red[i * 32 + lane] : 0.f;
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(kFullMask, x, m);
-    v[i] = x;
+    const float4 x = *reinterpret_cast<const float4*>(red + i * 32);
+    v[i] = (x.x + x.y) + (x.z + x.w);
   }
+  for (int k = 4; k < nwarps; k += 4)
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(red + i * 32 + k);
+      v[i] += (x.x + x.y) + (x.z + x.w);
+    }
 }
 
 // V parameters from column col: one or two vector loads where the vector is
@@ -194,10 +198,11 @@ __global__ void __launch_bounds__(512) ln_fwd_ring(const LnArgs a, int stages) {
   using E = typename Fmt<DT>::E;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kMaxStages];
-  __shared__ float red[2][32];
+  __shared__ __align__(16) float red[2][32];
   const uint32_t row_bytes = static_cast<uint32_t>(a.D) * sizeof(E);
   const int t = threadIdx.x, T = blockDim.x, nwarps = T >> 5;
   const int64_t step = gridDim.x;
+  if (t < 32) red[0][t] = red[1][t] = 0.f;
   auto fill = [&](int64_t row, int s) {
     mbar_arrive_expect_tx(&full[s], row_bytes);
     bulk_load(ring + s * row_bytes, static_cast<const E*>(a.x) + row * a.xs0, row_bytes, &full[s]);
@@ -414,10 +419,11 @@ __global__ void __launch_bounds__(MAXT) ln_bwd_ring(const LnBwdArgs a, int stage
   using E = typename Fmt<DT>::E;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kMaxStages];
-  __shared__ float red0[32], red1[96];
+  __shared__ __align__(16) float red0[32], red1[96];
   const uint32_t row_bytes = static_cast<uint32_t>(a.D) * sizeof(E);
   const int t = threadIdx.x, T = blockDim.x, nwarps = T >> 5;
   const int64_t step = gridDim.x;
+  if (t < 32) red0[t] = red1[t] = red1[32 + t] = red1[64 + t] = 0.f;
   auto fill = [&](int64_t row, int s) {
     mbar_arrive_expect_tx(&full[s], 2 * row_bytes);
     bulk_load(ring + 2 * s * row_bytes, static_cast<const E*>(a.x) + row * a.xs0, row_bytes, &full[s]);
@@ -559,21 +565,24 @@ __global__ void ln_bwd_any(const LnBwdArgs a) {
   }
 }
 
-// dw and db: partials added in order, 8 strided subsequences and then these.
-__global__ void ln_bwd_reduce(const LnBwdArgs a, int P) {
+// dw and db: partials added in order, 32 strided subsequences and then these.
+__global__ void __launch_bounds__(1024) ln_bwd_reduce(const LnBwdArgs a, int P) {
   pdl_enter();
-  __shared__ float sh[8][33];
+  __shared__ float sh[32][33];
   const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + c;
   float x = 0.f;
-  if (col < 2 * a.D)
-    for (int p = r; p < P; p += 8) x += a.part[static_cast<int64_t>(p) * 2 * a.D + col];
+  if (col < 2 * a.D) {
+    const float* p = a.part + col;
+#pragma unroll 8
+    for (int i = r; i < P; i += 32) x += p[static_cast<int64_t>(i) * 2 * a.D];
+  }
   sh[r][c] = x;
   __syncthreads();
   if (r == 0 && col < 2 * a.D) {
     x = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x += sh[i][c];
+    for (int i = 0; i < 32; ++i) x += sh[i][c];
     if (col < a.D) {
       if (a.dw != nullptr) st_param(a.dw, col * a.dws, a.wdt, x);
     } else if (a.db != nullptr) {
@@ -586,8 +595,13 @@ bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 unsigned threads(int64_t n, int nv) { return static_cast<unsigned>(((n + nv - 1) / nv + 31) / 32 * 32); }
 
-// Blocks of an SM and stages of a block for rows of `bytes` a stage.
-int ring_blocks(unsigned T) { return T >= 512 ? 2 : static_cast<int>(1024 / T < 8 ? 1024 / T : 8); }
+// Blocks of an SM (by the registers of NV vectors a thread) and stages of a
+// block for rows of `bytes` a stage.  [16384,5120] bf16: 62.3 us with four
+// vectors a thread and three blocks, 69.3 with two and three, 79 with four and two.
+int ring_blocks(unsigned T, int NV) {
+  const int n = (NV >= 4 ? 512 : 1024) / static_cast<int>(T);
+  return n < 1 ? 1 : n < 8 ? n : 8;
+}
 int ring_stages(int blocks, int64_t bytes) {
   const int64_t n = kRingBytes / (blocks * bytes);
   return static_cast<int>(n < kMaxStages ? n : kMaxStages);
@@ -597,7 +611,7 @@ template <int DT, int NV>
 cudaError_t fwd_ring(const LnArgs& a, const Device& dev, cudaStream_t s) {
   const unsigned T = threads(a.D / Fmt<DT>::VEC, NV);
   const int64_t bytes = a.D * static_cast<int64_t>(sizeof(typename Fmt<DT>::E));
-  const int blocks = ring_blocks(T), stages = ring_stages(blocks, bytes);
+  const int blocks = ring_blocks(T, NV), stages = ring_stages(blocks, bytes);
   const int64_t grid = static_cast<int64_t>(dev.sm_count) * blocks;
   const cudaError_t e =
       cudaFuncSetAttribute(ln_fwd_ring<DT, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
@@ -618,7 +632,7 @@ cudaError_t fwd_dt(const LnArgs& a, const Device& dev, cudaStream_t s) {
     if (n <= 32) return launch_pdl(ln_fwd_kernel<DT, V, 1, true>, warps_grid, 256, 0, s, a);
     if (n <= 64) return launch_pdl(ln_fwd_kernel<DT, V, 2, true>, warps_grid, 256, 0, s, a);
     if (n <= 256) return fwd_ring<DT, 1>(a, dev, s);
-    if (n <= 1024) return fwd_ring<DT, 2>(a, dev, s);
+    if (n <= 512) return fwd_ring<DT, 2>(a, dev, s);
     if (n <= 2048) return fwd_ring<DT, 4>(a, dev, s);
   } else {
     if (a.D <= 256) return launch_pdl(ln_fwd_kernel<DT, 1, 8, true>, warps_grid, 256, 0, s, a);
@@ -643,7 +657,7 @@ template <int DT>
 cudaError_t bwd_dt(const LnBwdArgs& a, cudaStream_t s) {
   if (a.N == 0) {  // no rows: the parameters' gradients are zero
     if (a.dw == nullptr && a.db == nullptr) return cudaSuccess;
-    return launch_pdl(ln_bwd_reduce, static_cast<unsigned>((2 * a.D + 31) / 32), 256, 0, s, a, 0);
+    return launch_pdl(ln_bwd_reduce, static_cast<unsigned>((2 * a.D + 31) / 32), 1024, 0, s, a, 0);
   }
   constexpr int V = Fmt<DT>::VEC;
   const bool vec = a.xs1 == 1 && a.gs1 == 1 && a.dxs1 == 1 && a.D % V == 0 && al16(a.x) && al16(a.dout) &&
@@ -657,8 +671,10 @@ cudaError_t bwd_dt(const LnBwdArgs& a, cudaStream_t s) {
     e = launch_pdl(ln_bwd_kernel<DT, V, 1, true, 256>, grid, 256, warp_sh, s, a);
   else if (!vec && a.D <= 128)
     e = launch_pdl(ln_bwd_kernel<DT, 1, 4, true, 256>, grid, 256, warp_sh, s, a);
+  else if (vec && n <= 128)
+    e = bwd_ring<DT, 1, 128>(a, grid, s);
   else if (vec && n <= 512)
-    e = bwd_ring<DT, 1, 512>(a, grid, s);
+    e = bwd_ring<DT, 2, 256>(a, grid, s);
   else if (vec && n <= 1024)
     e = bwd_ring<DT, 2, 512>(a, grid, s);
   else if (vec && n <= 2048)
@@ -668,7 +684,7 @@ cudaError_t bwd_dt(const LnBwdArgs& a, cudaStream_t s) {
   else
     e = launch_pdl(ln_bwd_any<DT>, grid, 512, 0, s, a);
   if (e != cudaSuccess || a.part == nullptr) return e;
-  return launch_pdl(ln_bwd_reduce, static_cast<unsigned>((2 * a.D + 31) / 32), 256, 0, s, a, static_cast<int>(grid));
+  return launch_pdl(ln_bwd_reduce, static_cast<unsigned>((2 * a.D + 31) / 32), 1024, 0, s, a, static_cast<int>(grid));
 }
 
 }  // namespace

@@ -263,7 +263,7 @@ ccv_status ccv_gdr_fwd(const void* q, const int64_t q_strides[4], const void* k,
   a.B = B, a.L = L, a.Hk = Hk, a.Hv = Hv, a.Dk = Dk, a.Dv = Dv, a.scale = scale;
   const ccv::Dtype dt = static_cast<ccv::Dtype>(dtype);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (w.total == 0) return launched(ccv::launch_gdr_step(a, dt, dev, s), "gdr_step");
+  if (w.total == 0) return launched(ccv::launch_gdr_token(a, dt, s), "gdr_token");
   uint8_t* qk_ws = static_cast<uint8_t*>(workspace);
   uint8_t* pack_ws = qk_ws + w.qk;
   cudaError_t err = ccv::launch_gdr_prep(a, dt, qk_ws, pack_ws, gdr_chunks(L), s);
@@ -317,8 +317,10 @@ ccv_status ccv_gdr_step(const void* q, const int64_t q_strides[4], const void* k
   copy(a.bs, beta_strides, 3), copy(a.s0s, state_strides, 4), copy(a.s1s, state_strides, 4);
   copy(a.os, out_strides, 4);
   a.B = B, a.L = S, a.Hk = Hk, a.Hv = Hv, a.Dk = Dk, a.Dv = Dv, a.scale = scale;
-  return launched(ccv::launch_gdr_step(a, static_cast<ccv::Dtype>(dtype), dev, static_cast<cudaStream_t>(stream)),
-                  "gdr_step");
+  const ccv::Dtype dt = static_cast<ccv::Dtype>(dtype);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (ccv::gdr_step_eligible(a, dev)) return launched(ccv::launch_gdr_step(a, dt, s), "gdr_step");
+  return launched(ccv::launch_gdr_token(a, dt, s), "gdr_step");
 }
 
 ccv_status ccv_gdr_bwd_workspace_size(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,

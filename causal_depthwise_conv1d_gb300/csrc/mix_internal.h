@@ -58,9 +58,12 @@ struct GdrGrads {
   int64_t ds0s[4];
 };
 
-// One token at a time with the state in registers: the decode step
-// (slots/n_slots) and short or unusual whole sequences.
-cudaError_t launch_gdr_step(const GdrArgs& a, Dtype dt, const Device& dev, cudaStream_t stream);
+// One token after the other with the state in registers: sequences and decode
+// steps of any sizes, and the decode step of a large batch.
+bool gdr_vec4_state(const float* p, const int64_t* strides);
+cudaError_t launch_gdr_token(const GdrArgs& a, Dtype dt, cudaStream_t stream);
+bool gdr_step_eligible(const GdrArgs& a, const Device& dev);
+cudaError_t launch_gdr_step(const GdrArgs& a, Dtype dt, cudaStream_t stream);
 
 // Chunked forward pass: the parts that do not depend on the state (qk_ws,
 // pack_ws: see gdr_chunk.cuh), then the scan that carries it.  nc = chunks.

@@ -475,7 +475,7 @@ const char* ccv_last_error(void);
 /* Name of the kernel variant the last successful ccv_fwd, ccv_update or
  * ccv_bwd on this thread enqueued (e.g. "time_vec", "chlast_tma",
  * "chlast_vec", "generic", "update", "bwd_time", "bwd_chlast",
- * "bwd_generic", "gdr_step", "gdr_chunk", "gdr_bwd", "ln_fwd", "ln_bwd", "none"). */
+ * "bwd_generic", "gdr_step", "gdr_token", "gdr_chunk", "gdr_bwd", "ln_fwd", "ln_bwd", "none"). */
 const char* ccv_last_kernel(void);
 
 /* Library ABI version: (major << 16) | minor. */
