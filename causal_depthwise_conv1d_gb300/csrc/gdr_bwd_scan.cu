@@ -22,7 +22,8 @@ namespace {
 
 __device__ unsigned g_fault;
 
-template <int DT, int DK, int NW>
+// NW groups of 16 value channels a block, H warps each (as in the forward scan).
+template <int DT, int DK, int NW, int H>
 struct Cfg {
   static constexpr int TERMS = DT == kF32 ? 2 : 1;
   static constexpr int TILE = qk_tile_bytes(DK);
@@ -31,9 +32,12 @@ struct Cfg {
   static constexpr int ROW = DT == kF32 ? 64 : 32;
   static constexpr int GBYTES = kC * ROW;                     // dO of one warp
   static constexpr int OBYTES = DT == kF32 ? 0 : kC * 32;     // dV of one warp
+  static constexpr int WARPS = NW * H;
+  static constexpr int XBYTES = H == 2 ? 4096 : 0;            // a warp's share of K D for the other
+  static constexpr int PER_WARP = GBYTES + OBYTES + XBYTES;
   // FP32 tiles leave room for one stage only
-  static constexpr int STAGES = 2 * STAGE + NW * (GBYTES + OBYTES) + 64 <= 232448 ? 2 : 1;
-  static constexpr int BYTES = STAGES * STAGE + NW * (GBYTES + OBYTES) + 64;
+  static constexpr int STAGES = 2 * STAGE + WARPS * PER_WARP + 64 <= 232448 ? 2 : 1;
+  static constexpr int BYTES = STAGES * STAGE + WARPS * PER_WARP + 64;
 };
 
 template <int DT>
@@ -65,9 +69,11 @@ __device__ __forceinline__ void fetch(const void* base, const int64_t* st, int64
 // One chunk token by token, last token first, from the original inputs: the
 // definition's own backward step on the warp's 16 rows of D^T.
 //   D += q (scale dO)^T;   dR = D^T k;   dV = beta dR;   D <- a (D - k dV^T)
-template <int DT, int DK>
-__device__ __noinline__ void token_by_token(const GdrArgs& a, const GdrGrads& gr, float (&d)[DK / 8][4], int64_t b,
-                                            int64_t h, int64_t t0, int64_t v0, float* r_out, int64_t dvp, int lane) {
+template <int DT, int NK, int H>
+__device__ __noinline__ void token_by_token(const GdrArgs& a, const GdrGrads& gr, float (&d)[NK][4], int64_t b,
+                                            int64_t h, int64_t t0, int64_t v0, float* r_out, int64_t dvp, int lane,
+                                            int half, int pair, float* xb, const float* xo) {
+  const int k0 = half * NK * 8;
   using F = Fmt<DT>;
   using E = typename F::E;
   const int g = lane >> 2, qd = lane & 3;
@@ -78,7 +84,7 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, const GdrGrads& gr
   for (int i = kC - 1; i >= 0; --i) {
     const int64_t t = t0 + i;
     if (t >= a.L) {
-      if (qd == 0) r_out[i * dvp + r0] = r_out[i * dvp + r1] = 0.f;
+      if (qd == 0 && half == 0) r_out[i * dvp + r0] = r_out[i * dvp + r1] = 0.f;
       continue;
     }
     const float dec = expf(a.g[b * a.gs[0] + t * a.gs[1] + h * a.gs[2]]);
@@ -90,10 +96,10 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, const GdrGrads& gr
     const float o1 = r1 < a.Dv ? a.scale * F::to_f(op[r1 * gr.dos[3]]) : 0.f;
     float p0 = 0.f, p1 = 0.f;
 #pragma unroll
-    for (int n = 0; n < DK / 8; ++n)
+    for (int n = 0; n < NK; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int64_t kd = 8 * n + 2 * qd + e;
+        const int64_t kd = k0 + 8 * n + 2 * qd + e;
         if (kd < a.Dk) {
           const float kv = F::to_f(kp[t * a.ks[1] + kd * a.ks[3]]), qv = F::to_f(qp[t * a.qs[1] + kd * a.qs[3]]);
           d[n][e] = fmaf(qv, o0, d[n][e]);
@@ -107,8 +113,15 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, const GdrGrads& gr
       p0 += __shfl_xor_sync(kFullMask, p0, m);
       p1 += __shfl_xor_sync(kFullMask, p1, m);
     }
+    if constexpr (H == 2) {
+      xb[lane] = p0;
+      xb[32 + lane] = p1;
+      pair_sync(pair);
+      p0 += xo[lane], p1 += xo[32 + lane];
+      pair_sync(pair);
+    }
     const float w0 = be * p0, w1 = be * p1;
-    if (qd == 0) {
+    if (qd == 0 && half == 0) {
       r_out[i * dvp + r0] = p0;
       r_out[i * dvp + r1] = p1;
       E* vp = static_cast<E*>(gr.dv) + b * gr.dvs[0] + t * gr.dvs[1] + h * gr.dvs[2];
@@ -116,10 +129,10 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, const GdrGrads& gr
       if (r1 < a.Dv) vp[r1 * gr.dvs[3]] = F::from_f(w1);
     }
 #pragma unroll
-    for (int n = 0; n < DK / 8; ++n)
+    for (int n = 0; n < NK; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int64_t kd = 8 * n + 2 * qd + e;
+        const int64_t kd = k0 + 8 * n + 2 * qd + e;
         if (first) {
           d[n][e] = d[n][2 + e] = 0.f;
         } else if (kd < a.Dk) {
@@ -131,21 +144,22 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, const GdrGrads& gr
   }
 }
 
-template <int DT, int DK, int NW>
-__global__ void __launch_bounds__(32 * NW, 1)
+template <int DT, int DK, int NW, int H>
+__global__ void __launch_bounds__(32 * NW * H, 1)
     gdr_bwd_scan_kernel(const GdrArgs a, const GdrGrads gr, const GdrBwdWs w, int nc, int vtiles, bool gvec,
                         bool ovec) {
   pdl_enter();
-  using C = Cfg<DT, DK, NW>;
+  using C = Cfg<DT, DK, NW, H>;
   using F = Fmt<DT>;
   using E = typename F::E;
   constexpr int RB = DK * 2;
-  constexpr int NK = DK / 8;
+  constexpr int NK = DK / 8 / H;
   constexpr int NS = C::STAGES;
   extern __shared__ __align__(128) uint8_t sm[];
   uint8_t* gbuf0 = sm + NS * C::STAGE;
-  uint8_t* obuf0 = gbuf0 + NW * C::GBYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(obuf0 + NW * C::OBYTES);
+  uint8_t* obuf0 = gbuf0 + C::WARPS * C::GBYTES;
+  uint8_t* xbuf0 = obuf0 + C::WARPS * C::OBYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(xbuf0 + C::WARPS * C::XBYTES);
   unsigned* left = reinterpret_cast<unsigned*>(full + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -153,7 +167,12 @@ __global__ void __launch_bounds__(32 * NW, 1)
   const int64_t bh = blockIdx.x / vtiles;
   const int64_t b = bh / a.Hv, h = bh - b * a.Hv;
   const int64_t hk = h / (a.Hv / a.Hk);
-  const int64_t v0 = (static_cast<int64_t>(blockIdx.x % vtiles) * NW + warp) * 16;
+  const int grp = warp / H, half = warp % H;
+  const int64_t v0 = (static_cast<int64_t>(blockIdx.x % vtiles) * NW + grp) * 16;
+  const int k0 = half * NK * 8;  // first key channel of this warp
+  const int pair = grp + 1;      // its barrier
+  float* xb = reinterpret_cast<float*>(xbuf0 + warp * C::XBYTES);
+  const float* xo = reinterpret_cast<const float*>(xbuf0 + (warp ^ 1) * C::XBYTES);
   const uint8_t* qk = w.qk + (b * a.Hk + hk) * nc * qk_pack_bytes(DK, C::TERMS);
   const uint8_t* pkg = w.pack + bh * nc * kPackBytes;
   // step n takes chunk nc - 1 - n
@@ -186,7 +205,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
   for (int n = 0; n < NK; ++n)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int64_t kd = 8 * n + 2 * qd + (j & 1), vc = v0 + g + (j >> 1) * 8;
+      const int64_t kd = k0 + 8 * n + 2 * qd + (j & 1), vc = v0 + g + (j >> 1) * 8;
       d[n][j] = (gr.ds1 != nullptr && kd < a.Dk && vc < a.Dv)
                     ? gr.ds1[b * gr.ds1s[0] + h * gr.ds1s[1] + kd * gr.ds1s[2] + vc * gr.ds1s[3]]
                     : 0.f;
@@ -197,7 +216,9 @@ __global__ void __launch_bounds__(32 * NW, 1)
   for (int n0 = 0; n0 < nc; ++n0) {
     const int s = n0 % NS, c = nc - 1 - n0;
     const int64_t t0 = static_cast<int64_t>(c) * kC;
-    if (!mbar_wait(&full[s], (n0 / NS) & 1)) {
+    bool late = !mbar_wait(&full[s], (n0 / NS) & 1);
+    if constexpr (H == 2) late = pair_any(pair, late);  // a pair gives up together
+    if (late) {
       if (lane == 0) {
         atomicOr(&g_fault, kFaultConsumerWait);
         if (NS == 2 && n0 + 1 < nc && !mbar_wait(&full[s ^ 1], ((n0 + 1) / NS) & 1))
@@ -212,7 +233,8 @@ __global__ void __launch_bounds__(32 * NW, 1)
       const uint32_t qt_lo = qt_hi + C::TILE;
       const float* vecs = reinterpret_cast<const float*>(sm + s * C::STAGE + C::QKB);
       const float* slot = vecs + kVecHead;
-      const uint32_t th = kt_hi + C::QKB + kVecBytes, tl = th + kMatBytes, ph = tl + kMatBytes, pl = ph + kMatBytes;
+      const uint32_t th = kt_hi + C::QKB + kVecBytes, tl = th + kMatBytes;
+      const uint32_t ph = kt_hi + C::QKB + kOffP, pl = ph + kMatBytes;
       const float ga = vecs[kHdGa];
 
       float a0 = 0.f, a1 = 0.f;
@@ -220,7 +242,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
       for (int n = 0; n < NK; ++n) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dst[(8 * n + 2 * qd + (j & 1)) * dvp + v0 + g + (j >> 1) * 8] = d[n][j];
+        for (int j = 0; j < 4; ++j) dst[(k0 + 8 * n + 2 * qd + (j & 1)) * dvp + v0 + g + (j >> 1) * 8] = d[n][j];
         a0 = amax3(a0, d[n][0], d[n][1]);
         a1 = amax3(a1, d[n][2], d[n][3]);
       }
@@ -240,7 +262,8 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) u[n][j] = 0.f;
 #pragma unroll
-      for (int kt = 0; kt < DK / 16; ++kt) {
+      for (int kt = 0; kt < NK / 2; ++kt) {
+        const int piece = k0 / 8 + 2 * kt;
         uint32_t hi[4], lo[4];
         split2f(d[2 * kt][0], d[2 * kt][1], p0, hi[0], lo[0]);
         split2f(d[2 * kt][2], d[2 * kt][3], p1, hi[1], lo[1]);
@@ -249,16 +272,32 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
           uint32_t bk[4];
-          ldsm4(bk, addr_b<RB>(kt_hi, np * 16, 2 * kt, lane));
+          ldsm4(bk, addr_b<RB>(kt_hi, np * 16, piece, lane));
           mma(u[2 * np], hi, bk[0], bk[1]);
           mma(u[2 * np + 1], hi, bk[2], bk[3]);
           mma(u[2 * np], lo, bk[0], bk[1]);
           mma(u[2 * np + 1], lo, bk[2], bk[3]);
           if constexpr (DT == kF32) {
-            ldsm4(bk, addr_b<RB>(kt_lo, np * 16, 2 * kt, lane));
+            ldsm4(bk, addr_b<RB>(kt_lo, np * 16, piece, lane));
             mma(u[2 * np], hi, bk[0], bk[1]);
             mma(u[2 * np + 1], hi, bk[2], bk[3]);
           }
+        }
+      }
+
+      // true values, and the other half's share
+#pragma unroll
+      for (int n = 0; n < 8; ++n) u[n][0] *= di0, u[n][1] *= di0, u[n][2] *= di1, u[n][3] *= di1;
+      if constexpr (H == 2) {
+        float4* x4 = reinterpret_cast<float4*>(xb);
+        const float4* o4 = reinterpret_cast<const float4*>(xo);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) x4[n * 32 + lane] = make_float4(u[n][0], u[n][1], u[n][2], u[n][3]);
+        pair_sync(pair);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const float4 o = o4[n * 32 + lane];
+          u[n][0] += o.x, u[n][1] += o.y, u[n][2] += o.z, u[n][3] += o.w;
         }
       }
 
@@ -323,8 +362,8 @@ __global__ void __launch_bounds__(32 * NW, 1)
             const float2 cu = *reinterpret_cast<const float2*>(slot + kVU * kC + n * 8 + qd * 2);
             const float2 ti = *reinterpret_cast<const float2*>(slot + kVTInv * kC + n * 8 + qd * 2);
             // a factor of zero (another sequence) selects: a state with infinities must not leak
-            const float k0 = cu.x == 0.f ? 0.f : cu.x * (u[n][0] * di0), k1 = cu.y == 0.f ? 0.f : cu.y * (u[n][1] * di0);
-            const float k2 = cu.x == 0.f ? 0.f : cu.x * (u[n][2] * di1), k3 = cu.y == 0.f ? 0.f : cu.y * (u[n][3] * di1);
+            const float k0 = cu.x == 0.f ? 0.f : cu.x * u[n][0], k1 = cu.y == 0.f ? 0.f : cu.y * u[n][1];
+            const float k2 = cu.x == 0.f ? 0.f : cu.x * u[n][2], k3 = cu.y == 0.f ? 0.f : cu.y * u[n][3];
             u[n][0] = ti.x * fmaf(s0, z[t][0], k0);
             u[n][1] = ti.y * fmaf(s0, z[t][1], k1);
             u[n][2] = ti.x * fmaf(s1, z[t][2], k2);
@@ -336,13 +375,15 @@ __global__ void __launch_bounds__(32 * NW, 1)
       float* rw = w.r + (bh * nc + c) * kC * dvp;
       float ui0, ui1;
       split_rows<8, true>(u, hi, lo, ui0, ui1, bad);
-      if (__any_sync(kFullMask, bad)) {
+      // (with two warps: also the barrier after which the exchange buffers may be written again)
+      bad = H == 2 ? pair_any(pair, bad) : __any_sync(kFullMask, bad) != 0;
+      if (bad) {
         float tmp[NK][4];  // a copy: D itself has to stay in registers
 #pragma unroll
         for (int n = 0; n < NK; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) tmp[n][j] = d[n][j];
-        token_by_token<DT, DK>(a, gr, tmp, b, h, t0, v0, rw, dvp, lane);
+        token_by_token<DT, NK, H>(a, gr, tmp, b, h, t0, v0, rw, dvp, lane, half, pair, xb, xo);
 #pragma unroll
         for (int n = 0; n < NK; ++n)
 #pragma unroll
@@ -384,11 +425,13 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int n = 2 * np + t;
+          if (H == 1 || (np >> 1) == half)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) rw[(n * 8 + qd * 2 + (j & 1)) * dvp + v0 + g + (j >> 1) * 8] = u[n][j];
+            for (int j = 0; j < 4; ++j) rw[(n * 8 + qd * 2 + (j & 1)) * dvp + v0 + g + (j >> 1) * 8] = u[n][j];
           const float2 be = *reinterpret_cast<const float2*>(slot + kVBeta * kC + n * 8 + qd * 2);
           y[t][0] = u[n][0] * be.x, y[t][1] = u[n][1] * be.y, y[t][2] = u[n][2] * be.x, y[t][3] = u[n][3] * be.y;
         }
+        if (H == 2 && (np >> 1) != half) continue;  // the other warp's tokens
         if (DT != kF32 && wovec) {
           if constexpr (DT != kF32) {
             const uint32_t r[4] = {F::pack2(y[0][0], y[0][1]), F::pack2(y[0][2], y[0][3]), F::pack2(y[1][0], y[1][1]),
@@ -410,8 +453,8 @@ __global__ void __launch_bounds__(32 * NW, 1)
         __syncwarp();
         E* op = static_cast<E*>(gr.dv) + b * gr.dvs[0] + h * gr.dvs[2] + v0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int y = i * 32 + lane, r = y >> 1, pc = y & 1;
+        for (int i = 0; i < 4 / H; ++i) {
+          const int y = (half * 2 + i) * 32 + lane, r = y >> 1, pc = y & 1;
           const uint4 v = lds128(ob + r * 32 + pc * 16);
           if (t0 + r < a.L) *reinterpret_cast<uint4*>(op + (t0 + r) * gr.dvs[1] + pc * 8) = v;
         }
@@ -446,15 +489,15 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
           for (int kt = 0; kt < 4; ++kt) {
             uint32_t bk[2][4];
-            ldsm4t(bk[0], addr_bt<RB>(th_, kt * 16, n4 * 4, lane));
-            ldsm4t(bk[1], addr_bt<RB>(th_, kt * 16, n4 * 4 + 2, lane));
+            ldsm4t(bk[0], addr_bt<RB>(th_, kt * 16, k0 / 8 + n4 * 4, lane));
+            ldsm4t(bk[1], addr_bt<RB>(th_, kt * 16, k0 / 8 + n4 * 4 + 2, lane));
 #pragma unroll
             for (int i = 0; i < 4; ++i) mma(z[i], hi[kt], bk[i >> 1][(i & 1) * 2], bk[i >> 1][(i & 1) * 2 + 1]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) mma(z[i], lo[kt], bk[i >> 1][(i & 1) * 2], bk[i >> 1][(i & 1) * 2 + 1]);
             if constexpr (DT == kF32) {
-              ldsm4t(bk[0], addr_bt<RB>(tl_, kt * 16, n4 * 4, lane));
-              ldsm4t(bk[1], addr_bt<RB>(tl_, kt * 16, n4 * 4 + 2, lane));
+              ldsm4t(bk[0], addr_bt<RB>(tl_, kt * 16, k0 / 8 + n4 * 4, lane));
+              ldsm4t(bk[1], addr_bt<RB>(tl_, kt * 16, k0 / 8 + n4 * 4 + 2, lane));
 #pragma unroll
               for (int i = 0; i < 4; ++i) mma(z[i], hi[kt], bk[i >> 1][(i & 1) * 2], bk[i >> 1][(i & 1) * 2 + 1]);
             }
@@ -477,7 +520,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
     if (lane == 0) {
       unsigned n;
       asm volatile("atom.acq_rel.cta.shared.add.u32 %0, [%1], 1;" : "=r"(n) : "r"(smem_u32(&left[s])) : "memory");
-      if (n == NW - 1) {
+      if (n == C::WARPS - 1) {
         left[s] = 0;
         if (n0 + NS < nc) fill(n0 + NS);
       }
@@ -488,16 +531,16 @@ __global__ void __launch_bounds__(32 * NW, 1)
     for (int n = 0; n < NK; ++n)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t kd = 8 * n + 2 * qd + (j & 1), vc = v0 + g + (j >> 1) * 8;
+        const int64_t kd = k0 + 8 * n + 2 * qd + (j & 1), vc = v0 + g + (j >> 1) * 8;
         if (kd < a.Dk && vc < a.Dv)
           gr.ds0[b * gr.ds0s[0] + h * gr.ds0s[1] + kd * gr.ds0s[2] + vc * gr.ds0s[3]] = d[n][j];
       }
   }
 }
 
-template <int DT, int DK, int NW>
+template <int DT, int DK, int NW, int H>
 cudaError_t launch(const GdrArgs& a, const GdrGrads& g, const GdrBwdWs& w, int nc, cudaStream_t s) {
-  using C = Cfg<DT, DK, NW>;
+  using C = Cfg<DT, DK, NW, H>;
   static_assert(C::BYTES <= 232448, "shared memory of one block");
   using E = typename Fmt<DT>::E;
   constexpr int64_t V = 16 / sizeof(E);
@@ -506,20 +549,24 @@ cudaError_t launch(const GdrArgs& a, const GdrGrads& g, const GdrBwdWs& w, int n
   };
   const int vtiles = static_cast<int>((a.Dv + 16 * NW - 1) / (16 * NW));
   const cudaError_t e =
-      cudaFuncSetAttribute(gdr_bwd_scan_kernel<DT, DK, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+      cudaFuncSetAttribute(gdr_bwd_scan_kernel<DT, DK, NW, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e != cudaSuccess) return e;
-  return launch_pdl(gdr_bwd_scan_kernel<DT, DK, NW>, static_cast<unsigned>(a.B * a.Hv * vtiles), 32 * NW, C::BYTES, s,
+  return launch_pdl(gdr_bwd_scan_kernel<DT, DK, NW, H>, static_cast<unsigned>(a.B * a.Hv * vtiles), 32 * C::WARPS, C::BYTES, s,
                     a, g, w, nc, vtiles, al(g.dout, g.dos), al(g.dv, g.dvs));
 }
 
 template <int DT, int DK>
 cudaError_t launch_nw(const GdrArgs& a, const GdrGrads& g, const GdrBwdWs& w, int nc, const Device& dev,
                       cudaStream_t s) {
-  const int64_t heads = a.B * a.Hv, groups = (a.Dv + 15) / 16;  // as in the forward scan
-  if (heads * ((groups + 1) / 2) <= dev.sm_count) return launch<DT, DK, 2>(a, g, w, nc, s);
-  if (DT == kF32 || heads * ((groups + 3) / 4) <= dev.sm_count) return launch<DT, DK, 4>(a, g, w, nc, s);
-  if constexpr (DT != kF32) return launch<DT, DK, 8>(a, g, w, nc, s);
-  return cudaErrorInvalidValue;
+  const int64_t heads = a.B * a.Hv, groups = (a.Dv + 15) / 16, sms = dev.sm_count;  // as in the forward scan
+  if constexpr (DT == kF32) {
+    if (heads * ((groups + 1) / 2) <= sms) return launch<DT, DK, 2, 1>(a, g, w, nc, s);
+    return launch<DT, DK, 4, 1>(a, g, w, nc, s);
+  } else {
+    if (heads * ((groups + 1) / 2) <= sms) return launch<DT, DK, 2, 2>(a, g, w, nc, s);
+    if (heads * ((groups + 3) / 4) <= sms) return launch<DT, DK, 4, 1>(a, g, w, nc, s);
+    return launch<DT, DK, 8, 1>(a, g, w, nc, s);
+  }
 }
 
 template <int DT>

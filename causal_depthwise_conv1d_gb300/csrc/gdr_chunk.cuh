@@ -54,7 +54,9 @@ constexpr int kVecBytes = 4096;
 constexpr int kVecFwdBytes = (kVecHead + 6 * kC) * 4;  // what the forward scan reads
 static_assert((kVecHead + kVSlots * kC) * 4 <= kVecBytes, "vector part");
 constexpr int kMatBytes = kC * kC * 2;                     // one FP16 64 x 64 matrix
-constexpr int kPackBytes = kVecBytes + 4 * kMatBytes;      // factors, T hi, T lo, P hi, P lo
+constexpr int kPadBytes = 1024;                            // L, as FP32 with padded rows, lies where T goes
+constexpr int kOffP = kVecBytes + 2 * kMatBytes + kPadBytes;
+constexpr int kPackBytes = kOffP + 2 * kMatBytes;          // factors, T hi, T lo, padding, P hi, P lo
 
 // Bytes of the [64, DK] FP16 tiles of k and q of one chunk and key head
 // (hi, and lo for FP32 inputs): k hi, (k lo,) q hi, (q lo).
@@ -205,6 +207,19 @@ __device__ __forceinline__ void split_rows(const float (&x)[NT][4], uint32_t (&h
         hi[i][2 * j + 1] = h2(x[2 * i + j][2] * f1, x[2 * i + j][3] * f1);
       }
     }
+}
+
+// Barriers of one pair of warps (id from 1).
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+      "barrier.cta.red.or.pred p, %1, 64, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
 }
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool in) {

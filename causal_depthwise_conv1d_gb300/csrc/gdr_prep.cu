@@ -22,7 +22,8 @@ namespace ccv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kLd = 68;  // leading dimension of X
+constexpr int kLd = 68;  // leading dimension of L and X
+static_assert(kC * kLd * 4 <= 2 * kMatBytes + kPadBytes, "L fits where T goes");
 
 template <int DT, int DK>
 struct PrepSmem {
@@ -32,10 +33,6 @@ struct PrepSmem {
   static constexpr int FIRST = QK > MAT ? QK : MAT;  // k and q, then X
   static constexpr int BYTES = FIRST + kPackBytes + 6 * kC * 4 + 64;
 };
-
-// L is kept in the 16 KB of T's tiles: row i rotated by 4 i columns, so that
-// eight rows at one column lie in different banks.
-__device__ __forceinline__ int l_at(int i, int j) { return i * kC + ((j + 4 * i) & (kC - 1)); }
 
 // Eight rows of k or q a warp to FP16 tiles, each row scaled by its power of
 // two; eight elements a lane.
@@ -115,66 +112,85 @@ struct RowLoad {
   }
 };
 
-// X = (I + L)^-1; only X[i][j], j <= i, is defined after it.
+// y (two or four columns from c) += sign * A[row][0..n) X[0..n)[c..], rows of A and X kLd apart.
+template <int N, int COLS>
+__device__ __forceinline__ void row_times(const float* arow, const float* x, uint64_t (&y)[COLS / 2]) {
+#pragma unroll
+  for (int m = 0; m < N; m += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(arow + m);
+    const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t ll = pk(lv[j], lv[j]);
+      if constexpr (COLS == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(x + (m + j) * kLd);
+        y[0] = ffma2(ll, pk(v.x, v.y), y[0]);
+        y[1] = ffma2(ll, pk(v.z, v.w), y[1]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(x + (m + j) * kLd);
+        y[0] = ffma2(ll, pk(v.x, v.y), y[0]);
+      }
+    }
+  }
+}
+
+// X = (I + L)^-1; only X[i][j], j <= i, is defined after it.  The blocks below
+// the diagonal are -D' (C A'): the product in brackets goes to the block above
+// the diagonal, negated.
 __device__ __forceinline__ void invert(const float* L, float* X) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp < 4 && lane < 16) {
-    const int o = warp * 16;
+    const float* Lb = L + warp * 16 * (kLd + 1);
+    float* Xb = X + warp * 16 * (kLd + 1) + lane;
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float s = i == lane ? 1.f : 0.f;
 #pragma unroll
-      for (int m = 0; m < i; ++m) s = fmaf(-L[l_at(o + i, o + m)], x[m], s);
+      for (int m = 0; m < i; m += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(Lb + i * kLd + m);
+        s = fmaf(-l.x, x[m], s);
+        if (m + 1 < i) s = fmaf(-l.y, x[m + 1], s);
+        if (m + 2 < i) s = fmaf(-l.z, x[m + 2], s);
+        if (m + 3 < i) s = fmaf(-l.w, x[m + 3], s);
+      }
       x[i] = s;
-      X[(o + i) * kLd + o + lane] = s;
+      Xb[i * kLd] = s;
     }
   }
   __syncthreads();
-  {  // 16 x 16 blocks (1,0) and (3,2); the scratch is the block above the diagonal
+  float a, b;
+  {  // 16 x 16 blocks (1,0) and (3,2)
     const int p = tid >> 7, r = (tid >> 3) & 15, c = (tid & 7) * 2;
     const int r0 = 32 * p + 16, c0 = 32 * p;
-    float y0 = 0.f, y1 = 0.f;
-#pragma unroll
-    for (int m = 0; m < 16; ++m) {
-      const float l = L[l_at(r0 + r, c0 + m)];
-      const float2 v = *reinterpret_cast<const float2*>(X + (c0 + m) * kLd + c0 + c);
-      y0 = fmaf(l, v.x, y0), y1 = fmaf(l, v.y, y1);
-    }
+    uint64_t y[1] = {0};
+    row_times<16, 2>(L + (r0 + r) * kLd + c0, X + c0 * kLd + c0 + c, y);
     float2* scratch = reinterpret_cast<float2*>(X + (c0 + r) * kLd + r0 + c);
-    *scratch = make_float2(y0, y1);
+    upk(y[0], a, b);
+    *scratch = make_float2(-a, -b);
     __syncthreads();
-    y0 = y1 = 0.f;
-#pragma unroll
-    for (int m = 0; m < 16; ++m) {
-      const float l = X[(r0 + r) * kLd + r0 + m];
-      const float2 v = *reinterpret_cast<const float2*>(X + (c0 + m) * kLd + r0 + c);
-      y0 = fmaf(-l, v.x, y0), y1 = fmaf(-l, v.y, y1);
-    }
-    *reinterpret_cast<float2*>(X + (r0 + r) * kLd + c0 + c) = make_float2(y0, y1);
+    y[0] = 0;
+    row_times<16, 2>(X + (r0 + r) * kLd + r0, X + c0 * kLd + r0 + c, y);
+    upk(y[0], a, b);
+    *reinterpret_cast<float2*>(X + (r0 + r) * kLd + c0 + c) = make_float2(a, b);
     __syncthreads();
     *scratch = make_float2(0.f, 0.f);  // read as part of X below
     __syncthreads();
   }
   {  // the 32 x 32 block
     const int r = tid >> 3, c = (tid & 7) * 4;
-    float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int m = 0; m < 32; ++m) {
-      const float l = L[l_at(32 + r, m)];
-      const float4 v = *reinterpret_cast<const float4*>(X + m * kLd + c);
-      y[0] = fmaf(l, v.x, y[0]), y[1] = fmaf(l, v.y, y[1]), y[2] = fmaf(l, v.z, y[2]), y[3] = fmaf(l, v.w, y[3]);
-    }
-    *reinterpret_cast<float4*>(X + r * kLd + 32 + c) = make_float4(y[0], y[1], y[2], y[3]);
+    uint64_t y[2] = {0, 0};
+    float d, e;
+    row_times<32, 4>(L + (32 + r) * kLd, X + c, y);
+    upk(y[0], a, b);
+    upk(y[1], d, e);
+    *reinterpret_cast<float4*>(X + r * kLd + 32 + c) = make_float4(-a, -b, -d, -e);
     __syncthreads();
-    y[0] = y[1] = y[2] = y[3] = 0.f;
-#pragma unroll 8
-    for (int m = 0; m < 32; ++m) {
-      const float l = X[(32 + r) * kLd + 32 + m];
-      const float4 v = *reinterpret_cast<const float4*>(X + m * kLd + 32 + c);
-      y[0] = fmaf(-l, v.x, y[0]), y[1] = fmaf(-l, v.y, y[1]), y[2] = fmaf(-l, v.z, y[2]), y[3] = fmaf(-l, v.w, y[3]);
-    }
-    *reinterpret_cast<float4*>(X + (32 + r) * kLd + c) = make_float4(y[0], y[1], y[2], y[3]);
+    y[0] = y[1] = 0;
+    row_times<32, 4>(X + (32 + r) * kLd + 32, X + 32 + c, y);
+    upk(y[0], a, b);
+    upk(y[1], d, e);
+    *reinterpret_cast<float4*>(X + (32 + r) * kLd + c) = make_float4(a, b, d, e);
     __syncthreads();
   }
 }
@@ -199,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 3)
   float* slot = vecs + kVecHead;
   uint8_t* th = pack + kVecBytes;
   uint8_t* tl = th + kMatBytes;
-  uint8_t* ph = tl + kMatBytes;
+  uint8_t* ph = pack + kOffP;
   uint8_t* pl = ph + kMatBytes;
   float* L = reinterpret_cast<float*>(th);  // until T is written
   float* kinv = reinterpret_cast<float*>(pack + kPackBytes);
@@ -396,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 3)
                                        ((e < 2 ? gl0 : gl1) - ((e & 1) ? lj.y : lj.x)));
           // selected, not multiplied: nothing crosses the diagonal or a new sequence
           p[n][e] = in ? gam * qq[n][e] : 0.f;
-          if (j < i) L[l_at(i, j)] = in ? (e < 2 ? b0 : b1) * gam * kk[n][e] : 0.f;
+          if (j < i) L[i * kLd + j] = in ? (e < 2 ? b0 : b1) * gam * kk[n][e] : 0.f;
         }
         m0 = amax3(m0, p[n][0], p[n][1]);
         m1 = amax3(m1, p[n][2], p[n][3]);

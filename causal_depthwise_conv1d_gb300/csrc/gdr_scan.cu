@@ -15,6 +15,12 @@
 // another and none is set aside for the copies.  v is fetched by each warp for
 // itself.
 //
+// With few heads a group of 16 channels takes two warps (H = 2), each with half
+// of the key channels: both form their share of K S, exchange it through
+// shared memory, take the triangular system both (its result is an operand of
+// both halves of the state), and split the output by tokens.  A chunk's chain
+// is then about 0.6 as long.
+//
 // What bounds it: the tensor instructions of 16-bit mma.sync (8 cycles each a
 // quarter SM) in the chain of one chunk after the other; a head's columns are
 // spread over as many blocks as it takes to fill the SMs.
@@ -29,7 +35,8 @@ namespace {
 
 __device__ unsigned g_fault;
 
-template <int DT, int DK, int NW, bool SAVE>
+// NW groups of 16 value channels a block, H warps each.
+template <int DT, int DK, int NW, int H, bool SAVE>
 struct ScanCfg {
   static constexpr int TERMS = DT == kF32 ? 2 : 1;             // of k and q
   // Terms of S, U and P in the output: bf16 outputs (8 bits) take 11 bits of
@@ -37,13 +44,14 @@ struct ScanCfg {
   static constexpr bool OLO = DT != kBF16;
   static constexpr int TILE = qk_tile_bytes(DK);
   static constexpr int QKB = SAVE ? TERMS * TILE : 2 * TERMS * TILE;  // k alone, or k and q
-  static constexpr int MATS = SAVE ? 2 : (OLO ? 4 : 3);        // T hi, T lo, P hi, P lo
-  static constexpr int STAGE = QKB + kVecBytes + MATS * kMatBytes;
+  static constexpr int MATB = SAVE ? 2 * kMatBytes : 2 * kMatBytes + kPadBytes + (OLO ? 2 : 1) * kMatBytes;
+  static constexpr int STAGE = QKB + kVecBytes + MATB;
   static constexpr int VROW = DT == kF32 ? 64 : 32;            // bytes of a warp's 16 channels of one token
   static constexpr int VBYTES = kC * VROW;
   static constexpr int OBYTES = (DT == kF32 || SAVE) ? 0 : kC * 32;
-  static constexpr int BYTES = 2 * STAGE + NW * (VBYTES + OBYTES) + 64;
-  static constexpr int THREADS = 32 * NW;
+  static constexpr int WARPS = NW * H;
+  static constexpr int XBYTES = H == 2 ? (SAVE ? 4096 : 6144) : 0;  // a warp's share of K S (and Q S) for the other
+  static constexpr int BYTES = 2 * STAGE + WARPS * (VBYTES + OBYTES + XBYTES) + 64;
 };
 
 // This warp's v of one chunk into its buffer; rows past the sequence and
@@ -77,9 +85,11 @@ __device__ __forceinline__ void fetch_v(const GdrArgs& a, int64_t b, int64_t h, 
 
 // One chunk token by token, from the original inputs, on the warp's 16 rows
 // of S^T (rows g and g + 8 of this thread, key channels 8 i + 2 qd + {0, 1}).
-template <int DT, int DK, bool SAVE>
-__device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[DK / 8][4], int64_t b, int64_t h,
-                                            int64_t t0, int64_t v0, float* u_out, int64_t dvp, int lane) {
+// Two warps of a pair add their sums through xb (own) and xo (the other's).
+template <int DT, int NK, int H, bool SAVE>
+__device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[NK][4], int64_t b, int64_t h, int64_t t0,
+                                            int64_t v0, float* u_out, int64_t dvp, int lane, int half, int pair,
+                                            float* xb, const float* xo) {
   using F = Fmt<DT>;
   using E = typename F::E;
   const int g = lane >> 2, qd = lane & 3;
@@ -87,7 +97,8 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[DK / 8
   const E* kp = static_cast<const E*>(a.k) + b * a.ks[0] + hk * a.ks[2];
   const E* qp = static_cast<const E*>(a.q) + b * a.qs[0] + hk * a.qs[2];
   const int64_t r0 = v0 + g, r1 = v0 + g + 8;
-  if (SAVE && qd == 0) {  // rows past the sequence
+  const int k0 = half * NK * 8;
+  if (SAVE && qd == 0 && half == 0) {  // rows past the sequence
     for (int64_t i = a.L - t0; i < kC; ++i) u_out[i * dvp + r0] = u_out[i * dvp + r1] = 0.f;
   }
   for (int i = 0; i < kC && t0 + i < a.L; ++i) {
@@ -97,16 +108,16 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[DK / 8
     if (a.seq != nullptr && t > 0 && a.seq[b * a.ss[0] + t * a.ss[1]] != a.seq[b * a.ss[0] + (t - 1) * a.ss[1]]) {
       dec = 0.f;
 #pragma unroll
-      for (int n = 0; n < DK / 8; ++n)
+      for (int n = 0; n < NK; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) st[n][j] = 0.f;
     }
     float p0 = 0.f, p1 = 0.f, o0 = 0.f, o1 = 0.f, qk = 0.f;
 #pragma unroll
-    for (int n = 0; n < DK / 8; ++n)
+    for (int n = 0; n < NK; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int64_t kd = 8 * n + 2 * qd + e;
+        const int64_t kd = k0 + 8 * n + 2 * qd + e;
         const float kv = kd < a.Dk ? F::to_f(kp[t * a.ks[1] + kd * a.ks[3]]) : 0.f;
         const float qv = kd < a.Dk ? F::to_f(qp[t * a.qs[1] + kd * a.qs[3]]) : 0.f;
         if (kd < a.Dk) {
@@ -125,10 +136,18 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[DK / 8
       o1 += __shfl_xor_sync(kFullMask, o1, m);
       qk += __shfl_xor_sync(kFullMask, qk, m);
     }
+    if constexpr (H == 2) {
+      const float x[5] = {p0, p1, o0, o1, qk};
+#pragma unroll
+      for (int j = 0; j < 5; ++j) xb[j * 32 + lane] = x[j];
+      pair_sync(pair);
+      p0 += xo[lane], p1 += xo[32 + lane], o0 += xo[64 + lane], o1 += xo[96 + lane], qk += xo[128 + lane];
+      pair_sync(pair);
+    }
     const E* vp = static_cast<const E*>(a.v) + b * a.vs[0] + t * a.vs[1] + h * a.vs[2];
     const float x0 = r0 < a.Dv ? F::to_f(vp[r0 * a.vs[3]]) : 0.f, x1 = r1 < a.Dv ? F::to_f(vp[r1 * a.vs[3]]) : 0.f;
     const float u0 = be * (x0 - dec * p0), u1 = be * (x1 - dec * p1);
-    if (qd == 0) {
+    if (qd == 0 && half == 0) {
       if constexpr (SAVE) {
         u_out[i * dvp + r0] = u0;
         u_out[i * dvp + r1] = u1;
@@ -139,10 +158,10 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[DK / 8
       }
     }
 #pragma unroll
-    for (int n = 0; n < DK / 8; ++n)
+    for (int n = 0; n < NK; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int64_t kd = 8 * n + 2 * qd + e;
+        const int64_t kd = k0 + 8 * n + 2 * qd + e;
         const float kv = kd < a.Dk ? F::to_f(kp[t * a.ks[1] + kd * a.ks[3]]) : 0.f;
         if (kd < a.Dk) {
           st[n][e] = fmaf(kv, u0, dec * st[n][e]);
@@ -152,20 +171,21 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[DK / 8
   }
 }
 
-template <int DT, int DK, int NW, bool SAVE>
-__global__ void __launch_bounds__(32 * NW, 1)
+template <int DT, int DK, int NW, int H, bool SAVE>
+__global__ void __launch_bounds__(32 * NW * H, 1)
     gdr_scan_kernel(const GdrArgs a, const uint8_t* qk_ws, const uint8_t* pack_ws, float* s_ws, float* u_ws,
                     unsigned* s_max, int nc, int vtiles, bool vvec, bool ovec) {
   pdl_enter();
-  using C = ScanCfg<DT, DK, NW, SAVE>;
+  using C = ScanCfg<DT, DK, NW, H, SAVE>;
   using F = Fmt<DT>;
   using E = typename F::E;
   constexpr int RB = DK * 2;
-  constexpr int NK = DK / 8;
+  constexpr int NK = DK / 8 / H;  // key channel tiles of a warp
   extern __shared__ __align__(128) uint8_t sm[];
   uint8_t* vbuf0 = sm + 2 * C::STAGE;
-  uint8_t* obuf0 = vbuf0 + NW * C::VBYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(obuf0 + NW * C::OBYTES);
+  uint8_t* obuf0 = vbuf0 + C::WARPS * C::VBYTES;
+  uint8_t* xbuf0 = obuf0 + C::WARPS * C::OBYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(xbuf0 + C::WARPS * C::XBYTES);
   unsigned* left = reinterpret_cast<unsigned*>(full + 2);  // warps that have left a stage
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -173,7 +193,12 @@ __global__ void __launch_bounds__(32 * NW, 1)
   const int64_t bh = blockIdx.x / vtiles;
   const int64_t b = bh / a.Hv, h = bh - b * a.Hv;
   const int64_t hk = h / (a.Hv / a.Hk);
-  const int64_t v0 = (static_cast<int64_t>(blockIdx.x % vtiles) * NW + warp) * 16;
+  const int grp = warp / H, half = warp % H;
+  const int64_t v0 = (static_cast<int64_t>(blockIdx.x % vtiles) * NW + grp) * 16;
+  const int k0 = half * NK * 8;  // first key channel of this warp
+  const int pair = grp + 1;      // its barrier
+  float* xb = reinterpret_cast<float*>(xbuf0 + warp * C::XBYTES);
+  const float* xo = reinterpret_cast<const float*>(xbuf0 + (warp ^ 1) * C::XBYTES);
 
   const uint8_t* qk = qk_ws + (b * a.Hk + hk) * nc * qk_pack_bytes(DK, C::TERMS);
   const uint8_t* pkg = pack_ws + bh * nc * kPackBytes;
@@ -182,10 +207,10 @@ __global__ void __launch_bounds__(32 * NW, 1)
     uint64_t* bar = &full[c & 1];
     constexpr uint32_t kVec = SAVE ? kVecBytes : kVecFwdBytes;
     const uint8_t* pc = pkg + static_cast<int64_t>(c) * kPackBytes;
-    mbar_arrive_expect_tx(bar, C::QKB + kVec + C::MATS * kMatBytes);
+    mbar_arrive_expect_tx(bar, C::QKB + kVec + C::MATB);
     bulk_load(dst, qk + static_cast<int64_t>(c) * qk_pack_bytes(DK, C::TERMS), C::QKB, bar);
     bulk_load(dst + C::QKB, pc, kVec, bar);
-    bulk_load(dst + C::QKB + kVecBytes, pc + kVecBytes, C::MATS * kMatBytes, bar);
+    bulk_load(dst + C::QKB + kVecBytes, pc + kVecBytes, C::MATB, bar);
   };
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -208,7 +233,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
   for (int n = 0; n < NK; ++n)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int64_t kd = 8 * n + 2 * qd + (j & 1), vc = v0 + g + (j >> 1) * 8;
+      const int64_t kd = k0 + 8 * n + 2 * qd + (j & 1), vc = v0 + g + (j >> 1) * 8;
       st[n][j] = (a.s0 != nullptr && kd < a.Dk && vc < a.Dv)
                      ? a.s0[b * a.s0s[0] + h * a.s0s[1] + kd * a.s0s[2] + vc * a.s0s[3]]
                      : 0.f;
@@ -218,7 +243,9 @@ __global__ void __launch_bounds__(32 * NW, 1)
   for (int c = 0; c < nc; ++c) {
     const int s = c & 1;
     const int64_t t0 = static_cast<int64_t>(c) * kC;
-    if (!mbar_wait(&full[s], (c >> 1) & 1)) {
+    bool late = !mbar_wait(&full[s], (c >> 1) & 1);
+    if constexpr (H == 2) late = pair_any(pair, late);  // a pair gives up together
+    if (late) {
       // give up: the other stage's copy must not outlive the block either
       if (lane == 0) {
         atomicOr(&g_fault, kFaultConsumerWait);
@@ -233,7 +260,8 @@ __global__ void __launch_bounds__(32 * NW, 1)
       const uint32_t qt_lo = qt_hi + C::TILE;
       const float* vecs = reinterpret_cast<const float*>(sm + s * C::STAGE + C::QKB);
       const float* slot = vecs + kVecHead;
-      const uint32_t th = kt_hi + C::QKB + kVecBytes, tl = th + kMatBytes, ph = tl + kMatBytes, pl = ph + kMatBytes;
+      const uint32_t th = kt_hi + C::QKB + kVecBytes, tl = th + kMatBytes;
+      const uint32_t ph = kt_hi + C::QKB + kOffP, pl = ph + kMatBytes;
       const float ga = vecs[kHdGa];
       float* u_out = SAVE ? u_ws + (bh * nc + c) * kC * dvp : nullptr;
       if constexpr (SAVE) {
@@ -241,7 +269,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
         for (int n = 0; n < NK; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) so[(8 * n + 2 * qd + (j & 1)) * dvp + v0 + g + (j >> 1) * 8] = st[n][j];
+          for (int j = 0; j < 4; ++j) so[(k0 + 8 * n + 2 * qd + (j & 1)) * dvp + v0 + g + (j >> 1) * 8] = st[n][j];
       }
       bool bad = vecs[kHdBad] != 0.f;
 
@@ -270,7 +298,8 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) ks[n][j] = qs[n][j] = 0.f;
 #pragma unroll
-      for (int kt = 0; kt < DK / 16; ++kt) {
+      for (int kt = 0; kt < NK / 2; ++kt) {
+        const int piece = k0 / 8 + 2 * kt;
         uint32_t hi[4], lo[4];
         split2f(st[2 * kt][0], st[2 * kt][1], p0, hi[0], lo[0]);
         split2f(st[2 * kt][2], st[2 * kt][3], p1, hi[1], lo[1]);
@@ -279,18 +308,18 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
           uint32_t bk[4];
-          ldsm4(bk, addr_b<RB>(kt_hi, np * 16, 2 * kt, lane));
+          ldsm4(bk, addr_b<RB>(kt_hi, np * 16, piece, lane));
           mma(ks[2 * np], hi, bk[0], bk[1]);
           mma(ks[2 * np + 1], hi, bk[2], bk[3]);
           mma(ks[2 * np], lo, bk[0], bk[1]);
           mma(ks[2 * np + 1], lo, bk[2], bk[3]);
           if constexpr (DT == kF32) {
-            ldsm4(bk, addr_b<RB>(kt_lo, np * 16, 2 * kt, lane));
+            ldsm4(bk, addr_b<RB>(kt_lo, np * 16, piece, lane));
             mma(ks[2 * np], hi, bk[0], bk[1]);
             mma(ks[2 * np + 1], hi, bk[2], bk[3]);
           }
           if constexpr (!SAVE) {
-            ldsm4(bk, addr_b<RB>(qt_hi, np * 16, 2 * kt, lane));
+            ldsm4(bk, addr_b<RB>(qt_hi, np * 16, piece, lane));
             mma(qs[2 * np], hi, bk[0], bk[1]);
             mma(qs[2 * np + 1], hi, bk[2], bk[3]);
             if constexpr (C::OLO) {
@@ -298,10 +327,52 @@ __global__ void __launch_bounds__(32 * NW, 1)
               mma(qs[2 * np + 1], lo, bk[2], bk[3]);
             }
             if constexpr (DT == kF32) {
-              ldsm4(bk, addr_b<RB>(qt_lo, np * 16, 2 * kt, lane));
+              ldsm4(bk, addr_b<RB>(qt_lo, np * 16, piece, lane));
               mma(qs[2 * np], hi, bk[0], bk[1]);
               mma(qs[2 * np + 1], hi, bk[2], bk[3]);
             }
+          }
+        }
+      }
+
+      // true values, and the other half's share; O: this warp's tokens are 16 np0.. and 16 np1..
+      const int np0 = H == 2 ? half : 0, np1 = H == 2 ? 3 - half : 0;
+      float qo[H == 2 ? 4 : 1][4];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        ks[n][0] *= si0, ks[n][1] *= si0, ks[n][2] *= si1, ks[n][3] *= si1;
+        if constexpr (!SAVE) qs[n][0] *= si0, qs[n][1] *= si0, qs[n][2] *= si1, qs[n][3] *= si1;
+      }
+      if constexpr (H == 2) {
+        float4* x4 = reinterpret_cast<float4*>(xb);
+        const float4* o4 = reinterpret_cast<const float4*>(xo);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) x4[n * 32 + lane] = make_float4(ks[n][0], ks[n][1], ks[n][2], ks[n][3]);
+        if constexpr (!SAVE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // tiles 0, 1, 6, 7 are the first half's tokens, 2..5 the second's
+            const int lo_t = i < 2 ? i : i + 4, hi_t = i + 2;
+            float send[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              send[j] = half == 0 ? qs[hi_t][j] : qs[lo_t][j];
+              qo[i][j] = half == 0 ? qs[lo_t][j] : qs[hi_t][j];
+            }
+            x4[(8 + i) * 32 + lane] = make_float4(send[0], send[1], send[2], send[3]);
+          }
+        }
+        pair_sync(pair);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const float4 o = o4[n * 32 + lane];
+          ks[n][0] += o.x, ks[n][1] += o.y, ks[n][2] += o.z, ks[n][3] += o.w;
+        }
+        if constexpr (!SAVE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 o = o4[(8 + i) * 32 + lane];
+            // the second half's tokens are 16 np0 = 16 (tiles 2, 3) and 16 np1 = 32 (tiles 4, 5)
+            qo[i][0] += o.x, qo[i][1] += o.y, qo[i][2] += o.z, qo[i][3] += o.w;
           }
         }
       }
@@ -332,16 +403,17 @@ __global__ void __launch_bounds__(32 * NW, 1)
           const int n = 2 * np + t;
           const float2 cf = *reinterpret_cast<const float2*>(slot + kVKS * kC + n * 8 + qd * 2);
           const float2 be = *reinterpret_cast<const float2*>(slot + kVBeta * kC + n * 8 + qd * 2);
-          ks[n][0] = be.x * (x[t][0] - cf.x * (ks[n][0] * si0));
-          ks[n][1] = be.y * (x[t][1] - cf.y * (ks[n][1] * si0));
-          ks[n][2] = be.x * (x[t][2] - cf.x * (ks[n][2] * si1));
-          ks[n][3] = be.y * (x[t][3] - cf.y * (ks[n][3] * si1));
+          ks[n][0] = be.x * (x[t][0] - cf.x * ks[n][0]);
+          ks[n][1] = be.y * (x[t][1] - cf.y * ks[n][1]);
+          ks[n][2] = be.x * (x[t][2] - cf.x * ks[n][2]);
+          ks[n][3] = be.y * (x[t][3] - cf.y * ks[n][3]);
         }
       }
       uint32_t hi[4][4], lo[4][4];
       float ri0, ri1;
       split_rows<8, true>(ks, hi, lo, ri0, ri1, bad);
-      bad = __any_sync(kFullMask, bad);
+      // (with two warps: also the barrier after which the exchange buffers may be written again)
+      bad = H == 2 ? pair_any(pair, bad) : __any_sync(kFullMask, bad) != 0;
 
       if (bad) {
         float tmp[NK][4];  // a copy: the state itself has to stay in registers
@@ -349,7 +421,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
         for (int n = 0; n < NK; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) tmp[n][j] = st[n][j];
-        token_by_token<DT, DK, SAVE>(a, tmp, b, h, t0, v0, u_out, dvp, lane);
+        token_by_token<DT, NK, H, SAVE>(a, tmp, b, h, t0, v0, u_out, dvp, lane, half, pair, xb, xo);
 #pragma unroll
         for (int n = 0; n < NK; ++n)
 #pragma unroll
@@ -392,20 +464,23 @@ __global__ void __launch_bounds__(32 * NW, 1)
         if constexpr (SAVE) {
 #pragma unroll
           for (int n = 0; n < 8; ++n)
+            if (H == 1 || (n >> 2) == half)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) u_out[(n * 8 + qd * 2 + (j & 1)) * dvp + v0 + g + (j >> 1) * 8] = u[n][j];
+              for (int j = 0; j < 4; ++j) u_out[(n * 8 + qd * 2 + (j & 1)) * dvp + v0 + g + (j >> 1) * 8] = u[n][j];
         } else {
           // O^T = scale (gi (Q S)^T + U^T P^T)
           float ui0, ui1;
           bool ignore = false;
           split_rows<8, C::OLO>(u, hi, lo, ui0, ui1, ignore);
 #pragma unroll
-          for (int np = 0; np < 4; ++np) {
+          for (int i = 0; i < 4 / H; ++i) {
+            const int np = H == 1 ? i : i == 0 ? np0 : np1;
             float x[2][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[0][j] = x[1][j] = 0.f;
 #pragma unroll
-            for (int kt = 0; kt <= np; ++kt) {
+            for (int kt = 0; kt < 4; ++kt) {
+              if (kt > np) continue;
               uint32_t bp[4];
               ldsm4(bp, addr_b<128>(ph, np * 16, 2 * kt, lane));
               mma(x[0], hi[kt], bp[0], bp[1]);
@@ -421,12 +496,13 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               const int n = 2 * np + t;
+              const float* qv = H == 1 ? qs[2 * i + t] : qo[H == 2 ? 2 * i + t : 0];
               const float2 cq = *reinterpret_cast<const float2*>(slot + kVQS * kC + n * 8 + qd * 2);
               const float2 cp = *reinterpret_cast<const float2*>(slot + kVP * kC + n * 8 + qd * 2);
-              x[t][0] = fmaf(cp.x * ui0, x[t][0], cq.x * (qs[n][0] * si0));
-              x[t][1] = fmaf(cp.y * ui0, x[t][1], cq.y * (qs[n][1] * si0));
-              x[t][2] = fmaf(cp.x * ui1, x[t][2], cq.x * (qs[n][2] * si1));
-              x[t][3] = fmaf(cp.y * ui1, x[t][3], cq.y * (qs[n][3] * si1));
+              x[t][0] = fmaf(cp.x * ui0, x[t][0], cq.x * qv[0]);
+              x[t][1] = fmaf(cp.y * ui0, x[t][1], cq.y * qv[1]);
+              x[t][2] = fmaf(cp.x * ui1, x[t][2], cq.x * qv[2]);
+              x[t][3] = fmaf(cp.y * ui1, x[t][3], cq.y * qv[3]);
             }
             if (DT != kF32 && wovec) {
               if constexpr (DT != kF32) {
@@ -449,8 +525,8 @@ __global__ void __launch_bounds__(32 * NW, 1)
             __syncwarp();
             E* op = static_cast<E*>(a.out) + b * a.os[0] + h * a.os[2] + v0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int x = i * 32 + lane, r = x >> 1, pc = x & 1;
+            for (int i = 0; i < 4 / H; ++i) {
+              const int x = (H == 1 ? i : i == 0 ? np0 : np1) * 32 + lane, r = x >> 1, pc = x & 1;
               const uint4 w = lds128(ob + r * 32 + pc * 16);
               if (t0 + r < a.L) *reinterpret_cast<uint4*>(op + (t0 + r) * a.os[1] + pc * 8) = w;
             }
@@ -475,15 +551,15 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
           for (int kt = 0; kt < 4; ++kt) {
             uint32_t bk[2][4];
-            ldsm4t(bk[0], addr_bt<RB>(kt_hi, kt * 16, n4 * 4, lane));
-            ldsm4t(bk[1], addr_bt<RB>(kt_hi, kt * 16, n4 * 4 + 2, lane));
+            ldsm4t(bk[0], addr_bt<RB>(kt_hi, kt * 16, k0 / 8 + n4 * 4, lane));
+            ldsm4t(bk[1], addr_bt<RB>(kt_hi, kt * 16, k0 / 8 + n4 * 4 + 2, lane));
 #pragma unroll
             for (int i = 0; i < 4; ++i) mma(x[i], hi[kt], bk[i >> 1][(i & 1) * 2], bk[i >> 1][(i & 1) * 2 + 1]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) mma(x[i], lo[kt], bk[i >> 1][(i & 1) * 2], bk[i >> 1][(i & 1) * 2 + 1]);
             if constexpr (DT == kF32) {
-              ldsm4t(bk[0], addr_bt<RB>(kt_lo, kt * 16, n4 * 4, lane));
-              ldsm4t(bk[1], addr_bt<RB>(kt_lo, kt * 16, n4 * 4 + 2, lane));
+              ldsm4t(bk[0], addr_bt<RB>(kt_lo, kt * 16, k0 / 8 + n4 * 4, lane));
+              ldsm4t(bk[1], addr_bt<RB>(kt_lo, kt * 16, k0 / 8 + n4 * 4 + 2, lane));
 #pragma unroll
               for (int i = 0; i < 4; ++i) mma(x[i], hi[kt], bk[i >> 1][(i & 1) * 2], bk[i >> 1][(i & 1) * 2 + 1]);
             }
@@ -503,7 +579,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
     if (lane == 0) {
       unsigned n;
       asm volatile("atom.acq_rel.cta.shared.add.u32 %0, [%1], 1;" : "=r"(n) : "r"(smem_u32(&left[s])) : "memory");
-      if (n == NW - 1) {  // every warp has left the stage
+      if (n == C::WARPS - 1) {  // every warp has left the stage
         left[s] = 0;
         if (c + 2 < nc) fill(c + 2);
       }
@@ -514,17 +590,17 @@ __global__ void __launch_bounds__(32 * NW, 1)
     for (int n = 0; n < NK; ++n)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t kd = 8 * n + 2 * qd + (j & 1), vc = v0 + g + (j >> 1) * 8;
+        const int64_t kd = k0 + 8 * n + 2 * qd + (j & 1), vc = v0 + g + (j >> 1) * 8;
         if (kd < a.Dk && vc < a.Dv)
           a.s1[b * a.s1s[0] + h * a.s1s[1] + kd * a.s1s[2] + vc * a.s1s[3]] = st[n][j];
       }
   }
 }
 
-template <int DT, int DK, int NW, bool SAVE>
-cudaError_t launch(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, unsigned* sm, int nc,
+template <int DT, int DK, int NW, int H, bool SAVE>
+cudaError_t launch(const GdrArgs& a, const uint8_t* qk, const uint8_t* pkg, float* sw, float* uw, unsigned* sm, int nc,
                    cudaStream_t s) {
-  using C = ScanCfg<DT, DK, NW, SAVE>;
+  using C = ScanCfg<DT, DK, NW, H, SAVE>;
   static_assert(C::BYTES <= 232448, "shared memory of one block");
   using E = typename Fmt<DT>::E;
   constexpr int64_t V = 16 / sizeof(E);
@@ -532,24 +608,29 @@ cudaError_t launch(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float
     return st[3] == 1 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && st[0] % V == 0 && st[1] % V == 0 && st[2] % V == 0;
   };
   const int vtiles = static_cast<int>((a.Dv + 16 * NW - 1) / (16 * NW));
-  const cudaError_t e = cudaFuncSetAttribute(gdr_scan_kernel<DT, DK, NW, SAVE>,
+  const cudaError_t e = cudaFuncSetAttribute(gdr_scan_kernel<DT, DK, NW, H, SAVE>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e != cudaSuccess) return e;
-  return launch_pdl(gdr_scan_kernel<DT, DK, NW, SAVE>, static_cast<unsigned>(a.B * a.Hv * vtiles), C::THREADS,
-                    C::BYTES, s, a, qk, pk, sw, uw, sm, nc, vtiles, al(a.v, a.vs), !SAVE && al(a.out, a.os));
+  return launch_pdl(gdr_scan_kernel<DT, DK, NW, H, SAVE>, static_cast<unsigned>(a.B * a.Hv * vtiles), 32 * C::WARPS,
+                    C::BYTES, s, a, qk, pkg, sw, uw, sm, nc, vtiles, al(a.v, a.vs), !SAVE && al(a.out, a.os));
 }
 
 template <int DT, int DK, bool SAVE>
-cudaError_t launch_nw(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, unsigned* sm, int nc,
-                      const Device& dev, cudaStream_t s) {
-  // Blocks of few warps while that still puts no more than one on an SM: a
-  // warp alone on its quarter of an SM runs its chain at full rate.
-  const int64_t heads = a.B * a.Hv, groups = (a.Dv + 15) / 16;
-  if (heads * ((groups + 1) / 2) <= dev.sm_count) return launch<DT, DK, 2, SAVE>(a, qk, pk, sw, uw, sm, nc, s);
-  if (DT == kF32 || heads * ((groups + 3) / 4) <= dev.sm_count)
-    return launch<DT, DK, 4, SAVE>(a, qk, pk, sw, uw, sm, nc, s);
-  if constexpr (DT != kF32) return launch<DT, DK, 8, SAVE>(a, qk, pk, sw, uw, sm, nc, s);
-  return cudaErrorInvalidValue;
+cudaError_t launch_nw(const GdrArgs& a, const uint8_t* qk, const uint8_t* pkg, float* sw, float* uw, unsigned* sm,
+                      int nc, const Device& dev, cudaStream_t s) {
+  // Blocks of few channels while that still puts no more than one on an SM.
+  // Two warps a group only where one each would leave half the quarters of an
+  // SM idle (32 heads, 8192 tokens: 537 -> 368 us; with 64 heads, four groups
+  // a block, 119 -> 145 us in the state-keeping scan).
+  const int64_t heads = a.B * a.Hv, groups = (a.Dv + 15) / 16, sms = dev.sm_count;
+  if constexpr (DT == kF32) {  // two terms of k and q: the stages leave room for one warp a group, four groups
+    if (heads * ((groups + 1) / 2) <= sms) return launch<DT, DK, 2, 1, SAVE>(a, qk, pkg, sw, uw, sm, nc, s);
+    return launch<DT, DK, 4, 1, SAVE>(a, qk, pkg, sw, uw, sm, nc, s);
+  } else {
+    if (heads * ((groups + 1) / 2) <= sms) return launch<DT, DK, 2, 2, SAVE>(a, qk, pkg, sw, uw, sm, nc, s);
+    if (heads * ((groups + 3) / 4) <= sms) return launch<DT, DK, 4, 1, SAVE>(a, qk, pkg, sw, uw, sm, nc, s);
+    return launch<DT, DK, 8, 1, SAVE>(a, qk, pkg, sw, uw, sm, nc, s);
+  }
 }
 
 template <int DT, int DK>
