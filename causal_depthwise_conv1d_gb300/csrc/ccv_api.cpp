@@ -240,7 +240,8 @@ ccv_status ccv_device_fault(unsigned* fault_bits) {
   g_last_error.clear();
   if (fault_bits == nullptr) return fail(CCV_ERR_INVALID_ARG, "fault_bits is required");
   const unsigned words[] = {ccv::read_and_clear_fault_chlast_tma(), ccv::read_and_clear_fault_gdr(),
-                            ccv::read_and_clear_fault_gdr_bwd(), ccv::read_and_clear_fault_ln()};
+                            ccv::read_and_clear_fault_gdr_bwd(), ccv::read_and_clear_fault_gdr_grad(),
+                            ccv::read_and_clear_fault_ln()};
   unsigned v = 0;
   for (const unsigned w : words) v |= w;
   if (v == ~0u) return fail(CCV_ERR_CUDA, "cannot read the fault word");

@@ -15,63 +15,112 @@
 // (the row sums of dP P and dL L are dot products of q and k with the products
 // above, so neither matrix is formed again).  A chunk needs nothing of
 // another, so all of them run at once; the value heads that share a key head
-// are summed here one after the other, in registers and in a fixed order.
+// are summed here one after the other, in a fixed order.
+//
+// The scans left their parts as FP16 tiles (hi and lo, every value channel
+// scaled by its own power of two), a slice of 16 channels at a time: a block
+// streams the slices through a ring of bulk copies and does nothing per slice
+// but matrix loads and products.  A slice is one step of 16 of the sum over
+// the channels, so the channels' factors are multiplied into the A operand
+// (powers of two at most 1, relative to the product's largest; what falls
+// below 2^-24 of it is zero), and <S0, D> is the trace of a product.
 //
 // What bounds it: the tensor instructions (about 7400 of 16 x 8 x 16 a chunk
-// and head of 128 x 128, products of two FP32 operands taking three) and the
-// reading of S0 and D.
+// and head of 128 x 128, products of two FP32 operands taking three) at 8
+// cycles each a quarter SM.
 #include "gdr_chunk.cuh"
 
 namespace ccv {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kVB = 64;  // value channels staged at a time
+__device__ unsigned g_fault;
 
-template <int DT, int DK>
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// Products over the value channels, each with its own factors.
+enum { kOS0 = 0, kOS1, kRS0, kRS1, kUD0, kUD1, kSD0, kSD1, kOU, kRU, kProducts };
+
+template <int DT, int DK, bool REP>
 struct Cfg {
   static constexpr int TERMS = DT == kF32 ? 2 : 1;
   static constexpr int TILE = qk_tile_bytes(DK);
   static constexpr int QKB = qk_pack_bytes(DK, TERMS);
-  static constexpr int TOK = kC * kVB * 2;                 // a [64 tokens][64 v] tile
-  static constexpr int ST = DK * kVB * 2;                  // a [DK][64 v] tile
-  static constexpr int BIG = 4 * ST > 8 * kMatBytes ? 4 * ST : 8 * kMatBytes;
-  static constexpr int O_DO = QKB + kVecBytes;
-  static constexpr int O_DR = O_DO + TERMS * TOK;
-  static constexpr int O_U = O_DR + 2 * TOK;
-  static constexpr int O_S = O_U + 2 * TOK;                // S hi, S lo, D hi, D lo; then the four matrices
-  static constexpr int O_F = O_S + BIG;                    // floats
+  static constexpr int STAGE = ImgF::bytes(DK) + ImgB::bytes(DK, TERMS);
+  static constexpr int STAGES = DT == kF32 ? 2 : 3;
+  static constexpr int RING = STAGES * STAGE > 8 * kMatBytes ? STAGES * STAGE : 8 * kMatBytes;  // later: A and B
+  static constexpr int TOTAL = REP ? 2 * kC * DK * 4 : 0;  // dQ and dK of the heads so far
+  static constexpr int O_RING = QKB + kVecBytes;
+  static constexpr int O_TOTAL = O_RING + RING;
+  static constexpr int O_MULT = O_TOTAL + TOTAL;           // half [kProducts][kGdrBwdDv]
+  static constexpr int O_F = O_MULT + kProducts * kGdrBwdDv * 2;
   static constexpr int BYTES = O_F + 1024 * 4;
 };
 
 // Float scratch.
-enum { kFDo = 0, kFDr = 64, kFU = 128, kFVdr = 192, kFPart = 256 /* [2][3][64] */, kFdG = 640, kFRed = 704 /* [2][8] */,
-       kFMax = 720 /* 4 unsigned */, kFCarry = 724 };
+enum { kFVdr = 0, kFPart = 64 /* [2][3][64] */, kFdG = 448, kFRed = 512 /* [2][8] */, kFMax = 528 /* 4 unsigned */,
+       kFRef = 532 /* kProducts ints */, kFBar = 544 /* barriers and counters, 8-byte aligned */ };
 
-template <int DT>
-__device__ __forceinline__ float ld1(const void* p, int64_t off) {
-  return Fmt<DT>::to_f(static_cast<const typename Fmt<DT>::E*>(p)[off]);
+__device__ __forceinline__ uint32_t hmul(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-template <int DT, int DK>
+// An A operand times factors of its summed index: lo for the first eight, hi for the others.
+__device__ __forceinline__ void scaled(uint32_t (&r)[4], const uint32_t (&a)[4], uint32_t m_lo, uint32_t m_hi) {
+  r[0] = hmul(a[0], m_lo);
+  r[1] = hmul(a[1], m_lo);
+  r[2] = hmul(a[2], m_hi);
+  r[3] = hmul(a[3], m_hi);
+}
+
+// d (two column tiles) += (hi + lo of a) (hi + lo of b), without lo lo; LO: a has a lo part.
+template <bool LO>
+__device__ __forceinline__ void mma3(float (*d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
+                                     const uint32_t (&bh)[4], const uint32_t (&bl)[4]) {
+  mma(d[0], ah, bh[0], bh[1]);
+  mma(d[1], ah, bh[2], bh[3]);
+  mma(d[0], ah, bl[0], bl[1]);
+  mma(d[1], ah, bl[2], bl[3]);
+  if constexpr (LO) {
+    mma(d[0], al, bh[0], bh[1]);
+    mma(d[1], al, bh[2], bh[3]);
+  }
+}
+
+// Multiply by 2^e for any int e that a sum of two float exponents can be.
+struct Pow2 {
+  float a, b;
+  __device__ __forceinline__ explicit Pow2(int e) {
+    const int h = e >> 1, r = e - h;
+    a = __uint_as_float(static_cast<unsigned>(max(1, min(254, h + 127))) << 23);
+    b = __uint_as_float(static_cast<unsigned>(max(1, min(254, r + 127))) << 23);
+  }
+  __device__ __forceinline__ float operator()(float x) const { return x * a * b; }
+};
+
+template <int DT, int DK, bool REP>
 __global__ void __launch_bounds__(kThreads, 1)
     gdr_bwd_grad_kernel(const GdrArgs a, const GdrGrads gr, const GdrBwdWs w, int nc) {
   pdl_enter();
-  using C = Cfg<DT, DK>;
+  using C = Cfg<DT, DK, REP>;
   using F = Fmt<DT>;
   using E = typename F::E;
-  constexpr int RB = DK * 2, VRB = kVB * 2;
+  constexpr int RB = DK * 2;
   constexpr int NT = DK / 16;  // column tiles of 8 of one warp (half of DK)
+  constexpr bool OLO = DT == kF32;
   extern __shared__ __align__(128) uint8_t sm[];
   float* fs = reinterpret_cast<float*>(sm + C::O_F);
+  uint64_t* full = reinterpret_cast<uint64_t*>(fs + kFBar);
+  unsigned* left = reinterpret_cast<unsigned*>(full + C::STAGES);
+  int* ref = reinterpret_cast<int*>(fs + kFRef);
+  uint16_t* mult = reinterpret_cast<uint16_t*>(sm + C::O_MULT);
   const float* vecs = reinterpret_cast<const float*>(sm + C::QKB);
   const float* slot = vecs + kVecHead;
   const int* seg = reinterpret_cast<const int*>(slot + kVSeg * kC);
   const uint32_t base = smem_u32(sm);
   const uint32_t kt_hi = base, kt_lo = base + C::TILE, qt_hi = base + C::TERMS * C::TILE, qt_lo = qt_hi + C::TILE;
-  const uint32_t do_hi = base + C::O_DO, do_lo = do_hi + C::TOK, dr_hi = base + C::O_DR, dr_lo = dr_hi + C::TOK;
-  const uint32_t u_hi = base + C::O_U, u_lo = u_hi + C::TOK;
-  const uint32_t s_hi = base + C::O_S, s_lo = s_hi + C::ST, d_hi = s_lo + C::ST, d_lo = d_hi + C::ST;
+  const uint32_t mats = base + C::O_RING;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, qd = lane & 3;
@@ -83,60 +132,79 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t t0 = c * kC;
   const int nt = static_cast<int>(a.L - t0 < kC ? a.L - t0 : kC);
   const int64_t rep = a.Hv / a.Hk;
-  const int64_t dvp = (a.Dv + 15) / 16 * 16;
+  const int ns = static_cast<int>((a.Dv + 15) / 16);
+  constexpr int BF = ImgF::bytes(DK), BB = ImgB::bytes(DK, C::TERMS);
 
+  int64_t ch = (b * a.Hv + hk * rep) * nc + c;
+  auto fill = [&](int sl, int n) {  // slice sl as the block's n-th copy
+    uint8_t* dst = sm + C::O_RING + (n % C::STAGES) * C::STAGE;
+    uint64_t* bar = &full[n % C::STAGES];
+    mbar_arrive_expect_tx(bar, C::STAGE);
+    bulk_load(dst, w.img_f + (ch * ns + sl) * BF, BF, bar);
+    bulk_load(dst + BF, w.img_b + (ch * ns + sl) * BB, BB, bar);
+  };
+  if (tid == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      left[s] = 0;
+    }
+    fence_barrier_init();
+  }
   {  // k and q tiles
     const uint4* src = reinterpret_cast<const uint4*>(w.qk + id * C::QKB);
     uint4* dst = reinterpret_cast<uint4*>(sm);
 #pragma unroll 8
     for (int i = tid; i < C::QKB / 16; i += kThreads) dst[i] = src[i];
   }
-  float tq[NT][4], tk[NT][4];  // sums over the value heads
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) tq[n][j] = tk[n][j] = 0.f;
+  float4* total = reinterpret_cast<float4*>(sm + C::O_TOTAL);  // this thread's tiles at [tile][tid]
+  int n_copy = 0;  // copies consumed so far
 
-  for (int64_t r = 0; r < rep; ++r) {
-    const int64_t h = hk * rep + r, bh = b * a.Hv + h, ch = bh * nc + c;
-    const float* sw = w.s + ch * DK * dvp;
-    const float* dw = w.d + ch * DK * dvp;
-    const float* uw = w.u + ch * kC * dvp;
-    const float* rw = w.r + ch * kC * dvp;
-    const int64_t go = b * gr.dos[0] + t0 * gr.dos[1] + h * gr.dos[2];
-    const int64_t vo = b * a.vs[0] + t0 * a.vs[1] + h * a.vs[2];
-    __syncthreads();
+  for (int64_t r = 0; r < rep; ++r, ch += nc) {
+    const int64_t h = hk * rep + r;
+    const uint8_t* imf = w.img_f + ch * ns * BF;
+    const uint8_t* imb = w.img_b + ch * ns * BB;
+    __syncthreads();  // the last head's matrices, factors and sums have been read
+    if (tid == 0) {
+      fence_proxy_async_smem();  // the ring held matrices written by threads
+      for (int sl = 0; sl < C::STAGES && sl < ns; ++sl) fill(sl, n_copy + sl);
+    }
     reinterpret_cast<uint4*>(sm + C::QKB)[tid] = reinterpret_cast<const uint4*>(w.pack + ch * kPackBytes)[tid];
     if (tid < 4) reinterpret_cast<unsigned*>(fs + kFMax)[tid] = 0;
-    // row factors of dO, dR and U over all value channels, and dR.v
-    float fdo[8], fdr[8], fu[8];
-#pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
-      const int row = warp * 8 + i;
-      unsigned mo = 0, mr = 0, mu = 0;
-      float vd = 0.f;
-      for (int64_t v = lane; v < dvp; v += 32) {
-        const float x = rw[row * dvp + v];
-        mr = max(mr, mag(x));
-        mu = max(mu, mag(uw[row * dvp + v]));
-        if (row < nt && v < a.Dv) {
-          mo = max(mo, mag(ld1<DT>(gr.dout, go + row * gr.dos[1] + v * gr.dos[3])));
-          vd = fmaf(x, ld1<DT>(a.v, vo + row * a.vs[1] + v * a.vs[3]), vd);
-        }
-      }
-#pragma unroll
-      for (int m = 16; m > 0; m >>= 1) vd += __shfl_xor_sync(kFullMask, vd, m);
-      float io, ir, iu;
-      row_factor(warp_max(mo), fdo[i], io);
-      row_factor(warp_max(mr), fdr[i], ir);
-      row_factor(warp_max(mu), fu[i], iu);
-      if (lane == 0) fs[kFDo + row] = io, fs[kFDr + row] = ir, fs[kFU + row] = iu, fs[kFVdr + row] = vd;
+    if (tid < kProducts) ref[tid] = -1000;
+    if (tid < kC) {  // dR.v: the slices in order
+      float x = 0.f;
+      for (int sl = 0; sl < ns; ++sl) x += reinterpret_cast<const float*>(imb + sl * BB + ImgB::inv(DK, C::TERMS))[64 + tid];
+      fs[kFVdr + tid] = x;
     }
-    float f_s, i_s, f_d, i_d;
-    row_factor(w.s_max[ch], f_s, i_s);
-    row_factor(w.d_max[ch], f_d, i_d);
+    __syncthreads();
+    // exponents of the channels' factors; each product's largest
+    for (int v = tid; v < (ns * 16 + 31) / 32 * 32; v += kThreads) {
+      int e[kProducts];
+      const bool in = v < ns * 16;
+      const float* pf = reinterpret_cast<const float*>(imf + (in ? v >> 4 : 0) * BF + ImgF::inv(DK)) + (v & 15);
+      const float* pb = reinterpret_cast<const float*>(imb + (in ? v >> 4 : 0) * BB + ImgB::inv(DK, C::TERMS)) + (v & 15);
+      auto ex = [](float x) { return static_cast<int>(__float_as_uint(x) >> 23) - 127; };
+      const int s0 = ex(pf[0]), s1 = ex(pf[16]), u = ex(pf[32]), d0 = ex(pb[0]), d1 = ex(pb[16]), rr = ex(pb[32]),
+                o = ex(pb[48]);
+      e[kOS0] = o + s0, e[kOS1] = o + s1, e[kRS0] = rr + s0, e[kRS1] = rr + s1, e[kUD0] = u + d0, e[kUD1] = u + d1;
+      e[kSD0] = s0 + d0, e[kSD1] = s1 + d1, e[kOU] = o + u, e[kRU] = rr + u;
+#pragma unroll
+      for (int p = 0; p < kProducts; ++p) {
+        const int m = __reduce_max_sync(kFullMask, in ? e[p] : -1000);
+        if (lane == 0) atomicMax(&ref[p], m);
+        // kept as a biased exponent until the largest is known
+        if (in) mult[p * kGdrBwdDv + v] = static_cast<uint16_t>(e[p] + 1000);
+      }
+    }
+    __syncthreads();
+    for (int x = tid; x < kProducts * ns * 16; x += kThreads) {
+      const int p = x / (ns * 16), v = x - p * (ns * 16);
+      const int d = static_cast<int>(mult[p * kGdrBwdDv + v]) - 1000 - ref[p];
+      mult[p * kGdrBwdDv + v] = d >= -14 ? (d + 15) << 10 : d >= -24 ? 1 << (d + 24) : 0;
+    }
+    __syncthreads();
 
-    float dq[NT][4], z[NT][4], dk[NT][4], dp[4][4], dl[4][4];
+    float dq[NT][4], z[NT][4], dk[NT][4], dp[4][4], dl[4][4], tr[2][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -145,120 +213,98 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; n < 4; ++n)
 #pragma unroll
       for (int j = 0; j < 4; ++j) dp[n][j] = dl[n][j] = 0.f;
-    float sd = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) tr[0][j] = tr[1][j] = 0.f;
 
-    for (int64_t v0 = 0; v0 < dvp; v0 += kVB) {
-      __syncthreads();
-      // token tiles: a warp's eight rows, two channels a lane
-#pragma unroll 4
-      for (int i = 0; i < 8; ++i) {
-        const int row = warp * 8 + i;
-        const int64_t v = v0 + 2 * lane;
-        float2 x = make_float2(0.f, 0.f), y = x, o = x;
-        if (v < dvp) {
-          x = *reinterpret_cast<const float2*>(rw + row * dvp + v);
-          y = *reinterpret_cast<const float2*>(uw + row * dvp + v);
+    for (int sl = 0; sl < ns; ++sl, ++n_copy) {
+      const int s = n_copy % C::STAGES;
+      if (!mbar_wait(&full[s], (n_copy / C::STAGES) & 1)) {
+        // give up: wait for the copies still in flight as well
+        if (lane == 0) {
+          atomicOr(&g_fault, kFaultConsumerWait);
+          for (int k = 1; k < C::STAGES && sl + k < ns; ++k)
+            mbar_wait(&full[(n_copy + k) % C::STAGES], ((n_copy + k) / C::STAGES) & 1);
         }
-        if (row < nt) {
-          if (v < a.Dv) o.x = ld1<DT>(gr.dout, go + row * gr.dos[1] + v * gr.dos[3]);
-          if (v + 1 < a.Dv) o.y = ld1<DT>(gr.dout, go + row * gr.dos[1] + (v + 1) * gr.dos[3]);
-        }
-        const uint32_t off = tile_off<VRB>(row, lane >> 2) + (lane & 3) * 4;
-        uint32_t hi, lo;
-        split2(x.x * fdr[i], x.y * fdr[i], hi, lo);
-        *reinterpret_cast<uint32_t*>(sm + C::O_DR + off) = hi;
-        *reinterpret_cast<uint32_t*>(sm + C::O_DR + C::TOK + off) = lo;
-        split2(y.x * fu[i], y.y * fu[i], hi, lo);
-        *reinterpret_cast<uint32_t*>(sm + C::O_U + off) = hi;
-        *reinterpret_cast<uint32_t*>(sm + C::O_U + C::TOK + off) = lo;
-        split2(o.x * fdo[i], o.y * fdo[i], hi, lo);
-        *reinterpret_cast<uint32_t*>(sm + C::O_DO + off) = hi;
-        if constexpr (DT == kF32) *reinterpret_cast<uint32_t*>(sm + C::O_DO + C::TOK + off) = lo;
+        return;
       }
-      // S0 and D
-#pragma unroll 4
-      for (int x = tid; x < DK * (kVB / 4); x += kThreads) {
-        const int row = x / (kVB / 4), q4 = x % (kVB / 4);
-        const int64_t v = v0 + 4 * q4;
-        float4 p = make_float4(0.f, 0.f, 0.f, 0.f), q = p;
-        if (v < dvp) {
-          p = *reinterpret_cast<const float4*>(sw + row * dvp + v);
-          q = *reinterpret_cast<const float4*>(dw + row * dvp + v);
-        }
-        sd = fmaf(p.x, q.x, fmaf(p.y, q.y, fmaf(p.z, q.z, fmaf(p.w, q.w, sd))));
-        const uint32_t off = tile_off<VRB>(row, q4 >> 1) + (q4 & 1) * 8;
-        uint2 hi, lo;
-        split2(p.x * f_s, p.y * f_s, hi.x, lo.x);
-        split2(p.z * f_s, p.w * f_s, hi.y, lo.y);
-        *reinterpret_cast<uint2*>(sm + C::O_S + off) = hi;
-        *reinterpret_cast<uint2*>(sm + C::O_S + C::ST + off) = lo;
-        split2(q.x * f_d, q.y * f_d, hi.x, lo.x);
-        split2(q.z * f_d, q.w * f_d, hi.y, lo.y);
-        *reinterpret_cast<uint2*>(sm + C::O_S + 2 * C::ST + off) = hi;
-        *reinterpret_cast<uint2*>(sm + C::O_S + 3 * C::ST + off) = lo;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int kt = 0; kt < kVB / 16; ++kt) {
-        uint32_t oh[4], ol[4], rh[4], rl[4], uh[4], ul[4];
-        ldsm4(oh, addr_a<VRB>(do_hi, wr * 16, 2 * kt, lane));
-        if constexpr (DT == kF32) ldsm4(ol, addr_a<VRB>(do_lo, wr * 16, 2 * kt, lane));
-        ldsm4(rh, addr_a<VRB>(dr_hi, wr * 16, 2 * kt, lane));
-        ldsm4(rl, addr_a<VRB>(dr_lo, wr * 16, 2 * kt, lane));
-        ldsm4(uh, addr_a<VRB>(u_hi, wr * 16, 2 * kt, lane));
-        ldsm4(ul, addr_a<VRB>(u_lo, wr * 16, 2 * kt, lane));
-#pragma unroll
-        for (int np = 0; np < NT / 2; ++np) {
-          const int n0 = wc * (DK / 2) + np * 16;
-          uint32_t bh_[4], bl_[4];
-          ldsm4(bh_, addr_b<VRB>(s_hi, n0, 2 * kt, lane));
-          ldsm4(bl_, addr_b<VRB>(s_lo, n0, 2 * kt, lane));
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            mma(dq[2 * np + t], oh, bh_[2 * t], bh_[2 * t + 1]);
-            mma(z[2 * np + t], rh, bh_[2 * t], bh_[2 * t + 1]);
-          }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            mma(dq[2 * np + t], oh, bl_[2 * t], bl_[2 * t + 1]);
-            mma(z[2 * np + t], rh, bl_[2 * t], bl_[2 * t + 1]);
-          }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            mma(z[2 * np + t], rl, bh_[2 * t], bh_[2 * t + 1]);
-            if constexpr (DT == kF32) mma(dq[2 * np + t], ol, bh_[2 * t], bh_[2 * t + 1]);
-          }
-          ldsm4(bh_, addr_b<VRB>(d_hi, n0, 2 * kt, lane));
-          ldsm4(bl_, addr_b<VRB>(d_lo, n0, 2 * kt, lane));
-#pragma unroll
-          for (int t = 0; t < 2; ++t) mma(dk[2 * np + t], uh, bh_[2 * t], bh_[2 * t + 1]);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) mma(dk[2 * np + t], uh, bl_[2 * t], bl_[2 * t + 1]);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) mma(dk[2 * np + t], ul, bh_[2 * t], bh_[2 * t + 1]);
-        }
+      const uint32_t f0 = base + C::O_RING + s * C::STAGE, b0 = f0 + BF;
+      const uint32_t s_hi = f0, s_lo = s_hi + img_state_bytes(DK), u_hi = f0 + ImgF::u(DK), u_lo = u_hi + kTokBytes;
+      const uint32_t d_hi = b0, d_lo = d_hi + img_state_bytes(DK), r_hi = b0 + ImgB::r(DK), r_lo = r_hi + kTokBytes;
+      const uint32_t o_hi = b0 + ImgB::o(DK), o_lo = o_hi + kTokBytes;
+      auto factors = [&](int p, uint32_t& lo, uint32_t& hi) {
+        const uint32_t* m = reinterpret_cast<const uint32_t*>(mult + p * kGdrBwdDv + sl * 16);
+        lo = m[qd];
+        hi = m[4 + qd];
+      };
+      const uint32_t at = off32(wr * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
+      uint32_t oh[4], ol[4], rh[4], rl[4], m0, m1;
+      ldsm4(oh, o_hi + at);
+      if constexpr (OLO) ldsm4(ol, o_lo + at);
+      ldsm4(rh, r_hi + at);
+      ldsm4(rl, r_lo + at);
+      if (wc * 2 <= wr) {  // dO U^T and dR U^T, the column tiles up to the diagonal
+        uint32_t xo[4], xl[4], yh[4], yl[4];
+        factors(kOU, m0, m1);
+        scaled(xo, oh, m0, m1);
+        if constexpr (OLO) scaled(xl, ol, m0, m1);
+        factors(kRU, m0, m1);
+        scaled(yh, rh, m0, m1);
+        scaled(yl, rl, m0, m1);
 #pragma unroll
         for (int np = 0; np < 2; ++np) {
-          const int n0 = wc * 32 + np * 16;
-          if (n0 > wr * 16 + 15) continue;
-          uint32_t bh_[4], bl_[4];
-          ldsm4(bh_, addr_b<VRB>(u_hi, n0, 2 * kt, lane));
-          ldsm4(bl_, addr_b<VRB>(u_lo, n0, 2 * kt, lane));
+          if (wc * 2 + np > wr) continue;
+          uint32_t bh[4], bl[4];
+          const uint32_t bt = off32(wc * 32 + np * 16 + (lane & 7) + ((lane >> 4) & 1) * 8, (lane >> 3) & 1);
+          ldsm4(bh, u_hi + bt);
+          ldsm4(bl, u_lo + bt);
+          mma3<OLO>(&dp[2 * np], xo, xl, bh, bl);
+          mma3<true>(&dl[2 * np], yh, yl, bh, bl);
+        }
+      }
+      uint32_t uh[4], ul[4];
+      ldsm4(uh, u_hi + at);
+      ldsm4(ul, u_lo + at);
+      factors(kOS0 + wc, m0, m1);
+      scaled(oh, oh, m0, m1);
+      if constexpr (OLO) scaled(ol, ol, m0, m1);
+      factors(kRS0 + wc, m0, m1);
+      scaled(rh, rh, m0, m1);
+      scaled(rl, rl, m0, m1);
+      factors(kUD0 + wc, m0, m1);
+      scaled(uh, uh, m0, m1);
+      scaled(ul, ul, m0, m1);
+      const int rowt = (lane & 7) + ((lane >> 3) & 1) * 8, pct = lane >> 4;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            mma(dp[2 * np + t], oh, bh_[2 * t], bh_[2 * t + 1]);
-            mma(dl[2 * np + t], rh, bh_[2 * t], bh_[2 * t + 1]);
-          }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            mma(dp[2 * np + t], oh, bl_[2 * t], bl_[2 * t + 1]);
-            mma(dl[2 * np + t], rh, bl_[2 * t], bl_[2 * t + 1]);
-          }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            mma(dl[2 * np + t], rl, bh_[2 * t], bh_[2 * t + 1]);
-            if constexpr (DT == kF32) mma(dp[2 * np + t], ol, bh_[2 * t], bh_[2 * t + 1]);
-          }
+      for (int np = 0; np < NT / 2; ++np) {
+        const int n0 = wc * (DK / 2) + np * 16;
+        const uint32_t bt = (n0 >> 5) * kBlkBytes + off64(rowt, ((n0 & 31) >> 3) + pct);
+        uint32_t bh[4], bl[4];
+        ldsm4t(bh, s_hi + bt);
+        ldsm4t(bl, s_lo + bt);
+        mma3<OLO>(&dq[2 * np], oh, ol, bh, bl);
+        mma3<true>(&z[2 * np], rh, rl, bh, bl);
+        if (np == wr) {  // <S0, D>: each warp's row group takes one tile pair; the diagonal of D S0^T
+          uint32_t ah[4], al[4];
+          const uint32_t tt = (n0 >> 5) * kBlkBytes +
+                              off64((lane & 7) + ((lane >> 4) & 1) * 8, ((n0 & 31) >> 3) + ((lane >> 3) & 1));
+          ldsm4t(ah, d_hi + tt);
+          ldsm4t(al, d_lo + tt);
+          factors(kSD0 + wc, m0, m1);
+          scaled(ah, ah, m0, m1);
+          scaled(al, al, m0, m1);
+          mma3<true>(tr, ah, al, bh, bl);
+        }
+        ldsm4t(bh, d_hi + bt);
+        ldsm4t(bl, d_lo + bt);
+        mma3<true>(&dk[2 * np], uh, ul, bh, bl);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        unsigned n;
+        asm volatile("atom.acq_rel.cta.shared.add.u32 %0, [%1], 1;" : "=r"(n) : "r"(smem_u32(&left[s])) : "memory");
+        if (n == kWarps - 1) {  // every warp has left the stage
+          left[s] = 0;
+          if (sl + C::STAGES < ns) fill(sl + C::STAGES, n_copy + C::STAGES);
         }
       }
     }
@@ -269,36 +315,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
       const float gi0 = slot[kVGi * kC + i0], gi1 = slot[kVGi * kC + i1];
       const float gc0 = slot[kVGc * kC + i0], gc1 = slot[kVGc * kC + i1];
-      const float q0 = a.scale * gi0 * (fs[kFDo + i0] * i_s), q1 = a.scale * gi1 * (fs[kFDo + i1] * i_s);
-      const float z0 = -gi0 * (fs[kFDr + i0] * i_s), z1 = -gi1 * (fs[kFDr + i1] * i_s);
-      const float k0 = gc0 * (fs[kFU + i0] * i_d), k1 = gc1 * (fs[kFU + i1] * i_d);
+      const Pow2 po(ref[kOS0 + wc]), pr(ref[kRS0 + wc]), pd(ref[kUD0 + wc]);
+      const float q0 = a.scale * gi0, q1 = a.scale * gi1;
       const float ki0 = slot[kVKInv * kC + i0], ki1 = slot[kVKInv * kC + i1];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // factors of zero (another sequence) select
-          dq[n][j] = (j < 2 ? gi0 : gi1) == 0.f ? 0.f : dq[n][j] * (j < 2 ? q0 : q1);
-          z[n][j] = (j < 2 ? gi0 : gi1) == 0.f ? 0.f : z[n][j] * (j < 2 ? z0 : z1);
-          dk[n][j] = (j < 2 ? gc0 : gc1) == 0.f ? 0.f : dk[n][j] * (j < 2 ? k0 : k1);
-        }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int col = wc * (DK / 2) + n * 8 + qd * 2;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int row = e ? i1 : i0;
-          const float ki = e ? ki1 : ki0;
-          const uint32_t off = tile_off<RB>(row, col >> 3) + (col & 7) * 2;
+          const float gi = e ? gi1 : gi0, gc = e ? gc1 : gc0, qf = e ? q1 : q0;
+          const uint32_t off = tile_off<RB>(e ? i1 : i0, col >> 3) + (col & 7) * 2;
           float2 k2 = __half22float2(*reinterpret_cast<const __half2*>(sm + off));
           if constexpr (DT == kF32) {
             const float2 l2 = __half22float2(*reinterpret_cast<const __half2*>(sm + C::TILE + off));
             k2.x += l2.x, k2.y += l2.y;
           }
-          klast = fmaf(k2.x * ki, dk[n][2 * e], fmaf(k2.y * ki, dk[n][2 * e + 1], klast));
+          float part = 0.f;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int j = 2 * e + x;
+            // factors of zero (another sequence) select
+            dq[n][j] = gi == 0.f ? 0.f : po(dq[n][j]) * qf;
+            z[n][j] = gi == 0.f ? 0.f : -(pr(z[n][j]) * gi);
+            dk[n][j] = gc == 0.f ? 0.f : pd(dk[n][j]) * gc;
+            part = fmaf(x ? k2.y : k2.x, dk[n][j], part);
+          }
+          klast = fmaf(e ? ki1 : ki0, part, klast);
         }
       }
     }
+    // the diagonal of tr: row g (g + 8) of tile 0 (1) is column 2 qd + e
+    float sd = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (2 * qd + e == g) sd += tr[0][e] + tr[1][2 + e];
+    sd = Pow2(ref[kSD0 + wc])(sd);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) {
       klast += __shfl_xor_sync(kFullMask, klast, m);
@@ -307,62 +358,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) fs[kFRed + warp] = klast, fs[kFRed + 8 + warp] = sd;
 
     // A and B with the factors of the products they enter; one power of two a matrix
-    unsigned mx[4] = {0, 0, 0, 0};
+    float mx[4] = {0.f, 0.f, 0.f, 0.f};
     {
       const float gh0 = slot[kVGHi * kC + i0], gl0 = slot[kVGLo * kC + i0];
       const float gh1 = slot[kVGHi * kC + i1], gl1 = slot[kVGLo * kC + i1];
       const int s0 = seg[i0], s1 = seg[i1];
-      const float po0 = a.scale * fs[kFDo + i0], po1 = a.scale * fs[kFDo + i1];
-      const float ro0 = -fs[kFDr + i0], ro1 = -fs[kFDr + i1];
+      const Pow2 pu(ref[kOU]), pr(ref[kRU]);
       const float qi0 = slot[kVQInv * kC + i0], qi1 = slot[kVQInv * kC + i1];
       const float bk0 = be0 * slot[kVKInv * kC + i0], bk1 = be1 * slot[kVKInv * kC + i1];
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int n = 0; n < 4; ++n) {
+        const int j0 = wc * 32 + n * 8 + qd * 2;
+        const float2 gj = *reinterpret_cast<const float2*>(slot + kVGHi * kC + j0);
+        const float2 lj = *reinterpret_cast<const float2*>(slot + kVGLo * kC + j0);
+        const float2 kj = *reinterpret_cast<const float2*>(slot + kVKInv * kC + j0);
+        const int2 sj = *reinterpret_cast<const int2*>(seg + j0);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int j = wc * 32 + n * 8 + qd * 2 + (e & 1);
-          const int i = e < 2 ? i0 : i1;
-          const bool in = j <= i && seg[j] == (e < 2 ? s0 : s1);
-          const float ju = fs[kFU + j];
-          const float gam = in ? ex2_approx(((e < 2 ? gh0 : gh1) - slot[kVGHi * kC + j]) +
-                                      ((e < 2 ? gl0 : gl1) - slot[kVGLo * kC + j]))
-                               : 0.f;
-          dp[n][e] = in ? dp[n][e] * ((e < 2 ? po0 : po1) * ju) * gam : 0.f;
-          dl[n][e] = in && j < i ? dl[n][e] * ((e < 2 ? ro0 : ro1) * ju) * gam : 0.f;
-          const float kj = slot[kVKInv * kC + j];
-          mx[0] = max(mx[0], mag(dp[n][e] * kj));
-          mx[1] = max(mx[1], mag(dp[n][e] * (e < 2 ? qi0 : qi1)));
-          mx[2] = max(mx[2], mag(dl[n][e] * kj));
-          mx[3] = max(mx[3], mag(dl[n][e] * (e < 2 ? bk0 : bk1)));
+          const int j = j0 + (e & 1), i = e < 2 ? i0 : i1;
+          const bool in = j <= i && ((e & 1) ? sj.y : sj.x) == (e < 2 ? s0 : s1);
+          const float gam = ex2_approx(((e < 2 ? gh0 : gh1) - ((e & 1) ? gj.y : gj.x)) +
+                                       ((e < 2 ? gl0 : gl1) - ((e & 1) ? lj.y : lj.x)));
+          dp[n][e] = in ? pu(dp[n][e]) * (a.scale * gam) : 0.f;
+          dl[n][e] = in && j < i ? -(pr(dl[n][e]) * gam) : 0.f;
         }
+        mx[0] = amax3(amax3(mx[0], dp[n][0] * kj.x, dp[n][1] * kj.y), dp[n][2] * kj.x, dp[n][3] * kj.y);
+        mx[1] = amax3(amax3(mx[1], dp[n][0] * qi0, dp[n][1] * qi0), dp[n][2] * qi1, dp[n][3] * qi1);
+        mx[2] = amax3(amax3(mx[2], dl[n][0] * kj.x, dl[n][1] * kj.y), dl[n][2] * kj.x, dl[n][3] * kj.y);
+        mx[3] = amax3(amax3(mx[3], dl[n][0] * bk0, dl[n][1] * bk0), dl[n][2] * bk1, dl[n][3] * bk1);
+      }
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        mx[m] = warp_max(mx[m]);
-        if (lane == 0) atomicMax(reinterpret_cast<unsigned*>(fs + kFMax) + m, mx[m]);
+        const unsigned x = warp_max(__float_as_uint(mx[m]));
+        if (lane == 0) atomicMax(reinterpret_cast<unsigned*>(fs + kFMax) + m, x);
       }
-      __syncthreads();  // also: every warp is done with S0 and D
+      __syncthreads();  // also: every warp is done with the ring
       float f[4], inv[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) row_factor(reinterpret_cast<const unsigned*>(fs + kFMax)[m], f[m], inv[m]);
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         const int col = wc * 32 + n * 8 + qd * 2;
-        const float kj0 = slot[kVKInv * kC + col], kj1 = slot[kVKInv * kC + col + 1];
+        const float2 kj = *reinterpret_cast<const float2*>(slot + kVKInv * kC + col);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint32_t off = tile_off<128>(e ? i1 : i0, col >> 3) + (col & 7) * 2;
           const float qi = e ? qi1 : qi0, bk = e ? bk1 : bk0;
           const float p0 = dp[n][2 * e], p1 = dp[n][2 * e + 1], l0 = dl[n][2 * e], l1 = dl[n][2 * e + 1];
-          const float x[4][2] = {{p0 * kj0 * f[0], p1 * kj1 * f[0]},
-                                 {p0 * qi * f[1], p1 * qi * f[1]},
-                                 {l0 * kj0 * f[2], l1 * kj1 * f[2]},
-                                 {l0 * bk * f[3], l1 * bk * f[3]}};
+          const float x[4][2] = {{p0 * kj.x, p1 * kj.y}, {p0 * qi, p1 * qi}, {l0 * kj.x, l1 * kj.y}, {l0 * bk, l1 * bk}};
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             uint32_t hi, lo;
-            split2(x[m][0], x[m][1], hi, lo);
-            *reinterpret_cast<uint32_t*>(sm + C::O_S + 2 * m * kMatBytes + off) = hi;
-            *reinterpret_cast<uint32_t*>(sm + C::O_S + (2 * m + 1) * kMatBytes + off) = lo;
+            split2f(x[m][0], x[m][1], pk(f[m], f[m]), hi, lo);
+            *reinterpret_cast<uint32_t*>(sm + C::O_RING + 2 * m * kMatBytes + off) = hi;
+            *reinterpret_cast<uint32_t*>(sm + C::O_RING + (2 * m + 1) * kMatBytes + off) = lo;
           }
         }
       }
@@ -370,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // products over the chunk's tokens
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const uint32_t mh = s_hi + 2 * m * kMatBytes, ml = mh + kMatBytes;
+        const uint32_t mh = mats + 2 * m * kMatBytes, ml = mh + kMatBytes;
         const uint32_t bh_t = m == 1 ? qt_hi : kt_hi, bl_t = m == 1 ? qt_lo : kt_lo;
         uint32_t ah[4][4], al[4][4];
 #pragma unroll
@@ -423,15 +472,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
 
-    // dK complete; dot products of each token's rows; sums over the heads
+    // dK complete; dot products of each token's rows
     float dots[3][2] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int col = wc * (DK / 2) + n * 8 + qd * 2;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int row = e ? i1 : i0;
-        const uint32_t off = tile_off<RB>(row, col >> 3) + (col & 7) * 2;
+        const uint32_t off = tile_off<RB>(e ? i1 : i0, col >> 3) + (col & 7) * 2;
         float2 k2 = __half22float2(*reinterpret_cast<const __half2*>(sm + off));
         float2 q2 = __half22float2(*reinterpret_cast<const __half2*>(sm + C::TERMS * C::TILE + off));
         if constexpr (DT == kF32) {
@@ -448,8 +496,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           dots[0][e] = fmaf(qv, dq[n][j], dots[0][e]);
           dots[1][e] = fmaf(kv, dk[n][j], dots[1][e]);
           dots[2][e] = fmaf(kv, z[n][j], dots[2][e]);
-          tq[n][j] += dq[n][j];
-          tk[n][j] += dk[n][j];
         }
       }
     }
@@ -462,6 +508,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         x += __shfl_xor_sync(kFullMask, x, 2);
         if (qd == 0) fs[kFPart + (wc * 3 + d) * kC + (e ? i1 : i0)] = x;
       }
+    // sums over the heads, and out with the last
+    if constexpr (REP) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (r > 0) {
+          const float4 x = total[n * kThreads + tid], y = total[(NT + n) * kThreads + tid];
+          dq[n][0] += x.x, dq[n][1] += x.y, dq[n][2] += x.z, dq[n][3] += x.w;
+          dk[n][0] += y.x, dk[n][1] += y.y, dk[n][2] += y.z, dk[n][3] += y.w;
+        }
+        if (r + 1 < rep) {
+          total[n * kThreads + tid] = make_float4(dq[n][0], dq[n][1], dq[n][2], dq[n][3]);
+          total[(NT + n) * kThreads + tid] = make_float4(dk[n][0], dk[n][1], dk[n][2], dk[n][3]);
+        }
+      }
+    }
+    if (r + 1 == rep) {
+      E* qo = static_cast<E*>(gr.dq) + b * gr.dqs[0] + hk * gr.dqs[2];
+      E* ko = static_cast<E*>(gr.dk) + b * gr.dks[0] + hk * gr.dks[2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int col = wc * (DK / 2) + n * 8 + qd * 2 + (j & 1), row = j < 2 ? i0 : i1;
+          if (row < nt && col < a.Dk) {
+            qo[(t0 + row) * gr.dqs[1] + col * gr.dqs[3]] = F::from_f(dq[n][j]);
+            ko[(t0 + row) * gr.dks[1] + col * gr.dks[3]] = F::from_f(dk[n][j]);
+          }
+        }
+    }
     __syncthreads();
     if (tid < kC) {
       const int i = tid;
@@ -501,35 +576,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       gr.dg[b * gr.dgs[0] + t * gr.dgs[1] + h * gr.dgs[2]] = first ? 0.f : x;
     }
   }
-
-  E* qo = static_cast<E*>(gr.dq) + b * gr.dqs[0] + hk * gr.dqs[2];
-  E* ko = static_cast<E*>(gr.dk) + b * gr.dks[0] + hk * gr.dks[2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int col = wc * (DK / 2) + n * 8 + qd * 2 + (j & 1), row = j < 2 ? i0 : i1;
-      if (row < nt && col < a.Dk) {
-        qo[(t0 + row) * gr.dqs[1] + col * gr.dqs[3]] = F::from_f(tq[n][j]);
-        ko[(t0 + row) * gr.dks[1] + col * gr.dks[3]] = F::from_f(tk[n][j]);
-      }
-    }
 }
 
-template <int DT, int DK>
+template <int DT, int DK, bool REP>
 cudaError_t launch(const GdrArgs& a, const GdrGrads& g, const GdrBwdWs& w, int nc, cudaStream_t s) {
-  using C = Cfg<DT, DK>;
+  using C = Cfg<DT, DK, REP>;
   static_assert(C::BYTES <= 232448, "shared memory of one block");
   const cudaError_t e =
-      cudaFuncSetAttribute(gdr_bwd_grad_kernel<DT, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+      cudaFuncSetAttribute(gdr_bwd_grad_kernel<DT, DK, REP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e != cudaSuccess) return e;
-  return launch_pdl(gdr_bwd_grad_kernel<DT, DK>, static_cast<unsigned>(a.B * a.Hk * nc), kThreads, C::BYTES, s, a, g,
-                    w, nc);
+  return launch_pdl(gdr_bwd_grad_kernel<DT, DK, REP>, static_cast<unsigned>(a.B * a.Hk * nc), kThreads, C::BYTES, s, a,
+                    g, w, nc);
 }
 
 template <int DT>
 cudaError_t launch_dt(const GdrArgs& a, const GdrGrads& g, const GdrBwdWs& w, int nc, cudaStream_t s) {
-  return a.Dk <= 64 ? launch<DT, 64>(a, g, w, nc, s) : launch<DT, 128>(a, g, w, nc, s);
+  if (a.Hv == a.Hk) return a.Dk <= 64 ? launch<DT, 64, false>(a, g, w, nc, s) : launch<DT, 128, false>(a, g, w, nc, s);
+  return a.Dk <= 64 ? launch<DT, 64, true>(a, g, w, nc, s) : launch<DT, 128, true>(a, g, w, nc, s);
 }
 
 }  // namespace
@@ -542,6 +605,17 @@ cudaError_t launch_gdr_bwd_grad(const GdrArgs& a, const GdrGrads& g, Dtype dt, c
     case kBF16: return launch_dt<kBF16>(a, g, w, nc, stream);
   }
   return cudaErrorInvalidValue;
+}
+
+uint64_t gdr_img_f_bytes(int64_t Dk) { return ImgF::bytes(Dk <= 64 ? 64 : 128); }
+uint64_t gdr_img_b_bytes(int64_t Dk, Dtype dt) { return ImgB::bytes(Dk <= 64 ? 64 : 128, dt == kF32 ? 2 : 1); }
+
+unsigned read_and_clear_fault_gdr_grad() {
+  unsigned v = 0;
+  const unsigned zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_fault, sizeof(v)) != cudaSuccess) return ~0u;
+  if (v != 0 && cudaMemcpyToSymbol(g_fault, &zero, sizeof(zero)) != cudaSuccess) return ~0u;
+  return v;
 }
 
 }  // namespace ccv

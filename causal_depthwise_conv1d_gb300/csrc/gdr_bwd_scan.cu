@@ -7,8 +7,9 @@
 //   D <- ga D + Q^T (gi dO) - K^T X          (the gradient of the state before it)
 //
 // Laid out as the forward scan (gdr_scan.cu): a warp owns 16 value channels,
-// everything is transposed, D^T stays in registers.  D before each step and
-// dR go to the workspace for the gradients that sum over the value channels.
+// everything is transposed, D^T stays in registers.  D before each step, dR
+// and dO go to the workspace, as tiles that the gradients' matrix loads can
+// take (gdr_chunk.cuh), with the products dR.v of this warp's channels.
 //
 // A chunk with a value that is not finite is taken token by token, as there.
 //
@@ -34,7 +35,10 @@ struct Cfg {
   static constexpr int OBYTES = DT == kF32 ? 0 : kC * 32;     // dV of one warp
   static constexpr int WARPS = NW * H;
   static constexpr int XBYTES = H == 2 ? 4096 : 0;            // a warp's share of K D for the other
-  static constexpr int PER_WARP = GBYTES + OBYTES + XBYTES;
+  static constexpr int DIMG = 2 * img_state_bytes(DK) / H;    // this warp's part of D hi and D lo
+  static constexpr int RIMG = 2 * kTokBytes;                  // dR hi and lo
+  static constexpr int OIMG = TERMS * kTokBytes;              // dO
+  static constexpr int PER_WARP = 2 * GBYTES + OBYTES + XBYTES + DIMG + RIMG + OIMG;
   // FP32 tiles leave room for one stage only
   static constexpr int STAGES = 2 * STAGE + WARPS * PER_WARP + 64 <= 232448 ? 2 : 1;
   static constexpr int BYTES = STAGES * STAGE + WARPS * PER_WARP + 64;
@@ -71,8 +75,8 @@ __device__ __forceinline__ void fetch(const void* base, const int64_t* st, int64
 //   D += q (scale dO)^T;   dR = D^T k;   dV = beta dR;   D <- a (D - k dV^T)
 template <int DT, int NK, int H>
 __device__ __noinline__ void token_by_token(const GdrArgs& a, const GdrGrads& gr, float (&d)[NK][4], int64_t b,
-                                            int64_t h, int64_t t0, int64_t v0, float* r_out, int64_t dvp, int lane,
-                                            int half, int pair, float* xb, const float* xo) {
+                                            int64_t h, int64_t t0, int64_t v0, float (&u)[8][4], int lane, int half,
+                                            int pair, float* xb, const float* xo) {
   const int k0 = half * NK * 8;
   using F = Fmt<DT>;
   using E = typename F::E;
@@ -83,10 +87,8 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, const GdrGrads& gr
   const int64_t r0 = v0 + g, r1 = v0 + g + 8;
   for (int i = kC - 1; i >= 0; --i) {
     const int64_t t = t0 + i;
-    if (t >= a.L) {
-      if (qd == 0 && half == 0) r_out[i * dvp + r0] = r_out[i * dvp + r1] = 0.f;
-      continue;
-    }
+    if (((i >> 1) & 3) == qd) u[i >> 3][i & 1] = u[i >> 3][2 + (i & 1)] = 0.f;
+    if (t >= a.L) continue;
     const float dec = expf(a.g[b * a.gs[0] + t * a.gs[1] + h * a.gs[2]]);
     const float be = F::to_f(static_cast<const E*>(a.beta)[b * a.bs[0] + t * a.bs[1] + h * a.bs[2]]);
     const bool first =
@@ -121,9 +123,8 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, const GdrGrads& gr
       pair_sync(pair);
     }
     const float w0 = be * p0, w1 = be * p1;
+    if (((i >> 1) & 3) == qd) u[i >> 3][i & 1] = p0, u[i >> 3][2 + (i & 1)] = p1;
     if (qd == 0 && half == 0) {
-      r_out[i * dvp + r0] = p0;
-      r_out[i * dvp + r1] = p1;
       E* vp = static_cast<E*>(gr.dv) + b * gr.dvs[0] + t * gr.dvs[1] + h * gr.dvs[2];
       if (r0 < a.Dv) vp[r0 * gr.dvs[3]] = F::from_f(w0);
       if (r1 < a.Dv) vp[r1 * gr.dvs[3]] = F::from_f(w1);
@@ -147,7 +148,7 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, const GdrGrads& gr
 template <int DT, int DK, int NW, int H>
 __global__ void __launch_bounds__(32 * NW * H, 1)
     gdr_bwd_scan_kernel(const GdrArgs a, const GdrGrads gr, const GdrBwdWs w, int nc, int vtiles, bool gvec,
-                        bool ovec) {
+                        bool vvec, bool ovec) {
   pdl_enter();
   using C = Cfg<DT, DK, NW, H>;
   using F = Fmt<DT>;
@@ -157,9 +158,11 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
   constexpr int NS = C::STAGES;
   extern __shared__ __align__(128) uint8_t sm[];
   uint8_t* gbuf0 = sm + NS * C::STAGE;
-  uint8_t* obuf0 = gbuf0 + C::WARPS * C::GBYTES;
+  uint8_t* obuf0 = gbuf0 + 2 * C::WARPS * C::GBYTES;  // dO, then v
   uint8_t* xbuf0 = obuf0 + C::WARPS * C::OBYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(xbuf0 + C::WARPS * C::XBYTES);
+  uint8_t* ibuf0 = xbuf0 + C::WARPS * C::XBYTES;
+  constexpr int IMG = C::DIMG + C::RIMG + C::OIMG;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ibuf0 + C::WARPS * IMG);
   unsigned* left = reinterpret_cast<unsigned*>(full + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -196,9 +199,12 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
 
   const bool active = v0 < a.Dv;
   uint8_t* gb = gbuf0 + warp * C::GBYTES;
+  uint8_t* vb = gb + C::WARPS * C::GBYTES;
   uint8_t* ob = obuf0 + warp * C::OBYTES;
-  const bool wgvec = gvec && v0 + 16 <= a.Dv, wovec = ovec && v0 + 16 <= a.Dv;
-  const int64_t dvp = (a.Dv + 15) / 16 * 16;
+  uint8_t* ibuf = ibuf0 + warp * IMG;
+  const uint32_t dimg = smem_u32(ibuf), rimg = dimg + C::DIMG, oimg = rimg + C::RIMG;
+  const int ns = static_cast<int>((a.Dv + 15) / 16);
+  const bool wgvec = gvec && v0 + 16 <= a.Dv, wvvec = vvec && v0 + 16 <= a.Dv, wovec = ovec && v0 + 16 <= a.Dv;
 
   float d[NK][4];
 #pragma unroll
@@ -210,8 +216,12 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
                     ? gr.ds1[b * gr.ds1s[0] + h * gr.ds1s[1] + kd * gr.ds1s[2] + vc * gr.ds1s[3]]
                     : 0.f;
     }
+  auto fetch2 = [&](int64_t t0) {
+    fetch<DT>(gr.dout, gr.dos, a.L, a.Dv, b, h, t0, v0, wgvec, gb, lane);
+    fetch<DT>(a.v, a.vs, a.L, a.Dv, b, h, t0, v0, wvvec, vb, lane);
+  };
   if (active && nc > 0)
-    fetch<DT>(gr.dout, gr.dos, a.L, a.Dv, b, h, static_cast<int64_t>(nc - 1) * kC, v0, wgvec, gb, lane);
+    fetch2(static_cast<int64_t>(nc - 1) * kC);
 
   for (int n0 = 0; n0 < nc; ++n0) {
     const int s = n0 % NS, c = nc - 1 - n0;
@@ -238,18 +248,17 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
       const float ga = vecs[kHdGa];
 
       float a0 = 0.f, a1 = 0.f;
-      float* dst = w.d + (bh * nc + c) * DK * dvp;
+      uint8_t* gimg = w.img_b + ((bh * nc + c) * ns + v0 / 16) * ImgB::bytes(DK, C::TERMS);
+      float* ginv = reinterpret_cast<float*>(gimg + ImgB::inv(DK, C::TERMS));
+      if (lane == 0) bulk_wait_read();
+      __syncwarp();
 #pragma unroll
       for (int n = 0; n < NK; ++n) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dst[(k0 + 8 * n + 2 * qd + (j & 1)) * dvp + v0 + g + (j >> 1) * 8] = d[n][j];
         a0 = amax3(a0, d[n][0], d[n][1]);
         a1 = amax3(a1, d[n][2], d[n][3]);
       }
       const unsigned m0 = quad_max(__float_as_uint(a0)), m1 = quad_max(__float_as_uint(a1));
       bool bad = vecs[kHdBad] != 0.f || m0 >= kInfBits || m1 >= kInfBits;
-      const unsigned mx = warp_max(max(m0, m1));
-      if (lane == 0) atomicMax(w.d_max + bh * nc + c, mx);
       float f0, f1, di0, di1;
       row_factor(m0, f0, di0);
       row_factor(m1, f1, di1);
@@ -269,6 +278,12 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
         split2f(d[2 * kt][2], d[2 * kt][3], p1, hi[1], lo[1]);
         split2f(d[2 * kt + 1][0], d[2 * kt + 1][1], p0, hi[2], lo[2]);
         split2f(d[2 * kt + 1][2], d[2 * kt + 1][3], p1, hi[3], lo[3]);
+        {
+          const uint32_t at = dimg + (kt >> 1) * kBlkBytes +
+                              off64((lane & 7) + ((lane >> 3) & 1) * 8, (kt & 1) * 2 + (lane >> 4));
+          stsm4(at, hi);
+          stsm4(at + C::DIMG / 2, lo);
+        }
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
           uint32_t bk[4];
@@ -283,6 +298,18 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
             mma(u[2 * np + 1], hi, bk[2], bk[3]);
           }
         }
+      }
+
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        bulk_store(gimg + half * (C::DIMG / 2), ibuf, C::DIMG / 2);
+        bulk_store(gimg + img_state_bytes(DK) + half * (C::DIMG / 2), ibuf + C::DIMG / 2, C::DIMG / 2);
+        bulk_commit();
+      }
+      if (qd == 0) {
+#pragma unroll
+        for (int y = 0; y < 2 / H; ++y) ginv[(half + y) * 16 + g] = di0, ginv[(half + y) * 16 + g + 8] = di1;
       }
 
       // true values, and the other half's share
@@ -323,11 +350,78 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
             for (int j = 0; j < 4; ++j) x[2 * np + t][j] = F::word_elem(r[2 * t + (j >> 1)], j & 1);
         }
       }
+      float xv[8][4];  // v, for dR.v
+      if (half == 0) {
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+          if constexpr (DT == kF32) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                xv[2 * np + t][j] = *reinterpret_cast<const float*>(vb + (np * 16 + t * 8 + qd * 2 + (j & 1)) * C::ROW +
+                                                                    (g + (j >> 1) * 8) * 4);
+          } else {
+            uint32_t r[4];
+            ldsm4t(r, smem_u32(vb) + (np * 16 + (lane & 7) + ((lane >> 4) & 1) * 8) * C::ROW + ((lane >> 3) & 1) * 16);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) xv[2 * np + t][j] = F::word_elem(r[2 * t + (j >> 1)], j & 1);
+          }
+        }
+      }
       __syncwarp();
-      if (n0 + 1 < nc) fetch<DT>(gr.dout, gr.dos, a.L, a.Dv, b, h, t0 - kC, v0, wgvec, gb, lane);
+      if (n0 + 1 < nc) fetch2(t0 - kC);
 
       uint32_t hi[4][4], lo[4][4];
       bool ignore = false;
+      // a [64 tokens][16 v] tile from fragments of rows v
+      auto put_tok = [&](uint32_t tile, const uint32_t (&r)[4][4]) {
+#pragma unroll
+        for (int np = 0; np < 4; ++np)
+          stsm4t(tile + off32(np * 16 + (lane & 7) + ((lane >> 4) & 1) * 8, (lane >> 3) & 1), r[np]);
+      };
+      if (half == 0) {
+        float i0, i1;
+        split_rows<8, DT == kF32>(x, hi, lo, i0, i1, ignore);
+        put_tok(oimg, hi);
+        if constexpr (DT == kF32) put_tok(oimg + kTokBytes, lo);
+        if (qd == 0) ginv[48 + g] = i0, ginv[48 + g + 8] = i1;
+      }
+      // after dR: its image and dR.v of this warp's channels, and all parts out
+      auto save_r = [&](const float (&r)[8][4]) {
+        if (half != 0) return;
+        uint32_t rh[4][4], rl[4][4];
+        float i0, i1;
+        bool skip = false;
+        split_rows<8, true>(r, rh, rl, i0, i1, skip);
+        put_tok(rimg, rh);
+        put_tok(rimg + kTokBytes, rl);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bulk_store(gimg + ImgB::r(DK), ibuf + C::DIMG, C::RIMG + C::OIMG);
+          bulk_commit();
+        }
+        if (qd == 0) ginv[32 + g] = i0, ginv[32 + g + 8] = i1;
+        // sums over the 16 rows: two here, eight lanes by a halving exchange;
+        // a lane ends with tokens 2 lane and 2 lane + 1
+        float y[16];
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) y[2 * n + e] = fmaf(r[n][e], xv[n][e], r[n][2 + e] * xv[n][2 + e]);
+#pragma unroll
+        for (int m = 8; m >= 2; m >>= 1)
+#pragma unroll
+          for (int j = 0; j < m; ++j) {
+            const bool up = (lane & (2 * m)) != 0;
+            const float mine = up ? y[m + j] : y[j], other = up ? y[j] : y[m + j];
+            y[j] = mine + __shfl_xor_sync(kFullMask, other, 2 * m);
+          }
+        *reinterpret_cast<float2*>(ginv + 64 + 2 * lane) = make_float2(y[0], y[1]);
+      };
       {  // dU^T = dO^T P + gc (K D)^T: 16-bit dO times powers of two is exact in hi
         float y[8][4], yi0, yi1;
 #pragma unroll
@@ -372,7 +466,6 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
         }
       }
       // dR^T = dU^T T (the factors of T's rows are in dU now)
-      float* rw = w.r + (bh * nc + c) * kC * dvp;
       float ui0, ui1;
       split_rows<8, true>(u, hi, lo, ui0, ui1, bad);
       // (with two warps: also the barrier after which the exchange buffers may be written again)
@@ -383,7 +476,9 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
         for (int n = 0; n < NK; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) tmp[n][j] = d[n][j];
-        token_by_token<DT, NK, H>(a, gr, tmp, b, h, t0, v0, rw, dvp, lane, half, pair, xb, xo);
+        float ut[8][4];
+        token_by_token<DT, NK, H>(a, gr, tmp, b, h, t0, v0, ut, lane, half, pair, xb, xo);
+        save_r(ut);
 #pragma unroll
         for (int n = 0; n < NK; ++n)
 #pragma unroll
@@ -418,16 +513,14 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
           }
         }
       }
-      // dR to the workspace, dV out
+      save_r(u);
+      // dV out
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
         float y[2][4];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int n = 2 * np + t;
-          if (H == 1 || (np >> 1) == half)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) rw[(n * 8 + qd * 2 + (j & 1)) * dvp + v0 + g + (j >> 1) * 8] = u[n][j];
           const float2 be = *reinterpret_cast<const float2*>(slot + kVBeta * kC + n * 8 + qd * 2);
           y[t][0] = u[n][0] * be.x, y[t][1] = u[n][1] * be.y, y[t][2] = u[n][2] * be.x, y[t][3] = u[n][3] * be.y;
         }
@@ -526,6 +619,7 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
       }
     }
   }
+  if (lane == 0) bulk_wait_all();
   if (gr.ds0 != nullptr) {
 #pragma unroll
     for (int n = 0; n < NK; ++n)
@@ -552,21 +646,16 @@ cudaError_t launch(const GdrArgs& a, const GdrGrads& g, const GdrBwdWs& w, int n
       cudaFuncSetAttribute(gdr_bwd_scan_kernel<DT, DK, NW, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e != cudaSuccess) return e;
   return launch_pdl(gdr_bwd_scan_kernel<DT, DK, NW, H>, static_cast<unsigned>(a.B * a.Hv * vtiles), 32 * C::WARPS, C::BYTES, s,
-                    a, g, w, nc, vtiles, al(g.dout, g.dos), al(g.dv, g.dvs));
+                    a, g, w, nc, vtiles, al(g.dout, g.dos), al(a.v, a.vs), al(g.dv, g.dvs));
 }
 
 template <int DT, int DK>
 cudaError_t launch_nw(const GdrArgs& a, const GdrGrads& g, const GdrBwdWs& w, int nc, const Device& dev,
                       cudaStream_t s) {
-  const int64_t heads = a.B * a.Hv, groups = (a.Dv + 15) / 16, sms = dev.sm_count;  // as in the forward scan
-  if constexpr (DT == kF32) {
-    if (heads * ((groups + 1) / 2) <= sms) return launch<DT, DK, 2, 1>(a, g, w, nc, s);
-    return launch<DT, DK, 4, 1>(a, g, w, nc, s);
-  } else {
-    if (heads * ((groups + 1) / 2) <= sms) return launch<DT, DK, 2, 2>(a, g, w, nc, s);
-    if (heads * ((groups + 3) / 4) <= sms) return launch<DT, DK, 4, 1>(a, g, w, nc, s);
-    return launch<DT, DK, 8, 1>(a, g, w, nc, s);
-  }
+  // as in the forward scan; the tiles that go to the workspace leave no room for eight groups a block
+  const int64_t heads = a.B * a.Hv, groups = (a.Dv + 15) / 16, sms = dev.sm_count;
+  if (heads * ((groups + 1) / 2) > sms) return launch<DT, DK, 4, 1>(a, g, w, nc, s);
+  return launch<DT, DK, 2, DT == kF32 ? 1 : 2>(a, g, w, nc, s);
 }
 
 template <int DT>

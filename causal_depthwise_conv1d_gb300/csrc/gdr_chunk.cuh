@@ -63,6 +63,38 @@ constexpr int kPackBytes = kOffP + 2 * kMatBytes;          // factors, T hi, T l
 __host__ __device__ constexpr int qk_tile_bytes(int DK) { return kC * DK * 2; }
 __host__ __device__ constexpr int qk_pack_bytes(int DK, int terms) { return 2 * terms * qk_tile_bytes(DK); }
 
+// What the backward pass keeps of a chunk, per group ("slice") of 16 value
+// channels, as FP16 tiles ready for matrix loads: the state before the chunk
+// and U from the forward scan, D, dR and dO from the reverse scan, each row of
+// a value channel scaled by its power of two and split in hi and lo (dO of
+// 16-bit inputs is exact in hi).  S and D: blocks of 32 key channels, [16 v][32
+// k]; U, dR, dO: [64 tokens][16 v].  The inverse row factors follow; S and D
+// have one for each half of the key channels (a scan with two warps a slice
+// has two).
+constexpr int kSliceV = 16;
+constexpr int kBlkBytes = kSliceV * 32 * 2;
+constexpr int kTokBytes = kC * kSliceV * 2;
+__host__ __device__ constexpr int img_state_bytes(int DK) { return DK / 32 * kBlkBytes; }  // hi, or lo
+struct ImgF {  // S hi, S lo, U hi, U lo, 1/factors of S [2][16], of U [16]
+  static __host__ __device__ constexpr int u(int DK) { return 2 * img_state_bytes(DK); }
+  static __host__ __device__ constexpr int inv(int DK) { return u(DK) + 2 * kTokBytes; }
+  static __host__ __device__ constexpr int bytes(int DK) { return inv(DK) + 256; }
+};
+struct ImgB {  // D hi, D lo, dR hi, dR lo, dO hi, (dO lo,) 1/factors of D [2][16], dR, dO, then dR.v of 64 tokens
+  static __host__ __device__ constexpr int r(int DK) { return 2 * img_state_bytes(DK); }
+  static __host__ __device__ constexpr int o(int DK) { return r(DK) + 2 * kTokBytes; }
+  static __host__ __device__ constexpr int inv(int DK, int terms) { return o(DK) + terms * kTokBytes; }
+  static __host__ __device__ constexpr int bytes(int DK, int terms) { return inv(DK, terms) + 512; }
+};
+// Rows of 64 and 32 bytes whose 16-byte pieces are placed so that eight rows
+// at one piece lie in different banks.
+__device__ __forceinline__ uint32_t off64(int row, int piece) {
+  return static_cast<uint32_t>(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+}
+__device__ __forceinline__ uint32_t off32(int row, int piece) {
+  return static_cast<uint32_t>(row * 32 + ((piece ^ ((row >> 2) & 1)) << 4));
+}
+
 // Tiles are rows of RB bytes in 16-byte pieces; piece p of row r lies at
 // p ^ (r & 7), so the eight rows of a matrix load touch all banks.
 template <int RB>
@@ -86,6 +118,12 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
 
 __device__ __forceinline__ void stsm4t(uint32_t addr, const uint32_t (&r)[4]) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+__device__ __forceinline__ void stsm4(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3])
                : "memory");
 }

@@ -50,8 +50,10 @@ struct ScanCfg {
   static constexpr int VBYTES = kC * VROW;
   static constexpr int OBYTES = (DT == kF32 || SAVE) ? 0 : kC * 32;
   static constexpr int WARPS = NW * H;
+  static constexpr int SIMG = SAVE ? 2 * img_state_bytes(DK) / H : 0;  // this warp's part of S hi and S lo
+  static constexpr int UIMG = SAVE ? 2 * kTokBytes / H : 0;             // U hi and lo, or one of them
   static constexpr int XBYTES = H == 2 ? (SAVE ? 4096 : 6144) : 0;  // a warp's share of K S (and Q S) for the other
-  static constexpr int BYTES = 2 * STAGE + WARPS * (VBYTES + OBYTES + XBYTES) + 64;
+  static constexpr int BYTES = 2 * STAGE + WARPS * (VBYTES + OBYTES + XBYTES + SIMG + UIMG) + 64;
 };
 
 // This warp's v of one chunk into its buffer; rows past the sequence and
@@ -88,8 +90,8 @@ __device__ __forceinline__ void fetch_v(const GdrArgs& a, int64_t b, int64_t h, 
 // Two warps of a pair add their sums through xb (own) and xo (the other's).
 template <int DT, int NK, int H, bool SAVE>
 __device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[NK][4], int64_t b, int64_t h, int64_t t0,
-                                            int64_t v0, float* u_out, int64_t dvp, int lane, int half, int pair,
-                                            float* xb, const float* xo) {
+                                            int64_t v0, float (&u)[8][4], int lane, int half, int pair, float* xb,
+                                            const float* xo) {
   using F = Fmt<DT>;
   using E = typename F::E;
   const int g = lane >> 2, qd = lane & 3;
@@ -98,9 +100,8 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[NK][4]
   const E* qp = static_cast<const E*>(a.q) + b * a.qs[0] + hk * a.qs[2];
   const int64_t r0 = v0 + g, r1 = v0 + g + 8;
   const int k0 = half * NK * 8;
-  if (SAVE && qd == 0 && half == 0) {  // rows past the sequence
-    for (int64_t i = a.L - t0; i < kC; ++i) u_out[i * dvp + r0] = u_out[i * dvp + r1] = 0.f;
-  }
+  for (int n = 0; n < 8; ++n)
+    for (int j = 0; j < 4; ++j) u[n][j] = 0.f;
   for (int i = 0; i < kC && t0 + i < a.L; ++i) {
     const int64_t t = t0 + i;
     float dec = expf(a.g[b * a.gs[0] + t * a.gs[1] + h * a.gs[2]]);
@@ -147,15 +148,12 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[NK][4]
     const E* vp = static_cast<const E*>(a.v) + b * a.vs[0] + t * a.vs[1] + h * a.vs[2];
     const float x0 = r0 < a.Dv ? F::to_f(vp[r0 * a.vs[3]]) : 0.f, x1 = r1 < a.Dv ? F::to_f(vp[r1 * a.vs[3]]) : 0.f;
     const float u0 = be * (x0 - dec * p0), u1 = be * (x1 - dec * p1);
-    if (qd == 0 && half == 0) {
-      if constexpr (SAVE) {
-        u_out[i * dvp + r0] = u0;
-        u_out[i * dvp + r1] = u1;
-      } else {
+    if constexpr (SAVE) {
+      if (((i >> 1) & 3) == qd) u[i >> 3][i & 1] = u0, u[i >> 3][2 + (i & 1)] = u1;
+    } else if (qd == 0 && half == 0) {
         E* op = static_cast<E*>(a.out) + b * a.os[0] + t * a.os[1] + h * a.os[2];
         if (r0 < a.Dv) op[r0 * a.os[3]] = F::from_f(a.scale * fmaf(qk, u0, dec * o0));
         if (r1 < a.Dv) op[r1 * a.os[3]] = F::from_f(a.scale * fmaf(qk, u1, dec * o1));
-      }
     }
 #pragma unroll
     for (int n = 0; n < NK; ++n)
@@ -173,8 +171,8 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[NK][4]
 
 template <int DT, int DK, int NW, int H, bool SAVE>
 __global__ void __launch_bounds__(32 * NW * H, 1)
-    gdr_scan_kernel(const GdrArgs a, const uint8_t* qk_ws, const uint8_t* pack_ws, float* s_ws, float* u_ws,
-                    unsigned* s_max, int nc, int vtiles, bool vvec, bool ovec) {
+    gdr_scan_kernel(const GdrArgs a, const uint8_t* qk_ws, const uint8_t* pack_ws, uint8_t* img, int nc, int vtiles,
+                    bool vvec, bool ovec) {
   pdl_enter();
   using C = ScanCfg<DT, DK, NW, H, SAVE>;
   using F = Fmt<DT>;
@@ -185,7 +183,8 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
   uint8_t* vbuf0 = sm + 2 * C::STAGE;
   uint8_t* obuf0 = vbuf0 + C::WARPS * C::VBYTES;
   uint8_t* xbuf0 = obuf0 + C::WARPS * C::OBYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(xbuf0 + C::WARPS * C::XBYTES);
+  uint8_t* ibuf0 = xbuf0 + C::WARPS * C::XBYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ibuf0 + C::WARPS * (C::SIMG + C::UIMG));
   unsigned* left = reinterpret_cast<unsigned*>(full + 2);  // warps that have left a stage
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -225,8 +224,9 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
   const bool active = v0 < a.Dv;
   uint8_t* vb = vbuf0 + warp * C::VBYTES;
   uint8_t* ob = obuf0 + warp * C::OBYTES;
+  uint8_t* ibuf = ibuf0 + warp * (C::SIMG + C::UIMG);
+  const uint32_t simg = smem_u32(ibuf), uimg = simg + C::SIMG;
   const bool wvec = vvec && v0 + 16 <= a.Dv, wovec = ovec && v0 + 16 <= a.Dv;
-  const int64_t dvp = (a.Dv + 15) / 16 * 16;
 
   float st[NK][4];
 #pragma unroll
@@ -263,16 +263,39 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
       const uint32_t th = kt_hi + C::QKB + kVecBytes, tl = th + kMatBytes;
       const uint32_t ph = kt_hi + C::QKB + kOffP, pl = ph + kMatBytes;
       const float ga = vecs[kHdGa];
-      float* u_out = SAVE ? u_ws + (bh * nc + c) * kC * dvp : nullptr;
+      // SAVE: this slice's image of the chunk, and the staging of its parts
+      const int ns = static_cast<int>((a.Dv + 15) / 16);
+      uint8_t* gimg = SAVE ? img + ((bh * nc + c) * ns + v0 / 16) * ImgF::bytes(DK) : nullptr;
       if constexpr (SAVE) {
-        float* so = s_ws + (bh * nc + c) * DK * dvp;
-#pragma unroll
-        for (int n = 0; n < NK; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) so[(k0 + 8 * n + 2 * qd + (j & 1)) * dvp + v0 + g + (j >> 1) * 8] = st[n][j];
+        if (lane == 0) bulk_wait_read();
+        __syncwarp();
       }
       bool bad = vecs[kHdBad] != 0.f;
 
+      auto save_u = [&](const float (&x)[8][4]) {  // of two warps one keeps hi, the other lo
+        uint32_t uh[4][4], ul[4][4];
+        float i0, i1;
+        bool ignore = false;
+        split_rows<8, true>(x, uh, ul, i0, i1, ignore);
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+          // tokens 16 np..: fragments of rows v are read back as rows of tokens
+          const uint32_t at = uimg + off32(np * 16 + (lane & 7) + ((lane >> 4) & 1) * 8, (lane >> 3) & 1);
+          if (H == 1 || half == 0) stsm4t(at, uh[np]);
+          if (H == 1) stsm4t(at + kTokBytes, ul[np]);
+          if (H == 2 && half == 1) stsm4t(at, ul[np]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bulk_store(gimg + ImgF::u(DK) + half * kTokBytes, ibuf + C::SIMG, C::UIMG);
+          bulk_commit();
+        }
+        if (qd == 0 && half == 0) {
+          float* inv = reinterpret_cast<float*>(gimg + ImgF::inv(DK)) + 32;
+          inv[g] = i0, inv[g + 8] = i1;
+        }
+      };
       // the state's row factors
       float a0 = 0.f, a1 = 0.f;
 #pragma unroll
@@ -286,11 +309,6 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
       row_factor(m0, f0, si0);
       row_factor(m1, f1, si1);
       const uint64_t p0 = pk(f0, f0), p1 = pk(f1, f1);
-      if constexpr (SAVE) {  // the chunk's largest state element: one factor for the whole matrix later
-        const unsigned mx = warp_max(max(m0, m1));
-        if (lane == 0) atomicMax(s_max + bh * nc + c, mx);
-      }
-
       // (K S)^T and (Q S)^T
       float ks[8][4], qs[8][4];
 #pragma unroll
@@ -305,6 +323,12 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
         split2f(st[2 * kt][2], st[2 * kt][3], p1, hi[1], lo[1]);
         split2f(st[2 * kt + 1][0], st[2 * kt + 1][1], p0, hi[2], lo[2]);
         split2f(st[2 * kt + 1][2], st[2 * kt + 1][3], p1, hi[3], lo[3]);
+        if constexpr (SAVE) {
+          const uint32_t at = simg + (kt >> 1) * kBlkBytes +
+                              off64((lane & 7) + ((lane >> 3) & 1) * 8, (kt & 1) * 2 + (lane >> 4));
+          stsm4(at, hi);
+          stsm4(at + C::SIMG / 2, lo);
+        }
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
           uint32_t bk[4];
@@ -335,6 +359,20 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
         }
       }
 
+      if constexpr (SAVE) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bulk_store(gimg + half * (C::SIMG / 2), ibuf, C::SIMG / 2);
+          bulk_store(gimg + img_state_bytes(DK) + half * (C::SIMG / 2), ibuf + C::SIMG / 2, C::SIMG / 2);
+          bulk_commit();
+        }
+        if (qd == 0) {
+          float* inv = reinterpret_cast<float*>(gimg + ImgF::inv(DK));
+#pragma unroll
+          for (int x = 0; x < 2 / H; ++x) inv[(half + x) * 16 + g] = si0, inv[(half + x) * 16 + g + 8] = si1;
+        }
+      }
       // true values, and the other half's share; O: this warp's tokens are 16 np0.. and 16 np1..
       const int np0 = H == 2 ? half : 0, np1 = H == 2 ? 3 - half : 0;
       float qo[H == 2 ? 4 : 1][4];
@@ -421,7 +459,9 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
         for (int n = 0; n < NK; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) tmp[n][j] = st[n][j];
-        token_by_token<DT, NK, H, SAVE>(a, tmp, b, h, t0, v0, u_out, dvp, lane, half, pair, xb, xo);
+        float ut[8][4];
+        token_by_token<DT, NK, H, SAVE>(a, tmp, b, h, t0, v0, ut, lane, half, pair, xb, xo);
+        if constexpr (SAVE) save_u(ut);
 #pragma unroll
         for (int n = 0; n < NK; ++n)
 #pragma unroll
@@ -462,11 +502,7 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
           }
         }
         if constexpr (SAVE) {
-#pragma unroll
-          for (int n = 0; n < 8; ++n)
-            if (H == 1 || (n >> 2) == half)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) u_out[(n * 8 + qd * 2 + (j & 1)) * dvp + v0 + g + (j >> 1) * 8] = u[n][j];
+          save_u(u);
         } else {
           // O^T = scale (gi (Q S)^T + U^T P^T)
           float ui0, ui1;
@@ -585,6 +621,7 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
       }
     }
   }
+  if (SAVE && lane == 0) bulk_wait_all();
   if (a.s1 != nullptr) {
 #pragma unroll
     for (int n = 0; n < NK; ++n)
@@ -598,7 +635,7 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
 }
 
 template <int DT, int DK, int NW, int H, bool SAVE>
-cudaError_t launch(const GdrArgs& a, const uint8_t* qk, const uint8_t* pkg, float* sw, float* uw, unsigned* sm, int nc,
+cudaError_t launch(const GdrArgs& a, const uint8_t* qk, const uint8_t* pkg, uint8_t* img, int nc,
                    cudaStream_t s) {
   using C = ScanCfg<DT, DK, NW, H, SAVE>;
   static_assert(C::BYTES <= 232448, "shared memory of one block");
@@ -612,49 +649,48 @@ cudaError_t launch(const GdrArgs& a, const uint8_t* qk, const uint8_t* pkg, floa
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e != cudaSuccess) return e;
   return launch_pdl(gdr_scan_kernel<DT, DK, NW, H, SAVE>, static_cast<unsigned>(a.B * a.Hv * vtiles), 32 * C::WARPS,
-                    C::BYTES, s, a, qk, pkg, sw, uw, sm, nc, vtiles, al(a.v, a.vs), !SAVE && al(a.out, a.os));
+                    C::BYTES, s, a, qk, pkg, img, nc, vtiles, al(a.v, a.vs), !SAVE && al(a.out, a.os));
 }
 
 template <int DT, int DK, bool SAVE>
-cudaError_t launch_nw(const GdrArgs& a, const uint8_t* qk, const uint8_t* pkg, float* sw, float* uw, unsigned* sm,
-                      int nc, const Device& dev, cudaStream_t s) {
+cudaError_t launch_nw(const GdrArgs& a, const uint8_t* qk, const uint8_t* pkg, uint8_t* img, int nc, const Device& dev, cudaStream_t s) {
   // Blocks of few channels while that still puts no more than one on an SM.
   // Two warps a group only where one each would leave half the quarters of an
   // SM idle (32 heads, 8192 tokens: 537 -> 368 us; with 64 heads, four groups
   // a block, 119 -> 145 us in the state-keeping scan).
   const int64_t heads = a.B * a.Hv, groups = (a.Dv + 15) / 16, sms = dev.sm_count;
   if constexpr (DT == kF32) {  // two terms of k and q: the stages leave room for one warp a group, four groups
-    if (heads * ((groups + 1) / 2) <= sms) return launch<DT, DK, 2, 1, SAVE>(a, qk, pkg, sw, uw, sm, nc, s);
-    return launch<DT, DK, 4, 1, SAVE>(a, qk, pkg, sw, uw, sm, nc, s);
+    if (heads * ((groups + 1) / 2) <= sms) return launch<DT, DK, 2, 1, SAVE>(a, qk, pkg, img, nc, s);
+    return launch<DT, DK, 4, 1, SAVE>(a, qk, pkg, img, nc, s);
   } else {
-    if (heads * ((groups + 1) / 2) <= sms) return launch<DT, DK, 2, 2, SAVE>(a, qk, pkg, sw, uw, sm, nc, s);
-    if (heads * ((groups + 3) / 4) <= sms) return launch<DT, DK, 4, 1, SAVE>(a, qk, pkg, sw, uw, sm, nc, s);
-    return launch<DT, DK, 8, 1, SAVE>(a, qk, pkg, sw, uw, sm, nc, s);
+    if (heads * ((groups + 1) / 2) <= sms) return launch<DT, DK, 2, 2, SAVE>(a, qk, pkg, img, nc, s);
+    if (heads * ((groups + 3) / 4) <= sms) return launch<DT, DK, 4, 1, SAVE>(a, qk, pkg, img, nc, s);
+    return launch<DT, DK, 8, 1, SAVE>(a, qk, pkg, img, nc, s);
   }
 }
 
 template <int DT, int DK>
-cudaError_t launch_k(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, unsigned* sm, int nc,
+cudaError_t launch_k(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, uint8_t* img, int nc,
                      const Device& dev, cudaStream_t s) {
-  return sw != nullptr ? launch_nw<DT, DK, true>(a, qk, pk, sw, uw, sm, nc, dev, s)
-                       : launch_nw<DT, DK, false>(a, qk, pk, sw, uw, sm, nc, dev, s);
+  return img != nullptr ? launch_nw<DT, DK, true>(a, qk, pk, img, nc, dev, s)
+                       : launch_nw<DT, DK, false>(a, qk, pk, img, nc, dev, s);
 }
 
 template <int DT>
-cudaError_t launch_dt(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, float* sw, float* uw, unsigned* sm, int nc,
+cudaError_t launch_dt(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, uint8_t* img, int nc,
                       const Device& dev, cudaStream_t s) {
-  return a.Dk <= 64 ? launch_k<DT, 64>(a, qk, pk, sw, uw, sm, nc, dev, s)
-                    : launch_k<DT, 128>(a, qk, pk, sw, uw, sm, nc, dev, s);
+  return a.Dk <= 64 ? launch_k<DT, 64>(a, qk, pk, img, nc, dev, s)
+                    : launch_k<DT, 128>(a, qk, pk, img, nc, dev, s);
 }
 
 }  // namespace
 
-cudaError_t launch_gdr_scan(const GdrArgs& a, Dtype dt, const uint8_t* qk_ws, const uint8_t* pack_ws, float* s_ws,
-                            float* u_ws, unsigned* s_max, int nc, const Device& dev, cudaStream_t stream) {
+cudaError_t launch_gdr_scan(const GdrArgs& a, Dtype dt, const uint8_t* qk_ws, const uint8_t* pack_ws, uint8_t* img,
+                            int nc, const Device& dev, cudaStream_t stream) {
   switch (dt) {
-    case kF32: return launch_dt<kF32>(a, qk_ws, pack_ws, s_ws, u_ws, s_max, nc, dev, stream);
-    case kF16: return launch_dt<kF16>(a, qk_ws, pack_ws, s_ws, u_ws, s_max, nc, dev, stream);
-    case kBF16: return launch_dt<kBF16>(a, qk_ws, pack_ws, s_ws, u_ws, s_max, nc, dev, stream);
+    case kF32: return launch_dt<kF32>(a, qk_ws, pack_ws, img, nc, dev, stream);
+    case kF16: return launch_dt<kF16>(a, qk_ws, pack_ws, img, nc, dev, stream);
+    case kBF16: return launch_dt<kBF16>(a, qk_ws, pack_ws, img, nc, dev, stream);
   }
   return cudaErrorInvalidValue;
 }

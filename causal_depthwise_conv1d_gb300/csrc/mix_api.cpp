@@ -49,24 +49,24 @@ GdrWorkspace gdr_workspace(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t
 
 // The backward pass: every part on a 256-byte boundary.
 struct GdrBwdWorkspace {
-  uint64_t qk, pack, state, tok, max, total;
+  uint64_t qk, pack, img_f, img_b, total;
 };
 
 GdrBwdWorkspace gdr_bwd_workspace(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
                                   ccv_dtype dtype) {
-  GdrBwdWorkspace w = {0, 0, 0, 0, 0, 0};
+  GdrBwdWorkspace w = {0, 0, 0, 0, 0};
   if (B == 0 || Hv == 0 || Dv == 0 || L == 0) return w;
   ccv::GdrArgs a = {};
   a.B = B, a.L = L, a.Hk = Hk, a.Hv = Hv, a.Dk = Dk, a.Dv = Dv;
+  const ccv::Dtype dt = static_cast<ccv::Dtype>(dtype);
   const int nc = gdr_chunks(L);
-  const uint64_t chunks = static_cast<uint64_t>(B * Hv) * nc, dvp = static_cast<uint64_t>((Dv + 15) / 16 * 16);
+  const uint64_t slices = static_cast<uint64_t>(B * Hv) * nc * static_cast<uint64_t>((Dv + 15) / 16);
   auto up = [](uint64_t x) { return (x + 255) / 256 * 256; };
-  w.qk = up(ccv::gdr_qk_bytes(a, static_cast<ccv::Dtype>(dtype), nc));
+  w.qk = up(ccv::gdr_qk_bytes(a, dt, nc));
   w.pack = up(ccv::gdr_pack_bytes(a, nc));
-  w.state = up(chunks * (Dk <= 64 ? 64 : 128) * dvp * 4);
-  w.tok = up(chunks * ccv::kGdrChunk * dvp * 4);
-  w.max = up(chunks * 4);
-  w.total = w.qk + w.pack + 2 * (w.state + w.tok + w.max);
+  w.img_f = up(slices * ccv::gdr_img_f_bytes(Dk));
+  w.img_b = up(slices * ccv::gdr_img_b_bytes(Dk, dt));
+  w.total = w.qk + w.pack + w.img_f + w.img_b;
   return w;
 }
 
@@ -201,6 +201,12 @@ ccv_status check_gdr_sizes(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t
   return CCV_OK;
 }
 
+ccv_status check_bwd_dv(int64_t Dv) {
+  if (Dv > ccv::kGdrBwdDv)
+    CCV_FAIL(CCV_ERR_UNSUPPORTED, "Dv must be at most %d (got %lld)", ccv::kGdrBwdDv, (long long)Dv);
+  return CCV_OK;
+}
+
 void copy(int64_t* dst, const int64_t* src, int n) {
   for (int i = 0; i < n; ++i) dst[i] = src != nullptr ? src[i] : 0;
 }
@@ -267,7 +273,7 @@ ccv_status ccv_gdr_fwd(const void* q, const int64_t q_strides[4], const void* k,
   uint8_t* qk_ws = static_cast<uint8_t*>(workspace);
   uint8_t* pack_ws = qk_ws + w.qk;
   cudaError_t err = ccv::launch_gdr_prep(a, dt, qk_ws, pack_ws, gdr_chunks(L), s);
-  if (err == cudaSuccess) err = ccv::launch_gdr_scan(a, dt, qk_ws, pack_ws, nullptr, nullptr, nullptr, gdr_chunks(L), dev, s);
+  if (err == cudaSuccess) err = ccv::launch_gdr_scan(a, dt, qk_ws, pack_ws, nullptr, gdr_chunks(L), dev, s);
   return launched(err, "gdr_chunk");
 }
 
@@ -328,6 +334,7 @@ ccv_status ccv_gdr_bwd_workspace_size(int64_t B, int64_t L, int64_t Hk, int64_t 
   ccv::api_begin();
   if (bytes == nullptr) CCV_FAIL(CCV_ERR_INVALID_ARG, "bytes is required");
   CCV_TRY(check_gdr_sizes(B, L, Hk, Hv, Dk, Dv, ccv::kGdrChunkDk, dtype));
+  CCV_TRY(check_bwd_dv(Dv));
   *bytes = gdr_bwd_workspace(B, L, Hk, Hv, Dk, Dv, dtype).total;
   return CCV_OK;
 }
@@ -352,6 +359,7 @@ ccv_status ccv_gdr_bwd(const void* q, const int64_t q_strides[4], const void* k,
     return CCV_OK;
   }
   if (Dv == 0) CCV_FAIL(CCV_ERR_INVALID_ARG, "Dv must be >= 1");
+  CCV_TRY(check_bwd_dv(Dv));
   const int64_t e = dtype_size(dtype);
   const int64_t qk[4] = {B, L, Hk, Dk}, vo[4] = {B, L, Hv, Dv}, gate[3] = {B, L, Hv}, st[4] = {B, Hv, Dk, Dv},
                 ids[2] = {B, L};
@@ -396,18 +404,12 @@ ccv_status ccv_gdr_bwd(const void* q, const int64_t q_strides[4], const void* k,
   const int nc = gdr_chunks(L);
   uint8_t* p = static_cast<uint8_t*>(workspace);
   uint8_t *qk_ws = p, *pack_ws = qk_ws + ws.qk;
-  float* s_ws = reinterpret_cast<float*>(pack_ws + ws.pack);
-  float* u_ws = s_ws + ws.state / 4;
-  float* d_ws = u_ws + ws.tok / 4;
-  float* r_ws = d_ws + ws.state / 4;
-  unsigned* s_max = reinterpret_cast<unsigned*>(r_ws + ws.tok / 4);
-  unsigned* d_max = s_max + ws.max / 4;
-  const ccv::GdrBwdWs w = {qk_ws, pack_ws, s_ws, u_ws, s_max, d_ws, r_ws, d_max};
+  uint8_t *img_f = pack_ws + ws.pack, *img_b = img_f + ws.img_f;
+  const ccv::GdrBwdWs w = {qk_ws, pack_ws, img_f, img_b};
   cudaError_t err = cudaSuccess;
   if (L > 0) {
-    err = cudaMemsetAsync(s_max, 0, 2 * ws.max, s);
-    if (err == cudaSuccess) err = ccv::launch_gdr_prep(a, dt, qk_ws, pack_ws, nc, s);
-    if (err == cudaSuccess) err = ccv::launch_gdr_scan(a, dt, qk_ws, pack_ws, s_ws, u_ws, s_max, nc, dev, s);
+    err = ccv::launch_gdr_prep(a, dt, qk_ws, pack_ws, nc, s);
+    if (err == cudaSuccess) err = ccv::launch_gdr_scan(a, dt, qk_ws, pack_ws, img_f, nc, dev, s);
   }
   if (err == cudaSuccess) err = ccv::launch_gdr_bwd_scan(a, gr, dt, w, nc, dev, s);
   if (err == cudaSuccess && L > 0) err = ccv::launch_gdr_bwd_grad(a, gr, dt, w, nc, s);

@@ -9,6 +9,7 @@ namespace ccv {
 constexpr int kGdrChunk = 64;     // tokens of one chunk of the chunked kernels
 constexpr int kGdrMaxDk = 256;    // largest key size of the token-by-token kernel
 constexpr int kGdrChunkDk = 128;  // largest key size of the chunked kernels
+constexpr int kGdrBwdDv = 512;    // largest value size of the backward pass
 
 // Validated arguments of the gated delta rule.  q, k: [B,L,Hk,Dk]; v, out:
 // [B,L,Hv,Dv]; g (FP32), beta: [B,L,Hv]; states FP32 [.,Hv,Dk,Dv].  Strides in
@@ -68,32 +69,30 @@ cudaError_t launch_gdr_step(const GdrArgs& a, Dtype dt, cudaStream_t stream);
 // Chunked forward pass: the parts that do not depend on the state (qk_ws,
 // pack_ws: see gdr_chunk.cuh), then the scan that carries it.  nc = chunks.
 cudaError_t launch_gdr_prep(const GdrArgs& a, Dtype dt, uint8_t* qk_ws, uint8_t* pack_ws, int nc, cudaStream_t stream);
-// For the backward pass the scan makes no output but keeps each chunk's first
-// state and its U (FP32, [b][h][chunk][DK or 64][dvp], DK = 64 or 128 and dvp
-// = Dv rounded up to 16) in s_ws and u_ws, and raises s_max[b][h][chunk] to the
-// magnitude (as bits) of the state's largest element.
-cudaError_t launch_gdr_scan(const GdrArgs& a, Dtype dt, const uint8_t* qk_ws, const uint8_t* pack_ws, float* s_ws,
-                            float* u_ws, unsigned* s_max, int nc, const Device& dev, cudaStream_t stream);
+// For the backward pass (img given) the scan makes no output but keeps each
+// chunk's first state and its U as images [b][h][chunk][16 value channels].
+cudaError_t launch_gdr_scan(const GdrArgs& a, Dtype dt, const uint8_t* qk_ws, const uint8_t* pack_ws, uint8_t* img,
+                            int nc, const Device& dev, cudaStream_t stream);
 
-// Backward pass after these two: the reverse scan (dv, the state's gradient
-// after each chunk in d_ws, the gradient of U in r_ws) and the gradients of
-// one chunk each.
+// Backward pass after these two: the reverse scan (dv, and its own images) and
+// the gradients of one chunk each.
 struct GdrBwdWs {
-  const uint8_t *qk, *pack;
-  const float *s, *u;
-  const unsigned* s_max;
-  float *d, *r;
-  unsigned* d_max;
+  const uint8_t *qk, *pack, *img_f;
+  uint8_t* img_b;
 };
 cudaError_t launch_gdr_bwd_scan(const GdrArgs& a, const GdrGrads& g, Dtype dt, const GdrBwdWs& w, int nc,
                                 const Device& dev, cudaStream_t stream);
 cudaError_t launch_gdr_bwd_grad(const GdrArgs& a, const GdrGrads& g, Dtype dt, const GdrBwdWs& w, int nc,
                                 cudaStream_t stream);
+// Bytes of the images of one chunk, value head and 16 value channels.
+uint64_t gdr_img_f_bytes(int64_t Dk);
+uint64_t gdr_img_b_bytes(int64_t Dk, Dtype dt);
 // Bytes of qk_ws and pack_ws.
 uint64_t gdr_qk_bytes(const GdrArgs& a, Dtype dt, int nc);
 uint64_t gdr_pack_bytes(const GdrArgs& a, int nc);
 unsigned read_and_clear_fault_gdr();
 unsigned read_and_clear_fault_gdr_bwd();
+unsigned read_and_clear_fault_gdr_grad();
 
 struct LnArgs {
   const void* x;

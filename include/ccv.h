@@ -408,7 +408,7 @@ ccv_status ccv_gdr_step(const void* q, const int64_t q_strides[4], const void* k
  *                     [B,L,Hv] in dtype.  All five are required.
  *   dinitial_state    FP32 [B,Hv,Dk,Dv] or NULL; needs initial_state.
  *   workspace         ccv_gdr_bwd_workspace_size() bytes, 128-byte aligned.
- *   Dk                1..128.
+ *   Dk                1..128;  Dv  1..512.
  *
  * All sums are FP32 or better, in a fixed order (bitwise reproducible), with
  * one rounding to the output's type.  dg is zero at a sequence's first token
