@@ -187,6 +187,15 @@ __device__ __forceinline__ void split2f(float x, float y, uint64_t f, uint32_t& 
   lo = h2(a, b);
 }
 
+// Elements 0, 1 (row g) or 2, 3 (row g + 8) of an accumulator tile as a pair.
+__device__ __forceinline__ uint64_t pair_of(const float (&x)[4], int row) { return pk(x[2 * row], x[2 * row + 1]); }
+__device__ __forceinline__ void set_pair(float (&x)[4], int row, uint64_t v) { upk(v, x[2 * row], x[2 * row + 1]); }
+__device__ __forceinline__ uint64_t both(float x) { return pk(x, x); }
+__device__ __forceinline__ uint64_t ld_pair(const float* p) {
+  const float2 x = *reinterpret_cast<const float2*>(p);
+  return pk(x.x, x.y);
+}
+
 // max(m, |x|, |y|), NaN where one of them is.
 __device__ __forceinline__ float amax3(float m, float x, float y) {
   float d;

@@ -376,11 +376,20 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
       // true values, and the other half's share; O: this warp's tokens are 16 np0.. and 16 np1..
       const int np0 = H == 2 ? half : 0, np1 = H == 2 ? 3 - half : 0;
       float qo[H == 2 ? 4 : 1][4];
+      if constexpr (H == 2) {
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        ks[n][0] *= si0, ks[n][1] *= si0, ks[n][2] *= si1, ks[n][3] *= si1;
-        if constexpr (!SAVE) qs[n][0] *= si0, qs[n][1] *= si0, qs[n][2] *= si1, qs[n][3] *= si1;
+        for (int n = 0; n < 8; ++n) {
+          set_pair(ks[n], 0, fmul2(pair_of(ks[n], 0), both(si0)));
+          set_pair(ks[n], 1, fmul2(pair_of(ks[n], 1), both(si1)));
+          if constexpr (!SAVE) {
+            set_pair(qs[n], 0, fmul2(pair_of(qs[n], 0), both(si0)));
+            set_pair(qs[n], 1, fmul2(pair_of(qs[n], 1), both(si1)));
+          }
+        }
       }
+      // what is left of the state's factors to be taken out (with two warps: nothing)
+      const uint64_t ks0 = both(H == 2 ? -1.f : -si0), ks1 = both(H == 2 ? -1.f : -si1);
+      const uint64_t qs0 = both(H == 2 ? 1.f : si0), qs1 = both(H == 2 ? 1.f : si1);
       if constexpr (H == 2) {
         float4* x4 = reinterpret_cast<float4*>(xb);
         const float4* o4 = reinterpret_cast<const float4*>(xo);
@@ -439,12 +448,10 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int n = 2 * np + t;
-          const float2 cf = *reinterpret_cast<const float2*>(slot + kVKS * kC + n * 8 + qd * 2);
-          const float2 be = *reinterpret_cast<const float2*>(slot + kVBeta * kC + n * 8 + qd * 2);
-          ks[n][0] = be.x * (x[t][0] - cf.x * ks[n][0]);
-          ks[n][1] = be.y * (x[t][1] - cf.y * ks[n][1]);
-          ks[n][2] = be.x * (x[t][2] - cf.x * ks[n][2]);
-          ks[n][3] = be.y * (x[t][3] - cf.y * ks[n][3]);
+          const uint64_t cf = ld_pair(slot + kVKS * kC + n * 8 + qd * 2), be = ld_pair(slot + kVBeta * kC + n * 8 + qd * 2);
+          const uint64_t c0 = fmul2(cf, ks0), c1 = H == 2 ? c0 : fmul2(cf, ks1);
+          set_pair(ks[n], 0, fmul2(be, ffma2(c0, pair_of(ks[n], 0), pair_of(x[t], 0))));
+          set_pair(ks[n], 1, fmul2(be, ffma2(c1, pair_of(ks[n], 1), pair_of(x[t], 1))));
         }
       }
       uint32_t hi[4][4], lo[4][4];
@@ -494,11 +501,11 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
           }
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            const float2 ti = *reinterpret_cast<const float2*>(slot + kVTInv * kC + (2 * np + t) * 8 + qd * 2);
-            u[2 * np + t][0] = (x[0][t][0] + x[1][t][0]) * (ti.x * ri0);
-            u[2 * np + t][1] = (x[0][t][1] + x[1][t][1]) * (ti.y * ri0);
-            u[2 * np + t][2] = (x[0][t][2] + x[1][t][2]) * (ti.x * ri1);
-            u[2 * np + t][3] = (x[0][t][3] + x[1][t][3]) * (ti.y * ri1);
+            const uint64_t ti = ld_pair(slot + kVTInv * kC + (2 * np + t) * 8 + qd * 2);
+            set_pair(u[2 * np + t], 0,
+                     fmul2(fadd2(pair_of(x[0][t], 0), pair_of(x[1][t], 0)), fmul2(ti, both(ri0))));
+            set_pair(u[2 * np + t], 1,
+                     fmul2(fadd2(pair_of(x[0][t], 1), pair_of(x[1][t], 1)), fmul2(ti, both(ri1))));
           }
         }
         if constexpr (SAVE) {
@@ -532,13 +539,10 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               const int n = 2 * np + t;
-              const float* qv = H == 1 ? qs[2 * i + t] : qo[H == 2 ? 2 * i + t : 0];
-              const float2 cq = *reinterpret_cast<const float2*>(slot + kVQS * kC + n * 8 + qd * 2);
-              const float2 cp = *reinterpret_cast<const float2*>(slot + kVP * kC + n * 8 + qd * 2);
-              x[t][0] = fmaf(cp.x * ui0, x[t][0], cq.x * qv[0]);
-              x[t][1] = fmaf(cp.y * ui0, x[t][1], cq.y * qv[1]);
-              x[t][2] = fmaf(cp.x * ui1, x[t][2], cq.x * qv[2]);
-              x[t][3] = fmaf(cp.y * ui1, x[t][3], cq.y * qv[3]);
+              const float(&qv)[4] = H == 1 ? qs[2 * i + t] : qo[H == 2 ? 2 * i + t : 0];
+              const uint64_t cq = ld_pair(slot + kVQS * kC + n * 8 + qd * 2), cp = ld_pair(slot + kVP * kC + n * 8 + qd * 2);
+              set_pair(x[t], 0, ffma2(fmul2(cp, both(ui0)), pair_of(x[t], 0), fmul2(fmul2(cq, qs0), pair_of(qv, 0))));
+              set_pair(x[t], 1, ffma2(fmul2(cp, both(ui1)), pair_of(x[t], 1), fmul2(fmul2(cq, qs1), pair_of(qv, 1))));
             }
             if (DT != kF32 && wovec) {
               if constexpr (DT != kF32) {
@@ -571,8 +575,9 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
         // S^T <- ga S^T + (gc U)^T K
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-          const float2 cu = *reinterpret_cast<const float2*>(slot + kVU * kC + n * 8 + qd * 2);
-          u[n][0] *= cu.x, u[n][1] *= cu.y, u[n][2] *= cu.x, u[n][3] *= cu.y;
+          const uint64_t cu = ld_pair(slot + kVU * kC + n * 8 + qd * 2);
+          set_pair(u[n], 0, fmul2(cu, pair_of(u[n], 0)));
+          set_pair(u[n], 1, fmul2(cu, pair_of(u[n], 1)));
         }
         float ui0, ui1;
         bool ignore = false;
@@ -603,10 +608,8 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int n = n4 * 4 + i;
-            st[n][0] = fmaf(ga, st[n][0], ui0 * x[i][0]);
-            st[n][1] = fmaf(ga, st[n][1], ui0 * x[i][1]);
-            st[n][2] = fmaf(ga, st[n][2], ui1 * x[i][2]);
-            st[n][3] = fmaf(ga, st[n][3], ui1 * x[i][3]);
+            set_pair(st[n], 0, ffma2(both(ui0), pair_of(x[i], 0), fmul2(both(ga), pair_of(st[n], 0))));
+            set_pair(st[n], 1, ffma2(both(ui1), pair_of(x[i], 1), fmul2(both(ga), pair_of(st[n], 1))));
           }
         }
       }
