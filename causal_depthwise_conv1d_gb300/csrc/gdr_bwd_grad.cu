@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 4; ++e) {
           const int j = j0 + (e & 1), i = e < 2 ? i0 : i1;
           const bool in = j <= i && ((e & 1) ? sj.y : sj.x) == (e < 2 ? s0 : s1);
-          const float gam = ex2_approx(((e < 2 ? gh0 : gh1) - ((e & 1) ? gj.y : gj.x)) +
+          const float gam = exp2f(((e < 2 ? gh0 : gh1) - ((e & 1) ? gj.y : gj.x)) +
                                        ((e < 2 ? gl0 : gl1) - ((e & 1) ? lj.y : lj.x)));
           dp[n][e] = in ? pu(dp[n][e]) * (a.scale * gam) : 0.f;
           dl[n][e] = in && j < i ? -(pr(dl[n][e]) * gam) : 0.f;

@@ -54,9 +54,8 @@ constexpr int kVecBytes = 4096;
 constexpr int kVecFwdBytes = (kVecHead + 6 * kC) * 4;  // what the forward scan reads
 static_assert((kVecHead + kVSlots * kC) * 4 <= kVecBytes, "vector part");
 constexpr int kMatBytes = kC * kC * 2;                     // one FP16 64 x 64 matrix
-constexpr int kPadBytes = 1024;                            // L, as FP32 with padded rows, lies where T goes
-constexpr int kOffP = kVecBytes + 2 * kMatBytes + kPadBytes;
-constexpr int kPackBytes = kOffP + 2 * kMatBytes;          // factors, T hi, T lo, padding, P hi, P lo
+constexpr int kOffP = kVecBytes + 2 * kMatBytes;
+constexpr int kPackBytes = kOffP + 2 * kMatBytes;          // factors, T hi, T lo, P hi, P lo
 
 // Bytes of the [64, DK] FP16 tiles of k and q of one chunk and key head
 // (hi, and lo for FP32 inputs): k hi, (k lo,) q hi, (q lo).

@@ -11,8 +11,8 @@
 // This is as stable as substitution and has 16 + 4 dependent steps instead of 64.
 //
 // What bounds it: latency (the steps follow one another), so shared memory is
-// kept small enough for three blocks an SM: L lies where T goes, and the
-// inverse where k and q were.
+// kept small enough for several blocks an SM: the inverse and L lie where k and
+// q were, and T where L was.
 //
 // The results leave as bulk copies of the shared-memory image that the scan
 // reads back, already in its tile order.
@@ -23,15 +23,14 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kLd = 68;  // leading dimension of L and X
-static_assert(kC * kLd * 4 <= 2 * kMatBytes + kPadBytes, "L fits where T goes");
 
 template <int DT, int DK>
 struct PrepSmem {
   static constexpr int TERMS = DT == kF32 ? 2 : 1;
   static constexpr int QK = qk_pack_bytes(DK, TERMS);
   static constexpr int MAT = kC * kLd * 4;
-  static constexpr int FIRST = QK > MAT ? QK : MAT;  // k and q, then X
-  static constexpr int BYTES = FIRST + kPackBytes + 6 * kC * 4 + 64;
+  static constexpr int FIRST = QK > 2 * MAT ? QK : 2 * MAT;  // k and q, then X and L, and T over L
+  static constexpr int BYTES = FIRST + kVecBytes + 2 * kMatBytes + 6 * kC * 4 + 64;
 };
 
 // Eight rows of k or q a warp to FP16 tiles, each row scaled by its power of
@@ -196,8 +195,8 @@ __device__ __forceinline__ void invert(const float* L, float* X) {
 }
 
 template <int DT, int DK>
-__global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 3)
-    gdr_prep_kernel(const GdrArgs a, uint8_t* qk_ws, uint8_t* pack_ws, int nc, bool vec) {
+__global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
+    gdr_prep_kernel(const GdrArgs a, uint8_t* qk_ws, uint8_t* pack_ws, int nc, bool vec, bool plo) {
   pdl_enter();
   using S = PrepSmem<DT, DK>;
   using F = Fmt<DT>;
@@ -213,12 +212,12 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 3)
   uint8_t* pack = sm + S::FIRST;
   float* vecs = reinterpret_cast<float*>(pack);
   float* slot = vecs + kVecHead;
-  uint8_t* th = pack + kVecBytes;
+  float* L = X + kC * kLd;
+  uint8_t* th = reinterpret_cast<uint8_t*>(L);  // once the inverse is done
   uint8_t* tl = th + kMatBytes;
-  uint8_t* ph = pack + kOffP;
+  uint8_t* ph = pack + kVecBytes;
   uint8_t* pl = ph + kMatBytes;
-  float* L = reinterpret_cast<float*>(th);  // until T is written
-  float* kinv = reinterpret_cast<float*>(pack + kPackBytes);
+  float* kinv = reinterpret_cast<float*>(pl + kMatBytes);
   float* qinv = kinv + kC;
   float* ghi = qinv + kC;
   float* glo = ghi + kC;
@@ -408,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 3)
         for (int e = 0; e < 4; ++e) {
           const int j = j0 + (e & 1), i = e < 2 ? i0 : i1;
           const bool in = j <= i && ((e & 1) ? sj.y : sj.x) == (e < 2 ? s0 : s1);
-          const float gam = ex2_approx(((e < 2 ? gh0 : gh1) - ((e & 1) ? gj.y : gj.x)) +
+          const float gam = exp2f(((e < 2 ? gh0 : gh1) - ((e & 1) ? gj.y : gj.x)) +
                                        ((e < 2 ? gl0 : gl1) - ((e & 1) ? lj.y : lj.x)));
           // selected, not multiplied: nothing crosses the diagonal or a new sequence
           p[n][e] = in ? gam * qq[n][e] : 0.f;
@@ -443,11 +442,11 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 3)
         split2f(p[n][0], p[n][1], w0, hi, lo);
         uint32_t off = tile_off<128>(i0, wc * 4 + n) + qd * 4;
         *reinterpret_cast<uint32_t*>(ph + off) = hi;
-        *reinterpret_cast<uint32_t*>(pl + off) = lo;
+        if (plo) *reinterpret_cast<uint32_t*>(pl + off) = lo;
         split2f(p[n][2], p[n][3], w1, hi, lo);
         off = tile_off<128>(i1, wc * 4 + n) + qd * 4;
         *reinterpret_cast<uint32_t*>(ph + off) = hi;
-        *reinterpret_cast<uint32_t*>(pl + off) = lo;
+        if (plo) *reinterpret_cast<uint32_t*>(pl + off) = lo;
       }
     }
     invert(L, X);
@@ -481,7 +480,10 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 3)
       vecs[kHdBad] = *flag ? 1.f : 0.f;
       *flag &= 1u;  // k and q are shared by the next head, its own factors are not
       fence_proxy_async_smem();
-      bulk_store(pack_ws + ((b * a.Hv + h) * nc + c) * kPackBytes, pack, kPackBytes);
+      uint8_t* dst = pack_ws + ((b * a.Hv + h) * nc + c) * kPackBytes;
+      bulk_store(dst, pack, kVecBytes);
+      bulk_store(dst + kVecBytes, th, 2 * kMatBytes);
+      bulk_store(dst + kOffP, ph, plo ? 2 * kMatBytes : kMatBytes);
       bulk_commit();
     }
   }
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 3)
 }
 
 template <int DT, int DK>
-cudaError_t launch(const GdrArgs& a, uint8_t* qk_ws, uint8_t* pack_ws, int nc, cudaStream_t s) {
+cudaError_t launch(const GdrArgs& a, uint8_t* qk_ws, uint8_t* pack_ws, int nc, bool plo, cudaStream_t s) {
   constexpr int64_t V = Fmt<DT>::VEC;
   auto ok = [&](const void* p, const int64_t* st) {
     return st[3] == 1 && a.Dk == DK && reinterpret_cast<uintptr_t>(p) % 16 == 0 && st[0] % V == 0 && st[1] % V == 0 &&
@@ -501,21 +503,23 @@ cudaError_t launch(const GdrArgs& a, uint8_t* qk_ws, uint8_t* pack_ws, int nc, c
       cudaFuncSetAttribute(gdr_prep_kernel<DT, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(gdr_prep_kernel<DT, DK>, static_cast<unsigned>(a.B * a.Hk * nc), kThreads, smem, s, a, qk_ws,
-                    pack_ws, nc, vec);
+                    pack_ws, nc, vec, plo);
 }
 
 template <int DT>
-cudaError_t launch_dt(const GdrArgs& a, uint8_t* q, uint8_t* p, int nc, cudaStream_t s) {
-  return a.Dk <= 64 ? launch<DT, 64>(a, q, p, nc, s) : launch<DT, 128>(a, q, p, nc, s);
+cudaError_t launch_dt(const GdrArgs& a, uint8_t* q, uint8_t* p, int nc, bool plo, cudaStream_t s) {
+  return a.Dk <= 64 ? launch<DT, 64>(a, q, p, nc, plo, s) : launch<DT, 128>(a, q, p, nc, plo, s);
 }
 
 }  // namespace
 
-cudaError_t launch_gdr_prep(const GdrArgs& a, Dtype dt, uint8_t* qk_ws, uint8_t* pack_ws, int nc, cudaStream_t s) {
+cudaError_t launch_gdr_prep(const GdrArgs& a, Dtype dt, uint8_t* qk_ws, uint8_t* pack_ws, int nc, bool backward,
+                            cudaStream_t s) {
+  const bool plo = backward || dt != kBF16;  // a bf16 output takes P's first 11 bits alone
   switch (dt) {
-    case kF32: return launch_dt<kF32>(a, qk_ws, pack_ws, nc, s);
-    case kF16: return launch_dt<kF16>(a, qk_ws, pack_ws, nc, s);
-    case kBF16: return launch_dt<kBF16>(a, qk_ws, pack_ws, nc, s);
+    case kF32: return launch_dt<kF32>(a, qk_ws, pack_ws, nc, plo, s);
+    case kF16: return launch_dt<kF16>(a, qk_ws, pack_ws, nc, plo, s);
+    case kBF16: return launch_dt<kBF16>(a, qk_ws, pack_ws, nc, plo, s);
   }
   return cudaErrorInvalidValue;
 }

@@ -44,7 +44,7 @@ struct ScanCfg {
   static constexpr bool OLO = DT != kBF16;
   static constexpr int TILE = qk_tile_bytes(DK);
   static constexpr int QKB = SAVE ? TERMS * TILE : 2 * TERMS * TILE;  // k alone, or k and q
-  static constexpr int MATB = SAVE ? 2 * kMatBytes : 2 * kMatBytes + kPadBytes + (OLO ? 2 : 1) * kMatBytes;
+  static constexpr int MATB = SAVE ? 2 * kMatBytes : (OLO ? 4 : 3) * kMatBytes;
   static constexpr int STAGE = QKB + kVecBytes + MATB;
   static constexpr int VROW = DT == kF32 ? 64 : 32;            // bytes of a warp's 16 channels of one token
   static constexpr int VBYTES = kC * VROW;
