@@ -27,6 +27,18 @@ constexpr int kCols = 4;                    // columns of a warp
 constexpr int kBlockCols = kWarps * kCols;
 constexpr int kTok = 8;                     // tokens of one stage: one a warp
 
+// A store under a predicate instead of a branch: the token loop stays converged.
+__device__ __forceinline__ void store_if(uint16_t* p, uint16_t v, bool on) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.u16 [%0], %1;\n\t}" ::"l"(p), "h"(v),
+               "r"(static_cast<uint32_t>(on))
+               : "memory");
+}
+__device__ __forceinline__ void store_if(uint32_t* p, uint32_t v, bool on) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.u32 [%0], %1;\n\t}" ::"l"(p), "r"(v),
+               "r"(static_cast<uint32_t>(on))
+               : "memory");
+}
+
 template <int DT, int R>
 __global__ void __launch_bounds__(kThreads) gdr_token_kernel(const GdrArgs a, int tiles, bool svec, bool kvec) {
   using F = Fmt<DT>;
@@ -130,6 +142,9 @@ __global__ void __launch_bounds__(kThreads) gdr_token_kernel(const GdrArgs a, in
 
   const int vi = lane >> 2;   // the sum this lane holds after the exchange: p of column 0..3, r of column 0..3
   const int vc = vi & 3;
+  // lanes 16, 20, 24, 28 write the outputs of the four columns
+  const bool writes = lane >= 16 && (lane & 3) == 0 && col + vc < Dv;
+  E* op = static_cast<E*>(a.out) + b * a.os[0] + h * a.os[2] + (col + vc) * a.os[3];
   int st = 0;
   for (int64_t t0 = 0; t0 < a.L; t0 += kTok, st ^= 1) {
     const int nt = static_cast<int>(a.L - t0 < kTok ? a.L - t0 : kTok);
@@ -139,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) gdr_token_kernel(const GdrArgs a, in
       const float4 gate = sg[st][t];
       const float vv = sv[st][t][warp * kCols + vc];
       float dec = gate.x;
-      if (gate.w != 0.f) {  // selected, not multiplied: a state with infinities must not leak
+      if (__any_sync(kFullMask, gate.w != 0.f)) {  // selected, not multiplied: a state with infinities must not leak
         dec = 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i)
@@ -185,11 +200,9 @@ __global__ void __launch_bounds__(kThreads) gdr_token_kernel(const GdrArgs a, in
       float u[kCols];
 #pragma unroll
       for (int j = 0; j < kCols; ++j) u[j] = __shfl_sync(kFullMask, uw, 4 * j);
-      if (lane >= 16 && (lane & 3) == 0 && col + vc < Dv) {
-        const float uc = vc < 2 ? (vc == 0 ? u[0] : u[1]) : (vc == 2 ? u[2] : u[3]);
-        static_cast<E*>(a.out)[b * a.os[0] + (t0 + t) * a.os[1] + h * a.os[2] + (col + vc) * a.os[3]] =
-            F::from_f(a.scale * fmaf(gate.z, uc, dec * w));
-      }
+      const float uc = vc < 2 ? (vc == 0 ? u[0] : u[1]) : (vc == 2 ? u[2] : u[3]);
+      store_if(op, F::from_f(a.scale * fmaf(gate.z, uc, dec * w)), writes);
+      op += a.os[1];
 #pragma unroll
       for (int i = 0; i < R; ++i)
 #pragma unroll

@@ -104,6 +104,22 @@ __device__ __forceinline__ void block_sum(float (&v)[NS], float* red, int nwarps
     }
 }
 
+// The vector at p as pairs; zeros where it lies outside the row.
+template <int DT>
+__device__ __forceinline__ void load_pairs(const uint8_t* p, bool in, uint64_t* f) {
+  constexpr int V = Fmt<DT>::VEC;
+  float x[V];
+  unpack16<DT>(in ? lds128(p) : make_uint4(0, 0, 0, 0), x);
+#pragma unroll
+  for (int j = 0; j < V / 2; ++j) f[j] = pk(x[2 * j], x[2 * j + 1]);
+}
+
+__device__ __forceinline__ float pair_sum(uint64_t v) {
+  float a, b;
+  upk(v, a, b);
+  return a + b;
+}
+
 // V parameters from column col: one or two vector loads where the vector is
 // dense and aligned (`vec`).
 template <int V>
@@ -214,14 +230,21 @@ __global__ void __launch_bounds__(512) ln_fwd_ring(const LnArgs a, int stages) {
   pdl_enter();
   if (t == 0)
     for (int s = 0; s < stages && blockIdx.x + s * step < a.N; ++s) fill(blockIdx.x + s * step, s);
-  float w[NV][V], b[NV][V];
+  // elements in pairs: packed arithmetic
+  constexpr int H = V / 2;
+  uint64_t w[NV][H], b[NV][H];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int64_t col = (static_cast<int64_t>(i) * T + t) * V;
+    float pw[V], pb[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) pw[j] = pb[j] = 0.f;
     if (col < a.D) {
-      load_par_vec<V>(a.w, col, a.ws, a.wdt, a.wvec, 1.f, w[i]);
-      load_par_vec<V>(a.b, col, a.bs, a.wdt, a.wvec, 0.f, b[i]);
+      load_par_vec<V>(a.w, col, a.ws, a.wdt, a.wvec, 1.f, pw);
+      load_par_vec<V>(a.b, col, a.bs, a.wdt, a.wvec, 0.f, pb);
     }
+#pragma unroll
+    for (int j = 0; j < H; ++j) w[i][j] = pk(pw[2 * j], pw[2 * j + 1]), b[i][j] = pk(pb[2 * j], pb[2 * j + 1]);
   }
   __syncthreads();
   const float inv_d = 1.f / static_cast<float>(a.D);
@@ -236,44 +259,44 @@ __global__ void __launch_bounds__(512) ln_fwd_ring(const LnArgs a, int stages) {
       }
       return;
     }
-    float f[NV][V];
-    float sum[1] = {0.f};
+    uint64_t f[NV][H];
+    uint64_t acc = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * T + t) * V;
-      if (col < a.D) {
-        unpack16<DT>(lds128(ring + s * row_bytes + col * sizeof(E)), f[i]);
-      } else {
+      load_pairs<DT>(ring + s * row_bytes + col * sizeof(E), col < a.D, f[i]);
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[i][j] = 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j) sum[0] += f[i][j];
+      for (int j = 0; j < H; ++j) acc = fadd2(acc, f[i][j]);
     }
+    float sum[1] = {pair_sum(acc)};
     block_sum(sum, red[0], nwarps);
     if (t == 0 && row + stages * step < a.N) fill(row + stages * step, s);
     if (++s == stages) s = 0, parity ^= 1;
     const float mean = sum[0] * inv_d;
-    float q[1] = {0.f};
+    const uint64_t minus = pk(-mean, -mean);
+    acc = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const bool in = (i * T + t) * V < a.D;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        f[i][j] -= mean;
-        if (in) q[0] = fmaf(f[i][j], f[i][j], q[0]);
+      for (int j = 0; j < H; ++j) {
+        f[i][j] = fadd2(f[i][j], minus);
+        if (in) acc = ffma2(f[i][j], f[i][j], acc);
       }
     }
+    float q[1] = {pair_sum(acc)};
     block_sum(q, red[1], nwarps);
     const float r = rsqrtf(q[0] * inv_d + a.eps);
+    const uint64_t r2 = pk(r, r);
     E* y = static_cast<E*>(a.out) + row * a.os0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * T + t) * V;
       if (col < a.D) {
+        float o[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[i][j] = fmaf(f[i][j] * r, w[i][j], b[i][j]);
-        *reinterpret_cast<uint4*>(y + col) = pack16<DT>(f[i]);
+        for (int j = 0; j < H; ++j) upk(ffma2(fmul2(f[i][j], r2), w[i][j], b[i][j]), o[2 * j], o[2 * j + 1]);
+        *reinterpret_cast<uint4*>(y + col) = pack16<DT>(o);
       }
     }
   }
@@ -436,13 +459,21 @@ __global__ void __launch_bounds__(MAXT) ln_bwd_ring(const LnBwdArgs a, int stage
   pdl_enter();
   if (t == 0)
     for (int s = 0; s < stages && blockIdx.x + s * step < a.N; ++s) fill(blockIdx.x + s * step, s);
-  float w[NV][V], dw[NV][V], db[NV][V];
+  // elements in pairs: packed arithmetic
+  constexpr int H = V / 2;
+  uint64_t w[NV][H], dw[NV][H], db[NV][H];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int64_t col = (static_cast<int64_t>(i) * T + t) * V;
+    float pw[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) dw[i][j] = db[i][j] = w[i][j] = 0.f;
-    if (col < a.D) load_par_vec<V>(a.w, col, a.ws, a.wdt, a.wvec, 1.f, w[i]);
+    for (int j = 0; j < V; ++j) pw[j] = 0.f;
+    if (col < a.D) load_par_vec<V>(a.w, col, a.ws, a.wdt, a.wvec, 1.f, pw);
+#pragma unroll
+    for (int j = 0; j < H; ++j) {
+      w[i][j] = pk(pw[2 * j], pw[2 * j + 1]);
+      dw[i][j] = db[i][j] = 0;
+    }
   }
   __syncthreads();
   const float inv_d = 1.f / static_cast<float>(a.D);
@@ -457,53 +488,54 @@ __global__ void __launch_bounds__(MAXT) ln_bwd_ring(const LnBwdArgs a, int stage
       }
       return;
     }
-    float f[NV][V], d[NV][V];
-    float sum[1] = {0.f};
+    uint64_t f[NV][H], d[NV][H];
+    uint64_t acc = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * T + t) * V;
-      if (col < a.D) {
-        unpack16<DT>(lds128(ring + 2 * s * row_bytes + col * sizeof(E)), f[i]);
-        unpack16<DT>(lds128(ring + (2 * s + 1) * row_bytes + col * sizeof(E)), d[i]);
-      } else {
+      load_pairs<DT>(ring + 2 * s * row_bytes + col * sizeof(E), col < a.D, f[i]);
+      load_pairs<DT>(ring + (2 * s + 1) * row_bytes + col * sizeof(E), col < a.D, d[i]);
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[i][j] = d[i][j] = 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j) sum[0] += f[i][j];
+      for (int j = 0; j < H; ++j) acc = fadd2(acc, f[i][j]);
     }
+    float sum[1] = {pair_sum(acc)};
     block_sum(sum, red0, nwarps);
     if (t == 0 && row + stages * step < a.N) fill(row + stages * step, s);
     if (++s == stages) s = 0, parity ^= 1;
     const float mean = sum[0] * inv_d;
-    float q[3] = {0.f, 0.f, 0.f};
+    const uint64_t minus = pk(-mean, -mean);
+    uint64_t a0 = 0, a1 = 0, a2 = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const bool in = (i * T + t) * V < a.D;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        f[i][j] = in ? f[i][j] - mean : 0.f;
-        q[0] = fmaf(f[i][j], f[i][j], q[0]);
-        const float dd = d[i][j] * w[i][j];
-        q[1] += dd;
-        q[2] = fmaf(dd, f[i][j], q[2]);
+      for (int j = 0; j < H; ++j) {
+        f[i][j] = in ? fadd2(f[i][j], minus) : 0;
+        a0 = ffma2(f[i][j], f[i][j], a0);
+        const uint64_t dd = fmul2(d[i][j], w[i][j]);
+        a1 = fadd2(a1, dd);
+        a2 = ffma2(dd, f[i][j], a2);
       }
     }
+    float q[3] = {pair_sum(a0), pair_sum(a1), pair_sum(a2)};
     block_sum(q, red1, nwarps);
     const float r = rsqrtf(q[0] * inv_d + a.eps);
     const float c1 = q[1] * inv_d, c2 = q[2] * inv_d * r;
+    // dx = r (d w - c1 - xh c2) = (r w) d + (-r c1) + (-r c2) xh
+    const uint64_t r2 = pk(r, r), rc1 = pk(-r * c1, -r * c1), rc2 = pk(-r * c2, -r * c2);
     E* dx = static_cast<E*>(a.dx) + row * a.dxs0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * T + t) * V;
+      float o[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float xh = f[i][j] * r;
-        dw[i][j] = fmaf(d[i][j], xh, dw[i][j]);
-        db[i][j] += d[i][j];
-        f[i][j] = r * (d[i][j] * w[i][j] - c1 - xh * c2);
+      for (int j = 0; j < H; ++j) {
+        const uint64_t xh = fmul2(f[i][j], r2);
+        dw[i][j] = ffma2(d[i][j], xh, dw[i][j]);
+        db[i][j] = fadd2(db[i][j], d[i][j]);
+        upk(ffma2(fmul2(d[i][j], w[i][j]), r2, ffma2(xh, rc2, rc1)), o[2 * j], o[2 * j + 1]);
       }
-      if (col < a.D) *reinterpret_cast<uint4*>(dx + col) = pack16<DT>(f[i]);
+      if (col < a.D) *reinterpret_cast<uint4*>(dx + col) = pack16<DT>(o);
     }
   }
   if (a.part == nullptr) return;
@@ -513,10 +545,14 @@ __global__ void __launch_bounds__(MAXT) ln_bwd_ring(const LnBwdArgs a, int stage
     const int64_t col = (static_cast<int64_t>(i) * T + t) * V;
     if (col < a.D)
 #pragma unroll
-      for (int j = 0; j < V; j += 4) {
-        *reinterpret_cast<float4*>(part + col + j) = make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
-        *reinterpret_cast<float4*>(part + a.D + col + j) =
-            make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]);
+      for (int j = 0; j < H; j += 2) {
+        float x[4];
+        upk(dw[i][j], x[0], x[1]);
+        upk(dw[i][j + 1], x[2], x[3]);
+        *reinterpret_cast<float4*>(part + col + 2 * j) = make_float4(x[0], x[1], x[2], x[3]);
+        upk(db[i][j], x[0], x[1]);
+        upk(db[i][j + 1], x[2], x[3]);
+        *reinterpret_cast<float4*>(part + a.D + col + 2 * j) = make_float4(x[0], x[1], x[2], x[3]);
       }
   }
 }
