@@ -147,8 +147,8 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, const GdrGrads& gr
 
 template <int DT, int DK, int NW, int H>
 __global__ void __launch_bounds__(32 * NW * H, 1)
-    gdr_bwd_scan_kernel(const GdrArgs a, const GdrGrads gr, const GdrBwdWs w, int nc, int vtiles, bool gvec,
-                        bool vvec, bool ovec) {
+    gdr_bwd_scan_kernel(const GdrArgs a, const GdrGrads gr, const GdrBwdWs w, int nc, int64_t head0, int vtiles,
+                        bool gvec, bool vvec, bool ovec) {
   pdl_enter();
   using C = Cfg<DT, DK, NW, H>;
   using F = Fmt<DT>;
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, qd = lane & 3;
-  const int64_t bh = blockIdx.x / vtiles;
+  const int64_t bh = head0 + blockIdx.x / vtiles;
   const int64_t b = bh / a.Hv, h = bh - b * a.Hv;
   const int64_t hk = h / (a.Hv / a.Hk);
   const int grp = warp / H, half = warp % H;
@@ -633,7 +633,8 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
 }
 
 template <int DT, int DK, int NW, int H>
-cudaError_t launch(const GdrArgs& a, const GdrGrads& g, const GdrBwdWs& w, int nc, cudaStream_t s) {
+cudaError_t launch(const GdrArgs& a, const GdrGrads& g, const GdrBwdWs& w, int nc, int64_t head0, int64_t heads,
+                   cudaStream_t s) {
   using C = Cfg<DT, DK, NW, H>;
   static_assert(C::BYTES <= 232448, "shared memory of one block");
   using E = typename Fmt<DT>::E;
@@ -645,17 +646,26 @@ cudaError_t launch(const GdrArgs& a, const GdrGrads& g, const GdrBwdWs& w, int n
   const cudaError_t e =
       cudaFuncSetAttribute(gdr_bwd_scan_kernel<DT, DK, NW, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e != cudaSuccess) return e;
-  return launch_pdl(gdr_bwd_scan_kernel<DT, DK, NW, H>, static_cast<unsigned>(a.B * a.Hv * vtiles), 32 * C::WARPS, C::BYTES, s,
-                    a, g, w, nc, vtiles, al(g.dout, g.dos), al(a.v, a.vs), al(g.dv, g.dvs));
+  return launch_pdl(gdr_bwd_scan_kernel<DT, DK, NW, H>, static_cast<unsigned>(heads * vtiles), 32 * C::WARPS,
+                    C::BYTES, s, a, g, w, nc, head0, vtiles, al(g.dout, g.dos), al(a.v, a.vs), al(g.dv, g.dvs));
 }
 
 template <int DT, int DK>
 cudaError_t launch_nw(const GdrArgs& a, const GdrGrads& g, const GdrBwdWs& w, int nc, const Device& dev,
                       cudaStream_t s) {
-  // as in the forward scan; the tiles that go to the workspace leave no room for eight groups a block
+  // As in the forward scan; the tiles that go to the workspace leave no room
+  // for eight groups a block.
+  constexpr int H2 = DT == kF32 ? 1 : 2;
   const int64_t heads = a.B * a.Hv, groups = (a.Dv + 15) / 16, sms = dev.sm_count;
-  if (heads * ((groups + 1) / 2) > sms) return launch<DT, DK, 4, 1>(a, g, w, nc, s);
-  return launch<DT, DK, 2, DT == kF32 ? 1 : 2>(a, g, w, nc, s);
+  const int64_t small = (groups + 1) / 2, large = (groups + 3) / 4;  // blocks of a head
+  if (heads * small <= sms) return launch<DT, DK, 2, H2>(a, g, w, nc, 0, heads, s);
+  // heads of a last round that would leave half of the SMs idle take the small blocks
+  const int64_t round = sms / large, rest = round > 0 ? heads % round : 0;
+  if (heads > round && rest > 0 && rest * small <= sms) {
+    const cudaError_t e = launch<DT, DK, 4, 1>(a, g, w, nc, 0, heads - rest, s);
+    return e != cudaSuccess ? e : launch<DT, DK, 2, H2>(a, g, w, nc, heads - rest, rest, s);
+  }
+  return launch<DT, DK, 4, 1>(a, g, w, nc, 0, heads, s);
 }
 
 template <int DT>

@@ -171,8 +171,8 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[NK][4]
 
 template <int DT, int DK, int NW, int H, bool SAVE>
 __global__ void __launch_bounds__(32 * NW * H, 1)
-    gdr_scan_kernel(const GdrArgs a, const uint8_t* qk_ws, const uint8_t* pack_ws, uint8_t* img, int nc, int vtiles,
-                    bool vvec, bool ovec) {
+    gdr_scan_kernel(const GdrArgs a, const uint8_t* qk_ws, const uint8_t* pack_ws, uint8_t* img, int nc, int64_t head0,
+                    int vtiles, bool vvec, bool ovec) {
   pdl_enter();
   using C = ScanCfg<DT, DK, NW, H, SAVE>;
   using F = Fmt<DT>;
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, qd = lane & 3;
-  const int64_t bh = blockIdx.x / vtiles;
+  const int64_t bh = head0 + blockIdx.x / vtiles;
   const int64_t b = bh / a.Hv, h = bh - b * a.Hv;
   const int64_t hk = h / (a.Hv / a.Hk);
   const int grp = warp / H, half = warp % H;
@@ -637,8 +637,13 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
   }
 }
 
+// Heads head0 .. head0 + heads - 1 of the [B, Hv].
+struct Heads {
+  int64_t head0, heads;
+};
+
 template <int DT, int DK, int NW, int H, bool SAVE>
-cudaError_t launch(const GdrArgs& a, const uint8_t* qk, const uint8_t* pkg, uint8_t* img, int nc,
+cudaError_t launch(const GdrArgs& a, const uint8_t* qk, const uint8_t* pkg, uint8_t* img, int nc, Heads hd,
                    cudaStream_t s) {
   using C = ScanCfg<DT, DK, NW, H, SAVE>;
   static_assert(C::BYTES <= 232448, "shared memory of one block");
@@ -651,32 +656,43 @@ cudaError_t launch(const GdrArgs& a, const uint8_t* qk, const uint8_t* pkg, uint
   const cudaError_t e = cudaFuncSetAttribute(gdr_scan_kernel<DT, DK, NW, H, SAVE>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e != cudaSuccess) return e;
-  return launch_pdl(gdr_scan_kernel<DT, DK, NW, H, SAVE>, static_cast<unsigned>(a.B * a.Hv * vtiles), 32 * C::WARPS,
-                    C::BYTES, s, a, qk, pkg, img, nc, vtiles, al(a.v, a.vs), !SAVE && al(a.out, a.os));
+  return launch_pdl(gdr_scan_kernel<DT, DK, NW, H, SAVE>, static_cast<unsigned>(hd.heads * vtiles), 32 * C::WARPS,
+                    C::BYTES, s, a, qk, pkg, img, nc, hd.head0, vtiles, al(a.v, a.vs), !SAVE && al(a.out, a.os));
 }
 
 template <int DT, int DK, bool SAVE>
-cudaError_t launch_nw(const GdrArgs& a, const uint8_t* qk, const uint8_t* pkg, uint8_t* img, int nc, const Device& dev, cudaStream_t s) {
+cudaError_t launch_nw(const GdrArgs& a, const uint8_t* qk, const uint8_t* pkg, uint8_t* img, int nc, Heads hd,
+                      const Device& dev, cudaStream_t s) {
   // Blocks of few channels while that still puts no more than one on an SM.
   // Two warps a group only where one each would leave half the quarters of an
   // SM idle (32 heads, 8192 tokens: 537 -> 368 us; with 64 heads, four groups
   // a block, 119 -> 145 us in the state-keeping scan).
-  const int64_t heads = a.B * a.Hv, groups = (a.Dv + 15) / 16, sms = dev.sm_count;
+  const int64_t groups = (a.Dv + 15) / 16, sms = dev.sm_count;
   if constexpr (DT == kF32) {  // two terms of k and q: the stages leave room for one warp a group, four groups
-    if (heads * ((groups + 1) / 2) <= sms) return launch<DT, DK, 2, 1, SAVE>(a, qk, pkg, img, nc, s);
-    return launch<DT, DK, 4, 1, SAVE>(a, qk, pkg, img, nc, s);
+    if (hd.heads * ((groups + 1) / 2) <= sms) return launch<DT, DK, 2, 1, SAVE>(a, qk, pkg, img, nc, hd, s);
+    return launch<DT, DK, 4, 1, SAVE>(a, qk, pkg, img, nc, hd, s);
   } else {
-    if (heads * ((groups + 1) / 2) <= sms) return launch<DT, DK, 2, 2, SAVE>(a, qk, pkg, img, nc, s);
-    if (heads * ((groups + 3) / 4) <= sms) return launch<DT, DK, 4, 1, SAVE>(a, qk, pkg, img, nc, s);
-    return launch<DT, DK, 8, 1, SAVE>(a, qk, pkg, img, nc, s);
+    if (hd.heads * ((groups + 1) / 2) <= sms) return launch<DT, DK, 2, 2, SAVE>(a, qk, pkg, img, nc, hd, s);
+    if (hd.heads * ((groups + 3) / 4) <= sms) return launch<DT, DK, 4, 1, SAVE>(a, qk, pkg, img, nc, hd, s);
+    // More than one block an SM: full rounds of whole heads, and the heads of
+    // a last round that would not fill the SMs spread over smaller blocks
+    // behind them (a chunk takes 6.2, 3.7 or 2.9 us by the three shapes).
+    const int64_t rest = hd.heads % sms;
+    if (hd.heads > sms && groups <= 8 && rest > 0 && rest * ((groups + 3) / 4) <= sms) {
+      const cudaError_t e =
+          launch<DT, DK, 8, 1, SAVE>(a, qk, pkg, img, nc, Heads{hd.head0, hd.heads - rest}, s);
+      if (e != cudaSuccess) return e;
+      return launch_nw<DT, DK, SAVE>(a, qk, pkg, img, nc, Heads{hd.head0 + hd.heads - rest, rest}, dev, s);
+    }
+    return launch<DT, DK, 8, 1, SAVE>(a, qk, pkg, img, nc, hd, s);
   }
 }
 
 template <int DT, int DK>
 cudaError_t launch_k(const GdrArgs& a, const uint8_t* qk, const uint8_t* pk, uint8_t* img, int nc,
                      const Device& dev, cudaStream_t s) {
-  return img != nullptr ? launch_nw<DT, DK, true>(a, qk, pk, img, nc, dev, s)
-                       : launch_nw<DT, DK, false>(a, qk, pk, img, nc, dev, s);
+  return img != nullptr ? launch_nw<DT, DK, true>(a, qk, pk, img, nc, Heads{0, a.B * a.Hv}, dev, s)
+                       : launch_nw<DT, DK, false>(a, qk, pk, img, nc, Heads{0, a.B * a.Hv}, dev, s);
 }
 
 template <int DT>

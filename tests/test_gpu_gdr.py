@@ -56,6 +56,16 @@ def test_packed_sequences_and_states(size, seqs, dtype):
     check_fwd(c, dtype)
 
 
+MANY = [  # enough heads for every block shape of the scans, a last round of few heads among them
+    (2, 70, 8, 32, 64, 128), (1, 66, 40, 160, 64, 64), (4, 66, 20, 40, 128, 128), (1, 66, 160, 160, 32, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("size", MANY, ids=str)
+def test_many_heads(size, dtype):
+    check_fwd(ref.gdr_inputs(17, *size, dtype, seqs=2, state=True), dtype)
+
+
 def test_a_sequence_that_begins_at_a_chunk_boundary():
     c = ref.gdr_inputs(6, 1, 200, 1, 1, 128, 64, "f32", state=True)
     ids = torch.zeros(1, 200, dtype=torch.int32)
@@ -282,6 +292,12 @@ def test_backward_of_packed_sequences_and_states(size, seqs, dtype):
     first = torch.zeros_like(c["seq_idx"], dtype=torch.bool)
     first[:, 1:] = c["seq_idx"][:, 1:] != c["seq_idx"][:, :-1]
     assert not got["dg"].cpu()[first].any()  # nothing decays into a new sequence
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("size", MANY, ids=str)
+def test_backward_many_heads(size, dtype):
+    check_bwd(ref.gdr_inputs(29, *size, dtype, seqs=2, state=True, grads=True), dtype)
 
 
 def test_backward_against_differences_of_the_forward():

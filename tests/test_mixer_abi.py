@@ -102,7 +102,7 @@ def bwd_args(mx, **kw):
 
 
 @pytest.mark.parametrize("kw,st,needle", [
-    (dict(dtype=4), 1, "unknown dtype"), (dict(Dk=129), 2, "at most 128"), (dict(dout=None), 1, "dout is required"),
+    (dict(dtype=4), 1, "unknown dtype"), (dict(Dk=129), 2, "at most 128"), (dict(Dv=513), 2, "at most 512"), (dict(dout=None), 1, "dout is required"),
     (dict(dq=None), 1, "dq is required"), (dict(dg=None), 1, "dg is required"), (dict(dbeta=None), 1, "dbeta is req"),
     (dict(ds0=13 * F), 1, "requires initial_state"), (dict(ws=None), 1, "workspace too small"),
     (dict(wsb=4096), 1, "workspace too small"), (dict(ws=12 * F + 16), 1, "workspace must be aligned"),
