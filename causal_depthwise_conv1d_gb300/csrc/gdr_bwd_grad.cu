@@ -126,12 +126,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = lane >> 2, qd = lane & 3;
   const int wr = warp & 3, wc = warp >> 2;
   const int i0 = wr * 16 + g, i1 = i0 + 8;
+  // indices below 2^31 (checked on the host): 32-bit divisions
   const int64_t id = blockIdx.x;
-  const int64_t c = id % nc, bk_ = id / nc;
-  const int64_t hk = bk_ % a.Hk, b = bk_ / a.Hk;
+  const unsigned uc = blockIdx.x % static_cast<unsigned>(nc), ubk = blockIdx.x / static_cast<unsigned>(nc);
+  const int64_t c = uc, hk = ubk % static_cast<unsigned>(a.Hk), b = ubk / static_cast<unsigned>(a.Hk);
   const int64_t t0 = c * kC;
   const int nt = static_cast<int>(a.L - t0 < kC ? a.L - t0 : kC);
-  const int64_t rep = a.Hv / a.Hk;
+  const int64_t rep = static_cast<unsigned>(a.Hv) / static_cast<unsigned>(a.Hk);
   const int ns = static_cast<int>((a.Dv + 15) / 16);
   constexpr int BF = ImgF::bytes(DK), BB = ImgB::bytes(DK, C::TERMS);
 

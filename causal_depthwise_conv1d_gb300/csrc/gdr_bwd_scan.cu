@@ -147,7 +147,7 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, const GdrGrads& gr
 
 template <int DT, int DK, int NW, int H>
 __global__ void __launch_bounds__(32 * NW * H, 1)
-    gdr_bwd_scan_kernel(const GdrArgs a, const GdrGrads gr, const GdrBwdWs w, int nc, int64_t head0, int vtiles,
+    gdr_bwd_scan_kernel(const GdrArgs a, const GdrGrads gr, const GdrBwdWs w, int nc, int64_t head0, unsigned vtiles,
                         bool gvec, bool vvec, bool ovec) {
   pdl_enter();
   using C = Cfg<DT, DK, NW, H>;
@@ -167,9 +167,10 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, qd = lane & 3;
-  const int64_t bh = head0 + blockIdx.x / vtiles;
-  const int64_t b = bh / a.Hv, h = bh - b * a.Hv;
-  const int64_t hk = h / (a.Hv / a.Hk);
+  // indices below 2^31 (checked on the host): 32-bit divisions
+  const unsigned Hv = static_cast<unsigned>(a.Hv), ubh = static_cast<unsigned>(head0) + blockIdx.x / vtiles;
+  const unsigned ub = ubh / Hv, uh = ubh - ub * Hv;
+  const int64_t bh = ubh, b = ub, h = uh, hk = uh / (Hv / static_cast<unsigned>(a.Hk));
   const int grp = warp / H, half = warp % H;
   const int64_t v0 = (static_cast<int64_t>(blockIdx.x % vtiles) * NW + grp) * 16;
   const int k0 = half * NK * 8;  // first key channel of this warp
@@ -642,7 +643,7 @@ cudaError_t launch(const GdrArgs& a, const GdrGrads& g, const GdrBwdWs& w, int n
   auto al = [&](const void* p, const int64_t* st) {
     return st[3] == 1 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && st[0] % V == 0 && st[1] % V == 0 && st[2] % V == 0;
   };
-  const int vtiles = static_cast<int>((a.Dv + 16 * NW - 1) / (16 * NW));
+  const unsigned vtiles = static_cast<unsigned>((a.Dv + 16 * NW - 1) / (16 * NW));
   const cudaError_t e =
       cudaFuncSetAttribute(gdr_bwd_scan_kernel<DT, DK, NW, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e != cudaSuccess) return e;

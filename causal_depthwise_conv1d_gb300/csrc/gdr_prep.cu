@@ -228,12 +228,14 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, qd = lane & 3;
   const int wr = warp & 3, wc = warp >> 2;  // 16 rows and 32 columns of the 64 x 64 matrices
+  // indices below 2^31 (checked on the host): 32-bit divisions
   const int64_t id = blockIdx.x;
-  const int64_t c = id % nc, bh = id / nc;
-  const int64_t hk = bh % a.Hk, b = bh / a.Hk;
+  const unsigned uc = blockIdx.x % static_cast<unsigned>(nc), ubh = blockIdx.x / static_cast<unsigned>(nc);
+  const unsigned uhk = ubh % static_cast<unsigned>(a.Hk), ub = ubh / static_cast<unsigned>(a.Hk);
+  const int64_t c = uc, hk = uhk, b = ub;
   const int64_t t0 = c * kC;
   const int nt = static_cast<int>(a.L - t0 < kC ? a.L - t0 : kC);
-  const int64_t rep = a.Hv / a.Hk;
+  const int64_t rep = static_cast<unsigned>(a.Hv) / static_cast<unsigned>(a.Hk);
 
   // warp 0 has the gates: two tokens a lane, those of the next head fetched ahead
   float gv[2] = {0.f, 0.f}, bv[2] = {0.f, 0.f};

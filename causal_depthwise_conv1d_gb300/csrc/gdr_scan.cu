@@ -172,7 +172,7 @@ __device__ __noinline__ void token_by_token(const GdrArgs& a, float (&st)[NK][4]
 template <int DT, int DK, int NW, int H, bool SAVE>
 __global__ void __launch_bounds__(32 * NW * H, 1)
     gdr_scan_kernel(const GdrArgs a, const uint8_t* qk_ws, const uint8_t* pack_ws, uint8_t* img, int nc, int64_t head0,
-                    int vtiles, bool vvec, bool ovec) {
+                    unsigned vtiles, bool vvec, bool ovec) {
   pdl_enter();
   using C = ScanCfg<DT, DK, NW, H, SAVE>;
   using F = Fmt<DT>;
@@ -189,9 +189,10 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, qd = lane & 3;
-  const int64_t bh = head0 + blockIdx.x / vtiles;
-  const int64_t b = bh / a.Hv, h = bh - b * a.Hv;
-  const int64_t hk = h / (a.Hv / a.Hk);
+  // indices below 2^31 (checked on the host): 32-bit divisions
+  const unsigned Hv = static_cast<unsigned>(a.Hv), ubh = static_cast<unsigned>(head0) + blockIdx.x / vtiles;
+  const unsigned ub = ubh / Hv, uh = ubh - ub * Hv;
+  const int64_t bh = ubh, b = ub, h = uh, hk = uh / (Hv / static_cast<unsigned>(a.Hk));
   const int grp = warp / H, half = warp % H;
   const int64_t v0 = (static_cast<int64_t>(blockIdx.x % vtiles) * NW + grp) * 16;
   const int k0 = half * NK * 8;  // first key channel of this warp
@@ -652,7 +653,7 @@ cudaError_t launch(const GdrArgs& a, const uint8_t* qk, const uint8_t* pkg, uint
   auto al = [&](const void* p, const int64_t* st) {
     return st[3] == 1 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && st[0] % V == 0 && st[1] % V == 0 && st[2] % V == 0;
   };
-  const int vtiles = static_cast<int>((a.Dv + 16 * NW - 1) / (16 * NW));
+  const unsigned vtiles = static_cast<unsigned>((a.Dv + 16 * NW - 1) / (16 * NW));
   const cudaError_t e = cudaFuncSetAttribute(gdr_scan_kernel<DT, DK, NW, H, SAVE>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e != cudaSuccess) return e;

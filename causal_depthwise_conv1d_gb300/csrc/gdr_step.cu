@@ -24,7 +24,7 @@ constexpr int kRows = kThreads / kLanes;  // rows of one sweep step
 constexpr int kWarps = kThreads / 32;
 
 template <int DT, int MAXK>
-__global__ void __launch_bounds__(kThreads, 4) gdr_step_kernel(const GdrArgs a, int tiles) {
+__global__ void __launch_bounds__(kThreads, 4) gdr_step_kernel(const GdrArgs a, unsigned tiles) {
   using F = Fmt<DT>;
   using E = typename F::E;
   constexpr int R = MAXK / kRows;  // rows of one thread
@@ -34,9 +34,9 @@ __global__ void __launch_bounds__(kThreads, 4) gdr_step_kernel(const GdrArgs a, 
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cl = tid % kLanes, rg = tid / kLanes;
-  const int64_t bh = blockIdx.x / tiles;
-  const int64_t b = bh / a.Hv, h = bh - b * a.Hv;
-  const int64_t hk = h / (a.Hv / a.Hk);
+  // indices below 2^31 (checked on the host): 32-bit divisions
+  const unsigned Hv = static_cast<unsigned>(a.Hv), ubh = blockIdx.x / tiles, ub = ubh / Hv, uh = ubh - ub * Hv;
+  const int64_t b = ub, h = uh, hk = uh / (Hv / static_cast<unsigned>(a.Hk));
   const int64_t col = static_cast<int64_t>(blockIdx.x % tiles) * kCols + cl * 4;
   const bool in = col < a.Dv;  // Dv is a multiple of four here
   const int64_t slot = a.slots != nullptr ? a.slots[b * a.slot_stride] : b;
@@ -129,7 +129,7 @@ template <int DT, int MAXK>
 cudaError_t launch_tile(const GdrArgs& a, cudaStream_t s) {
   const int64_t tiles = (a.Dv + kCols - 1) / kCols, grid = a.B * a.Hv * tiles;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  gdr_step_kernel<DT, MAXK><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, static_cast<int>(tiles));
+  gdr_step_kernel<DT, MAXK><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, static_cast<unsigned>(tiles));
   return cudaGetLastError();
 }
 

@@ -40,7 +40,7 @@ __device__ __forceinline__ void store_if(uint32_t* p, uint32_t v, bool on) {
 }
 
 template <int DT, int R>
-__global__ void __launch_bounds__(kThreads) gdr_token_kernel(const GdrArgs a, int tiles, bool svec, bool kvec) {
+__global__ void __launch_bounds__(kThreads) gdr_token_kernel(const GdrArgs a, unsigned tiles, bool svec, bool kvec) {
   using F = Fmt<DT>;
   using E = typename F::E;
   constexpr int MAXK = 32 * R;
@@ -50,9 +50,9 @@ __global__ void __launch_bounds__(kThreads) gdr_token_kernel(const GdrArgs a, in
   __shared__ float4 sg[2][kTok];  // decay, beta, q.k, 1 where a new sequence begins
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t bh = blockIdx.x / tiles;
-  const int64_t b = bh / a.Hv, h = bh - b * a.Hv;
-  const int64_t hk = h / (a.Hv / a.Hk);
+  // indices below 2^31 (checked on the host): 32-bit divisions
+  const unsigned Hv = static_cast<unsigned>(a.Hv), ubh = blockIdx.x / tiles, ub = ubh / Hv, uh = ubh - ub * Hv;
+  const int64_t b = ub, h = uh, hk = uh / (Hv / static_cast<unsigned>(a.Hk));
   const int64_t bcol = static_cast<int64_t>(blockIdx.x % tiles) * kBlockCols;
   const int64_t col = bcol + warp * kCols;
   const int row0 = lane * R;
@@ -240,7 +240,7 @@ cudaError_t launch(const GdrArgs& a, cudaStream_t s) {
   };
   const bool kvec = a.Dk == 32 * R && words(a.k, a.ks) && words(a.q, a.qs);
   const bool svec = a.Dv % 4 == 0 && gdr_vec4_state(a.s0, a.s0s) && gdr_vec4_state(a.s1, a.s1s);
-  gdr_token_kernel<DT, R><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, static_cast<int>(tiles), svec, kvec);
+  gdr_token_kernel<DT, R><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, static_cast<unsigned>(tiles), svec, kvec);
   return cudaGetLastError();
 }
 
