@@ -35,8 +35,8 @@ namespace {
 
 __device__ unsigned g_fault;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;  // 4 groups of 16 tokens x 4 quarters of the columns
 
 // Products over the value channels, each with its own factors.
 enum { kOS0 = 0, kOS1, kRS0, kRS1, kUD0, kUD1, kSD0, kSD1, kOU, kRU, kProducts };
@@ -54,12 +54,12 @@ struct Cfg {
   static constexpr int O_TOTAL = O_RING + RING;
   static constexpr int O_MULT = O_TOTAL + TOTAL;           // half [kProducts][kGdrBwdDv]
   static constexpr int O_F = O_MULT + kProducts * kGdrBwdDv * 2;
-  static constexpr int BYTES = O_F + 1024 * 4;
+  static constexpr int BYTES = O_F + 1536 * 4;
 };
 
 // Float scratch.
-enum { kFVdr = 0, kFPart = 64 /* [2][3][64] */, kFdG = 448, kFRed = 512 /* [2][8] */, kFMax = 528 /* 4 unsigned */,
-       kFRef = 532 /* kProducts ints */, kFBar = 544 /* barriers and counters, 8-byte aligned */ };
+enum { kFVdr = 0, kFPart = 64 /* [4][3][64] */, kFdG = 832, kFRed = 896 /* [2][kWarps] */, kFMax = 928 /* 4 unsigned */,
+       kFRef = 932 /* kProducts ints */, kFBar = 944 /* barriers and counters, 8-byte aligned */ };
 
 __device__ __forceinline__ uint32_t hmul(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using F = Fmt<DT>;
   using E = typename F::E;
   constexpr int RB = DK * 2;
-  constexpr int NT = DK / 16;  // column tiles of 8 of one warp (half of DK)
+  constexpr int NT = DK / 32;  // column tiles of 8 of one warp (a quarter of DK)
   constexpr bool OLO = DT == kF32;
   extern __shared__ __align__(128) uint8_t sm[];
   float* fs = reinterpret_cast<float*>(sm + C::O_F);
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, qd = lane & 3;
-  const int wr = warp & 3, wc = warp >> 2;
+  const int wr = warp & 3, wc = warp >> 2, half = wc >> 1;
   const int i0 = wr * 16 + g, i1 = i0 + 8;
   // indices below 2^31 (checked on the host): 32-bit divisions
   const int64_t id = blockIdx.x;
@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();  // the ring held matrices written by threads
       for (int sl = 0; sl < C::STAGES && sl < ns; ++sl) fill(sl, n_copy + sl);
     }
-    reinterpret_cast<uint4*>(sm + C::QKB)[tid] = reinterpret_cast<const uint4*>(w.pack + ch * kPackBytes)[tid];
+    if (tid < kVecBytes / 16)
+      reinterpret_cast<uint4*>(sm + C::QKB)[tid] = reinterpret_cast<const uint4*>(w.pack + ch * kPackBytes)[tid];
     if (tid < 4) reinterpret_cast<unsigned*>(fs + kFMax)[tid] = 0;
     if (tid < kProducts) ref[tid] = -1000;
     if (tid < kC) {  // dR.v: the slices in order
@@ -205,13 +206,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
 
-    float dq[NT][4], z[NT][4], dk[NT][4], dp[4][4], dl[4][4], tr[2][4];
+    float dq[NT][4], z[NT][4], dk[NT][4], dp[2][4], dl[2][4], tr[2][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int j = 0; j < 4; ++j) dq[n][j] = z[n][j] = dk[n][j] = 0.f;
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int j = 0; j < 4; ++j) dp[n][j] = dl[n][j] = 0.f;
 #pragma unroll
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (OLO) ldsm4(ol, o_lo + at);
       ldsm4(rh, r_hi + at);
       ldsm4(rl, r_lo + at);
-      if (wc * 2 <= wr) {  // dO U^T and dR U^T, the column tiles up to the diagonal
+      if (wc <= wr) {  // dO U^T and dR U^T, the column tiles up to the diagonal
         uint32_t xo[4], xl[4], yh[4], yl[4];
         factors(kOU, m0, m1);
         scaled(xo, oh, m0, m1);
@@ -251,46 +252,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         factors(kRU, m0, m1);
         scaled(yh, rh, m0, m1);
         scaled(yl, rl, m0, m1);
-#pragma unroll
-        for (int np = 0; np < 2; ++np) {
-          if (wc * 2 + np > wr) continue;
-          uint32_t bh[4], bl[4];
-          const uint32_t bt = off32(wc * 32 + np * 16 + (lane & 7) + ((lane >> 4) & 1) * 8, (lane >> 3) & 1);
-          ldsm4(bh, u_hi + bt);
-          ldsm4(bl, u_lo + bt);
-          mma3<OLO>(&dp[2 * np], xo, xl, bh, bl);
-          mma3<true>(&dl[2 * np], yh, yl, bh, bl);
-        }
+        uint32_t bh[4], bl[4];
+        const uint32_t bt = off32(wc * 16 + (lane & 7) + ((lane >> 4) & 1) * 8, (lane >> 3) & 1);
+        ldsm4(bh, u_hi + bt);
+        ldsm4(bl, u_lo + bt);
+        mma3<OLO>(dp, xo, xl, bh, bl);
+        mma3<true>(dl, yh, yl, bh, bl);
       }
       uint32_t uh[4], ul[4];
       ldsm4(uh, u_hi + at);
       ldsm4(ul, u_lo + at);
-      factors(kOS0 + wc, m0, m1);
+      factors(kOS0 + half, m0, m1);
       scaled(oh, oh, m0, m1);
       if constexpr (OLO) scaled(ol, ol, m0, m1);
-      factors(kRS0 + wc, m0, m1);
+      factors(kRS0 + half, m0, m1);
       scaled(rh, rh, m0, m1);
       scaled(rl, rl, m0, m1);
-      factors(kUD0 + wc, m0, m1);
+      factors(kUD0 + half, m0, m1);
       scaled(uh, uh, m0, m1);
       scaled(ul, ul, m0, m1);
       const int rowt = (lane & 7) + ((lane >> 3) & 1) * 8, pct = lane >> 4;
 #pragma unroll
       for (int np = 0; np < NT / 2; ++np) {
-        const int n0 = wc * (DK / 2) + np * 16;
+        const int n0 = wc * (DK / 4) + np * 16;
         const uint32_t bt = (n0 >> 5) * kBlkBytes + off64(rowt, ((n0 & 31) >> 3) + pct);
         uint32_t bh[4], bl[4];
         ldsm4t(bh, s_hi + bt);
         ldsm4t(bl, s_lo + bt);
         mma3<OLO>(&dq[2 * np], oh, ol, bh, bl);
         mma3<true>(&z[2 * np], rh, rl, bh, bl);
-        if (np == wr) {  // <S0, D>: each warp's row group takes one tile pair; the diagonal of D S0^T
+        if (np == wr) {  // <S0, D>: one row group for each tile pair; the diagonal of D S0^T
           uint32_t ah[4], al[4];
           const uint32_t tt = (n0 >> 5) * kBlkBytes +
                               off64((lane & 7) + ((lane >> 4) & 1) * 8, ((n0 & 31) >> 3) + ((lane >> 3) & 1));
           ldsm4t(ah, d_hi + tt);
           ldsm4t(al, d_lo + tt);
-          factors(kSD0 + wc, m0, m1);
+          factors(kSD0 + half, m0, m1);
           scaled(ah, ah, m0, m1);
           scaled(al, al, m0, m1);
           mma3<true>(tr, ah, al, bh, bl);
@@ -316,12 +313,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
       const float gi0 = slot[kVGi * kC + i0], gi1 = slot[kVGi * kC + i1];
       const float gc0 = slot[kVGc * kC + i0], gc1 = slot[kVGc * kC + i1];
-      const Pow2 po(ref[kOS0 + wc]), pr(ref[kRS0 + wc]), pd(ref[kUD0 + wc]);
+      const Pow2 po(ref[kOS0 + half]), pr(ref[kRS0 + half]), pd(ref[kUD0 + half]);
       const float q0 = a.scale * gi0, q1 = a.scale * gi1;
       const float ki0 = slot[kVKInv * kC + i0], ki1 = slot[kVKInv * kC + i1];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int col = wc * (DK / 2) + n * 8 + qd * 2;
+        const int col = wc * (DK / 4) + n * 8 + qd * 2;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float gi = e ? gi1 : gi0, gc = e ? gc1 : gc0, qf = e ? q1 : q0;
@@ -350,13 +347,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       if (2 * qd + e == g) sd += tr[0][e] + tr[1][2 + e];
-    sd = Pow2(ref[kSD0 + wc])(sd);
+    sd = Pow2(ref[kSD0 + half])(sd);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) {
       klast += __shfl_xor_sync(kFullMask, klast, m);
       sd += __shfl_xor_sync(kFullMask, sd, m);
     }
-    if (lane == 0) fs[kFRed + warp] = klast, fs[kFRed + 8 + warp] = sd;
+    if (lane == 0) fs[kFRed + warp] = klast, fs[kFRed + kWarps + warp] = sd;
 
     // A and B with the factors of the products they enter; one power of two a matrix
     float mx[4] = {0.f, 0.f, 0.f, 0.f};
@@ -368,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float qi0 = slot[kVQInv * kC + i0], qi1 = slot[kVQInv * kC + i1];
       const float bk0 = be0 * slot[kVKInv * kC + i0], bk1 = be1 * slot[kVKInv * kC + i1];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int j0 = wc * 32 + n * 8 + qd * 2;
+      for (int n = 0; n < 2; ++n) {
+        const int j0 = wc * 16 + n * 8 + qd * 2;
         const float2 gj = *reinterpret_cast<const float2*>(slot + kVGHi * kC + j0);
         const float2 lj = *reinterpret_cast<const float2*>(slot + kVGLo * kC + j0);
         const float2 kj = *reinterpret_cast<const float2*>(slot + kVKInv * kC + j0);
@@ -398,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int m = 0; m < 4; ++m) row_factor(reinterpret_cast<const unsigned*>(fs + kFMax)[m], f[m], inv[m]);
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int col = wc * 32 + n * 8 + qd * 2;
+      for (int n = 0; n < 2; ++n) {
+        const int col = wc * 16 + n * 8 + qd * 2;
         const float2 kj = *reinterpret_cast<const float2*>(slot + kVKInv * kC + col);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -449,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kt = 0; kt < 4; ++kt) {
             const bool use = (m & 1) ? kt >= wr : kt <= wr;
             if (!use) continue;
-            const int piece = (wc * (DK / 2) + np * 16) / 8;
+            const int piece = (wc * (DK / 4) + np * 16) / 8;
             uint32_t bb[4];
             ldsm4t(bb, addr_bt<RB>(bh_t, kt * 16, piece, lane));
             mma(x[0], ah[kt], bb[0], bb[1]);
@@ -477,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float dots[3][2] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int col = wc * (DK / 2) + n * 8 + qd * 2;
+      const int col = wc * (DK / 4) + n * 8 + qd * 2;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint32_t off = tile_off<RB>(e ? i1 : i0, col >> 3) + (col & 7) * 2;
@@ -531,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int col = wc * (DK / 2) + n * 8 + qd * 2 + (j & 1), row = j < 2 ? i0 : i1;
+          const int col = wc * (DK / 4) + n * 8 + qd * 2 + (j & 1), row = j < 2 ? i0 : i1;
           if (row < nt && col < a.Dk) {
             qo[(t0 + row) * gr.dqs[1] + col * gr.dqs[3]] = F::from_f(dq[n][j]);
             ko[(t0 + row) * gr.dks[1] + col * gr.dks[3]] = F::from_f(dk[n][j]);
@@ -543,16 +540,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i = tid;
       const int64_t t = t0 + i;
       const float ki = slot[kVKInv * kC + i], qi = slot[kVQInv * kC + i], be = slot[kVBeta * kC + i];
-      const float qdq = qi * (fs[kFPart + i] + fs[kFPart + 3 * kC + i]);
-      const float kdk = ki * (fs[kFPart + kC + i] + fs[kFPart + 4 * kC + i]);
-      const float kz = ki * (fs[kFPart + 2 * kC + i] + fs[kFPart + 5 * kC + i]);
+      auto dot = [&](int d) {  // the four quarters in order
+        const float* p = fs + kFPart + d * kC + i;
+        return (p[0] + p[3 * kC]) + (p[6 * kC] + p[9 * kC]);
+      };
+      const float qdq = qi * dot(0), kdk = ki * dot(1), kz = ki * dot(2);
       if (i < nt)
         static_cast<E*>(gr.dbeta)[b * gr.dbs[0] + t * gr.dbs[1] + h * gr.dbs[2]] = F::from_f(fs[kFVdr + i] + kz);
       float x = qdq - kdk + 2.f * be * kz;
       if (i == kC - 1) {
         float kl = 0.f, sdot = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) kl += fs[kFRed + k], sdot += fs[kFRed + 8 + k];
+        for (int k = 0; k < kWarps; ++k) kl += fs[kFRed + k], sdot += fs[kFRed + kWarps + k];
         const float ga = vecs[kHdGa];
         x += kl + (ga == 0.f ? 0.f : ga * sdot);
       }
