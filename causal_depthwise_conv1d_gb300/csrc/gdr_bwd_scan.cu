@@ -557,11 +557,11 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
 
       // D <- ga D + Q^T (gi scale dO) - K^T (beta gi dR), one product after the other
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int part = 0; part < 2; ++part) {
         float y[8][4], yi0, yi1;
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-          if (half == 0) {
+          if (part == 0) {
             const float2 cq = *reinterpret_cast<const float2*>(slot + kVQS * kC + n * 8 + qd * 2);
             y[n][0] = x[n][0] * cq.x, y[n][1] = x[n][1] * cq.y, y[n][2] = x[n][2] * cq.x, y[n][3] = x[n][3] * cq.y;
           } else {
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
           }
         }
         split_rows<8, true>(y, hi, lo, yi0, yi1, ignore);
-        const uint32_t th_ = half == 0 ? qt_hi : kt_hi, tl_ = half == 0 ? qt_lo : kt_lo;
+        const uint32_t th_ = part == 0 ? qt_hi : kt_hi, tl_ = part == 0 ? qt_lo : kt_lo;
 #pragma unroll
         for (int n4 = 0; n4 < NK / 4; ++n4) {
           float z[4][4];
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
               for (int i = 0; i < 4; ++i) mma(z[i], hi[kt], bk[i >> 1][(i & 1) * 2], bk[i >> 1][(i & 1) * 2 + 1]);
             }
           }
-          const float keep = half == 0 ? ga : 1.f;
+          const float keep = part == 0 ? ga : 1.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int n = n4 * 4 + i;

@@ -52,12 +52,28 @@ void check(int dev, const char* name, const Opt& t, Shape shape, at::ScalarType 
   if (t) check(dev, name, *t, shape, dtype);
 }
 
-Tensor given(Opt& t, int dev, const char* name, Shape shape, at::ScalarType dtype) {
-  if (t) {
-    check(dev, name, *t, shape, dtype);
-    return *t;
+// The stream of the call: the one given, or the device's current one.
+struct Stream {
+  int dev;
+  std::optional<c10::cuda::CUDAStream> given;
+  Stream(int d, const std::optional<int64_t>& s) : dev(d) {
+    if (s) given = c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(*s), static_cast<c10::DeviceIndex>(d));
   }
-  return at::empty(shape, at::TensorOptions().dtype(dtype).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
+  void* raw() const {
+    return given ? given->stream() : c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
+  }
+  // A new tensor; its memory is not reused before a given stream is done with it.
+  Tensor empty(Shape shape, at::ScalarType dtype) const {
+    Tensor t = at::empty(shape, at::TensorOptions().dtype(dtype).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
+    if (given && t.numel() > 0) t.record_stream(given->unwrap());
+    return t;
+  }
+};
+
+Tensor given(Opt& t, const Stream& s, const char* name, Shape shape, at::ScalarType dtype) {
+  if (!t) return s.empty(shape, dtype);
+  check(s.dev, name, *t, shape, dtype);
+  return *t;
 }
 
 // Pointer and strides of a tensor or of a missing one.
@@ -74,25 +90,19 @@ int cuda_index(const Tensor& t) {
   return t.get_device();
 }
 
-void* stream_of(int dev, const std::optional<int64_t>& stream) {
-  if (stream) return reinterpret_cast<void*>(*stream);
-  return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
-}
-
 // A workspace of `need` bytes: the caller's (its size is checked by the ABI), or a new one.
 struct Workspace {
   Tensor own;
   void* p = nullptr;
   uint64_t bytes = 0;
-  Workspace(const Opt& given, uint64_t need, int dev) {
+  Workspace(const Opt& given, uint64_t need, const Stream& s) {
     if (given) {
-      if (!given->is_cuda() || given->get_device() != dev || !given->is_contiguous())
+      if (!given->is_cuda() || given->get_device() != s.dev || !given->is_contiguous())
         throw py::value_error("workspace must be a contiguous tensor on the inputs' CUDA device");
       p = given->data_ptr();
       bytes = static_cast<uint64_t>(given->numel()) * given->element_size();
     } else if (need > 0) {
-      own = at::empty({static_cast<int64_t>(need)},
-                      at::TensorOptions().dtype(at::kByte).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
+      own = s.empty({static_cast<int64_t>(need)}, at::kByte);
       p = own.data_ptr();
       bytes = need;
     }
@@ -140,17 +150,18 @@ std::tuple<int, Tensor, Opt> gdr_fwd(const Tensor& q, const Tensor& k, const Ten
   check(s.dev, "seq_idx", seq_idx, {s.B, s.L}, at::kInt);
   check(s.dev, "initial_state", initial_state, {s.B, s.Hv, s.Dk, s.Dv}, at::kFloat);
   const c10::cuda::OptionalCUDAGuard guard(v.device());
-  const Tensor out = given(out_given, s.dev, "out", {s.B, s.L, s.Hv, s.Dv}, s.type);
+  const Stream on(s.dev, stream);
+  const Tensor out = given(out_given, on, "out", {s.B, s.L, s.Hv, s.Dv}, s.type);
   if (want_final || final_out)
-    final_out = given(final_out, s.dev, "final_state_out", {s.B, s.Hv, s.Dk, s.Dv}, at::kFloat);
+    final_out = given(final_out, on, "final_state_out", {s.B, s.Hv, s.Dk, s.Dv}, at::kFloat);
   uint64_t need = 0;
   int rc = ccv_gdr_fwd_workspace_size(s.B, s.L, s.Hk, s.Hv, s.Dk, s.Dv, s.dt, &need);
   if (rc == CCV_OK) {
-    const Workspace w(workspace, need, s.dev);
+    const Workspace w(workspace, need, on);
     rc = ccv_gdr_fwd(ptr(q), str(q), ptr(k), str(k), ptr(v), str(v), f32(ptr(g)), str(g), ptr(beta), str(beta),
                      static_cast<const int32_t*>(ptr(seq_idx)), str(seq_idx), f32(ptr(initial_state)),
                      str(initial_state), out_ptr(out), str(out), f32(out_ptr(final_out)), str(final_out), w.p, w.bytes,
-                     s.B, s.L, s.Hk, s.Hv, s.Dk, s.Dv, s.scale, s.dt, stream_of(s.dev, stream));
+                     s.B, s.L, s.Hk, s.Hv, s.Dk, s.Dv, s.scale, s.dt, on.raw());
   }
   return {rc, out, final_out};
 }
@@ -167,12 +178,13 @@ std::tuple<int, Tensor> gdr_step(const Tensor& q_, const Tensor& k_, const Tenso
   check(s.dev, "state", state, {state.size(0), s.Hv, s.Dk, s.Dv}, at::kFloat);
   check(s.dev, "state_indices", state_indices, {s.B}, at::kInt);
   const c10::cuda::OptionalCUDAGuard guard(v.device());
+  const Stream on(s.dev, stream);
   Opt shaped = out_given ? Opt(tok(*out_given)) : Opt();
-  const Tensor out = given(shaped, s.dev, "out", {s.B, s.L, s.Hv, s.Dv}, s.type);
+  const Tensor out = given(shaped, on, "out", {s.B, s.L, s.Hv, s.Dv}, s.type);
   const int rc = ccv_gdr_step(ptr(q), str(q), ptr(k), str(k), ptr(v), str(v), f32(ptr(g)), str(g), ptr(beta), str(beta),
                               f32(out_ptr(state)), str(state), state.size(0),
                               static_cast<const int32_t*>(ptr(state_indices)), stride0(state_indices), out_ptr(out),
-                              str(out), s.B, s.L, s.Hk, s.Hv, s.Dk, s.Dv, s.scale, s.dt, stream_of(s.dev, stream));
+                              str(out), s.B, s.L, s.Hk, s.Hv, s.Dk, s.Dv, s.scale, s.dt, on.raw());
   return {rc, out_given ? *out_given : one ? out.squeeze(1) : out};
 }
 
@@ -189,20 +201,21 @@ std::tuple<int, Tensor, Tensor, Tensor, Tensor, Tensor, Opt> gdr_bwd(
   check(s.dev, "dout", dout, vo, s.type);
   check(s.dev, "dfinal_state", dfinal_state, st, at::kFloat);
   const c10::cuda::OptionalCUDAGuard guard(v.device());
-  const Tensor dq = given(dq_, s.dev, "dq", qk, s.type), dk = given(dk_, s.dev, "dk", qk, s.type);
-  const Tensor dv = given(dv_, s.dev, "dv", vo, s.type), dg = given(dg_, s.dev, "dg", gate, at::kFloat);
-  const Tensor dbeta = given(dbeta_, s.dev, "dbeta", gate, s.type);
-  if (ds0 || (want_ds0 && initial_state)) ds0 = given(ds0, s.dev, "dinitial_state", st, at::kFloat);
+  const Stream on(s.dev, stream);
+  const Tensor dq = given(dq_, on, "dq", qk, s.type), dk = given(dk_, on, "dk", qk, s.type);
+  const Tensor dv = given(dv_, on, "dv", vo, s.type), dg = given(dg_, on, "dg", gate, at::kFloat);
+  const Tensor dbeta = given(dbeta_, on, "dbeta", gate, s.type);
+  if (ds0 || (want_ds0 && initial_state)) ds0 = given(ds0, on, "dinitial_state", st, at::kFloat);
   uint64_t need = 0;
   int rc = ccv_gdr_bwd_workspace_size(s.B, s.L, s.Hk, s.Hv, s.Dk, s.Dv, s.dt, &need);
   if (rc == CCV_OK) {
-    const Workspace w(workspace, need, s.dev);
+    const Workspace w(workspace, need, on);
     rc = ccv_gdr_bwd(ptr(q), str(q), ptr(k), str(k), ptr(v), str(v), f32(ptr(g)), str(g), ptr(beta), str(beta),
                      static_cast<const int32_t*>(ptr(seq_idx)), str(seq_idx), f32(ptr(initial_state)),
                      str(initial_state), ptr(dout), str(dout), f32(ptr(dfinal_state)), str(dfinal_state), out_ptr(dq),
                      str(dq), out_ptr(dk), str(dk), out_ptr(dv), str(dv), f32(out_ptr(dg)), str(dg), out_ptr(dbeta),
                      str(dbeta), f32(out_ptr(ds0)), str(ds0), w.p, w.bytes, s.B, s.L, s.Hk, s.Hv, s.Dk, s.Dv, s.scale,
-                     s.dt, stream_of(s.dev, stream));
+                     s.dt, on.raw());
   }
   return {rc, dq, dk, dv, dg, dbeta, ds0};
 }
@@ -258,11 +271,12 @@ std::tuple<int, Tensor> ln_fwd(const Tensor& x, const Opt& weight, const Opt& bi
                                std::optional<int64_t> stream) {
   const LnSizes s = ln_sizes(x, weight, bias);
   const c10::cuda::OptionalCUDAGuard guard(x.device());
-  const Tensor out = given(out_given, s.dev, "out", x.sizes(), x.scalar_type());
+  const Stream on(s.dev, stream);
+  const Tensor out = given(out_given, on, "out", x.sizes(), x.scalar_type());
   if (s.N == 0) return {CCV_OK, out};
   const Rows xr = rows(x), yr = rows(out);
   const int rc = ccv_ln_fwd(ptr(x), xr.strides, ptr(weight), stride0(weight), ptr(bias), stride0(bias), out_ptr(out),
-                            yr.strides, s.N, s.D, static_cast<float>(eps), s.dt, s.wdt, stream_of(s.dev, stream));
+                            yr.strides, s.N, s.D, static_cast<float>(eps), s.dt, s.wdt, on.raw());
   return {rc, out};
 }
 
@@ -272,19 +286,20 @@ std::tuple<int, Tensor, Opt, Opt> ln_bwd(const Tensor& x, const Opt& weight, con
   const LnSizes s = ln_sizes(x, weight, bias);
   check(s.dev, "dout", dout, x.sizes(), x.scalar_type());
   const c10::cuda::OptionalCUDAGuard guard(x.device());
-  const Tensor dx = given(dx_, s.dev, "dx", x.sizes(), x.scalar_type());
-  if (dweight || weight) dweight = given(dweight, s.dev, "dweight", {s.D}, s.wtype);
-  if (dbias || bias) dbias = given(dbias, s.dev, "dbias", {s.D}, s.wtype);
+  const Stream on(s.dev, stream);
+  const Tensor dx = given(dx_, on, "dx", x.sizes(), x.scalar_type());
+  if (dweight || weight) dweight = given(dweight, on, "dweight", {s.D}, s.wtype);
+  if (dbias || bias) dbias = given(dbias, on, "dbias", {s.D}, s.wtype);
   Rows xr = {{0, 1}}, gr = xr, dr = xr;
   if (s.N > 0) xr = rows(x), gr = rows(dout), dr = rows(dx);
   uint64_t need = 0;
   int rc = CCV_OK;
   if (dweight || dbias) rc = ccv_ln_bwd_workspace_size(s.N, s.D, &need);
   if (rc == CCV_OK) {
-    const Workspace w(workspace, need, s.dev);
+    const Workspace w(workspace, need, on);
     rc = ccv_ln_bwd(ptr(x), xr.strides, ptr(weight), stride0(weight), ptr(dout), gr.strides, out_ptr(dx), dr.strides,
                     out_ptr(dweight), stride0(dweight), out_ptr(dbias), stride0(dbias), w.p, w.bytes, s.N, s.D,
-                    static_cast<float>(eps), s.dt, s.wdt, stream_of(s.dev, stream));
+                    static_cast<float>(eps), s.dt, s.wdt, on.raw());
   }
   return {rc, dx, dweight, dbias};
 }
