@@ -16,6 +16,13 @@
 // P^T and T^T are the tiles of the forward pass read by transposed matrix
 // loads; the row factors of those tiles run along the summed index here and
 // are multiplied into dO and dU.
+//
+// What bounds it: as in the forward scan, the chain of a chunk (3250 warp
+// instructions a warp and chunk; tensor pipe 28 %, issue slots 23 % busy with
+// four warps an SM, and the loop's code is larger than the instruction cache).
+// 2 x 2048 tokens x 32 heads of 128 x 128, bf16: 231 us, 32 chunks of 7.2 us.
+// Packed arithmetic between the products, which helps the forward scan,
+// measured 250 us here, and the update of D as a rolled loop 239 us.
 #include "gdr_chunk.cuh"
 
 namespace ccv {

@@ -10,9 +10,13 @@
 // a lane holds a column), then twice [A 0; C D]^-1 = [A' 0; -D' C A' D'].
 // This is as stable as substitution and has 16 + 4 dependent steps instead of 64.
 //
-// What bounds it: latency (the steps follow one another), so shared memory is
-// kept small enough for several blocks an SM: the inverse and L lie where k and
-// q were, and T where L was.
+// What bounds it: shared memory.  The steps of one block follow one another, so
+// it is kept small enough for four blocks an SM (the inverse and L lie where k
+// and q were, and T where L was; 64 registers), and then the load/store path is
+// the busiest unit: 72-77 % of its cycles, 51 % of the issue slots, the tensor
+// pipe 9 %.  10240 chunks and heads of 128 x 128 (8 x 2048 tokens x 40) take
+// 300 us, 4096 with two value heads a key head 104 us.  Blocks of four warps
+// took 940 us for the first, three blocks of eight warps an SM 338 us.
 //
 // The results leave as bulk copies of the shared-memory image that the scan
 // reads back, already in its tile order.
@@ -111,31 +115,52 @@ struct RowLoad {
   }
 };
 
-// y (two or four columns from c) += sign * A[row][0..n) X[0..n)[c..], rows of A and X kLd apart.
-template <int N, int COLS>
-__device__ __forceinline__ void row_times(const float* arow, const float* x, uint64_t (&y)[COLS / 2]) {
+// An FP32 value as a sum of two tf32 values (11 bits each).
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+}
+
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// d += a (8 columns m of 16 rows) times the values at `row` (two of a row, of
+// the summed index), both split: the summed index of an operand's registers
+// runs 0, 2, 4, 6 and 1, 3, 5, 7, so that an accumulator tile is the next
+// product's operand as it is.
+__device__ __forceinline__ void step_tf32(float (&d)[4], const float (&a)[4], const float* row) {
+  const float2 bv = *reinterpret_cast<const float2*>(row);
+  uint32_t ah[4], al[4], bh[2], bl[2];
 #pragma unroll
-  for (int m = 0; m < N; m += 4) {
-    const float4 l = *reinterpret_cast<const float4*>(arow + m);
-    const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint64_t ll = pk(lv[j], lv[j]);
-      if constexpr (COLS == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(x + (m + j) * kLd);
-        y[0] = ffma2(ll, pk(v.x, v.y), y[0]);
-        y[1] = ffma2(ll, pk(v.z, v.w), y[1]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(x + (m + j) * kLd);
-        y[0] = ffma2(ll, pk(v.x, v.y), y[0]);
-      }
-    }
-  }
+  for (int i = 0; i < 4; ++i) split_tf32(a[i], ah[i], al[i]);
+  split_tf32(bv.x, bh[0], bl[0]);
+  split_tf32(bv.y, bh[1], bl[1]);
+  mma_tf32(d, al, bh[0], bh[1]);
+  mma_tf32(d, ah, bl[0], bl[1]);
+  mma_tf32(d, ah, bh[0], bh[1]);
+}
+
+// The same with the left operand from 8 rows of x (a thread's two rows and two columns).
+__device__ __forceinline__ void step_rows(float (&d)[4], const float* x, const float* row) {
+  const float a[4] = {x[0], x[8], x[kLd], x[kLd + 8]};
+  step_tf32(d, a, row);
+}
+
+__device__ __forceinline__ void store_neg(float* x, const float (&d)[4]) {
+  x[0] = -d[0];
+  x[kLd] = -d[1];
+  x[8] = -d[2];
+  x[kLd + 8] = -d[3];
 }
 
 // X = (I + L)^-1; only X[i][j], j <= i, is defined after it.  The blocks below
-// the diagonal are -D' (C A'): the product in brackets goes to the block above
-// the diagonal, negated.
+// the diagonal are -D' (C A'), made transposed, (A'^T C^T) D'^T: a 16 x 8
+// accumulator tile is then an operand of the second product.  The 32 x 32
+// product in brackets goes through the block above the diagonal, negated.
 __device__ __forceinline__ void invert(const float* L, float* X) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp < 4 && lane < 16) {
@@ -158,38 +183,46 @@ __device__ __forceinline__ void invert(const float* L, float* X) {
     }
   }
   __syncthreads();
-  float a, b;
-  {  // 16 x 16 blocks (1,0) and (3,2)
-    const int p = tid >> 7, r = (tid >> 3) & 15, c = (tid & 7) * 2;
-    const int r0 = 32 * p + 16, c0 = 32 * p;
-    uint64_t y[1] = {0};
-    row_times<16, 2>(L + (r0 + r) * kLd + c0, X + c0 * kLd + c0 + c, y);
-    float2* scratch = reinterpret_cast<float2*>(X + (c0 + r) * kLd + r0 + c);
-    upk(y[0], a, b);
-    *scratch = make_float2(-a, -b);
-    __syncthreads();
-    y[0] = 0;
-    row_times<16, 2>(X + (r0 + r) * kLd + r0, X + c0 * kLd + r0 + c, y);
-    upk(y[0], a, b);
-    *reinterpret_cast<float2*>(X + (r0 + r) * kLd + c0 + c) = make_float2(a, b);
-    __syncthreads();
-    *scratch = make_float2(0.f, 0.f);  // read as part of X below
-    __syncthreads();
+  const int g = lane >> 2, q2 = (lane & 3) * 2;
+  if (warp < 4) {  // 16 x 16 blocks (1,0) and (3,2), half of the rows a warp
+    const int n = warp & 1, c0 = (warp >> 1) * 32, r0 = c0 + 16;
+    float m[2][4] = {}, d[4] = {};
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        step_rows(m[t], X + (c0 + 8 * s + q2) * kLd + c0 + g, L + (r0 + 8 * t + g) * kLd + c0 + 8 * s + q2);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (s > n) continue;  // D' is lower triangular
+      const float a[4] = {m[s][0], m[s][2], m[s][1], m[s][3]};
+      step_tf32(d, a, X + (r0 + 8 * n + g) * kLd + r0 + 8 * s + q2);
+    }
+    store_neg(X + (r0 + 8 * n + q2) * kLd + c0 + g, d);
   }
-  {  // the 32 x 32 block
-    const int r = tid >> 3, c = (tid & 7) * 4;
-    uint64_t y[2] = {0, 0};
-    float d, e;
-    row_times<32, 4>(L + (32 + r) * kLd, X + c, y);
-    upk(y[0], a, b);
-    upk(y[1], d, e);
-    *reinterpret_cast<float4*>(X + r * kLd + 32 + c) = make_float4(-a, -b, -d, -e);
+  __syncthreads();
+  {  // the 32 x 32 block: 16 columns and 8 rows a warp
+    const int c0 = (warp & 1) * 16, n = warp >> 1;
+    float d[4] = {};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (8 * s < c0) continue;  // A' is lower triangular
+      step_rows(d, X + (8 * s + q2) * kLd + c0 + g, L + (32 + 8 * n + g) * kLd + 8 * s + q2);
+    }
+    store_neg(X + (8 * n + q2) * kLd + 32 + c0 + g, d);
     __syncthreads();
-    y[0] = y[1] = 0;
-    row_times<32, 4>(X + (32 + r) * kLd + 32, X + 32 + c, y);
-    upk(y[0], a, b);
-    upk(y[1], d, e);
-    *reinterpret_cast<float4*>(X + (32 + r) * kLd + c) = make_float4(a, b, d, e);
+    d[0] = d[1] = d[2] = d[3] = 0.f;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (s > n) continue;
+      step_rows(d, X + (8 * s + q2) * kLd + 32 + c0 + g, X + (32 + 8 * n + g) * kLd + 32 + 8 * s + q2);
+    }
+    // minus the negated product
+    float* x = X + (32 + 8 * n + q2) * kLd + c0 + g;
+    x[0] = d[0];
+    x[kLd] = d[1];
+    x[8] = d[2];
+    x[kLd + 8] = d[3];
     __syncthreads();
   }
 }

@@ -21,9 +21,18 @@
 // both halves of the state), and split the output by tokens.  A chunk's chain
 // is then about 0.6 as long.
 //
-// What bounds it: the tensor instructions of 16-bit mma.sync (8 cycles each a
-// quarter SM) in the chain of one chunk after the other; a head's columns are
-// spread over as many blocks as it takes to fill the SMs.
+// What bounds it: the chain of one chunk after the other, in which a warp
+// alternates between tensor instructions (16-bit mma.sync, measured at 8 cycles
+// each a quarter SM) and the splitting of their results into the next operands
+// (2373 warp instructions a warp and chunk of 128 x 128, bf16).  With eight
+// warps a block the tensor pipe is 48 % and the issue slots 36 % busy; a second
+// block does not fit beside 255 registers a thread (two warps a block, three
+// blocks an SM: spills, 611 us for 597).  A head's columns are spread over as
+// many blocks as it takes to fill the SMs; a chunk then takes 6.2 us in blocks
+// of eight groups, 3.7 us in blocks of four and 2.9 us in blocks of two groups
+// with two warps each.  8192 tokens x 32 heads: 365 us, 128 chunks of 2.9 us;
+// 8 x 2048 tokens x 40 heads: 398 us for the 304 heads that fill whole rounds
+// and 94 us for the other 16, in small blocks.
 //
 // A chunk with a value that is not finite (in its inputs or in the state) is
 // taken token by token from the original inputs instead, so that nothing

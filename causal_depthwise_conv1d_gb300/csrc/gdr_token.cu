@@ -14,7 +14,11 @@
 // p and r go through a halving exchange (4 + 2 + 1 + 1 + 1 shuffles), four
 // lanes form u, four shuffles hand it back.  A block is eight warps on 32
 // columns of one head that share the tokens' k, q, v and gates, staged kTok
-// at a time, the next ones while these are worked on.
+// at a time, the next ones while these are worked on.  128 x 128 heads, bf16:
+// 0.37 us a token once running; one token of one request with 32 heads (4.2 MB
+// of states) 6.2 us a call, of which 4.2 us are left when calls are replayed
+// from a graph; five tokens of 16 requests x 16 heads 14.3 us.  Fetching a
+// token's operands into registers one token ahead measured 0.49 us a token.
 #include "ccv_common.cuh"
 #include "mix_internal.h"
 

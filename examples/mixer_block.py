@@ -9,10 +9,13 @@ at a time; a training step takes the same block backwards.  The projections are
 plain matrix products of the framework; everything else on the path is this
 library's (the unit length of q and k and the gates are elementwise).
 
-    python examples/mixer_block.py          # prefill, decode, one training step; prints what it checked
+    python examples/mixer_block.py          # prefill, decode, a few training steps; prints what it saw
+    python examples/mixer_block.py --time gdr_bwd --batch 2 --tokens 2048 --key-heads 16 --value-heads 32
+                                            # one operator alone: gdr_fwd, gdr_bwd, gdr_step, ln_fwd, ln_bwd
 """
 from __future__ import annotations
 
+import argparse
 import os
 import sys
 
@@ -142,7 +145,43 @@ def train_step(block: Block, x, target, seq_idx=None, lr: float = 0.0):
     return loss.detach(), grads
 
 
-def main():
+def time_operator(name: str, batch: int, tokens: int, key_heads: int, value_heads: int, head: int, steps: int):
+    """Microseconds of one call of an operator on bf16 data of these sizes, calls back to back on the device."""
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    T = 1 if name == "gdr_step" else tokens
+    q, k = (F.normalize(rnd(batch, T, key_heads, head), dim=-1).bfloat16() for _ in range(2))
+    v, dout = (rnd(batch, T, value_heads, head).bfloat16() for _ in range(2))
+    g, beta = -F.softplus(rnd(batch, T, value_heads)), torch.sigmoid(rnd(batch, T, value_heads)).bfloat16()
+    state = rnd(batch, value_heads, head, head)
+    x, w = v.reshape(batch * T, -1), torch.ones(value_heads * head, device="cuda").bfloat16()
+    call = {"gdr_fwd": lambda: ccv.gated_delta_rule_fwd(q, k, v, g, beta, return_final_state=True),
+            "gdr_bwd": lambda: ccv.gated_delta_rule_bwd(q, k, v, g, beta, dout),
+            "gdr_step": lambda: ccv.gated_delta_rule_step(q, k, v, g, beta, state),
+            "ln_fwd": lambda: ccv.layer_norm_fwd(x, w, w),
+            "ln_bwd": lambda: ccv.layer_norm_bwd(x, w, dout.reshape(x.shape), w)}[name]
+    for _ in range(3):
+        call()
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    for _ in range(steps):
+        call()
+    end.record()
+    torch.cuda.synchronize()
+    return start.elapsed_time(end) / steps * 1e3
+
+
+def main(argv=None):
+    ap = argparse.ArgumentParser(description="The block's operators together, or one of them timed.")
+    ap.add_argument("--time", choices=("gdr_fwd", "gdr_bwd", "gdr_step", "ln_fwd", "ln_bwd"))
+    for flag, n in (("batch", 2), ("tokens", 2048), ("key-heads", 16), ("value-heads", 32), ("head", 128),
+                    ("steps", 20)):
+        ap.add_argument("--" + flag, type=int, default=n)
+    a = ap.parse_args(argv)
+    if a.time:
+        us = time_operator(a.time, a.batch, a.tokens, a.key_heads, a.value_heads, a.head, a.steps)
+        print(f"{a.time}: {us:.1f} us")
+        return
     block = Block(dim=256, key_heads=2, value_heads=4, head=64)
     gen = torch.Generator(device="cuda").manual_seed(1)
     x = torch.randn((2, 160, 256), generator=gen, device="cuda").to(torch.bfloat16)
