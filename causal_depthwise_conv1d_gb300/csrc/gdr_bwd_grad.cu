@@ -42,6 +42,11 @@ __device__ unsigned g_fault;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;  // 4 groups of 16 tokens x 4 quarters of the columns
 
+template <typename E>
+struct alignas(2 * sizeof(E)) Pair {
+  E x, y;
+};
+
 // Products over the value channels, each with its own factors.
 enum { kOS0 = 0, kOS1, kRS0, kRS1, kUD0, kUD1, kSD0, kSD1, kOU, kRU, kProducts };
 
@@ -53,6 +58,8 @@ struct Cfg {
   static constexpr int STAGE = ImgF::bytes(DK) + ImgB::bytes(DK, TERMS);
   static constexpr int STAGES = DT == kF32 ? 2 : 3;
   static constexpr int RING = STAGES * STAGE > 8 * kMatBytes ? STAGES * STAGE : 8 * kMatBytes;  // later: A and B
+  static constexpr int OROW = DK * (DT == kF32 ? 4 : 2);  // a row of dQ or dK on its way out, in the ring's memory
+  static_assert(2 * kC * OROW <= RING, "dQ and dK in the ring");
   static constexpr int TOTAL = REP ? 2 * kC * DK * 4 : 0;  // dQ and dK of the heads so far
   static constexpr int O_RING = QKB + kVecBytes;
   static constexpr int O_TOTAL = O_RING + RING;
@@ -105,7 +112,7 @@ struct Pow2 {
 
 template <int DT, int DK, bool REP>
 __global__ void __launch_bounds__(kThreads, 1)
-    gdr_bwd_grad_kernel(const GdrArgs a, const GdrGrads gr, const GdrBwdWs w, int nc) {
+    gdr_bwd_grad_kernel(const GdrArgs a, const GdrGrads gr, const GdrBwdWs w, int nc, bool vec) {
   pdl_enter();
   using C = Cfg<DT, DK, REP>;
   using F = Fmt<DT>;
@@ -141,12 +148,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int BF = ImgF::bytes(DK), BB = ImgB::bytes(DK, C::TERMS);
 
   int64_t ch = (b * a.Hv + hk * rep) * nc + c;
-  auto fill = [&](int sl, int n) {  // slice sl as the block's n-th copy
+  auto fill = [&](int64_t ch, int sl, int n) {  // slice sl of this chunk and head as the block's n-th copy
     uint8_t* dst = sm + C::O_RING + (n % C::STAGES) * C::STAGE;
     uint64_t* bar = &full[n % C::STAGES];
     mbar_arrive_expect_tx(bar, C::STAGE);
     bulk_load(dst, w.img_f + (ch * ns + sl) * BF, BF, bar);
     bulk_load(dst + BF, w.img_b + (ch * ns + sl) * BB, BB, bar);
+  };
+  // What a head needs before its slices, one element a thread: the channel's
+  // seven factors, a piece of the vector part, a share of dR.v.  Fetched while
+  // the head before is finished.
+  static_assert(kGdrBwdDv <= kThreads && kVecBytes / 16 <= kThreads, "one element a thread");
+  const bool channel = tid < ns * 16;
+  float fac[7], vdr;
+  uint4 vpiece;
+  auto fetch = [&](int64_t ch) {
+    const uint8_t* imf = w.img_f + ch * ns * BF + ImgF::inv(DK);
+    const uint8_t* imb = w.img_b + ch * ns * BB + ImgB::inv(DK, C::TERMS);
+    if (channel) {
+      const float* pf = reinterpret_cast<const float*>(imf + (tid >> 4) * BF) + (tid & 15);
+      const float* pb = reinterpret_cast<const float*>(imb + (tid >> 4) * BB) + (tid & 15);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) fac[i] = pf[16 * i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fac[3 + i] = pb[16 * i];
+    }
+    if (tid < kVecBytes / 16) vpiece = reinterpret_cast<const uint4*>(w.pack + ch * kPackBytes)[tid];
+    vdr = 0.f;
+    for (int sl = tid / kC; sl < ns; sl += kThreads / kC)
+      vdr += reinterpret_cast<const float*>(imb + sl * BB)[64 + tid % kC];
+  };
+  auto start = [&](int64_t ch, int n) {  // the head's maxima and first slices
+    if (tid < 4) reinterpret_cast<unsigned*>(fs + kFMax)[tid] = 0;
+    if (tid < kProducts) ref[tid] = -1000;
+    if (tid == 0)
+      for (int sl = 0; sl < C::STAGES && sl < ns; ++sl) fill(ch, sl, n + sl);
   };
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -155,6 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_barrier_init();
   }
+  start(ch, 0);
+  fetch(ch);
   {  // k and q tiles
     const uint4* src = reinterpret_cast<const uint4*>(w.qk + id * C::QKB);
     uint4* dst = reinterpret_cast<uint4*>(sm);
@@ -166,47 +204,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   for (int64_t r = 0; r < rep; ++r, ch += nc) {
     const int64_t h = hk * rep + r;
-    const uint8_t* imf = w.img_f + ch * ns * BF;
-    const uint8_t* imb = w.img_b + ch * ns * BB;
-    __syncthreads();  // the last head's matrices, factors and sums have been read
-    if (tid == 0) {
-      fence_proxy_async_smem();  // the ring held matrices written by threads
-      for (int sl = 0; sl < C::STAGES && sl < ns; ++sl) fill(sl, n_copy + sl);
-    }
-    if (tid < kVecBytes / 16)
-      reinterpret_cast<uint4*>(sm + C::QKB)[tid] = reinterpret_cast<const uint4*>(w.pack + ch * kPackBytes)[tid];
-    if (tid < 4) reinterpret_cast<unsigned*>(fs + kFMax)[tid] = 0;
-    if (tid < kProducts) ref[tid] = -1000;
-    if (tid < kC) {  // dR.v: the slices in order
-      float x = 0.f;
-      for (int sl = 0; sl < ns; ++sl) x += reinterpret_cast<const float*>(imb + sl * BB + ImgB::inv(DK, C::TERMS))[64 + tid];
-      fs[kFVdr + tid] = x;
-    }
-    __syncthreads();
+    __syncthreads();  // the last head's factors and sums have been read
+    if (tid < kVecBytes / 16) reinterpret_cast<uint4*>(sm + C::QKB)[tid] = vpiece;
+    fs[kFPart + tid] = vdr;
     // exponents of the channels' factors; each product's largest
-    for (int v = tid; v < (ns * 16 + 31) / 32 * 32; v += kThreads) {
-      int e[kProducts];
-      const bool in = v < ns * 16;
-      const float* pf = reinterpret_cast<const float*>(imf + (in ? v >> 4 : 0) * BF + ImgF::inv(DK)) + (v & 15);
-      const float* pb = reinterpret_cast<const float*>(imb + (in ? v >> 4 : 0) * BB + ImgB::inv(DK, C::TERMS)) + (v & 15);
-      auto ex = [](float x) { return static_cast<int>(__float_as_uint(x) >> 23) - 127; };
-      const int s0 = ex(pf[0]), s1 = ex(pf[16]), u = ex(pf[32]), d0 = ex(pb[0]), d1 = ex(pb[16]), rr = ex(pb[32]),
-                o = ex(pb[48]);
+    int e[kProducts];
+    if (warp * 32 < ns * 16) {
+      int x[7];
+#pragma unroll
+      for (int i = 0; i < 7; ++i) x[i] = static_cast<int>(__float_as_uint(fac[i]) >> 23) - 127;
+      const int s0 = x[0], s1 = x[1], u = x[2], d0 = x[3], d1 = x[4], rr = x[5], o = x[6];
       e[kOS0] = o + s0, e[kOS1] = o + s1, e[kRS0] = rr + s0, e[kRS1] = rr + s1, e[kUD0] = u + d0, e[kUD1] = u + d1;
       e[kSD0] = s0 + d0, e[kSD1] = s1 + d1, e[kOU] = o + u, e[kRU] = rr + u;
 #pragma unroll
       for (int p = 0; p < kProducts; ++p) {
-        const int m = __reduce_max_sync(kFullMask, in ? e[p] : -1000);
+        const int m = __reduce_max_sync(kFullMask, channel ? e[p] : -1000);
         if (lane == 0) atomicMax(&ref[p], m);
-        // kept as a biased exponent until the largest is known
-        if (in) mult[p * kGdrBwdDv + v] = static_cast<uint16_t>(e[p] + 1000);
       }
     }
     __syncthreads();
-    for (int x = tid; x < kProducts * ns * 16; x += kThreads) {
-      const int p = x / (ns * 16), v = x - p * (ns * 16);
-      const int d = static_cast<int>(mult[p * kGdrBwdDv + v]) - 1000 - ref[p];
-      mult[p * kGdrBwdDv + v] = d >= -14 ? (d + 15) << 10 : d >= -24 ? 1 << (d + 24) : 0;
+    if (channel) {
+#pragma unroll
+      for (int p = 0; p < kProducts; ++p) {
+        const int d = e[p] - ref[p];
+        mult[p * kGdrBwdDv + tid] = d >= -14 ? (d + 15) << 10 : d >= -24 ? 1 << (d + 24) : 0;
+      }
+    }
+    if (tid < kC) {  // dR.v: the shares in order
+      float x = 0.f;
+#pragma unroll
+      for (int i = 0; i < kThreads / kC; ++i) x += fs[kFPart + i * kC + tid];
+      fs[kFVdr + tid] = x;
     }
     __syncthreads();
 
@@ -306,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("atom.acq_rel.cta.shared.add.u32 %0, [%1], 1;" : "=r"(n) : "r"(smem_u32(&left[s])) : "memory");
         if (n == kWarps - 1) {  // every warp has left the stage
           left[s] = 0;
-          if (sl + C::STAGES < ns) fill(sl + C::STAGES, n_copy + C::STAGES);
+          if (sl + C::STAGES < ns) fill(ch, sl + C::STAGES, n_copy + C::STAGES);
         }
       }
     }
@@ -525,21 +553,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (r + 1 == rep) {
-      E* qo = static_cast<E*>(gr.dq) + b * gr.dqs[0] + hk * gr.dqs[2];
-      E* ko = static_cast<E*>(gr.dk) + b * gr.dks[0] + hk * gr.dks[2];
+    const bool last = r + 1 == rep;
+    __syncthreads();  // the dot products are there; the matrices have been read
+    if (!last) {
+      fence_proxy_async_smem();  // the ring held matrices written by threads
+      start(ch + nc, n_copy);
+      fetch(ch + nc);
+    } else {  // dQ and dK through the ring's memory, to leave as whole rows
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int col = wc * (DK / 4) + n * 8 + qd * 2 + (j & 1), row = j < 2 ? i0 : i1;
-          if (row < nt && col < a.Dk) {
-            qo[(t0 + row) * gr.dqs[1] + col * gr.dqs[3]] = F::from_f(dq[n][j]);
-            ko[(t0 + row) * gr.dks[1] + col * gr.dks[3]] = F::from_f(dk[n][j]);
-          }
+        for (int e = 0; e < 2; ++e) {
+          const int at = (wc * (DK / 4) + n * 8 + qd * 2) * static_cast<int>(sizeof(E));
+          uint8_t* o = sm + C::O_RING + tile_off<C::OROW>(e ? i1 : i0, at >> 4) + (at & 15);
+          Pair<E> x{F::from_f(dq[n][2 * e]), F::from_f(dq[n][2 * e + 1])};
+          *reinterpret_cast<Pair<E>*>(o) = x;
+          x = {F::from_f(dk[n][2 * e]), F::from_f(dk[n][2 * e + 1])};
+          *reinterpret_cast<Pair<E>*>(o + kC * C::OROW) = x;
         }
     }
-    __syncthreads();
     if (tid < kC) {
       const int i = tid;
       const int64_t t = t0 + i;
@@ -579,6 +611,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool first = i > 0 ? seg[i] != seg[i - 1] : seg[0] != 0 || (t == 0 && a.s0 == nullptr);
       gr.dg[b * gr.dgs[0] + t * gr.dgs[1] + h * gr.dgs[2]] = first ? 0.f : x;
     }
+    if (last) {
+      constexpr int PIECES = C::OROW / 16;
+      E* const base_o[2] = {static_cast<E*>(gr.dq) + b * gr.dqs[0] + hk * gr.dqs[2],
+                            static_cast<E*>(gr.dk) + b * gr.dks[0] + hk * gr.dks[2]};
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const int64_t* st = o ? gr.dks : gr.dqs;
+        const uint8_t* src = sm + C::O_RING + o * kC * C::OROW;
+        for (int x = tid; x < kC * PIECES; x += kThreads) {
+          const int row = x / PIECES, piece = x % PIECES;
+          if (row >= nt) break;
+          E* dst = base_o[o] + (t0 + row) * st[1];
+          const int col = piece * F::VEC;
+          const uint4 y = *reinterpret_cast<const uint4*>(src + tile_off<C::OROW>(row, piece));
+          if (vec) {
+            if (col < a.Dk) *reinterpret_cast<uint4*>(dst + col) = y;
+          } else {
+            E e[F::VEC];
+            memcpy(e, &y, 16);
+#pragma unroll
+            for (int j = 0; j < F::VEC; ++j)
+              if (col + j < a.Dk) dst[(col + j) * st[3]] = e[j];
+          }
+        }
+      }
+    }
   }
 }
 
@@ -589,8 +647,14 @@ cudaError_t launch(const GdrArgs& a, const GdrGrads& g, const GdrBwdWs& w, int n
   const cudaError_t e =
       cudaFuncSetAttribute(gdr_bwd_grad_kernel<DT, DK, REP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e != cudaSuccess) return e;
+  constexpr int64_t V = Fmt<DT>::VEC;
+  auto ok = [&](const void* p, const int64_t* st) {
+    return st[3] == 1 && a.Dk % V == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && st[0] % V == 0 &&
+           st[1] % V == 0 && st[2] % V == 0;
+  };
+  const bool vec = ok(g.dq, g.dqs) && ok(g.dk, g.dks);
   return launch_pdl(gdr_bwd_grad_kernel<DT, DK, REP>, static_cast<unsigned>(a.B * a.Hk * nc), kThreads, C::BYTES, s, a,
-                    g, w, nc);
+                    g, w, nc, vec);
 }
 
 template <int DT>
