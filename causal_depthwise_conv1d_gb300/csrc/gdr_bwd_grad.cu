@@ -56,7 +56,7 @@ struct Cfg {
   static constexpr int TILE = qk_tile_bytes(DK);
   static constexpr int QKB = qk_pack_bytes(DK, TERMS);
   static constexpr int STAGE = ImgF::bytes(DK) + ImgB::bytes(DK, TERMS);
-  static constexpr int STAGES = DT == kF32 ? 2 : 3;
+  static constexpr int STAGES = DT == kF32 ? 2 : 4;
   static constexpr int RING = STAGES * STAGE > 8 * kMatBytes ? STAGES * STAGE : 8 * kMatBytes;  // later: A and B
   static constexpr int OROW = DK * (DT == kF32 ? 4 : 2);  // a row of dQ or dK on its way out, in the ring's memory
   static_assert(2 * kC * OROW <= RING, "dQ and dK in the ring");
@@ -174,21 +174,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 4; ++i) fac[3 + i] = pb[16 * i];
     }
     if (tid < kVecBytes / 16) vpiece = reinterpret_cast<const uint4*>(w.pack + ch * kPackBytes)[tid];
-    vdr = 0.f;
-    for (int sl = tid / kC; sl < ns; sl += kThreads / kC)
-      vdr += reinterpret_cast<const float*>(imb + sl * BB)[64 + tid % kC];
+    auto share = [&](int sl) { return reinterpret_cast<const float*>(imb + sl * BB)[64 + tid % kC]; };
+    vdr = tid / kC < ns ? share(tid / kC) : 0.f;  // not added to anything here: nothing waits for it
+    for (int sl = tid / kC + kThreads / kC; sl < ns; sl += kThreads / kC) vdr += share(sl);
   };
   auto start = [&](int64_t ch, int n) {  // the head's maxima and first slices
     if (tid < 4) reinterpret_cast<unsigned*>(fs + kFMax)[tid] = 0;
     if (tid < kProducts) ref[tid] = -1000;
-    if (tid == 0)
-      for (int sl = 0; sl < C::STAGES && sl < ns; ++sl) fill(ch, sl, n + sl);
+    if (warp == kWarps - 1 && lane < C::STAGES && lane < ns) fill(ch, lane, n + lane);
   };
-  if (tid == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 1);
-      left[s] = 0;
-    }
+  if (warp == kWarps - 1 && lane < C::STAGES) {
+    mbar_init(&full[lane], 1);
+    left[lane] = 0;
     fence_barrier_init();
   }
   start(ch, 0);
@@ -311,8 +308,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t bh[4], bl[4];
         ldsm4t(bh, s_hi + bt);
         ldsm4t(bl, s_lo + bt);
-        mma3<OLO>(&dq[2 * np], oh, ol, bh, bl);
-        mma3<true>(&z[2 * np], rh, rl, bh, bl);
+        // two pairs of sums in turn: a sum's next instruction is four away
+        mma(dq[2 * np], oh, bh[0], bh[1]);
+        mma(dq[2 * np + 1], oh, bh[2], bh[3]);
+        mma(z[2 * np], rh, bh[0], bh[1]);
+        mma(z[2 * np + 1], rh, bh[2], bh[3]);
+        mma(dq[2 * np], oh, bl[0], bl[1]);
+        mma(dq[2 * np + 1], oh, bl[2], bl[3]);
+        mma(z[2 * np], rh, bl[0], bl[1]);
+        mma(z[2 * np + 1], rh, bl[2], bl[3]);
+        if constexpr (OLO) {
+          mma(dq[2 * np], ol, bh[0], bh[1]);
+          mma(dq[2 * np + 1], ol, bh[2], bh[3]);
+        }
+        mma(z[2 * np], rl, bh[0], bh[1]);
+        mma(z[2 * np + 1], rl, bh[2], bh[3]);
         if (np == wr) {  // <S0, D>: one row group for each tile pair; the diagonal of D S0^T
           uint32_t ah[4], al[4];
           const uint32_t tt = (n0 >> 5) * kBlkBytes +
@@ -451,54 +461,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int m = 0; m < 4; ++m) {
         const uint32_t mh = mats + 2 * m * kMatBytes, ml = mh + kMatBytes;
         const uint32_t bh_t = m == 1 ? qt_hi : kt_hi, bl_t = m == 1 ? qt_lo : kt_lo;
-        uint32_t ah[4][4], al[4][4];
+        float x[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[n][j] = 0.f;
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt) {
           // rows i, summed j <= i; or rows j, summed i >= j by transposed loads
-          const bool use = (m & 1) ? kt >= wr : kt <= wr;
-          if (use) {
-            if (m & 1) {
-              ldsm4t(ah[kt], addr_at<128>(mh, kt * 16, wr * 2, lane));
-              ldsm4t(al[kt], addr_at<128>(ml, kt * 16, wr * 2, lane));
-            } else {
-              ldsm4(ah[kt], addr_a<128>(mh, wr * 16, 2 * kt, lane));
-              ldsm4(al[kt], addr_a<128>(ml, wr * 16, 2 * kt, lane));
-            }
+          if ((m & 1) ? kt < wr : kt > wr) continue;
+          uint32_t ah[4], al[4];
+          if (m & 1) {
+            ldsm4t(ah, addr_at<128>(mh, kt * 16, wr * 2, lane));
+            ldsm4t(al, addr_at<128>(ml, kt * 16, wr * 2, lane));
           } else {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) ah[kt][x] = al[kt][x] = 0;
+            ldsm4(ah, addr_a<128>(mh, wr * 16, 2 * kt, lane));
+            ldsm4(al, addr_a<128>(ml, wr * 16, 2 * kt, lane));
           }
-        }
 #pragma unroll
-        for (int np = 0; np < NT / 2; ++np) {
-          float x[2][4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[0][j] = x[1][j] = 0.f;
-#pragma unroll
-          for (int kt = 0; kt < 4; ++kt) {
-            const bool use = (m & 1) ? kt >= wr : kt <= wr;
-            if (!use) continue;
+          for (int np = 0; np < NT / 2; ++np) {
             const int piece = (wc * (DK / 4) + np * 16) / 8;
             uint32_t bb[4];
             ldsm4t(bb, addr_bt<RB>(bh_t, kt * 16, piece, lane));
-            mma(x[0], ah[kt], bb[0], bb[1]);
-            mma(x[1], ah[kt], bb[2], bb[3]);
-            mma(x[0], al[kt], bb[0], bb[1]);
-            mma(x[1], al[kt], bb[2], bb[3]);
+            mma(x[2 * np], ah, bb[0], bb[1]);
+            mma(x[2 * np + 1], ah, bb[2], bb[3]);
+            mma(x[2 * np], al, bb[0], bb[1]);
+            mma(x[2 * np + 1], al, bb[2], bb[3]);
             if constexpr (DT == kF32) {
               ldsm4t(bb, addr_bt<RB>(bl_t, kt * 16, piece, lane));
-              mma(x[0], ah[kt], bb[0], bb[1]);
-              mma(x[1], ah[kt], bb[2], bb[3]);
+              mma(x[2 * np], ah, bb[0], bb[1]);
+              mma(x[2 * np + 1], ah, bb[2], bb[3]);
             }
           }
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float& dst = m == 0 ? dq[2 * np + t][j] : m == 2 ? z[2 * np + t][j] : dk[2 * np + t][j];
-              dst = fmaf(inv[m], x[t][j], dst);
-            }
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float& dst = m == 0 ? dq[n][j] : m == 2 ? z[n][j] : dk[n][j];
+            dst = fmaf(inv[m], x[n][j], dst);
+          }
       }
     }
 
@@ -556,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool last = r + 1 == rep;
     __syncthreads();  // the dot products are there; the matrices have been read
     if (!last) {
-      fence_proxy_async_smem();  // the ring held matrices written by threads
+      if (warp == kWarps - 1) fence_proxy_async_smem();  // the ring held matrices written by threads
       start(ch + nc, n_copy);
       fetch(ch + nc);
     } else {  // dQ and dK through the ring's memory, to leave as whole rows
