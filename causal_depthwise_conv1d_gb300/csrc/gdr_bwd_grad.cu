@@ -41,6 +41,10 @@ __device__ unsigned g_fault;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;  // 4 groups of 16 tokens x 4 quarters of the columns
+// Two bits a warp: its group of tokens.  In this order each quarter of the SM
+// has two or three of the ten warps whose tiles of the 64 x 64 matrices are not
+// all above the diagonal.
+constexpr unsigned kRowOf = 0x9c9339e4u;
 
 template <typename E>
 struct alignas(2 * sizeof(E)) Pair {
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, qd = lane & 3;
-  const int wr = warp & 3, wc = warp >> 2, half = wc >> 1;
+  const int wc = warp >> 2, half = wc >> 1, wr = kRowOf >> (2 * warp) & 3;
   const int i0 = wr * 16 + g, i1 = i0 + 8;
   // indices below 2^31 (checked on the host): 32-bit divisions
   const int64_t id = blockIdx.x;
@@ -156,8 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bulk_load(dst + BF, w.img_b + (ch * ns + sl) * BB, BB, bar);
   };
   // What a head needs before its slices, one element a thread: the channel's
-  // seven factors, a piece of the vector part, a share of dR.v.  Fetched while
-  // the head before is finished.
+  // seven factors, a piece of the vector part, a share of dR.v.  Brought to the
+  // L2 cache a head ahead.
   static_assert(kGdrBwdDv <= kThreads && kVecBytes / 16 <= kThreads, "one element a thread");
   const bool channel = tid < ns * 16;
   float fac[7], vdr;
@@ -178,6 +182,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     vdr = tid / kC < ns ? share(tid / kC) : 0.f;  // not added to anything here: nothing waits for it
     for (int sl = tid / kC + kThreads / kC; sl < ns; sl += kThreads / kC) vdr += share(sl);
   };
+  auto ahead = [&](int64_t ch) {
+    const int y = tid - ns * 6;  // two lines of factors of the one image, four of the other, the vector part
+    const uint8_t* p = nullptr;
+    if (tid < ns * 2)
+      p = w.img_f + (ch * ns + (tid >> 1)) * BF + ImgF::inv(DK) + (tid & 1) * 128;
+    else if (tid < ns * 6)
+      p = w.img_b + (ch * ns + ((tid - ns * 2) >> 2)) * BB + ImgB::inv(DK, C::TERMS) + ((tid - ns * 2) & 3) * 128;
+    else if (y < kVecBytes / 128)
+      p = w.pack + ch * kPackBytes + y * 128;
+    if (p != nullptr) asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+  };
   auto start = [&](int64_t ch, int n) {  // the head's maxima and first slices
     if (tid < 4) reinterpret_cast<unsigned*>(fs + kFMax)[tid] = 0;
     if (tid < kProducts) ref[tid] = -1000;
@@ -189,7 +204,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   start(ch, 0);
-  fetch(ch);
   {  // k and q tiles
     const uint4* src = reinterpret_cast<const uint4*>(w.qk + id * C::QKB);
     uint4* dst = reinterpret_cast<uint4*>(sm);
@@ -201,6 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   for (int64_t r = 0; r < rep; ++r, ch += nc) {
     const int64_t h = hk * rep + r;
+    fetch(ch);
+    if (r + 1 < rep) ahead(ch + nc);
     __syncthreads();  // the last head's factors and sums have been read
     if (tid < kVecBytes / 16) reinterpret_cast<uint4*>(sm + C::QKB)[tid] = vpiece;
     fs[kFPart + tid] = vdr;
@@ -406,8 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Pow2 pu(ref[kOU]), pr(ref[kRU]);
       const float qi0 = slot[kVQInv * kC + i0], qi1 = slot[kVQInv * kC + i1];
       const float bk0 = be0 * slot[kVKInv * kC + i0], bk1 = be1 * slot[kVKInv * kC + i1];
+      const bool lower = wc <= wr;  // the tiles above the diagonal are never read
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
+        if (!lower) break;
         const int j0 = wc * 16 + n * 8 + qd * 2;
         const float2 gj = *reinterpret_cast<const float2*>(slot + kVGHi * kC + j0);
         const float2 lj = *reinterpret_cast<const float2*>(slot + kVGLo * kC + j0);
@@ -438,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int m = 0; m < 4; ++m) row_factor(reinterpret_cast<const unsigned*>(fs + kFMax)[m], f[m], inv[m]);
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
+        if (!lower) break;
         const int col = wc * 16 + n * 8 + qd * 2;
         const float2 kj = *reinterpret_cast<const float2*>(slot + kVKInv * kC + col);
 #pragma unroll
@@ -560,7 +579,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!last) {
       if (warp == kWarps - 1) fence_proxy_async_smem();  // the ring held matrices written by threads
       start(ch + nc, n_copy);
-      fetch(ch + nc);
     } else {  // dQ and dK through the ring's memory, to leave as whole rows
 #pragma unroll
       for (int n = 0; n < NT; ++n)
