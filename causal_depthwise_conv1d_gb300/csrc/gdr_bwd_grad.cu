@@ -29,9 +29,14 @@
 // 7400 tensor instructions of 16 x 8 x 16 (products of two FP32 operands take
 // three; 8 cycles each a quarter SM: 97 us of the 308 below) and 62 thousand
 // warp instructions, and one block of sixteen warps fills the registers of an
-// SM, so its phases (the slices, the 64 x 64 products, the sums) follow one
-// another: tensor pipe 34 %, issue slots 36 %, load/store path 46 % busy.  2 x
-// 2048 tokens x 32 heads on 16 key heads, bf16: 308 us (eight warps: 313 us).
+// SM, so its phases follow one another.  Of some 34 thousand cycles a head, the
+// slices take 17 (their tensor instructions alone 11), the matrices A and B 4,
+// the products with them 4, and the rest is the factors before the slices and
+// the sums after them.  What measured faster: factors and first slices of the
+// next head on their way while this one is finished, dQ and dK leaving as whole
+// rows (308 -> 281 us), sums of independent products in turn (281 -> 266 us),
+// nothing for tiles above the diagonal (263 us; all for 2 x 2048 tokens x 32
+// heads on 16 key heads, bf16; eight warps instead of sixteen cost 5 us more).
 #include "gdr_chunk.cuh"
 
 namespace ccv {

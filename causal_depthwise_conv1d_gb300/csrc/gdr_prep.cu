@@ -9,14 +9,18 @@
 // the four 16 x 16 diagonal blocks by forward substitution (one warp each,
 // a lane holds a column), then twice [A 0; C D]^-1 = [A' 0; -D' C A' D'].
 // This is as stable as substitution and has 16 + 4 dependent steps instead of 64.
+// The block products run on tf32 tensor instructions, every operand as the sum
+// of two tf32 values (22 bits; the exponent range of FP32, so nothing is scaled)
+// and FP32 sums; on the FP32 units, whose operands all come from shared memory,
+// they took 104 us for 90 below.
 //
-// What bounds it: shared memory.  The steps of one block follow one another, so
-// it is kept small enough for four blocks an SM (the inverse and L lie where k
-// and q were, and T where L was; 64 registers), and then the load/store path is
-// the busiest unit: 72-77 % of its cycles, 51 % of the issue slots, the tensor
-// pipe 9 %.  10240 chunks and heads of 128 x 128 (8 x 2048 tokens x 40) take
-// 300 us, 4096 with two value heads a key head 104 us.  Blocks of four warps
-// took 940 us for the first, three blocks of eight warps an SM 338 us.
+// What bounds it: the steps of one block follow one another between barriers,
+// so shared memory is kept small enough for four blocks an SM (the inverse and
+// L lie where k and q were, and T where L was; 64 registers).  The issue slots
+// are then 55 % busy, the load/store path 49 %, the integer pipe 38 %.  4096
+// chunks of 128 channels with two value heads each (8192 tokens x 32 heads) take
+// 90 us, 2048 take 48 us.  Blocks of four warps were 2.8 times as slow as three
+// blocks of eight an SM, which were 1.1 times as slow as four.
 //
 // The results leave as bulk copies of the shared-memory image that the scan
 // reads back, already in its tile order.
