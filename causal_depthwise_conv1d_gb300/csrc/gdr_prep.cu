@@ -12,15 +12,17 @@
 // The block products run on tf32 tensor instructions, every operand as the sum
 // of two tf32 values (22 bits; the exponent range of FP32, so nothing is scaled)
 // and FP32 sums; on the FP32 units, whose operands all come from shared memory,
-// they took 104 us for 90 below.
+// the 89 us below were 104.
 //
 // What bounds it: the steps of one block follow one another between barriers,
 // so shared memory is kept small enough for four blocks an SM (the inverse and
 // L lie where k and q were, and T where L was; 64 registers).  The issue slots
 // are then 55 % busy, the load/store path 49 %, the integer pipe 38 %.  4096
-// chunks of 128 channels with two value heads each (8192 tokens x 32 heads) take
-// 90 us, 2048 take 48 us.  Blocks of four warps were 2.8 times as slow as three
-// blocks of eight an SM, which were 1.1 times as slow as four.
+// chunks and heads of 128 channels on half as many key heads (8192 tokens x 32
+// heads) take 89 us, 2048 take 47 us, 10240 with a key head each 277 us.  Blocks
+// of four warps were 2.8 times as slow as three blocks of eight an SM, which
+// were 1.1 times as slow as four.  The scan of the decays runs while k and q are
+// on their way (282 us beside the other warps' wait for it).
 //
 // The results leave as bulk copies of the shared-memory image that the scan
 // reads back, already in its tile order.
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
   const int nt = static_cast<int>(a.L - t0 < kC ? a.L - t0 : kC);
   const int64_t rep = static_cast<unsigned>(a.Hv) / static_cast<unsigned>(a.Hk);
 
-  // warp 0 has the gates: two tokens a lane, those of the next head fetched ahead
+  // warp 0 has the gates: two tokens a lane
   float gv[2] = {0.f, 0.f}, bv[2] = {0.f, 0.f};
   int nw[2] = {0, 0};
   auto gates = [&](int64_t h) {
@@ -284,6 +286,38 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
       gv[j] = t < a.L ? a.g[b * a.gs[0] + t * a.gs[1] + h * a.gs[2]] : 0.f;
       bv[j] = t < a.L ? F::to_f(static_cast<const E*>(a.beta)[b * a.bs[0] + t * a.bs[1] + h * a.bs[2]]) : 0.f;
     }
+  };
+  // Warp 0: the inclusive scan of the pair sums of g log2 e; G is kept as hi +
+  // lo so that differences stay exact.  Then the next head's gates.
+  auto decays = [&](int64_t h) {
+    const float a0 = gv[0] * kLog2e, a1 = gv[1] * kLog2e;
+    float hi = a0 + a1;
+    const float bb = hi - a0;
+    float lo = (a0 - (hi - bb)) + (a1 - bb);
+    int sn = nw[0] + nw[1];
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const float oh = __shfl_up_sync(kFullMask, hi, m), ol = __shfl_up_sync(kFullMask, lo, m);
+      const int os = __shfl_up_sync(kFullMask, sn, m);
+      if (lane >= m) {
+        const float s = hi + oh, z = s - hi;
+        lo += ol + ((hi - (s - z)) + (oh - z));
+        hi = s;
+        sn += os;
+      }
+    }
+    // token 2 lane: the pair's sum without its second element
+    const float s = hi - a1, z = s - hi;
+    const float2 gh = make_float2(s, hi), gl = make_float2(lo + ((hi - (s - z)) + (-a1 - z)), lo);
+    const int2 sg = make_int2(sn - nw[1], sn);
+    reinterpret_cast<float2*>(ghi)[lane] = gh;
+    reinterpret_cast<float2*>(glo)[lane] = gl;
+    reinterpret_cast<int2*>(seg)[lane] = sg;
+    reinterpret_cast<float2*>(slot + kVGHi * kC)[lane] = gh;
+    reinterpret_cast<float2*>(slot + kVGLo * kC)[lane] = gl;
+    reinterpret_cast<int2*>(slot + kVSeg * kC)[lane] = sg;
+    reinterpret_cast<float2*>(slot + kVBeta * kC)[lane] = make_float2(bv[0], bv[1]);
+    if (h + 1 < (hk + 1) * rep) gates(h + 1);
   };
   if (warp == 0) {
     gates(hk * rep);
@@ -300,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
     RowLoad<DT, DK> lk, lq;
     lk.load(a.k, a.ks, b, hk, t0, nt, a.Dk, vec);
     if constexpr (DT != kF32) lq.load(a.q, a.qs, b, hk, t0, nt, a.Dk, vec);
+    if (warp == 0) decays(hk * rep);  // the first head's, while k and q are on their way
     lk.store(k_hi, k_lo, kinv, bad_qk);
     if constexpr (DT == kF32) lq.load(a.q, a.qs, b, hk, t0, nt, a.Dk, vec);
     lq.store(q_hi, q_lo, qinv, bad_qk);
@@ -368,64 +403,31 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
 
   for (int64_t r = 0; r < rep; ++r) {
     const int64_t h = hk * rep + r;
-    if (tid == 0) bulk_wait_read();  // the tiles and the package are free again
-    __syncthreads();
     if (tid < kC) pmax[tid] = 0;
-    if (warp == 0) {
-      // inclusive scan of the pair sums of g log2 e; G is kept as hi + lo so
-      // that differences stay exact
-      const float a0 = gv[0] * kLog2e, a1 = gv[1] * kLog2e;
-      float hi = a0 + a1;
-      const float bb = hi - a0;
-      float lo = (a0 - (hi - bb)) + (a1 - bb);
-      int sn = nw[0] + nw[1];
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const float oh = __shfl_up_sync(kFullMask, hi, m), ol = __shfl_up_sync(kFullMask, lo, m);
-        const int os = __shfl_up_sync(kFullMask, sn, m);
-        if (lane >= m) {
-          const float s = hi + oh, z = s - hi;
-          lo += ol + ((hi - (s - z)) + (oh - z));
-          hi = s;
-          sn += os;
-        }
-      }
-      // token 2 lane: the pair's sum without its second element
-      const float s = hi - a1, z = s - hi;
-      const float gh[2] = {s, hi}, gl[2] = {lo + ((hi - (s - z)) + (-a1 - z)), lo};
-      const int sg[2] = {sn - nw[1], sn};
-      const float eh = __shfl_sync(kFullMask, hi, 31), el = __shfl_sync(kFullMask, lo, 31);
-      const int se = __shfl_sync(kFullMask, sn, 31);
-      bool nf = false;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int i = 2 * lane + j;
-        const float gi = sg[j] == 0 ? exp2f(gh[j] + gl[j]) : 0.f;
-        const float gc = sg[j] == se ? exp2f((eh - gh[j]) + (el - gl[j])) : 0.f;
-        const float cks = gi * kinv[i], cqs = a.scale * gi * qinv[i], cu = gc * kinv[i];
-        ghi[i] = gh[j];
-        glo[i] = gl[j];
-        seg[i] = sg[j];
-        slot[kVKS * kC + i] = cks;
-        slot[kVQS * kC + i] = cqs;
-        slot[kVBeta * kC + i] = bv[j];
-        slot[kVU * kC + i] = cu;
-        slot[kVGi * kC + i] = gi;
-        slot[kVGc * kC + i] = gc;
-        slot[kVKInv * kC + i] = kinv[i];
-        slot[kVQInv * kC + i] = qinv[i];
-        slot[kVGHi * kC + i] = gh[j];
-        slot[kVGLo * kC + i] = gl[j];
-        reinterpret_cast<int*>(slot)[kVSeg * kC + i] = sg[j];
-        if (i == kC - 1) vecs[kHdGa] = gi;
-        // growing decays: the combined factors must be finite too
-        nf = nf || mag(bv[j]) >= kInfBits || mag(gi) >= kInfBits || mag(gc) >= kInfBits || mag(cks) >= kInfBits ||
-             mag(cqs) >= kInfBits || mag(cu) >= kInfBits;
-      }
-      if (nf) atomicOr(flag, 2u);
-      if (r + 1 < rep) gates(h + 1);
-    }
+    if (tid == 0) bulk_wait_read();  // the tiles and the package are free again
+    if (warp == 0 && r > 0) decays(h);
     __syncthreads();
+
+    if (wc == 1 && wr < 2) {  // these two warps have no tile below the diagonal: the tokens' factors
+      const int i = wr * 32 + lane;
+      const float gh = ghi[i], gl = glo[i], bv = slot[kVBeta * kC + i];
+      const float gi = seg[i] == 0 ? exp2f(gh + gl) : 0.f;
+      const float gc = seg[i] == seg[kC - 1] ? exp2f((ghi[kC - 1] - gh) + (glo[kC - 1] - gl)) : 0.f;
+      const float ki = kinv[i], qi = qinv[i];
+      const float cks = gi * ki, cqs = a.scale * gi * qi, cu = gc * ki;
+      slot[kVKS * kC + i] = cks;
+      slot[kVQS * kC + i] = cqs;
+      slot[kVU * kC + i] = cu;
+      slot[kVGi * kC + i] = gi;
+      slot[kVGc * kC + i] = gc;
+      slot[kVKInv * kC + i] = ki;
+      slot[kVQInv * kC + i] = qi;
+      if (i == kC - 1) vecs[kHdGa] = gi;
+      // growing decays: the combined factors must be finite too
+      if (mag(bv) >= kInfBits || mag(gi) >= kInfBits || mag(gc) >= kInfBits || mag(cks) >= kInfBits ||
+          mag(cqs) >= kInfBits || mag(cu) >= kInfBits)
+        atomicOr(flag, 2u);
+    }
 
     // Gam; L into shared memory; P
     float p[4][4];
