@@ -29,10 +29,10 @@
 // block does not fit beside 255 registers a thread (two warps a block, three
 // blocks an SM: spills, 611 us for 597).  A head's columns are spread over as
 // many blocks as it takes to fill the SMs; a chunk then takes 6.2 us in blocks
-// of eight groups, 3.7 us in blocks of four and 2.9 us in blocks of two groups
-// with two warps each.  8192 tokens x 32 heads: 365 us, 128 chunks of 2.9 us;
-// 8 x 2048 tokens x 40 heads: 398 us for the 304 heads that fill whole rounds
-// and 94 us for the other 16, in small blocks.
+// of eight groups, 3.7 us in blocks of four and 2.8 us in blocks of two groups
+// with two warps each.  8192 tokens x 32 heads: 361 us, 128 chunks of 2.8 us;
+// 8 x 2048 tokens x 40 heads: 410 us for the 304 heads that fill whole rounds
+// and 93 us for the other 16, in small blocks.
 //
 // A chunk with a value that is not finite (in its inputs or in the state) is
 // taken token by token from the original inputs instead, so that nothing
