@@ -235,7 +235,7 @@ __device__ __forceinline__ void invert(const float* L, float* X) {
 
 template <int DT, int DK>
 __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
-    gdr_prep_kernel(const GdrArgs a, uint8_t* qk_ws, uint8_t* pack_ws, int nc, bool vec, bool plo) {
+    gdr_prep_kernel(const GdrArgs a, uint8_t* qk_ws, uint8_t* pack_ws, int nc, bool vec) {
   pdl_enter();
   using S = PrepSmem<DT, DK>;
   using F = Fmt<DT>;
@@ -483,11 +483,11 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
         split2f(p[n][0], p[n][1], w0, hi, lo);
         uint32_t off = tile_off<128>(i0, wc * 4 + n) + qd * 4;
         *reinterpret_cast<uint32_t*>(ph + off) = hi;
-        if (plo) *reinterpret_cast<uint32_t*>(pl + off) = lo;
+        *reinterpret_cast<uint32_t*>(pl + off) = lo;
         split2f(p[n][2], p[n][3], w1, hi, lo);
         off = tile_off<128>(i1, wc * 4 + n) + qd * 4;
         *reinterpret_cast<uint32_t*>(ph + off) = hi;
-        if (plo) *reinterpret_cast<uint32_t*>(pl + off) = lo;
+        *reinterpret_cast<uint32_t*>(pl + off) = lo;
       }
     }
     invert(L, X);
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
       uint8_t* dst = pack_ws + ((b * a.Hv + h) * nc + c) * kPackBytes;
       bulk_store(dst, pack, kVecBytes);
       bulk_store(dst + kVecBytes, th, 2 * kMatBytes);
-      bulk_store(dst + kOffP, ph, plo ? 2 * kMatBytes : kMatBytes);
+      bulk_store(dst + kOffP, ph, 2 * kMatBytes);
       bulk_commit();
     }
   }
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
 }
 
 template <int DT, int DK>
-cudaError_t launch(const GdrArgs& a, uint8_t* qk_ws, uint8_t* pack_ws, int nc, bool plo, cudaStream_t s) {
+cudaError_t launch(const GdrArgs& a, uint8_t* qk_ws, uint8_t* pack_ws, int nc, cudaStream_t s) {
   constexpr int64_t V = Fmt<DT>::VEC;
   auto ok = [&](const void* p, const int64_t* st) {
     return st[3] == 1 && a.Dk == DK && reinterpret_cast<uintptr_t>(p) % 16 == 0 && st[0] % V == 0 && st[1] % V == 0 &&
@@ -544,23 +544,22 @@ cudaError_t launch(const GdrArgs& a, uint8_t* qk_ws, uint8_t* pack_ws, int nc, b
       cudaFuncSetAttribute(gdr_prep_kernel<DT, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(gdr_prep_kernel<DT, DK>, static_cast<unsigned>(a.B * a.Hk * nc), kThreads, smem, s, a, qk_ws,
-                    pack_ws, nc, vec, plo);
+                    pack_ws, nc, vec);
 }
 
 template <int DT>
-cudaError_t launch_dt(const GdrArgs& a, uint8_t* q, uint8_t* p, int nc, bool plo, cudaStream_t s) {
-  return a.Dk <= 64 ? launch<DT, 64>(a, q, p, nc, plo, s) : launch<DT, 128>(a, q, p, nc, plo, s);
+cudaError_t launch_dt(const GdrArgs& a, uint8_t* q, uint8_t* p, int nc, cudaStream_t s) {
+  return a.Dk <= 64 ? launch<DT, 64>(a, q, p, nc, s) : launch<DT, 128>(a, q, p, nc, s);
 }
 
 }  // namespace
 
-cudaError_t launch_gdr_prep(const GdrArgs& a, Dtype dt, uint8_t* qk_ws, uint8_t* pack_ws, int nc, bool backward,
+cudaError_t launch_gdr_prep(const GdrArgs& a, Dtype dt, uint8_t* qk_ws, uint8_t* pack_ws, int nc,
                             cudaStream_t s) {
-  const bool plo = backward || dt != kBF16;  // a bf16 output takes P's first 11 bits alone
   switch (dt) {
-    case kF32: return launch_dt<kF32>(a, qk_ws, pack_ws, nc, plo, s);
-    case kF16: return launch_dt<kF16>(a, qk_ws, pack_ws, nc, plo, s);
-    case kBF16: return launch_dt<kBF16>(a, qk_ws, pack_ws, nc, plo, s);
+    case kF32: return launch_dt<kF32>(a, qk_ws, pack_ws, nc, s);
+    case kF16: return launch_dt<kF16>(a, qk_ws, pack_ws, nc, s);
+    case kBF16: return launch_dt<kBF16>(a, qk_ws, pack_ws, nc, s);
   }
   return cudaErrorInvalidValue;
 }

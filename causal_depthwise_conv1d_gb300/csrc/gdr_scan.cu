@@ -48,12 +48,9 @@ __device__ unsigned g_fault;
 template <int DT, int DK, int NW, int H, bool SAVE>
 struct ScanCfg {
   static constexpr int TERMS = DT == kF32 ? 2 : 1;             // of k and q
-  // Terms of S, U and P in the output: bf16 outputs (8 bits) take 11 bits of
-  // each operand, the others 22.
-  static constexpr bool OLO = DT != kBF16;
   static constexpr int TILE = qk_tile_bytes(DK);
   static constexpr int QKB = SAVE ? TERMS * TILE : 2 * TERMS * TILE;  // k alone, or k and q
-  static constexpr int MATB = SAVE ? 2 * kMatBytes : (OLO ? 4 : 3) * kMatBytes;
+  static constexpr int MATB = (SAVE ? 2 : 4) * kMatBytes;
   static constexpr int STAGE = QKB + kVecBytes + MATB;
   static constexpr int VROW = DT == kF32 ? 64 : 32;            // bytes of a warp's 16 channels of one token
   static constexpr int VBYTES = kC * VROW;
@@ -356,10 +353,8 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
             ldsm4(bk, addr_b<RB>(qt_hi, np * 16, piece, lane));
             mma(qs[2 * np], hi, bk[0], bk[1]);
             mma(qs[2 * np + 1], hi, bk[2], bk[3]);
-            if constexpr (C::OLO) {
-              mma(qs[2 * np], lo, bk[0], bk[1]);
-              mma(qs[2 * np + 1], lo, bk[2], bk[3]);
-            }
+            mma(qs[2 * np], lo, bk[0], bk[1]);
+            mma(qs[2 * np + 1], lo, bk[2], bk[3]);
             if constexpr (DT == kF32) {
               ldsm4(bk, addr_b<RB>(qt_lo, np * 16, piece, lane));
               mma(qs[2 * np], hi, bk[0], bk[1]);
@@ -524,7 +519,7 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
           // O^T = scale (gi (Q S)^T + U^T P^T)
           float ui0, ui1;
           bool ignore = false;
-          split_rows<8, C::OLO>(u, hi, lo, ui0, ui1, ignore);
+          split_rows<8, true>(u, hi, lo, ui0, ui1, ignore);
 #pragma unroll
           for (int i = 0; i < 4 / H; ++i) {
             const int np = H == 1 ? i : i == 0 ? np0 : np1;
@@ -538,13 +533,11 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
               ldsm4(bp, addr_b<128>(ph, np * 16, 2 * kt, lane));
               mma(x[0], hi[kt], bp[0], bp[1]);
               mma(x[1], hi[kt], bp[2], bp[3]);
-              if constexpr (C::OLO) {
-                mma(x[0], lo[kt], bp[0], bp[1]);
-                mma(x[1], lo[kt], bp[2], bp[3]);
-                ldsm4(bp, addr_b<128>(pl, np * 16, 2 * kt, lane));
-                mma(x[0], hi[kt], bp[0], bp[1]);
-                mma(x[1], hi[kt], bp[2], bp[3]);
-              }
+              mma(x[0], lo[kt], bp[0], bp[1]);
+              mma(x[1], lo[kt], bp[2], bp[3]);
+              ldsm4(bp, addr_b<128>(pl, np * 16, 2 * kt, lane));
+              mma(x[0], hi[kt], bp[0], bp[1]);
+              mma(x[1], hi[kt], bp[2], bp[3]);
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {

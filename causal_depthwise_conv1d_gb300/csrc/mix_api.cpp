@@ -278,7 +278,7 @@ ccv_status ccv_gdr_fwd(const void* q, const int64_t q_strides[4], const void* k,
   if (w.total == 0) return launched(ccv::launch_gdr_token(a, dt, s), "gdr_token");
   uint8_t* qk_ws = static_cast<uint8_t*>(workspace);
   uint8_t* pack_ws = qk_ws + w.qk;
-  cudaError_t err = ccv::launch_gdr_prep(a, dt, qk_ws, pack_ws, gdr_chunks(L), false, s);
+  cudaError_t err = ccv::launch_gdr_prep(a, dt, qk_ws, pack_ws, gdr_chunks(L), s);
   if (err == cudaSuccess) err = ccv::launch_gdr_scan(a, dt, qk_ws, pack_ws, nullptr, gdr_chunks(L), dev, s);
   return launched(err, "gdr_chunk");
 }
@@ -414,7 +414,7 @@ ccv_status ccv_gdr_bwd(const void* q, const int64_t q_strides[4], const void* k,
   const ccv::GdrBwdWs w = {qk_ws, pack_ws, img_f, img_b};
   cudaError_t err = cudaSuccess;
   if (L > 0) {
-    err = ccv::launch_gdr_prep(a, dt, qk_ws, pack_ws, nc, true, s);
+    err = ccv::launch_gdr_prep(a, dt, qk_ws, pack_ws, nc, s);
     if (err == cudaSuccess) err = ccv::launch_gdr_scan(a, dt, qk_ws, pack_ws, img_f, nc, dev, s);
   }
   if (err == cudaSuccess) err = ccv::launch_gdr_bwd_scan(a, gr, dt, w, nc, dev, s);

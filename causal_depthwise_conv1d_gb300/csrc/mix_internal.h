@@ -68,7 +68,7 @@ cudaError_t launch_gdr_step(const GdrArgs& a, Dtype dt, cudaStream_t stream);
 
 // Chunked forward pass: the parts that do not depend on the state (qk_ws,
 // pack_ws: see gdr_chunk.cuh), then the scan that carries it.  nc = chunks.
-cudaError_t launch_gdr_prep(const GdrArgs& a, Dtype dt, uint8_t* qk_ws, uint8_t* pack_ws, int nc, bool backward,
+cudaError_t launch_gdr_prep(const GdrArgs& a, Dtype dt, uint8_t* qk_ws, uint8_t* pack_ws, int nc,
                             cudaStream_t stream);
 // For the backward pass (img given) the scan makes no output but keeps each
 // chunk's first state and its U as images [b][h][chunk][16 value channels].
