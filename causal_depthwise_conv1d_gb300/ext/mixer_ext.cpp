@@ -62,10 +62,17 @@ struct Stream {
   void* raw() const {
     return given ? given->stream() : c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
   }
-  // A new tensor; its memory is not reused before a given stream is done with it.
+  // A new tensor.  For a given stream it comes from that stream's memory: a
+  // block freed on the current one may have kernels of the current stream
+  // pending, which the given stream does not wait for.  The current stream is
+  // where the caller will use it, so it is not reused before that is done either.
   Tensor empty(Shape shape, at::ScalarType dtype) const {
-    Tensor t = at::empty(shape, at::TensorOptions().dtype(dtype).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
-    if (given && t.numel() > 0) t.record_stream(given->unwrap());
+    const auto opt = at::TensorOptions().dtype(dtype).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev));
+    if (!given) return at::empty(shape, opt);
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev));
+    const c10::cuda::CUDAStreamGuard on(*given);
+    Tensor t = at::empty(shape, opt);
+    if (t.numel() > 0) t.record_stream(current.unwrap());
     return t;
   }
 };
