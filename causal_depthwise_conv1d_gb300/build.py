@@ -89,26 +89,32 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    ext_tmp = EXT + f".tmp{os.getpid()}"
-    procs.append((EXT_SRC, subprocess.Popen(_ext_command(ext_tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    failed = []
-    logs = []
-    for src, p in procs:
-        out, _ = p.communicate()
-        text = out.decode(errors="replace")
-        if text.strip():
-            logs.append(f"== {os.path.basename(src)}\n{text}")
-        if p.returncode != 0:
-            failed.append(src)
-    if failed:
-        raise RuntimeError("compilation failed for " + ", ".join(failed) + "\n" + "\n".join(logs))
-    if verbose or ptxas_info:
-        print("\n".join(logs), file=sys.stderr)
-    tmp = LIB + f".tmp{os.getpid()}"
-    link = [nvcc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs
-    subprocess.run(link, check=True)
-    os.replace(tmp, LIB)
-    os.replace(ext_tmp, EXT)
+    # finished files are moved into place together; nothing else is left if a step fails
+    tmp, ext_tmp = (os.path.join(BUILD, f"{os.path.basename(f)}.{os.getpid()}") for f in (LIB, EXT))
+    try:
+        procs.append((EXT_SRC, subprocess.Popen(_ext_command(ext_tmp), stdout=subprocess.PIPE,
+                                                stderr=subprocess.STDOUT)))
+        failed = []
+        logs = []
+        for src, p in procs:
+            out, _ = p.communicate()
+            text = out.decode(errors="replace")
+            if text.strip():
+                logs.append(f"== {os.path.basename(src)}\n{text}")
+            if p.returncode != 0:
+                failed.append(src)
+        if failed:
+            raise RuntimeError("compilation failed for " + ", ".join(failed) + "\n" + "\n".join(logs))
+        if verbose or ptxas_info:
+            print("\n".join(logs), file=sys.stderr)
+        link = [nvcc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs
+        subprocess.run(link, check=True)
+        os.replace(tmp, LIB)
+        os.replace(ext_tmp, EXT)
+    finally:
+        for f in (tmp, ext_tmp):
+            if os.path.exists(f):
+                os.remove(f)
     return LIB
 
 
