@@ -116,9 +116,10 @@ class Tensors {
     return CCV_OK;
   }
 
-  // No output shares an element with another tensor.  Views that interleave
-  // token by token (channel slices of one buffer) are told apart; other
-  // interleaved views of different strides are the caller's responsibility.
+  // No output shares an element with another tensor.  Views whose dimensions
+  // nest (a stride spans what lies within it), as slices and transposes of
+  // buffers do, are told apart exactly; others pass unless one of the two fills
+  // its whole range.
   ccv_status disjoint() const {
     for (int i = 0; i < n_; ++i) {
       if (!t_[i].out) continue;
@@ -150,26 +151,65 @@ class Tensors {
     return n == static_cast<__int128>(t.hi - t.lo) + 1;
   }
 
-  static bool overlaps(const T& a, const T& b) {
-    if (dense(a) || dense(b)) return true;
-    if (a.nd < 2 || b.nd < 2 || a.esz != b.esz) return false;
-    // channel slices: the same token stride, and the channels of one token
-    // inside one stride, apart from each other
-    const int64_t sa = a.strides[1] * a.esz, sb = b.strides[1] * b.esz;
-    if (a.nd != 4 || b.nd != 4 || sa != sb || sa <= 0) return false;
-    int64_t w[2];
-    const T* t[2] = {&a, &b};
-    for (int k = 0; k < 2; ++k) {
-      w[k] = t[k]->esz;
-      for (int d = 2; d < 4; ++d) {
-        if (t[k]->strides[d] < 0) return false;
-        w[k] += t[k]->strides[d] * (t[k]->shape[d] - 1) * t[k]->esz;
+  // A tensor as nested blocks of bytes: dimensions of size > 1, positive strides, the largest first.
+  struct Box {
+    const char* lo;
+    int nd;
+    __int128 stride[4], span[5];  // span[d]: bytes from the first to the last element of dimensions d..
+    int64_t n[4];
+
+    explicit Box(const T& t) : lo(t.lo), nd(0) {
+      for (int d = 0; d < t.nd; ++d) {
+        if (t.shape[d] == 1 || t.strides[d] == 0) continue;
+        const __int128 s = static_cast<__int128>(t.strides[d]) * t.esz;
+        int i = nd++;
+        for (; i > 0 && stride[i - 1] < (s < 0 ? -s : s); --i) stride[i] = stride[i - 1], n[i] = n[i - 1];
+        stride[i] = s < 0 ? -s : s;
+        n[i] = t.shape[d];
       }
+      span[nd] = t.esz;
+      for (int d = nd - 1; d >= 0; --d) span[d] = stride[d] * (n[d] - 1) + span[d + 1];
     }
-    if (w[0] > sa || w[1] > sa) return false;
-    int64_t m = (b.base - a.base) % sa;
-    if (m < 0) m += sa;
-    return !(m >= w[0] && m + w[1] <= sa);
+    bool nested(int d) const { return d < nd && span[d + 1] <= stride[d]; }
+  };
+
+  enum Answer { kNo, kYes, kUnknown };
+
+  // Does a's block of dimensions i.. at 0 meet b's of dimensions j.. at `at`?
+  // The block with the larger stride is cut at it: of a nested one at most two
+  // pieces meet a block that is no longer than the stride, and where both have
+  // the same stride their pieces meet at no more than two distances.
+  static Answer meet(const Box& a, int i, const Box& b, int j, __int128 at, int* left) {
+    if (at >= a.span[i] || at + b.span[j] <= 0) return kNo;
+    if (i == a.nd && j == b.nd) return kYes;
+    if (--*left < 0) return kUnknown;
+    const __int128 sa = i < a.nd ? a.stride[i] : 0, sb = j < b.nd ? b.stride[j] : 0;
+    if (sa < sb) return meet(b, j, a, i, -at, left);
+    if (!a.nested(i)) return kUnknown;
+    const bool both = sa == sb;
+    if (both && !b.nested(j)) return kUnknown;
+    // piece k of a lies at k sa; both: the distances k between pieces of b and of a
+    const __int128 wa = a.span[i + 1], wb = both ? b.span[j + 1] : b.span[j];
+    const __int128 first = both ? -(static_cast<__int128>(b.n[j]) - 1) : 0, last = a.n[i] - 1;
+    // k sa < at + wb and at < k sa + wa
+    __int128 k0 = floor_div(at - wa, sa) + 1, k1 = floor_div(at + wb - 1, sa);
+    if (k0 < first) k0 = first;
+    if (k1 > last) k1 = last;
+    Answer r = kNo;
+    for (__int128 k = k0; k <= k1; ++k) {
+      const Answer x = meet(a, i + 1, b, both ? j + 1 : j, at - k * sa, left);
+      if (x == kYes) return kYes;
+      if (x == kUnknown) r = kUnknown;
+      if (*left < 0) return kUnknown;
+    }
+    return r;
+  }
+  static __int128 floor_div(__int128 x, __int128 y) { return x / y - (x % y < 0 ? 1 : 0); }
+
+  static bool overlaps(const T& a, const T& b) {
+    int left = 256;
+    const Answer r = meet(Box(a), 0, Box(b), 0, b.lo - a.lo, &left);
+    return r == kYes || (r == kUnknown && (dense(a) || dense(b)));
   }
 
   T t_[20];
