@@ -63,7 +63,7 @@ N_SETS = 4
 # dram__bytes_read.sum + dram__bytes_write.sum per launch from one ncu capture,
 # keyed by a hash of the kernel sources it was taken on (stale -> null).
 NCU_TRAFFIC = {
-    "0de6bb9780ea35ef": {
+    "c5f244f57f793779": {
         "c2_bf16_contig_B8_C5120_L2048_K4_silu": 291081728,
         "c3_bf16_chlast_view_B4_C5120_L4096_K4_silu_states": 287014144,
         "c4_f16_chlast_B1_C4096_L16384_K4_silu_seqidx": 218449920,
@@ -76,11 +76,16 @@ NCU_TRAFFIC = {
 }
 
 
-def kernel_source_hash() -> str:
-    """Of the convolution's kernels: their translation units and the headers these include."""
-    h = hashlib.sha256()
+def kernel_sources():
+    """The convolution's kernels: their translation units and the headers these include."""
     csrc = os.path.join(ROOT, "causal_depthwise_conv1d_gb300", "csrc")
-    for p in sorted(glob.glob(os.path.join(csrc, "ccv_*.cu")) + glob.glob(os.path.join(csrc, "ccv_*.cuh"))):
+    return sorted(p for pattern in ("ccv_*.cu", "ccv_*.cuh", "ccv_internal.h") for p in
+                  glob.glob(os.path.join(csrc, pattern)))
+
+
+def kernel_source_hash() -> str:
+    h = hashlib.sha256()
+    for p in kernel_sources():
         with open(p, "rb") as fh:
             h.update(os.path.basename(p).encode())
             h.update(fh.read())
