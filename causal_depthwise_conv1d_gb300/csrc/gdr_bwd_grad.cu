@@ -108,12 +108,15 @@ __device__ __forceinline__ void mma3(float (*d)[4], const uint32_t (&ah)[4], con
   }
 }
 
-// Multiply by 2^e for any int e that a sum of two float exponents can be.
+// The exponent of a row that was lost (kLostBits): more than any product's.
+constexpr int kLost = 1024;
+
+// Multiply by 2^e for any int e that a sum of two float exponents can be; NaN for a lost row's.
 struct Pow2 {
   float a, b;
   __device__ __forceinline__ explicit Pow2(int e) {
     const int h = e >> 1, r = e - h;
-    a = __uint_as_float(static_cast<unsigned>(max(1, min(254, h + 127))) << 23);
+    a = __uint_as_float(e >= kLost / 2 ? 0x7fffffffu : static_cast<unsigned>(max(1, min(254, h + 127))) << 23);
     b = __uint_as_float(static_cast<unsigned>(max(1, min(254, r + 127))) << 23);
   }
   __device__ __forceinline__ float operator()(float x) const { return x * a * b; }
@@ -230,7 +233,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp * 32 < ns * 16) {
       int x[7];
 #pragma unroll
-      for (int i = 0; i < 7; ++i) x[i] = static_cast<int>(__float_as_uint(fac[i]) >> 23) - 127;
+      for (int i = 0; i < 7; ++i) {
+        const unsigned f = __float_as_uint(fac[i]);
+        x[i] = f == kLostBits ? kLost : static_cast<int>(f >> 23) - 127;
+      }
       const int s0 = x[0], s1 = x[1], u = x[2], d0 = x[3], d1 = x[4], rr = x[5], o = x[6];
       e[kOS0] = o + s0, e[kOS1] = o + s1, e[kRS0] = rr + s0, e[kRS1] = rr + s1, e[kUD0] = u + d0, e[kUD1] = u + d1;
       e[kSD0] = s0 + d0, e[kSD1] = s1 + d1, e[kOU] = o + u, e[kRU] = rr + u;
@@ -378,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float gc0 = slot[kVGc * kC + i0], gc1 = slot[kVGc * kC + i1];
       const Pow2 po(ref[kOS0 + half]), pr(ref[kRS0 + half]), pd(ref[kUD0 + half]);
       const float q0 = a.scale * gi0, q1 = a.scale * gi1;
-      const float ki0 = slot[kVKInv * kC + i0], ki1 = slot[kVKInv * kC + i1];
+      const float ki0 = gc0 == 0.f ? 0.f : slot[kVKInv * kC + i0], ki1 = gc1 == 0.f ? 0.f : slot[kVKInv * kC + i1];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int col = wc * (DK / 4) + n * 8 + qd * 2;
@@ -455,21 +461,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned x = warp_max(__float_as_uint(mx[m]));
         if (lane == 0) atomicMax(reinterpret_cast<unsigned*>(fs + kFMax) + m, x);
       }
+      // rows i0 (e = 0) or i1, columns of tile n: the entries with the four products' factors
+      auto entries = [&](int n, int e, float (&x)[4][2]) {
+        const float2 kj = *reinterpret_cast<const float2*>(slot + kVKInv * kC + wc * 16 + n * 8 + qd * 2);
+        const float qi = e ? qi1 : qi0, bk = e ? bk1 : bk0;
+        const float p0 = dp[n][2 * e], p1 = dp[n][2 * e + 1], l0 = dl[n][2 * e], l1 = dl[n][2 * e + 1];
+        // selected: a factor that is not finite stays in its sequence and below the diagonal
+        auto by = [](float x, float f) { return x == 0.f ? 0.f : x * f; };
+        x[0][0] = by(p0, kj.x), x[0][1] = by(p1, kj.y), x[1][0] = by(p0, qi), x[1][1] = by(p1, qi);
+        x[2][0] = by(l0, kj.x), x[2][1] = by(l1, kj.y), x[3][0] = by(l0, bk), x[3][1] = by(l1, bk);
+      };
+      unsigned* top = reinterpret_cast<unsigned*>(fs + kFMax);
       __syncthreads();  // also: every warp is done with the ring
+      if (max(max(top[0], top[1]), max(top[2], top[3])) >= kInfBits) {  // the largest finite ones (finite_max)
+        __syncthreads();
+        if (tid < 4) top[tid] = 0;
+        __syncthreads();
+        unsigned fin[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (!lower) continue;
+            float x[4][2];
+            entries(n, e, x);
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) fin[m] = max(fin[m], mag(x[m][j]) < kInfBits ? mag(x[m][j]) : 0u);
+          }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const unsigned x = warp_max(fin[m]);
+          if (lane == 0) atomicMax(&top[m], x);
+        }
+        __syncthreads();
+      }
       float f[4], inv[4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) row_factor(reinterpret_cast<const unsigned*>(fs + kFMax)[m], f[m], inv[m]);
+      for (int m = 0; m < 4; ++m) row_factor(top[m], f[m], inv[m]);
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         if (!lower) break;
         const int col = wc * 16 + n * 8 + qd * 2;
-        const float2 kj = *reinterpret_cast<const float2*>(slot + kVKInv * kC + col);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint32_t off = tile_off<128>(e ? i1 : i0, col >> 3) + (col & 7) * 2;
-          const float qi = e ? qi1 : qi0, bk = e ? bk1 : bk0;
-          const float p0 = dp[n][2 * e], p1 = dp[n][2 * e + 1], l0 = dl[n][2 * e], l1 = dl[n][2 * e + 1];
-          const float x[4][2] = {{p0 * kj.x, p1 * kj.y}, {p0 * qi, p1 * qi}, {l0 * kj.x, l1 * kj.y}, {l0 * bk, l1 * bk}};
+          float x[4][2];
+          entries(n, e, x);
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             uint32_t hi, lo;

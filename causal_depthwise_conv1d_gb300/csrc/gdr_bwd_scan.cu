@@ -308,17 +308,20 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
         }
       }
 
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        bulk_store(gimg + half * (C::DIMG / 2), ibuf, C::DIMG / 2);
-        bulk_store(gimg + img_state_bytes(DK) + half * (C::DIMG / 2), ibuf + C::DIMG / 2, C::DIMG / 2);
-        bulk_commit();
-      }
-      if (qd == 0) {
+      auto save_d = [&](float i0, float i1) {  // D's tiles are in the staging memory
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bulk_store(gimg + half * (C::DIMG / 2), ibuf, C::DIMG / 2);
+          bulk_store(gimg + img_state_bytes(DK) + half * (C::DIMG / 2), ibuf + C::DIMG / 2, C::DIMG / 2);
+          bulk_commit();
+        }
+        if (qd == 0) {
 #pragma unroll
-        for (int y = 0; y < 2 / H; ++y) ginv[(half + y) * 16 + g] = di0, ginv[(half + y) * 16 + g + 8] = di1;
-      }
+          for (int y = 0; y < 2 / H; ++y) ginv[(half + y) * 16 + g] = i0, ginv[(half + y) * 16 + g + 8] = i1;
+        }
+      };
+      save_d(di0, di1);
 
       // true values, and the other half's share
 #pragma unroll
@@ -390,20 +393,24 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
         for (int np = 0; np < 4; ++np)
           stsm4t(tile + off32(np * 16 + (lane & 7) + ((lane >> 4) & 1) * 8, (lane >> 3) & 1), r[np]);
       };
-      if (half == 0) {
+      auto put_o = [&](auto kept) {  // dO's image
+        if (half != 0) return;
         float i0, i1;
-        split_rows<8, DT == kF32>(x, hi, lo, i0, i1, ignore);
+        split_rows<8, DT == kF32, kept.value>(x, hi, lo, i0, i1, ignore);
         put_tok(oimg, hi);
         if constexpr (DT == kF32) put_tok(oimg + kTokBytes, lo);
         if (qd == 0) ginv[48 + g] = i0, ginv[48 + g + 8] = i1;
-      }
-      // after dR: its image and dR.v of this warp's channels, and all parts out
-      auto save_r = [&](const float (&r)[8][4]) {
+      };
+      put_o(std::false_type{});
+      // after dR: its image and dR.v of this warp's channels, and all parts out;
+      // `kept`: a chunk with values that are not finite
+      auto save_r = [&](const float (&r)[8][4], auto kept) {
         if (half != 0) return;
         uint32_t rh[4][4], rl[4][4];
         float i0, i1;
-        bool skip = false;
-        split_rows<8, true>(r, rh, rl, i0, i1, skip);
+        bool lost = false;
+        split_rows<8, true, kept.value>(r, rh, rl, i0, i1, lost);
+        if (!kept.value && lost) i0 = i1 = __uint_as_float(kLostBits);
         put_tok(rimg, rh);
         put_tok(rimg + kTokBytes, rl);
         fence_proxy_async_smem();
@@ -484,9 +491,17 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
         for (int n = 0; n < NK; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) tmp[n][j] = d[n][j];
+        {  // D's and dO's images again
+          if (lane == 0) bulk_wait_all();
+          __syncwarp();
+          float i0, i1;
+          keep_state(tmp, dimg, C::DIMG / 2, lane, i0, i1);
+          save_d(i0, i1);
+          put_o(std::true_type{});
+        }
         float ut[8][4];
         token_by_token<DT, NK, H>(a, gr, tmp, b, h, t0, v0, ut, lane, half, pair, xb, xo);
-        save_r(ut);
+        save_r(ut, std::true_type{});
 #pragma unroll
         for (int n = 0; n < NK; ++n)
 #pragma unroll
@@ -521,7 +536,7 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
           }
         }
       }
-      save_r(u);
+      save_r(u, std::false_type{});
       // dV out
 #pragma unroll
       for (int np = 0; np < 4; ++np) {

@@ -22,6 +22,8 @@
 // row factors are powers of two and are taken out exactly in FP32.
 #pragma once
 
+#include <type_traits>
+
 #include "ccv_common.cuh"
 #include "ccv_tma.cuh"
 #include "mix_internal.h"
@@ -223,10 +225,28 @@ __device__ __forceinline__ unsigned warp_max(unsigned m) {
   return __reduce_max_sync(kFullMask, m);
 }
 
+// What the backward pass keeps of a chunk with values that are not finite: each
+// row is scaled by the largest of its finite ones, so that these stay what they
+// are and only sums that the others enter are lost.  That largest of rows g and g + 8:
+template <int NT>
+__device__ __forceinline__ void finite_max(const float (&x)[NT][4], unsigned& m0, unsigned& m1) {
+  unsigned m[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const unsigned u = mag(x[i][j]);
+      m[j >> 1] = max(m[j >> 1], u < kInfBits ? u : 0u);
+    }
+  m0 = quad_max(m[0]);
+  m1 = quad_max(m[1]);
+}
+
 // 16 x 64 accumulator fragments (8 column tiles) as A operands of the next
 // product: each row scaled by its factor and split.  Returns the inverse
 // factors of rows g and g + 8; `bad` is set where a value is not finite.
-template <int NT, bool LO>
+// KEPT: by their finite values (finite_max).
+template <int NT, bool LO, bool KEPT = false>
 __device__ __forceinline__ void split_rows(const float (&x)[NT][4], uint32_t (&hi)[NT / 2][4],
                                            uint32_t (&lo)[NT / 2][4], float& inv0, float& inv1, bool& bad) {
   float a0 = 0.f, a1 = 0.f;
@@ -235,8 +255,9 @@ __device__ __forceinline__ void split_rows(const float (&x)[NT][4], uint32_t (&h
     a0 = amax3(a0, x[i][0], x[i][1]);
     a1 = amax3(a1, x[i][2], x[i][3]);
   }
-  const unsigned m0 = quad_max(__float_as_uint(a0)), m1 = quad_max(__float_as_uint(a1));
+  unsigned m0 = quad_max(__float_as_uint(a0)), m1 = quad_max(__float_as_uint(a1));
   bad = bad || m0 >= kInfBits || m1 >= kInfBits;
+  if constexpr (KEPT) finite_max(x, m0, m1);
   float f0, f1;
   row_factor(m0, f0, inv0);
   row_factor(m1, f1, inv1);
@@ -254,6 +275,26 @@ __device__ __forceinline__ void split_rows(const float (&x)[NT][4], uint32_t (&h
       }
     }
 }
+
+// A warp's rows of S^T or D^T as kept for the backward pass, in a chunk with
+// values that are not finite: hi to `tile`, lo behind it by `lo_at`.
+template <int NK>
+__device__ __noinline__ void keep_state(const float (&x)[NK][4], uint32_t tile, uint32_t lo_at, int lane, float& inv0,
+                                        float& inv1) {
+  uint32_t hi[NK / 2][4], lo[NK / 2][4];
+  bool ignore = false;
+  split_rows<NK, true, true>(x, hi, lo, inv0, inv1, ignore);
+#pragma unroll
+  for (int kt = 0; kt < NK / 2; ++kt) {
+    const uint32_t at = tile + (kt >> 1) * kBlkBytes + off64((lane & 7) + ((lane >> 3) & 1) * 8, (kt & 1) * 2 + (lane >> 4));
+    stsm4(at, hi[kt]);
+    stsm4(at + lo_at, lo[kt]);
+  }
+}
+
+// The inverse factor of a row that overflowed although nothing that enters it
+// is infinite: the gradients that it enters become NaN.
+constexpr unsigned kLostBits = kInfBits;
 
 // Barriers of one pair of warps (id from 1).
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }

@@ -86,6 +86,9 @@ struct RowLoad {
     }
   }
 
+  // A row with a value that is not finite is stored as zeros with the factor NaN.
+  // Entries of the matrices that its token enters become NaN by the factor; zeros
+  // of them, above the diagonal or across a new sequence, meet no infinity here.
   __device__ __forceinline__ void store(uint8_t* hi, uint8_t* lo, float* inv, bool& bad) const {
     constexpr int RB = DK * 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -102,9 +105,11 @@ struct RowLoad {
       unsigned m = __float_as_uint(mf);
 #pragma unroll
       for (int k = 1; k < LPR; k <<= 1) m = max(m, __shfl_xor_sync(kFullMask, m, k));
-      bad = bad || m >= kInfBits;
+      const bool lost = m >= kInfBits;
+      bad = bad || lost;
       float f, iv;
       row_factor(m, f, iv);
+      if (lost) iv = __uint_as_float(0x7fffffffu);
       if (lane % LPR == 0) inv[r] = iv;
       const uint32_t off = tile_off<RB>(r, c0 >> 3);
       uint32_t h[4], l[4];
@@ -114,6 +119,7 @@ struct RowLoad {
           split2(x[2 * j] * f, x[2 * j + 1] * f, h[j], l[j]);
         else
           h[j] = h2(x[2 * j] * f, x[2 * j + 1] * f);
+        if (lost) h[j] = l[j] = 0u;
       }
       *reinterpret_cast<uint4*>(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
       if constexpr (DT == kF32) *reinterpret_cast<uint4*>(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);

@@ -279,11 +279,13 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
       }
       bool bad = vecs[kHdBad] != 0.f;
 
-      auto save_u = [&](const float (&x)[8][4]) {  // of two warps one keeps hi, the other lo
+      // U's image; `kept`: a chunk with values that are not finite.  Of two warps one keeps hi, the other lo.
+      auto save_u = [&](const float (&x)[8][4], auto kept) {
         uint32_t uh[4][4], ul[4][4];
         float i0, i1;
-        bool ignore = false;
-        split_rows<8, true>(x, uh, ul, i0, i1, ignore);
+        bool lost = false;
+        split_rows<8, true, kept.value>(x, uh, ul, i0, i1, lost);
+        if (!kept.value && lost) i0 = i1 = __uint_as_float(kLostBits);
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
           // tokens 16 np..: fragments of rows v are read back as rows of tokens
@@ -301,6 +303,20 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
         if (qd == 0 && half == 0) {
           float* inv = reinterpret_cast<float*>(gimg + ImgF::inv(DK)) + 32;
           inv[g] = i0, inv[g + 8] = i1;
+        }
+      };
+      auto save_state = [&](float i0, float i1) {  // its tiles are in the staging memory
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bulk_store(gimg + half * (C::SIMG / 2), ibuf, C::SIMG / 2);
+          bulk_store(gimg + img_state_bytes(DK) + half * (C::SIMG / 2), ibuf + C::SIMG / 2, C::SIMG / 2);
+          bulk_commit();
+        }
+        if (qd == 0) {
+          float* inv = reinterpret_cast<float*>(gimg + ImgF::inv(DK));
+#pragma unroll
+          for (int x = 0; x < 2 / H; ++x) inv[(half + x) * 16 + g] = i0, inv[(half + x) * 16 + g + 8] = i1;
         }
       };
       // the state's row factors
@@ -364,20 +380,7 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
         }
       }
 
-      if constexpr (SAVE) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          bulk_store(gimg + half * (C::SIMG / 2), ibuf, C::SIMG / 2);
-          bulk_store(gimg + img_state_bytes(DK) + half * (C::SIMG / 2), ibuf + C::SIMG / 2, C::SIMG / 2);
-          bulk_commit();
-        }
-        if (qd == 0) {
-          float* inv = reinterpret_cast<float*>(gimg + ImgF::inv(DK));
-#pragma unroll
-          for (int x = 0; x < 2 / H; ++x) inv[(half + x) * 16 + g] = si0, inv[(half + x) * 16 + g + 8] = si1;
-        }
-      }
+      if constexpr (SAVE) save_state(si0, si1);
       // true values, and the other half's share; O: this warp's tokens are 16 np0.. and 16 np1..
       const int np0 = H == 2 ? half : 0, np1 = H == 2 ? 3 - half : 0;
       float qo[H == 2 ? 4 : 1][4];
@@ -471,9 +474,16 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
         for (int n = 0; n < NK; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) tmp[n][j] = st[n][j];
+        if constexpr (SAVE) {  // the state's image again
+          if (lane == 0) bulk_wait_all();
+          __syncwarp();
+          float i0, i1;
+          keep_state(tmp, simg, C::SIMG / 2, lane, i0, i1);
+          save_state(i0, i1);
+        }
         float ut[8][4];
         token_by_token<DT, NK, H, SAVE>(a, tmp, b, h, t0, v0, ut, lane, half, pair, xb, xo);
-        if constexpr (SAVE) save_u(ut);
+        if constexpr (SAVE) save_u(ut, std::true_type{});
 #pragma unroll
         for (int n = 0; n < NK; ++n)
 #pragma unroll
@@ -514,7 +524,7 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
           }
         }
         if constexpr (SAVE) {
-          save_u(u);
+          save_u(u, std::false_type{});
         } else {
           // O^T = scale (gi (Q S)^T + U^T P^T)
           float ui0, ui1;
