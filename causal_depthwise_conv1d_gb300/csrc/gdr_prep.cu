@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kLd = 68;  // leading dimension of L and X
+constexpr float kFarDecay = 16384.f;  // of log 2: a decay by more is this one
 
 template <int DT, int DK>
 struct PrepSmem {
@@ -296,7 +297,11 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
   // Warp 0: the inclusive scan of the pair sums of g log2 e; G is kept as hi +
   // lo so that differences stay exact.  Then the next head's gates.
   auto decays = [&](int64_t h) {
-    const float a0 = gv[0] * kLog2e, a1 = gv[1] * kLog2e;
+    // A factor that far below FP32's range is zero (minus infinity's too; a select
+    // keeps NaN).  64 of them come to 2^20, so that the second term of a sum
+    // has room for what the other tokens add.
+    auto low = [](float x) { return x < -kFarDecay ? -kFarDecay : x; };
+    const float a0 = low(gv[0] * kLog2e), a1 = low(gv[1] * kLog2e);
     float hi = a0 + a1;
     const float bb = hi - a0;
     float lo = (a0 - (hi - bb)) + (a1 - bb);
