@@ -337,7 +337,8 @@ ccv_status ccv_bwd_mixed(const void* x, const int64_t x_strides[3],
  *
  *   q, k              [B,L,Hk,Dk], strides q_strides, k_strides.
  *   v, out            [B,L,Hv,Dv].
- *   g                 FP32 [B,L,Hv], the logarithm of the decay (usually <= 0).
+ *   g                 FP32 [B,L,Hv], the logarithm of the decay (usually <= 0;
+ *                     -infinity, or any very negative number, forgets the state).
  *   beta              [B,L,Hv] in dtype.
  *   seq_idx           int32 [B,L] or NULL.  Where seq_idx[b,t] differs from
  *                     seq_idx[b,t-1] a new sequence begins: token t sees the
@@ -352,8 +353,19 @@ ccv_status ccv_bwd_mixed(const void* x, const int64_t x_strides[3],
  *   Dk                1..256.  Dv >= 1.  Any strides; rows of 16-byte aligned
  *                     vectors with unit stride in the last dimension are the
  *                     fast ones.
- *   dtype             of q, k, v, beta and out.  All arithmetic keeps at least
- *                     FP32 precision; out is rounded once (nearest even).
+ *   dtype             of q, k, v, beta and out; out is rounded once (nearest
+ *                     even).
+ *
+ * Precision.  States, decays and sums are FP32.  Sequences below 48 tokens (in
+ * FP32 with few heads 96) and Dk > 128 have FP32 products too.  Longer ones go
+ * in aligned chunks of 64 tokens through FP16 tensor instructions with FP32 (truncated)
+ * sums: 16-bit q and k enter exactly, every other operand as two FP16 terms (22
+ * bits), without the product of two low terms.  The terms share a power of two
+ * along a row: for q and k a token's channels, for v, and what is made of it, a
+ * value channel's tokens of the chunk.  There a value beside a token 2^n times
+ * larger keeps min(22, 39 - n) bits, also where seq_idx parts the two.
+ * A call repeats bit for bit; the last bits of a head may change with the number
+ * of heads in the call.
  *
  * out and final_state_out must not share memory with an input or each other.
  * Non-finite values affect what the token-by-token definition says, and
@@ -410,12 +422,19 @@ ccv_status ccv_gdr_step(const void* q, const int64_t q_strides[4], const void* k
  *   workspace         ccv_gdr_bwd_workspace_size() bytes, 128-byte aligned.
  *   Dk                1..128;  Dv  1..512.
  *
- * All sums are FP32 or better, in a fixed order (bitwise reproducible), with
- * one rounding to the output's type.  dg is zero at a sequence's first token
- * that has no state before it.  A non-finite value may reach the gradients of
- * every token of its aligned chunk of 64 besides those that the definition
- * gives, but no other chunk of another sequence.  Outputs must not share
- * memory with an input or each other.
+ * Precision as for chunks in ccv_gdr_fwd at any length; dout is a row a value
+ * channel like v, and a product over the value channels keeps min(22, 39 - n) bits
+ * of an entry 2^n times below the largest of its chunk.  Sums are FP32 in a fixed
+ * order (bitwise reproducible), with one rounding to the output's type.  dg is
+ * zero at a sequence's first token that has no state before it.
+ * What a non-finite value enters by the definition is not finite.  In its aligned
+ * chunk of 64 it may also reach gradients that it does not enter (dg of its
+ * sequence, a channel of dq and dk from one in a state, what follows one in g),
+ * which are then not finite either; a finite gradient is right.
+ * The workspace has about 27 KB for each chunk, value head and 16 value channels
+ * at Dk = 128, and 37 KB for each chunk and head: 0.56 GB for 2 x 2048 tokens x 32
+ * heads of 128 x 128, 18 GB for 131072 tokens of them.
+ * Outputs must not share memory with an input or each other.
  */
 ccv_status ccv_gdr_bwd(const void* q, const int64_t q_strides[4], const void* k, const int64_t k_strides[4],
                        const void* v, const int64_t v_strides[4], const float* g, const int64_t g_strides[3],
