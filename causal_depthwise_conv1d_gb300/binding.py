@@ -160,6 +160,23 @@ def ccv_fwd_ptr(x: int, x_strides, out: int, out_strides, weight: int, weight_st
         raise CcvError(rc, lib.ccv_last_error().decode())
 
 
+def _new(stream: Optional[torch.cuda.Stream], device: torch.device, make) -> torch.Tensor:
+    """A new tensor of a call, from the memory of the stream that the call runs on.
+
+    A block that the current stream has freed may have kernels pending there,
+    for which another stream does not wait; and one used on a stream that does
+    not own it would be handed out again too early."""
+    if stream is None:
+        return make()
+    current = torch.cuda.current_stream(device)
+    if stream == current:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(current)  # where the caller uses it
+    return t
+
+
 def _dense_like_fast_dim(x: torch.Tensor, B: int, C: int, n: int) -> torch.Tensor:
     """[B, C, n] tensor, dense along x's smaller-stride dimension: channel-last
     when x's channel stride is the smaller one (channel-last x, or channels
@@ -212,11 +229,11 @@ def ccv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] 
     if initial_states is not None and tuple(initial_states.shape) != (B, C, K - 1):
         raise ValueError("initial_states must be [B, C, K-1]")
     if out is None:
-        out = _dense_like_fast_dim(x, B, C, L)
+        out = _new(stream, x.device, lambda: _dense_like_fast_dim(x, B, C, L))
     elif tuple(out.shape) != (B, C, L):
         raise ValueError("out must be [B, C, L]")
     if return_final_states and final_states_out is None:
-        final_states_out = _dense_like_fast_dim(x, B, C, K - 1)
+        final_states_out = _new(stream, x.device, lambda: _dense_like_fast_dim(x, B, C, K - 1))
     if final_states_out is not None and tuple(final_states_out.shape) != (B, C, K - 1):
         raise ValueError("final_states_out must be [B, C, K-1]")
     if stream is None:
@@ -268,7 +285,7 @@ def ccv_update(x: torch.Tensor, conv_state: torch.Tensor, weight: torch.Tensor,
     if bias is not None and tuple(bias.shape) != (C,):
         raise ValueError("bias must be [C]")
     if out is None:
-        out = torch.empty_like(x3)
+        out = _new(stream, x.device, lambda: torch.empty_like(x3))
     out3 = out.unsqueeze(-1) if out.dim() == 2 else out
     if tuple(out3.shape) != (B, C, S):
         raise ValueError("out must have x's shape")
@@ -367,17 +384,17 @@ def ccv_bwd(x: torch.Tensor, weight: torch.Tensor, dout: torch.Tensor, bias: Opt
         if t is not None and (not t.is_cuda or t.device != x.device):
             raise ValueError("all tensors must live on x's CUDA device")
     if dx is None:
-        dx = _dense_like_fast_dim(x, B, C, L)
+        dx = _new(stream, x.device, lambda: _dense_like_fast_dim(x, B, C, L))
     if dweight is None:
-        dweight = torch.empty((C, K), dtype=weight.dtype, device=x.device)
+        dweight = _new(stream, x.device, lambda: torch.empty((C, K), dtype=weight.dtype, device=x.device))
     if dbias is None and bias is not None:
-        dbias = torch.empty((C,), dtype=weight.dtype, device=x.device)
+        dbias = _new(stream, x.device, lambda: torch.empty((C,), dtype=weight.dtype, device=x.device))
     if dinitial_states is None and return_dinitial_states and initial_states is not None:
-        dinitial_states = torch.empty((B, C, K - 1), dtype=x.dtype, device=x.device)
+        dinitial_states = _new(stream, x.device, lambda: torch.empty((B, C, K - 1), dtype=x.dtype, device=x.device))
     dt = TORCH_DTYPE[x.dtype]
     need = ccv_bwd_workspace_size(x.stride(), dout.stride(), dx.stride(), B, C, L, K, dt)
     if workspace is None:
-        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=x.device)
+        workspace = _new(stream, x.device, lambda: torch.empty((max(need, 16),), dtype=torch.uint8, device=x.device))
     if stream is None:
         stream = torch.cuda.current_stream(x.device)
     with torch.cuda.device(x.device):
