@@ -236,11 +236,13 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
     const int64_t t0 = static_cast<int64_t>(c) * kC;
     bool late = !mbar_wait(&full[s], (n0 / NS) & 1);
     if constexpr (H == 2) late = pair_any(pair, late);  // a pair gives up together
-    if (late) {
+    if (late) {  // give up: no copy of this warp's, nor the other stage's, must outlive the block
+      cp_async_wait_all();
       if (lane == 0) {
         atomicOr(&g_fault, kFaultConsumerWait);
         if (NS == 2 && n0 + 1 < nc && !mbar_wait(&full[s ^ 1], ((n0 + 1) / NS) & 1))
           atomicOr(&g_fault, kFaultDrainWait);
+        bulk_wait_all();
       }
       return;
     }

@@ -253,10 +253,12 @@ __global__ void __launch_bounds__(32 * NW * H, 1)
     bool late = !mbar_wait(&full[s], (c >> 1) & 1);
     if constexpr (H == 2) late = pair_any(pair, late);  // a pair gives up together
     if (late) {
-      // give up: the other stage's copy must not outlive the block either
+      // give up: no copy of this warp's, nor the other stage's, must outlive the block
+      cp_async_wait_all();
       if (lane == 0) {
         atomicOr(&g_fault, kFaultConsumerWait);
         if (c + 1 < nc && !mbar_wait(&full[s ^ 1], ((c + 1) >> 1) & 1)) atomicOr(&g_fault, kFaultDrainWait);
+        if constexpr (SAVE) bulk_wait_all();
       }
       return;
     }
