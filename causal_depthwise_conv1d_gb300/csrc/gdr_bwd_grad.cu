@@ -25,18 +25,18 @@
 // (powers of two at most 1, relative to the product's largest; what falls
 // below 2^-24 of it is zero), and <S0, D> is the trace of a product.
 //
-// What bounds it: no unit alone.  A chunk and head of 128 x 128 takes about
-// 7400 tensor instructions of 16 x 8 x 16 (products of two FP32 operands take
-// three; 8 cycles each a quarter SM: 97 us of the 308 below) and 62 thousand
-// warp instructions, and one block of sixteen warps fills the registers of an
-// SM, so its phases follow one another.  Of some 34 thousand cycles a head, the
-// slices take 17 (their tensor instructions alone 11), the matrices A and B 4,
-// the products with them 4, and the rest is the factors before the slices and
-// the sums after them.  What measured faster: factors and first slices of the
-// next head on their way while this one is finished, dQ and dK leaving as whole
-// rows (308 -> 281 us), sums of independent products in turn (281 -> 266 us),
-// nothing for tiles above the diagonal (263 us; all for 2 x 2048 tokens x 32
-// heads on 16 key heads, bf16; eight warps instead of sixteen cost 5 us more).
+// What bounds it: no unit alone.  Of 265 us (2 x 2048 tokens x 32 heads on 16 key
+// heads, 128 x 128, bf16) the tensor pipe is busy 35 % (products of two FP32
+// operands take three instructions) and the issue slots 38 %: a chunk and head
+// takes 56 thousand warp instructions, and one block of sixteen warps fills the
+// registers of an SM, so its phases follow one another.  Of some 34 thousand
+// cycles a head, the slices take 17, the matrices A and B 4, the products with
+// them 4, and the rest is the factors before the slices and the sums after them.
+// What measured faster: factors and first slices of the next head on their way
+// while this one is finished, dQ and dK leaving as whole rows (308 -> 281 us),
+// sums of independent products in turn (281 -> 266 us), nothing for tiles above
+// the diagonal (263 us; eight warps instead of sixteen cost 5 us more).  That
+// values which are not finite stay where they are costs 2 us.
 #include "gdr_chunk.cuh"
 
 namespace ccv {

@@ -12,17 +12,17 @@
 // The block products run on tf32 tensor instructions, every operand as the sum
 // of two tf32 values (22 bits; the exponent range of FP32, so nothing is scaled)
 // and FP32 sums; on the FP32 units, whose operands all come from shared memory,
-// the 89 us below were 104.
+// the 92 us below were 107.
 //
 // What bounds it: the steps of one block follow one another between barriers,
 // so shared memory is kept small enough for four blocks an SM (the inverse and
 // L lie where k and q were, and T where L was; 64 registers).  The issue slots
-// are then 55 % busy, the load/store path 49 %, the integer pipe 38 %.  4096
+// are then 56 % busy, the load/store path 47 %, the integer pipe 38 %.  4096
 // chunks and heads of 128 channels on half as many key heads (8192 tokens x 32
-// heads) take 89 us, 2048 take 47 us, 10240 with a key head each 277 us.  Blocks
+// heads) take 92 us, 2048 take 48 us, 10240 with a key head each 281 us.  Blocks
 // of four warps were 2.8 times as slow as three blocks of eight an SM, which
 // were 1.1 times as slow as four.  The scan of the decays runs while k and q are
-// on their way (282 us beside the other warps' wait for it).
+// on their way (5 us more beside the other warps' wait for it).
 //
 // The results leave as bulk copies of the shared-memory image that the scan
 // reads back, already in its tile order.

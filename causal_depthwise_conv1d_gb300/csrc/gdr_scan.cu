@@ -24,15 +24,17 @@
 // What bounds it: the chain of one chunk after the other, in which a warp
 // alternates between tensor instructions (16-bit mma.sync, measured at 8 cycles
 // each a quarter SM) and the splitting of their results into the next operands
-// (2373 warp instructions a warp and chunk of 128 x 128, bf16).  With eight
-// warps a block the tensor pipe is 48 % and the issue slots 36 % busy; a second
+// (2324 warp instructions a warp and chunk of 128 x 128, bf16).  With eight
+// warps a block the tensor pipe is 55 % and the issue slots 31 % busy; a second
 // block does not fit beside 255 registers a thread (two warps a block, three
 // blocks an SM: spills, 611 us for 597).  A head's columns are spread over as
-// many blocks as it takes to fill the SMs; a chunk then takes 6.2 us in blocks
-// of eight groups, 3.7 us in blocks of four and 2.8 us in blocks of two groups
-// with two warps each.  8192 tokens x 32 heads: 361 us, 128 chunks of 2.8 us;
-// 8 x 2048 tokens x 40 heads: 410 us for the 304 heads that fill whole rounds
-// and 93 us for the other 16, in small blocks.
+// many blocks as it takes to fill the SMs; a chunk then takes 7.2 us in blocks
+// of eight groups, 4.8 us in blocks of four and 3.1 us in blocks of two groups
+// with two warps each.  8192 tokens x 32 heads: 399 us, 128 chunks of 3.1 us;
+// 8 x 2048 tokens x 40 heads: 459 us for the 304 heads that fill whole rounds
+// and 103 us for the other 16, in small blocks.  All operands of the output have
+// both terms, for bf16 too: with one (11 bits) these took 361, 410 and 93 us, and
+// one output in ten was another number than the exact value rounded.
 //
 // A chunk with a value that is not finite (in its inputs or in the state) is
 // taken token by token from the original inputs instead, so that nothing
@@ -680,8 +682,8 @@ cudaError_t launch_nw(const GdrArgs& a, const uint8_t* qk, const uint8_t* pkg, u
                       const Device& dev, cudaStream_t s) {
   // Blocks of few channels while that still puts no more than one on an SM.
   // Two warps a group only where one each would leave half the quarters of an
-  // SM idle (32 heads, 8192 tokens: 537 -> 368 us; with 64 heads, four groups
-  // a block, 119 -> 145 us in the state-keeping scan).
+  // SM idle (32 heads, 8192 tokens: 662 -> 493 us with all kernels; with 64
+  // heads, four groups a block, 119 -> 145 us in the state-keeping scan).
   const int64_t groups = (a.Dv + 15) / 16, sms = dev.sm_count;
   if constexpr (DT == kF32) {  // two terms of k and q: the stages leave room for one warp a group, four groups
     if (hd.heads * ((groups + 1) / 2) <= sms) return launch<DT, DK, 2, 1, SAVE>(a, qk, pkg, img, nc, hd, s);
@@ -691,7 +693,8 @@ cudaError_t launch_nw(const GdrArgs& a, const uint8_t* qk, const uint8_t* pkg, u
     if (hd.heads * ((groups + 3) / 4) <= sms) return launch<DT, DK, 4, 1, SAVE>(a, qk, pkg, img, nc, hd, s);
     // More than one block an SM: full rounds of whole heads, and the heads of
     // a last round that would not fill the SMs spread over smaller blocks
-    // behind them (a chunk takes 6.2, 3.7 or 2.9 us by the three shapes).
+    // behind them (a chunk takes 7.2, 4.8 or 3.1 us by the three shapes; 8 x 2048
+    // tokens x 40 heads 970 -> 870 us).
     const int64_t rest = hd.heads % sms;
     if (hd.heads > sms && groups <= 8 && rest > 0 && rest * ((groups + 3) / 4) <= sms) {
       const cudaError_t e =

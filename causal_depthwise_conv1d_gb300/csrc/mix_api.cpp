@@ -29,8 +29,10 @@ int64_t dtype_size(ccv_dtype d) { return d == CCV_F32 ? 4 : 2; }
 // The chunked kernels take Dk up to kGdrChunkDk.  They cost about 20 us before
 // their first chunk (FP32, with two terms of k and q, 30), the token-by-token
 // kernel 0.37 us a token while its blocks, three an SM of 152, run at once:
-// 64 tokens of 32 heads of 128 take 23.8 against 29.1 us in bf16, 77 tokens of
-// 24 heads 39.2 against 31.3 in FP32, 48 tokens of 256 heads 74 against 88.
+// 64 tokens of 32 heads of 128 take 22.6 against 28.7 us in bf16, 48 of them 22.3
+// against 22.6, of 256 heads 53 against 84 (FP32 74 against 88), and 77 tokens of
+// 24 heads in FP32 39.2 against 31.3.  (152: the workspace's size, which follows
+// from this, is a function of the sizes alone.)
 bool gdr_chunked(int64_t B, int64_t L, int64_t Hv, int64_t Dk, int64_t Dv, ccv_dtype dtype) {
   if (Dk > ccv::kGdrChunkDk) return false;
   const bool at_once = B * Hv * ((Dv + 31) / 32) <= 3 * 152;
