@@ -358,12 +358,13 @@ ccv_status ccv_bwd_mixed(const void* x, const int64_t x_strides[3],
  *
  * Precision.  States, decays and sums are FP32.  Sequences below 48 tokens (in
  * FP32 with few heads 96) and Dk > 128 have FP32 products too.  Longer ones go
- * in aligned chunks of 64 tokens through FP16 tensor instructions with FP32 (truncated)
- * sums: 16-bit q and k enter exactly, every other operand as two FP16 terms (22
- * bits), without the product of two low terms.  The terms share a power of two
- * along a row: for q and k a token's channels, for v, and what is made of it, a
- * value channel's tokens of the chunk.  There a value beside a token 2^n times
- * larger keeps min(22, 39 - n) bits, also where seq_idx parts the two.
+ * in aligned chunks of 64 tokens through FP16 tensor instructions, whose FP32
+ * sums truncate: 16-bit q and k enter exactly, every other operand as two FP16
+ * terms (22 bits), without the product of two low terms.  The terms share a
+ * power of two along a row: for q and k a token's channels, for v, and what is
+ * made of it, a value channel's tokens of the chunk.  There a value beside a
+ * token 2^n times larger keeps min(22, 39 - n) bits, also where seq_idx parts
+ * the two.
  * A call repeats bit for bit; the last bits of a head may change with the number
  * of heads in the call.
  *

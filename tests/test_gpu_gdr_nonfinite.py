@@ -58,3 +58,25 @@ def test_non_finite_values(dtype, L, Dv, what, value):
             assert bool(torch.isfinite(g[:, :20]).all()) and bool(torch.isfinite(g[:, 44:]).all()), n
         if what == "dout" or (what == "v" and n != "dg"):  # and the tokens that the definition leaves alone
             assert bool((torch.isfinite(g) == torch.isfinite(e)).all()), n
+
+
+@pytest.mark.parametrize("what", ["dout", "v", "k"])
+@pytest.mark.parametrize("heads,L", [((40, 160), 66), ((16, 64), 70)])  # four and eight groups of channels a block
+def test_many_heads(heads, L, what):
+    c = ref.gdr_inputs(62, 1, L, *heads, 64, 64, "bf16", state=True, grads=True)
+    ids = torch.zeros((1, L), dtype=torch.int32)
+    ids[:, 20:] = 1
+    ids[:, 44:] = 2
+    c["seq_idx"] = ids
+    c[what][0, 30, 3, 7] = float("nan")
+    got = backward(c)
+    for n, (e, bound) in gdr_bounds.gdr_bwd(c).items():
+        if n not in ("dg", "dinitial_state"):
+            bound = bound + ref.rounding(e, "bf16")
+        g, bound = got[n].double().cpu(), bound.expand_as(e)
+        at = torch.isfinite(e) & torch.isfinite(bound) & torch.isfinite(g)
+        assert bool(((g - e).abs() <= bound)[at].all()), n
+        assert not bool(torch.isfinite(g)[~torch.isfinite(e)].any()), n
+        if n != "dinitial_state":
+            assert bool(torch.isfinite(g[:, :20]).all()) and bool(torch.isfinite(g[:, 44:]).all()), n
+            assert bool(torch.isfinite(g[:, :, -1]).all()), n  # a head without one
