@@ -1,0 +1,73 @@
+// Shared by the kernels of the gated linear recurrence.
+//
+//   r = sigmoid(p), i = sigmoid(q), l = -rate r, a = exp(l), m = sqrt(1 - a^2)
+//   h_t = a_t h_{t-1} + m_t i_t x_t
+//
+// Where the decay is close to one both a and 1 - a^2 come from E = expm1(l):
+// a = 1 + E, 1 - a^2 = -E (2 + E).  For -0.35 <= l E is its Taylor polynomial
+// of degree 7 (remainder 0.35^7 / 8! = 1.6e-8 relative), below that 2^(l log2 e)
+// - 1 with the hardware's exponential (2^-22 relative, while 1 - a >= 0.29).  So a
+// is within 2^-24 of the exact decay where a state lasts longer than three
+// tokens, and m keeps its relative precision down to the smallest rates; from
+// a rounded to FP32, 1 - a^2 would have lost 10 of its 24 bits at a = 0.9995.
+#pragma once
+
+#include "ccv_common.cuh"
+#include "rec_internal.h"
+
+namespace ccv {
+
+constexpr float kGlrSeries = -0.35f;  // down to here the polynomial
+
+struct GlrGate {
+  float a, m2;   // decay, 1 - a^2
+  float r, omr;  // sigmoid of the decay gate, and 1 minus it
+  float l;       // log a
+  float i, omi;  // sigmoid of the input gate, and 1 minus it
+};
+
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// sigmoid(z) and 1 - sigmoid(z) = e^-z sigmoid(z) (one where e^-z leaves the
+// exponent's range).
+__device__ __forceinline__ void glr_sigmoid(float z, float& s, float& om) {
+  const float e = ex2_approx(__fmul_rn(z, -kLog2e));
+  s = rcp_approx(__fadd_rn(1.f, e));
+  om = e < 0x1p100f ? __fmul_rn(e, s) : 1.f;
+}
+
+__device__ __forceinline__ void glr_decay(float l, float& a, float& m2) {
+  float E = fmaf(l, 1.f / 5040.f, 1.f / 720.f);
+  E = fmaf(E, l, 1.f / 120.f);
+  E = fmaf(E, l, 1.f / 24.f);
+  E = fmaf(E, l, 1.f / 6.f);
+  E = fmaf(E, l, 0.5f);
+  E = fmaf(E, l, 1.f);
+  E = __fmul_rn(E, l);
+  const float far = ex2_approx(__fmul_rn(l, kLog2e));
+  const bool near = l >= kGlrSeries;
+  a = near ? __fadd_rn(1.f, E) : far;
+  E = near ? E : __fadd_rn(far, -1.f);
+  m2 = __fmul_rn(-E, __fadd_rn(2.f, E));
+}
+
+__device__ __forceinline__ GlrGate glr_gate(float p, float q, float rate) {
+  GlrGate g;
+  glr_sigmoid(p, g.r, g.omr);
+  glr_sigmoid(q, g.i, g.omi);
+  g.l = __fmul_rn(-rate, g.r);
+  glr_decay(g.l, g.a, g.m2);
+  return g;
+}
+
+}  // namespace ccv

@@ -25,6 +25,7 @@
 #include "ccv_common.cuh"
 #include "ccv_tma.cuh"
 #include "mix_internal.h"
+#include "rec_internal.h"
 
 namespace ccv {
 namespace {
@@ -745,6 +746,13 @@ int64_t ln_bwd_blocks(int64_t N, int64_t D) {
   const int64_t rows = D <= 256 ? (N + 7) / 8 : N;
   const int64_t most = 152 * (D <= 1024 ? 6 : D <= 2048 ? 4 : D <= 4096 ? 2 : 1);
   return rows < most ? rows : most;
+}
+
+cudaError_t launch_param_sums(const float* part, int64_t P, int64_t C, void* dw, int64_t dws, void* db, int64_t dbs,
+                              int wdt, cudaStream_t stream) {
+  LnBwdArgs a = {};
+  a.part = const_cast<float*>(part), a.D = C, a.dw = dw, a.dws = dws, a.db = db, a.dbs = dbs, a.wdt = wdt;
+  return launch_pdl(ln_bwd_reduce, static_cast<unsigned>((2 * C + 31) / 32), 1024, 0, stream, a, static_cast<int>(P));
 }
 
 unsigned read_and_clear_fault_ln() {

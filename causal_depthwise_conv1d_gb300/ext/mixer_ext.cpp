@@ -1,4 +1,5 @@
-// Tensor front end of the gated delta rule and layer normalisation: checks
+// Tensor front end of the gated delta rule, the gated linear recurrence and the
+// layer and group norms: checks
 // that need tensors, allocation of missing outputs and of the workspace, and
 // the C-ABI call (include/ccv.h) on the stream.  It does what mixer.py would
 // do in Python; a decode step or a small norm takes a few microseconds on the
@@ -311,6 +312,190 @@ std::tuple<int, Tensor, Opt, Opt> ln_bwd(const Tensor& x, const Opt& weight, con
   return {rc, dx, dweight, dbias};
 }
 
+struct GlrSizes {
+  int64_t B, L, C, chunks;
+  ccv_dtype dt;
+  at::ScalarType type;
+  int dev;
+};
+
+GlrSizes glr_sizes(const Tensor& x, const Tensor& p, const Tensor& q, const Tensor& rate) {
+  if (x.dim() != 3) throw py::value_error("x must be [B, L, C]");
+  GlrSizes s;
+  s.dt = dtype_of(x, "dtype");
+  s.type = x.scalar_type();
+  s.B = x.size(0), s.L = x.size(1), s.C = x.size(2), s.chunks = (s.L + 63) / 64;
+  s.dev = cuda_index(x);
+  check(s.dev, "decay_gate", p, {s.B, s.L, s.C}, s.type);
+  check(s.dev, "input_gate", q, {s.B, s.L, s.C}, s.type);
+  check(s.dev, "rate", rate, {s.C}, at::kFloat);
+  return s;
+}
+
+std::tuple<int, Tensor, Opt, Opt> glr_fwd(const Tensor& x, const Tensor& p, const Tensor& q, const Tensor& rate,
+                                          const Opt& seq_idx, const Opt& initial_state, bool want_final, Opt final_out,
+                                          bool want_chunks, Opt chunks_out, Opt out_given, const Opt& workspace,
+                                          std::optional<int64_t> stream) {
+  const GlrSizes s = glr_sizes(x, p, q, rate);
+  check(s.dev, "seq_idx", seq_idx, {s.B, s.L}, at::kInt);
+  check(s.dev, "initial_state", initial_state, {s.B, s.C}, at::kFloat);
+  const c10::cuda::OptionalCUDAGuard guard(x.device());
+  const Stream on(s.dev, stream);
+  const Tensor out = given(out_given, on, "out", {s.B, s.L, s.C}, s.type);
+  if (want_final || final_out) final_out = given(final_out, on, "final_state_out", {s.B, s.C}, at::kFloat);
+  if (want_chunks || chunks_out)
+    chunks_out = given(chunks_out, on, "chunk_states_out", {s.B, s.chunks, s.C}, at::kFloat);
+  uint64_t need = 0;
+  int rc = ccv_glr_fwd_workspace_size(s.B, s.L, s.C, s.dt, &need);
+  if (rc == CCV_OK) {
+    const Workspace w(workspace, need, on);
+    rc = ccv_glr_fwd(ptr(x), str(x), ptr(p), str(p), ptr(q), str(q), f32(ptr(rate)), rate.stride(0),
+                     static_cast<const int32_t*>(ptr(seq_idx)), str(seq_idx), f32(ptr(initial_state)),
+                     str(initial_state), out_ptr(out), str(out), f32(out_ptr(final_out)), str(final_out),
+                     f32(out_ptr(chunks_out)), str(chunks_out), w.p, w.bytes, s.B, s.L, s.C, s.dt, on.raw());
+  }
+  return {rc, out, final_out, chunks_out};
+}
+
+std::tuple<int, Tensor> glr_step(const Tensor& x_, const Tensor& p_, const Tensor& q_, const Tensor& rate,
+                                 const Tensor& state, const Opt& state_indices, Opt out_given,
+                                 std::optional<int64_t> stream) {
+  const bool one = x_.dim() == 2;
+  auto tok = [one](const Tensor& t) { return one ? t.unsqueeze(1) : t; };
+  const Tensor x = tok(x_), p = tok(p_), q = tok(q_);
+  const GlrSizes s = glr_sizes(x, p, q, rate);
+  if (state.dim() != 2) throw py::value_error("state must be [n_slots, C]");
+  check(s.dev, "state", state, {state.size(0), s.C}, at::kFloat);
+  check(s.dev, "state_indices", state_indices, {s.B}, at::kInt);
+  const c10::cuda::OptionalCUDAGuard guard(x.device());
+  const Stream on(s.dev, stream);
+  Opt shaped = out_given ? Opt(tok(*out_given)) : Opt();
+  const Tensor out = given(shaped, on, "out", {s.B, s.L, s.C}, s.type);
+  const int rc = ccv_glr_step(ptr(x), str(x), ptr(p), str(p), ptr(q), str(q), f32(ptr(rate)), rate.stride(0),
+                              f32(out_ptr(state)), str(state), state.size(0),
+                              static_cast<const int32_t*>(ptr(state_indices)), stride0(state_indices), out_ptr(out),
+                              str(out), s.B, s.L, s.C, s.dt, on.raw());
+  return {rc, out_given ? *out_given : one ? out.squeeze(1) : out};
+}
+
+std::tuple<int, Tensor, Tensor, Tensor, Tensor, Opt> glr_bwd(
+    const Tensor& x, const Tensor& p, const Tensor& q, const Tensor& rate, const Tensor& dout, const Opt& seq_idx,
+    const Opt& initial_state, const Opt& dfinal_state, const Opt& chunk_states, Opt dx_, Opt dp_, Opt dq_, Opt drate_,
+    Opt ds0, bool want_ds0, const Opt& workspace, std::optional<int64_t> stream) {
+  const GlrSizes s = glr_sizes(x, p, q, rate);
+  const int64_t blc[3] = {s.B, s.L, s.C}, bc[2] = {s.B, s.C};
+  check(s.dev, "seq_idx", seq_idx, {s.B, s.L}, at::kInt);
+  check(s.dev, "initial_state", initial_state, bc, at::kFloat);
+  check(s.dev, "dout", dout, blc, s.type);
+  check(s.dev, "dfinal_state", dfinal_state, bc, at::kFloat);
+  check(s.dev, "chunk_states", chunk_states, {s.B, s.chunks, s.C}, at::kFloat);
+  const c10::cuda::OptionalCUDAGuard guard(x.device());
+  const Stream on(s.dev, stream);
+  const Tensor dx = given(dx_, on, "dx", blc, s.type), dp = given(dp_, on, "ddecay_gate", blc, s.type);
+  const Tensor dq = given(dq_, on, "dinput_gate", blc, s.type), drate = given(drate_, on, "drate", {s.C}, at::kFloat);
+  if (ds0 || (want_ds0 && initial_state)) ds0 = given(ds0, on, "dinitial_state", bc, at::kFloat);
+  uint64_t need = 0;
+  int rc = ccv_glr_bwd_workspace_size(s.B, s.L, s.C, s.dt, &need);
+  if (rc == CCV_OK) {
+    const Workspace w(workspace, need, on);
+    rc = ccv_glr_bwd(ptr(x), str(x), ptr(p), str(p), ptr(q), str(q), f32(ptr(rate)), rate.stride(0),
+                     static_cast<const int32_t*>(ptr(seq_idx)), str(seq_idx), f32(ptr(initial_state)),
+                     str(initial_state), ptr(dout), str(dout), f32(ptr(dfinal_state)), str(dfinal_state),
+                     f32(ptr(chunk_states)), str(chunk_states), out_ptr(dx), str(dx), out_ptr(dp), str(dp), out_ptr(dq),
+                     str(dq), f32(out_ptr(drate)), drate.stride(0), f32(out_ptr(ds0)), str(ds0), w.p, w.bytes, s.B,
+                     s.L, s.C, s.dt, on.raw());
+  }
+  return {rc, dx, dp, dq, drate, ds0};
+}
+
+// [N, ..., C] as [N, S, C] without a copy: the strides of the three dimensions.
+struct Samples {
+  int64_t strides[3];
+};
+Samples samples(const Tensor& x) {
+  Samples r = {{x.stride(0), 0, x.stride(x.dim() - 1)}};
+  int64_t step = 0;
+  bool first = true;
+  for (int64_t d = x.dim() - 2; d >= 1; --d) {
+    if (x.size(d) == 1) continue;
+    if (first) {
+      r.strides[1] = x.stride(d);
+      first = false;
+    } else if (x.stride(d) != step) {
+      throw py::value_error(
+          "the inner dimensions of a group norm's tensor must collapse into one stride (pass a 3-D view)");
+    }
+    step = x.stride(d) * x.size(d);
+  }
+  if (first) r.strides[1] = x.size(x.dim() - 1);  // one position
+  return r;
+}
+
+struct GnSizes {
+  int64_t N, S, C;
+  ccv_dtype dt, wdt;
+  at::ScalarType wtype;
+  int dev;
+};
+
+GnSizes gn_sizes(const Tensor& x, const Opt& weight, const Opt& bias) {
+  if (x.dim() < 2) throw py::value_error("x must be [N, ..., C]");
+  GnSizes s;
+  s.dt = dtype_of(x, "dtype");
+  const Tensor& par = weight ? *weight : bias ? *bias : x;
+  s.wdt = dtype_of(par, "weight dtype");
+  s.wtype = par.scalar_type();
+  s.N = x.size(0), s.C = x.size(x.dim() - 1), s.S = 1;
+  for (int64_t d = 1; d + 1 < x.dim(); ++d) s.S *= x.size(d);
+  s.dev = cuda_index(x);
+  check(s.dev, "weight", weight, {s.C}, s.wtype);
+  check(s.dev, "bias", bias, {s.C}, s.wtype);
+  return s;
+}
+
+std::tuple<int, Tensor> gn_fwd(const Tensor& x, int64_t groups, const Opt& weight, const Opt& bias, double eps,
+                               bool silu, Opt out_given, const Opt& workspace, std::optional<int64_t> stream) {
+  const GnSizes s = gn_sizes(x, weight, bias);
+  const c10::cuda::OptionalCUDAGuard guard(x.device());
+  const Stream on(s.dev, stream);
+  const Tensor out = given(out_given, on, "out", x.sizes(), x.scalar_type());
+  Samples xr = {{0, 0, 0}}, yr = xr;
+  if (x.numel() > 0) xr = samples(x), yr = samples(out);
+  uint64_t need = 0;
+  int rc = ccv_gn_fwd_workspace_size(s.N, s.S, s.C, groups, &need);
+  if (rc == CCV_OK) {
+    const Workspace w(workspace, need, on);
+    rc = ccv_gn_fwd(ptr(x), xr.strides, ptr(weight), stride0(weight), ptr(bias), stride0(bias), out_ptr(out),
+                    yr.strides, w.p, w.bytes, s.N, s.S, s.C, groups, static_cast<float>(eps),
+                    silu ? CCV_ACT_SILU : CCV_ACT_NONE, s.dt, s.wdt, on.raw());
+  }
+  return {rc, out};
+}
+
+std::tuple<int, Tensor, Opt, Opt> gn_bwd(const Tensor& x, int64_t groups, const Opt& weight, const Tensor& dout,
+                                         const Opt& bias, double eps, bool silu, Opt dx_, Opt dweight, Opt dbias,
+                                         const Opt& workspace, std::optional<int64_t> stream) {
+  const GnSizes s = gn_sizes(x, weight, bias);
+  check(s.dev, "dout", dout, x.sizes(), x.scalar_type());
+  const c10::cuda::OptionalCUDAGuard guard(x.device());
+  const Stream on(s.dev, stream);
+  const Tensor dx = given(dx_, on, "dx", x.sizes(), x.scalar_type());
+  if (dweight || weight) dweight = given(dweight, on, "dweight", {s.C}, s.wtype);
+  if (dbias || bias) dbias = given(dbias, on, "dbias", {s.C}, s.wtype);
+  Samples xr = {{0, 0, 0}}, gr = xr, dr = xr;
+  if (x.numel() > 0) xr = samples(x), gr = samples(dout), dr = samples(dx);
+  uint64_t need = 0;
+  int rc = ccv_gn_bwd_workspace_size(s.N, s.S, s.C, groups, &need);
+  if (rc == CCV_OK) {
+    const Workspace w(workspace, need, on);
+    rc = ccv_gn_bwd(ptr(x), xr.strides, ptr(weight), stride0(weight), ptr(bias), stride0(bias), ptr(dout), gr.strides,
+                    out_ptr(dx), dr.strides, out_ptr(dweight), stride0(dweight), out_ptr(dbias), stride0(dbias), w.p,
+                    w.bytes, s.N, s.S, s.C, groups, static_cast<float>(eps), silu ? CCV_ACT_SILU : CCV_ACT_NONE, s.dt,
+                    s.wdt, on.raw());
+  }
+  return {rc, dx, dweight, dbias};
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_mixer_ext, m) {
@@ -319,4 +504,9 @@ PYBIND11_MODULE(_mixer_ext, m) {
   m.def("gdr_bwd", &gdr_bwd);
   m.def("ln_fwd", &ln_fwd);
   m.def("ln_bwd", &ln_bwd);
+  m.def("glr_fwd", &glr_fwd);
+  m.def("glr_step", &glr_step);
+  m.def("glr_bwd", &glr_bwd);
+  m.def("gn_fwd", &gn_fwd);
+  m.def("gn_bwd", &gn_bwd);
 }

@@ -1,4 +1,5 @@
-"""Binding of the gated delta rule and of layer normalisation (include/ccv.h).
+"""Binding of the gated delta rule, the gated linear recurrence and the layer
+and group norms (include/ccv.h).
 
 As in ``binding.py``: argument checks that need tensors, allocation of missing
 outputs and of the workspace, and the C call on the tensor's current stream.
@@ -11,6 +12,12 @@ the library's kernels alone.
     gated_delta_rule_step   decode step             (ccv_gdr_step)
     layer_norm_fwd          layer normalisation     (ccv_ln_fwd)
     layer_norm_bwd          its backward pass       (ccv_ln_bwd)
+
+    gated_linear_recurrence_fwd    whole sequences      (ccv_glr_fwd)
+    gated_linear_recurrence_bwd    its backward pass    (ccv_glr_bwd)
+    gated_linear_recurrence_step   decode step          (ccv_glr_step)
+    group_norm_fwd                 group normalisation  (ccv_gn_fwd)
+    group_norm_bwd                 its backward pass    (ccv_gn_bwd)
 """
 from __future__ import annotations
 
@@ -37,6 +44,16 @@ _SIGNATURES = {
     "ccv_ln_fwd": _T + [_vp, _i64] * 2 + _T + [_i64, _i64, _f32, _int, _int, _vp],
     "ccv_ln_bwd": _T + [_vp, _i64] + _T * 2 + [_vp, _i64] * 2 + [_vp, _u64, _i64, _i64, _f32, _int, _int, _vp],
     "ccv_ln_bwd_workspace_size": [_i64, _i64, ctypes.POINTER(_u64)],
+    "ccv_glr_fwd": _T * 3 + [_vp, _i64] + _T * 5 + [_vp, _u64] + [_i64] * 3 + [_int, _vp],
+    "ccv_glr_fwd_workspace_size": [_i64] * 3 + [_int, ctypes.POINTER(_u64)],
+    "ccv_glr_step": _T * 3 + [_vp, _i64] + _T + [_i64, _vp, _i64] + _T + [_i64] * 3 + [_int, _vp],
+    "ccv_glr_bwd": _T * 3 + [_vp, _i64] + _T * 8 + [_vp, _i64] + _T + [_vp, _u64] + [_i64] * 3 + [_int, _vp],
+    "ccv_glr_bwd_workspace_size": [_i64] * 3 + [_int, ctypes.POINTER(_u64)],
+    "ccv_gn_fwd": _T + [_vp, _i64] * 2 + _T + [_vp, _u64] + [_i64] * 4 + [_f32, _int, _int, _int, _vp],
+    "ccv_gn_fwd_workspace_size": [_i64] * 4 + [ctypes.POINTER(_u64)],
+    "ccv_gn_bwd": _T + [_vp, _i64] * 2 + _T * 2 + [_vp, _i64] * 2 + [_vp, _u64] + [_i64] * 4 +
+                  [_f32, _int, _int, _int, _vp],
+    "ccv_gn_bwd_workspace_size": [_i64] * 4 + [ctypes.POINTER(_u64)],
 }
 _bound = {}
 
@@ -192,8 +209,142 @@ def ccv_ln_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], dout: torch.Tens
     return tuple(grads)
 
 
+def ccv_glr_fwd_workspace_size(B: int, L: int, C: int, dtype: int) -> int:
+    """Bytes of workspace ``ccv_glr_fwd`` needs for these sizes."""
+    return _need("ccv_glr_fwd_workspace_size", B, L, C, dtype)
+
+
+def ccv_glr_fwd(x: torch.Tensor, decay_gate: torch.Tensor, input_gate: torch.Tensor, rate: torch.Tensor,
+                seq_idx: Optional[torch.Tensor] = None, initial_state: Optional[torch.Tensor] = None,
+                return_final_state: bool = False, final_state_out: Optional[torch.Tensor] = None,
+                return_chunk_states: bool = False, chunk_states_out: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None):
+    """Gated linear recurrence over whole sequences: with
+    a = exp(-rate sigmoid(decay_gate)), h_t = a h_{t-1} + sqrt(1 - a^2) sigmoid(input_gate) x.
+
+    x, decay_gate, input_gate [B,L,C] (any strides; the gates before their
+    sigmoid), rate FP32 [C] >= 0, seq_idx int32 [B,L], initial_state FP32 [B,C].
+    Returns ``out`` [B,L,C], followed, where requested, by the final state FP32
+    [B,C] and by the states before every 64th token FP32 [B,ceil(L/64),C],
+    which ``ccv_glr_bwd`` takes.
+    """
+    rc, out, *extra = (_ext_module or _ext()).glr_fwd(x, decay_gate, input_gate, rate, seq_idx, initial_state,
+                                                      return_final_state, final_state_out, return_chunk_states,
+                                                      chunk_states_out, out, workspace,
+                                                      None if stream is None else stream.cuda_stream)
+    if rc:
+        _raise(rc)
+    extra = [t for t in extra if t is not None]
+    return (out, *extra) if extra else out
+
+
+def ccv_glr_step(x: torch.Tensor, decay_gate: torch.Tensor, input_gate: torch.Tensor, rate: torch.Tensor,
+                 state: torch.Tensor, state_indices: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Decode step of the gated linear recurrence: S new tokens per request
+    against the cache ``state`` FP32 [n_slots,C], advanced in place.
+
+    x, decay_gate, input_gate [B,S,C], or [B,C] for one token.
+    ``state_indices`` int32 [B] names each request's slot (default: request b
+    uses slot b); negative or too large: a padding row, whose outputs are zero.
+    Returns out in x's shape.
+    """
+    rc, out = (_ext_module or _ext()).glr_step(x, decay_gate, input_gate, rate, state, state_indices, out,
+                                               None if stream is None else stream.cuda_stream)
+    if rc:
+        _raise(rc)
+    return out
+
+
+def ccv_glr_bwd_workspace_size(B: int, L: int, C: int, dtype: int) -> int:
+    """Bytes of workspace ``ccv_glr_bwd`` needs for these sizes."""
+    return _need("ccv_glr_bwd_workspace_size", B, L, C, dtype)
+
+
+def ccv_glr_bwd(x: torch.Tensor, decay_gate: torch.Tensor, input_gate: torch.Tensor, rate: torch.Tensor,
+                dout: torch.Tensor, seq_idx: Optional[torch.Tensor] = None,
+                initial_state: Optional[torch.Tensor] = None, dfinal_state: Optional[torch.Tensor] = None,
+                chunk_states: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                ddecay_gate: Optional[torch.Tensor] = None, dinput_gate: Optional[torch.Tensor] = None,
+                drate: Optional[torch.Tensor] = None, dinitial_state: Optional[torch.Tensor] = None,
+                return_dinitial_state: bool = False, workspace: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None):
+    """Backward pass of ``ccv_glr_fwd``: returns (dx, ddecay_gate, dinput_gate, drate, dinitial_state).
+
+    The forward's inputs plus dout [B,L,C] and dfinal_state FP32 [B,C] (or
+    None).  ``chunk_states`` is what the forward pass returned with
+    ``return_chunk_states``; without it the states are computed once more.
+    Gradients have their inputs' shapes and dtypes; dinitial_state is made when
+    initial_state is given and ``return_dinitial_state`` is set (or the tensor
+    is passed in).
+    """
+    rc, *grads = (_ext_module or _ext()).glr_bwd(x, decay_gate, input_gate, rate, dout, seq_idx, initial_state,
+                                                 dfinal_state, chunk_states, dx, ddecay_gate, dinput_gate, drate,
+                                                 dinitial_state, return_dinitial_state, workspace,
+                                                 None if stream is None else stream.cuda_stream)
+    if rc:
+        _raise(rc)
+    return tuple(grads)
+
+
+def _silu(activation: Optional[str]) -> bool:
+    if activation not in (None, "silu", "swish"):
+        raise ValueError(f"activation must be None, 'silu' or 'swish', got {activation!r}")
+    return activation is not None
+
+
+def ccv_gn_fwd_workspace_size(N: int, S: int, C: int, groups: int) -> int:
+    """Bytes of workspace ``ccv_gn_fwd`` needs."""
+    return _need("ccv_gn_fwd_workspace_size", N, S, C, groups)
+
+
+def ccv_gn_fwd(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, eps: float = 1e-5, activation: Optional[str] = None,
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Group normalisation of x [N, ..., C], channels last, then the activation (None, "silu" or "swish").
+
+    Statistics of C / groups adjacent channels over all inner dimensions; with
+    x [N, C] every row's groups on their own, as the norm of a token's heads.
+    weight and bias [C] in a dtype of their own, or None.
+    """
+    rc, out = (_ext_module or _ext()).gn_fwd(x, groups, weight, bias, eps, _silu(activation), out, workspace,
+                                             None if stream is None else stream.cuda_stream)
+    if rc:
+        _raise(rc)
+    return out
+
+
+def ccv_gn_bwd_workspace_size(N: int, S: int, C: int, groups: int) -> int:
+    """Bytes of workspace ``ccv_gn_bwd`` needs."""
+    return _need("ccv_gn_bwd_workspace_size", N, S, C, groups)
+
+
+def ccv_gn_bwd(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor], dout: torch.Tensor,
+               bias: Optional[torch.Tensor] = None, eps: float = 1e-5, activation: Optional[str] = None,
+               dx: Optional[torch.Tensor] = None, dweight: Optional[torch.Tensor] = None,
+               dbias: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None):
+    """Backward pass of ``ccv_gn_fwd``: returns (dx, dweight, dbias).
+
+    x, groups, weight, bias, eps, activation: the forward's; dout in x's shape.
+    dweight (dbias) is made when weight (bias) is given, in its dtype.
+    """
+    rc, *grads = (_ext_module or _ext()).gn_bwd(x, groups, weight, dout, bias, eps, _silu(activation), dx, dweight,
+                                                dbias, workspace, None if stream is None else stream.cuda_stream)
+    if rc:
+        _raise(rc)
+    return tuple(grads)
+
+
 gated_delta_rule_fwd = ccv_gdr_fwd
 gated_delta_rule_bwd = ccv_gdr_bwd
 gated_delta_rule_step = ccv_gdr_step
 layer_norm_fwd = ccv_ln_fwd
 layer_norm_bwd = ccv_ln_bwd
+gated_linear_recurrence_fwd = ccv_glr_fwd
+gated_linear_recurrence_bwd = ccv_glr_bwd
+gated_linear_recurrence_step = ccv_glr_step
+group_norm_fwd = ccv_gn_fwd
+group_norm_bwd = ccv_gn_bwd

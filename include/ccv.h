@@ -488,6 +488,159 @@ ccv_status ccv_ln_bwd(const void* x, const int64_t x_strides[2], const void* wei
 /* Bytes of workspace ccv_ln_bwd needs (0 where N or D is 0).  Host only. */
 ccv_status ccv_ln_bwd_workspace_size(int64_t N, int64_t D, uint64_t* bytes);
 
+/*
+ * ccv_glr_fwd -- gated linear recurrence over whole sequences.
+ *
+ * For every batch row b and channel c, with a state h that starts as
+ * initial_state (or zero), token by token:
+ *     a = exp(-rate[c] sigmoid(decay_gate[b,t,c]))
+ *     h <- a h + sqrt(1 - a^2) sigmoid(input_gate[b,t,c]) x[b,t,c]
+ *     out[b,t,c] = h
+ *
+ *   x, decay_gate, input_gate, out   [B,L,C] in dtype.  The gates are given
+ *                     before their sigmoid.
+ *   rate              FP32 [C], >= 0 (a negative one gives NaN or a state that
+ *                     grows).
+ *   seq_idx           int32 [B,L] or NULL.  Where seq_idx[b,t] differs from
+ *                     seq_idx[b,t-1] a new sequence begins: token t sees the
+ *                     zero state.  initial_state belongs to the sequence of
+ *                     token 0.
+ *   initial_state     FP32 [B,C] or NULL (zero).
+ *   final_state_out   FP32 [B,C] or NULL; the state after token L-1.
+ *   chunk_states_out  FP32 [B,ceil(L/64),C] or NULL; the state before every
+ *                     64th token, which ccv_glr_bwd takes.
+ *   workspace         device buffer of ccv_glr_fwd_workspace_size() bytes,
+ *                     128-byte aligned (may be NULL where that is 0).  Contents
+ *                     undefined before and after; calls in flight at the same
+ *                     time must not share it.
+ * Any strides; unit stride along the channels with rows on 16-byte boundaries
+ * is the fast layout (gates as slices of one projection are).
+ *
+ * Precision.  Gates, decays, states and sums are FP32; exponentials and
+ * reciprocals are the hardware's (2^-22 relative).  sqrt(1 - a^2) keeps its
+ * relative precision where a is close to one.  out is rounded once (nearest
+ * even).  The order of operations depends on the sizes alone: a call repeats
+ * bit for bit.
+ *
+ * out, final_state_out and chunk_states_out must not share memory with an
+ * input or each other.  Non-finite values affect what the definition says, and
+ * nothing before their own token or across a change of seq_idx.
+ * B or C == 0 is a no-op; L == 0 copies the initial state.
+ */
+ccv_status ccv_glr_fwd(const void* x, const int64_t x_strides[3], const void* decay_gate,
+                       const int64_t decay_gate_strides[3], const void* input_gate,
+                       const int64_t input_gate_strides[3], const float* rate, int64_t rate_stride,
+                       const int32_t* seq_idx, const int64_t seq_idx_strides[2], const float* initial_state,
+                       const int64_t initial_state_strides[2], void* out, const int64_t out_strides[3],
+                       float* final_state_out, const int64_t final_state_strides[2], float* chunk_states_out,
+                       const int64_t chunk_states_strides[3], void* workspace, uint64_t workspace_bytes, int64_t B,
+                       int64_t L, int64_t C, ccv_dtype dtype, void* stream);
+
+/* Bytes of workspace ccv_glr_fwd needs for these sizes (0: none).  Host only. */
+ccv_status ccv_glr_fwd_workspace_size(int64_t B, int64_t L, int64_t C, ccv_dtype dtype, uint64_t* bytes);
+
+/*
+ * ccv_glr_step -- gated linear recurrence, decode step: S new tokens per
+ * request (S is usually 1) against a cache of states, advanced in place.
+ *
+ *   state             FP32 [n_slots,C], read and overwritten.
+ *   state_indices     int32 [B] or NULL (request b uses slot b).  A negative
+ *                     index, or one >= n_slots, marks a padding row: no state
+ *                     is touched and its outputs are zero.  Two requests of
+ *                     one call must not name the same slot.
+ *   x, decay_gate, input_gate, rate, out as for ccv_glr_fwd with L = S.
+ */
+ccv_status ccv_glr_step(const void* x, const int64_t x_strides[3], const void* decay_gate,
+                        const int64_t decay_gate_strides[3], const void* input_gate,
+                        const int64_t input_gate_strides[3], const float* rate, int64_t rate_stride, float* state,
+                        const int64_t state_strides[2], int64_t n_slots, const int32_t* state_indices,
+                        int64_t state_indices_stride, void* out, const int64_t out_strides[3], int64_t B, int64_t S,
+                        int64_t C, ccv_dtype dtype, void* stream);
+
+/*
+ * ccv_glr_bwd -- gated linear recurrence, backward pass: the gradients of
+ * sum(out dout) + sum(final_state dfinal_state).
+ *
+ *   x .. initial_state  the forward pass's arguments.
+ *   dout              [B,L,C] in dtype.
+ *   dfinal_state      FP32 [B,C] or NULL (zero).
+ *   chunk_states      what ccv_glr_fwd wrote for the same arguments, or NULL:
+ *                     then the states are computed once more.
+ *   dx, ddecay_gate, dinput_gate   [B,L,C] in dtype.  Required.
+ *   drate             FP32 [C], summed over B and L.  Required.
+ *   dinitial_state    FP32 [B,C] or NULL; needs initial_state.
+ *   workspace         ccv_glr_bwd_workspace_size() bytes, 128-byte aligned.
+ *
+ * Precision as for ccv_glr_fwd; sums are FP32 in a fixed order (bitwise
+ * reproducible).  Where 1 - a^2 is zero in FP32 (a rate of zero, a gate that is
+ * closed completely) the derivative of its root is taken as zero: that is its
+ * limit in ddecay_gate, while the one in drate has none.
+ * Outputs must not share memory with an input or each other.
+ * C == 0 is a no-op; with B or L == 0 drate is zero and dinitial_state is
+ * dfinal_state.
+ */
+ccv_status ccv_glr_bwd(const void* x, const int64_t x_strides[3], const void* decay_gate,
+                       const int64_t decay_gate_strides[3], const void* input_gate,
+                       const int64_t input_gate_strides[3], const float* rate, int64_t rate_stride,
+                       const int32_t* seq_idx, const int64_t seq_idx_strides[2], const float* initial_state,
+                       const int64_t initial_state_strides[2], const void* dout, const int64_t dout_strides[3],
+                       const float* dfinal_state, const int64_t dfinal_state_strides[2], const float* chunk_states,
+                       const int64_t chunk_states_strides[3], void* dx, const int64_t dx_strides[3],
+                       void* ddecay_gate, const int64_t ddecay_gate_strides[3], void* dinput_gate,
+                       const int64_t dinput_gate_strides[3], float* drate, int64_t drate_stride,
+                       float* dinitial_state, const int64_t dinitial_state_strides[2], void* workspace,
+                       uint64_t workspace_bytes, int64_t B, int64_t L, int64_t C, ccv_dtype dtype, void* stream);
+
+/* Bytes of workspace ccv_glr_bwd needs for these sizes.  Host only. */
+ccv_status ccv_glr_bwd_workspace_size(int64_t B, int64_t L, int64_t C, ccv_dtype dtype, uint64_t* bytes);
+
+/*
+ * ccv_gn_fwd -- group normalisation of x [N,S,C], channels last, with an
+ * activation:
+ *     out = act((x - mean) / sqrt(var + eps) * weight[c] + bias[c]),
+ * mean and (biased) variance of sample n's group of C / groups adjacent
+ * channels over all S positions, in FP32; out is rounded once to dtype.
+ * S == 1 normalises every row on its own, for instance each token's heads.
+ *
+ *   weight, bias      [C] in weight_dtype, or NULL (one, zero); any of the
+ *                     nine pairs of dtype and weight_dtype.
+ *   groups            >= 1, divides C.
+ *   eps               >= 0.
+ *   workspace         ccv_gn_fwd_workspace_size() bytes, 128-byte aligned (may
+ *                     be NULL where that is 0).
+ * Any strides; unit stride along the channels with rows and groups on 16-byte
+ * boundaries is the fast layout.
+ * out must not share memory with an input.  N, S or C == 0 is a no-op.
+ */
+ccv_status ccv_gn_fwd(const void* x, const int64_t x_strides[3], const void* weight, int64_t weight_stride,
+                      const void* bias, int64_t bias_stride, void* out, const int64_t out_strides[3], void* workspace,
+                      uint64_t workspace_bytes, int64_t N, int64_t S, int64_t C, int64_t groups, float eps,
+                      ccv_activation activation, ccv_dtype dtype, ccv_dtype weight_dtype, void* stream);
+
+/* Bytes of workspace ccv_gn_fwd needs for these sizes (0: none).  Host only. */
+ccv_status ccv_gn_fwd_workspace_size(int64_t N, int64_t S, int64_t C, int64_t groups, uint64_t* bytes);
+
+/*
+ * ccv_gn_bwd -- its backward pass.  Statistics and activations are taken again
+ * from x: nothing has to be kept from the forward pass.  With xh the
+ * normalised input, dz = dout act'(xh weight + bias) and d = dz weight:
+ *     dx      = (d - mean(d) - xh mean(d xh)) / sqrt(var + eps)
+ *     dweight = sum over N and S of dz * xh,   dbias = sum over N and S of dz
+ *   dx                [N,S,C] in dtype, required.
+ *   dweight, dbias    [C] in weight_dtype, or NULL.  Summed in FP32 in a fixed
+ *                     order (bitwise reproducible); zero where N or S == 0.
+ *   workspace         ccv_gn_bwd_workspace_size() bytes, 128-byte aligned.
+ */
+ccv_status ccv_gn_bwd(const void* x, const int64_t x_strides[3], const void* weight, int64_t weight_stride,
+                      const void* bias, int64_t bias_stride, const void* dout, const int64_t dout_strides[3], void* dx,
+                      const int64_t dx_strides[3], void* dweight, int64_t dweight_stride, void* dbias,
+                      int64_t dbias_stride, void* workspace, uint64_t workspace_bytes, int64_t N, int64_t S, int64_t C,
+                      int64_t groups, float eps, ccv_activation activation, ccv_dtype dtype, ccv_dtype weight_dtype,
+                      void* stream);
+
+/* Bytes of workspace ccv_gn_bwd needs (0 where N, S or C is 0).  Host only. */
+ccv_status ccv_gn_bwd_workspace_size(int64_t N, int64_t S, int64_t C, int64_t groups, uint64_t* bytes);
+
 /* Message for the last non-OK status returned on the calling thread ("" if
  * none).  The pointer stays valid until the next ccv_* call on that thread. */
 const char* ccv_last_error(void);
@@ -495,7 +648,8 @@ const char* ccv_last_error(void);
 /* Name of the kernel variant the last successful ccv_fwd, ccv_update or
  * ccv_bwd on this thread enqueued (e.g. "time_vec", "chlast_tma",
  * "chlast_vec", "generic", "update", "bwd_time", "bwd_chlast",
- * "bwd_generic", "gdr_step", "gdr_token", "gdr_chunk", "gdr_bwd", "ln_fwd", "ln_bwd", "none"). */
+ * "bwd_generic", "gdr_step", "gdr_token", "gdr_chunk", "gdr_bwd", "ln_fwd", "ln_bwd",
+ * "glr_fwd", "glr_step", "glr_bwd", "gn_fwd", "gn_bwd", "none"). */
 const char* ccv_last_kernel(void);
 
 /* Library ABI version: (major << 16) | minor. */
