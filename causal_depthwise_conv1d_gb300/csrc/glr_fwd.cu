@@ -1,0 +1,330 @@
+// Gated linear recurrence over whole sequences: one pass, every input read and
+// every output written once.
+//
+// A block of four warps takes tiles of 64 tokens x 64 channels; a warp has 16
+// tokens, a lane two channels.  Tensor copies bring the next tile's x and gates
+// into shared memory while the present one is worked on.  A warp computes its
+// tokens' decays and inputs into registers and their (A, H), the first warp
+// joins these, publishes them and gets the state before the tile (see
+// glr_tile.cuh), and every warp then runs its tokens from that state and writes
+// them.  So a state costs no second pass over the inputs, however few channels
+// there are to split the device by.
+#include "glr_tile.cuh"
+
+namespace ccv {
+namespace {
+
+__device__ unsigned g_fault;
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRun = kGlrT / kWarps;  // tokens of a warp
+constexpr int kStages = 2;
+
+struct Maps {
+  CUtensorMap x, p, q;
+};
+
+template <int DT>
+constexpr int plane_bytes() {
+  return kGlrT * kGlrC * (DT == kF32 ? 4 : 2);
+}
+
+struct __align__(16) Shared {
+  uint64_t full[kStages];
+  int tile[kStages];
+  float4 pair[2][kWarps][32];
+  float2 carry[2][32];
+  int late;
+};
+
+template <int DT, bool SEQ>
+__global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
+    glr_fwd_kernel(const GlrArgs a, const GlrTiles g, const GlrChain chain, const __grid_constant__ Maps maps) {
+  constexpr int PLANE = plane_bytes<DT>();
+  extern __shared__ __align__(128) uint8_t stages[];
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool chained = g.levels > 1;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1);
+    fence_barrier_init();
+    sh.late = 0;
+  }
+  pdl_enter();
+  __syncthreads();
+
+  // Thread 0 draws tiles and starts their copies.
+  int drawn = 0;
+  auto draw = [&]() -> int {
+    if (chained) return static_cast<int>(atomicAdd(chain.ticket, 1u));
+    const int t = static_cast<int>(blockIdx.x + drawn * gridDim.x);
+    ++drawn;
+    return t;
+  };
+  auto fill = [&](int s, int t) {
+    sh.tile[s] = t;
+    if (t >= g.total || !g.tma) {
+      mbar_arrive(&sh.full[s]);
+      return;
+    }
+    const int level = t / g.ncols, col = t - level * g.ncols, b = col / g.nct, c0 = (col - b * g.nct) * kGlrC;
+    uint8_t* st = stages + s * 3 * PLANE;
+    mbar_arrive_expect_tx(&sh.full[s], 3 * PLANE);
+    tma_load_3d(st, &maps.x, c0, level * kGlrT, b, &sh.full[s]);
+    tma_load_3d(st + PLANE, &maps.p, c0, level * kGlrT, b, &sh.full[s]);
+    tma_load_3d(st + 2 * PLANE, &maps.q, c0, level * kGlrT, b, &sh.full[s]);
+  };
+  int next = g.total;
+  if (tid == 0) {
+    fill(0, draw());
+    if (!g.one) fill(1, draw()), next = draw();
+  }
+
+  for (int it = 0;; ++it) {
+    const int s = it & 1, odd = it & 1;
+    if (it == 1 && g.one) return;
+    if (!mbar_wait(&sh.full[s], (it >> 1) & 1)) {
+      if (tid == 0) {
+        atomicOr(&g_fault, kFaultConsumerWait);
+        if (!g.one) mbar_wait(&sh.full[s ^ 1], ((it + 1) >> 1) & 1);  // the other copies in flight
+      }
+      return;
+    }
+    const int tile = sh.tile[s];
+    if (tile >= g.total) return;
+    const int level = tile / g.ncols, col = tile - level * g.ncols, b = col / g.nct;
+    const int c = (col - b * g.nct) * kGlrC + 2 * lane;
+    const int64_t t0 = static_cast<int64_t>(level) * kGlrT + warp * kRun;
+    const bool in0 = c < a.C, in1 = c + 1 < a.C;
+    const int64_t left = a.L - t0;
+    const int n = left >= kRun ? kRun : left > 0 ? static_cast<int>(left) : 0;  // tokens of this warp
+    unsigned reset = 0;  // bit j: a sequence starts at the warp's token j
+    if constexpr (SEQ) {
+      bool start = false;
+      if (lane < n && t0 + lane > 0) {
+        const int32_t* id = a.seq + b * a.ss[0] + (t0 + lane) * a.ss[1];
+        start = id[0] != id[-a.ss[1]];
+      }
+      reset = __ballot_sync(kFullMask, start);
+    }
+    const uint64_t rate = pk(in0 ? -__ldg(a.rate + c * a.rs) : 0.f, in1 ? -__ldg(a.rate + (c + 1) * a.rs) : 0.f);
+
+    uint64_t dec[kRun], in[kRun], A = pk(1.f, 1.f), H = 0;
+    const uint8_t* st = stages + s * 3 * PLANE;
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      uint64_t x, p, q;
+      if (g.tma) {
+        x = glr_lds<DT>(st, warp * kRun + j, lane);
+        p = glr_lds<DT>(st + PLANE, warp * kRun + j, lane);
+        q = glr_lds<DT>(st + 2 * PLANE, warp * kRun + j, lane);
+      } else {
+        const bool on = j < n;
+        const int64_t t = t0 + j;
+        x = glr_ldg<DT>(a.x, b * a.xs[0] + t * a.xs[1] + c * a.xs[2], a.xs[2], on && in0, on && in1);
+        p = glr_ldg<DT>(a.p, b * a.ps[0] + t * a.ps[1] + c * a.ps[2], a.ps[2], on && in0, on && in1);
+        q = glr_ldg<DT>(a.q, b * a.qs[0] + t * a.qs[1] + c * a.qs[2], a.qs[2], on && in0, on && in1);
+      }
+      uint64_t r, i, e, m2;
+      glr_sigmoid2(p, r, e);
+      glr_sigmoid2(q, i, e);
+      glr_decay2(fmul2(rate, r), dec[j], m2);
+      float u, v;
+      upk(m2, u, v);
+      in[j] = fmul2(pk(sqrt_approx(u), sqrt_approx(v)), fmul2(i, x));
+      if (j >= n) dec[j] = pk(1.f, 1.f), in[j] = 0;
+      if (SEQ && (reset >> j & 1)) {
+        A = pk(kMinusZero, kMinusZero);
+        H = in[j];
+      } else {
+        A = fmul2(A, dec[j]);
+        H = ffma2(dec[j], H, in[j]);
+      }
+    }
+    {
+      float2 x, y;
+      upk(A, x.x, x.y), upk(H, y.x, y.y);
+      sh.pair[odd][warp][lane] = make_float4(x.x, y.x, x.y, y.y);
+    }
+    __syncthreads();  // pairs are there, the stage has been read
+    if (tid == 0 && !g.one) {
+      fence_proxy_async_smem();
+      fill(s, next);
+      next = draw();
+    }
+    if (warp == 0) {
+      float2 h = make_float2(0.f, 0.f);
+      float4 m = sh.pair[odd][0][lane];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) {
+        const float4 v = sh.pair[odd][w][lane];
+        glr_join(v.x, v.y, m.x, m.y);
+        glr_join(v.z, v.w, m.z, m.w);
+      }
+      bool ok = true;
+      if (level == 0) {
+        if (a.s0 != nullptr) {
+          const float* p = a.s0 + b * a.s0s[0] + c * a.s0s[1];
+          h = make_float2(in0 ? p[0] : 0.f, in1 ? p[a.s0s[1]] : 0.f);
+        }
+      } else {
+        glr_publish_pair(chain, tile, lane, make_float2(m.x, m.z), make_float2(m.y, m.w));
+        ok = glr_look_back(chain, g, level, col, lane, h);
+      }
+      if (ok && level + 1 < g.levels)
+        glr_publish_state(chain, tile, lane, make_float2(glr_map(m.x, m.y, h.x), glr_map(m.z, m.w, h.y)));
+      if (!ok && lane == 0) {
+        atomicOr(&g_fault, kFaultConsumerWait);
+        sh.late = 1;
+      }
+      sh.carry[odd][lane] = h;
+      if (a.cs != nullptr) {
+        float* p = a.cs + b * a.css[0] + level * a.css[1] + c * a.css[2];
+        if (in0) p[0] = h.x;
+        if (in1) p[a.css[2]] = h.y;
+      }
+    }
+    __syncthreads();
+    if (sh.late) {
+      if (tid == 0 && !g.one) {  // the copies in flight
+        mbar_wait(&sh.full[s ^ 1], ((it + 1) >> 1) & 1);
+        mbar_wait(&sh.full[s], ((it + 2) >> 1) & 1);
+      }
+      return;
+    }
+    float2 h2 = sh.carry[odd][lane];
+    for (int w = 0; w < warp; ++w) {
+      const float4 v = sh.pair[odd][w][lane];
+      h2 = make_float2(glr_map(v.x, v.y, h2.x), glr_map(v.z, v.w, h2.y));
+    }
+    uint64_t h = pk(h2.x, h2.y);
+    const int64_t off = b * a.os[0] + t0 * a.os[1] + c * a.os[2];
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      h = SEQ && (reset >> j & 1) ? in[j] : ffma2(dec[j], h, in[j]);
+      if (j < n && a.out != nullptr) glr_stg<DT>(a.out, off + j * a.os[1], a.os[2], g.pair, in0, in1, h);
+    }
+    if (a.s1 != nullptr && n > 0 && t0 + n == a.L) {
+      float* p = a.s1 + b * a.s1s[0] + c * a.s1s[1];
+      upk(h, h2.x, h2.y);
+      if (in0) p[0] = h2.x;
+      if (in1) p[a.s1s[1]] = h2.y;
+    }
+  }
+}
+
+template <int DT, bool SEQ>
+cudaError_t launch(const GlrArgs& a, const GlrTiles& t, const GlrChain& chain, const Device& dev, cudaStream_t s) {
+  Maps maps = {};
+  if (t.tma) {
+    const int64_t box[2] = {kGlrC, kGlrT};
+    if (!glr_map3(&maps.x, a.x, a.xs, a.B, a.L, a.C, box, static_cast<Dtype>(DT)) ||
+        !glr_map3(&maps.p, a.p, a.ps, a.B, a.L, a.C, box, static_cast<Dtype>(DT)) ||
+        !glr_map3(&maps.q, a.q, a.qs, a.B, a.L, a.C, box, static_cast<Dtype>(DT)))
+      return cudaErrorInvalidValue;
+  }
+  const int smem = t.tma ? kStages * 3 * plane_bytes<DT>() : 0;
+  cudaError_t e = cudaFuncSetAttribute(glr_fwd_kernel<DT, SEQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kStages * 3 * plane_bytes<DT>());
+  if (e != cudaSuccess) return e;
+  const int64_t most = static_cast<int64_t>(dev.sm_count) * (DT == kF32 ? 2 : 4);
+  GlrTiles g = t;
+  g.one = g.total <= most;
+  return glr_launch(glr_fwd_kernel<DT, SEQ>, g, static_cast<unsigned>(g.one ? g.total : most), kThreads, smem, s, a, g,
+                    chain, maps);
+}
+
+template <int DT>
+cudaError_t fwd_dt(const GlrArgs& a, const GlrTiles& t, const GlrChain& c, const Device& dev, cudaStream_t s) {
+  return a.seq != nullptr ? launch<DT, true>(a, t, c, dev, s) : launch<DT, false>(a, t, c, dev, s);
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+  static EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+}  // namespace
+
+// A tensor copy takes rows of unit stride on 16-byte boundaries, in strides that the copy's map can hold.
+bool glr_map_eligible(const void* p, const int64_t* s, int64_t B, int64_t L, int64_t C, Dtype dt) {
+  const int64_t e = dt == kF32 ? 4 : 2, lim = int64_t(1) << 39;
+  return s[2] == 1 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && C < lim &&
+         (L == 1 || (s[1] * e % 16 == 0 && s[1] >= C && s[1] * e < lim)) &&
+         (B == 1 || (s[0] * e % 16 == 0 && s[0] > 0 && s[0] * e < lim)) && encoder() != nullptr;
+}
+
+bool glr_map3(CUtensorMap* m, const void* p, const int64_t* s, int64_t B, int64_t L, int64_t C, const int64_t* box2,
+              Dtype dt) {
+  const int64_t e = dt == kF32 ? 4 : 2, row = (C * e + 15) / 16 * 16;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(C), static_cast<cuuint64_t>(L), static_cast<cuuint64_t>(B)};
+  const int64_t s1 = L > 1 ? s[1] * e : row;
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1), static_cast<cuuint64_t>(B > 1 ? s[0] * e : s1 * L)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box2[0]), static_cast<cuuint32_t>(box2[1]), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encoder()(m, dt == kF32 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
+                   const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+GlrTiles glr_tiles(int64_t B, int64_t L, int64_t C) {
+  GlrTiles t = {};
+  t.nct = static_cast<int>((C + kGlrC - 1) / kGlrC);
+  t.ncols = static_cast<int>(B * t.nct);
+  t.levels = static_cast<int>((L + kGlrT - 1) / kGlrT);
+  t.total = static_cast<int>(static_cast<int64_t>(t.ncols) * t.levels);
+  return t;
+}
+
+bool glr_pair_out(const void* p, const int64_t* s, Dtype dt) {
+  const int64_t e = dt == kF32 ? 4 : 2;
+  return s[2] == 1 && s[0] % 2 == 0 && s[1] % 2 == 0 && reinterpret_cast<uintptr_t>(p) % (2 * e) == 0;
+}
+
+uint64_t glr_fwd_workspace(int64_t B, int64_t L, int64_t C) {
+  const GlrTiles t = glr_tiles(B, L, C);
+  return t.levels > 1 ? glr_chain_bytes(t.total) : 0;
+}
+
+cudaError_t launch_glr_fwd(const GlrArgs& a, void* ws, Dtype dt, const Device& dev, cudaStream_t stream) {
+  GlrTiles t = glr_tiles(a.B, a.L, a.C);
+  t.tma = glr_map_eligible(a.x, a.xs, a.B, a.L, a.C, dt) && glr_map_eligible(a.p, a.ps, a.B, a.L, a.C, dt) &&
+          glr_map_eligible(a.q, a.qs, a.B, a.L, a.C, dt);
+  t.pair = a.out != nullptr && glr_pair_out(a.out, a.os, dt);
+  GlrChain chain = {};
+  if (t.levels > 1) {
+    chain = glr_chain(ws, t.total);
+    const cudaError_t e = cudaMemsetAsync(ws, 0, glr_flag_bytes(t.total), stream);
+    if (e != cudaSuccess) return e;
+  }
+  switch (dt) {
+    case kF32: return fwd_dt<kF32>(a, t, chain, dev, stream);
+    case kF16: return fwd_dt<kF16>(a, t, chain, dev, stream);
+    case kBF16: return fwd_dt<kBF16>(a, t, chain, dev, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+unsigned read_and_clear_fault_glr() {
+  unsigned v = 0;
+  const unsigned zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_fault, sizeof(v)) != cudaSuccess) return ~0u;
+  if (v != 0 && cudaMemcpyToSymbol(g_fault, &zero, sizeof(zero)) != cudaSuccess) return ~0u;
+  return v;
+}
+
+}  // namespace ccv

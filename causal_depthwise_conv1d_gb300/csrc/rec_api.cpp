@@ -21,7 +21,7 @@ ccv_status check_glr_sizes(int64_t B, int64_t L, int64_t C, ccv_dtype dtype) {
   return CCV_OK;
 }
 
-// The backward pass: the states before every 64th token, partial sums of drate.
+// The backward pass: the states before every 64th token, partial sums of drate, the chain's workspace.
 struct GlrBwdWorkspace {
   uint64_t states, part, total;
 };
@@ -30,8 +30,8 @@ GlrBwdWorkspace glr_bwd_workspace(int64_t B, int64_t L, int64_t C) {
   GlrBwdWorkspace w = {0, 0, 0};
   if (B == 0 || L == 0 || C == 0) return w;
   w.states = up256(static_cast<uint64_t>(B) * static_cast<uint64_t>(glr_chunks(L)) * static_cast<uint64_t>(C) * 4);
-  w.part = up256(static_cast<uint64_t>(B) * static_cast<uint64_t>(C) * 4);
-  w.total = w.states + w.part;
+  w.part = w.states;
+  w.total = w.states + w.part + ccv::glr_fwd_workspace(B, L, C);
   return w;
 }
 
@@ -43,7 +43,7 @@ ccv_status ccv_glr_fwd_workspace_size(int64_t B, int64_t L, int64_t C, ccv_dtype
   ccv::api_begin();
   if (bytes == nullptr) CCV_FAIL(CCV_ERR_INVALID_ARG, "bytes is required");
   CCV_TRY(check_glr_sizes(B, L, C, dtype));
-  *bytes = 0;
+  *bytes = B > 0 && L > 0 && C > 0 ? ccv::glr_fwd_workspace(B, L, C) : 0;
   return CCV_OK;
 }
 
@@ -73,8 +73,7 @@ ccv_status ccv_glr_fwd(const void* x, const int64_t x_strides[3], const void* de
   CCV_TRY(t.add("out", out, out_strides, 3, blc, e, true, true));
   CCV_TRY(t.add("final_state_out", final_state_out, final_state_strides, 2, bc, 4, true, false));
   CCV_TRY(t.add("chunk_states_out", chunk_states_out, chunk_states_strides, 3, cs, 4, true, false));
-  (void)workspace;
-  (void)workspace_bytes;
+  CCV_TRY(add_workspace(t, workspace, workspace_bytes, L > 0 ? ccv::glr_fwd_workspace(B, L, C) : 0, 128));
   CCV_TRY(t.disjoint());
   if (L == 0 && final_state_out == nullptr) {
     ccv::api_kernel("none");
@@ -87,8 +86,12 @@ ccv_status ccv_glr_fwd(const void* x, const int64_t x_strides[3], const void* de
   copy(a.ss, seq_idx_strides, 2), copy(a.s0s, initial_state_strides, 2), copy(a.s1s, final_state_strides, 2);
   copy(a.css, chunk_states_strides, 3), copy(a.os, out_strides, 3);
   a.B = B, a.L = L, a.C = C;
-  return launched(ccv::launch_glr_step(a, static_cast<ccv::Dtype>(dtype), static_cast<cudaStream_t>(stream)),
-                  "glr_fwd");
+  const ccv::Dtype dt = static_cast<ccv::Dtype>(dtype);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (L == 0) return launched(ccv::launch_glr_step(a, dt, s), "glr_fwd");  // copies the state
+  ccv::Device dev;
+  CCV_TRY(static_cast<ccv_status>(ccv::api_device(&dev)));
+  return launched(ccv::launch_glr_fwd(a, workspace, dt, dev, s), "glr_fwd");
 }
 
 ccv_status ccv_glr_step(const void* x, const int64_t x_strides[3], const void* decay_gate,
@@ -184,13 +187,16 @@ ccv_status ccv_glr_bwd(const void* x, const int64_t x_strides[3], const void* de
   a.B = B, a.L = L, a.C = C;
   cudaError_t err = cudaSuccess;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* chain = ws + w.states + w.part;
+  ccv::Device dev;
+  CCV_TRY(static_cast<ccv_status>(ccv::api_device(&dev)));
   if (chunk_states != nullptr) {
     a.cs = const_cast<float*>(chunk_states);
     copy(a.css, chunk_states_strides, 3);
   } else if (B > 0 && L > 0) {
     a.cs = reinterpret_cast<float*>(ws);
     a.css[0] = glr_chunks(L) * C, a.css[1] = C, a.css[2] = 1;
-    err = ccv::launch_glr_step(a, dt, s);
+    err = ccv::launch_glr_fwd(a, chain, dt, dev, s);
   }
   ccv::GlrGrads g = {};
   g.dout = dout, g.ds1 = dfinal_state, g.dx = dx, g.dp = ddecay_gate, g.dq = dinput_gate, g.drate = drate;
@@ -198,7 +204,16 @@ ccv_status ccv_glr_bwd(const void* x, const int64_t x_strides[3], const void* de
   copy(g.dos, dout_strides, 3), copy(g.ds1s, dfinal_state_strides, 2), copy(g.dxs, dx_strides, 3);
   copy(g.dps, ddecay_gate_strides, 3), copy(g.dqs, dinput_gate_strides, 3), copy(g.ds0s, dinitial_state_strides, 2);
   g.part = reinterpret_cast<float*>(ws + w.states);
-  if (err == cudaSuccess) err = ccv::launch_glr_bwd(a, g, dt, s);
+  if (err == cudaSuccess && B > 0 && L > 0) err = ccv::launch_glr_bwd(a, g, chain, dt, dev, s);
+  if (err == cudaSuccess && L == 0 && dinitial_state != nullptr && B > 0) {
+    // no tokens: the state passes through
+    ccv::GlrArgs c = {};
+    c.rate = rate, c.rs = rate_stride, c.s0 = dfinal_state, c.s1 = dinitial_state, c.B = B, c.C = C, c.n_slots = B;
+    copy(c.s0s, dfinal_state_strides, 2), copy(c.s1s, dinitial_state_strides, 2);
+    err = ccv::launch_glr_step(c, dt, s);
+  }
+  if (err == cudaSuccess)
+    err = ccv::launch_glr_rate(g.part, L > 0 ? B * glr_chunks(L) : 0, C, drate, drate_stride, s);
   return launched(err, "glr_bwd");
 }
 

@@ -56,7 +56,16 @@ struct GlrGrads {
 };
 
 cudaError_t launch_glr_step(const GlrArgs& a, Dtype dt, cudaStream_t stream);
-cudaError_t launch_glr_bwd(const GlrArgs& a, const GlrGrads& g, Dtype dt, cudaStream_t stream);
+// Whole sequences; ws: glr_fwd_workspace() bytes (a function of the sizes alone).
+uint64_t glr_fwd_workspace(int64_t B, int64_t L, int64_t C);
+cudaError_t launch_glr_fwd(const GlrArgs& a, void* ws, Dtype dt, const Device& dev, cudaStream_t stream);
+// Backward pass with the same workspace; then drate from the partial sums, one
+// for each batch row and chunk.
+cudaError_t launch_glr_bwd(const GlrArgs& a, const GlrGrads& g, void* ws, Dtype dt, const Device& dev,
+                           cudaStream_t stream);
+cudaError_t launch_glr_rate(const float* part, int64_t P, int64_t C, float* drate, int64_t drs, cudaStream_t stream);
+unsigned read_and_clear_fault_glr();
+unsigned read_and_clear_fault_glr_bwd();
 
 // Validated arguments of group normalisation.  x, out: [N,S,C]; weight and
 // bias [C] in their own dtype, or null (one, zero).
