@@ -4,12 +4,14 @@
 //   h_t = a_t h_{t-1} + m_t i_t x_t
 //
 // Where the decay is close to one both a and 1 - a^2 come from E = expm1(l):
-// a = 1 + E, 1 - a^2 = -E (2 + E).  For -0.35 <= l E is its Taylor polynomial
-// of degree 7 (remainder 0.35^7 / 8! = 1.6e-8 relative), below that 2^(l log2 e)
-// - 1 with the hardware's exponential (2^-22 relative, while 1 - a >= 0.29).  So a
-// is within 2^-24 of the exact decay where a state lasts longer than three
+// a = 1 + E, 1 - a^2 = -E (2 + E).  For -0.85 <= l E is its Taylor polynomial
+// of degree 9 (remainder 0.85^9 / 10! = 6e-8 relative), below that 2^(l log2 e)
+// - 1 with the hardware's exponential (2^-22 relative, while 1 - a >= 0.57).  So a
+// is within 2^-24 of the exact decay where a state lasts longer than two
 // tokens, and m keeps its relative precision down to the smallest rates; from
 // a rounded to FP32, 1 - a^2 would have lost 10 of its 24 bits at a = 0.9995.
+// As -rate <= l, channels whose rate is at most 0.85 need no exponential here,
+// and a warp that has no others takes the shorter code (the same values).
 #pragma once
 
 #include "ccv_common.cuh"
@@ -17,7 +19,7 @@
 
 namespace ccv {
 
-constexpr float kGlrSeries = -0.35f;  // down to here the polynomial
+constexpr float kGlrSeries = -0.85f;  // down to here the polynomial
 
 struct GlrGate {
   float a, m2;   // decay, 1 - a^2
@@ -47,7 +49,9 @@ __device__ __forceinline__ void glr_sigmoid(float z, float& s, float& om) {
 }
 
 __device__ __forceinline__ void glr_decay(float l, float& a, float& m2) {
-  float E = fmaf(l, 1.f / 5040.f, 1.f / 720.f);
+  float E = fmaf(l, 1.f / 362880.f, 1.f / 40320.f);
+  E = fmaf(E, l, 1.f / 5040.f);
+  E = fmaf(E, l, 1.f / 720.f);
   E = fmaf(E, l, 1.f / 120.f);
   E = fmaf(E, l, 1.f / 24.f);
   E = fmaf(E, l, 1.f / 6.f);

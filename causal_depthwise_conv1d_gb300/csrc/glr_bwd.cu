@@ -12,6 +12,8 @@
 // smaller one of r and 1 - r (with a sign that tells which), 1 - i; when the state
 // before the token is known, G's factors u, b (1 - i), W l (1 - r), W r take
 // their places.  So every sigmoid and root is taken once.
+#include <type_traits>
+
 #include "glr_tile.cuh"
 
 namespace ccv {
@@ -46,7 +48,7 @@ struct __align__(16) Shared {
 // 1 - s of a sigmoid s = 1 / (1 + e), relatively precise.
 __device__ __forceinline__ float one_minus(float s, float e) { return e < 0x1p100f ? __fmul_rn(e, s) : 1.f; }
 
-template <int DT, bool SEQ>
+template <int DT, bool SEQ, bool TMA>
 __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
     glr_bwd_kernel(const GlrArgs a, const GlrGrads gr, const GlrTiles g, const GlrChain chain,
                    const __grid_constant__ Maps maps) {
@@ -66,7 +68,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
 
   int drawn = 0;
   auto draw = [&]() -> int {
-    if (chained) return static_cast<int>(atomicAdd(chain.ticket, 1u));
+    if (chained) return static_cast<int>(atomicAdd(chain.ticket, 1u) + 1u);
     const int t = static_cast<int>(blockIdx.x + drawn * gridDim.x);
     ++drawn;
     return t;
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
   // Tile t in the order of work: the last tokens first.
   auto fill = [&](int s, int t) {
     sh.tile[s] = t;
-    if (t >= g.total || !g.tma) {
+    if (!TMA || t >= g.total) {
       mbar_arrive(&sh.full[s]);
       return;
     }
@@ -106,11 +108,13 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
     const int tile = sh.tile[s];
     if (tile >= g.total) return;
     const int back = tile / g.ncols, col = tile - back * g.ncols, b = col / g.nct, level = g.levels - 1 - back;
-    const int c = (col - b * g.nct) * kGlrC + 2 * lane;
+    const int c0 = (col - b * g.nct) * kGlrC, c = c0 + 2 * lane;
     const int64_t t0 = static_cast<int64_t>(level) * kGlrT + warp * kRun;
     const bool in0 = c < a.C, in1 = c + 1 < a.C;
     const int64_t left = a.L - t0;
     const int n = left >= kRun ? kRun : left > 0 ? static_cast<int>(left) : 0;  // tokens of this warp
+    uint4 before = make_uint4(kSlotEmpty, 0u, 0u, 0u);
+    if (warp == 0 && back > 0) before = ld_slot(glr_slot(chain, tile - g.ncols, lane));  // it may be there already
     unsigned reset = 0;  // bit j: a sequence starts at the warp's token j
     if constexpr (SEQ) {
       bool start = false;
@@ -120,26 +124,26 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
       }
       reset = __ballot_sync(kFullMask, start);
     }
-    const uint64_t rate = pk(in0 ? -__ldg(a.rate + c * a.rs) : 0.f, in1 ? -__ldg(a.rate + (c + 1) * a.rs) : 0.f);
+    const float rate0 = in0 ? __ldg(a.rate + c * a.rs) : 0.f, rate1 = in1 ? __ldg(a.rate + (c + 1) * a.rs) : 0.f;
+    const uint64_t rate = pk(-rate0, -rate1);
     const float* csp = a.cs + b * a.css[0] + level * a.css[1] + c * a.css[2];
     float2 h2 = make_float2(in0 ? csp[0] : 0.f, in1 ? csp[a.css[2]] : 0.f);
     const uint8_t* st = stages + s * 4 * PLANE;
     auto load = [&](int plane, const void* p, const int64_t* str, int j) -> uint64_t {
-      if (g.tma) return glr_lds<DT>(st + plane * PLANE, warp * kRun + j, lane);
-      return glr_ldg<DT>(p, b * str[0] + (t0 + j) * str[1] + c * str[2], str[2], j < n && in0, j < n && in1);
+      if constexpr (TMA) return glr_lds<DT>(st + plane * PLANE, warp * kRun + j, lane);
+      else return glr_ldg<DT>(p, b * str[0] + (t0 + j) * str[1] + c * str[2], str[2], j < n && in0, j < n && in1);
     };
 
     // dec: a;  f0: k, then W l (1 - r);  f1: u;  f2: the smaller one of r, 1 - r, then W r;  f3: 1 - i, then b (1 - i)
     uint64_t dec[kRun], f0[kRun], f1[kRun], f2[kRun], f3[kRun];
-    {
-      uint64_t A = pk(1.f, 1.f), H = 0;
+    auto gates = [&](auto near) {
 #pragma unroll
       for (int j = 0; j < kRun; ++j) {
-        const uint64_t x = load(0, a.x, a.xs, j), p = load(1, a.p, a.ps, j), q = load(2, a.q, a.qs, j);
+        const uint64_t p = load(1, a.p, a.ps, j), q = load(2, a.q, a.qs, j);
         uint64_t r, ep, i, eq, m2;
         glr_sigmoid2(p, r, ep);
         glr_sigmoid2(q, i, eq);
-        glr_decay2(fmul2(rate, r), dec[j], m2);
+        glr_decay2<decltype(near)::value>(fmul2(rate, r), dec[j], m2);
         float v0, v1, e0, e1, m0, m1, s0, s1;
         upk(m2, m0, m1);
         // 1 / m, zero where m is: u and k are zero there too
@@ -153,15 +157,24 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
         f2[j] = pk(v0 < 0.5f ? v0 : -one_minus(v0, e0), v1 < 0.5f ? v1 : -one_minus(v1, e1));
         upk(i, v0, v1), upk(eq, e0, e1);
         f3[j] = pk(one_minus(v0, e0), one_minus(v1, e1));
-        uint64_t in = fmul2(f1[j], x);
-        if (j >= n) dec[j] = pk(1.f, 1.f), in = 0;
-        if (SEQ && (reset >> j & 1)) {
-          A = pk(kMinusZero, kMinusZero);
-          H = in;
-        } else {
-          A = fmul2(A, dec[j]);
-          H = ffma2(dec[j], H, in);
-        }
+      }
+    };
+    if (__all_sync(kFullMask, rate0 <= -kGlrSeries && rate1 <= -kGlrSeries))
+      gates(std::true_type{});
+    else
+      gates(std::false_type{});
+    if (n < kRun)  // nothing happens at tokens past the end
+#pragma unroll
+      for (int j = 0; j < kRun; ++j)
+        if (j >= n) dec[j] = pk(1.f, 1.f), f1[j] = 0;
+    {
+      uint64_t A = pk(1.f, 1.f), H = 0;
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) {
+        const uint64_t in = fmul2(f1[j], load(0, a.x, a.xs, j));
+        const bool cut = SEQ && (reset >> j & 1);
+        A = cut ? pk(kMinusZero, kMinusZero) : fmul2(A, dec[j]);
+        H = cut ? in : ffma2(dec[j], H, in);
       }
       float2 x, y;
       upk(A, x.x, x.y), upk(H, y.x, y.y);
@@ -171,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
 #pragma unroll
       for (int j = kRun - 1; j >= 0; --j) {
         const uint64_t o = load(3, gr.dout, gr.dos, j);
-        R = SEQ && (reset >> j & 1) ? 0 : fmul2(dec[j], j < n ? fadd2(o, R) : R);
+        R = SEQ && (reset >> j & 1) ? 0 : fmul2(dec[j], fadd2(o, R));
       }
       upk(R, y.x, y.y);
       sh.bwd[warp][lane] = make_float4(x.x, y.x, x.y, y.y);
@@ -193,12 +206,14 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
           const float* p = gr.ds1 + b * gr.ds1s[0] + c * gr.ds1s[1];
           d = make_float2(in0 ? p[0] : 0.f, in1 ? p[gr.ds1s[1]] : 0.f);
         }
+      } else if (__all_sync(kFullMask, before.x == kSlotState)) {
+        d = glr_slot_state(before);
       } else {
-        glr_publish_pair(chain, tile, lane, make_float2(m.x, m.z), make_float2(m.y, m.w));
+        if (level > 0) glr_put_pair(chain, tile, lane, m);
         ok = glr_look_back(chain, g, back, col, lane, d);
       }
       const float2 after = make_float2(glr_map(m.x, m.y, d.x), glr_map(m.z, m.w, d.y));
-      if (ok && level > 0) glr_publish_state(chain, tile, lane, after);
+      if (ok && level > 0) glr_put_state(chain, tile, lane, after);
       if (level == 0 && gr.ds0 != nullptr) {
         float* p = gr.ds0 + b * gr.ds0s[0] + c * gr.ds0s[1];
         if (in0) p[0] = after.x;
@@ -220,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
       if (SEQ && (reset >> j & 1)) h = 0;
-      const uint64_t in = j < n ? fmul2(f1[j], load(0, a.x, a.xs, j)) : 0;
+      const uint64_t in = fmul2(f1[j], load(0, a.x, a.xs, j));
       const uint64_t ah = fmul2(dec[j], h);
       const uint64_t W = ffma2(fmul2(f0[j], pk(-1.f, -1.f)), in, ah);
       h = fadd2(ah, in);
@@ -244,20 +259,31 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
       d2 = make_float2(glr_map(v.x, v.y, d2.x), glr_map(v.z, v.w, d2.y));
     }
     uint64_t d = pk(d2.x, d2.y), sum = 0;
-    const int64_t ox = b * gr.dxs[0] + t0 * gr.dxs[1] + c * gr.dxs[2];
-    const int64_t op = b * gr.dps[0] + t0 * gr.dps[1] + c * gr.dps[2];
-    const int64_t oq = b * gr.dqs[0] + t0 * gr.dqs[1] + c * gr.dqs[2];
+    const bool pair = g.pair && c0 + kGlrC <= a.C;
+    using E = typename Fmt<DT>::E;
+    const int64_t tl = t0 + kRun - 1;  // from the last token back
+    E* dx = static_cast<E*>(gr.dx) + (b * gr.dxs[0] + tl * gr.dxs[1] + c * gr.dxs[2]);
+    E* dp = static_cast<E*>(gr.dp) + (b * gr.dps[0] + tl * gr.dps[1] + c * gr.dps[2]);
+    E* dq = static_cast<E*>(gr.dq) + (b * gr.dqs[0] + tl * gr.dqs[1] + c * gr.dqs[2]);
+    auto run = [&](auto whole) {
+      constexpr bool W = decltype(whole)::value;
 #pragma unroll
-    for (int j = kRun - 1; j >= 0; --j) {
-      if (j < n) {
-        const uint64_t G = fadd2(d, load(3, gr.dout, gr.dos, j));
-        glr_stg<DT>(gr.dx, ox + j * gr.dxs[1], gr.dxs[2], g.pair, in0, in1, fmul2(G, f1[j]));
-        glr_stg<DT>(gr.dp, op + j * gr.dps[1], gr.dps[2], g.pair, in0, in1, fmul2(G, f0[j]));
-        glr_stg<DT>(gr.dq, oq + j * gr.dqs[1], gr.dqs[2], g.pair, in0, in1, fmul2(G, f3[j]));
-        sum = ffma2(G, f2[j], sum);
-        d = SEQ && (reset >> j & 1) ? 0 : fmul2(dec[j], G);
+      for (int j = kRun - 1; j >= 0; --j) {
+        if (W || j < n) {
+          const uint64_t G = fadd2(d, load(3, gr.dout, gr.dos, j));
+          glr_stg<DT>(dx, gr.dxs[2], W || pair, W || in0, W || in1, fmul2(G, f1[j]));
+          glr_stg<DT>(dp, gr.dps[2], W || pair, W || in0, W || in1, fmul2(G, f0[j]));
+          glr_stg<DT>(dq, gr.dqs[2], W || pair, W || in0, W || in1, fmul2(G, f3[j]));
+          sum = ffma2(G, f2[j], sum);
+          d = SEQ && (reset >> j & 1) ? 0 : fmul2(dec[j], G);
+        }
+        dx -= gr.dxs[1], dp -= gr.dps[1], dq -= gr.dqs[1];
       }
-    }
+    };
+    if (pair && n == kRun)
+      run(std::true_type{});
+    else
+      run(std::false_type{});
     upk(sum, d2.x, d2.y);
     sh.rate[warp][lane] = d2;
     __syncthreads();  // the stage has been read, the sums are there
@@ -300,33 +326,35 @@ __global__ void __launch_bounds__(1024) glr_rate_kernel(const float* part, int64
   }
 }
 
-template <int DT, bool SEQ>
+template <int DT, bool SEQ, bool TMA>
 cudaError_t launch(const GlrArgs& a, const GlrGrads& gr, const GlrTiles& t, const GlrChain& chain, const Device& dev,
                    cudaStream_t s) {
   Maps maps = {};
   constexpr Dtype dt = static_cast<Dtype>(DT);
-  if (t.tma) {
+  if constexpr (TMA) {
     const int64_t box[2] = {kGlrC, kGlrT};
     if (!glr_map3(&maps.x, a.x, a.xs, a.B, a.L, a.C, box, dt) || !glr_map3(&maps.p, a.p, a.ps, a.B, a.L, a.C, box, dt) ||
         !glr_map3(&maps.q, a.q, a.qs, a.B, a.L, a.C, box, dt) ||
         !glr_map3(&maps.o, gr.dout, gr.dos, a.B, a.L, a.C, box, dt))
       return cudaErrorInvalidValue;
   }
-  const int smem = kStages * 4 * plane_bytes<DT>();
+  const int smem = TMA ? kStages * 4 * plane_bytes<DT>() : 0;
   const cudaError_t e =
-      cudaFuncSetAttribute(glr_bwd_kernel<DT, SEQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaFuncSetAttribute(glr_bwd_kernel<DT, SEQ, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t most = static_cast<int64_t>(dev.sm_count) * (DT == kF32 ? 1 : 2);
   GlrTiles g = t;
   g.one = g.total <= most;
-  return glr_launch(glr_bwd_kernel<DT, SEQ>, g, static_cast<unsigned>(g.one ? g.total : most), kThreads,
-                    t.tma ? smem : 0, s, a, gr, g, chain, maps);
+  return glr_launch(glr_bwd_kernel<DT, SEQ, TMA>, g, static_cast<unsigned>(g.one ? g.total : most), kThreads,
+                    smem, s, a, gr, g, chain, maps);
 }
 
 template <int DT>
-cudaError_t bwd_dt(const GlrArgs& a, const GlrGrads& g, const GlrTiles& t, const GlrChain& c, const Device& dev,
-                   cudaStream_t s) {
-  return a.seq != nullptr ? launch<DT, true>(a, g, t, c, dev, s) : launch<DT, false>(a, g, t, c, dev, s);
+cudaError_t bwd_dt(const GlrArgs& a, const GlrGrads& g, const GlrTiles& t, const GlrChain& c, bool tma,
+                   const Device& dev, cudaStream_t s) {
+  if (a.seq != nullptr)
+    return tma ? launch<DT, true, true>(a, g, t, c, dev, s) : launch<DT, true, false>(a, g, t, c, dev, s);
+  return tma ? launch<DT, false, true>(a, g, t, c, dev, s) : launch<DT, false, false>(a, g, t, c, dev, s);
 }
 
 }  // namespace
@@ -334,20 +362,20 @@ cudaError_t bwd_dt(const GlrArgs& a, const GlrGrads& g, const GlrTiles& t, const
 cudaError_t launch_glr_bwd(const GlrArgs& a, const GlrGrads& gr, void* ws, Dtype dt, const Device& dev,
                            cudaStream_t stream) {
   GlrTiles t = glr_tiles(a.B, a.L, a.C);
-  t.tma = glr_map_eligible(a.x, a.xs, a.B, a.L, a.C, dt) && glr_map_eligible(a.p, a.ps, a.B, a.L, a.C, dt) &&
+  const bool tma = glr_map_eligible(a.x, a.xs, a.B, a.L, a.C, dt) && glr_map_eligible(a.p, a.ps, a.B, a.L, a.C, dt) &&
           glr_map_eligible(a.q, a.qs, a.B, a.L, a.C, dt) && glr_map_eligible(gr.dout, gr.dos, a.B, a.L, a.C, dt);
   t.pair = glr_pair_out(gr.dx, gr.dxs, dt) && glr_pair_out(gr.dp, gr.dps, dt) && glr_pair_out(gr.dq, gr.dqs, dt);
   GlrChain chain = {};
   cudaError_t e = cudaSuccess;
   if (t.levels > 1) {
-    chain = glr_chain(ws, t.total);
-    e = cudaMemsetAsync(ws, 0, glr_flag_bytes(t.total), stream);
+    chain = glr_chain(ws);
+    e = cudaMemsetAsync(ws, 0xff, glr_chain_bytes(t.total), stream);
     if (e != cudaSuccess) return e;
   }
   switch (dt) {
-    case kF32: e = bwd_dt<kF32>(a, gr, t, chain, dev, stream); break;
-    case kF16: e = bwd_dt<kF16>(a, gr, t, chain, dev, stream); break;
-    case kBF16: e = bwd_dt<kBF16>(a, gr, t, chain, dev, stream); break;
+    case kF32: e = bwd_dt<kF32>(a, gr, t, chain, tma, dev, stream); break;
+    case kF16: e = bwd_dt<kF16>(a, gr, t, chain, tma, dev, stream); break;
+    case kBF16: e = bwd_dt<kBF16>(a, gr, t, chain, tma, dev, stream); break;
   }
   return e;
 }

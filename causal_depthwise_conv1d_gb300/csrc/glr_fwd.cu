@@ -9,6 +9,8 @@
 // glr_tile.cuh), and every warp then runs its tokens from that state and writes
 // them.  So a state costs no second pass over the inputs, however few channels
 // there are to split the device by.
+#include <type_traits>
+
 #include "glr_tile.cuh"
 
 namespace ccv {
@@ -38,7 +40,7 @@ struct __align__(16) Shared {
   int late;
 };
 
-template <int DT, bool SEQ>
+template <int DT, bool SEQ, bool TMA>
 __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
     glr_fwd_kernel(const GlrArgs a, const GlrTiles g, const GlrChain chain, const __grid_constant__ Maps maps) {
   constexpr int PLANE = plane_bytes<DT>();
@@ -58,14 +60,14 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
   // Thread 0 draws tiles and starts their copies.
   int drawn = 0;
   auto draw = [&]() -> int {
-    if (chained) return static_cast<int>(atomicAdd(chain.ticket, 1u));
+    if (chained) return static_cast<int>(atomicAdd(chain.ticket, 1u) + 1u);
     const int t = static_cast<int>(blockIdx.x + drawn * gridDim.x);
     ++drawn;
     return t;
   };
   auto fill = [&](int s, int t) {
     sh.tile[s] = t;
-    if (t >= g.total || !g.tma) {
+    if (!TMA || t >= g.total) {
       mbar_arrive(&sh.full[s]);
       return;
     }
@@ -95,11 +97,13 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
     const int tile = sh.tile[s];
     if (tile >= g.total) return;
     const int level = tile / g.ncols, col = tile - level * g.ncols, b = col / g.nct;
-    const int c = (col - b * g.nct) * kGlrC + 2 * lane;
+    const int c0 = (col - b * g.nct) * kGlrC, c = c0 + 2 * lane;
     const int64_t t0 = static_cast<int64_t>(level) * kGlrT + warp * kRun;
     const bool in0 = c < a.C, in1 = c + 1 < a.C;
     const int64_t left = a.L - t0;
     const int n = left >= kRun ? kRun : left > 0 ? static_cast<int>(left) : 0;  // tokens of this warp
+    uint4 before = make_uint4(kSlotEmpty, 0u, 0u, 0u);
+    if (warp == 0 && level > 0) before = ld_slot(glr_slot(chain, tile - g.ncols, lane));  // it may be there already
     unsigned reset = 0;  // bit j: a sequence starts at the warp's token j
     if constexpr (SEQ) {
       bool start = false;
@@ -109,38 +113,56 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
       }
       reset = __ballot_sync(kFullMask, start);
     }
-    const uint64_t rate = pk(in0 ? -__ldg(a.rate + c * a.rs) : 0.f, in1 ? -__ldg(a.rate + (c + 1) * a.rs) : 0.f);
+    const float rate0 = in0 ? __ldg(a.rate + c * a.rs) : 0.f, rate1 = in1 ? __ldg(a.rate + (c + 1) * a.rs) : 0.f;
+    const uint64_t rate = pk(-rate0, -rate1);
 
-    uint64_t dec[kRun], in[kRun], A = pk(1.f, 1.f), H = 0;
+    uint64_t dec[kRun], in[kRun];
     const uint8_t* st = stages + s * 3 * PLANE;
+    auto gates = [&](auto near) {
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-      uint64_t x, p, q;
-      if (g.tma) {
-        x = glr_lds<DT>(st, warp * kRun + j, lane);
-        p = glr_lds<DT>(st + PLANE, warp * kRun + j, lane);
-        q = glr_lds<DT>(st + 2 * PLANE, warp * kRun + j, lane);
-      } else {
-        const bool on = j < n;
-        const int64_t t = t0 + j;
-        x = glr_ldg<DT>(a.x, b * a.xs[0] + t * a.xs[1] + c * a.xs[2], a.xs[2], on && in0, on && in1);
-        p = glr_ldg<DT>(a.p, b * a.ps[0] + t * a.ps[1] + c * a.ps[2], a.ps[2], on && in0, on && in1);
-        q = glr_ldg<DT>(a.q, b * a.qs[0] + t * a.qs[1] + c * a.qs[2], a.qs[2], on && in0, on && in1);
+      for (int j = 0; j < kRun; ++j) {
+        uint64_t x, p, q;
+        if constexpr (TMA) {
+          x = glr_lds<DT>(st, warp * kRun + j, lane);
+          p = glr_lds<DT>(st + PLANE, warp * kRun + j, lane);
+          q = glr_lds<DT>(st + 2 * PLANE, warp * kRun + j, lane);
+        } else {
+          const bool on = j < n;
+          const int64_t t = t0 + j;
+          x = glr_ldg<DT>(a.x, b * a.xs[0] + t * a.xs[1] + c * a.xs[2], a.xs[2], on && in0, on && in1);
+          p = glr_ldg<DT>(a.p, b * a.ps[0] + t * a.ps[1] + c * a.ps[2], a.ps[2], on && in0, on && in1);
+          q = glr_ldg<DT>(a.q, b * a.qs[0] + t * a.qs[1] + c * a.qs[2], a.qs[2], on && in0, on && in1);
+        }
+        uint64_t r, i, e, m2;
+        glr_sigmoid2(p, r, e);
+        glr_sigmoid2(q, i, e);
+        glr_decay2<decltype(near)::value>(fmul2(rate, r), dec[j], m2);
+        float u, v;
+        upk(m2, u, v);
+        in[j] = fmul2(pk(sqrt_approx(u), sqrt_approx(v)), fmul2(i, x));
       }
-      uint64_t r, i, e, m2;
-      glr_sigmoid2(p, r, e);
-      glr_sigmoid2(q, i, e);
-      glr_decay2(fmul2(rate, r), dec[j], m2);
-      float u, v;
-      upk(m2, u, v);
-      in[j] = fmul2(pk(sqrt_approx(u), sqrt_approx(v)), fmul2(i, x));
-      if (j >= n) dec[j] = pk(1.f, 1.f), in[j] = 0;
-      if (SEQ && (reset >> j & 1)) {
-        A = pk(kMinusZero, kMinusZero);
-        H = in[j];
-      } else {
+    };
+    if (__all_sync(kFullMask, rate0 <= -kGlrSeries && rate1 <= -kGlrSeries))
+      gates(std::true_type{});
+    else
+      gates(std::false_type{});
+    if (n < kRun)
+#pragma unroll
+      for (int j = 0; j < kRun; ++j)
+        if (j >= n) dec[j] = pk(1.f, 1.f), in[j] = 0;
+    uint64_t A = dec[0], H = in[0];
+    if (!SEQ || reset == 0) {
+#pragma unroll
+      for (int j = 1; j < kRun; ++j) {
         A = fmul2(A, dec[j]);
         H = ffma2(dec[j], H, in[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) {
+        const bool cut = reset >> j & 1;
+        A = cut ? pk(kMinusZero, kMinusZero) : j == 0 ? A : fmul2(A, dec[j]);
+        H = cut || j == 0 ? in[j] : ffma2(dec[j], H, in[j]);
       }
     }
     {
@@ -169,12 +191,14 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
           const float* p = a.s0 + b * a.s0s[0] + c * a.s0s[1];
           h = make_float2(in0 ? p[0] : 0.f, in1 ? p[a.s0s[1]] : 0.f);
         }
+      } else if (__all_sync(kFullMask, before.x == kSlotState)) {
+        h = glr_slot_state(before);
       } else {
-        glr_publish_pair(chain, tile, lane, make_float2(m.x, m.z), make_float2(m.y, m.w));
+        if (level + 1 < g.levels) glr_put_pair(chain, tile, lane, m);
         ok = glr_look_back(chain, g, level, col, lane, h);
       }
       if (ok && level + 1 < g.levels)
-        glr_publish_state(chain, tile, lane, make_float2(glr_map(m.x, m.y, h.x), glr_map(m.z, m.w, h.y)));
+        glr_put_state(chain, tile, lane, make_float2(glr_map(m.x, m.y, h.x), glr_map(m.z, m.w, h.y)));
       if (!ok && lane == 0) {
         atomicOr(&g_fault, kFaultConsumerWait);
         sh.late = 1;
@@ -200,12 +224,24 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
       h2 = make_float2(glr_map(v.x, v.y, h2.x), glr_map(v.z, v.w, h2.y));
     }
     uint64_t h = pk(h2.x, h2.y);
-    const int64_t off = b * a.os[0] + t0 * a.os[1] + c * a.os[2];
+    const bool pair = g.pair && c0 + kGlrC <= a.C;
+    typename Fmt<DT>::E* out = static_cast<typename Fmt<DT>::E*>(a.out) + (b * a.os[0] + t0 * a.os[1] + c * a.os[2]);
+    auto run = [&](auto whole) {
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-      h = SEQ && (reset >> j & 1) ? in[j] : ffma2(dec[j], h, in[j]);
-      if (j < n && a.out != nullptr) glr_stg<DT>(a.out, off + j * a.os[1], a.os[2], g.pair, in0, in1, h);
-    }
+      for (int j = 0; j < kRun; ++j) {
+        h = SEQ && (reset >> j & 1) ? in[j] : ffma2(dec[j], h, in[j]);
+        if (decltype(whole)::value) {
+          glr_stg<DT>(out, a.os[2], true, true, true, h);
+        } else if (j < n && a.out != nullptr) {
+          glr_stg<DT>(out, a.os[2], pair, in0, in1, h);
+        }
+        out += a.os[1];
+      }
+    };
+    if (pair && n == kRun)
+      run(std::true_type{});
+    else
+      run(std::false_type{});
     if (a.s1 != nullptr && n > 0 && t0 + n == a.L) {
       float* p = a.s1 + b * a.s1s[0] + c * a.s1s[1];
       upk(h, h2.x, h2.y);
@@ -215,30 +251,31 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
   }
 }
 
-template <int DT, bool SEQ>
+template <int DT, bool SEQ, bool TMA>
 cudaError_t launch(const GlrArgs& a, const GlrTiles& t, const GlrChain& chain, const Device& dev, cudaStream_t s) {
   Maps maps = {};
-  if (t.tma) {
+  if constexpr (TMA) {
     const int64_t box[2] = {kGlrC, kGlrT};
     if (!glr_map3(&maps.x, a.x, a.xs, a.B, a.L, a.C, box, static_cast<Dtype>(DT)) ||
         !glr_map3(&maps.p, a.p, a.ps, a.B, a.L, a.C, box, static_cast<Dtype>(DT)) ||
         !glr_map3(&maps.q, a.q, a.qs, a.B, a.L, a.C, box, static_cast<Dtype>(DT)))
       return cudaErrorInvalidValue;
   }
-  const int smem = t.tma ? kStages * 3 * plane_bytes<DT>() : 0;
-  cudaError_t e = cudaFuncSetAttribute(glr_fwd_kernel<DT, SEQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kStages * 3 * plane_bytes<DT>());
+  const int smem = TMA ? kStages * 3 * plane_bytes<DT>() : 0;
+  cudaError_t e = cudaFuncSetAttribute(glr_fwd_kernel<DT, SEQ, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t most = static_cast<int64_t>(dev.sm_count) * (DT == kF32 ? 2 : 4);
   GlrTiles g = t;
   g.one = g.total <= most;
-  return glr_launch(glr_fwd_kernel<DT, SEQ>, g, static_cast<unsigned>(g.one ? g.total : most), kThreads, smem, s, a, g,
+  return glr_launch(glr_fwd_kernel<DT, SEQ, TMA>, g, static_cast<unsigned>(g.one ? g.total : most), kThreads, smem, s, a, g,
                     chain, maps);
 }
 
 template <int DT>
-cudaError_t fwd_dt(const GlrArgs& a, const GlrTiles& t, const GlrChain& c, const Device& dev, cudaStream_t s) {
-  return a.seq != nullptr ? launch<DT, true>(a, t, c, dev, s) : launch<DT, false>(a, t, c, dev, s);
+cudaError_t fwd_dt(const GlrArgs& a, const GlrTiles& t, const GlrChain& c, bool tma, const Device& dev,
+                   cudaStream_t s) {
+  if (a.seq != nullptr) return tma ? launch<DT, true, true>(a, t, c, dev, s) : launch<DT, true, false>(a, t, c, dev, s);
+  return tma ? launch<DT, false, true>(a, t, c, dev, s) : launch<DT, false, false>(a, t, c, dev, s);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -302,19 +339,19 @@ uint64_t glr_fwd_workspace(int64_t B, int64_t L, int64_t C) {
 
 cudaError_t launch_glr_fwd(const GlrArgs& a, void* ws, Dtype dt, const Device& dev, cudaStream_t stream) {
   GlrTiles t = glr_tiles(a.B, a.L, a.C);
-  t.tma = glr_map_eligible(a.x, a.xs, a.B, a.L, a.C, dt) && glr_map_eligible(a.p, a.ps, a.B, a.L, a.C, dt) &&
-          glr_map_eligible(a.q, a.qs, a.B, a.L, a.C, dt);
+  const bool tma = glr_map_eligible(a.x, a.xs, a.B, a.L, a.C, dt) && glr_map_eligible(a.p, a.ps, a.B, a.L, a.C, dt) &&
+                   glr_map_eligible(a.q, a.qs, a.B, a.L, a.C, dt);
   t.pair = a.out != nullptr && glr_pair_out(a.out, a.os, dt);
   GlrChain chain = {};
   if (t.levels > 1) {
-    chain = glr_chain(ws, t.total);
-    const cudaError_t e = cudaMemsetAsync(ws, 0, glr_flag_bytes(t.total), stream);
+    chain = glr_chain(ws);
+    const cudaError_t e = cudaMemsetAsync(ws, 0xff, glr_chain_bytes(t.total), stream);
     if (e != cudaSuccess) return e;
   }
   switch (dt) {
-    case kF32: return fwd_dt<kF32>(a, t, chain, dev, stream);
-    case kF16: return fwd_dt<kF16>(a, t, chain, dev, stream);
-    case kBF16: return fwd_dt<kBF16>(a, t, chain, dev, stream);
+    case kF32: return fwd_dt<kF32>(a, t, chain, tma, dev, stream);
+    case kF16: return fwd_dt<kF16>(a, t, chain, tma, dev, stream);
+    case kBF16: return fwd_dt<kBF16>(a, t, chain, tma, dev, stream);
   }
   return cudaErrorInvalidValue;
 }
