@@ -243,7 +243,7 @@ ccv_status ccv_device_fault(unsigned* fault_bits) {
   const unsigned words[] = {ccv::read_and_clear_fault_chlast_tma(), ccv::read_and_clear_fault_gdr(),
                             ccv::read_and_clear_fault_gdr_bwd(), ccv::read_and_clear_fault_gdr_grad(),
                             ccv::read_and_clear_fault_ln(), ccv::read_and_clear_fault_glr(),
-                            ccv::read_and_clear_fault_glr_bwd()};
+                            ccv::read_and_clear_fault_glr_bwd(), ccv::read_and_clear_fault_gn()};
   unsigned v = 0;
   for (const unsigned w : words) v |= w;
   if (v == ~0u) return fail(CCV_ERR_CUDA, "cannot read the fault word");

@@ -333,9 +333,9 @@ cudaError_t launch(const GlrArgs& a, const GlrGrads& gr, const GlrTiles& t, cons
   constexpr Dtype dt = static_cast<Dtype>(DT);
   if constexpr (TMA) {
     const int64_t box[2] = {kGlrC, kGlrT};
-    if (!glr_map3(&maps.x, a.x, a.xs, a.B, a.L, a.C, box, dt) || !glr_map3(&maps.p, a.p, a.ps, a.B, a.L, a.C, box, dt) ||
-        !glr_map3(&maps.q, a.q, a.qs, a.B, a.L, a.C, box, dt) ||
-        !glr_map3(&maps.o, gr.dout, gr.dos, a.B, a.L, a.C, box, dt))
+    if (!tensor_map3(&maps.x, a.x, a.xs, a.B, a.L, a.C, box, dt) || !tensor_map3(&maps.p, a.p, a.ps, a.B, a.L, a.C, box, dt) ||
+        !tensor_map3(&maps.q, a.q, a.qs, a.B, a.L, a.C, box, dt) ||
+        !tensor_map3(&maps.o, gr.dout, gr.dos, a.B, a.L, a.C, box, dt))
       return cudaErrorInvalidValue;
   }
   const int smem = TMA ? kStages * 4 * plane_bytes<DT>() : 0;
@@ -362,8 +362,8 @@ cudaError_t bwd_dt(const GlrArgs& a, const GlrGrads& g, const GlrTiles& t, const
 cudaError_t launch_glr_bwd(const GlrArgs& a, const GlrGrads& gr, void* ws, Dtype dt, const Device& dev,
                            cudaStream_t stream) {
   GlrTiles t = glr_tiles(a.B, a.L, a.C);
-  const bool tma = glr_map_eligible(a.x, a.xs, a.B, a.L, a.C, dt) && glr_map_eligible(a.p, a.ps, a.B, a.L, a.C, dt) &&
-          glr_map_eligible(a.q, a.qs, a.B, a.L, a.C, dt) && glr_map_eligible(gr.dout, gr.dos, a.B, a.L, a.C, dt);
+  const bool tma = tensor_map_eligible(a.x, a.xs, a.B, a.L, a.C, dt) && tensor_map_eligible(a.p, a.ps, a.B, a.L, a.C, dt) &&
+          tensor_map_eligible(a.q, a.qs, a.B, a.L, a.C, dt) && tensor_map_eligible(gr.dout, gr.dos, a.B, a.L, a.C, dt);
   t.pair = glr_pair_out(gr.dx, gr.dxs, dt) && glr_pair_out(gr.dp, gr.dps, dt) && glr_pair_out(gr.dq, gr.dqs, dt);
   GlrChain chain = {};
   cudaError_t e = cudaSuccess;

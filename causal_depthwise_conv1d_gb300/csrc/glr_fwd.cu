@@ -256,9 +256,9 @@ cudaError_t launch(const GlrArgs& a, const GlrTiles& t, const GlrChain& chain, c
   Maps maps = {};
   if constexpr (TMA) {
     const int64_t box[2] = {kGlrC, kGlrT};
-    if (!glr_map3(&maps.x, a.x, a.xs, a.B, a.L, a.C, box, static_cast<Dtype>(DT)) ||
-        !glr_map3(&maps.p, a.p, a.ps, a.B, a.L, a.C, box, static_cast<Dtype>(DT)) ||
-        !glr_map3(&maps.q, a.q, a.qs, a.B, a.L, a.C, box, static_cast<Dtype>(DT)))
+    if (!tensor_map3(&maps.x, a.x, a.xs, a.B, a.L, a.C, box, static_cast<Dtype>(DT)) ||
+        !tensor_map3(&maps.p, a.p, a.ps, a.B, a.L, a.C, box, static_cast<Dtype>(DT)) ||
+        !tensor_map3(&maps.q, a.q, a.qs, a.B, a.L, a.C, box, static_cast<Dtype>(DT)))
       return cudaErrorInvalidValue;
   }
   const int smem = TMA ? kStages * 3 * plane_bytes<DT>() : 0;
@@ -278,45 +278,7 @@ cudaError_t fwd_dt(const GlrArgs& a, const GlrTiles& t, const GlrChain& c, bool 
   return tma ? launch<DT, false, true>(a, t, c, dev, s) : launch<DT, false, false>(a, t, c, dev, s);
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encoder() {
-  static EncodeTiled fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiled>(p);
-  }();
-  return fn;
-}
-
 }  // namespace
-
-// A tensor copy takes rows of unit stride on 16-byte boundaries, in strides that the copy's map can hold.
-bool glr_map_eligible(const void* p, const int64_t* s, int64_t B, int64_t L, int64_t C, Dtype dt) {
-  const int64_t e = dt == kF32 ? 4 : 2, lim = int64_t(1) << 39;
-  return s[2] == 1 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && C < lim &&
-         (L == 1 || (s[1] * e % 16 == 0 && s[1] >= C && s[1] * e < lim)) &&
-         (B == 1 || (s[0] * e % 16 == 0 && s[0] > 0 && s[0] * e < lim)) && encoder() != nullptr;
-}
-
-bool glr_map3(CUtensorMap* m, const void* p, const int64_t* s, int64_t B, int64_t L, int64_t C, const int64_t* box2,
-              Dtype dt) {
-  const int64_t e = dt == kF32 ? 4 : 2, row = (C * e + 15) / 16 * 16;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(C), static_cast<cuuint64_t>(L), static_cast<cuuint64_t>(B)};
-  const int64_t s1 = L > 1 ? s[1] * e : row;
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1), static_cast<cuuint64_t>(B > 1 ? s[0] * e : s1 * L)};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box2[0]), static_cast<cuuint32_t>(box2[1]), 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return encoder()(m, dt == kF32 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
-                   const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 GlrTiles glr_tiles(int64_t B, int64_t L, int64_t C) {
   GlrTiles t = {};
@@ -339,8 +301,8 @@ uint64_t glr_fwd_workspace(int64_t B, int64_t L, int64_t C) {
 
 cudaError_t launch_glr_fwd(const GlrArgs& a, void* ws, Dtype dt, const Device& dev, cudaStream_t stream) {
   GlrTiles t = glr_tiles(a.B, a.L, a.C);
-  const bool tma = glr_map_eligible(a.x, a.xs, a.B, a.L, a.C, dt) && glr_map_eligible(a.p, a.ps, a.B, a.L, a.C, dt) &&
-                   glr_map_eligible(a.q, a.qs, a.B, a.L, a.C, dt);
+  const bool tma = tensor_map_eligible(a.x, a.xs, a.B, a.L, a.C, dt) && tensor_map_eligible(a.p, a.ps, a.B, a.L, a.C, dt) &&
+                   tensor_map_eligible(a.q, a.qs, a.B, a.L, a.C, dt);
   t.pair = a.out != nullptr && glr_pair_out(a.out, a.os, dt);
   GlrChain chain = {};
   if (t.levels > 1) {

@@ -22,6 +22,7 @@
 
 #include "ccv_tma.cuh"
 #include "glr.cuh"
+#include "tensor_map.h"
 
 namespace ccv {
 
@@ -141,11 +142,8 @@ __device__ __forceinline__ bool glr_look_back(const GlrChain& c, const GlrTiles&
   }
 }
 
-// Host side (glr_fwd.cu): sizes, maps of the tensor copies, outputs in pairs.
+// Host side (glr_fwd.cu): sizes, outputs in pairs.
 GlrTiles glr_tiles(int64_t B, int64_t L, int64_t C);
-bool glr_map_eligible(const void* p, const int64_t* s, int64_t B, int64_t L, int64_t C, Dtype dt);
-bool glr_map3(CUtensorMap* m, const void* p, const int64_t* s, int64_t B, int64_t L, int64_t C, const int64_t* box2,
-              Dtype dt);
 bool glr_pair_out(const void* p, const int64_t* s, Dtype dt);
 
 // A chained kernel follows the memset of its flags: a plain launch.

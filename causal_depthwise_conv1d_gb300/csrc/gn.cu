@@ -11,6 +11,8 @@
 #include "ccv_common.cuh"
 #include "rec_internal.h"
 
+#include <initializer_list>
+
 namespace ccv {
 namespace {
 
@@ -264,19 +266,11 @@ cudaError_t bwd_dt(const GnArgs& a, cudaStream_t s) {
   const GnPlan p = gn_plan(a.N, a.S, a.C, a.G);
   const unsigned grid = static_cast<unsigned>(a.N * a.G * p.slabs);
   const unsigned sums = static_cast<unsigned>(p.slots * a.G * p.slabs);
-  cudaError_t e = cudaSuccess;
-  if (a.N > 0 && a.S > 0) {
-    if (p.slabs == 1) {
-      e = launch_pdl(gn_any_bwd_sums<DT, true>, sums, kThreads, 0, s, a, p);
-    } else {
-      e = launch_pdl(gn_any_stats<DT>, grid, kThreads, 0, s, a, p);
-      if (e == cudaSuccess) e = launch_pdl(gn_any_bwd_sums<DT, false>, sums, kThreads, 0, s, a, p);
-      if (e == cudaSuccess) e = launch_pdl(gn_any_bwd_dx<DT>, grid, kThreads, 0, s, a, p);
-    }
-  }
-  if (e != cudaSuccess || (a.dw == nullptr && a.db == nullptr)) return e;
-  return launch_param_sums(a.part, a.N > 0 && a.S > 0 ? p.slots * p.slabs : 0, a.C, a.dw, a.dws, a.db, a.dbs, a.wdt,
-                           s);
+  if (p.slabs == 1) return launch_pdl(gn_any_bwd_sums<DT, true>, sums, kThreads, 0, s, a, p);
+  cudaError_t e = launch_pdl(gn_any_stats<DT>, grid, kThreads, 0, s, a, p);
+  if (e == cudaSuccess) e = launch_pdl(gn_any_bwd_sums<DT, false>, sums, kThreads, 0, s, a, p);
+  if (e == cudaSuccess) e = launch_pdl(gn_any_bwd_dx<DT>, grid, kThreads, 0, s, a, p);
+  return e;
 }
 
 }  // namespace
@@ -301,7 +295,22 @@ GnPlan gn_plan(int64_t N, int64_t S, int64_t C, int64_t G) {
   return p;
 }
 
+int64_t gn_parts(int64_t N, int64_t S, int64_t C, int64_t G) {
+  const GnPlan p = gn_plan(N, S, C, G);
+  int64_t most = p.slots * p.slabs;
+  for (const int64_t esize : {2, 4}) {
+    const int64_t v = 16 / esize;
+    if (C / G % v != 0) continue;
+    const int64_t n = S == 1 && C / G / v <= 128 ? gn_rows_slots(N, C, G, esize, true)
+                                                 : gn_cluster_parts(N, S, C, G, esize);
+    if (n > most) most = n;
+  }
+  return most;
+}
+
 cudaError_t launch_gn_fwd(const GnArgs& a, Dtype dt, cudaStream_t stream) {
+  if (gn_rows_eligible(a, dt, false)) return launch_gn_rows(a, dt, false, stream);
+  if (gn_cluster_eligible(a, dt, false)) return launch_gn_cluster(a, dt, false, stream);
   switch (dt) {
     case kF32: return fwd_dt<kF32>(a, stream);
     case kF16: return fwd_dt<kF16>(a, stream);
@@ -311,12 +320,27 @@ cudaError_t launch_gn_fwd(const GnArgs& a, Dtype dt, cudaStream_t stream) {
 }
 
 cudaError_t launch_gn_bwd(const GnArgs& a, Dtype dt, cudaStream_t stream) {
-  switch (dt) {
-    case kF32: return bwd_dt<kF32>(a, stream);
-    case kF16: return bwd_dt<kF16>(a, stream);
-    case kBF16: return bwd_dt<kBF16>(a, stream);
+  const bool some = a.N > 0 && a.S > 0;
+  const int64_t esize = dt == kF32 ? 4 : 2;
+  int64_t parts = 0;
+  cudaError_t e = cudaSuccess;
+  if (some && gn_rows_eligible(a, dt, true)) {
+    e = launch_gn_rows(a, dt, true, stream);
+    parts = gn_rows_slots(a.N, a.C, a.G, esize, true);
+  } else if (some && gn_cluster_eligible(a, dt, true)) {
+    e = launch_gn_cluster(a, dt, true, stream);
+    parts = gn_cluster_parts(a.N, a.S, a.C, a.G, esize);
+  } else if (some) {
+    switch (dt) {
+      case kF32: e = bwd_dt<kF32>(a, stream); break;
+      case kF16: e = bwd_dt<kF16>(a, stream); break;
+      case kBF16: e = bwd_dt<kBF16>(a, stream); break;
+    }
+    const GnPlan p = gn_plan(a.N, a.S, a.C, a.G);
+    parts = p.slots * p.slabs;
   }
-  return cudaErrorInvalidValue;
+  if (e != cudaSuccess || (a.dw == nullptr && a.db == nullptr)) return e;
+  return launch_param_sums(a.part, parts, a.C, a.dw, a.dws, a.db, a.dbs, a.wdt, stream);
 }
 
 }  // namespace ccv

@@ -252,7 +252,7 @@ GnWorkspace gn_workspace(int64_t N, int64_t S, int64_t C, int64_t G, bool backwa
     w.stats = up256(static_cast<uint64_t>(N * G * p.slabs) * 8);
     if (backward) w.sums = w.stats;
   }
-  if (params) w.part = up256(static_cast<uint64_t>(p.slots * p.slabs) * 8 * static_cast<uint64_t>(C));
+  if (params) w.part = up256(static_cast<uint64_t>(ccv::gn_parts(N, S, C, G)) * 8 * static_cast<uint64_t>(C));
   w.total = w.stats + w.sums + w.part;
   return w;
 }

@@ -106,6 +106,19 @@ GnPlan gn_plan(int64_t N, int64_t S, int64_t C, int64_t G);
 cudaError_t launch_gn_fwd(const GnArgs& a, Dtype dt, cudaStream_t stream);
 cudaError_t launch_gn_bwd(const GnArgs& a, Dtype dt, cudaStream_t stream);
 
+// Rows on their own (S = 1; gn_rows.cu) and groups that fit into a cluster's
+// shared memory (gn_cluster.cu): aligned layouts.  The partial sums of dw and db
+// that the backward pass makes there are functions of the sizes alone.
+bool gn_rows_eligible(const GnArgs& a, Dtype dt, bool bwd);
+int64_t gn_rows_slots(int64_t N, int64_t C, int64_t G, int64_t esize, bool bwd);
+cudaError_t launch_gn_rows(const GnArgs& a, Dtype dt, bool bwd, cudaStream_t stream);
+bool gn_cluster_eligible(const GnArgs& a, Dtype dt, bool bwd);
+int64_t gn_cluster_parts(int64_t N, int64_t S, int64_t C, int64_t G, int64_t esize);
+cudaError_t launch_gn_cluster(const GnArgs& a, Dtype dt, bool bwd, cudaStream_t stream);
+// The most partial sums any of the kernels makes for these sizes.
+int64_t gn_parts(int64_t N, int64_t S, int64_t C, int64_t G);
+unsigned read_and_clear_fault_gn();
+
 // Sums of P partial sums [P][2][C] in a fixed order into dw and db (ln.cu).
 cudaError_t launch_param_sums(const float* part, int64_t P, int64_t C, void* dw, int64_t dws, void* db, int64_t dbs,
                               int wdt, cudaStream_t stream);
