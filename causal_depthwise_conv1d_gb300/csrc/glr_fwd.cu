@@ -4,11 +4,11 @@
 // A block of four warps takes tiles of 64 tokens x 64 channels; a warp has 16
 // tokens, a lane two channels.  Tensor copies bring the next tile's x and gates
 // into shared memory while the present one is worked on.  A warp computes its
-// tokens' decays and inputs into registers and their (A, H), the first warp
-// joins these, publishes them and gets the state before the tile (see
-// glr_tile.cuh), and every warp then runs its tokens from that state and writes
-// them.  So a state costs no second pass over the inputs, however few channels
-// there are to split the device by.
+// tokens' decays and inputs into registers and their (A, H); after the tile's
+// one barrier every warp gets the state before the tile (see glr_tile.cuh), the
+// first one publishes the state after it, and each runs its tokens, writes them
+// over x in the stage and stores them as a box.  So a state costs no second
+// pass over the inputs, however few channels there are to split the device by.
 #include <type_traits>
 
 #include "glr_tile.cuh"
@@ -24,7 +24,7 @@ constexpr int kRun = kGlrT / kWarps;  // tokens of a warp
 constexpr int kStages = 2;
 
 struct Maps {
-  CUtensorMap x, p, q;
+  CUtensorMap x, p, q, out;
 };
 
 template <int DT>
@@ -33,11 +33,9 @@ constexpr int plane_bytes() {
 }
 
 struct __align__(16) Shared {
-  uint64_t full[kStages];
-  int tile[kStages];
   float4 pair[2][kWarps][32];
-  float2 carry[2][32];
-  int late;
+  uint64_t full[kStages];
+  GlrPlace place[kStages];
 };
 
 template <int DT, bool SEQ, bool TMA>
@@ -52,7 +50,6 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1);
     fence_barrier_init();
-    sh.late = 0;
   }
   pdl_enter();
   __syncthreads();
@@ -66,44 +63,42 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
     return t;
   };
   auto fill = [&](int s, int t) {
-    sh.tile[s] = t;
+    GlrPlace p;
+    p.tile = t;
+    p.level = t / g.ncols, p.col = t - p.level * g.ncols, p.b = p.col / g.nct, p.c0 = (p.col - p.b * g.nct) * kGlrC;
+    sh.place[s] = p;
     if (!TMA || t >= g.total) {
       mbar_arrive(&sh.full[s]);
       return;
     }
-    const int level = t / g.ncols, col = t - level * g.ncols, b = col / g.nct, c0 = (col - b * g.nct) * kGlrC;
     uint8_t* st = stages + s * 3 * PLANE;
     mbar_arrive_expect_tx(&sh.full[s], 3 * PLANE);
-    tma_load_3d(st, &maps.x, c0, level * kGlrT, b, &sh.full[s]);
-    tma_load_3d(st + PLANE, &maps.p, c0, level * kGlrT, b, &sh.full[s]);
-    tma_load_3d(st + 2 * PLANE, &maps.q, c0, level * kGlrT, b, &sh.full[s]);
+    tma_load_3d(st, &maps.x, p.c0, p.level * kGlrT, p.b, &sh.full[s]);
+    tma_load_3d(st + PLANE, &maps.p, p.c0, p.level * kGlrT, p.b, &sh.full[s]);
+    tma_load_3d(st + 2 * PLANE, &maps.q, p.c0, p.level * kGlrT, p.b, &sh.full[s]);
   };
   int next = g.total;
   if (tid == 0) {
     fill(0, draw());
-    if (!g.one) fill(1, draw()), next = draw();
+    if (!g.one) next = draw();
   }
 
   for (int it = 0;; ++it) {
-    const int s = it & 1, odd = it & 1;
-    if (it == 1 && g.one) return;
+    const int s = it & 1;
+    if (it == 1 && g.one) break;
     if (!mbar_wait(&sh.full[s], (it >> 1) & 1)) {
-      if (tid == 0) {
-        atomicOr(&g_fault, kFaultConsumerWait);
-        if (!g.one) mbar_wait(&sh.full[s ^ 1], ((it + 1) >> 1) & 1);  // the other copies in flight
-      }
-      return;
+      if (lane == 0) atomicOr(&g_fault, kFaultConsumerWait);
+      break;  // no other copy of the block is in flight
     }
-    const int tile = sh.tile[s];
-    if (tile >= g.total) return;
-    const int level = tile / g.ncols, col = tile - level * g.ncols, b = col / g.nct;
-    const int c0 = (col - b * g.nct) * kGlrC, c = c0 + 2 * lane;
+    const GlrPlace at = sh.place[s];
+    if (at.tile >= g.total) break;
+    const int level = at.level, b = at.b, c = at.c0 + 2 * lane;
     const int64_t t0 = static_cast<int64_t>(level) * kGlrT + warp * kRun;
     const bool in0 = c < a.C, in1 = c + 1 < a.C;
     const int64_t left = a.L - t0;
     const int n = left >= kRun ? kRun : left > 0 ? static_cast<int>(left) : 0;  // tokens of this warp
     uint4 before = make_uint4(kSlotEmpty, 0u, 0u, 0u);
-    if (warp == 0 && level > 0) before = ld_slot(glr_slot(chain, tile - g.ncols, lane));  // it may be there already
+    if (level > 0) before = ld_slot(glr_slot(chain, at.tile - g.ncols, lane));  // it may be there already
     unsigned reset = 0;  // bit j: a sequence starts at the warp's token j
     if constexpr (SEQ) {
       bool start = false;
@@ -117,15 +112,15 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
     const uint64_t rate = pk(-rate0, -rate1);
 
     uint64_t dec[kRun], in[kRun];
-    const uint8_t* st = stages + s * 3 * PLANE;
+    uint8_t* st = stages + s * 3 * PLANE + warp * (PLANE / kWarps);  // this warp's rows
     auto gates = [&](auto near) {
 #pragma unroll
       for (int j = 0; j < kRun; ++j) {
         uint64_t x, p, q;
         if constexpr (TMA) {
-          x = glr_lds<DT>(st, warp * kRun + j, lane);
-          p = glr_lds<DT>(st + PLANE, warp * kRun + j, lane);
-          q = glr_lds<DT>(st + 2 * PLANE, warp * kRun + j, lane);
+          x = glr_lds<DT>(st, j, lane);
+          p = glr_lds<DT>(st + PLANE, j, lane);
+          q = glr_lds<DT>(st + 2 * PLANE, j, lane);
         } else {
           const bool on = j < n;
           const int64_t t = t0 + j;
@@ -165,83 +160,90 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
         H = cut || j == 0 ? in[j] : ffma2(dec[j], H, in[j]);
       }
     }
+    float4 (*pairs)[32] = sh.pair[s];
     {
       float2 x, y;
       upk(A, x.x, x.y), upk(H, y.x, y.y);
-      sh.pair[odd][warp][lane] = make_float4(x.x, y.x, x.y, y.y);
+      pairs[warp][lane] = make_float4(x.x, y.x, x.y, y.y);
     }
-    __syncthreads();  // pairs are there, the stage has been read
+    if (TMA && lane == 0) bulk_wait_read();  // the box of the tile before has left its stage
+    __syncthreads();  // pairs are there, the other stage is free
     if (tid == 0 && !g.one) {
       fence_proxy_async_smem();
-      fill(s, next);
-      next = draw();
+      fill(s ^ 1, next);
+      if (next < g.total) next = draw();
+    }
+
+    float2 h2 = make_float2(0.f, 0.f);
+    if (level == 0) {
+      if (a.s0 != nullptr) {
+        const float* p = a.s0 + b * a.s0s[0] + c * a.s0s[1];
+        h2 = make_float2(in0 ? p[0] : 0.f, in1 ? p[a.s0s[1]] : 0.f);
+      }
+    } else if (__all_sync(kFullMask, before.x == kSlotState)) {
+      h2 = glr_slot_state(before);
+    } else {
+      if (warp == 0 && level + 1 < g.levels) {
+        float4 m = pairs[0][lane];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+          const float4 v = pairs[w][lane];
+          glr_join(v.x, v.y, m.x, m.y);
+          glr_join(v.z, v.w, m.z, m.w);
+        }
+        glr_put_pair(chain, at.tile, lane, m);
+      }
+      if (!glr_look_back(chain, g, level, at.col, lane, h2)) {
+        if (lane == 0) atomicOr(&g_fault, kFaultConsumerWait);
+        h2 = make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));  // no state: nothing that passes for one
+      }
     }
     if (warp == 0) {
-      float2 h = make_float2(0.f, 0.f);
-      float4 m = sh.pair[odd][0][lane];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) {
-        const float4 v = sh.pair[odd][w][lane];
-        glr_join(v.x, v.y, m.x, m.y);
-        glr_join(v.z, v.w, m.z, m.w);
-      }
-      bool ok = true;
-      if (level == 0) {
-        if (a.s0 != nullptr) {
-          const float* p = a.s0 + b * a.s0s[0] + c * a.s0s[1];
-          h = make_float2(in0 ? p[0] : 0.f, in1 ? p[a.s0s[1]] : 0.f);
-        }
-      } else if (__all_sync(kFullMask, before.x == kSlotState)) {
-        h = glr_slot_state(before);
-      } else {
-        if (level + 1 < g.levels) glr_put_pair(chain, tile, lane, m);
-        ok = glr_look_back(chain, g, level, col, lane, h);
-      }
-      if (ok && level + 1 < g.levels)
-        glr_put_state(chain, tile, lane, make_float2(glr_map(m.x, m.y, h.x), glr_map(m.z, m.w, h.y)));
-      if (!ok && lane == 0) {
-        atomicOr(&g_fault, kFaultConsumerWait);
-        sh.late = 1;
-      }
-      sh.carry[odd][lane] = h;
       if (a.cs != nullptr) {
         float* p = a.cs + b * a.css[0] + level * a.css[1] + c * a.css[2];
-        if (in0) p[0] = h.x;
-        if (in1) p[a.css[2]] = h.y;
+        if (in0) p[0] = h2.x;
+        if (in1) p[a.css[2]] = h2.y;
+      }
+      if (level + 1 < g.levels) {
+        float4 m = pairs[0][lane];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+          const float4 v = pairs[w][lane];
+          glr_join(v.x, v.y, m.x, m.y);
+          glr_join(v.z, v.w, m.z, m.w);
+        }
+        glr_put_state(chain, at.tile, lane, make_float2(glr_map(m.x, m.y, h2.x), glr_map(m.z, m.w, h2.y)));
       }
     }
-    __syncthreads();
-    if (sh.late) {
-      if (tid == 0 && !g.one) {  // the copies in flight
-        mbar_wait(&sh.full[s ^ 1], ((it + 1) >> 1) & 1);
-        mbar_wait(&sh.full[s], ((it + 2) >> 1) & 1);
-      }
-      return;
-    }
-    float2 h2 = sh.carry[odd][lane];
     for (int w = 0; w < warp; ++w) {
-      const float4 v = sh.pair[odd][w][lane];
+      const float4 v = pairs[w][lane];
       h2 = make_float2(glr_map(v.x, v.y, h2.x), glr_map(v.z, v.w, h2.y));
     }
     uint64_t h = pk(h2.x, h2.y);
-    const bool pair = g.pair && c0 + kGlrC <= a.C;
-    typename Fmt<DT>::E* out = static_cast<typename Fmt<DT>::E*>(a.out) + (b * a.os[0] + t0 * a.os[1] + c * a.os[2]);
-    auto run = [&](auto whole) {
+    if (TMA) {
 #pragma unroll
       for (int j = 0; j < kRun; ++j) {
         h = SEQ && (reset >> j & 1) ? in[j] : ffma2(dec[j], h, in[j]);
-        if (decltype(whole)::value) {
-          glr_stg<DT>(out, a.os[2], true, true, true, h);
-        } else if (j < n && a.out != nullptr) {
-          glr_stg<DT>(out, a.os[2], pair, in0, in1, h);
+        glr_sts<DT>(st, j, lane, h);
+      }
+      if (a.out != nullptr && n > 0) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&maps.out, st, at.c0, static_cast<int>(t0), b);
+          bulk_commit();
         }
+      }
+    } else {
+      const bool pair = g.pair && in1;
+      typename Fmt<DT>::E* out = static_cast<typename Fmt<DT>::E*>(a.out) + (b * a.os[0] + t0 * a.os[1] + c * a.os[2]);
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) {
+        h = SEQ && (reset >> j & 1) ? in[j] : ffma2(dec[j], h, in[j]);
+        if (j < n && a.out != nullptr) glr_stg<DT>(out, a.os[2], pair, in0, in1, h);
         out += a.os[1];
       }
-    };
-    if (pair && n == kRun)
-      run(std::true_type{});
-    else
-      run(std::false_type{});
+    }
     if (a.s1 != nullptr && n > 0 && t0 + n == a.L) {
       float* p = a.s1 + b * a.s1s[0] + c * a.s1s[1];
       upk(h, h2.x, h2.y);
@@ -249,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
       if (in1) p[a.s1s[1]] = h2.y;
     }
   }
+  if (TMA && lane == 0) bulk_wait_read();
 }
 
 template <int DT, bool SEQ, bool TMA>
@@ -259,6 +262,9 @@ cudaError_t launch(const GlrArgs& a, const GlrTiles& t, const GlrChain& chain, c
     if (!tensor_map3(&maps.x, a.x, a.xs, a.B, a.L, a.C, box, static_cast<Dtype>(DT)) ||
         !tensor_map3(&maps.p, a.p, a.ps, a.B, a.L, a.C, box, static_cast<Dtype>(DT)) ||
         !tensor_map3(&maps.q, a.q, a.qs, a.B, a.L, a.C, box, static_cast<Dtype>(DT)))
+      return cudaErrorInvalidValue;
+    const int64_t run[2] = {kGlrC, kRun};
+    if (a.out != nullptr && !tensor_map3(&maps.out, a.out, a.os, a.B, a.L, a.C, run, static_cast<Dtype>(DT)))
       return cudaErrorInvalidValue;
   }
   const int smem = TMA ? kStages * 3 * plane_bytes<DT>() : 0;
@@ -302,7 +308,8 @@ uint64_t glr_fwd_workspace(int64_t B, int64_t L, int64_t C) {
 cudaError_t launch_glr_fwd(const GlrArgs& a, void* ws, Dtype dt, const Device& dev, cudaStream_t stream) {
   GlrTiles t = glr_tiles(a.B, a.L, a.C);
   const bool tma = tensor_map_eligible(a.x, a.xs, a.B, a.L, a.C, dt) && tensor_map_eligible(a.p, a.ps, a.B, a.L, a.C, dt) &&
-                   tensor_map_eligible(a.q, a.qs, a.B, a.L, a.C, dt);
+                   tensor_map_eligible(a.q, a.qs, a.B, a.L, a.C, dt) &&
+                   (a.out == nullptr || tensor_map_eligible(a.out, a.os, a.B, a.L, a.C, dt));
   t.pair = a.out != nullptr && glr_pair_out(a.out, a.os, dt);
   GlrChain chain = {};
   if (t.levels > 1) {

@@ -22,6 +22,7 @@
 
 #include "ccv_tma.cuh"
 #include "glr.cuh"
+#include "rec_pairs.cuh"
 #include "tensor_map.h"
 
 namespace ccv {
@@ -42,6 +43,11 @@ inline GlrChain glr_chain(void* ws) {
   uint8_t* p = static_cast<uint8_t*>(ws);
   return {reinterpret_cast<unsigned*>(p), reinterpret_cast<uint4*>(p + 256)};
 }
+
+// A tile's place, found once by the thread that starts its copies.
+struct GlrPlace {
+  int tile, level, col, b, c0;
+};
 
 // What the tile kernels get beside their arguments: sizes in 32 bits.
 struct GlrTiles {
@@ -98,6 +104,7 @@ __device__ __forceinline__ float2 glr_slot_state(const uint4& v) {
   return make_float2(__uint_as_float(v.y), __uint_as_float(v.w));
 }
 __device__ __forceinline__ float2 glr_slot_map(const uint4& v, float2 h) {
+  if (v.x == kSlotState) return glr_slot_state(v);
   return make_float2(glr_map(__uint_as_float(v.x), __uint_as_float(v.y), h.x),
                      glr_map(__uint_as_float(v.z), __uint_as_float(v.w), h.y));
 }
@@ -105,40 +112,47 @@ __device__ __forceinline__ float2 glr_slot_map(const uint4& v, float2 h) {
 // The state before the tile of this level (> 0) and column, two channels a
 // lane: from the nearest state among the kWindow tiles before it, through the
 // pairs that follow it.  One warp.  False when the wait ran out.
+// Older slots are never behind: where one holds a state, those before it do.
 constexpr int kWindow = 8;
 __device__ __forceinline__ bool glr_look_back(const GlrChain& c, const GlrTiles& g, int level, int col, int lane,
                                               float2& h) {
   const long long start = clock64();
-  bool found = false;
+  const uint4* slot = glr_slot(c, (level - 1) * g.ncols + col, lane);
+  const int64_t step = static_cast<int64_t>(g.ncols) * 32;
   for (;;) {
-    if (!found) {
-      uint4 v[kWindow];
-      int n = -1;
-      bool whole = true;  // every slot so far holds a pair
+    uint4 v[kWindow];
+    int n = -1, k = 0;  // n: where the whole warp found states; k: slots that are not empty
+    v[0] = ld_slot(slot);
+    if (__all_sync(kFullMask, v[0].x == kSlotState)) {
+      h = glr_slot_state(v[0]);
+      return true;
+    }
+    if (__all_sync(kFullMask, v[0].x != kSlotEmpty)) {
+      k = 1;
 #pragma unroll
-      for (int k = 0; k < kWindow; k += 4) {
+      for (int i = 1; i < kWindow; i += 4) {
+        if (k != i || n >= 0) break;
 #pragma unroll
-        for (int i = k; i < k + 4; ++i)
-          v[i] = whole && n < 0 && level - 1 - i >= 0
-                     ? ld_slot(glr_slot(c, (level - 1 - i) * g.ncols + col, lane))
-                     : make_uint4(kSlotEmpty, 0u, 0u, 0u);
+        for (int j = i; j < i + 4 && j < kWindow; ++j)
+          v[j] = j < level ? ld_slot(slot - j * step) : make_uint4(kSlotEmpty, 0u, 0u, 0u);
 #pragma unroll
-        for (int i = k; i < k + 4; ++i) {
-          if (whole && n < 0 && v[i].x == kSlotState) n = i;
-          whole = whole && v[i].x != kSlotEmpty;
-        }
+        for (int j = i; j < i + 4 && j < kWindow; ++j)
+          if (k == j && n < 0) {
+            if (__all_sync(kFullMask, v[j].x == kSlotState)) n = j;
+            if (__all_sync(kFullMask, v[j].x != kSlotEmpty)) k = j + 1;
+          }
       }
-      if (n >= 0) {
-        found = true;
+      if (n > 0) {
 #pragma unroll
         for (int i = kWindow - 1; i >= 0; --i) {
           if (i == n) h = glr_slot_state(v[i]);
           if (i < n) h = glr_slot_map(v[i], h);
         }
+        return true;
       }
     }
-    if (__all_sync(kFullMask, found)) return true;
     if (clock64() - start > kWaitBudgetCycles) return false;
+    __nanosleep(40);
   }
 }
 
@@ -157,6 +171,16 @@ cudaError_t glr_launch(void (*kernel)(P...), const GlrTiles& g, unsigned grid, u
 
 // ---------------------------------------------------------------- pairs of channels
 
+// Tiled store of a box from shared memory, in the thread's current group of
+// bulk copies; and the wait until the group's boxes have been read.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+               "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
 // Two adjacent channels of a staged row (rows of 64 elements).
 template <int DT>
 __device__ __forceinline__ uint64_t glr_lds(const uint8_t* base, int row, int lane) {
@@ -166,6 +190,17 @@ __device__ __forceinline__ uint64_t glr_lds(const uint8_t* base, int row, int la
   } else {
     const uint32_t w = *reinterpret_cast<const uint32_t*>(base + row * (kGlrC * 2) + lane * 4);
     return pk(Fmt<DT>::word_elem(w, 0), Fmt<DT>::word_elem(w, 1));
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void glr_sts(uint8_t* base, int row, int lane, uint64_t v) {
+  float a, b;
+  upk(v, a, b);
+  if constexpr (DT == kF32) {
+    *reinterpret_cast<float2*>(base + row * (kGlrC * 4) + lane * 8) = make_float2(a, b);
+  } else {
+    *reinterpret_cast<uint32_t*>(base + row * (kGlrC * 2) + lane * 4) = Fmt<DT>::pack2(a, b);
   }
 }
 
@@ -195,9 +230,9 @@ __device__ __forceinline__ void glr_stg(typename Fmt<DT>::E* e, int64_t cs, bool
 // Sigmoids of a pair: s, and e = 2^(-z log2 e) as it was taken.
 __device__ __forceinline__ void glr_sigmoid2(uint64_t z, uint64_t& s, uint64_t& e) {
   float a, b;
-  upk(fmul2(z, pk(-kLog2e, -kLog2e)), a, b);
+  upk(fmul2(z, twice(-kLog2e)), a, b);
   e = pk(ex2_approx(a), ex2_approx(b));
-  upk(fadd2(e, pk(1.f, 1.f)), a, b);
+  upk(fadd2(e, twice(1.f)), a, b);
   s = pk(rcp_approx(a), rcp_approx(b));
 }
 
@@ -205,33 +240,24 @@ __device__ __forceinline__ void glr_sigmoid2(uint64_t z, uint64_t& s, uint64_t& 
 // kGlrSeries).
 template <bool NEAR>
 __device__ __forceinline__ void glr_decay2(uint64_t l, uint64_t& a, uint64_t& m2) {
-  auto two = [](float x) { return pk(x, x); };
-  uint64_t E = ffma2(l, two(1.f / 362880.f), two(1.f / 40320.f));
-  E = ffma2(E, l, two(1.f / 5040.f));
-  E = ffma2(E, l, two(1.f / 720.f));
-  E = ffma2(E, l, two(1.f / 120.f));
-  E = ffma2(E, l, two(1.f / 24.f));
-  E = ffma2(E, l, two(1.f / 6.f));
-  E = ffma2(E, l, two(0.5f));
-  E = ffma2(E, l, two(1.f));
+  constexpr float c[] = {1.f / 362880.f, 1.f / 40320.f, 1.f / 5040.f, 1.f / 720.f, 1.f / 120.f,
+                         1.f / 24.f,     1.f / 6.f,     0.5f,         1.f};
+  uint64_t E = ffma2(l, twice(c[0]), twice(c[1]));
+#pragma unroll
+  for (int i = 2; i < 9; ++i) E = ffma2(E, l, twice(c[i]));
   E = fmul2(E, l);
-  a = fadd2(E, two(1.f));
-  if constexpr (NEAR) {
-    m2 = fmul2(E, ffma2(E, two(-1.f), two(-2.f)));
-    return;
+  a = fadd2(E, twice(1.f));
+  if constexpr (!NEAR) {
+    float f0, f1, n0, n1, l0, l1, e0, e1;
+    upk(l, l0, l1);
+    f0 = ex2_approx(__fmul_rn(l0, kLog2e)), f1 = ex2_approx(__fmul_rn(l1, kLog2e));
+    upk(a, n0, n1);
+    upk(E, e0, e1);
+    const bool c0 = l0 >= kGlrSeries, c1 = l1 >= kGlrSeries;
+    a = pk(c0 ? n0 : f0, c1 ? n1 : f1);
+    E = pk(c0 ? e0 : __fadd_rn(f0, -1.f), c1 ? e1 : __fadd_rn(f1, -1.f));
   }
-  float t0, t1, n0, n1, l0, l1, e0, e1;
-  upk(fmul2(l, two(kLog2e)), t0, t1);
-  const float f0 = ex2_approx(t0), f1 = ex2_approx(t1);
-  float g0, g1;
-  upk(fadd2(pk(f0, f1), two(-1.f)), g0, g1);
-  upk(a, n0, n1);
-  upk(l, l0, l1);
-  upk(E, e0, e1);
-  const bool c0 = l0 >= kGlrSeries, c1 = l1 >= kGlrSeries;
-  a = pk(c0 ? n0 : f0, c1 ? n1 : f1);
-  E = pk(c0 ? e0 : g0, c1 ? e1 : g1);
-  m2 = fmul2(E, ffma2(E, two(-1.f), two(-2.f)));
+  m2 = fmul2(E, ffma2(E, twice(-1.f), twice(-2.f)));
 }
 
 }  // namespace ccv
