@@ -27,7 +27,7 @@ constexpr int kRun = kGlrT / kWarps;  // tokens of a warp
 constexpr int kStages = 2;
 
 struct Maps {
-  CUtensorMap x, p, q, o;
+  CUtensorMap x, p, q, o, dx, dp, dq;
 };
 
 template <int DT>
@@ -36,14 +36,24 @@ constexpr int plane_bytes() {
 }
 
 struct __align__(16) Shared {
-  uint64_t full[kStages];
-  int tile[kStages];
   float4 fwd[kWarps][32];  // (A, H) of the states
   float4 bwd[kWarps][32];  // (A, R) of the carries
   float2 rate[kWarps][32];
-  float2 carry[32];
-  int late;
+  uint64_t full[kStages];
+  GlrPlace place[kStages];
 };
+
+// The runs' maps of the carry, last run first, as one.
+__device__ __forceinline__ float4 joined(const float4 (*runs)[32], int lane) {
+  float4 m = runs[kWarps - 1][lane];
+#pragma unroll
+  for (int w = kWarps - 2; w >= 0; --w) {
+    const float4 v = runs[w][lane];
+    glr_join(v.x, v.y, m.x, m.y);
+    glr_join(v.z, v.w, m.z, m.w);
+  }
+  return m;
+}
 
 // 1 - s of a sigmoid s = 1 / (1 + e), relatively precise.
 __device__ __forceinline__ float one_minus(float s, float e) { return e < 0x1p100f ? __fmul_rn(e, s) : 1.f; }
@@ -61,7 +71,6 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1);
     fence_barrier_init();
-    sh.late = 0;
   }
   pdl_enter();
   __syncthreads();
@@ -75,46 +84,45 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
   };
   // Tile t in the order of work: the last tokens first.
   auto fill = [&](int s, int t) {
-    sh.tile[s] = t;
+    GlrPlace p;
+    const int back = t / g.ncols;
+    p.tile = t;
+    p.level = g.levels - 1 - back, p.col = t - back * g.ncols, p.b = p.col / g.nct, p.c0 = (p.col - p.b * g.nct) * kGlrC;
+    sh.place[s] = p;
     if (!TMA || t >= g.total) {
       mbar_arrive(&sh.full[s]);
       return;
     }
-    const int back = t / g.ncols, col = t - back * g.ncols, b = col / g.nct, c0 = (col - b * g.nct) * kGlrC;
-    const int t0 = (g.levels - 1 - back) * kGlrT;
+    const int t0 = p.level * kGlrT;
     uint8_t* st = stages + s * 4 * PLANE;
     mbar_arrive_expect_tx(&sh.full[s], 4 * PLANE);
-    tma_load_3d(st, &maps.x, c0, t0, b, &sh.full[s]);
-    tma_load_3d(st + PLANE, &maps.p, c0, t0, b, &sh.full[s]);
-    tma_load_3d(st + 2 * PLANE, &maps.q, c0, t0, b, &sh.full[s]);
-    tma_load_3d(st + 3 * PLANE, &maps.o, c0, t0, b, &sh.full[s]);
+    tma_load_3d(st, &maps.x, p.c0, t0, p.b, &sh.full[s]);
+    tma_load_3d(st + PLANE, &maps.p, p.c0, t0, p.b, &sh.full[s]);
+    tma_load_3d(st + 2 * PLANE, &maps.q, p.c0, t0, p.b, &sh.full[s]);
+    tma_load_3d(st + 3 * PLANE, &maps.o, p.c0, t0, p.b, &sh.full[s]);
   };
   int next = g.total;
   if (tid == 0) {
     fill(0, draw());
-    if (!g.one) fill(1, draw()), next = draw();
+    if (!g.one) next = draw();
   }
 
   for (int it = 0;; ++it) {
     const int s = it & 1;
-    if (it == 1 && g.one) return;
+    if (it == 1 && g.one) break;
     if (!mbar_wait(&sh.full[s], (it >> 1) & 1)) {
-      if (tid == 0) {
-        atomicOr(&g_fault, kFaultConsumerWait);
-        if (!g.one) mbar_wait(&sh.full[s ^ 1], ((it + 1) >> 1) & 1);  // the other copies in flight
-      }
-      return;
+      if (lane == 0) atomicOr(&g_fault, kFaultConsumerWait);
+      break;  // no other copy of the block is in flight
     }
-    const int tile = sh.tile[s];
-    if (tile >= g.total) return;
-    const int back = tile / g.ncols, col = tile - back * g.ncols, b = col / g.nct, level = g.levels - 1 - back;
-    const int c0 = (col - b * g.nct) * kGlrC, c = c0 + 2 * lane;
+    const GlrPlace at = sh.place[s];
+    if (at.tile >= g.total) break;
+    const int level = at.level, back = g.levels - 1 - level, b = at.b, c = at.c0 + 2 * lane;
     const int64_t t0 = static_cast<int64_t>(level) * kGlrT + warp * kRun;
     const bool in0 = c < a.C, in1 = c + 1 < a.C;
     const int64_t left = a.L - t0;
     const int n = left >= kRun ? kRun : left > 0 ? static_cast<int>(left) : 0;  // tokens of this warp
     uint4 before = make_uint4(kSlotEmpty, 0u, 0u, 0u);
-    if (warp == 0 && back > 0) before = ld_slot(glr_slot(chain, tile - g.ncols, lane));  // it may be there already
+    if (back > 0) before = ld_slot(glr_slot(chain, at.tile - g.ncols, lane));  // it may be there already
     unsigned reset = 0;  // bit j: a sequence starts at the warp's token j
     if constexpr (SEQ) {
       bool start = false;
@@ -128,9 +136,9 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
     const uint64_t rate = pk(-rate0, -rate1);
     const float* csp = a.cs + b * a.css[0] + level * a.css[1] + c * a.css[2];
     float2 h2 = make_float2(in0 ? csp[0] : 0.f, in1 ? csp[a.css[2]] : 0.f);
-    const uint8_t* st = stages + s * 4 * PLANE;
+    uint8_t* st = stages + s * 4 * PLANE + warp * (PLANE / kWarps);  // this warp's rows
     auto load = [&](int plane, const void* p, const int64_t* str, int j) -> uint64_t {
-      if constexpr (TMA) return glr_lds<DT>(st + plane * PLANE, warp * kRun + j, lane);
+      if constexpr (TMA) return glr_lds<DT>(st + plane * PLANE, j, lane);
       else return glr_ldg<DT>(p, b * str[0] + (t0 + j) * str[1] + c * str[2], str[2], j < n && in0, j < n && in1);
     };
 
@@ -189,41 +197,39 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
       upk(R, y.x, y.y);
       sh.bwd[warp][lane] = make_float4(x.x, y.x, x.y, y.y);
     }
-    __syncthreads();  // the runs' maps are there
+    if (TMA && lane == 0) bulk_wait_read();  // the boxes of the tile before have left its stage
+    __syncthreads();  // the runs' maps are there, the other stage is free
+    if (tid == 0 && !g.one) {
+      fence_proxy_async_smem();
+      fill(s ^ 1, next);
+      if (next < g.total) next = draw();
+    }
 
-    if (warp == 0) {
-      float4 m = sh.bwd[kWarps - 1][lane];
-#pragma unroll
-      for (int w = kWarps - 2; w >= 0; --w) {
-        const float4 v = sh.bwd[w][lane];
-        glr_join(v.x, v.y, m.x, m.y);
-        glr_join(v.z, v.w, m.z, m.w);
+    float2 d2 = make_float2(0.f, 0.f);  // the carry into the tile's last token
+    if (back == 0) {
+      if (gr.ds1 != nullptr) {
+        const float* p = gr.ds1 + b * gr.ds1s[0] + c * gr.ds1s[1];
+        d2 = make_float2(in0 ? p[0] : 0.f, in1 ? p[gr.ds1s[1]] : 0.f);
       }
-      float2 d = make_float2(0.f, 0.f);
-      bool ok = true;
-      if (back == 0) {
-        if (gr.ds1 != nullptr) {
-          const float* p = gr.ds1 + b * gr.ds1s[0] + c * gr.ds1s[1];
-          d = make_float2(in0 ? p[0] : 0.f, in1 ? p[gr.ds1s[1]] : 0.f);
-        }
-      } else if (__all_sync(kFullMask, before.x == kSlotState)) {
-        d = glr_slot_state(before);
+    } else if (__all_sync(kFullMask, before.x == kSlotState)) {
+      d2 = glr_slot_state(before);
+    } else {
+      if (warp == 0 && level > 0) glr_put_pair(chain, at.tile, lane, joined(sh.bwd, lane));
+      if (!glr_look_back(chain, g, back, at.col, lane, d2)) {
+        if (lane == 0) atomicOr(&g_fault, kFaultConsumerWait);
+        d2 = make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));  // nothing that passes for one
+      }
+    }
+    if (warp == 0 && (level > 0 || gr.ds0 != nullptr)) {
+      const float4 m = joined(sh.bwd, lane);
+      const float2 after = make_float2(glr_map(m.x, m.y, d2.x), glr_map(m.z, m.w, d2.y));
+      if (level > 0) {
+        glr_put_state(chain, at.tile, lane, after);
       } else {
-        if (level > 0) glr_put_pair(chain, tile, lane, m);
-        ok = glr_look_back(chain, g, back, col, lane, d);
-      }
-      const float2 after = make_float2(glr_map(m.x, m.y, d.x), glr_map(m.z, m.w, d.y));
-      if (ok && level > 0) glr_put_state(chain, tile, lane, after);
-      if (level == 0 && gr.ds0 != nullptr) {
         float* p = gr.ds0 + b * gr.ds0s[0] + c * gr.ds0s[1];
         if (in0) p[0] = after.x;
         if (in1) p[gr.ds0s[1]] = after.y;
       }
-      if (!ok && lane == 0) {
-        atomicOr(&g_fault, kFaultConsumerWait);
-        sh.late = 1;
-      }
-      sh.carry[lane] = d;
     }
 
     // the states, and with them G's factors
@@ -248,50 +254,54 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
       f0[j] = fmul2(f2[j], fmul2(rate, om));
       f3[j] = fmul2(in, f3[j]);
     }
-    __syncthreads();  // the carry is there
-    if (sh.late) {
-      if (tid == 0 && !g.one) mbar_wait(&sh.full[s ^ 1], ((it + 1) >> 1) & 1);  // the copies in flight
-      return;
-    }
-    float2 d2 = sh.carry[lane];
     for (int w = kWarps - 1; w > warp; --w) {
       const float4 v = sh.bwd[w][lane];
       d2 = make_float2(glr_map(v.x, v.y, d2.x), glr_map(v.z, v.w, d2.y));
     }
     uint64_t d = pk(d2.x, d2.y), sum = 0;
-    const bool pair = g.pair && c0 + kGlrC <= a.C;
-    using E = typename Fmt<DT>::E;
-    const int64_t tl = t0 + kRun - 1;  // from the last token back
-    E* dx = static_cast<E*>(gr.dx) + (b * gr.dxs[0] + tl * gr.dxs[1] + c * gr.dxs[2]);
-    E* dp = static_cast<E*>(gr.dp) + (b * gr.dps[0] + tl * gr.dps[1] + c * gr.dps[2]);
-    E* dq = static_cast<E*>(gr.dq) + (b * gr.dqs[0] + tl * gr.dqs[1] + c * gr.dqs[2]);
-    auto run = [&](auto whole) {
-      constexpr bool W = decltype(whole)::value;
+    if (TMA) {
 #pragma unroll
       for (int j = kRun - 1; j >= 0; --j) {
-        if (W || j < n) {
+        const uint64_t G = fadd2(d, load(3, gr.dout, gr.dos, j));
+        glr_sts<DT>(st, j, lane, fmul2(G, f1[j]));
+        glr_sts<DT>(st + PLANE, j, lane, fmul2(G, f0[j]));
+        glr_sts<DT>(st + 2 * PLANE, j, lane, fmul2(G, f3[j]));
+        if (j < n) sum = ffma2(G, f2[j], sum);
+        d = SEQ && (reset >> j & 1) ? 0 : fmul2(dec[j], G);
+      }
+      if (n > 0) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&maps.dx, st, at.c0, static_cast<int>(t0), b);
+          tma_store_3d(&maps.dp, st + PLANE, at.c0, static_cast<int>(t0), b);
+          tma_store_3d(&maps.dq, st + 2 * PLANE, at.c0, static_cast<int>(t0), b);
+          bulk_commit();
+        }
+      }
+    } else {
+      const bool pair = g.pair && in1;
+      using E = typename Fmt<DT>::E;
+      const int64_t tl = t0 + kRun - 1;  // from the last token back
+      E* dx = static_cast<E*>(gr.dx) + (b * gr.dxs[0] + tl * gr.dxs[1] + c * gr.dxs[2]);
+      E* dp = static_cast<E*>(gr.dp) + (b * gr.dps[0] + tl * gr.dps[1] + c * gr.dps[2]);
+      E* dq = static_cast<E*>(gr.dq) + (b * gr.dqs[0] + tl * gr.dqs[1] + c * gr.dqs[2]);
+#pragma unroll
+      for (int j = kRun - 1; j >= 0; --j) {
+        if (j < n) {
           const uint64_t G = fadd2(d, load(3, gr.dout, gr.dos, j));
-          glr_stg<DT>(dx, gr.dxs[2], W || pair, W || in0, W || in1, fmul2(G, f1[j]));
-          glr_stg<DT>(dp, gr.dps[2], W || pair, W || in0, W || in1, fmul2(G, f0[j]));
-          glr_stg<DT>(dq, gr.dqs[2], W || pair, W || in0, W || in1, fmul2(G, f3[j]));
+          glr_stg<DT>(dx, gr.dxs[2], pair, in0, in1, fmul2(G, f1[j]));
+          glr_stg<DT>(dp, gr.dps[2], pair, in0, in1, fmul2(G, f0[j]));
+          glr_stg<DT>(dq, gr.dqs[2], pair, in0, in1, fmul2(G, f3[j]));
           sum = ffma2(G, f2[j], sum);
           d = SEQ && (reset >> j & 1) ? 0 : fmul2(dec[j], G);
         }
         dx -= gr.dxs[1], dp -= gr.dps[1], dq -= gr.dqs[1];
       }
-    };
-    if (pair && n == kRun)
-      run(std::true_type{});
-    else
-      run(std::false_type{});
+    }
     upk(sum, d2.x, d2.y);
     sh.rate[warp][lane] = d2;
-    __syncthreads();  // the stage has been read, the sums are there
-    if (tid == 0 && !g.one) {
-      fence_proxy_async_smem();
-      fill(s, next);
-      next = draw();
-    }
+    __syncthreads();  // the sums are there
     if (warp == kWarps - 1) {
 #pragma unroll
       for (int w = kWarps - 2; w >= 0; --w) {
@@ -303,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
       if (in1) part[1] = -d2.y;
     }
   }
+  if (TMA && lane == 0) bulk_wait_read();
 }
 
 // drate: the partial sums [P][C] in 32 interleaved subsequences and then these.
@@ -337,6 +348,11 @@ cudaError_t launch(const GlrArgs& a, const GlrGrads& gr, const GlrTiles& t, cons
         !tensor_map3(&maps.q, a.q, a.qs, a.B, a.L, a.C, box, dt) ||
         !tensor_map3(&maps.o, gr.dout, gr.dos, a.B, a.L, a.C, box, dt))
       return cudaErrorInvalidValue;
+    const int64_t run[2] = {kGlrC, kRun};
+    if (!tensor_map3(&maps.dx, gr.dx, gr.dxs, a.B, a.L, a.C, run, dt) ||
+        !tensor_map3(&maps.dp, gr.dp, gr.dps, a.B, a.L, a.C, run, dt) ||
+        !tensor_map3(&maps.dq, gr.dq, gr.dqs, a.B, a.L, a.C, run, dt))
+      return cudaErrorInvalidValue;
   }
   const int smem = TMA ? kStages * 4 * plane_bytes<DT>() : 0;
   const cudaError_t e =
@@ -363,7 +379,9 @@ cudaError_t launch_glr_bwd(const GlrArgs& a, const GlrGrads& gr, void* ws, Dtype
                            cudaStream_t stream) {
   GlrTiles t = glr_tiles(a.B, a.L, a.C);
   const bool tma = tensor_map_eligible(a.x, a.xs, a.B, a.L, a.C, dt) && tensor_map_eligible(a.p, a.ps, a.B, a.L, a.C, dt) &&
-          tensor_map_eligible(a.q, a.qs, a.B, a.L, a.C, dt) && tensor_map_eligible(gr.dout, gr.dos, a.B, a.L, a.C, dt);
+          tensor_map_eligible(a.q, a.qs, a.B, a.L, a.C, dt) && tensor_map_eligible(gr.dout, gr.dos, a.B, a.L, a.C, dt) &&
+          tensor_map_eligible(gr.dx, gr.dxs, a.B, a.L, a.C, dt) && tensor_map_eligible(gr.dp, gr.dps, a.B, a.L, a.C, dt) &&
+          tensor_map_eligible(gr.dq, gr.dqs, a.B, a.L, a.C, dt);
   t.pair = glr_pair_out(gr.dx, gr.dxs, dt) && glr_pair_out(gr.dp, gr.dps, dt) && glr_pair_out(gr.dq, gr.dqs, dt);
   GlrChain chain = {};
   cudaError_t e = cudaSuccess;
