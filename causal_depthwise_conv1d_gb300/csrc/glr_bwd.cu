@@ -41,6 +41,7 @@ struct __align__(16) Shared {
   float2 rate[kWarps][32];
   uint64_t full[kStages];
   GlrPlace place[kStages];
+  int late;
 };
 
 // The runs' maps of the carry, last run first, as one.
@@ -71,6 +72,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1);
     fence_barrier_init();
+    sh.late = 0;
   }
   pdl_enter();
   __syncthreads();
@@ -110,10 +112,13 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
   for (int it = 0;; ++it) {
     const int s = it & 1;
     if (it == 1 && g.one) break;
-    if (!mbar_wait(&sh.full[s], (it >> 1) & 1)) {
+    // One warp polls and the others wait at the barrier: polls of all took up to a third of the issue slots.
+    if (warp == 0 && !mbar_wait(&sh.full[s], (it >> 1) & 1)) {
       if (lane == 0) atomicOr(&g_fault, kFaultConsumerWait);
-      break;  // no other copy of the block is in flight
+      sh.late = 1;  // no other copy of the block is in flight
     }
+    __syncthreads();
+    if (sh.late) break;
     const GlrPlace at = sh.place[s];
     if (at.tile >= g.total) break;
     const int level = at.level, back = g.levels - 1 - level, b = at.b, c = at.c0 + 2 * lane;
@@ -197,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
       upk(R, y.x, y.y);
       sh.bwd[warp][lane] = make_float4(x.x, y.x, x.y, y.y);
     }
-    if (TMA && lane == 0) bulk_wait_read();  // the boxes of the tile before have left its stage
+    if (TMA && lane == 0) bulk_wait_read<>();  // the boxes of the tile before have left its stage
     __syncthreads();  // the runs' maps are there, the other stage is free
     if (tid == 0 && !g.one) {
       fence_proxy_async_smem();
@@ -313,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
       if (in1) part[1] = -d2.y;
     }
   }
-  if (TMA && lane == 0) bulk_wait_read();
+  if (TMA && lane == 0) bulk_wait_read<>();
 }
 
 // drate: the partial sums [P][C] in 32 interleaved subsequences and then these.

@@ -36,6 +36,7 @@ struct __align__(16) Shared {
   float4 pair[2][kWarps][32];
   uint64_t full[kStages];
   GlrPlace place[kStages];
+  int late;
 };
 
 template <int DT, bool SEQ, bool TMA>
@@ -50,6 +51,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1);
     fence_barrier_init();
+    sh.late = 0;
   }
   pdl_enter();
   __syncthreads();
@@ -86,10 +88,13 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
   for (int it = 0;; ++it) {
     const int s = it & 1;
     if (it == 1 && g.one) break;
-    if (!mbar_wait(&sh.full[s], (it >> 1) & 1)) {
+    // One warp polls and the others wait at the barrier: polls of all took up to a third of the issue slots.
+    if (warp == 0 && !mbar_wait(&sh.full[s], (it >> 1) & 1)) {
       if (lane == 0) atomicOr(&g_fault, kFaultConsumerWait);
-      break;  // no other copy of the block is in flight
+      sh.late = 1;  // no other copy of the block is in flight
     }
+    __syncthreads();
+    if (sh.late) break;
     const GlrPlace at = sh.place[s];
     if (at.tile >= g.total) break;
     const int level = at.level, b = at.b, c = at.c0 + 2 * lane;
@@ -166,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
       upk(A, x.x, x.y), upk(H, y.x, y.y);
       pairs[warp][lane] = make_float4(x.x, y.x, x.y, y.y);
     }
-    if (TMA && lane == 0) bulk_wait_read();  // the box of the tile before has left its stage
+    if (TMA && lane == 0) bulk_wait_read<>();  // the box of the tile before has left its stage
     __syncthreads();  // pairs are there, the other stage is free
     if (tid == 0 && !g.one) {
       fence_proxy_async_smem();
@@ -251,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
       if (in1) p[a.s1s[1]] = h2.y;
     }
   }
-  if (TMA && lane == 0) bulk_wait_read();
+  if (TMA && lane == 0) bulk_wait_read<>();
 }
 
 template <int DT, bool SEQ, bool TMA>

@@ -24,6 +24,7 @@
 #include "glr.cuh"
 #include "rec_pairs.cuh"
 #include "tensor_map.h"
+#include "tma_store.cuh"
 
 namespace ccv {
 
@@ -170,16 +171,6 @@ cudaError_t glr_launch(void (*kernel)(P...), const GlrTiles& g, unsigned grid, u
 }
 
 // ---------------------------------------------------------------- pairs of channels
-
-// Tiled store of a box from shared memory, in the thread's current group of
-// bulk copies; and the wait until the group's boxes have been read.
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-               "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 // Two adjacent channels of a staged row (rows of 64 elements).
 template <int DT>

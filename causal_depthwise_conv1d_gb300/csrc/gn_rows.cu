@@ -6,8 +6,11 @@
 // its channels' parameters (and, backwards, their gradients' sums) in registers
 // and walks over rows; the loads of the next rows are in flight while the
 // present ones are worked on.  What bounds it: HBM.
+#include <type_traits>
+
 #include "ccv_common.cuh"
 #include "rec_internal.h"
+#include "rec_pairs.cuh"
 
 namespace ccv {
 namespace {
@@ -22,21 +25,6 @@ __device__ __forceinline__ void lanes_sum(float (&v)[NS]) {
   for (int m = LPG / 2; m > 0; m >>= 1)
 #pragma unroll
     for (int i = 0; i < NS; ++i) v[i] += __shfl_xor_sync(kFullMask, v[i], m);
-}
-
-__device__ __forceinline__ float pair_sum(uint64_t v) {
-  float a, b;
-  upk(v, a, b);
-  return a + b;
-}
-
-template <int DT>
-__device__ __forceinline__ void unpack_pairs(const uint4& v, uint64_t* f) {
-  constexpr int V = Fmt<DT>::VEC;
-  float x[V];
-  unpack16<DT>(v, x);
-#pragma unroll
-  for (int j = 0; j < V / 2; ++j) f[j] = pk(x[2 * j], x[2 * j + 1]);
 }
 
 // A lane's place: its group, vectors and rows.  Warp tasks are (rows, column
@@ -57,8 +45,8 @@ struct Lane {
   }
 };
 
-template <int DT, int LPG, int NV>
-__global__ void __launch_bounds__(kThreads) gn_rows_fwd(const GnArgs a, int colblocks) {
+template <int DT, int LPG, int NV, bool FULL, bool SILU>
+__global__ void __launch_bounds__(kThreads, NV == 1 ? 4 : NV == 2 ? 3 : 1) gn_rows_fwd(const GnArgs a, int colblocks) {
   constexpr int V = Fmt<DT>::VEC, H = V / 2;
   using E = typename Fmt<DT>::E;
   pdl_enter();
@@ -70,7 +58,7 @@ __global__ void __launch_bounds__(kThreads) gn_rows_fwd(const GnArgs a, int colb
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int64_t col = (l.sub + i * LPG) * V, ch = l.g * cg + col;
-    in[i] = l.on && col < cg;
+    in[i] = FULL || (l.on && col < cg);
 #pragma unroll
     for (int j = 0; j < H; ++j) {
       float x[2], y[2];
@@ -82,13 +70,15 @@ __global__ void __launch_bounds__(kThreads) gn_rows_fwd(const GnArgs a, int colb
       w[i][j] = pk(x[0], x[1]), b[i][j] = pk(y[0], y[1]);
     }
   }
-  const E* x = static_cast<const E*>(a.x) + l.g * cg + l.sub * V;
-  E* out = static_cast<E*>(a.out) + l.g * cg + l.sub * V;
+  const E* x = static_cast<const E*>(a.x) + l.row * a.xs[0] + l.g * cg + l.sub * V;
+  E* out = static_cast<E*>(a.out) + l.row * a.os[0] + l.g * cg + l.sub * V;
+  const int64_t x_hop = l.step * a.xs[0], out_hop = l.step * a.os[0];
   uint4 raw[NV];
   auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      raw[i] = in[i] && row < a.N ? ld_stream16(x + row * a.xs[0] + i * LPG * V) : make_uint4(0, 0, 0, 0);
+      raw[i] = (FULL || in[i]) && row < a.N ? ld_stream16(x + i * LPG * V) : make_uint4(0, 0, 0, 0);
+    x += x_hop;
   };
   fetch(l.row);
   for (int64_t row = l.row; row < a.N; row += l.step) {
@@ -109,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) gn_rows_fwd(const GnArgs a, int colb
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < H; ++j) {
-        f[i][j] = in[i] ? fadd2(f[i][j], minus) : 0;
+        f[i][j] = FULL || in[i] ? fadd2(f[i][j], minus) : 0;
         acc = ffma2(f[i][j], f[i][j], acc);
       }
     s[0] = pair_sum(acc);
@@ -122,16 +112,17 @@ __global__ void __launch_bounds__(kThreads) gn_rows_fwd(const GnArgs a, int colb
 #pragma unroll
       for (int j = 0; j < H; ++j) {
         uint64_t z = ffma2(fmul2(f[i][j], r2), w[i][j], b[i][j]);
-        if (a.silu) z = activate2_for<true, DT>(z);
+        if constexpr (SILU) z = silu_pair(z);
         upk(z, o[2 * j], o[2 * j + 1]);
       }
-      if (in[i]) st16_stream(out + row * a.os[0] + i * LPG * V, pack16<DT>(o));
+      if (FULL || in[i]) st16_stream(out + i * LPG * V, pack16<DT>(o));
     }
+    out += out_hop;
   }
 }
 
-template <int DT, int LPG, int NV>
-__global__ void __launch_bounds__(kThreads) gn_rows_bwd(const GnArgs a, int colblocks) {
+template <int DT, int LPG, int NV, bool FULL, bool SILU>
+__global__ void __launch_bounds__(kThreads, NV == 1 ? 3 : NV == 2 ? 2 : 1) gn_rows_bwd(const GnArgs a, int colblocks) {
   constexpr int V = Fmt<DT>::VEC, H = V / 2;
   using E = typename Fmt<DT>::E;
   __shared__ float sums[kWarps][32][NV * V];
@@ -144,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) gn_rows_bwd(const GnArgs a, int colb
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int64_t col = (l.sub + i * LPG) * V, ch = l.g * cg + col;
-    in[i] = l.on && col < cg;
+    in[i] = FULL || (l.on && col < cg);
 #pragma unroll
     for (int j = 0; j < H; ++j) {
       float x[2], y[2];
@@ -158,17 +149,19 @@ __global__ void __launch_bounds__(kThreads) gn_rows_bwd(const GnArgs a, int colb
     }
   }
   const int64_t c0 = l.g * cg + l.sub * V;
-  const E* x = static_cast<const E*>(a.x) + c0;
-  const E* dy = static_cast<const E*>(a.dout) + c0;
-  E* dx = static_cast<E*>(a.dx) + c0;
+  const E* x = static_cast<const E*>(a.x) + l.row * a.xs[0] + c0;
+  const E* dy = static_cast<const E*>(a.dout) + l.row * a.gs[0] + c0;
+  E* dx = static_cast<E*>(a.dx) + l.row * a.dxs[0] + c0;
+  const int64_t x_hop = l.step * a.xs[0], dy_hop = l.step * a.gs[0], dx_hop = l.step * a.dxs[0];
   uint4 rx[NV], rg[NV];
   auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const bool on = in[i] && row < a.N;
-      rx[i] = on ? ld_stream16(x + row * a.xs[0] + i * LPG * V) : make_uint4(0, 0, 0, 0);
-      rg[i] = on ? ld_stream16(dy + row * a.gs[0] + i * LPG * V) : make_uint4(0, 0, 0, 0);
+      const bool on = (FULL || in[i]) && row < a.N;
+      rx[i] = on ? ld_stream16(x + i * LPG * V) : make_uint4(0, 0, 0, 0);
+      rg[i] = on ? ld_stream16(dy + i * LPG * V) : make_uint4(0, 0, 0, 0);
     }
+    x += x_hop, dy += dy_hop;
   };
   fetch(l.row);
   for (int64_t row = l.row; row < a.N; row += l.step) {
@@ -190,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) gn_rows_bwd(const GnArgs a, int colb
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < H; ++j) {
-        f[i][j] = in[i] ? fadd2(f[i][j], minus) : 0;
+        f[i][j] = FULL || in[i] ? fadd2(f[i][j], minus) : 0;
         acc = ffma2(f[i][j], f[i][j], acc);
       }
     s[0] = pair_sum(acc);
@@ -203,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) gn_rows_bwd(const GnArgs a, int colb
 #pragma unroll
       for (int j = 0; j < H; ++j) {
         f[i][j] = fmul2(f[i][j], r2);  // xh
-        if (a.silu) d[i][j] = dz_pair<true>(ffma2(f[i][j], w[i][j], b[i][j]), d[i][j]);
+        if constexpr (SILU) d[i][j] = silu_grad_pair(ffma2(f[i][j], w[i][j], b[i][j]), d[i][j]);
         dw[i][j] = ffma2(d[i][j], f[i][j], dw[i][j]);
         db[i][j] = fadd2(db[i][j], d[i][j]);
         d[i][j] = fmul2(d[i][j], w[i][j]);
@@ -219,8 +212,9 @@ __global__ void __launch_bounds__(kThreads) gn_rows_bwd(const GnArgs a, int colb
       float o[V];
 #pragma unroll
       for (int j = 0; j < H; ++j) upk(ffma2(d[i][j], r2, ffma2(f[i][j], k2, k1)), o[2 * j], o[2 * j + 1]);
-      if (in[i]) st16_stream(dx + row * a.dxs[0] + i * LPG * V, pack16<DT>(o));
+      if (FULL || in[i]) st16_stream(dx + i * LPG * V, pack16<DT>(o));
     }
+    dx += dx_hop;
   }
   if (a.part == nullptr) return;
   // the block's warps in order, one partial sum a block
@@ -253,17 +247,16 @@ __global__ void __launch_bounds__(kThreads) gn_rows_bwd(const GnArgs a, int colb
   }
 }
 
-// Lanes of a group and vectors a lane: as few idle lanes as the sizes allow.
+// Lanes of a group and vectors a lane.  Two vectors a lane halve the exchanges
+// for each element.
 struct Shape {
   int lpg, nv;
 };
 Shape shape_of(int64_t vecs) {
-  if (vecs <= 1) return {1, 1};
-  if (vecs <= 2) return {2, 1};
   if (vecs <= 4) return {4, 1};
-  if (vecs <= 8) return {8, 1};
-  if (vecs <= 16) return {16, 1};
-  if (vecs <= 32) return {32, 1};
+  if (vecs <= 8) return {4, 2};
+  if (vecs <= 16) return {8, 2};
+  if (vecs <= 32) return {16, 2};
   if (vecs <= 64) return {32, 2};
   return {32, 4};
 }
@@ -272,20 +265,24 @@ template <int DT, int LPG, int NV>
 cudaError_t launch(const GnArgs& a, bool bwd, int64_t slots, cudaStream_t s) {
   const int colblocks = static_cast<int>((a.G + 32 / LPG - 1) / (32 / LPG));
   const unsigned grid = static_cast<unsigned>(colblocks * slots);
-  if (bwd) return launch_pdl(gn_rows_bwd<DT, LPG, NV>, grid, kThreads, 0, s, a, colblocks);
-  return launch_pdl(gn_rows_fwd<DT, LPG, NV>, grid, kThreads, 0, s, a, colblocks);
+  const bool full = a.C / a.G == LPG * NV * Fmt<DT>::VEC && a.G % (32 / LPG) == 0;
+  auto go = [&](auto f, auto y) {
+    constexpr bool F = decltype(f)::value, Y = decltype(y)::value;
+    if (bwd) return launch_pdl(gn_rows_bwd<DT, LPG, NV, F, Y>, grid, kThreads, 0, s, a, colblocks);
+    return launch_pdl(gn_rows_fwd<DT, LPG, NV, F, Y>, grid, kThreads, 0, s, a, colblocks);
+  };
+  if (full) return a.silu ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+  return a.silu ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
 }
 
 template <int DT>
 cudaError_t launch_dt(const GnArgs& a, bool bwd, int64_t slots, cudaStream_t s) {
   const Shape h = shape_of(a.C / a.G / Fmt<DT>::VEC);
   switch (h.lpg * 10 + h.nv) {
-    case 11: return launch<DT, 1, 1>(a, bwd, slots, s);
-    case 21: return launch<DT, 2, 1>(a, bwd, slots, s);
     case 41: return launch<DT, 4, 1>(a, bwd, slots, s);
-    case 81: return launch<DT, 8, 1>(a, bwd, slots, s);
-    case 161: return launch<DT, 16, 1>(a, bwd, slots, s);
-    case 321: return launch<DT, 32, 1>(a, bwd, slots, s);
+    case 42: return launch<DT, 4, 2>(a, bwd, slots, s);
+    case 82: return launch<DT, 8, 2>(a, bwd, slots, s);
+    case 162: return launch<DT, 16, 2>(a, bwd, slots, s);
     case 322: return launch<DT, 32, 2>(a, bwd, slots, s);
     default: return launch<DT, 32, 4>(a, bwd, slots, s);
   }
@@ -309,7 +306,7 @@ bool gn_rows_eligible(const GnArgs& a, Dtype dt, bool bwd) {
 int64_t gn_rows_slots(int64_t N, int64_t C, int64_t G, int64_t esize, bool bwd) {
   const Shape h = shape_of(C / G / (16 / esize));
   const int64_t colblocks = (G + 32 / h.lpg - 1) / (32 / h.lpg);
-  const int64_t most = 152 * (bwd ? (h.nv == 1 ? 3 : 1) : (h.nv == 1 ? 6 : h.nv == 2 ? 4 : 2));
+  const int64_t most = 152 * (bwd ? (h.nv == 1 ? 3 : h.nv == 2 ? 2 : 1) : (h.nv == 1 ? 4 : h.nv == 2 ? 3 : 1));
   int64_t slots = (most + colblocks - 1) / colblocks;
   const int64_t rows = (N + kWarps - 1) / kWarps;
   if (slots > rows) slots = rows;
