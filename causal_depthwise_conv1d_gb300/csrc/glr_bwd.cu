@@ -25,6 +25,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRun = kGlrT / kWarps;  // tokens of a warp
 constexpr int kStages = 2;
+constexpr int kPublisher = 1;  // the warp that publishes (the first one starts the copies)
 
 struct Maps {
   CUtensorMap x, p, q, o, dx, dp, dq;
@@ -41,7 +42,6 @@ struct __align__(16) Shared {
   float2 rate[kWarps][32];
   uint64_t full[kStages];
   GlrPlace place[kStages];
-  int late;
 };
 
 // The runs' maps of the carry, last run first, as one.
@@ -72,7 +72,6 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1);
     fence_barrier_init();
-    sh.late = 0;
   }
   pdl_enter();
   __syncthreads();
@@ -87,9 +86,10 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
   // Tile t in the order of work: the last tokens first.
   auto fill = [&](int s, int t) {
     GlrPlace p;
-    const int back = t / g.ncols;
+    const int back = glr_div(t, g.ncols_inv);
     p.tile = t;
-    p.level = g.levels - 1 - back, p.col = t - back * g.ncols, p.b = p.col / g.nct, p.c0 = (p.col - p.b * g.nct) * kGlrC;
+    p.level = g.levels - 1 - back, p.col = t - back * g.ncols;
+    p.b = glr_div(p.col, g.nct_inv), p.c0 = (p.col - p.b * g.nct) * kGlrC;
     sh.place[s] = p;
     if (!TMA || t >= g.total) {
       mbar_arrive(&sh.full[s]);
@@ -112,13 +112,10 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
   for (int it = 0;; ++it) {
     const int s = it & 1;
     if (it == 1 && g.one) break;
-    // One warp polls and the others wait at the barrier: polls of all took up to a third of the issue slots.
-    if (warp == 0 && !mbar_wait(&sh.full[s], (it >> 1) & 1)) {
+    if (!mbar_wait(&sh.full[s], (it >> 1) & 1)) {
       if (lane == 0) atomicOr(&g_fault, kFaultConsumerWait);
-      sh.late = 1;  // no other copy of the block is in flight
+      break;  // no other copy of the block is in flight
     }
-    __syncthreads();
-    if (sh.late) break;
     const GlrPlace at = sh.place[s];
     if (at.tile >= g.total) break;
     const int level = at.level, back = g.levels - 1 - level, b = at.b, c = at.c0 + 2 * lane;
@@ -219,13 +216,13 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
     } else if (__all_sync(kFullMask, before.x == kSlotState)) {
       d2 = glr_slot_state(before);
     } else {
-      if (warp == 0 && level > 0) glr_put_pair(chain, at.tile, lane, joined(sh.bwd, lane));
+      if (warp == kPublisher && level > 0) glr_put_pair(chain, at.tile, lane, joined(sh.bwd, lane));
       if (!glr_look_back(chain, g, back, at.col, lane, d2)) {
         if (lane == 0) atomicOr(&g_fault, kFaultConsumerWait);
         d2 = make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));  // nothing that passes for one
       }
     }
-    if (warp == 0 && (level > 0 || gr.ds0 != nullptr)) {
+    if (warp == kPublisher && (level > 0 || gr.ds0 != nullptr)) {
       const float4 m = joined(sh.bwd, lane);
       const float2 after = make_float2(glr_map(m.x, m.y, d2.x), glr_map(m.z, m.w, d2.y));
       if (level > 0) {

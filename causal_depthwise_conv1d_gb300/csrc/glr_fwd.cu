@@ -22,6 +22,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRun = kGlrT / kWarps;  // tokens of a warp
 constexpr int kStages = 2;
+constexpr int kPublisher = 1;  // the warp that publishes (the first one starts the copies)
 
 struct Maps {
   CUtensorMap x, p, q, out;
@@ -36,8 +37,19 @@ struct __align__(16) Shared {
   float4 pair[2][kWarps][32];
   uint64_t full[kStages];
   GlrPlace place[kStages];
-  int late;
 };
+
+// The runs' maps, first run first, as one.
+__device__ __forceinline__ float4 joined(const float4 (*runs)[32], int lane) {
+  float4 m = runs[0][lane];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) {
+    const float4 v = runs[w][lane];
+    glr_join(v.x, v.y, m.x, m.y);
+    glr_join(v.z, v.w, m.z, m.w);
+  }
+  return m;
+}
 
 template <int DT, bool SEQ, bool TMA>
 __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
@@ -51,7 +63,6 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1);
     fence_barrier_init();
-    sh.late = 0;
   }
   pdl_enter();
   __syncthreads();
@@ -67,7 +78,8 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
   auto fill = [&](int s, int t) {
     GlrPlace p;
     p.tile = t;
-    p.level = t / g.ncols, p.col = t - p.level * g.ncols, p.b = p.col / g.nct, p.c0 = (p.col - p.b * g.nct) * kGlrC;
+    p.level = glr_div(t, g.ncols_inv), p.col = t - p.level * g.ncols;
+    p.b = glr_div(p.col, g.nct_inv), p.c0 = (p.col - p.b * g.nct) * kGlrC;
     sh.place[s] = p;
     if (!TMA || t >= g.total) {
       mbar_arrive(&sh.full[s]);
@@ -88,13 +100,10 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
   for (int it = 0;; ++it) {
     const int s = it & 1;
     if (it == 1 && g.one) break;
-    // One warp polls and the others wait at the barrier: polls of all took up to a third of the issue slots.
-    if (warp == 0 && !mbar_wait(&sh.full[s], (it >> 1) & 1)) {
+    if (!mbar_wait(&sh.full[s], (it >> 1) & 1)) {
       if (lane == 0) atomicOr(&g_fault, kFaultConsumerWait);
-      sh.late = 1;  // no other copy of the block is in flight
+      break;  // no other copy of the block is in flight
     }
-    __syncthreads();
-    if (sh.late) break;
     const GlrPlace at = sh.place[s];
     if (at.tile >= g.total) break;
     const int level = at.level, b = at.b, c = at.c0 + 2 * lane;
@@ -188,36 +197,21 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
     } else if (__all_sync(kFullMask, before.x == kSlotState)) {
       h2 = glr_slot_state(before);
     } else {
-      if (warp == 0 && level + 1 < g.levels) {
-        float4 m = pairs[0][lane];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-          const float4 v = pairs[w][lane];
-          glr_join(v.x, v.y, m.x, m.y);
-          glr_join(v.z, v.w, m.z, m.w);
-        }
-        glr_put_pair(chain, at.tile, lane, m);
-      }
+      if (warp == kPublisher && level + 1 < g.levels) glr_put_pair(chain, at.tile, lane, joined(pairs, lane));
       if (!glr_look_back(chain, g, level, at.col, lane, h2)) {
         if (lane == 0) atomicOr(&g_fault, kFaultConsumerWait);
         h2 = make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));  // no state: nothing that passes for one
       }
     }
-    if (warp == 0) {
+    if (warp == kPublisher) {
+      if (level + 1 < g.levels) {
+        const float4 m = joined(pairs, lane);
+        glr_put_state(chain, at.tile, lane, make_float2(glr_map(m.x, m.y, h2.x), glr_map(m.z, m.w, h2.y)));
+      }
       if (a.cs != nullptr) {
         float* p = a.cs + b * a.css[0] + level * a.css[1] + c * a.css[2];
         if (in0) p[0] = h2.x;
         if (in1) p[a.css[2]] = h2.y;
-      }
-      if (level + 1 < g.levels) {
-        float4 m = pairs[0][lane];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-          const float4 v = pairs[w][lane];
-          glr_join(v.x, v.y, m.x, m.y);
-          glr_join(v.z, v.w, m.z, m.w);
-        }
-        glr_put_state(chain, at.tile, lane, make_float2(glr_map(m.x, m.y, h2.x), glr_map(m.z, m.w, h2.y)));
       }
     }
     for (int w = 0; w < warp; ++w) {
@@ -297,6 +291,8 @@ GlrTiles glr_tiles(int64_t B, int64_t L, int64_t C) {
   t.ncols = static_cast<int>(B * t.nct);
   t.levels = static_cast<int>((L + kGlrT - 1) / kGlrT);
   t.total = static_cast<int>(static_cast<int64_t>(t.ncols) * t.levels);
+  t.ncols_inv = (uint64_t(1) << 63) / static_cast<uint64_t>(t.ncols) + 1;
+  t.nct_inv = (uint64_t(1) << 63) / static_cast<uint64_t>(t.nct) + 1;
   return t;
 }
 

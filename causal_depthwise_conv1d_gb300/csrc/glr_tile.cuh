@@ -54,11 +54,17 @@ struct GlrPlace {
 struct GlrTiles {
   int ncols;   // columns: batch rows x channel tiles
   int nct;     // channel tiles of a row
+  uint64_t ncols_inv, nct_inv;  // 2^63 / n rounded up, for t / n of 0 <= t < 2^31
   int levels;  // tiles along the time
   int total;   // ncols * levels
   bool pair;   // outputs may be stored in pairs
   bool one;    // a block for every tile: a block takes one
 };
+
+// t / n, exact: the rounding adds less than t / 2^63 to a quotient whose fraction is at most 1 - 1 / n.
+__device__ __forceinline__ int glr_div(int t, uint64_t inv) {
+  return static_cast<int>(__umul64hi(static_cast<uint64_t>(t) << 1, inv));
+}
 
 constexpr float kMinusZero = -0.0f;
 __device__ __forceinline__ bool glr_cut(float A) { return __float_as_uint(A) == 0x80000000u; }
@@ -231,11 +237,9 @@ __device__ __forceinline__ void glr_sigmoid2(uint64_t z, uint64_t& s, uint64_t& 
 // kGlrSeries).
 template <bool NEAR>
 __device__ __forceinline__ void glr_decay2(uint64_t l, uint64_t& a, uint64_t& m2) {
-  constexpr float c[] = {1.f / 362880.f, 1.f / 40320.f, 1.f / 5040.f, 1.f / 720.f, 1.f / 120.f,
-                         1.f / 24.f,     1.f / 6.f,     0.5f,         1.f};
-  uint64_t E = ffma2(l, twice(c[0]), twice(c[1]));
+  uint64_t E = twice(glr_poly(0));
 #pragma unroll
-  for (int i = 2; i < 9; ++i) E = ffma2(E, l, twice(c[i]));
+  for (int i = 1; i < 7; ++i) E = ffma2(E, l, twice(glr_poly(i)));
   E = fmul2(E, l);
   a = fadd2(E, twice(1.f));
   if constexpr (!NEAR) {

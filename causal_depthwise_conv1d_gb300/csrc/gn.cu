@@ -298,18 +298,24 @@ GnPlan gn_plan(int64_t N, int64_t S, int64_t C, int64_t G) {
 int64_t gn_parts(int64_t N, int64_t S, int64_t C, int64_t G) {
   const GnPlan p = gn_plan(N, S, C, G);
   int64_t most = p.slots * p.slabs;
+  if (gn_narrow_eligible(S, C, G)) {
+    const int64_t n = gn_narrow_slots(N, C, G);
+    if (n > most) most = n;
+  }
   for (const int64_t esize : {2, 4}) {
     const int64_t v = 16 / esize;
     if (C / G % v != 0) continue;
-    const int64_t n = S == 1 && C / G / v <= 128 ? gn_rows_slots(N, C, G, esize, true)
-                                                 : gn_cluster_parts(N, S, C, G, esize);
+    const int64_t n = S == 1 && C / G / v <= 128 ? gn_rows_slots(N, C, G, esize, true) : 0;
+    const int64_t m = gn_cluster_parts(N, S, C, G, esize);
     if (n > most) most = n;
+    if (m > most) most = m;
   }
   return most;
 }
 
 cudaError_t launch_gn_fwd(const GnArgs& a, Dtype dt, cudaStream_t stream) {
   if (gn_rows_eligible(a, dt, false)) return launch_gn_rows(a, dt, false, stream);
+  if (gn_narrow_eligible(a.S, a.C, a.G)) return launch_gn_narrow(a, dt, false, stream);
   if (gn_cluster_eligible(a, dt, false)) return launch_gn_cluster(a, dt, false, stream);
   switch (dt) {
     case kF32: return fwd_dt<kF32>(a, stream);
@@ -327,6 +333,9 @@ cudaError_t launch_gn_bwd(const GnArgs& a, Dtype dt, cudaStream_t stream) {
   if (some && gn_rows_eligible(a, dt, true)) {
     e = launch_gn_rows(a, dt, true, stream);
     parts = gn_rows_slots(a.N, a.C, a.G, esize, true);
+  } else if (some && gn_narrow_eligible(a.S, a.C, a.G)) {
+    e = launch_gn_narrow(a, dt, true, stream);
+    parts = gn_narrow_slots(a.N, a.C, a.G);
   } else if (some && gn_cluster_eligible(a, dt, true)) {
     e = launch_gn_cluster(a, dt, true, stream);
     parts = gn_cluster_parts(a.N, a.S, a.C, a.G, esize);

@@ -115,6 +115,10 @@ cudaError_t launch_gn_rows(const GnArgs& a, Dtype dt, bool bwd, cudaStream_t str
 bool gn_cluster_eligible(const GnArgs& a, Dtype dt, bool bwd);
 int64_t gn_cluster_parts(int64_t N, int64_t S, int64_t C, int64_t G, int64_t esize);
 cudaError_t launch_gn_cluster(const GnArgs& a, Dtype dt, bool bwd, cudaStream_t stream);
+// Rows on their own in narrow groups of any width and strides (gn_narrow.cu).
+bool gn_narrow_eligible(int64_t S, int64_t C, int64_t G);
+int64_t gn_narrow_slots(int64_t N, int64_t C, int64_t G);
+cudaError_t launch_gn_narrow(const GnArgs& a, Dtype dt, bool bwd, cudaStream_t stream);
 // The most partial sums any of the kernels makes for these sizes.
 int64_t gn_parts(int64_t N, int64_t S, int64_t C, int64_t G);
 unsigned read_and_clear_fault_gn();
