@@ -42,6 +42,7 @@ struct __align__(16) Shared {
   float2 rate[kWarps][32];
   uint64_t full[kStages];
   GlrPlace place[kStages];
+  float2 carried[kStages][32];  // serial: the carry out of the tile before
 };
 
 // The runs' maps of the carry, last run first, as one.
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool chained = g.levels > 1;
+  const bool chained = g.levels > 1 && !g.serial;
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1);
@@ -79,9 +80,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
   int drawn = 0;
   auto draw = [&]() -> int {
     if (chained) return static_cast<int>(atomicAdd(chain.ticket, 1u) + 1u);
-    const int t = static_cast<int>(blockIdx.x + drawn * gridDim.x);
-    ++drawn;
-    return t;
+    return glr_serial_tile(g, drawn++);
   };
   // Tile t in the order of work: the last tokens first.
   auto fill = [&](int s, int t) {
@@ -124,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
     const int64_t left = a.L - t0;
     const int n = left >= kRun ? kRun : left > 0 ? static_cast<int>(left) : 0;  // tokens of this warp
     uint4 before = make_uint4(kSlotEmpty, 0u, 0u, 0u);
-    if (back > 0) before = ld_slot(glr_slot(chain, at.tile - g.ncols, lane));  // it may be there already
+    if (chained && back > 0) before = ld_slot(glr_slot(chain, at.tile - g.ncols, lane));  // it may be there already
     unsigned reset = 0;  // bit j: a sequence starts at the warp's token j
     if constexpr (SEQ) {
       bool start = false;
@@ -213,6 +212,8 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
         const float* p = gr.ds1 + b * gr.ds1s[0] + c * gr.ds1s[1];
         d2 = make_float2(in0 ? p[0] : 0.f, in1 ? p[gr.ds1s[1]] : 0.f);
       }
+    } else if (g.serial) {
+      d2 = sh.carried[s ^ 1][lane];
     } else if (__all_sync(kFullMask, before.x == kSlotState)) {
       d2 = glr_slot_state(before);
     } else {
@@ -226,7 +227,10 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
       const float4 m = joined(sh.bwd, lane);
       const float2 after = make_float2(glr_map(m.x, m.y, d2.x), glr_map(m.z, m.w, d2.y));
       if (level > 0) {
-        glr_put_state(chain, at.tile, lane, after);
+        if (g.serial)
+          sh.carried[s][lane] = after;
+        else
+          glr_put_state(chain, at.tile, lane, after);
       } else {
         float* p = gr.ds0 + b * gr.ds0s[0] + c * gr.ds0s[1];
         if (in0) p[0] = after.x;
@@ -362,8 +366,10 @@ cudaError_t launch(const GlrArgs& a, const GlrGrads& gr, const GlrTiles& t, cons
   if (e != cudaSuccess) return e;
   const int64_t most = static_cast<int64_t>(dev.sm_count) * (DT == kF32 ? 1 : 2);
   GlrTiles g = t;
-  g.one = g.total <= most;
-  return glr_launch(glr_bwd_kernel<DT, SEQ, TMA>, g, static_cast<unsigned>(g.one ? g.total : most), kThreads,
+  g.serial = g.levels > 1 && g.levels <= kGlrSerial;
+  g.one = !g.serial && g.total <= most;
+  const int64_t grid = g.serial ? g.ncols : g.total;
+  return glr_launch(glr_bwd_kernel<DT, SEQ, TMA>, g, static_cast<unsigned>(grid < most ? grid : most), kThreads,
                     smem, s, a, gr, g, chain, maps);
 }
 
@@ -387,11 +393,7 @@ cudaError_t launch_glr_bwd(const GlrArgs& a, const GlrGrads& gr, void* ws, Dtype
   t.pair = glr_pair_out(gr.dx, gr.dxs, dt) && glr_pair_out(gr.dp, gr.dps, dt) && glr_pair_out(gr.dq, gr.dqs, dt);
   GlrChain chain = {};
   cudaError_t e = cudaSuccess;
-  if (t.levels > 1) {
-    chain = glr_chain(ws);
-    e = cudaMemsetAsync(ws, 0xff, glr_chain_bytes(t.total), stream);
-    if (e != cudaSuccess) return e;
-  }
+  if (t.levels > kGlrSerial) chain = glr_chain(ws);
   switch (dt) {
     case kF32: e = bwd_dt<kF32>(a, gr, t, chain, tma, dev, stream); break;
     case kF16: e = bwd_dt<kF16>(a, gr, t, chain, tma, dev, stream); break;

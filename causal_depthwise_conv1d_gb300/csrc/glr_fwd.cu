@@ -37,6 +37,7 @@ struct __align__(16) Shared {
   float4 pair[2][kWarps][32];
   uint64_t full[kStages];
   GlrPlace place[kStages];
+  float2 carried[kStages][32];  // serial: the state after the tile before
 };
 
 // The runs' maps, first run first, as one.
@@ -58,7 +59,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool chained = g.levels > 1;
+  const bool chained = g.levels > 1 && !g.serial;
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1);
@@ -71,9 +72,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
   int drawn = 0;
   auto draw = [&]() -> int {
     if (chained) return static_cast<int>(atomicAdd(chain.ticket, 1u) + 1u);
-    const int t = static_cast<int>(blockIdx.x + drawn * gridDim.x);
-    ++drawn;
-    return t;
+    return glr_serial_tile(g, drawn++);
   };
   auto fill = [&](int s, int t) {
     GlrPlace p;
@@ -112,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
     const int64_t left = a.L - t0;
     const int n = left >= kRun ? kRun : left > 0 ? static_cast<int>(left) : 0;  // tokens of this warp
     uint4 before = make_uint4(kSlotEmpty, 0u, 0u, 0u);
-    if (level > 0) before = ld_slot(glr_slot(chain, at.tile - g.ncols, lane));  // it may be there already
+    if (chained && level > 0) before = ld_slot(glr_slot(chain, at.tile - g.ncols, lane));  // it may be there already
     unsigned reset = 0;  // bit j: a sequence starts at the warp's token j
     if constexpr (SEQ) {
       bool start = false;
@@ -194,6 +193,8 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
         const float* p = a.s0 + b * a.s0s[0] + c * a.s0s[1];
         h2 = make_float2(in0 ? p[0] : 0.f, in1 ? p[a.s0s[1]] : 0.f);
       }
+    } else if (g.serial) {
+      h2 = sh.carried[s ^ 1][lane];
     } else if (__all_sync(kFullMask, before.x == kSlotState)) {
       h2 = glr_slot_state(before);
     } else {
@@ -206,7 +207,11 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
     if (warp == kPublisher) {
       if (level + 1 < g.levels) {
         const float4 m = joined(pairs, lane);
-        glr_put_state(chain, at.tile, lane, make_float2(glr_map(m.x, m.y, h2.x), glr_map(m.z, m.w, h2.y)));
+        const float2 after = make_float2(glr_map(m.x, m.y, h2.x), glr_map(m.z, m.w, h2.y));
+        if (g.serial)
+          sh.carried[s][lane] = after;
+        else
+          glr_put_state(chain, at.tile, lane, after);
       }
       if (a.cs != nullptr) {
         float* p = a.cs + b * a.css[0] + level * a.css[1] + c * a.css[2];
@@ -271,8 +276,10 @@ cudaError_t launch(const GlrArgs& a, const GlrTiles& t, const GlrChain& chain, c
   if (e != cudaSuccess) return e;
   const int64_t most = static_cast<int64_t>(dev.sm_count) * (DT == kF32 ? 2 : 4);
   GlrTiles g = t;
-  g.one = g.total <= most;
-  return glr_launch(glr_fwd_kernel<DT, SEQ, TMA>, g, static_cast<unsigned>(g.one ? g.total : most), kThreads, smem, s, a, g,
+  g.serial = g.levels > 1 && g.levels <= kGlrSerial;
+  g.one = !g.serial && g.total <= most;
+  const int64_t grid = g.serial ? g.ncols : g.total;
+  return glr_launch(glr_fwd_kernel<DT, SEQ, TMA>, g, static_cast<unsigned>(grid < most ? grid : most), kThreads, smem, s, a, g,
                     chain, maps);
 }
 
@@ -303,7 +310,7 @@ bool glr_pair_out(const void* p, const int64_t* s, Dtype dt) {
 
 uint64_t glr_fwd_workspace(int64_t B, int64_t L, int64_t C) {
   const GlrTiles t = glr_tiles(B, L, C);
-  return t.levels > 1 ? glr_chain_bytes(t.total) : 0;
+  return t.levels > kGlrSerial ? glr_chain_bytes(t.total) : 0;
 }
 
 cudaError_t launch_glr_fwd(const GlrArgs& a, void* ws, Dtype dt, const Device& dev, cudaStream_t stream) {
@@ -313,11 +320,7 @@ cudaError_t launch_glr_fwd(const GlrArgs& a, void* ws, Dtype dt, const Device& d
                    (a.out == nullptr || tensor_map_eligible(a.out, a.os, a.B, a.L, a.C, dt));
   t.pair = a.out != nullptr && glr_pair_out(a.out, a.os, dt);
   GlrChain chain = {};
-  if (t.levels > 1) {
-    chain = glr_chain(ws);
-    const cudaError_t e = cudaMemsetAsync(ws, 0xff, glr_chain_bytes(t.total), stream);
-    if (e != cudaSuccess) return e;
-  }
+  if (t.levels > kGlrSerial) chain = glr_chain(ws);
   switch (dt) {
     case kF32: return fwd_dt<kF32>(a, t, chain, tma, dev, stream);
     case kF16: return fwd_dt<kF16>(a, t, chain, tma, dev, stream);

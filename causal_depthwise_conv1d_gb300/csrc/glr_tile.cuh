@@ -32,6 +32,11 @@ constexpr int kGlrT = kGlrChunk;  // tokens of a tile
 constexpr int kGlrC = 64;         // channels of a tile
 static_assert(kGlrT == 64 && kGlrC == 64, "reset masks are two words, a lane has two channels");
 
+// Few tiles along the time: a block carries the state itself.  The chain costs a
+// memset and a slot's round trip for each tile, a serial tile about 2 us: 3 x 77
+// tokens of 1001 channels take 8 us instead of 12, four tiles of them 14 and 13.
+constexpr int kGlrSerial = 4;
+
 // Workspace of the chain: ticket and slots [tile][lane]; all bits set before
 // the launch.
 struct GlrChain {
@@ -59,7 +64,15 @@ struct GlrTiles {
   int total;   // ncols * levels
   bool pair;   // outputs may be stored in pairs
   bool one;    // a block for every tile: a block takes one
+  bool serial; // a block takes the tiles of a column in turn: no chain
 };
+
+// Tiles in the order of a block's work without a chain: its columns one after
+// the other, each from the first tile on.
+__device__ __forceinline__ int glr_serial_tile(const GlrTiles& g, int k) {
+  const int64_t col = blockIdx.x + static_cast<int64_t>(k / g.levels) * gridDim.x;
+  return col < g.ncols ? k % g.levels * g.ncols + static_cast<int>(col) : g.total;
+}
 
 // t / n, exact: the rounding adds less than t / 2^63 to a quotient whose fraction is at most 1 - 1 / n.
 __device__ __forceinline__ int glr_div(int t, uint64_t inv) {
@@ -171,7 +184,7 @@ bool glr_pair_out(const void* p, const int64_t* s, Dtype dt);
 template <typename... P, typename... A>
 cudaError_t glr_launch(void (*kernel)(P...), const GlrTiles& g, unsigned grid, unsigned threads, size_t smem,
                        cudaStream_t stream, A&&... args) {
-  if (g.levels <= 1) return launch_pdl(kernel, grid, threads, smem, stream, std::forward<A>(args)...);
+  if (g.levels <= kGlrSerial) return launch_pdl(kernel, grid, threads, smem, stream, std::forward<A>(args)...);
   kernel<<<grid, threads, smem, stream>>>(std::forward<A>(args)...);
   return cudaGetLastError();
 }

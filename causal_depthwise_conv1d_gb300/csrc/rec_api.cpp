@@ -21,17 +21,19 @@ ccv_status check_glr_sizes(int64_t B, int64_t L, int64_t C, ccv_dtype dtype) {
   return CCV_OK;
 }
 
-// The backward pass: the states before every 64th token, partial sums of drate, the chain's workspace.
+// The backward pass: the states before every 64th token, partial sums of drate,
+// the chains of the states' recomputation and of the gradients.
 struct GlrBwdWorkspace {
-  uint64_t states, part, total;
+  uint64_t states, part, chain, total;
 };
 
 GlrBwdWorkspace glr_bwd_workspace(int64_t B, int64_t L, int64_t C) {
-  GlrBwdWorkspace w = {0, 0, 0};
+  GlrBwdWorkspace w = {0, 0, 0, 0};
   if (B == 0 || L == 0 || C == 0) return w;
   w.states = up256(static_cast<uint64_t>(B) * static_cast<uint64_t>(glr_chunks(L)) * static_cast<uint64_t>(C) * 4);
   w.part = w.states;
-  w.total = w.states + w.part + ccv::glr_fwd_workspace(B, L, C);
+  w.chain = up256(ccv::glr_fwd_workspace(B, L, C));
+  w.total = w.states + w.part + 2 * w.chain;
   return w;
 }
 
@@ -91,7 +93,10 @@ ccv_status ccv_glr_fwd(const void* x, const int64_t x_strides[3], const void* de
   if (L == 0) return launched(ccv::launch_glr_step(a, dt, s), "glr_fwd");  // copies the state
   ccv::Device dev;
   CCV_TRY(static_cast<ccv_status>(ccv::api_device(&dev)));
-  return launched(ccv::launch_glr_fwd(a, workspace, dt, dev, s), "glr_fwd");
+  const uint64_t chain = ccv::glr_fwd_workspace(B, L, C);
+  cudaError_t err = chain > 0 ? cudaMemsetAsync(workspace, 0xff, chain, s) : cudaSuccess;
+  if (err == cudaSuccess) err = ccv::launch_glr_fwd(a, workspace, dt, dev, s);
+  return launched(err, "glr_fwd");
 }
 
 ccv_status ccv_glr_step(const void* x, const int64_t x_strides[3], const void* decay_gate,
@@ -187,16 +192,18 @@ ccv_status ccv_glr_bwd(const void* x, const int64_t x_strides[3], const void* de
   a.B = B, a.L = L, a.C = C;
   cudaError_t err = cudaSuccess;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  uint8_t* chain = ws + w.states + w.part;
+  uint8_t *chain = ws + w.states + w.part, *chain_states = chain + w.chain;
   ccv::Device dev;
   CCV_TRY(static_cast<ccv_status>(ccv::api_device(&dev)));
   if (chunk_states != nullptr) {
     a.cs = const_cast<float*>(chunk_states);
     copy(a.css, chunk_states_strides, 3);
+    if (w.chain > 0) err = cudaMemsetAsync(chain, 0xff, w.chain, s);
   } else if (B > 0 && L > 0) {
+    if (w.chain > 0) err = cudaMemsetAsync(chain, 0xff, 2 * w.chain, s);
     a.cs = reinterpret_cast<float*>(ws);
     a.css[0] = glr_chunks(L) * C, a.css[1] = C, a.css[2] = 1;
-    err = ccv::launch_glr_fwd(a, chain, dt, dev, s);
+    if (err == cudaSuccess) err = ccv::launch_glr_fwd(a, chain_states, dt, dev, s);
   }
   ccv::GlrGrads g = {};
   g.dout = dout, g.ds1 = dfinal_state, g.dx = dx, g.dp = ddecay_gate, g.dq = dinput_gate, g.drate = drate;

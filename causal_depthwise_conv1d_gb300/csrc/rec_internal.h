@@ -56,10 +56,11 @@ struct GlrGrads {
 };
 
 cudaError_t launch_glr_step(const GlrArgs& a, Dtype dt, cudaStream_t stream);
-// Whole sequences; ws: glr_fwd_workspace() bytes (a function of the sizes alone).
+// Whole sequences; ws: glr_fwd_workspace() bytes (a function of the sizes
+// alone), all bits set by the caller on the same stream.
 uint64_t glr_fwd_workspace(int64_t B, int64_t L, int64_t C);
 cudaError_t launch_glr_fwd(const GlrArgs& a, void* ws, Dtype dt, const Device& dev, cudaStream_t stream);
-// Backward pass with the same workspace; then drate from the partial sums, one
+// Backward pass with a workspace as the forward's, of its own; then drate from the partial sums, one
 // for each batch row and chunk.
 cudaError_t launch_glr_bwd(const GlrArgs& a, const GlrGrads& g, void* ws, Dtype dt, const Device& dev,
                            cudaStream_t stream);

@@ -12,7 +12,7 @@ from tests import rec_ref as ref  # noqa: E402
 
 ARGS = ("x", "decay_gate", "input_gate", "rate")
 SIZES = [(1, 1, 1), (1, 2, 3), (2, 63, 64), (1, 64, 72), (2, 65, 130), (3, 77, 101), (1, 300, 200), (2, 1001, 40),
-         (1, 1500, 8), (5, 129, 64)]
+         (1, 1500, 8), (5, 129, 64), (1, 256, 72), (2, 257, 72), (90, 150, 520)]
 GRADS = ("dx", "ddecay_gate", "dinput_gate", "drate", "dinitial_state")
 
 
