@@ -6,7 +6,7 @@
 // Where the decay is close to one both a and 1 - a^2 come from E = expm1(l):
 // a = 1 + E, 1 - a^2 = -E (2 + E).  For -0.85 <= l E is l times a polynomial of
 // degree 6 (fitted for the least relative error on that interval by exchange:
-// 8e-10; the Taylor polynomial needs degree 8), below that 2^(l log2 e) - 1 with
+// 8e-10, 6e-9 with FP32 coefficients; the Taylor polynomial needs degree 8), below that 2^(l log2 e) - 1 with
 // the hardware's exponential (2^-22 relative, while 1 - a >= 0.57).  So a
 // is within 2^-24 of the exact decay where a state lasts longer than two
 // tokens, and m keeps its relative precision down to the smallest rates; from

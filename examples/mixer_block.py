@@ -9,9 +9,16 @@ at a time; a training step takes the same block backwards.  The projections are
 plain matrix products of the framework; everything else on the path is this
 library's (the unit length of q and k and the gates are elementwise).
 
+RecurrentBlock is the same with the elementwise recurrence in the delta rule's
+place and a group norm with SiLU behind it:
+
+    norm -> x and gate projections -> causal depthwise conv + SiLU on x -> gated linear recurrence
+         -> group norm of the heads + SiLU -> output projection (+ residual)
+
     python examples/mixer_block.py          # prefill, decode, a few training steps; prints what it saw
     python examples/mixer_block.py --time gdr_bwd --batch 2 --tokens 2048 --key-heads 16 --value-heads 32
-                                            # one operator alone: gdr_fwd, gdr_bwd, gdr_step, ln_fwd, ln_bwd
+                                            # one operator alone: gdr_fwd, gdr_bwd, gdr_step, ln_fwd, ln_bwd,
+                                            # rec_fwd, rec_bwd, rec_step, gn_fwd, gn_bwd
 """
 from __future__ import annotations
 
@@ -119,8 +126,89 @@ class Conv(torch.autograd.Function):
         return dx, dw, None
 
 
-def training_loss(block: Block, x, target, seq_idx=None):
+class Recurrence(torch.autograd.Function):
+    """The gated linear recurrence; the states of every 64th token are kept for the backward pass."""
+
+    @staticmethod
+    def forward(ctx, x, decay_gate, input_gate, rate, seq_idx):
+        out, states = ccv.gated_linear_recurrence_fwd(x, decay_gate, input_gate, rate, seq_idx=seq_idx,
+                                                      return_chunk_states=True)
+        ctx.save_for_backward(x, decay_gate, input_gate, rate, states)
+        ctx.seq_idx = seq_idx
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        x, p, q, rate, states = ctx.saved_tensors
+        return ccv.gated_linear_recurrence_bwd(x, p, q, rate, dout, seq_idx=ctx.seq_idx,
+                                               chunk_states=states)[:4] + (None,)
+
+
+class GroupNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, groups, weight, bias):
+        ctx.save_for_backward(x, weight, bias)
+        ctx.groups = groups
+        return ccv.group_norm_fwd(x, groups, weight, bias, activation="silu")
+
+    @staticmethod
+    def backward(ctx, dout):
+        x, weight, bias = ctx.saved_tensors
+        dx, dw, db = ccv.group_norm_bwd(x, ctx.groups, weight, dout.contiguous(), bias, activation="silu")
+        return dx, None, dw, db
+
+
+class RecurrentBlock:
+    def __init__(self, dim: int, channels: int, heads: int, width: int = 4, dtype=torch.bfloat16, seed: int = 0,
+                 device="cuda"):
+        gen = torch.Generator().manual_seed(seed)
+        rnd = lambda *s, scale: (torch.randn(s, generator=gen) * scale).to(dtype).to(device)  # noqa: E731
+        self.heads = heads
+        self.norm = (torch.ones(dim, device=device), torch.zeros(dim, device=device))
+        self.head_norm = (torch.ones(channels, device=device), torch.zeros(channels, device=device))
+        self.w_in = rnd(channels, dim, scale=dim ** -0.5)
+        self.w_gate = rnd(2 * channels, dim, scale=dim ** -0.5)
+        self.w_out = rnd(dim, channels, scale=channels ** -0.5)
+        self.conv = rnd(channels, width, scale=0.4)
+        self.log_rate = torch.log(torch.rand(channels, generator=gen).to(device) * 0.8 + 0.01)  # rates stay positive
+        self.params = [self.w_in, self.w_gate, self.w_out, self.conv, self.log_rate]
+
+    def _out(self, x, h):
+        y = ccv.group_norm_fwd(h.flatten(0, -2), self.heads, *self.head_norm, activation="silu").view(h.shape)
+        return x + F.linear(y, self.w_out)
+
+    def prefill(self, x, seq_idx=None):
+        """x [B, L, dim] -> (output, states): the convolution's last inputs and the recurrence's state."""
+        n = ccv.layer_norm_fwd(x, *self.norm)
+        y, conv_state = ccv.causal_conv1d_fwd(F.linear(n, self.w_in).transpose(1, 2), self.conv, activation="silu",
+                                              seq_idx=seq_idx, return_final_states=True)
+        p, q = F.linear(n, self.w_gate).chunk(2, -1)  # the recurrence reads both where they lie
+        h, state = ccv.gated_linear_recurrence_fwd(y.transpose(1, 2), p, q, self.log_rate.exp(), seq_idx=seq_idx,
+                                                   return_final_state=True)
+        return self._out(x, h), (conv_state.contiguous(), state)
+
+    def decode(self, x, states):
+        """x [B, dim], one token; the states are advanced in place."""
+        conv_state, state = states
+        n = ccv.layer_norm_fwd(x, *self.norm)
+        y = ccv.causal_conv1d_update(F.linear(n, self.w_in), conv_state, self.conv, activation="silu")
+        p, q = F.linear(n, self.w_gate).chunk(2, -1)
+        return self._out(x, ccv.gated_linear_recurrence_step(y, p, q, self.log_rate.exp(), state))
+
+    def forward(self, x, seq_idx=None):
+        """The output through functions that know their gradients."""
+        n = LayerNorm.apply(x, *self.norm)
+        y = Conv.apply(F.linear(n, self.w_in).transpose(1, 2), self.conv, seq_idx).transpose(1, 2)
+        p, q = F.linear(n, self.w_gate).chunk(2, -1)
+        h = Recurrence.apply(y, p, q, self.log_rate.exp(), seq_idx)
+        y = GroupNorm.apply(h.flatten(0, -2), self.heads, *self.head_norm).view(h.shape)
+        return x + F.linear(y, self.w_out)
+
+
+def training_loss(block, x, target, seq_idx=None):
     """The block's output through functions that know their gradients."""
+    if isinstance(block, RecurrentBlock):
+        return ((block.forward(x, seq_idx).float() - target) ** 2).mean()
     h = LayerNorm.apply(x, *block.norm)
     y = Conv.apply(F.linear(h, block.w_in).transpose(1, 2), block.conv, seq_idx)
     q, k, v = block._split(y.transpose(1, 2))
@@ -130,7 +218,7 @@ def training_loss(block: Block, x, target, seq_idx=None):
     return ((out.float() - target) ** 2).mean()
 
 
-def train_step(block: Block, x, target, seq_idx=None, lr: float = 0.0):
+def train_step(block, x, target, seq_idx=None, lr: float = 0.0):
     leaves = block.params + list(block.norm) + list(block.head_norm)
     for p in leaves:
         p.requires_grad_(True)
@@ -149,17 +237,25 @@ def time_operator(name: str, batch: int, tokens: int, key_heads: int, value_head
     """Microseconds of one call of an operator on bf16 data of these sizes, calls back to back on the device."""
     gen = torch.Generator(device="cuda").manual_seed(0)
     rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
-    T = 1 if name == "gdr_step" else tokens
+    T = 1 if name in ("gdr_step", "rec_step") else tokens
     q, k = (F.normalize(rnd(batch, T, key_heads, head), dim=-1).bfloat16() for _ in range(2))
     v, dout = (rnd(batch, T, value_heads, head).bfloat16() for _ in range(2))
     g, beta = -F.softplus(rnd(batch, T, value_heads)), torch.sigmoid(rnd(batch, T, value_heads)).bfloat16()
     state = rnd(batch, value_heads, head, head)
     x, w = v.reshape(batch * T, -1), torch.ones(value_heads * head, device="cuda").bfloat16()
+    x3, C = x.view(batch, T, -1), value_heads * head
+    p3, q3 = rnd(batch, T, 2 * C).bfloat16().chunk(2, -1)
+    rate, h0 = torch.rand(C, generator=gen, device="cuda"), rnd(batch, C)
     call = {"gdr_fwd": lambda: ccv.gated_delta_rule_fwd(q, k, v, g, beta, return_final_state=True),
             "gdr_bwd": lambda: ccv.gated_delta_rule_bwd(q, k, v, g, beta, dout),
             "gdr_step": lambda: ccv.gated_delta_rule_step(q, k, v, g, beta, state),
             "ln_fwd": lambda: ccv.layer_norm_fwd(x, w, w),
-            "ln_bwd": lambda: ccv.layer_norm_bwd(x, w, dout.reshape(x.shape), w)}[name]
+            "ln_bwd": lambda: ccv.layer_norm_bwd(x, w, dout.reshape(x.shape), w),
+            "rec_fwd": lambda: ccv.gated_linear_recurrence_fwd(x3, p3, q3, rate),
+            "rec_bwd": lambda: ccv.gated_linear_recurrence_bwd(x3, p3, q3, rate, dout.reshape(x3.shape)),
+            "rec_step": lambda: ccv.gated_linear_recurrence_step(x3, p3, q3, rate, h0),
+            "gn_fwd": lambda: ccv.group_norm_fwd(x, value_heads, w, w, activation="silu"),
+            "gn_bwd": lambda: ccv.group_norm_bwd(x, value_heads, w, dout.reshape(x.shape), w, activation="silu")}[name]
     for _ in range(3):
         call()
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
@@ -173,7 +269,8 @@ def time_operator(name: str, batch: int, tokens: int, key_heads: int, value_head
 
 def main(argv=None):
     ap = argparse.ArgumentParser(description="The block's operators together, or one of them timed.")
-    ap.add_argument("--time", choices=("gdr_fwd", "gdr_bwd", "gdr_step", "ln_fwd", "ln_bwd"))
+    ap.add_argument("--time", choices=("gdr_fwd", "gdr_bwd", "gdr_step", "ln_fwd", "ln_bwd", "rec_fwd", "rec_bwd",
+                                       "rec_step", "gn_fwd", "gn_bwd"))
     for flag, n in (("batch", 2), ("tokens", 2048), ("key-heads", 16), ("value-heads", 32), ("head", 128),
                     ("steps", 20)):
         ap.add_argument("--" + flag, type=int, default=n)
@@ -182,17 +279,21 @@ def main(argv=None):
         us = time_operator(a.time, a.batch, a.tokens, a.key_heads, a.value_heads, a.head, a.steps)
         print(f"{a.time}: {us:.1f} us")
         return
-    block = Block(dim=256, key_heads=2, value_heads=4, head=64)
+    for block in (Block(dim=256, key_heads=2, value_heads=4, head=64), RecurrentBlock(dim=256, channels=256, heads=4)):
+        show(type(block).__name__, block)
+
+
+def show(name, block):
     gen = torch.Generator(device="cuda").manual_seed(1)
     x = torch.randn((2, 160, 256), generator=gen, device="cuda").to(torch.bfloat16)
     whole, _ = block.prefill(x)
     first, states = block.prefill(x[:, :150].contiguous())
     tail = torch.stack([block.decode(x[:, t], states) for t in range(150, 160)], 1)
     gap = (torch.cat([first, tail], 1).float() - whole.float()).abs().max().item()
-    print(f"prefill of 160 tokens against prefill of 150 and ten decode steps: largest difference {gap:.4f}")
+    print(f"{name}: prefill of 160 tokens against prefill of 150 and ten decode steps: largest difference {gap:.4f}")
     target = torch.randn((2, 160, 256), generator=gen, device="cuda")
     losses = [train_step(block, x, target, lr=0.5)[0].item() for _ in range(8)]
-    print("training loss", " ".join(f"{v:.4f}" for v in losses))
+    print(name, "training loss", " ".join(f"{v:.4f}" for v in losses))
 
 
 if __name__ == "__main__":

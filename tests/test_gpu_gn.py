@@ -12,7 +12,10 @@ from tests import rec_ref as ref  # noqa: E402
 
 SIZES = [(1, 1, 1, 1), (3, 1, 8, 2), (700, 1, 512, 4), (9, 1, 1000, 8), (5, 1, 640, 4), (33, 1, 4096, 2),
          (2, 7, 24, 3), (3, 77, 200, 8), (2, 300, 256, 4), (1, 1000, 320, 2), (1, 2000, 640, 1), (2, 65, 96, 96),
-         (40, 3, 64, 1), (1, 5000, 16, 1), (2, 1, 5120, 1), (1, 3, 12000, 2), (1, 700, 2080, 1), (600, 2, 64, 8)]
+         (40, 3, 64, 1), (1, 5000, 16, 1), (2, 1, 5120, 1), (1, 3, 12000, 2), (1, 700, 2080, 1), (600, 2, 64, 8),
+         # slabs of unaligned groups, narrow rows, groups beyond a cluster, clusters of sixteen, samples in turn
+         (1, 3000, 21, 1), (2, 1500, 35, 5), (300, 1, 7, 1), (129, 1, 60, 12), (70, 1, 201, 3), (1, 9000, 512, 1),
+         (1, 5000, 128, 1), (64, 40, 64, 8), (3, 1100, 384, 2)]
 TYPES = [("f32", "f32", True), ("f16", "f32", False), ("bf16", "bf16", True), ("f16", "bf16", True)]
 
 
