@@ -24,19 +24,20 @@ EncodeTiled encoder() {
 
 }  // namespace
 
-// A tensor copy takes rows of unit stride on 16-byte boundaries, in strides that the copy's map can hold.
+// A tensor copy takes rows of unit stride on 16-byte boundaries, in strides that the copy's map can hold.  Rows
+// that end inside 16 bytes are not taken: a store clips there, so it would write zeros up to the boundary.
 bool tensor_map_eligible(const void* p, const int64_t* s, int64_t B, int64_t L, int64_t C, Dtype dt) {
   const int64_t e = dt == kF32 ? 4 : 2, lim = int64_t(1) << 39;
-  return s[2] == 1 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && C < lim &&
+  return s[2] == 1 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && C < lim && C * e % 16 == 0 &&
          (L == 1 || (s[1] * e % 16 == 0 && s[1] >= C && s[1] * e < lim)) &&
          (B == 1 || (s[0] * e % 16 == 0 && s[0] > 0 && s[0] * e < lim)) && encoder() != nullptr;
 }
 
 bool tensor_map3(CUtensorMap* m, const void* p, const int64_t* s, int64_t B, int64_t L, int64_t C, const int64_t* box2,
               Dtype dt) {
-  const int64_t e = dt == kF32 ? 4 : 2, row = (C * e + 15) / 16 * 16;
+  const int64_t e = dt == kF32 ? 4 : 2;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(C), static_cast<cuuint64_t>(L), static_cast<cuuint64_t>(B)};
-  const int64_t s1 = L > 1 ? s[1] * e : row;
+  const int64_t s1 = L > 1 ? s[1] * e : C * e;
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1), static_cast<cuuint64_t>(B > 1 ? s[0] * e : s1 * L)};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(box2[0]), static_cast<cuuint32_t>(box2[1]), 1};
   const cuuint32_t estr[3] = {1, 1, 1};

@@ -268,3 +268,30 @@ def test_refusals():
         backward(dict(c, initial_state=None), dinitial_state=torch.empty((2, 16), device="cuda"))
     with pytest.raises(ccv.CcvError, match="n_slots"):
         ccv.gated_linear_recurrence_step(*(c[n][:, 0] for n in ARGS[:3]), c["rate"], torch.zeros((1, 16), device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_channels_that_end_inside_a_vector(dtype):
+    """77 channels in rows of 80 on 16-byte boundaries: what lies beside them is neither used nor written."""
+    B, L, C, W = 2, 333, 77, 80
+    c = ref.glr_inputs(11, B, L, C, dtype, seqs=3, state=True, grads=True)
+    d = dev(c)
+
+    def padded(t, fill):
+        w = torch.full((B, L + 9, W), fill, dtype=d["x"].dtype, device="cuda")
+        if t is not None:
+            w[:, :L, :C] = t
+        return w
+
+    e = dict(d, **{n: padded(d[n], float("nan"))[:, :L, :C] for n in (*ARGS[:3], "dout")})
+    bufs = [padded(None, 5.0) for _ in range(4)]
+    out, dx, dp, dq = (t[:, :L, :C] for t in bufs)
+    check_forward(c, forward(e, out=out, return_final_state=True, return_chunk_states=True), dtype)
+    check_backward(c, backward(e, dx=dx, ddecay_gate=dp, dinput_gate=dq), dtype)
+    for t in bufs:
+        assert bool((t[:, L:] == 5).all()) and bool((t[..., C:] == 5).all())
+    # the same channels for every batch row: a stride of zero
+    same = dict(d, decay_gate=e["decay_gate"][:1].expand(B, L, C), dout=e["dout"][:, :1].expand(B, L, C))
+    c2 = dict(c, decay_gate=c["decay_gate"][:1].expand(B, L, C), dout=c["dout"][:, :1].expand(B, L, C))
+    check_forward(c2, forward(same, return_final_state=True, return_chunk_states=True), dtype)
+    check_backward(c2, backward(same), dtype)
