@@ -10,6 +10,7 @@
 // sums are FP32 in a fixed order.
 #include "ccv_common.cuh"
 #include "rec_internal.h"
+#include "rec_pairs.cuh"
 
 #include <initializer_list>
 
@@ -155,7 +156,7 @@ __device__ __forceinline__ float dz_of(const GnArgs& a, const Slab& b, float2 st
                                        float bias, float& xh) {
   xh = (ld<DT>(a.x, a.xs, b.n, t, ch) - st.x) * st.y;
   const float g = ld<DT>(a.dout, a.gs, b.n, t, ch);
-  return a.silu ? g * silu_grad(fmaf(xh, w, bias)) : g;
+  return a.silu ? g * silu_grad_cut(fmaf(xh, w, bias)) : g;
 }
 
 // Sums of d and d xh over the slab, and the columns' dw and db added to

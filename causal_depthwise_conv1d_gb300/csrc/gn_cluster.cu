@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int j = 0; j < H; ++j) {
             f[j] = fmul2(fadd2(f[j], minus), r2);
-            if constexpr (decltype(silu)::value) d[j] = dz_pair<true>(ffma2(f[j], w[j], b[j]), d[j]);
+            if constexpr (decltype(silu)::value) d[j] = silu_grad_pair2(ffma2(f[j], w[j], b[j]), d[j]);
             dw[j] = ffma2(d[j], f[j], dw[j]);
             db[j] = fadd2(db[j], d[j]);
             d[j] = fmul2(d[j], w[j]);
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int j = 0; j < H; ++j) {
               f[j] = fmul2(fadd2(f[j], minus), r2);
-              if constexpr (decltype(silu)::value) d[j] = dz_pair<true>(ffma2(f[j], w[j], b[j]), d[j]);
+              if constexpr (decltype(silu)::value) d[j] = silu_grad_pair2(ffma2(f[j], w[j], b[j]), d[j]);
               d[j] = fmul2(d[j], w[j]);
               upk(ffma2(d[j], r2, ffma2(f[j], k2, k1)), o[2 * j], o[2 * j + 1]);
             }

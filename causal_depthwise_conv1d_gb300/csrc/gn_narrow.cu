@@ -5,6 +5,7 @@
 // took 907 us).
 #include "ccv_common.cuh"
 #include "rec_internal.h"
+#include "rec_pairs.cuh"
 
 namespace ccv {
 namespace {
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) gn_narrow_kernel(const GnArgs a, int
     for (int i = 0; i < NV; ++i) {
       f[i] *= r;
       if constexpr (BWD) {
-        if (a.silu) d[i] *= silu_grad(fmaf(f[i], w[i], b[i]));
+        if (a.silu) d[i] *= silu_grad_cut(fmaf(f[i], w[i], b[i]));
         dw[i] = fmaf(d[i], f[i], dw[i]);
         db[i] += d[i];
         d[i] *= w[i];

@@ -175,3 +175,45 @@ def test_refusals():
         ccv.group_norm_fwd(x, 4, eps=-1.0)
     with pytest.raises(ccv.CcvError, match="workspace too small"):
         ccv.group_norm_bwd(x, 4, w, x, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,S,C,G", [(30, 1, 256, 4), (30, 1, 100, 4), (2, 90, 256, 4), (2, 90, 100, 4)])
+def test_activations_beyond_any_tail(N, S, C, G, dtype):
+    """SiLU and its derivative where z is huge: nothing is left of either below, not a floor times z."""
+    x, _, _, dy = (t.cuda() for t in ref.gn_inputs(8, N, S, C, dtype, "f32"))
+    w, far = torch.ones(C, device="cuda"), torch.zeros(C, device="cuda")
+    for k, z in enumerate((-150.0, -1e5, -1e20, -1e30, -3e38, 1e30)):
+        far[k::9] = z
+    y = ccv.group_norm_fwd(shaped(x), G, w, far, activation="silu").view(N, S, C)
+    plain = ccv.group_norm_fwd(shaped(x), G, w, far).view(N, S, C)
+    assert float(y[..., far < 0].abs().max()) < 1e-30
+    # a sigmoid of one, by the hardware's functions (four of 2^-22), and two roundings to the type
+    ratio = y[..., far > 1].double() / plain[..., far > 1].double()
+    assert float((ratio - 1).abs().max()) <= 4 * 2.0 ** -22 + 1.01 * torch.finfo(y.dtype).eps
+    _, dw, db = ccv.group_norm_bwd(shaped(x), G, w, shaped(dy), far, activation="silu")
+    assert float(db[far < 0].abs().max()) < 1e-28 and float(dw[far < 0].abs().max()) < 1e-28
+    # a derivative of one (five of 2^-22): the sum of N S values, each addition rounded
+    total = dy.double().sum((0, 1))[far > 1]
+    assert bool(((db[far > 1] - total).abs() <= (N * S + 24) * 2.0 ** -24 * dy.double().abs().sum((0, 1))[far > 1]).all())
+    # a parameter that is not finite stays in its channel
+    bad = far.clone()
+    bad[C // 2] = float("nan")
+    y2 = ccv.group_norm_fwd(shaped(x), G, w, bad, activation="silu").view(N, S, C)
+    keep = torch.arange(C, device="cuda") != C // 2
+    assert torch.equal(y2[..., keep], y[..., keep]) and bool(y2[..., ~keep].isnan().all())
+    db2 = ccv.group_norm_bwd(shaped(x), G, w, shaped(dy), bad, activation="silu")[2]
+    assert torch.equal(db2[keep], db[keep]) and bool(db2[~keep].isnan().all())
+
+
+@pytest.mark.parametrize("N,S,C,G", [(3, 77, 1000, 8), (2, 150, 515, 1)])
+def test_few_large_groups(N, S, C, G):
+    """Groups of 9625 and 77250 elements in blocks of 1024 threads, fewer and more channels than a block has."""
+    x, w, b, dy = ref.gn_inputs(9, N, S, C, "f32", "f32")
+    e, bound = ref.gn_fwd(x, G, w, b, silu=True)
+    assert ref.worst(ccv.group_norm_fwd(x.cuda(), G, w.cuda(), b.cuda(), activation="silu"), e, tol(e, bound, "f32")) <= 1
+    want = ref.gn_bwd(x, G, w, dy, b, silu=True)
+    got = ccv.group_norm_bwd(x.cuda(), G, w.cuda(), dy.cuda(), b.cuda(), activation="silu")
+    for n, t in zip(("dx", "dweight", "dbias"), got):
+        v, bd = want[n]
+        assert ref.worst(t, v, tol(v, bd, "f32")) <= 1, n
