@@ -101,7 +101,8 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 2 : 4)
     if (it == 1 && g.one) break;
     if (!mbar_wait(&sh.full[s], (it >> 1) & 1)) {
       if (lane == 0) atomicOr(&g_fault, kFaultConsumerWait);
-      break;  // no other copy of the block is in flight
+      mbar_wait(&sh.full[s], (it >> 1) & 1);  // the one copy in flight, again with a limit
+      break;
     }
     const GlrPlace at = sh.place[s];
     if (at.tile >= g.total) break;

@@ -89,7 +89,6 @@ cudaError_t launch_dt(const GlrArgs& a, cudaStream_t s) {
                    vec4(a.q, a.qs, 3, e) && vec4(a.out, a.os, 3, e) && vec4(a.s0, a.s0s, 2, 4) &&
                    vec4(a.s1, a.s1s, 2, 4) && vec4(a.rate, &a.rs, 1, 4);
   const int64_t tiles = (a.C + kThreads * (vec ? 4 : 1) - 1) / (kThreads * (vec ? 4 : 1));
-  if (a.B * tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>(a.B * tiles), n = static_cast<unsigned>(tiles);
   if (vec) return launch_pdl(glr_step_kernel<DT, 4>, grid, kThreads, 0, s, a, n);
   return launch_pdl(glr_step_kernel<DT, 1>, grid, kThreads, 0, s, a, n);

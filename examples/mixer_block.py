@@ -18,7 +18,8 @@ place and a group norm with SiLU behind it:
     python examples/mixer_block.py          # prefill, decode, a few training steps; prints what it saw
     python examples/mixer_block.py --time gdr_bwd --batch 2 --tokens 2048 --key-heads 16 --value-heads 32
                                             # one operator alone: gdr_fwd, gdr_bwd, gdr_step, ln_fwd, ln_bwd,
-                                            # rec_fwd, rec_bwd, rec_step, gn_fwd, gn_bwd
+                                            # rec_fwd, rec_bwd, rec_step, gn_fwd, gn_bwd (groups of a token),
+                                            # gn_seq_fwd, gn_seq_bwd (groups of a sequence)
 """
 from __future__ import annotations
 
@@ -255,7 +256,10 @@ def time_operator(name: str, batch: int, tokens: int, key_heads: int, value_head
             "rec_bwd": lambda: ccv.gated_linear_recurrence_bwd(x3, p3, q3, rate, dout.reshape(x3.shape)),
             "rec_step": lambda: ccv.gated_linear_recurrence_step(x3, p3, q3, rate, h0),
             "gn_fwd": lambda: ccv.group_norm_fwd(x, value_heads, w, w, activation="silu"),
-            "gn_bwd": lambda: ccv.group_norm_bwd(x, value_heads, w, dout.reshape(x.shape), w, activation="silu")}[name]
+            "gn_bwd": lambda: ccv.group_norm_bwd(x, value_heads, w, dout.reshape(x.shape), w, activation="silu"),
+            "gn_seq_fwd": lambda: ccv.group_norm_fwd(x3, value_heads, w, w, activation="silu"),
+            "gn_seq_bwd": lambda: ccv.group_norm_bwd(x3, value_heads, w, dout.reshape(x3.shape), w,
+                                                     activation="silu")}[name]
     for _ in range(3):
         call()
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
@@ -270,7 +274,7 @@ def time_operator(name: str, batch: int, tokens: int, key_heads: int, value_head
 def main(argv=None):
     ap = argparse.ArgumentParser(description="The block's operators together, or one of them timed.")
     ap.add_argument("--time", choices=("gdr_fwd", "gdr_bwd", "gdr_step", "ln_fwd", "ln_bwd", "rec_fwd", "rec_bwd",
-                                       "rec_step", "gn_fwd", "gn_bwd"))
+                                       "rec_step", "gn_fwd", "gn_bwd", "gn_seq_fwd", "gn_seq_bwd"))
     for flag, n in (("batch", 2), ("tokens", 2048), ("key-heads", 16), ("value-heads", 32), ("head", 128),
                     ("steps", 20)):
         ap.add_argument("--" + flag, type=int, default=n)

@@ -513,7 +513,7 @@ ccv_status ccv_ln_bwd_workspace_size(int64_t N, int64_t D, uint64_t* bytes);
  *                     128-byte aligned (may be NULL where that is 0).  Contents
  *                     undefined before and after; calls in flight at the same
  *                     time must not share it.
- * Any strides; unit stride along the channels with rows on 16-byte boundaries
+ * Any strides; unit stride along the channels with rows that start and end on 16-byte boundaries
  * is the fast layout (gates as slices of one projection are).
  *
  * Precision.  Gates, decays, states and sums are FP32; exponentials and
@@ -524,7 +524,9 @@ ccv_status ccv_ln_bwd_workspace_size(int64_t N, int64_t D, uint64_t* bytes);
  *
  * out, final_state_out and chunk_states_out must not share memory with an
  * input or each other.  Non-finite values affect what the definition says, and
- * nothing before their own token or across a change of seq_idx.
+ * nothing before their own token or across a change of seq_idx; an infinite
+ * state may become NaN after 64 tokens or more whose decays' product is zero in
+ * FP32.
  * B or C == 0 is a no-op; L == 0 copies the initial state.
  */
 ccv_status ccv_glr_fwd(const void* x, const int64_t x_strides[3], const void* decay_gate,
@@ -604,7 +606,7 @@ ccv_status ccv_glr_bwd_workspace_size(int64_t B, int64_t L, int64_t C, ccv_dtype
  *
  *   weight, bias      [C] in weight_dtype, or NULL (one, zero); any of the
  *                     nine pairs of dtype and weight_dtype.
- *   groups            >= 1, divides C.
+ *   groups            >= 1, divides C; at most 2^18 channels a group.
  *   eps               >= 0.
  *   workspace         ccv_gn_fwd_workspace_size() bytes, 128-byte aligned (may
  *                     be NULL where that is 0).

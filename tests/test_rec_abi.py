@@ -152,3 +152,13 @@ def test_workspaces_are_told_on_the_host(mx):  # noqa: F811
         assert mx._fn(name + "_workspace_size")(*key, ctypes.byref(n)) == 0
         assert mx._fn(name + "_workspace_size")(*key, None) == 1
         assert mx._fn(name + "_workspace_size")(-1, *key[1:], ctypes.byref(n)) == 1
+
+
+@pytest.mark.parametrize("kind", ["fwd", "bwd"])
+def test_groups_of_too_many_channels(mx, kind):  # noqa: F811
+    wide = 1 << 19
+    n = ctypes.c_uint64()
+    assert mx._fn(f"ccv_gn_{kind}_workspace_size")(1, 1, wide, 2, ctypes.byref(n)) == 0
+    assert mx._fn(f"ccv_gn_{kind}_workspace_size")(1, 1, wide, 1, ctypes.byref(n)) == 1
+    rc, msg = status(mx, "ccv_gn_" + kind, gn_args(mx, kind, N=1, S=1, C=wide, G=1))
+    assert rc == 1 and "262144 channels" in msg, msg
