@@ -2,8 +2,9 @@
 // request, or four adjacent ones where all rows allow vectors, its states in
 // registers, one token after the other.
 //
-// What bounds it: for one request a launch; for a batch HBM, 16 bytes an element
-// and token in bf16 (the state read and written in FP32).
+// What bounds it: the launch, and two dependent loads (slot, then state).  One
+// request of 5120 channels in bf16 4.4 us, 128 requests of a cache with 192 slots
+// 5.9 us (10.2 MB: 16 bytes an element and token, the state in FP32).
 #include "glr.cuh"
 
 namespace ccv {

@@ -5,7 +5,14 @@
 // are exchanges between these lanes: no barrier, no shared memory.  A lane keeps
 // its channels' parameters (and, backwards, their gradients' sums) in registers
 // and walks over rows; the loads of the next rows are in flight while the
-// present ones are worked on.  What bounds it: HBM.
+// present ones are worked on.
+//
+// bf16, 16384 rows x 5120 channels in 40 groups with SiLU 78.9 us (4.3 TB/s), the
+// backward pass of 8192 x 4096 in 32 groups 44.5 us (4.5 TB/s).  What bounds it:
+// 14 (24) instructions an element at 55 % of the issue slots beside the loads'
+// latency.  Two vectors a lane instead of one halve the exchanges (backward 68 ->
+// 45); a row more in flight (76, backward 50) and rings of bulk copies a warp did
+// not pay.
 #include <type_traits>
 
 #include "ccv_common.cuh"
