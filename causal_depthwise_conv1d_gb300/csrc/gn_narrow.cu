@@ -1,8 +1,8 @@
 // Group normalisation of rows on their own (S = 1) in groups that are no whole
 // vectors, any strides: as gn_rows.cu with single elements, LPG lanes a group
 // and NV channels a lane.  A block a group, as gn.cu has for every other case,
-// would leave 250 of 256 threads idle in groups of six channels (12.9 MB of them
-// took 907 us).
+// would leave 250 of 256 threads idle in groups of six channels: 179200 x 36 in
+// bf16 takes 28 us here (0.9 TB/s), bound by loads of single elements.
 #include "ccv_common.cuh"
 #include "rec_internal.h"
 #include "rec_pairs.cuh"
