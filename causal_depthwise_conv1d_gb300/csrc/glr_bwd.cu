@@ -186,9 +186,11 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
       for (int j = 0; j < kRun; ++j) {
         const uint64_t in = fmul2(f1[j], load(0, a.x, a.xs, j));
         const bool cut = SEQ && (reset >> j & 1);
-        A = cut ? pk(kMinusZero, kMinusZero) : fmul2(A, dec[j]);
+        A = fmul2(A, dec[j]);
         H = cut ? in : ffma2(dec[j], H, in);
       }
+      // the mark of a start: as a factor it would be lost to a later decay that is NaN, and R is what came before that
+      if (SEQ && reset != 0) A = pk(kMinusZero, kMinusZero);
       float2 x, y;
       upk(A, x.x, x.y), upk(H, y.x, y.y);
       sh.fwd[warp][lane] = make_float4(x.x, y.x, x.y, y.y);
