@@ -13,6 +13,11 @@
 // a rounded to FP32, 1 - a^2 would have lost 10 of its 24 bits at a = 0.9995.
 // As -rate <= l, channels whose rate is at most 0.85 need no exponential here,
 // and a warp that has no others takes the shorter code (the same values).
+//
+// A decay is positive, and so is every product of decays: neither is let down to
+// zero (glr_positive), so an infinite state stays infinite where 0 * inf would
+// make it NaN.  To a finite state h that adds at most 2^-149 |h|, as much as
+// the rounding of such a decay.
 #pragma once
 
 #include "ccv_common.cuh"
@@ -41,6 +46,9 @@ __device__ __forceinline__ float sqrt_approx(float x) {
   return y;
 }
 
+// +0 as the smallest positive number, 2^-149; -0 and NaN as they are.
+__device__ __forceinline__ float glr_positive(float a) { return __uint_as_float(max(__float_as_uint(a), 1u)); }
+
 __device__ __forceinline__ float rsqrt_approx(float x) {
   float y;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -60,7 +68,7 @@ __device__ __forceinline__ void glr_decay(float l, float& a, float& m2) {
 #pragma unroll
   for (int i = 1; i < 7; ++i) E = fmaf(E, l, glr_poly(i));
   E = __fmul_rn(E, l);
-  const float far = ex2_approx(__fmul_rn(l, kLog2e));
+  const float far = glr_positive(ex2_approx(__fmul_rn(l, kLog2e)));
   const bool near = l >= kGlrSeries;
   a = near ? __fadd_rn(1.f, E) : far;
   E = near ? E : __fadd_rn(far, -1.f);

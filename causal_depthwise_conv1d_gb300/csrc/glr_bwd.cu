@@ -57,6 +57,7 @@ __device__ __forceinline__ float4 joined(const float4 (*runs)[32], int lane) {
     glr_join(v.x, v.y, m.x, m.y);
     glr_join(v.z, v.w, m.z, m.w);
   }
+  m.x = glr_positive(m.x), m.z = glr_positive(m.z);
   return m;
 }
 
@@ -189,11 +190,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
         A = fmul2(A, dec[j]);
         H = cut ? in : ffma2(dec[j], H, in);
       }
-      // the mark of a start: as a factor it would be lost to a later decay that is NaN, and R is what came before that
-      if (SEQ && reset != 0) A = pk(kMinusZero, kMinusZero);
-      float2 x, y;
-      upk(A, x.x, x.y), upk(H, y.x, y.y);
-      sh.fwd[warp][lane] = make_float4(x.x, y.x, x.y, y.y);
+      sh.fwd[warp][lane] = glr_run(A, H, SEQ && reset != 0);
       // the carry's map, last token first
       uint64_t R = 0;
 #pragma unroll
@@ -201,8 +198,7 @@ __global__ void __launch_bounds__(kThreads, DT == kF32 ? 1 : 2)
         const uint64_t o = load(3, gr.dout, gr.dos, j);
         R = SEQ && (reset >> j & 1) ? 0 : fmul2(dec[j], fadd2(o, R));
       }
-      upk(R, y.x, y.y);
-      sh.bwd[warp][lane] = make_float4(x.x, y.x, x.y, y.y);
+      sh.bwd[warp][lane] = glr_run(A, R, SEQ && reset != 0);
     }
     if (TMA && lane == 0) bulk_wait_read<>();  // the boxes of the tile before have left its stage
     __syncthreads();  // the runs' maps are there, the other stage is free

@@ -88,6 +88,13 @@ __device__ __forceinline__ void glr_join(float A, float H, float& A0, float& H0)
   H0 = glr_map(A, H, H0);
   A0 = glr_cut(A) || glr_cut(A0) ? kMinusZero : __fmul_rn(A, A0);
 }
+// Maps of a run of tokens for two channels, from the product A of its decays (start: a sequence starts in it).  The mark of
+// a start is no factor of A: a later decay that is NaN would replace it.
+__device__ __forceinline__ float4 glr_run(uint64_t A, uint64_t H, bool start) {
+  float a, b, u, v;
+  upk(A, a, b), upk(H, u, v);
+  return start ? make_float4(kMinusZero, u, kMinusZero, v) : make_float4(glr_positive(a), u, glr_positive(b), v);
+}
 
 // A slot's first word: empty, or a state (in the second and fourth word), or
 // the decay of a pair.  (Both are NaNs with a sign; a decay that is one is
@@ -259,7 +266,7 @@ __device__ __forceinline__ void glr_decay2(uint64_t l, uint64_t& a, uint64_t& m2
   if constexpr (!NEAR) {
     float f0, f1, n0, n1, l0, l1, e0, e1;
     upk(l, l0, l1);
-    f0 = ex2_approx(__fmul_rn(l0, kLog2e)), f1 = ex2_approx(__fmul_rn(l1, kLog2e));
+    f0 = glr_positive(ex2_approx(__fmul_rn(l0, kLog2e))), f1 = glr_positive(ex2_approx(__fmul_rn(l1, kLog2e)));
     upk(a, n0, n1);
     upk(E, e0, e1);
     const bool c0 = l0 >= kGlrSeries, c1 = l1 >= kGlrSeries;

@@ -524,9 +524,9 @@ ccv_status ccv_ln_bwd_workspace_size(int64_t N, int64_t D, uint64_t* bytes);
  *
  * out, final_state_out and chunk_states_out must not share memory with an
  * input or each other.  Non-finite values affect what the definition says, and
- * nothing before their own token or across a change of seq_idx; an infinite
- * state may become NaN after 64 tokens or more whose decays' product is zero in
- * FP32.
+ * nothing before their own token or across a change of seq_idx.  Decays and
+ * their products are positive (2^-149 where FP32 has nothing smaller), so an
+ * infinite state stays infinite however long it decays.
  * B or C == 0 is a no-op; L == 0 copies the initial state.
  */
 ccv_status ccv_glr_fwd(const void* x, const int64_t x_strides[3], const void* decay_gate,
