@@ -612,6 +612,12 @@ ccv_status ccv_glr_bwd_workspace_size(int64_t B, int64_t L, int64_t C, ccv_dtype
  *                     be NULL where that is 0).
  * Any strides; unit stride along the channels with rows and groups on 16-byte
  * boundaries is the fast layout.
+ *
+ * Precision.  Statistics, parameters' sums and activations are FP32.  SiLU takes
+ * the hardware's exponential and reciprocal: 2^-17 relative, and where the
+ * sigmoid is below 2^-86 (far below zero) an absolute 2^-118; its derivative
+ * 2^-16 of s (1 + |z| (1 - s)) and 2^-107 absolute.
+ *
  * out must not share memory with an input.  N, S or C == 0 is a no-op.
  */
 ccv_status ccv_gn_fwd(const void* x, const int64_t x_strides[3], const void* weight, int64_t weight_stride,
