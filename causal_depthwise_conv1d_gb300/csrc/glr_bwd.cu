@@ -13,8 +13,9 @@
 // before the token is known, G's factors u, b (1 - i), W l (1 - r), W r take
 // their places.  So every sigmoid and root is taken once.
 //
-// bf16, 4 x 2048 x 4096 113 us (4.2 TB/s of 478 MB): 80 instructions an element at
-// 60 % of the issue slots.  Eight tokens a warp are what 128 registers hold.
+// bf16, 4 x 2048 x 4096 113 us (4.2 TB/s of 478 MB): 76 instructions an element at
+// 63 % of the issue slots (warps with a rate above 0.85: 80 instructions, 119 us).
+// Eight tokens a warp are what 128 registers hold.
 #include <type_traits>
 
 #include "glr_tile.cuh"

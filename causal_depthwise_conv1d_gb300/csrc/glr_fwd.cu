@@ -10,10 +10,11 @@
 // over x in the stage and stores them as a box.  So a state costs no second
 // pass over the inputs, however few channels there are to split the device by.
 //
-// bf16, 8192 x 5120 82 us (4.1 TB/s of 336 MB), 8 x 2048 x 5120 in five packed
-// sequences 128 us (5.3 TB/s); 35 instructions an element at 63 % of the issue slots
-// of 16 warps an SM.  Runs of 16 tokens: with eight 115 and 164 us; three blocks an
-// SM instead of four 98 and 149.
+// bf16, 8192 x 5120 83 us (4.1 TB/s of 336 MB), 8 x 2048 x 5120 in five packed
+// sequences 128 us (5.3 TB/s); 30 instructions an element at 57 % of the issue slots
+// of 16 warps an SM.  Warps with a rate above 0.85 take the exponential of the decay
+// too: 35 instructions at 63 %, 87 and 135 us.  Runs of 16 tokens: with eight 115 and
+// 164 us; three blocks an SM instead of four 98 and 149.
 #include <type_traits>
 
 #include "glr_tile.cuh"

@@ -15,7 +15,7 @@
 // wherever that fold starts, and results do not depend on timing.  A slot is
 // read and written whole (128-bit relaxed accesses), so nothing needs a fence:
 // with flags beside the values, released and acquired, 8192 tokens x 5120
-// channels took 327 us instead of 99 (and 82 with what came after).
+// channels took 327 us instead of 99 (and 83 with what came after).
 #pragma once
 
 #include <cuda.h>

@@ -284,7 +284,8 @@ cudaError_t bwd_dt(const GnArgs& a, cudaStream_t s) {
 }  // namespace
 
 // Slabs enough for eight blocks an SM of 152 unless that leaves them below
-// 8192 elements, and never more than 2^18 elements (at most 2048 a thread and sum).
+// 8192 elements, and never more positions than fill 2^18 elements, the last one
+// rounded up: at most 2048 elements a thread and sum.
 GnPlan gn_plan(int64_t N, int64_t S, int64_t C, int64_t G) {
   GnPlan p = {1, S > 0 ? S : 1, 1};
   if (N <= 0 || S <= 0 || C <= 0 || G <= 0) return p;

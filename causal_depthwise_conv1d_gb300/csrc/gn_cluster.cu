@@ -7,9 +7,10 @@
 // that: the first takes the boxes as they arrive, the last hands each box back
 // for the next group's copy as soon as it has been used.  A thread keeps its
 // vector of channels, so parameters stay in registers and the backward pass adds
-// dw and db there over all samples.  The cluster's blocks send one another the
-// mean of their part and the squares about it, and merge them in the same order
-// (sums of n_k (mean_k - mean)^2: no difference of large sums).
+// dw and db there over all samples.  A thread takes its squares about its mean from
+// one sweep, as a difference whose loss is bounded (see the loop); threads' and
+// blocks' means and squares, which the cluster's blocks send one another, are merged
+// in the same order as sums of n_k (mean_k - mean)^2, without differences of large sums.
 //
 // The backward pass reads dout in both of its sweeps, the second time from the
 // L2 cache: with dout in the stage as well, a group of 2048 x 128 bf16 took

@@ -237,7 +237,7 @@ ccv_status check_gn(int64_t N, int64_t S, int64_t C, int64_t G, float eps, ccv_a
     CCV_FAIL(CCV_ERR_INVALID_ARG, "unknown activation %d", static_cast<int>(act));
   if (G < 1 || C % G != 0)
     CCV_FAIL(CCV_ERR_INVALID_ARG, "C must be a multiple of groups (got %lld, %lld)", (long long)C, (long long)G);
-  // a thread's sums stay below 2^10 terms (see gn_plan)
+  // a thread's sums over a slab stay within 2^11 terms (see gn_plan)
   if (C / G > (1 << 18)) CCV_FAIL(CCV_ERR_INVALID_ARG, "groups of at most 262144 channels");
   if (!(eps >= 0.f)) CCV_FAIL(CCV_ERR_INVALID_ARG, "eps must be >= 0");
   const __int128 lim = static_cast<__int128>(INT64_MAX) >> 8;

@@ -246,7 +246,7 @@ def time_operator(name: str, batch: int, tokens: int, key_heads: int, value_head
     x, w = v.reshape(batch * T, -1), torch.ones(value_heads * head, device="cuda").bfloat16()
     x3, C = x.view(batch, T, -1), value_heads * head
     p3, q3 = rnd(batch, T, 2 * C).bfloat16().chunk(2, -1)
-    rate, h0 = torch.rand(C, generator=gen, device="cuda"), rnd(batch, C)
+    rate, h0 = torch.rand(C, generator=gen, device="cuda") * 0.8 + 0.01, rnd(batch, C)  # rates as RecurrentBlock's
     call = {"gdr_fwd": lambda: ccv.gated_delta_rule_fwd(q, k, v, g, beta, return_final_state=True),
             "gdr_bwd": lambda: ccv.gated_delta_rule_bwd(q, k, v, g, beta, dout),
             "gdr_step": lambda: ccv.gated_delta_rule_step(q, k, v, g, beta, state),

@@ -503,8 +503,10 @@ ccv_status ccv_ln_bwd_workspace_size(int64_t N, int64_t D, uint64_t* bytes);
  *                     grows).
  *   seq_idx           int32 [B,L] or NULL.  Where seq_idx[b,t] differs from
  *                     seq_idx[b,t-1] a new sequence begins: token t sees the
- *                     zero state.  initial_state belongs to the sequence of
- *                     token 0.
+ *                     zero state.  Its input keeps the factor sqrt(1 - a^2)
+ *                     like every other token's: a model that lets the first
+ *                     token of each sequence in with factor one is another
+ *                     one.  initial_state belongs to the sequence of token 0.
  *   initial_state     FP32 [B,C] or NULL (zero).
  *   final_state_out   FP32 [B,C] or NULL; the state after token L-1.
  *   chunk_states_out  FP32 [B,ceil(L/64),C] or NULL; the state before every
